@@ -60,8 +60,16 @@ extern "C" {
 
 /* Element type of a pool.  PKV_F16 / PKV_BF16: K and V stored as is.
  * PKV_Q8_BF16 / PKV_Q8_F16: 8-bit cache (one fp16 scale per 32 values; q and
- * out in bf16 / fp16), see kv_cache_write_q8. */
-typedef enum pkv_dtype { PKV_F16 = 0, PKV_BF16 = 1, PKV_Q8_BF16 = 2, PKV_Q8_F16 = 3 } pkv_dtype;
+ * out in bf16 / fp16), see kv_cache_write_q8.  PKV_B8_BF16 / PKV_B8_F16: 8-bit
+ * cache with one fp32 scale per block and kv head, see kv_cache_write_b8. */
+typedef enum pkv_dtype {
+    PKV_F16 = 0,
+    PKV_BF16 = 1,
+    PKV_Q8_BF16 = 2,
+    PKV_Q8_F16 = 3,
+    PKV_B8_BF16 = 4,
+    PKV_B8_F16 = 5
+} pkv_dtype;
 
 typedef enum pkv_status {
     PKV_OK = 0,
@@ -80,6 +88,7 @@ typedef enum pkv_status {
 #define PKV_DEV_BAD_BLOCK 0x2   /* attention: table entry outside [0, num_blocks)   */
 #define PKV_DEV_BAD_LEN   0x4   /* attention: context_len < 0 or longer than table  */
 #define PKV_DEV_TIMEOUT   0x8   /* a bounded wait inside a kernel ran out           */
+#define PKV_DEV_BAD_POS   0x10  /* rotated append: position outside the cos/sin table */
 
 typedef struct pkv_pool pkv_pool;
 
@@ -214,8 +223,8 @@ int kv_append_slots_cow(pkv_pool *pool, int32_t num_seqs, const int32_t *seq_len
  * device int32 [n]; destinations must differ from each other and from every
  * source (kv_append_slots_cow guarantees it: they are fresh blocks).  A pair
  * naming a block outside the pool is skipped and sets PKV_DEV_BAD_BLOCK.
- * 8-bit pools: k_pool is the record pool, v_pool is ignored (may be NULL); a
- * block is its num_kv_heads records.
+ * 8-bit pools (either kind): k_pool is the record pool, v_pool is ignored (may
+ * be NULL); a block is its num_kv_heads records.
  * Asynchronous on stream.  Errors: PKV_ERR_INVALID_ARG, PKV_ERR_CUDA. */
 int kv_block_copy(const pkv_pool *pool, const int32_t *src_ids, const int32_t *dst_ids,
                   int32_t n, void *k_pool, void *v_pool, int32_t *d_status, void *stream);
@@ -277,7 +286,8 @@ int paged_decode_attention_q8(const pkv_pool *pool, void *out, const void *q, co
  * staging layout: [n][2 (K, V)][num_kv_heads][block_size][head_dim], pool dtype,
  * device memory, 16-byte aligned, 2 * n * block bytes.  8-bit pools: k_pool is
  * the record pool, v_pool is ignored (may be NULL), staging is
- * [n][num_kv_heads][PKV_Q8_SLAB_BYTES] bytes.  ids: device int32 [n].
+ * [n][num_kv_heads][PKV_Q8_SLAB_BYTES] bytes (block-scaled pools:
+ * PKV_B8_RECORD_BYTES(head_dim)).  ids: device int32 [n].
  * Ids outside the pool are skipped and set PKV_DEV_BAD_BLOCK.  Asynchronous.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_CUDA. */
 int kv_gather_blocks(const pkv_pool *pool, const int32_t *ids, int32_t n, const void *k_pool,
@@ -502,6 +512,150 @@ int paged_decode_attention_noalloc(const pkv_pool *pool, void *out, const void *
                                    const int32_t *context_lens, int32_t num_seqs,
                                    int32_t num_q_heads, float scale, int32_t *d_status,
                                    void *stream);
+
+/* ------------------------------------------- appending with the rotation
+ * (An addition of this library: the source pages have no counterpart.)
+ *
+ * Models that encode positions by rotating pairs of a head's dimensions need
+ * each new K (and q) rotated by its token's position before the cache write.
+ * kv_cache_write_rope does both in one launch: it stores num_tokens tokens' K
+ * and V into their slots as kv_cache_write (16-bit pools) or kv_cache_write_b8
+ * (block-scaled 8-bit pools: k_pool is the record pool, v_pool is ignored)
+ * would, K rotated on the way, and writes the rotated queries to q_out.
+ *
+ * With half = rotary_dim / 2, c = cos_sin[p][i], s = cos_sin[p][half + i], p =
+ * positions[t], every head's row x becomes, for i < half,
+ *   interleaved == 0:  (x[i], x[i + half])    -> (x[i] c - x[i + half] s, x[i + half] c + x[i] s)
+ *   interleaved != 0:  (x[2i], x[2i + 1])     -> (x[2i] c - x[2i + 1] s, x[2i + 1] c + x[2i] s)
+ * in fp32 (every product and sum rounded by itself), rounded once; dimensions
+ * from rotary_dim on are unchanged, and so is V.
+ *   q, q_out        rows [num_tokens][num_q_heads][head_dim] in the pool's row
+ *                   type; num_q_heads == 0: no queries (both ignored).  q_out
+ *                   may be q (same stride): rotated in place.
+ *   k_new, v_new    rows [num_tokens][num_kv_heads][head_dim]
+ *   *_stride        elements from one token's row to the next (a fused
+ *                   projection's slices need no copy); a multiple of 8, at
+ *                   least heads * head_dim
+ *   positions       device int32 [num_tokens]
+ *   cos_sin         device fp32 [max_positions][rotary_dim]
+ *   slot_mapping    as in kv_cache_write
+ * A token with a negative slot is skipped: neither its K and V nor its query
+ * row is written.  So is one whose slot or position is out of range, which also
+ * sets PKV_DEV_BAD_SLOT / PKV_DEV_BAD_POS.  All device pointers 16-byte aligned
+ * (positions and status 4, slots 8).  16-bit pools of any block_size.
+ * Errors: PKV_ERR_INVALID_ARG (rotary_dim < 16 or beyond head_dim, sizes,
+ * strides, alignment, an 8-bit pool with one scale per 32 values),
+ * PKV_ERR_UNSUPPORTED (rotary_dim or head_dim not a multiple of 16; 8-bit pools
+ * of other shapes than kv_cache_write_b8 takes), PKV_ERR_CUDA. */
+int kv_cache_write_rope(const pkv_pool *pool, void *q_out, int64_t q_out_stride, const void *q,
+                        int64_t q_stride, int32_t num_q_heads, const void *k_new,
+                        int64_t k_stride, const void *v_new, int64_t v_stride,
+                        const int32_t *positions, const float *cos_sin, int32_t max_positions,
+                        int32_t rotary_dim, int32_t interleaved, const int64_t *slot_mapping,
+                        int32_t num_tokens, void *k_pool, void *v_pool, int32_t *d_status,
+                        void *stream);
+
+/* ---------------------------------------- 8-bit cache, one scale per block
+ * (An addition of this library; "kv-cache-by-model", section 1, gives the 8-bit
+ * cache with a scale per 32 values.)
+ *
+ * PKV_B8_BF16 / PKV_B8_F16 pools store K and V as one-byte codes with one fp32
+ * scale for each block of 16 tokens, kv head and K or V: 4,128 bytes per block
+ * and head of 128 dimensions (50.4 % of 16 bits; a scale per 32 values takes
+ * 53.1 %).  head_dim 64 or 128, block_size 16.  The pool is one record of
+ * PKV_B8_RECORD_BYTES(head_dim) bytes per (block, kv head), records in the
+ * order [num_blocks][num_kv_heads], D = head_dim:
+ *   bytes [0, 16 D)        K codes
+ *   bytes [16 D, 32 D)     V codes
+ *   bytes [32 D, 32 D + 8) fp32 scale of K, fp32 scale of V; then 24 unused bytes
+ * A code c (-127 .. 127) is stored as the byte c + 128.  16-byte chunk j
+ * (dimensions 16 j .. 16 j + 15) of token t sits at byte
+ *   128 * (t * D / 128) + 16 * (j XOR 4 (t mod 2) XOR 2 (t / 2 mod 4))
+ * of the K (V) codes.  The cached value is code * scale.
+ *
+ * A block's scale is its largest |x| / 127 (times rn(1 / 127) in fp32), over all
+ * tokens written to it since it was begun: the token at offset 0 of a block
+ * begins it anew (what the record held before does not count), and a later
+ * token with a larger value raises the scale, whereupon the codes of the tokens
+ * before it are rounded to the new scale, rn(code * rn(old / new)).  A new
+ * token's code is clamp(rn(x * rn(1 / scale)), -127, 127), ties to even; NaN
+ * stores 0, an infinity counts as the largest bf16; a block whose largest value
+ * is below 2^-100 stores zeros. */
+#define PKV_B8_RECORD_BYTES(head_dim) (32 * (head_dim) + 32)
+
+/* Quantising append: k_new / v_new rows [num_tokens][Hkv][head_dim] in bf16
+ * (PKV_B8_BF16) or fp16 (PKV_B8_F16), 16-byte aligned; slots as in
+ * kv_cache_write.  The tokens that one call adds to a block must be neighbours
+ * in slot_mapping, their slots rising by one (as kv_append_slots lists them),
+ * and a block's tokens come in order, call after call; a call that names one
+ * block in two places leaves that block's contents unspecified.
+ * Errors: PKV_ERR_INVALID_ARG (not a block-scaled pool, alignment),
+ * PKV_ERR_UNSUPPORTED (head_dim other than 64 or 128, block_size other than
+ * 16), PKV_ERR_CUDA.  Slots outside the pool: PKV_DEV_BAD_SLOT. */
+int kv_cache_write_b8(const pkv_pool *pool, const void *k_new, const void *v_new,
+                      const int64_t *slot_mapping, int32_t num_tokens, void *kv_b8,
+                      int32_t *d_status, void *stream);
+
+/* Blocks ids[0 .. n) of a block-scaled pool as 16-bit rows: k_out[i] and v_out[i]
+ * ([n][num_kv_heads][16][head_dim], the pool's row type, 16-byte aligned) receive
+ * code * scale of block ids[i], rounded once.  That is the layout of a 16-bit
+ * pool of n blocks, so paged_prefill_attention can run a chunk over an 8-bit
+ * prefix.  Ids outside the pool are skipped and set PKV_DEV_BAD_BLOCK; an id may
+ * occur several times.  Asynchronous.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA. */
+int kv_dequantize_blocks(const pkv_pool *pool, const int32_t *ids, int32_t n, const void *kv_b8,
+                         void *k_out, void *v_out, int32_t *d_status, void *stream);
+
+/* Paged decode attention over a block-scaled 8-bit cache: the result of
+ * paged_decode_attention with K and V taken as code * scale.  q and out in the
+ * pool's row type; G <= 16.  window > 0 with sinks: only the tokens that
+ * paged_decode_attention_window would attend to; window == 0: the whole context.
+ * No workspace; one launch.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA. */
+int paged_decode_attention_b8(const pkv_pool *pool, void *out, const void *q, const void *kv_b8,
+                              const int32_t *block_tables, int32_t max_blocks_per_seq,
+                              const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads,
+                              float scale, int32_t window, int32_t sinks, int32_t *d_status,
+                              void *stream);
+
+/* ------------------------------------------------ sliding window and sinks
+ * (An addition of this library: the source pages have no counterpart.)
+ *
+ * A query at position p attends to its last `window` tokens (itself included)
+ * and to the sequence's first `sinks` tokens:
+ *   j <= p  and  (j > p - window  or  j < sinks)
+ * window >= 1, sinks >= 0; a window as long as the context is plain attention.
+ * Table entries of blocks without a visible token are not read (a program may
+ * have given those blocks back), and nothing that hidden tokens hold, NaN
+ * included, reaches a result. */
+
+/* paged_decode_attention under that mask (the query of sequence s sits at
+ * position context_lens[s] - 1).  16-bit pools, head_dim 64 or 128, block_size
+ * 16, G <= 16.  No workspace; one launch.  Sequences with context_len == 0 get
+ * zero rows; a bad length or a bad table entry of a visible block gives a zero
+ * row and a status bit.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA. */
+int paged_decode_attention_window(const pkv_pool *pool, void *out, const void *q,
+                                  const void *k_pool, const void *v_pool,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t *context_lens, int32_t num_seqs,
+                                  int32_t num_q_heads, float scale, int32_t window, int32_t sinks,
+                                  int32_t *d_status, void *stream);
+
+/* paged_prefill_attention under that mask: query j of sequence s's chunk at
+ * position p = context_lens[s] - C_s + j.  Arguments, workspace
+ * (paged_prefill_workspace_bytes) and errors as paged_prefill_attention; room
+ * for the fp16 copy of V is not used.  A token that some queries of a tile of
+ * neighbouring queries (2 * (128 / G) tokens) see is hidden from the others by
+ * a weight of zero: a NaN or infinity in its V reaches them all the same, as
+ * the causal call's later tokens of the chunk do. */
+int paged_prefill_attention_window(const pkv_pool *pool, void *out, const void *q,
+                                   const void *k_pool, const void *v_pool,
+                                   const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t *query_start, const int32_t *context_lens,
+                                   int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
+                                   float scale, int32_t window, int32_t sinks, void *workspace,
+                                   size_t workspace_bytes, int32_t *d_status, void *stream);
 
 /* ------------------------------------------------------------ status word */
 

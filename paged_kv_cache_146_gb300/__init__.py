@@ -21,23 +21,29 @@ import ctypes
 import numpy as np
 
 from . import _native
-from ._native import (DEV_BAD_BLOCK, DEV_BAD_LEN, DEV_BAD_SLOT, DEV_TIMEOUT, PKV_BF16, PKV_F16,
-                      PKV_Q8_BF16, PKV_Q8_F16, PagedKVError, check, lib)
+from ._native import (DEV_BAD_BLOCK, DEV_BAD_LEN, DEV_BAD_POS, DEV_BAD_SLOT, DEV_TIMEOUT,
+                      PKV_B8_BF16, PKV_B8_F16, PKV_BF16, PKV_F16, PKV_Q8_BF16, PKV_Q8_F16,
+                      PagedKVError, check, lib)
 
 __all__ = ["KVPool", "PagedKVError", "cache_write", "block_copy", "gather_blocks",
            "scatter_blocks", "paged_decode_attention", "CapturedDecode",
            "paged_decode_attention_noalloc", "paged_prefill_attention",
            "decode_plan", "decode_plan_bytes", "paged_decode_attention_planned",
            "cache_write_q8", "paged_decode_attention_q8",
+           "cache_write_rope", "rope_table", "cache_write_b8", "dequantize_blocks",
+           "paged_decode_attention_b8", "paged_decode_attention_window",
+           "paged_prefill_attention_window",
            "prefill_workspace_bytes",
            "decode_workspace_bytes", "status_check", "kv_bytes_per_token",
            "kv_blocks_for_tokens", "kv_pool_bytes", "default_split", "lib",
-           "DEV_BAD_SLOT", "DEV_BAD_BLOCK", "DEV_BAD_LEN", "DEV_TIMEOUT"]
+           "DEV_BAD_SLOT", "DEV_BAD_BLOCK", "DEV_BAD_LEN", "DEV_TIMEOUT", "DEV_BAD_POS"]
 
 _DTYPES = {"f16": PKV_F16, "fp16": PKV_F16, "float16": PKV_F16,
            "bf16": PKV_BF16, "bfloat16": PKV_BF16,
-           "q8_bf16": PKV_Q8_BF16, "q8_f16": PKV_Q8_F16}
-_NAMES = {PKV_F16: "f16", PKV_BF16: "bf16", PKV_Q8_BF16: "q8_bf16", PKV_Q8_F16: "q8_f16"}
+           "q8_bf16": PKV_Q8_BF16, "q8_f16": PKV_Q8_F16,
+           "b8_bf16": PKV_B8_BF16, "b8_f16": PKV_B8_F16}
+_NAMES = {PKV_F16: "f16", PKV_BF16: "bf16", PKV_Q8_BF16: "q8_bf16", PKV_Q8_F16: "q8_f16",
+          PKV_B8_BF16: "b8_bf16", PKV_B8_F16: "b8_f16"}
 
 
 def _np_ptr(a: np.ndarray):
@@ -116,8 +122,8 @@ def _torch_int32():
 
 def _check_pool_tensor(name: str, t, pool: "KVPool") -> None:
     """A caller-supplied pool tensor must hold the pool's whole geometry."""
-    if pool.is_q8:
-        want, dt = pool.num_blocks * pool.num_kv_heads * _native.PKV_Q8_SLAB_BYTES, None
+    if pool.record_bytes:
+        want, dt = pool.num_blocks * pool.num_kv_heads * pool.record_bytes, None
     else:
         want = pool.num_blocks * pool.num_kv_heads * pool.block_size * pool.head_dim
         dt = _torch_dtype(pool.dtype_code)
@@ -158,7 +164,7 @@ def _torch_dtype(code: int):
     """Element type of K/V rows and queries for a pool type (8-bit pools take
     bf16 / fp16 rows and quantise them)."""
     import torch
-    return torch.bfloat16 if code in (PKV_BF16, PKV_Q8_BF16) else torch.float16
+    return torch.bfloat16 if code in (PKV_BF16, PKV_Q8_BF16, PKV_B8_BF16) else torch.float16
 
 
 # ------------------------------------------------------------------ sizing
@@ -191,6 +197,10 @@ class KVPool:
     values; head_dim 128, block_size 16) the device pool is ``kv`` uint8
     [num_blocks][num_kv_heads][4352]: one record per slab holding K codes, V codes
     and both scale runs (layout in include/pagedkv.h).
+
+    With ``dtype="b8_bf16"`` or ``"b8_f16"`` (8-bit cache, one fp32 scale per block,
+    kv head and K or V; head_dim 64 or 128, block_size 16) ``kv`` is uint8
+    [num_blocks][num_kv_heads][32 * head_dim + 32], one record per (block, kv head).
     """
 
     def __init__(self, num_blocks: int, num_kv_heads: int, head_dim: int, dtype: str = "bf16",
@@ -200,6 +210,10 @@ class KVPool:
         self.dtype_code = _DTYPES[dtype]
         self.dtype = _NAMES[self.dtype_code]
         self.is_q8 = self.dtype_code in (PKV_Q8_BF16, PKV_Q8_F16)
+        self.is_b8 = self.dtype_code in (PKV_B8_BF16, PKV_B8_F16)
+        # bytes of one (block, kv head) record; 0: separate 16-bit K and V pools
+        self.record_bytes = (_native.PKV_Q8_SLAB_BYTES if self.is_q8 else
+                             32 * head_dim + 32 if self.is_b8 else 0)
         order = None
         if free_order is not None:
             order = np.ascontiguousarray(free_order, dtype=np.int32)
@@ -213,8 +227,8 @@ class KVPool:
         self.k_pool = self.v_pool = self.kv = None
         if device is not None:
             import torch
-            if self.is_q8:
-                self.kv = torch.empty((num_blocks, num_kv_heads, _native.PKV_Q8_SLAB_BYTES),
+            if self.record_bytes:
+                self.kv = torch.empty((num_blocks, num_kv_heads, self.record_bytes),
                                       dtype=torch.uint8, device=device)
             else:
                 shape = (num_blocks, num_kv_heads, block_size, head_dim)
@@ -315,7 +329,7 @@ class KVPool:
 # ------------------------------------------------------------------ device ops
 def _pools(pool: KVPool, k_pool, v_pool):
     """Device pools of a call: (K, V), or (records, None) for an 8-bit pool."""
-    if pool.is_q8:
+    if pool.record_bytes:
         return (pool.kv if k_pool is None else k_pool), None
     return (pool.k_pool if k_pool is None else k_pool), (pool.v_pool if v_pool is None else v_pool)
 
@@ -376,7 +390,7 @@ def _check_block_pools(pool: KVPool, ids, status, k_pool, v_pool, staging=None) 
             pools.append((name, t))
     if staging is not None:
         _check_vector("ids", ids, None, None)
-        per_block = (pool.num_kv_heads * _native.PKV_Q8_SLAB_BYTES if pool.is_q8 else
+        per_block = (pool.num_kv_heads * pool.record_bytes if pool.record_bytes else
                      2 * pool.num_kv_heads * pool.block_size * pool.head_dim * 2)
         if staging.numel() * staging.element_size() < int(ids.shape[0]) * per_block:
             raise ValueError(f"staging holds fewer than {int(ids.shape[0])} blocks of "
@@ -387,7 +401,7 @@ def _check_block_pools(pool: KVPool, ids, status, k_pool, v_pool, staging=None) 
 
 def gather_blocks(pool: KVPool, ids, staging, status, k_pool=None, v_pool=None, stream=None):
     """Pack blocks ``ids`` (int32 device tensor) into ``staging`` (device,
-    [n][2][Hkv][16][D] in the pool dtype; 8-bit pools [n][Hkv][4352] bytes) for
+    [n][2][Hkv][16][D] in the pool dtype; 8-bit pools [n][Hkv][record bytes]) for
     one host copy (swap out)."""
     _check_layout({"ids": ids, "staging": staging}, int32={"ids": ids})
     k_pool, v_pool = _pools(pool, k_pool, v_pool)
@@ -668,6 +682,294 @@ def paged_decode_attention_q8(pool: KVPool, q, block_tables, context_lens, scale
                                           _t_ptr(context_lens), S, hq, float(scale),
                                           _t_ptr(workspace), nbytes, _t_ptr(status),
                                           _stream(stream)), "paged_decode_attention_q8")
+    return out
+
+
+# --------------------------------------- rotated append, 8-bit blocks, windows
+# The calls below are also made for a few rows at a time, where the host side is
+# most of their time: their checks read each attribute once.
+def _on_device(device, stream):
+    """(context, raw stream) of a launch: ``stream`` or the current stream of the
+    tensors' device, which is made current for the call if it is not."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"the call's tensors must be CUDA tensors, got {device}")
+    here = torch.cuda.current_device()
+    index = here if device.index is None else device.index
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        raw = stream if isinstance(stream, int) else stream.cuda_stream
+    return (None if here == index else torch.cuda.device(index)), raw
+
+
+def _launch(name: str, device, stream, *args) -> None:
+    """Call the library's ``name`` with ``args`` and the stream as last argument."""
+    guard, raw = _on_device(device, stream)
+    fn = getattr(lib(), name)
+    if guard is None:
+        rc = fn(*args, raw)
+    else:
+        with guard:
+            rc = fn(*args, raw)
+    if rc:
+        check(rc, name)
+
+
+def _want(name: str, t, shape: tuple, dtype, device, contiguous: bool = True) -> int:
+    """Check a tensor of the call; its address."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}, got "
+                        f"{str(t.dtype).replace('torch.', '')}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's rows are on {device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _want_rows(name: str, t, shape: tuple, dtype, device):
+    """Check rows [T][H][D] whose tokens may lie apart (slices of a fused
+    projection); their address and token stride in elements."""
+    ptr = _want(name, t, shape, dtype, device, False)
+    T, H, D = shape
+    s, sh, sd = t.stride()
+    if T > 0 and H > 0 and (sd != 1 or (sh != D and H > 1)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if T <= 1:
+        return ptr, H * D
+    if s < H * D or s % 8:
+        raise ValueError(f"{name}: the token stride must be a multiple of 8 and at least "
+                         f"{H * D}, got {s}")
+    return ptr, s
+
+
+def _want_status(status, device) -> int:
+    if status.dtype != _torch_int32() or status.numel() < 1:
+        raise TypeError("status must be an int32 tensor of at least one element")
+    if status.device != device:
+        raise ValueError(f"status is on {status.device}, the call's rows are on {device}")
+    return status.data_ptr()
+
+
+def _want_pools(pool: KVPool, device, k_pool=None, v_pool=None, kv=None):
+    """Addresses of the call's device pools: (K, V), or (records, 0)."""
+    import torch
+    if pool.record_bytes:
+        if not pool.is_b8:
+            raise ValueError("the call takes 16-bit and block-scaled 8-bit pools")
+        kv = pool.kv if kv is None else kv
+        if kv is None:
+            raise ValueError("the pool has no device memory")
+        return _want("kv", kv, (pool.num_blocks, pool.num_kv_heads, pool.record_bytes),
+                     torch.uint8, device), 0
+    k_pool = pool.k_pool if k_pool is None else k_pool
+    v_pool = pool.v_pool if v_pool is None else v_pool
+    if k_pool is None or v_pool is None:
+        raise ValueError("the pool has no device memory")
+    shape = (pool.num_blocks, pool.num_kv_heads, pool.block_size, pool.head_dim)
+    dt = _torch_dtype(pool.dtype_code)
+    return _want("k_pool", k_pool, shape, dt, device), _want("v_pool", v_pool, shape, dt, device)
+
+
+def rope_table(max_positions: int, rotary_dim: int, base: float = 10000.0, device=None):
+    """cos/sin table of ``cache_write_rope``: fp32 [max_positions][rotary_dim], row p
+    = the cosines, then the sines, of p * base^(-2 i / rotary_dim), i <
+    rotary_dim / 2, computed in fp64."""
+    import torch
+    if max_positions < 1 or rotary_dim < 16 or rotary_dim % 16:
+        raise ValueError("max_positions >= 1 and rotary_dim a multiple of 16")
+    half = rotary_dim // 2
+    freq = float(base) ** (-torch.arange(half, dtype=torch.float64) / half)
+    angle = torch.arange(max_positions, dtype=torch.float64)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).to(torch.float32).to(device)
+
+
+def cache_write_rope(pool: KVPool, k_new, v_new, positions, cos_sin, slot_mapping, status, q=None,
+                     q_out=None, interleaved: bool = False, k_pool=None, v_pool=None, kv=None,
+                     stream=None):
+    """Append tokens with their K (and queries) rotated by position, one launch.
+
+    ``k_new``/``v_new`` [T][Hkv][D] and ``q`` [T][Hq][D] device rows in the pool's
+    row type, tokens any stride apart (slices of a fused projection); ``positions``
+    int32 [T]; ``cos_sin`` fp32 [max_positions][rotary_dim] (``rope_table``);
+    ``slot_mapping`` int64 [T], negative = no token.  K and V go to their slots of a
+    16-bit pool or a block-scaled 8-bit pool; the rotated queries to ``q_out``
+    (default: a new tensor; ``q`` itself: in place), which is returned.  Rows of
+    skipped tokens in ``q_out`` are left as they were.  ``interleaved``: pairs of
+    neighbouring dimensions instead of the halves' (i, i + rotary_dim / 2)."""
+    import torch
+    device = k_new.device
+    dt, D, Hkv = _torch_dtype(pool.dtype_code), pool.head_dim, pool.num_kv_heads
+    T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
+    slots = _want("slot_mapping", slot_mapping, (T,), torch.int64, device)
+    k, ks = _want_rows("k_new", k_new, (T, Hkv, D), dt, device)
+    v, vs = _want_rows("v_new", v_new, (T, Hkv, D), dt, device)
+    pos = _want("positions", positions, (T,), torch.int32, device)
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [max_positions][rotary_dim]")
+    rows, rot = cos_sin.shape
+    table = _want("cos_sin", cos_sin, (rows, rot), torch.float32, device)
+    qp = qs = qo = qos = hq = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError(f"q must be [{T}][h][{D}], got {list(q.shape)}")
+        hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, hq, D), dtype=dt, device=device)
+        qp, qs = _want_rows("q", q, (T, hq, D), dt, device)
+        qo, qos = _want_rows("q_out", q_out, (T, hq, D), dt, device)
+        if qp == qo and qs != qos:
+            raise ValueError("q_out over q needs the same token stride")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    kp, vp = _want_pools(pool, device, k_pool, v_pool, kv)
+    _launch("kv_cache_write_rope", device, stream, pool.handle, qo, qos, qp, qs, hq, k, ks, v, vs,
+            pos, table, rows, rot, 1 if interleaved else 0, slots, T, kp, vp,
+            _want_status(status, device))
+    return q_out
+
+
+def cache_write_b8(pool: KVPool, k_new, v_new, slot_mapping, status, kv=None, stream=None) -> None:
+    """Quantising append into a block-scaled 8-bit pool: contiguous rows
+    ``k_new``/``v_new`` [T][Hkv][D] go to their slots; a block's scale covers the
+    largest value written to it since its first token, and the codes before the new
+    tokens are rounded to it when it grows.  The tokens of one block are neighbours
+    in ``slot_mapping``, slots rising by one (as the ledger hands them out)."""
+    import torch
+    device = k_new.device
+    if not pool.is_b8:
+        raise ValueError("cache_write_b8 takes a block-scaled 8-bit pool")
+    dt, shape = _torch_dtype(pool.dtype_code), (pool.num_kv_heads, pool.head_dim)
+    T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
+    slots = _want("slot_mapping", slot_mapping, (T,), torch.int64, device)
+    k = _want("k_new", k_new, (T, *shape), dt, device)
+    v = _want("v_new", v_new, (T, *shape), dt, device)
+    rec, _ = _want_pools(pool, device, kv=kv)
+    _launch("kv_cache_write_b8", device, stream, pool.handle, k, v, slots, T, rec,
+            _want_status(status, device))
+
+
+def dequantize_blocks(pool: KVPool, ids, k_out, v_out, status, kv=None, stream=None):
+    """Blocks ``ids`` (int32 device [n]) of a block-scaled 8-bit pool as 16-bit rows:
+    ``k_out``/``v_out`` [n][Hkv][16][D] in the pool's row type (the layout of a 16-bit
+    pool of n blocks).  Returns (k_out, v_out)."""
+    import torch
+    device = ids.device
+    if not pool.is_b8:
+        raise ValueError("dequantize_blocks takes a block-scaled 8-bit pool")
+    n = ids.shape[0] if ids.dim() == 1 else -1
+    i = _want("ids", ids, (n,), torch.int32, device)
+    dt, shape = _torch_dtype(pool.dtype_code), (n, pool.num_kv_heads, 16, pool.head_dim)
+    k = _want("k_out", k_out, shape, dt, device)
+    v = _want("v_out", v_out, shape, dt, device)
+    rec, _ = _want_pools(pool, device, kv=kv)
+    _launch("kv_dequantize_blocks", device, stream, pool.handle, i, n, rec, k, v,
+            _want_status(status, device))
+    return k_out, v_out
+
+
+def _decode_call(name: str, pool: KVPool, q, out, block_tables, context_lens, scale, window, sinks,
+                 status, k_pool, v_pool, kv, stream):
+    """Checks and launch of the workspace-free decode calls."""
+    import torch
+    device, dt, D = q.device, _torch_dtype(pool.dtype_code), pool.head_dim
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError(f"q must be [n][h][{D}], got {list(q.shape)}")
+    S, hq, _ = shape = tuple(q.shape)
+    if hq % pool.num_kv_heads:
+        raise ValueError(f"q has {hq} heads, not a multiple of the pool's "
+                         f"{pool.num_kv_heads} kv heads")
+    qp = _want("q", q, shape, dt, device)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=device)
+    op = _want("out", out, shape, dt, device)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must have 2 dimensions")
+    maxb = block_tables.shape[1]
+    tp = _want("block_tables", block_tables, (S, maxb), torch.int32, device)
+    lp = _want("context_lens", context_lens, (S,), torch.int32, device)
+    kp, vp = _want_pools(pool, device, k_pool, v_pool, kv)
+    pools = (kp,) if pool.is_b8 else (kp, vp)
+    _launch(name, device, stream, pool.handle, op, qp, *pools, tp, maxb, lp, S, hq, scale,
+            window, sinks, _want_status(status, device))
+    return out
+
+
+def _window(window, sinks):
+    window, sinks = int(window), int(sinks)
+    if window < 1 or sinks < 0 or window > 0x7fffffff or sinks > 0x7fffffff:
+        raise ValueError(f"window >= 1 and sinks >= 0 (32 bits), got {window} and {sinks}")
+    return window, sinks
+
+
+def paged_decode_attention_window(pool: KVPool, q, block_tables, context_lens, scale: float,
+                                  window: int, sinks: int, status, out=None, k_pool=None,
+                                  v_pool=None, stream=None):
+    """Decode attention over each sequence's last ``window`` tokens and its first
+    ``sinks`` tokens (16-bit pools; ``paged_decode_attention_b8`` has the same for
+    block-scaled 8-bit pools).  Arguments as ``paged_decode_attention``, without a
+    workspace; table entries of blocks without a visible token are not read."""
+    if pool.record_bytes:
+        raise ValueError("paged_decode_attention_window takes a 16-bit pool")
+    window, sinks = _window(window, sinks)
+    return _decode_call("paged_decode_attention_window", pool, q, out, block_tables, context_lens,
+                        scale, window, sinks, status, k_pool, v_pool, None, stream)
+
+
+def paged_decode_attention_b8(pool: KVPool, q, block_tables, context_lens, scale: float, status,
+                              window: int | None = None, sinks: int = 0, out=None, kv=None,
+                              stream=None):
+    """Decode attention over a block-scaled 8-bit pool (head_dim 64 or 128, G <= 16),
+    over the whole context or, with ``window``, over the last ``window`` and the first
+    ``sinks`` tokens.  ``q`` and the result in bf16 (b8_bf16) or fp16 (b8_f16); no
+    workspace."""
+    if not pool.is_b8:
+        raise ValueError("paged_decode_attention_b8 takes a block-scaled 8-bit pool")
+    if window is None:
+        if sinks:
+            raise ValueError("sinks without a window")
+        window = 0
+    else:
+        window, sinks = _window(window, sinks)
+    return _decode_call("paged_decode_attention_b8", pool, q, out, block_tables, context_lens,
+                        scale, window, sinks, status, None, None, kv, stream)
+
+
+def paged_prefill_attention_window(pool: KVPool, q, block_tables, query_start, context_lens,
+                                   scale: float, window: int, sinks: int, workspace, status,
+                                   out=None, k_pool=None, v_pool=None, stream=None):
+    """``paged_prefill_attention`` where a query at position p attends to tokens p -
+    window + 1 .. p and to the first ``sinks`` tokens (16-bit pools).  Workspace of
+    ``prefill_workspace_bytes(S, T, Hq, Hkv)`` bytes."""
+    import torch
+    if pool.record_bytes:
+        raise ValueError("paged_prefill_attention_window takes a 16-bit pool")
+    window, sinks = _window(window, sinks)
+    device, dt, D = q.device, _torch_dtype(pool.dtype_code), pool.head_dim
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError(f"q must be [n][h][{D}], got {list(q.shape)}")
+    T, hq, _ = shape = tuple(q.shape)
+    if hq % pool.num_kv_heads:
+        raise ValueError(f"q has {hq} heads, not a multiple of the pool's "
+                         f"{pool.num_kv_heads} kv heads")
+    qp = _want("q", q, shape, dt, device)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=device)
+    op = _want("out", out, shape, dt, device)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must have 2 dimensions")
+    S, maxb = block_tables.shape
+    tp = _want("block_tables", block_tables, (S, maxb), torch.int32, device)
+    lp = _want("context_lens", context_lens, (S,), torch.int32, device)
+    sp = _want("query_start", query_start, (S + 1,), torch.int32, device)
+    nbytes = workspace.numel()
+    wp = _want("workspace", workspace, (nbytes,), torch.uint8, device)
+    kp, vp = _want_pools(pool, device, k_pool, v_pool)
+    _launch("paged_prefill_attention_window", device, stream, pool.handle, op, qp, kp, vp, tp, maxb,
+            sp, lp, S, T, hq, scale, window, sinks, wp, nbytes, _want_status(status, device))
     return out
 
 

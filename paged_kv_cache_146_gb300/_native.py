@@ -12,7 +12,7 @@ import threading
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("PKV_LIBRARY") or os.path.join(PKG, "libpagedkv.so")
 
-PKV_F16, PKV_BF16, PKV_Q8_BF16, PKV_Q8_F16 = 0, 1, 2, 3
+PKV_F16, PKV_BF16, PKV_Q8_BF16, PKV_Q8_F16, PKV_B8_BF16, PKV_B8_F16 = 0, 1, 2, 3, 4, 5
 PKV_OK = 0
 PKV_Q8_SLAB_BYTES = 4352
 STATUS_NAMES = {
@@ -20,7 +20,7 @@ STATUS_NAMES = {
     -3: "PKV_ERR_BAD_BLOCK", -4: "PKV_ERR_CUDA", -5: "PKV_ERR_DEVICE_BOUNDS",
     -6: "PKV_ERR_DEVICE_TIMEOUT", -7: "PKV_ERR_SHARED_BLOCK", -8: "PKV_ERR_UNSUPPORTED",
 }
-DEV_BAD_SLOT, DEV_BAD_BLOCK, DEV_BAD_LEN, DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+DEV_BAD_SLOT, DEV_BAD_BLOCK, DEV_BAD_LEN, DEV_TIMEOUT, DEV_BAD_POS = 0x1, 0x2, 0x4, 0x8, 0x10
 
 # (name, restype, argtypes) of every symbol the header declares
 _i32, _i64, _sz, _f32, _p = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float, ctypes.c_void_p
@@ -67,6 +67,17 @@ SIGNATURES = [
     ("kv_cache_write_q8", ctypes.c_int, [_p, _p, _p, _p, _i32, _p, _p, _p]),
     ("paged_decode_attention_q8", ctypes.c_int,
      [_p, _p, _p, _p, _p, _i32, _p, _i32, _i32, _f32, _p, _sz, _p, _p]),
+    ("kv_cache_write_rope", ctypes.c_int,
+     [_p, _p, _i64, _p, _i64, _i32, _p, _i64, _p, _i64, _p, _p, _i32, _i32, _i32, _p, _i32, _p, _p,
+      _p, _p]),
+    ("kv_cache_write_b8", ctypes.c_int, [_p, _p, _p, _p, _i32, _p, _p, _p]),
+    ("kv_dequantize_blocks", ctypes.c_int, [_p, _p, _i32, _p, _p, _p, _p, _p]),
+    ("paged_decode_attention_b8", ctypes.c_int,
+     [_p, _p, _p, _p, _p, _i32, _p, _i32, _i32, _f32, _i32, _i32, _p, _p]),
+    ("paged_decode_attention_window", ctypes.c_int,
+     [_p, _p, _p, _p, _p, _p, _i32, _p, _i32, _i32, _f32, _i32, _i32, _p, _p]),
+    ("paged_prefill_attention_window", ctypes.c_int,
+     [_p, _p, _p, _p, _p, _p, _i32, _p, _p, _i32, _i32, _i32, _f32, _i32, _i32, _p, _sz, _p, _p]),
     ("kv_status_check", ctypes.c_int, [_p, _p, _pi32]),
 ]
 

@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libpagedkv.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["ledger.cpp", "cache_write.cu", "paged_decode.cu", "paged_decode_q8.cu",
-           "paged_prefill.cu"]
+           "paged_prefill.cu", "append_rope.cu", "paged_window.cu"]
 
 
 def nvcc() -> str:

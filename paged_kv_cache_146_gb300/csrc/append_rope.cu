@@ -1,0 +1,554 @@
+// Appending to the cache with the position rotation on the way, and the
+// block-scaled 8-bit pools' write and read-back.
+//
+// Rotation of one head's row x at position p (cos, sin = the table's row p,
+// half = rotary_dim / 2 entries each):
+//   halves      (x[i], x[i + half]) -> (x[i] c - x[i + half] s, x[i + half] c + x[i] s)
+//   neighbours  (x[2i], x[2i + 1])  -> (x[2i] c - x[2i + 1] s, x[2i + 1] c + x[2i] s)
+// for i < half; dimensions from rotary_dim on stay as they are.  Each product
+// and each sum is rounded to fp32 by itself (no fused multiply-add), so a
+// result does not depend on how the compiler contracts the expression; the
+// rotated value is rounded once more, to the row type (16-bit pools and
+// queries) or to a code (8-bit pools, straight from fp32).
+//
+// Every value is read once and written once, so the kernels are bound by HBM
+// (and, for a decode step's few rows, by the chain slot -> position -> table
+// row -> store and the launch).
+#include <algorithm>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "pagedkv.h"
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+namespace append {
+
+struct Params {
+    const void *q, *k, *v;               // rows; token strides below, heads contiguous
+    void *q_out;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;   // elements
+    const int32_t *positions;            // null: no rotation
+    const float *cos_sin;                // [max_positions][rotary_dim]: cos, then sin
+    const int64_t *slots;
+    int32_t num_tokens, num_q_heads, num_kv_heads, max_positions, rotary_dim;
+    int32_t block_size;
+    int64_t num_slots;
+    uint4 *k_pool, *v_pool;              // 16-bit pools
+    uint8_t *kv;                         // 8-bit records
+    int32_t *status;
+    int32_t span;                        // 8-bit write: tokens per warp (1 or 16)
+    int32_t write_blocks;                // 8-bit write: CTAs that write; the rest rotate queries
+};
+
+// A lane works on two 8-value chunks of a row.  Chunk pair i of the row: for
+// the halves form the pairs' two sides (i and i + rotary_dim / 16) while i
+// falls inside the rotated part, else two neighbouring chunks.
+struct ChunkPair {
+    int c0, c1;
+    bool turned;
+};
+
+template <bool NEIGHBOURS>
+__device__ __forceinline__ ChunkPair chunk_pair(int i, int rotary_dim)
+{
+    const int n = rotary_dim >> 4;       // chunk pairs of the rotated part
+    if (i < n) return NEIGHBOURS ? ChunkPair{2 * i, 2 * i + 1, true} : ChunkPair{i, i + n, true};
+    return ChunkPair{2 * i, 2 * i + 1, false};
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint4 &w, float *x)
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = Elem<BF16>::unpack(u[k]);
+        x[2 * k] = f.x;
+        x[2 * k + 1] = f.y;
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8(const float *x)
+{
+    using E = Elem<BF16>;
+    return make_uint4(E::pack(x[0], x[1]), E::pack(x[2], x[3]), E::pack(x[4], x[5]),
+                      E::pack(x[6], x[7]));
+}
+
+__device__ __forceinline__ void turn(float &a, float &b, float c, float s)
+{
+    const float x = a, y = b;
+    a = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+    b = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+}
+
+// Rotate the 16 values of chunk pair i in place; cs = the position's table row.
+template <bool NEIGHBOURS>
+__device__ __forceinline__ void rotate16(float (&x)[16], int i, int half, const float *cs)
+{
+    // halves: values e and 8 + e are angle 8i + e; neighbours: values 2e and
+    // 2e + 1 are angle 8i + e: either way the pair of chunks takes the table's
+    // entries 8i .. 8i + 7
+    const float4 *c4 = reinterpret_cast<const float4 *>(cs + 8 * i);
+    const float4 *s4 = reinterpret_cast<const float4 *>(cs + half + 8 * i);
+    const float4 ca = __ldg(c4), cb = __ldg(c4 + 1), sa = __ldg(s4), sb = __ldg(s4 + 1);
+    const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
+    const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if (NEIGHBOURS) turn(x[2 * e], x[2 * e + 1], c[e], s[e]);
+        else turn(x[e], x[8 + e], c[e], s[e]);
+    }
+}
+
+// 16-bit pools (and, with heads_kv = 0, the queries of an 8-bit append): one
+// thread per (token, head, chunk pair), heads in the order q, k, v.  A thread
+// reads what it writes and nothing else, so q_out may be q itself.
+template <bool BF16, bool NEIGHBOURS>
+__device__ __forceinline__ void append_rows(const Params &p, int D, int heads_kv, int64_t cta,
+                                            int64_t ctas)
+{
+    const int lanes = D >> 4;                             // chunk pairs of a row
+    const int heads = p.num_q_heads + 2 * heads_kv;
+    const int per_token = heads * lanes;
+    const int64_t total = (int64_t)p.num_tokens * per_token;
+    const int half = p.rotary_dim >> 1;
+    for (int64_t base = cta * blockDim.x; base < total; base += ctas * blockDim.x) {
+        const int64_t t0 = base / per_token;
+        const int within0 = (int)(base - t0 * per_token) + threadIdx.x;
+        const int dt = within0 / per_token;
+        const int64_t t = t0 + dt;
+        if (t >= p.num_tokens) continue;
+        const int within = within0 - dt * per_token;
+        const int head = within / lanes, i = within - head * lanes;
+        const int64_t slot = __ldg(p.slots + t);
+        const int pos = __ldg(p.positions + t);
+        const bool is_q = head < p.num_q_heads;
+        const int kvh = is_q ? 0 : (head - p.num_q_heads) % max(heads_kv, 1);
+        const bool is_k = !is_q && head < p.num_q_heads + heads_kv;
+        const ChunkPair cp = chunk_pair<NEIGHBOURS>(i, p.rotary_dim);
+        const uint16_t *row =
+            is_q ? static_cast<const uint16_t *>(p.q) + t * p.q_stride + (int64_t)head * D
+                 : (is_k ? static_cast<const uint16_t *>(p.k) + t * p.k_stride
+                         : static_cast<const uint16_t *>(p.v) + t * p.v_stride) +
+                       (int64_t)kvh * D;
+        uint4 w0 = reinterpret_cast<const uint4 *>(row)[cp.c0];
+        uint4 w1 = reinterpret_cast<const uint4 *>(row)[cp.c1];
+        if (slot < 0) continue;                           // no token here
+        if (slot >= p.num_slots || pos < 0 || pos >= p.max_positions) {
+            if (within == 0)
+                atomicOr(p.status, slot >= p.num_slots ? PKV_DEV_BAD_SLOT : PKV_DEV_BAD_POS);
+            continue;
+        }
+        if ((is_q || is_k) && cp.turned) {
+            float x[16];
+            unpack8<BF16>(w0, x);
+            unpack8<BF16>(w1, x + 8);
+            rotate16<NEIGHBOURS>(x, i, half, p.cos_sin + (int64_t)pos * p.rotary_dim);
+            w0 = pack8<BF16>(x);
+            w1 = pack8<BF16>(x + 8);
+        }
+        uint4 *dst;
+        if (is_q) {
+            dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.q_out) + t * p.q_out_stride +
+                                            (int64_t)head * D);
+        } else {
+            const int64_t block = slot / p.block_size;
+            const int64_t off = slot - block * p.block_size;
+            dst = (is_k ? p.k_pool : p.v_pool) +
+                  ((block * heads_kv + kvh) * p.block_size + off) * (D >> 3);
+        }
+        dst[cp.c0] = w0;
+        dst[cp.c1] = w1;
+    }
+}
+
+template <bool BF16, bool NEIGHBOURS>
+__global__ void __launch_bounds__(256) append_rope_kernel(const Params p, int D)
+{
+    append_rows<BF16, NEIGHBOURS>(p, D, p.num_kv_heads, blockIdx.x, gridDim.x);
+}
+
+// ------------------------------------------------------- block-scaled 8-bit pools
+// Byte of 16-byte chunk j of token t inside a record's K (or V) codes (see the
+// layout in pagedkv.h): lines of 128 bytes, chunk positions rotated so that the
+// attention kernel's wide shared-memory reads of either operand touch all banks.
+__device__ __forceinline__ int b8_chunk(int t, int j, int D)
+{
+    return ((t * D) >> 7) * 128 + ((j ^ ((t & 1) << 2) ^ (((t >> 1) & 3) << 1)) << 4);
+}
+
+// Values whose block maximum is below this store as zeros (scale 0): their
+// reciprocal scale would leave the fp32 range.
+constexpr float kB8Tiny = 0x1p-100f;
+
+// Rounding to an integer, ties to even, of |x| <= 2^22: adding 1.5 * 2^23 puts
+// the sum where the fp32 spacing is 1; its low byte is the integer's.
+__device__ __forceinline__ uint32_t round_bits(float x)
+{
+    return __float_as_uint(__fadd_rn(x, 12582912.0f));
+}
+
+// Four codes (clamped to [-127, 127]; NaN -> 0) of x * inv as stored bytes (code + 128).
+__device__ __forceinline__ uint32_t b8_codes4(const float *x, float inv)
+{
+    uint32_t b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float y = __fmul_rn(x[k], inv);
+        y = y == y ? y : 0.f;
+        b[k] = round_bits(fminf(fmaxf(y, -127.f), 127.f));
+    }
+    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410) ^
+           0x80808080u;
+}
+
+// Four stored bytes rounded to a larger scale (ratio = old / new <= 1).
+__device__ __forceinline__ uint32_t b8_rescale4(uint32_t w, float ratio)
+{
+    uint32_t b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float c = (float)((int)((w >> (8 * k)) & 0xffu) - 128);
+        b[k] = round_bits(__fmul_rn(c, ratio));
+    }
+    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410) ^
+           0x80808080u;
+}
+
+// Write K (part 0) or V (part 1) of one run of tokens t0 .. t0 + n - 1, whose
+// slots are off0, off0 + 1, ... of one block, by one warp.
+//   scale = max(scale before, amax * rn(1 / 127)),  code = rn(x * rn(1 / scale))
+// where "scale before" counts only when the run does not start the block (off0
+// > 0).  When the scale grows, the codes of tokens 0 .. off0 - 1 are rounded to
+// it: rn(code * rn(old / new)).
+// A row is D / 16 lanes of 16 values; all rows of the run stay in registers
+// between the maximum and the codes, so each value is read once.
+template <bool BF16, bool NEIGHBOURS, int D>
+__device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, int64_t t0, int n,
+                                             int64_t block, int off0, int lane)
+{
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPasses = 16 / kRows;
+    constexpr int kRecord = PKV_B8_RECORD_BYTES(D);
+    uint8_t *rec = p.kv + (block * p.num_kv_heads + h) * kRecord;
+    uint8_t *codes = rec + 16 * D * part;
+    float *scale_at = reinterpret_cast<float *>(rec + 32 * D) + part;
+    const int r = lane / kLanes, i = lane % kLanes;
+    const uint16_t *rows = part ? static_cast<const uint16_t *>(p.v) + (int64_t)h * D
+                                : static_cast<const uint16_t *>(p.k) + (int64_t)h * D;
+    const int64_t stride = part ? p.v_stride : p.k_stride;
+    const bool rotate = part == 0 && p.positions != nullptr;
+    const ChunkPair cp = rotate ? chunk_pair<NEIGHBOURS>(i, p.rotary_dim)
+                                : ChunkPair{2 * i, 2 * i + 1, false};
+    const float old = off0 > 0 ? *scale_at : 0.f;
+    uint4 w[kPasses][2];
+    int pos[kPasses];
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) {
+        const int j = k * kRows + r;
+        const bool in = j < n;
+        const uint4 *row = reinterpret_cast<const uint4 *>(rows + (t0 + (in ? j : 0)) * stride);
+        w[k][0] = in ? row[cp.c0] : make_uint4(0u, 0u, 0u, 0u);
+        w[k][1] = in ? row[cp.c1] : make_uint4(0u, 0u, 0u, 0u);
+        pos[k] = in && p.positions ? __ldg(p.positions + t0 + j) : 0;
+    }
+    float x[kPasses][16];
+    unsigned ok = 0;                     // bit k: row of pass k counts
+    float amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) {
+        if (k * kRows >= n) break;       // the same for the whole warp
+        const int j = k * kRows + r;
+        const bool good = !p.positions || (pos[k] >= 0 && pos[k] < p.max_positions);
+        if (j < n && !good && i == 0) atomicOr(p.status, PKV_DEV_BAD_POS);
+        if (j >= n || !good) continue;
+        ok |= 1u << k;
+        unpack8<BF16>(w[k][0], x[k]);
+        unpack8<BF16>(w[k][1], x[k] + 8);
+        if (cp.turned)
+            rotate16<NEIGHBOURS>(x[k], i, p.rotary_dim >> 1,
+                                 p.cos_sin + (int64_t)pos[k] * p.rotary_dim);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[k][e]));   // ignores NaN
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+    amax = amax < kB8Tiny ? 0.f : fminf(amax, 0x1.fep127f);   // an infinity takes the largest bf16
+    constexpr float kRcp127 = 0x1.020408p-7f;                 // rn(1 / 127)
+    const float fresh = __fmul_rn(amax, kRcp127);
+    const float now = fmaxf(old, fresh);
+    if (off0 > 0 && now > old) {
+        const float ratio = __fdiv_rn(old, now);
+        for (int c = lane; c < off0 * kLanes; c += 32) {
+            uint4 *at = reinterpret_cast<uint4 *>(codes + b8_chunk(c / kLanes, c % kLanes, D));
+            uint4 v = *at;
+            v.x = b8_rescale4(v.x, ratio);
+            v.y = b8_rescale4(v.y, ratio);
+            v.z = b8_rescale4(v.z, ratio);
+            v.w = b8_rescale4(v.w, ratio);
+            *at = v;
+        }
+    }
+    if (lane == 0 && now != old) *scale_at = now;
+    if (lane == 0 && off0 == 0 && now == old) *scale_at = 0.f;
+    const float inv = now > 0.f ? __fdiv_rn(1.f, now) : 0.f;
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) {
+        if (!((ok >> k) & 1u)) continue;
+        const int t = off0 + k * kRows + r;
+        *reinterpret_cast<uint2 *>(codes + b8_chunk(t, cp.c0 >> 1, D) + 8 * (cp.c0 & 1)) =
+            make_uint2(b8_codes4(x[k], inv), b8_codes4(x[k] + 4, inv));
+        *reinterpret_cast<uint2 *>(codes + b8_chunk(t, cp.c1 >> 1, D) + 8 * (cp.c1 & 1)) =
+            make_uint2(b8_codes4(x[k] + 8, inv), b8_codes4(x[k] + 12, inv));
+    }
+}
+
+// A warp takes `span` tokens (1 or 16), one kv head and K or V, and writes every
+// run that begins among its tokens.  A run is a chain of tokens whose slots
+// follow one another inside a block; lane l looks at token tb - 1 + l, so a run
+// that begins at the span's last token is seen to its end.
+template <bool BF16, bool NEIGHBOURS, int D>
+__global__ void __launch_bounds__(128) append_b8_kernel(const Params p)
+{
+    if ((int)blockIdx.x >= p.write_blocks) {              // queries only
+        append_rows<BF16, NEIGHBOURS>(p, D, 0, (int)blockIdx.x - p.write_blocks,
+                                      (int)gridDim.x - p.write_blocks);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    const int per_span = 2 * p.num_kv_heads;
+    const int64_t units = ((int64_t)p.num_tokens + p.span - 1) / p.span * per_span;
+    for (int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); u < units;
+         u += (int64_t)p.write_blocks * 4) {
+        const int64_t w = u / per_span;
+        const int rest = (int)(u - w * per_span);
+        const int part = rest & 1, h = rest >> 1;
+        const int64_t tb = w * p.span, t = tb - 1 + lane;
+        const int64_t slot = t >= 0 && t < p.num_tokens ? __ldg(p.slots + t) : -1;
+        const int64_t prev = __shfl_up_sync(kFull, slot, 1);
+        const bool valid = slot >= 0 && slot < p.num_slots;
+        const unsigned mine = p.span == 16 ? 0x1fffeu : 0x2u;
+        if ((__ballot_sync(kFull, slot >= p.num_slots) & mine) && lane == 0)
+            atomicOr(p.status, PKV_DEV_BAD_SLOT);
+        const bool linked = lane > 0 && valid && prev >= 0 && prev + 1 == slot && slot % kBlock != 0;
+        const unsigned links = __ballot_sync(kFull, linked);
+        unsigned leads = __ballot_sync(kFull, valid && !linked) & mine;
+        while (leads) {
+            const int l = __ffs(leads) - 1;
+            leads &= leads - 1;
+            const int64_t s0 = __shfl_sync(kFull, slot, l);
+            // links of the tokens after l: the run's length
+            const unsigned after = l < 31 ? ~(links >> (l + 1)) : ~0u;
+            const int n = __ffs(after);                   // 1 + trailing ones (bit 31 - l on is 0 links)
+            b8_write_run<BF16, NEIGHBOURS, D>(p, part, h, tb - 1 + l, n, s0 / kBlock,
+                                              (int)(s0 % kBlock), lane);
+        }
+    }
+}
+
+// Records of blocks ids[0 .. n) as K and V rows [n][Hkv][16][D] of the row type:
+// one thread per 16-byte code chunk (two 16-byte stores).
+template <bool BF16, int D>
+__global__ void __launch_bounds__(256)
+    dequantize_kernel(const uint8_t *__restrict__ kv, const int32_t *__restrict__ ids, int32_t n,
+                      int32_t num_kv_heads, int32_t num_blocks, uint4 *__restrict__ k_out,
+                      uint4 *__restrict__ v_out, int32_t *__restrict__ status)
+{
+    constexpr int kChunks = D;                            // chunks of one part of a record
+    const int per_block = num_kv_heads * 2 * kChunks;
+    const int64_t total = (int64_t)n * per_block;
+    for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < total;
+         e += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t b = e / per_block;
+        const int within = (int)(e - b * per_block);
+        const int h = within / (2 * kChunks), c = within % (2 * kChunks);
+        const int part = c / kChunks, t = (c % kChunks) / (D / 16), j = c % (D / 16);
+        const int32_t id = __ldg(ids + b);
+        if (id < 0 || id >= num_blocks) {
+            if (within == 0) atomicOr(status, PKV_DEV_BAD_BLOCK);
+            continue;
+        }
+        const uint8_t *rec = kv + ((int64_t)id * num_kv_heads + h) * PKV_B8_RECORD_BYTES(D);
+        const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(rec + 16 * D * part + b8_chunk(t, j, D)));
+        const float scale = __ldg(reinterpret_cast<const float *>(rec + 32 * D) + part);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        float x[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            x[k] = __fmul_rn((float)((int)((u[k >> 2] >> (8 * (k & 3))) & 0xffu) - 128), scale);
+        uint4 *out = (part ? v_out : k_out) + (((b * num_kv_heads + h) * kBlock + t) * D + 16 * j) / 8;
+        out[0] = pack8<BF16>(x);
+        out[1] = pack8<BF16>(x + 8);
+    }
+}
+
+// Spans of 16 tokens per warp once that still gives every resident warp work;
+// below that one warp per token.
+constexpr int64_t kSpanUnits = 8192;
+
+template <bool BF16, bool NEIGHBOURS>
+static int launch_b8(const Params &p0, int D, bool queries, cudaStream_t st)
+{
+    Params p = p0;
+    const int64_t spans = ((int64_t)p.num_tokens + 15) / 16 * 2 * p.num_kv_heads;
+    p.span = spans >= kSpanUnits ? 16 : 1;
+    const int64_t units = p.span == 16 ? spans : (int64_t)p.num_tokens * 2 * p.num_kv_heads;
+    p.write_blocks = (int32_t)std::min<int64_t>((units + 3) / 4, 152 * 64);
+    int64_t grid = p.write_blocks;
+    if (queries) {
+        const int64_t threads = (int64_t)p.num_tokens * p.num_q_heads * (D / 16);
+        grid += std::min<int64_t>((threads + 127) / 128, 152 * 64);
+    }
+    if (D == 128) append_b8_kernel<BF16, NEIGHBOURS, 128><<<(unsigned)grid, 128, 0, st>>>(p);
+    else append_b8_kernel<BF16, NEIGHBOURS, 64><<<(unsigned)grid, 128, 0, st>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+template <bool BF16, bool NEIGHBOURS>
+static int launch_16bit(const Params &p, int D, cudaStream_t st)
+{
+    const int64_t threads = (int64_t)p.num_tokens * (p.num_q_heads + 2 * p.num_kv_heads) * (D / 16);
+    const int64_t grid = std::min<int64_t>((threads + 255) / 256, 152 * 64);
+    append_rope_kernel<BF16, NEIGHBOURS><<<(unsigned)grid, 256, 0, st>>>(p, D);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+static bool rows_ok(const void *p, int64_t stride, int64_t width)
+{
+    return p && aligned16(p) && stride >= width && stride % 8 == 0;
+}
+
+}  // namespace append
+}  // namespace pkv
+
+extern "C" int kv_cache_write_rope(const pkv_pool *pool, void *q_out, int64_t q_out_stride,
+                                   const void *q, int64_t q_stride, int32_t num_q_heads,
+                                   const void *k_new, int64_t k_stride, const void *v_new,
+                                   int64_t v_stride, const int32_t *positions,
+                                   const float *cos_sin, int32_t max_positions, int32_t rotary_dim,
+                                   int32_t interleaved, const int64_t *slot_mapping,
+                                   int32_t num_tokens, void *k_pool, void *v_pool,
+                                   int32_t *d_status, void *stream)
+{
+    using namespace pkv::append;
+    pkv::PoolGeometry g;
+    if (!pkv::pool_geometry(pool, &g) || num_tokens < 0 || num_q_heads < 0)
+        return PKV_ERR_INVALID_ARG;
+    const bool b8 = pkv::is_b8(g);
+    if (!b8 && !pkv::is_16bit(g)) return PKV_ERR_INVALID_ARG;
+    if (rotary_dim < 16 || rotary_dim > g.head_dim || max_positions <= 0)
+        return PKV_ERR_INVALID_ARG;
+    if (rotary_dim % 16 || g.head_dim % 16) return PKV_ERR_UNSUPPORTED;
+    if (b8 && !pkv::b8_supported(g)) return PKV_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PKV_OK;
+    if (!k_pool || (!b8 && !v_pool) || !d_status || !positions || !cos_sin || !slot_mapping)
+        return PKV_ERR_INVALID_ARG;
+    const int64_t kw = (int64_t)g.num_kv_heads * g.head_dim, qw = (int64_t)num_q_heads * g.head_dim;
+    if (!rows_ok(k_new, k_stride, kw) || !rows_ok(v_new, v_stride, kw) ||
+        (num_q_heads > 0 &&
+         (!rows_ok(q, q_stride, qw) || !rows_ok(q_out, q_out_stride, qw))))
+        return PKV_ERR_INVALID_ARG;
+    if (!pkv::aligned16(k_pool) || (!b8 && !pkv::aligned16(v_pool)) || !pkv::aligned16(cos_sin) ||
+        ((uintptr_t)slot_mapping & 7u) || ((uintptr_t)positions & 3u) ||
+        ((uintptr_t)d_status & 3u))
+        return PKV_ERR_INVALID_ARG;
+    Params p = {};
+    p.q = q;
+    p.k = k_new;
+    p.v = v_new;
+    p.q_out = q_out;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_out_stride = q_out_stride;
+    p.positions = positions;
+    p.cos_sin = cos_sin;
+    p.slots = slot_mapping;
+    p.num_tokens = num_tokens;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = g.num_kv_heads;
+    p.max_positions = max_positions;
+    p.rotary_dim = rotary_dim;
+    p.block_size = g.block_size;
+    p.num_slots = (int64_t)g.num_blocks * g.block_size;
+    p.k_pool = static_cast<uint4 *>(k_pool);
+    p.v_pool = static_cast<uint4 *>(v_pool);
+    p.kv = static_cast<uint8_t *>(k_pool);
+    p.status = d_status;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool bf = g.dtype == PKV_BF16 || g.dtype == PKV_B8_BF16, nb = interleaved != 0;
+    if (b8) {
+        const bool q = num_q_heads > 0;
+        return bf ? (nb ? launch_b8<true, true>(p, g.head_dim, q, st)
+                        : launch_b8<true, false>(p, g.head_dim, q, st))
+                  : (nb ? launch_b8<false, true>(p, g.head_dim, q, st)
+                        : launch_b8<false, false>(p, g.head_dim, q, st));
+    }
+    return bf ? (nb ? launch_16bit<true, true>(p, g.head_dim, st)
+                    : launch_16bit<true, false>(p, g.head_dim, st))
+              : (nb ? launch_16bit<false, true>(p, g.head_dim, st)
+                    : launch_16bit<false, false>(p, g.head_dim, st));
+}
+
+extern "C" int kv_cache_write_b8(const pkv_pool *pool, const void *k_new, const void *v_new,
+                                 const int64_t *slot_mapping, int32_t num_tokens, void *kv_b8,
+                                 int32_t *d_status, void *stream)
+{
+    using namespace pkv::append;
+    pkv::PoolGeometry g;
+    if (!pkv::pool_geometry(pool, &g) || num_tokens < 0 || !pkv::is_b8(g)) return PKV_ERR_INVALID_ARG;
+    if (!pkv::b8_supported(g)) return PKV_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PKV_OK;
+    if (!k_new || !v_new || !slot_mapping || !kv_b8 || !d_status) return PKV_ERR_INVALID_ARG;
+    if (!pkv::aligned16(k_new) || !pkv::aligned16(v_new) || !pkv::aligned16(kv_b8) ||
+        ((uintptr_t)slot_mapping & 7u) || ((uintptr_t)d_status & 3u))
+        return PKV_ERR_INVALID_ARG;
+    Params p = {};
+    p.k = k_new;
+    p.v = v_new;
+    p.k_stride = p.v_stride = (int64_t)g.num_kv_heads * g.head_dim;
+    p.slots = slot_mapping;
+    p.num_tokens = num_tokens;
+    p.num_kv_heads = g.num_kv_heads;
+    p.block_size = g.block_size;
+    p.num_slots = (int64_t)g.num_blocks * g.block_size;
+    p.kv = static_cast<uint8_t *>(kv_b8);
+    p.status = d_status;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return g.dtype == PKV_B8_BF16 ? launch_b8<true, false>(p, g.head_dim, false, st)
+                                  : launch_b8<false, false>(p, g.head_dim, false, st);
+}
+
+extern "C" int kv_dequantize_blocks(const pkv_pool *pool, const int32_t *ids, int32_t n,
+                                    const void *kv_b8, void *k_out, void *v_out, int32_t *d_status,
+                                    void *stream)
+{
+    using namespace pkv::append;
+    pkv::PoolGeometry g;
+    if (!pkv::pool_geometry(pool, &g) || n < 0 || !pkv::is_b8(g)) return PKV_ERR_INVALID_ARG;
+    if (!pkv::b8_supported(g)) return PKV_ERR_UNSUPPORTED;
+    if (n == 0) return PKV_OK;
+    if (!ids || !kv_b8 || !k_out || !v_out || !d_status) return PKV_ERR_INVALID_ARG;
+    if (!pkv::aligned16(kv_b8) || !pkv::aligned16(k_out) || !pkv::aligned16(v_out) ||
+        ((uintptr_t)ids & 3u) || ((uintptr_t)d_status & 3u))
+        return PKV_ERR_INVALID_ARG;
+    const int64_t total = (int64_t)n * g.num_kv_heads * 2 * g.head_dim;
+    const unsigned grid = (unsigned)std::min<int64_t>((total + 255) / 256, 152 * 64);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool bf = g.dtype == PKV_B8_BF16;
+    const uint8_t *kv = static_cast<const uint8_t *>(kv_b8);
+    uint4 *ko = static_cast<uint4 *>(k_out), *vo = static_cast<uint4 *>(v_out);
+    if (g.head_dim == 128) {
+        if (bf) dequantize_kernel<true, 128><<<grid, 256, 0, st>>>(kv, ids, n, g.num_kv_heads, g.num_blocks, ko, vo, d_status);
+        else dequantize_kernel<false, 128><<<grid, 256, 0, st>>>(kv, ids, n, g.num_kv_heads, g.num_blocks, ko, vo, d_status);
+    } else {
+        if (bf) dequantize_kernel<true, 64><<<grid, 256, 0, st>>>(kv, ids, n, g.num_kv_heads, g.num_blocks, ko, vo, d_status);
+        else dequantize_kernel<false, 64><<<grid, 256, 0, st>>>(kv, ids, n, g.num_kv_heads, g.num_blocks, ko, vo, d_status);
+    }
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}

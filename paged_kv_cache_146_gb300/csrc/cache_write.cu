@@ -456,22 +456,37 @@ extern "C" int kv_cache_write_q8(const pkv_pool *pool, const void *k_new, const 
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
+// Pools of records (8-bit codes and their scales): K and V share one pool.
+static bool is_records(const pkv::PoolGeometry &g) { return pkv::is_8bit(g) || pkv::is_b8(g); }
+
+static bool record_shape_ok(const pkv::PoolGeometry &g)
+{
+    return pkv::is_b8(g) ? pkv::b8_supported(g) : g.head_dim == 128 && g.block_size == 16;
+}
+
+// Bytes of one block: its records, or its K (or V) rows.
+static int64_t block_bytes_of(const pkv::PoolGeometry &g)
+{
+    if (pkv::is_b8(g)) return (int64_t)g.num_kv_heads * PKV_B8_RECORD_BYTES(g.head_dim);
+    if (pkv::is_8bit(g)) return (int64_t)g.num_kv_heads * PKV_Q8_SLAB_BYTES;
+    return (int64_t)g.num_kv_heads * g.block_size * g.head_dim * 2;
+}
+
 static int launch_swap(const pkv_pool *pool, const int32_t *ids, int32_t n, void *k_pool,
                        void *v_pool, void *staging, bool to_staging, int32_t *d_status,
                        void *stream)
 {
     pkv::PoolGeometry g;
     if (!pkv::pool_geometry(pool, &g) || n < 0) return PKV_ERR_INVALID_ARG;
-    const bool q8 = pkv::is_8bit(g);
+    const bool q8 = is_records(g);
     if (q8) v_pool = nullptr;
     if (n == 0) return PKV_OK;
     if (!ids || !k_pool || (!q8 && !v_pool) || !staging || !d_status) return PKV_ERR_INVALID_ARG;
     if (!pkv::aligned16(k_pool) || (!q8 && !pkv::aligned16(v_pool)) || !pkv::aligned16(staging) ||
         ((uintptr_t)ids & 3u) || ((uintptr_t)d_status & 3u))
         return PKV_ERR_INVALID_ARG;
-    if (q8 && (g.head_dim != 128 || g.block_size != 16)) return PKV_ERR_UNSUPPORTED;
-    const int64_t block_bytes = q8 ? (int64_t)g.num_kv_heads * PKV_Q8_SLAB_BYTES
-                                   : (int64_t)g.num_kv_heads * g.block_size * g.head_dim * 2;
+    if (q8 && !record_shape_ok(g)) return PKV_ERR_UNSUPPORTED;
+    const int64_t block_bytes = block_bytes_of(g);
     if (block_bytes % 16 != 0) return PKV_ERR_UNSUPPORTED;
     const int64_t chunks = block_bytes / 16;
     const int threads = 256;
@@ -505,16 +520,15 @@ extern "C" int kv_block_copy(const pkv_pool *pool, const int32_t *src_ids, const
 {
     pkv::PoolGeometry g;
     if (!pkv::pool_geometry(pool, &g) || n < 0) return PKV_ERR_INVALID_ARG;
-    const bool q8 = pkv::is_8bit(g);
+    const bool q8 = is_records(g);
     if (q8) v_pool = nullptr;
     if (n == 0) return PKV_OK;
     if (!src_ids || !dst_ids || !k_pool || (!q8 && !v_pool) || !d_status) return PKV_ERR_INVALID_ARG;
     if (!pkv::aligned16(k_pool) || (!q8 && !pkv::aligned16(v_pool)) || ((uintptr_t)src_ids & 3u) ||
         ((uintptr_t)dst_ids & 3u) || ((uintptr_t)d_status & 3u))
         return PKV_ERR_INVALID_ARG;
-    if (q8 && (g.head_dim != 128 || g.block_size != 16)) return PKV_ERR_UNSUPPORTED;
-    const int64_t block_bytes = q8 ? (int64_t)g.num_kv_heads * PKV_Q8_SLAB_BYTES
-                                   : (int64_t)g.num_kv_heads * g.block_size * g.head_dim * 2;
+    if (q8 && !record_shape_ok(g)) return PKV_ERR_UNSUPPORTED;
+    const int64_t block_bytes = block_bytes_of(g);
     if (block_bytes % 16 != 0) return PKV_ERR_UNSUPPORTED;
     const int64_t chunks = block_bytes / 16;
     const int threads = 256;

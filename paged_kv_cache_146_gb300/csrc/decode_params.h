@@ -56,6 +56,9 @@ struct Params {
 
 using KernelFn = void (*)(CUtensorMap, CUtensorMap, Params);
 
+// 2-D tensor map of a 16-bit pool: boxes of 64 columns x 16 rows, 128-byte swizzle.
+bool make_pool_map(CUtensorMap *map, const void *pool, const PoolGeometry &g);
+
 }  // namespace decode
 
 namespace prefill {

@@ -100,6 +100,10 @@ size_t kv_pool_bytes(int32_t num_blocks, int32_t block_size, int32_t num_kv_head
         return head_dim % 32 ? 0
                              : (size_t)num_blocks * num_kv_heads * block_size *
                                    (head_dim + head_dim / 32 * 2) * 2;
+    if (dtype == PKV_B8_BF16 || dtype == PKV_B8_F16)   // codes + one scale per block, head and part
+        return block_size == 16 && (head_dim == 64 || head_dim == 128)
+                   ? (size_t)num_blocks * num_kv_heads * PKV_B8_RECORD_BYTES((size_t)head_dim)
+                   : 0;
     if (dtype != PKV_F16 && dtype != PKV_BF16) return 0;
     return (size_t)num_blocks * num_kv_heads * block_size * head_dim * 2;
 }
@@ -110,7 +114,8 @@ int kv_pool_create(int32_t num_blocks, int32_t block_size, int32_t num_kv_heads,
 {
     if (!out || num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0)
         return PKV_ERR_INVALID_ARG;
-    if (dtype != PKV_F16 && dtype != PKV_BF16 && dtype != PKV_Q8_BF16 && dtype != PKV_Q8_F16)
+    if (dtype != PKV_F16 && dtype != PKV_BF16 && dtype != PKV_Q8_BF16 && dtype != PKV_Q8_F16 &&
+        dtype != PKV_B8_BF16 && dtype != PKV_B8_F16)
         return PKV_ERR_INVALID_ARG;
     *out = nullptr;
     pkv_pool *p = new (std::nothrow) pkv_pool;

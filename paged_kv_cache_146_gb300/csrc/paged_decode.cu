@@ -1010,7 +1010,7 @@ static EncodeFn encode_fn()
 
 // 2-D view of a pool: rows = num_blocks * Hkv * 16 of head_dim elements; box of
 // 64 columns x 16 rows with the 128-byte swizzle.
-static bool make_pool_map(CUtensorMap *map, const void *pool, const PoolGeometry &g)
+bool make_pool_map(CUtensorMap *map, const void *pool, const PoolGeometry &g)
 {
     EncodeFn enc = encode_fn();
     if (!enc) return false;

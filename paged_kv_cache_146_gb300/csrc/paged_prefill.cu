@@ -37,6 +37,7 @@ struct Params {
     const int32_t *context_lens;    // [S]
     int32_t num_seqs, num_tokens, num_q_heads, num_kv_heads, group, max_blocks_per_seq;
     int32_t num_blocks, tile_tokens;
+    int32_t window, sinks;          // windowed calls only (tcp kernel, WINDOW)
     float scale_log2;
     int32_t *header;                // [0] = number of (sequence, tile) pairs
     int2 *items;                    // (sequence, tile)
@@ -352,7 +353,25 @@ struct Layout {
 struct Item {
     int s, g, r0, C, L, t0, t1, nkeys, ntiles;
     int kb0, chunk;      // shared-prefix mode: first block of the keys, piece of the chunk
+    // windowed calls: the item's keys are those of blocks 0 .. sink_blocks - 1
+    // and of blocks sink_blocks + gap on, numbered without the gap (nkeys and
+    // the tiles count them so); keys in [hide0, hide1), so numbered, are seen by
+    // no query of the item
+    int sink_blocks, gap, hide0, hide1;
 };
+
+// Keys an item of a windowed call reads: its first query (token t0) reaches
+// back furthest, to position lo; later ones see less of the front.
+__device__ __forceinline__ void item_window(Item &it, int window, int sinks)
+{
+    const int lo = max(0, it.L - it.C + it.t0 - window + 1);
+    const int seen = min(sinks, it.nkeys);                 // sinks up to the last query
+    it.sink_blocks = (seen + kBlock - 1) / kBlock;
+    it.gap = max(0, lo / kBlock - it.sink_blocks);
+    it.nkeys -= it.gap * kBlock;
+    it.hide0 = seen;
+    it.hide1 = lo - it.gap * kBlock;
+}
 
 template <bool PREFIX, int KEYS = kKeys>
 __device__ __forceinline__ Item load_item(const Params &p, int i, int total, int QT)
@@ -394,13 +413,17 @@ __device__ __forceinline__ Item load_item(const Params &p, int i, int total, int
 // one fp16 part of P and the result is scaled by 2^k.
 // PREFIX: shared-prefix mode of a decode call (see Params): items from
 // prefix_items, no causal limit, pieces instead of output rows.
-template <int D, bool BF16, bool VS, bool PREFIX>
+// WINDOW: a query at position p sees keys p - window + 1 .. p and those before
+// `sinks`; the item's tiles hold the blocks that some query of it sees (see
+// item_window), so a tile may join the sinks' last block and the window's first.
+template <int D, bool BF16, bool VS, bool PREFIX, bool WINDOW = false>
 __global__ void __launch_bounds__(kThreads)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ, const Params p)
 {
     static_assert(BF16 || !VS, "fp16 pools take V as it is");
     static_assert(!(VS && PREFIX), "the shared-prefix mode reads V from the pool");
+    static_assert(!(WINDOW && (VS || PREFIX)), "windowed calls read V from the pool");
     constexpr bool kTwoParts = BF16 && !VS;    // P as bf16 high + low parts
     using E = Elem<BF16>;
     using T = typename E::T;
@@ -459,7 +482,11 @@ __global__ void __launch_bounds__(kThreads)
             int last_par[LY::kStages], last_q = -1;          // phases of the last copies issued
             for (int k = 0; k < LY::kStages; ++k) last_par[k] = -1;
             for (int i = blockIdx.x; i < total && !*abort_flag; i += gridDim.x, ++it_cnt) {
-                const Item it = load_item<PREFIX>(p, i, total, QT);
+                Item it = load_item<PREFIX>(p, i, total, QT);
+                if constexpr (WINDOW) {
+                    item_window(it, p.window, p.sinks);
+                    it.ntiles = (it.nkeys + kKeys - 1) / kKeys;
+                }
                 if (it_cnt > 0 &&
                     !mbar_wait(smem_addr(q_empty), (it_cnt - 1) & 1u, abort_flag, p.status))
                     break;
@@ -482,7 +509,9 @@ __global__ void __launch_bounds__(kThreads)
                     int bad = 0;
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
-                        const int id = __ldg(row + min(4 * t + b, nb - 1));
+                        int blk = min(4 * t + b, nb - 1);
+                        if constexpr (WINDOW) blk += blk < it.sink_blocks ? 0 : it.gap;
+                        const int id = __ldg(row + blk);
                         const bool ok = id >= 0 && id < p.num_blocks;
                         bad |= !ok;
                         ids[b] = ok ? id : 0;
@@ -562,7 +591,11 @@ __global__ void __launch_bounds__(kThreads)
                 tc::mma_commit(smem_addr(&kv_empty[t % LY::kStages]));
             };
             for (int i = blockIdx.x; i < total && ok; i += gridDim.x, ++it_cnt) {
-                const Item it = load_item<PREFIX>(p, i, total, QT);
+                Item it = load_item<PREFIX>(p, i, total, QT);
+                if constexpr (WINDOW) {
+                    item_window(it, p.window, p.sinks);
+                    it.ntiles = (it.nkeys + kKeys - 1) / kKeys;
+                }
                 if (!mbar_wait(smem_addr(q_full), it_cnt & 1u, abort_flag, p.status)) break;
                 for (int t = 0; t < it.ntiles && ok; ++t, ++tg) {
                     const uint32_t st = tg % LY::kStages, sb = tg & 1u;
@@ -605,11 +638,24 @@ __global__ void __launch_bounds__(kThreads)
         uint32_t tg = 0, it_cnt = 0;
         bool alive = true;
         for (int i = blockIdx.x; i < total && alive; i += gridDim.x, ++it_cnt) {
-            const Item it = load_item<PREFIX>(p, i, total, QT);
+            Item it = load_item<PREFIX>(p, i, total, QT);
+            if constexpr (WINDOW) {
+                item_window(it, p.window, p.sinks);
+                it.ntiles = (it.nkeys + kKeys - 1) / kKeys;
+            }
             const int jj = r / G, h = r - (r / G) * G;
             const int tg0 = it.t0 + gr * QT;            // this group's first token
             const bool valid = r < QT * G && tg0 + jj < it.t1;
-            const int pos = valid && !PREFIX ? it.L - it.C + tg0 + jj : it.nkeys - 1;
+            int pos = valid && !PREFIX ? it.L - it.C + tg0 + jj : it.nkeys - 1;
+            int first = 0;               // windowed: the row's first key after the sinks
+            if constexpr (WINDOW) {
+                first = valid ? pos - p.window + 1 - it.gap * kBlock : 0;
+                if (valid) pos -= it.gap * kBlock;
+            }
+            // key n of the item hidden from this row
+            auto hidden = [&](int n) {
+                return n > pos || (WINDOW && n < first && n >= p.sinks);
+            };
             float m_ref = -INFINITY, l = 0.f;
             int bad = 0;
             for (int t = 0; t < it.ntiles; ++t, ++tg) {
@@ -636,12 +682,14 @@ __global__ void __launch_bounds__(kThreads)
                 // raw scores; the scale enters inside the exponent (one FFMA each).
                 // Hidden keys are kept out of the maximum here and get weight 0 below.
                 const int k0 = t * kKeys;
-                const bool cross = k0 + kKeys - 1 > pos;   // the tile crosses this row's position
+                bool cross = k0 + kKeys - 1 > pos;         // the tile crosses this row's position
+                if constexpr (WINDOW)                      // or holds keys behind its window
+                    cross |= k0 < first && k0 + kKeys > p.sinks;
                 if (cross) {
                     const float hide = p.scale_log2 < 0.f ? INFINITY : -INFINITY;
 #pragma unroll
                     for (int c = 0; c < kKeys; ++c)
-                        if (k0 + c > pos) x[c] = hide;
+                        if (hidden(k0 + c)) x[c] = hide;
                 }
                 float mx;
                 if (p.scale_log2 >= 0.f) {
@@ -676,8 +724,8 @@ __global__ void __launch_bounds__(kThreads)
                         const float2 e = unpack2f(fma2f(pack2f(x[c], x[c + 1]), sc2, nm2));
                         float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
                         if constexpr (decltype(masked)::value) {
-                            if (k0 + c > pos) p0 = 0.f;
-                            if (k0 + c + 1 > pos) p1 = 0.f;
+                            if (hidden(k0 + c)) p0 = 0.f;
+                            if (hidden(k0 + c + 1)) p1 = 0.f;
                         }
                         const uint64_t pp = pack2f(p0, p1);
                         lsum2 = add2f(lsum2, pp);
@@ -726,6 +774,19 @@ __global__ void __launch_bounds__(kThreads)
                                                    (rem & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                if constexpr (WINDOW) {  // and those of keys that no query of the item sees
+                    const int n0 = max(it.hide0 - k0, 0), n1 = min(it.hide1 - k0, kKeys);
+                    if (n0 < n1) {
+                        uint8_t *vs = stage_s + st * LY::kStageBytes + LY::kKVBytes;
+                        for (int e = r; e < (n1 - n0) * LY::kRegions * 8; e += kRows) {
+                            const int row = n0 + e / (LY::kRegions * 8);
+                            const int rem = e % (LY::kRegions * 8);
+                            *reinterpret_cast<uint4 *>(vs + (rem >> 3) * kKeys * 128 + row * 128 +
+                                                       (rem & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
                 }
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
@@ -1529,9 +1590,19 @@ struct TcPick {
     bool reg_split;     // setmaxnreg kernel: the launch must give tcw::kLaunchRegs
 };
 
-static bool pick_tc(int D, bool bf16, bool staged, TcPick *k)
+static bool pick_tc(int D, bool bf16, bool staged, bool window, TcPick *k)
 {
     if (D != 128 && D != 64) return false;
+    if (window) {
+        k->fn = D == 128 ? (bf16 ? &tcp::prefill_tc_kernel<128, true, false, false, true>
+                                 : &tcp::prefill_tc_kernel<128, false, false, false, true>)
+                         : (bf16 ? &tcp::prefill_tc_kernel<64, true, false, false, true>
+                                 : &tcp::prefill_tc_kernel<64, false, false, false, true>);
+        k->smem = D == 128 ? tcp::Layout<128>::kTotal : tcp::Layout<64>::kTotal;
+        k->threads = tcp::kThreads;
+        k->reg_split = false;
+        return true;
+    }
     if (!bf16 || !staged) {
         k->fn = D == 128 ? (bf16 ? &tcp::prefill_tc_kernel<128, true, false, false>
                                  : &tcp::prefill_tc_kernel<128, false, false, false>)
@@ -1622,13 +1693,13 @@ extern "C" size_t paged_prefill_workspace_bytes_staged(int32_t num_seqs, int32_t
         .total;
 }
 
-extern "C" int paged_prefill_attention(const pkv_pool *pool, void *out, const void *q,
-                                       const void *k_pool, const void *v_pool,
-                                       const int32_t *block_tables, int32_t max_blocks_per_seq,
-                                       const int32_t *query_start, const int32_t *context_lens,
-                                       int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
-                                       float scale, void *workspace, size_t workspace_bytes,
-                                       int32_t *d_status, void *stream)
+// window == 0: plain causal attention; > 0: the windowed call.
+static int prefill_call(const pkv_pool *pool, void *out, const void *q, const void *k_pool,
+                        const void *v_pool, const int32_t *block_tables,
+                        int32_t max_blocks_per_seq, const int32_t *query_start,
+                        const int32_t *context_lens, int32_t num_seqs, int32_t num_tokens,
+                        int32_t num_q_heads, float scale, int32_t window, int32_t sinks,
+                        void *workspace, size_t workspace_bytes, int32_t *d_status, void *stream)
 {
     using namespace pkv::prefill;
     pkv::PoolGeometry g;
@@ -1642,11 +1713,12 @@ extern "C" int paged_prefill_attention(const pkv_pool *pool, void *out, const vo
     // a bf16 pool whose caller gave room for the fp16 copy of V takes it
     const StagedLayout sl = staged_layout(num_seqs, num_tokens, G, g.num_kv_heads, g.head_dim,
                                           max_blocks_per_seq);
-    const bool staged = g.dtype == PKV_BF16 && workspace_bytes >= sl.total &&
+    const bool staged = window == 0 && g.dtype == PKV_BF16 && workspace_bytes >= sl.total &&
                         (int64_t)num_seqs * max_blocks_per_seq * g.num_kv_heads * pkv::kBlock <
                             ((int64_t)1 << 31);
     TcPick kp;
-    if (!pick_tc(g.head_dim, g.dtype == PKV_BF16, staged, &kp)) return PKV_ERR_UNSUPPORTED;
+    if (!pick_tc(g.head_dim, g.dtype == PKV_BF16, staged, window > 0, &kp))
+        return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
     if (!out || !q || !k_pool || !v_pool || !block_tables || !query_start || !context_lens ||
         !workspace || !d_status)
@@ -1685,6 +1757,8 @@ extern "C" int paged_prefill_attention(const pkv_pool *pool, void *out, const vo
     prm.max_blocks_per_seq = max_blocks_per_seq;
     prm.num_blocks = g.num_blocks;
     prm.tile_tokens = tile_tokens(G);
+    prm.window = window;
+    prm.sinks = sinks;
     prm.scale_log2 = scale * 1.4426950408889634f;
     prm.header = static_cast<int32_t *>(workspace);
     prm.items = reinterpret_cast<int2 *>(static_cast<char *>(workspace) + 256);
@@ -1727,6 +1801,36 @@ extern "C" int paged_prefill_attention(const pkv_pool *pool, void *out, const vo
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kp.fn, tk, tv, tq, prm) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+extern "C" int paged_prefill_attention(const pkv_pool *pool, void *out, const void *q,
+                                       const void *k_pool, const void *v_pool,
+                                       const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                       const int32_t *query_start, const int32_t *context_lens,
+                                       int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
+                                       float scale, void *workspace, size_t workspace_bytes,
+                                       int32_t *d_status, void *stream)
+{
+    return prefill_call(pool, out, q, k_pool, v_pool, block_tables, max_blocks_per_seq, query_start,
+                        context_lens, num_seqs, num_tokens, num_q_heads, scale, 0, 0, workspace,
+                        workspace_bytes, d_status, stream);
+}
+
+extern "C" int paged_prefill_attention_window(const pkv_pool *pool, void *out, const void *q,
+                                              const void *k_pool, const void *v_pool,
+                                              const int32_t *block_tables,
+                                              int32_t max_blocks_per_seq,
+                                              const int32_t *query_start,
+                                              const int32_t *context_lens, int32_t num_seqs,
+                                              int32_t num_tokens, int32_t num_q_heads, float scale,
+                                              int32_t window, int32_t sinks, void *workspace,
+                                              size_t workspace_bytes, int32_t *d_status,
+                                              void *stream)
+{
+    if (window < 1 || sinks < 0) return PKV_ERR_INVALID_ARG;
+    return prefill_call(pool, out, q, k_pool, v_pool, block_tables, max_blocks_per_seq, query_start,
+                        context_lens, num_seqs, num_tokens, num_q_heads, scale, window, sinks,
+                        workspace, workspace_bytes, d_status, stream);
 }
 
 // ------------------------------------------------- shared-prefix launcher

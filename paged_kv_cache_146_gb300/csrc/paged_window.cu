@@ -1,0 +1,803 @@
+// Single-token attention over the visible part of each sequence's cache: the
+// last `window` tokens and the first `sinks` tokens, over a 16-bit pool or a
+// block-scaled 8-bit pool (there also over the whole context).
+//
+//   x_j = scale <q, K_j>,  out = sum_j softmax(x)_j V_j   over the visible j:
+//   j < L  and  (j >= L - window  or  j < sinks)
+//
+// One launch, no workspace.  A (sequence, kv head) pair is one cluster of C
+// CTAs of four warps; its visible blocks -- the sinks' blocks, then the
+// window's, numbered without the gap between them -- are dealt to the C * 4
+// warps in turn.  Each warp is its own producer: it keeps a private ring of
+// stages, lane 0 copies block i + kStages (TMA) as soon as block i is consumed,
+// and block ids are fetched 32 at a time, one batch ahead.  The four warps'
+// (o, max, sum) meet in shared memory, the C CTAs' through distributed shared
+// memory, always in the same order, so results do not vary from run to run.
+//
+// Per 16-token block and warp, everything on mma.sync m16n8k16 with the tokens
+// (then the dimensions) as the 16 rows and eight query heads as the columns:
+//   S^T = K Q^T        rows = tokens, columns = heads
+//   P   = 2^(S - m)    fp32, against a lazy reference maximum m
+//   O^T += V^T P^T     rows = dimensions; P^T comes from S^T's accumulator
+//                      layout through one 8x8 transpose (movmatrix) per half
+// so no half of a matrix instruction works on empty rows (G <= 8), and the
+// statistics and the accumulators of a head sit in the same lanes.
+//
+// The bytes of the visible K and V bound it; a block is read once.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "decode_params.h"
+#include "pagedkv.h"
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+namespace window {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxHeads = 16;            // query heads per kv head
+// The reference maximum moves only when a score exceeds it by more than this
+// (log2 units): weights stay within 2^6, far inside fp16's and bf16's range.
+constexpr float kLazy = 6.f;
+
+struct Params {
+    void *out;
+    const void *q;
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    const uint8_t *kv;                   // 8-bit records
+    int32_t num_q_heads, num_kv_heads, group, max_blocks_per_seq, num_blocks;
+    int32_t window, sinks;               // window >= 1 (INT32_MAX: all)
+    int32_t ctas;                        // cluster size C
+    float scale_log2;
+    int32_t *status;
+};
+
+using KernelFn = void (*)(CUtensorMap, CUtensorMap, Params);
+
+// Visible blocks of a sequence of L tokens: logical blocks 0 .. sink_blocks - 1
+// and those from sink_blocks + gap on; n in all.
+struct Visible {
+    int L, lo, sinks, sink_blocks, gap, n;
+    __device__ __forceinline__ int block(int v) const { return v < sink_blocks ? v : v + gap; }
+    // bit t: token t of logical block b is visible
+    __device__ __forceinline__ uint32_t mask(int b) const
+    {
+        auto below = [](int x) { return x <= 0 ? 0u : x >= kBlock ? 0xffffu : (1u << x) - 1u; };
+        const int t0 = b * kBlock;
+        return below(L - t0) & (~below(lo - t0) | below(sinks - t0));
+    }
+};
+
+__device__ __forceinline__ Visible visible(int L, int window, int sinks)
+{
+    Visible v;
+    v.L = L;
+    v.lo = max(0, L - window);
+    v.sinks = min(sinks, L);
+    v.sink_blocks = (v.sinks + kBlock - 1) / kBlock;
+    v.gap = max(0, v.lo / kBlock - v.sink_blocks);
+    v.n = (L + kBlock - 1) / kBlock - v.gap;
+    return v;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Shared-memory address `addr` of this CTA in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float2 cluster_load2(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Shapes of one variant.  B8: block-scaled 8-bit records; else 16-bit pools.
+template <int D, bool B8, int NT>
+struct Shape {
+    static constexpr int kCopyBytes = B8 ? 32 * D + 16 : 64 * D;       // of one block and head
+    static constexpr int kStageBytes = B8 ? (32 * D + 16 + 127) / 128 * 128 : 64 * D;
+    // stages per warp: 16-bit 24 KB in flight, 2 CTAs per SM; 8-bit 16 KB, 3 CTAs per SM
+    static constexpr int kStages = B8 ? (D == 128 ? 4 : 8) : (D == 128 ? 3 : 6);
+    static constexpr int kMinBlocks = B8 ? 3 : 2;
+    static constexpr int kWarpBytes = kStages * kStageBytes;
+    static constexpr int kRow = D + 4;                                  // floats of a merge row
+    static constexpr int kBars = kWarps * kWarpBytes;
+    static constexpr int kMl = kBars + kWarps * 8 * 8;                  // [warps + 1][16] float2
+    static constexpr int kTotal = 1024 + kMl + (kWarps + 1) * kMaxHeads * 8;
+    static_assert(kStages <= 8 && 8 * NT * kRow * 4 <= kWarpBytes, "merge rows fit a warp's ring");
+};
+
+// A warp's running state for NT tiles of eight heads: lane (r, q4) = (lane / 4,
+// lane % 4) holds heads 2 q4 and 2 q4 + 1 of each tile; o[nt][m] = (dimension
+// A, head 0), (A, head 1), (B, head 0), (B, head 1) of 16-dimension tile m.
+template <int D, int NT>
+struct State {
+    float o[NT][D / 16][4];
+    float m[NT][2], l[NT][2];
+};
+
+// Scores (log2 domain) of tokens r and r + 8 -> weights, with the lazy
+// reference maximum; x[nt] = (r, head 0), (r, head 1), (r + 8, head 0), (r + 8, head 1).
+template <int D, int NT>
+__device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&x)[NT][4])
+{
+    bool raise = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) raise |= x[nt][e] > st.m[nt][e & 1] + kLazy;
+    if (__any_sync(kFull, raise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float mx = fmaxf(x[nt][h], x[nt][2 + h]);
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+                const float mn = fmaxf(st.m[nt][h], mx);
+                const float f = mn == -INFINITY ? 1.f : fast_exp2(st.m[nt][h] - mn);
+                st.m[nt][h] = mn;
+                st.l[nt][h] *= f;
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t) {
+                    st.o[nt][t][h] *= f;
+                    st.o[nt][t][2 + h] *= f;
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float m = st.m[nt][e & 1];
+            x[nt][e] = fast_exp2(x[nt][e] - (m == -INFINITY ? 0.f : m));
+            st.l[nt][e & 1] += x[nt][e];
+        }
+}
+
+// Weights x[4] of one head tile as the B operand of the P V product, in type E:
+// (b0, b1) = tokens 2 q4, 2 q4 + 1 and 8 + those, head r.
+template <typename E>
+__device__ __forceinline__ void weights_hi(const float (&x)[4], uint32_t (&b)[2], uint32_t (&raw)[2])
+{
+    raw[0] = E::pack(x[0], x[1]);
+    raw[1] = E::pack(x[2], x[3]);
+    b[0] = transpose8x8(raw[0]);
+    b[1] = transpose8x8(raw[1]);
+}
+
+// The weights' remainders after weights_hi, rounded to the same type.
+template <typename E>
+__device__ __forceinline__ void weights_lo(const float (&x)[4], const uint32_t (&raw)[2],
+                                           uint32_t (&b)[2])
+{
+    const float2 h0 = E::unpack(raw[0]), h1 = E::unpack(raw[1]);
+    b[0] = transpose8x8(E::pack(x[0] - h0.x, x[1] - h0.y));
+    b[1] = transpose8x8(E::pack(x[2] - h1.x, x[3] - h1.y));
+}
+
+// ------------------------------------------------------------------ 16-bit block
+// K and V slabs as TMA leaves them: boxes of 64 columns x 16 rows, 16-byte chunk
+// c of row t at position c ^ (t % 8).  qb = the query rows as B operands.
+// P goes in as a high and a low part of the pool's type, which carries the
+// weights to ~2^-17 (a bf16 weight alone would be off by 2^-9).
+template <int D, bool BF16, int NT>
+__device__ __forceinline__ void consume_16bit(uint32_t kb, const uint32_t (&qb)[NT][D / 16][2],
+                                              State<D, NT> &st, uint32_t mask, float scale_log2,
+                                              int lane)
+{
+    using E = Elem<BF16>;
+    const int r = lane >> 2, q4 = lane & 3, mi = lane >> 3, r8 = lane & 7;
+    const uint32_t vb = kb + 32 * D;
+    float c0[NT][4], c1[NT][4];          // two chains of products
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c0[nt][e] = c1[nt][e] = 0.f;
+    const int k_tok = ((mi & 1) << 3) + r8;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const int chunk = 2 * kk + (mi >> 1);
+        uint32_t a[4];
+        ldsm_x4(a, kb + (chunk >> 3) * kBoxBytes + k_tok * 128 + (((chunk & 7) ^ r8) << 4));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            E::mma(kk & 1 ? c1[nt] : c0[nt], a, qb[nt][kk][0], qb[nt][kk][1]);
+    }
+    const bool v0 = (mask >> r) & 1u, v1 = (mask >> (r + 8)) & 1u;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            c0[nt][e] = (e < 2 ? v0 : v1) ? (c0[nt][e] + c1[nt][e]) * scale_log2 : -INFINITY;
+    softmax_step<D, NT>(st, c0);
+    uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        uint32_t raw[2];
+        weights_hi<E>(c0[nt], hi[nt], raw);
+        weights_lo<E>(c0[nt], raw, lo[nt]);
+    }
+    // hidden tokens: their V rows may hold anything, and 0 * NaN is NaN
+    const uint32_t two_lo = mask >> (2 * q4), two_hi = mask >> (2 * q4 + 8);
+    const uint32_t keep_lo = (two_lo & 1u ? 0xffffu : 0u) | (two_lo & 2u ? 0xffff0000u : 0u);
+    const uint32_t keep_hi = (two_hi & 1u ? 0xffffu : 0u) | (two_hi & 2u ? 0xffff0000u : 0u);
+    const int v_tok = ((mi >> 1) << 3) + r8;
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) {
+        const int chunk = 2 * t + (mi & 1);
+        uint32_t a[4];
+        ldsm_x4_trans(a, vb + (chunk >> 3) * kBoxBytes + v_tok * 128 + (((chunk & 7) ^ r8) << 4));
+        a[0] &= keep_lo;
+        a[1] &= keep_lo;
+        a[2] &= keep_hi;
+        a[3] &= keep_hi;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            E::mma(st.o[nt][t], a, hi[nt][0], hi[nt][1]);
+            E::mma(st.o[nt][t], a, lo[nt][0], lo[nt][1]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------- 8-bit block
+// Byte u = code + 128 is the low mantissa of fp16 1024 + u (bits 0x6400 | u);
+// minus 1152 that is the code, exactly.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w)     // bytes 0 and 1
+{
+    uint32_t x = __byte_perm(w, 0x64646464u, 0x4140);
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0x64806480u));
+    return x;
+}
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w)     // bytes 2 and 3
+{
+    uint32_t x = __byte_perm(w, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0x64806480u));
+    return x;
+}
+
+// Offset of 16-byte chunk j of token t in the K or V codes (pagedkv.h).
+template <int D>
+__device__ __forceinline__ int chunk_at(int t, int j)
+{
+    return ((t * D) >> 7) * 128 + ((j ^ ((t & 1) << 2) ^ (((t >> 1) & 3) << 1)) << 4);
+}
+
+// Codes are exact in fp16, so both products run on fp16 operands; the block's
+// two scales stay out of them: K's multiplies the scores, V's the block's
+// product as it is added to the accumulator (weights of at most 2^6 then keep
+// fp16's full precision whatever the scale).  The reduction over dimensions
+// may take them in any order, so lane (r, q4) takes whole 16-byte chunks q4
+// (and q4 + 4) of tokens r and r + 8 as its A words, four dimensions to a step,
+// and the queries were laid out alike; of V it takes dimensions D/8 r ..
+// D/8 (r + 1) of its four tokens and pairs their bytes.
+// P: one fp16 part for bf16 rows (2^-12, below the output's 2^-9), two for fp16.
+template <int D, bool BF16, int NT>
+__device__ __forceinline__ void consume_b8(const uint8_t *rec, const uint32_t (&qb)[NT][D / 16][2],
+                                           const float (&scale_row)[NT][2], State<D, NT> &st,
+                                           uint32_t mask, int lane)
+{
+    using H = Elem<false>;
+    const int r = lane >> 2, q4 = lane & 3;
+    const float2 scales = *reinterpret_cast<const float2 *>(rec + 32 * D);
+    float x[NT][4];
+    {
+        float c0[NT][4], c1[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c0[nt][e] = c1[nt][e] = 0.f;
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half) {
+            const uint4 wa = *reinterpret_cast<const uint4 *>(rec + chunk_at<D>(r, q4 + 4 * half));
+            const uint4 wb = *reinterpret_cast<const uint4 *>(rec + chunk_at<D>(r + 8, q4 + 4 * half));
+            const uint32_t ua[4] = {wa.x, wa.y, wa.z, wa.w}, ub[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t a[4] = {codes_lo(ua[i]), codes_lo(ub[i]), codes_hi(ua[i]),
+                                       codes_hi(ub[i])};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    H::mma(i & 1 ? c1[nt] : c0[nt], a, qb[nt][4 * half + i][0],
+                           qb[nt][4 * half + i][1]);
+            }
+        }
+        const bool v0 = (mask >> r) & 1u, v1 = (mask >> (r + 8)) & 1u;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float f[2] = {scales.x * scale_row[nt][0], scales.x * scale_row[nt][1]};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[nt][e] = (e < 2 ? v0 : v1) ? (c0[nt][e] + c1[nt][e]) * f[e & 1] : -INFINITY;
+        }
+    }
+    softmax_step<D, NT>(st, x);
+    uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        uint32_t raw[2];
+        weights_hi<H>(x[nt], hi[nt], raw);
+        if constexpr (!BF16) weights_lo<H>(x[nt], raw, lo[nt]);
+    }
+    // words of tokens 2q4, 2q4 + 1, 2q4 + 8, 2q4 + 9: four dimensions each
+    constexpr int kWords = D / 32;
+    uint32_t w[4][kWords];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int t = 2 * q4 + (k & 1) + 8 * (k >> 1);
+        const uint8_t *at = rec + 16 * D;
+        if constexpr (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(at + chunk_at<D>(t, r));
+            w[k][0] = v.x; w[k][1] = v.y; w[k][2] = v.z; w[k][3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2 *>(at + chunk_at<D>(t, r >> 1) + 8 * (r & 1));
+            w[k][0] = v.x; w[k][1] = v.y;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+#pragma unroll
+        for (int pr = 0; pr < 2; ++pr) {          // dimensions 4i + 2 pr, 4i + 2 pr + 1
+            const uint32_t sel = pr ? 0x7362 : 0x5140;
+            const uint32_t p01 = __byte_perm(w[0][i], w[1][i], sel);
+            const uint32_t p89 = __byte_perm(w[2][i], w[3][i], sel);
+            const uint32_t a[4] = {codes_lo(p01), codes_hi(p01), codes_lo(p89), codes_hi(p89)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float c[4];
+                H::mma0(c, a, hi[nt][0], hi[nt][1]);
+                if constexpr (!BF16) H::mma(c, a, lo[nt][0], lo[nt][1]);
+                float *o = st.o[nt][2 * i + pr];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = fmaf(scales.y, c[e], o[e]);
+            }
+        }
+    }
+}
+
+// --------------------------------------------------------------------- the kernel
+template <int D, bool BF16, bool B8, int NT>
+__global__ void __launch_bounds__(kThreads, Shape<D, B8, NT>::kMinBlocks)
+    window_decode_kernel(const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const Params p)
+{
+    using SH = Shape<D, B8, NT>;
+    using E = Elem<BF16>;
+    using T = typename E::T;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = lane >> 2, q4 = lane & 3;
+    uint8_t *ring = base + warp * SH::kWarpBytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(base + SH::kBars) + warp * 8;
+    float2 *ml = reinterpret_cast<float2 *>(base + SH::kMl);             // [warps + 1][16]
+    __shared__ int abort_flags[kWarps];
+    volatile int *abort_flag = &abort_flags[warp];
+    if (lane == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < SH::kStages; ++i) mbar_init(smem_addr(&full[i]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+
+    const int C = p.ctas;
+    const int64_t pair = blockIdx.x / C;
+    const int rank = (int)(blockIdx.x - pair * C);
+    const int s = (int)(pair / p.num_kv_heads), g = (int)(pair - (int64_t)s * p.num_kv_heads);
+    const int G = p.group;
+    int L = __ldg(p.context_lens + s);
+    if (L < 0 || (int64_t)L > (int64_t)p.max_blocks_per_seq * kBlock) {
+        if (threadIdx.x == 0) atomicOr(p.status, PKV_DEV_BAD_LEN);
+        L = 0;
+    }
+    const Visible vis = visible(L, p.window, p.sinks);
+    const int gw = rank * kWarps + warp, stride = C * kWarps;
+    const int count = gw < vis.n ? (vis.n - 1 - gw) / stride + 1 : 0;   // this warp's blocks
+    const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
+    auto load_ids = [&](int i0) {
+        const int i = i0 + lane;
+        return i < count ? __ldg(row + vis.block(gw + i * stride)) : 0;
+    };
+    int ids = load_ids(0), ids_next = load_ids(32);
+    uint32_t bad = 0;
+    auto issue = [&](int i) {            // the warp's i-th block into stage i % kStages
+        if (i >= count) return;
+        if ((i & 31) == 0 && i > 0) {
+            ids = ids_next;
+            ids_next = load_ids(i + 32);
+        }
+        const int id = __shfl_sync(kFull, ids, i & 31);
+        const int slot = i % SH::kStages;
+        const bool ok = id >= 0 && id < p.num_blocks;
+        bad |= ok ? 0u : 1u;
+        if (lane == 0) {
+            const uint32_t fb = smem_addr(&full[slot]);
+            const uint32_t dst = smem_addr(ring + slot * SH::kStageBytes);
+            if (!ok) {
+                atomicOr(p.status, PKV_DEV_BAD_BLOCK);
+                mbar_arrive(fb);
+            } else if constexpr (B8) {
+                mbar_arrive_expect_tx(fb, SH::kCopyBytes);
+                bulk_load(dst, p.kv + ((int64_t)id * p.num_kv_heads + g) * PKV_B8_RECORD_BYTES(D),
+                          SH::kCopyBytes, fb);
+            } else {
+                mbar_arrive_expect_tx(fb, SH::kCopyBytes);
+                const int y = (id * p.num_kv_heads + g) * kBlock;
+#pragma unroll
+                for (int bx = 0; bx < D / kBoxCols; ++bx) {
+                    tma_load_2d(dst + bx * kBoxBytes, &tmK, bx * kBoxCols, y, fb);
+                    tma_load_2d(dst + 32 * D + bx * kBoxBytes, &tmV, bx * kBoxCols, y, fb);
+                }
+            }
+        }
+    };
+    for (int i = 0; i < SH::kStages; ++i) issue(i);
+
+    // query rows as B operands: head r of tile nt
+    uint32_t qb[NT][D / 16][2];
+    float scale_row[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int h = 8 * nt + r;
+        const T *qr = static_cast<const T *>(p.q) + ((int64_t)s * p.num_q_heads + (int64_t)g * G + h) * D;
+        scale_row[nt][0] = scale_row[nt][1] = p.scale_log2;
+        if constexpr (!B8) {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(qr);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                qb[nt][kk][0] = h < G ? __ldg(w + 8 * kk + q4) : 0u;
+                qb[nt][kk][1] = h < G ? __ldg(w + 8 * kk + 4 + q4) : 0u;
+            }
+        } else {
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {
+                const uint4 *w = reinterpret_cast<const uint4 *>(qr + 16 * (q4 + 4 * half));
+                const uint4 a = h < G ? __ldg(w) : make_uint4(0u, 0u, 0u, 0u);
+                const uint4 b = h < G ? __ldg(w + 1) : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) qb[nt][4 * half + (i >> 1)][i & 1] = u[i];
+            }
+            if constexpr (BF16) {
+                // bf16 row -> fp16: times the power of two that puts its largest
+                // magnitude into [2^14, 2^15); every value within 2^28 of it
+                // converts exactly.  The inverse goes into the row's scale.
+                float amax = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 f = E::unpack(qb[nt][kk][e]);
+                        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+                const int ex = max(-112, ((__float_as_int(amax) >> 23) & 0xff) - 127 - 14);
+                const float down = __int_as_float((127 - ex) << 23);
+                const float up = __int_as_float((127 + ex) << 23);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 f = E::unpack(qb[nt][kk][e]);
+                        qb[nt][kk][e] = Elem<false>::pack(f.x * down, f.y * down);
+                    }
+                scale_row[nt][0] *= __shfl_sync(kFull, up, 8 * q4);
+                scale_row[nt][1] *= __shfl_sync(kFull, up, 8 * q4 + 4);
+            }
+        }
+    }
+
+    State<D, NT> st;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        st.m[nt][0] = st.m[nt][1] = -INFINITY;
+        st.l[nt][0] = st.l[nt][1] = 0.f;
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st.o[nt][t][e] = 0.f;
+    }
+    for (int i = 0; i < count; ++i) {
+        const int slot = i % SH::kStages;
+        const bool landed = mbar_wait(smem_addr(&full[slot]), (uint32_t)(i / SH::kStages) & 1u,
+                                      abort_flag, p.status);
+        if (!__all_sync(kFull, landed)) {
+            // let the copies still in flight land, then give up
+            if (lane == 0) {
+                for (int k = i; k < min(i + SH::kStages, count); ++k) {
+                    const unsigned long long t0 = globaltimer();
+                    while (!mbar_try_wait(smem_addr(&full[k % SH::kStages]),
+                                          (uint32_t)(k / SH::kStages) & 1u))
+                        if (globaltimer() - t0 > kTimeoutNs) break;
+                }
+            }
+            __syncwarp();
+            bad = 1u;
+            break;
+        }
+        if (!bad) {
+            const uint32_t mask = vis.mask(vis.block(gw + i * stride));
+            uint8_t *stage = ring + slot * SH::kStageBytes;
+            if constexpr (B8) consume_b8<D, BF16, NT>(stage, qb, scale_row, st, mask, lane);
+            else consume_16bit<D, BF16, NT>(smem_addr(stage), qb, st, mask, p.scale_log2, lane);
+        }
+        // the stage's next contents come through the async proxy: order this
+        // warp's reads of it first
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        issue(i + SH::kStages);
+    }
+
+    // ---- the warp's piece, in its own ring: every copy into it has landed
+    float *piece = reinterpret_cast<float *>(ring);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float l = st.l[nt][h];
+            l += __shfl_xor_sync(kFull, l, 4);
+            l += __shfl_xor_sync(kFull, l, 8);
+            l += __shfl_xor_sync(kFull, l, 16);
+            const int head = 8 * nt + 2 * q4 + h;
+            if (r == 0) ml[warp * kMaxHeads + head] = make_float2(st.m[nt][h], bad ? -1.f : l);
+            float *dst = piece + head * SH::kRow;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+                if constexpr (B8) {
+                    *reinterpret_cast<float2 *>(dst + D / 8 * r + 2 * t) =
+                        make_float2(st.o[nt][t][h], st.o[nt][t][2 + h]);
+                } else {
+                    dst[16 * t + r] = st.o[nt][t][h];
+                    dst[16 * t + r + 8] = st.o[nt][t][2 + h];
+                }
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- the four warps: factors 2^(m_w - M), sums; a bad piece has sum -1
+    T *out = static_cast<T *>(p.out) + ((int64_t)s * p.num_q_heads + (int64_t)g * G) * D;
+    auto factor = [](float m, float M) { return m == -INFINITY ? 0.f : fast_exp2(m - M); };
+    auto store = [&](int u, float4 a, float l, bool poisoned) {
+        const float inv = 1.f / l;
+        uint2 w = make_uint2(0u, 0u);     // no visible token, or a bad block: zeros
+        if (vis.n > 0 && !poisoned) {
+            w.x = E::pack(a.x * inv, a.y * inv);
+            w.y = E::pack(a.z * inv, a.w * inv);
+        }
+        *reinterpret_cast<uint2 *>(out + 4 * u) = w;
+    };
+    const int units = G * (D / 4);        // four dimensions of a head each
+    for (int u = threadIdx.x; u < units; u += kThreads) {
+        const int h = u / (D / 4), d = 4 * (u - h * (D / 4));
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * kMaxHeads + h].x);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+        bool poisoned = false;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float2 v = ml[w * kMaxHeads + h];
+            const float f = factor(v.x, M);
+            const float4 x = *reinterpret_cast<const float4 *>(
+                base + w * SH::kWarpBytes + (h * SH::kRow + d) * 4);
+            a.x += x.x * f; a.y += x.y * f; a.z += x.z * f; a.w += x.w * f;
+            l += v.y * f;
+            poisoned |= v.y < 0.f;
+        }
+        if (C == 1) {
+            store(u, a, l, poisoned);
+        } else {                          // over warp 0's piece, which this thread alone reads here
+            *reinterpret_cast<float4 *>(base + (h * SH::kRow + d) * 4) = a;
+            if (d == 0) ml[kWarps * kMaxHeads + h] = make_float2(M, poisoned ? -1.f : l);
+        }
+    }
+    if (C == 1) return;
+
+    // ---- the cluster's CTAs: unit u goes to CTA u % C
+    cluster_sync();
+    for (int u = threadIdx.x * C + rank; u < units; u += kThreads * C) {
+        const int h = u / (D / 4), d = 4 * (u - h * (D / 4));
+        const uint32_t ml_at = smem_addr(ml + kWarps * kMaxHeads + h);
+        const uint32_t o_at = smem_addr(base + (h * SH::kRow + d) * 4);
+        float M = -INFINITY;
+        for (int c = 0; c < C; ++c) M = fmaxf(M, cluster_load2(cluster_addr(ml_at, c)).x);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+        bool poisoned = false;
+        for (int c = 0; c < C; ++c) {
+            const float2 v = cluster_load2(cluster_addr(ml_at, c));
+            const float4 x = cluster_load4(cluster_addr(o_at, c));
+            const float f = factor(v.x, M);
+            a.x += x.x * f; a.y += x.y * f; a.z += x.z * f; a.w += x.w * f;
+            l += v.y * f;
+            poisoned |= v.y < 0.f;
+        }
+        store(u, a, l, poisoned);
+    }
+    cluster_sync();                       // nobody leaves while its memory is read
+}
+
+// --------------------------------------------------------------------- host side
+struct Variant {
+    KernelFn fn;
+    int smem;
+};
+
+template <int D, bool B8>
+static Variant variant(bool bf16, bool wide)
+{
+    if (wide)
+        return bf16 ? Variant{&window_decode_kernel<D, true, B8, 2>, Shape<D, B8, 2>::kTotal}
+                    : Variant{&window_decode_kernel<D, false, B8, 2>, Shape<D, B8, 2>::kTotal};
+    return bf16 ? Variant{&window_decode_kernel<D, true, B8, 1>, Shape<D, B8, 1>::kTotal}
+                : Variant{&window_decode_kernel<D, false, B8, 1>, Shape<D, B8, 1>::kTotal};
+}
+
+// CTAs of a variant that fit on the current device at once, cached per device.
+static int resident_ctas(int which, const Variant &v)
+{
+    constexpr int kMaxDev = 64, kVariants = 16;
+    static std::mutex mu;
+    static int cache[kMaxDev][kVariants];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return -1;
+    std::lock_guard<std::mutex> lock(mu);
+    int &n = cache[dev][which];
+    if (n == 0) {
+        int sms = 0, per_sm = 0;
+        const void *fn = reinterpret_cast<const void *>(v.fn);
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) !=
+                cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, v.smem) !=
+                cudaSuccess ||
+            per_sm < 1)
+            return -1;
+        n = sms * per_sm;
+    }
+    return n;
+}
+
+static int launch(const pkv_pool *pool, bool want_b8, void *out, const void *q, const void *k_pool,
+                  const void *v_pool, const int32_t *block_tables, int32_t maxb,
+                  const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads, float scale,
+                  int32_t window, int32_t sinks, int32_t *d_status, void *stream)
+{
+    PoolGeometry g;
+    if (!pool_geometry(pool, &g)) return PKV_ERR_INVALID_ARG;
+    if (want_b8 ? !is_b8(g) : !is_16bit(g)) return PKV_ERR_INVALID_ARG;
+    if (num_seqs < 0 || num_q_heads <= 0 || maxb <= 0 || window < 1 || sinks < 0)
+        return PKV_ERR_INVALID_ARG;
+    if (num_q_heads % g.num_kv_heads) return PKV_ERR_INVALID_ARG;
+    if (!(scale == scale) || scale == INFINITY || scale == -INFINITY) return PKV_ERR_INVALID_ARG;
+    const int G = num_q_heads / g.num_kv_heads;
+    if (g.block_size != kBlock || G > kMaxHeads || (g.head_dim != 64 && g.head_dim != 128))
+        return PKV_ERR_UNSUPPORTED;
+    if ((int64_t)maxb * kBlock > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    if (!want_b8 && (int64_t)g.num_blocks * g.num_kv_heads * g.block_size > (int64_t)1 << 31)
+        return PKV_ERR_UNSUPPORTED;   // TMA row coordinate is a signed 32-bit value
+    if (num_seqs == 0) return PKV_OK;
+    if (!out || !q || !k_pool || (!want_b8 && !v_pool) || !block_tables || !context_lens || !d_status)
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || (!want_b8 && !aligned16(v_pool)) ||
+        ((uintptr_t)block_tables & 3u) || ((uintptr_t)context_lens & 3u) || ((uintptr_t)d_status & 3u))
+        return PKV_ERR_INVALID_ARG;
+    const bool bf = g.dtype == PKV_BF16 || g.dtype == PKV_B8_BF16, wide = G > 8;
+    const Variant v = g.head_dim == 128
+                          ? (want_b8 ? variant<128, true>(bf, wide) : variant<128, false>(bf, wide))
+                          : (want_b8 ? variant<64, true>(bf, wide) : variant<64, false>(bf, wide));
+    const int resident = resident_ctas((g.head_dim == 128) | want_b8 << 1 | bf << 2 | wide << 3, v);
+    if (resident < 1) return PKV_ERR_CUDA;
+
+    CUtensorMap tk = {}, tv = {};
+    if (!want_b8 && (!decode::make_pool_map(&tk, k_pool, g) || !decode::make_pool_map(&tv, v_pool, g)))
+        return PKV_ERR_CUDA;
+    Params p;
+    p.out = out;
+    p.q = q;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.kv = static_cast<const uint8_t *>(k_pool);
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = g.num_kv_heads;
+    p.group = G;
+    p.max_blocks_per_seq = maxb;
+    p.num_blocks = g.num_blocks;
+    p.window = window;
+    p.sinks = sinks;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.status = d_status;
+
+    // Cluster size: the most blocks a sequence can show is known here (its
+    // length is not).  Split a pair while the grid leaves SMs idle, and while a
+    // CTA would walk a long run of blocks by itself (the last pairs of a ragged
+    // batch then finish together); always leave each warp two blocks.
+    const int64_t pairs = (int64_t)num_seqs * g.num_kv_heads;
+    const int64_t most = std::min<int64_t>(
+        maxb, ((int64_t)window + 2 * kBlock - 2) / kBlock + ((int64_t)sinks + kBlock - 1) / kBlock);
+    int C = 1;
+    while (C < 8 && most > 2 * kWarps * C && (pairs * C < resident || most > 256 * C)) C *= 2;
+    p.ctas = C;
+    if (pairs * C > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(pairs * C));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)v.smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, v.fn, tk, tv, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace window
+}  // namespace pkv
+
+extern "C" int paged_decode_attention_window(const pkv_pool *pool, void *out, const void *q,
+                                             const void *k_pool, const void *v_pool,
+                                             const int32_t *block_tables,
+                                             int32_t max_blocks_per_seq,
+                                             const int32_t *context_lens, int32_t num_seqs,
+                                             int32_t num_q_heads, float scale, int32_t window,
+                                             int32_t sinks, int32_t *d_status, void *stream)
+{
+    return pkv::window::launch(pool, false, out, q, k_pool, v_pool, block_tables,
+                               max_blocks_per_seq, context_lens, num_seqs, num_q_heads, scale,
+                               window, sinks, d_status, stream);
+}
+
+extern "C" int paged_decode_attention_b8(const pkv_pool *pool, void *out, const void *q,
+                                         const void *kv_b8, const int32_t *block_tables,
+                                         int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                         int32_t num_seqs, int32_t num_q_heads, float scale,
+                                         int32_t window, int32_t sinks, int32_t *d_status,
+                                         void *stream)
+{
+    if (window < 0) return PKV_ERR_INVALID_ARG;
+    return pkv::window::launch(pool, true, out, q, kv_b8, nullptr, block_tables,
+                               max_blocks_per_seq, context_lens, num_seqs, num_q_heads, scale,
+                               window == 0 ? INT32_MAX : window, sinks, d_status, stream);
+}

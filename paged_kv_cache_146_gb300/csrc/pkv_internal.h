@@ -28,4 +28,13 @@ inline bool is_16bit(const PoolGeometry &g) { return g.dtype == PKV_F16 || g.dty
 // Pool holds 8-bit codes with fp16 scales.
 inline bool is_8bit(const PoolGeometry &g) { return g.dtype == PKV_Q8_BF16 || g.dtype == PKV_Q8_F16; }
 
+// Pool holds 8-bit codes with one fp32 scale per block, kv head and K or V.
+inline bool is_b8(const PoolGeometry &g) { return g.dtype == PKV_B8_BF16 || g.dtype == PKV_B8_F16; }
+
+// Shapes the block-scaled kernels take.
+inline bool b8_supported(const PoolGeometry &g)
+{
+    return (g.head_dim == 64 || g.head_dim == 128) && g.block_size == 16;
+}
+
 }  // namespace pkv

@@ -1,0 +1,295 @@
+"""Attention over a sliding window with sinks, decode and chunks of a prompt,
+against 64 bits; and the calls in the order a server makes them."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from paged_kv_cache_146_gb300 import (DEV_BAD_BLOCK, DEV_BAD_LEN, KVPool, cache_write_rope,  # noqa: E402
+                                      dequantize_blocks, paged_decode_attention_b8,
+                                      paged_decode_attention_window, paged_prefill_attention,
+                                      paged_prefill_attention_window, prefill_workspace_bytes,
+                                      rope_table, status_check)
+from serving_reference import (F16_HALF_STEP, Records, assert_within, attention, random_case,  # noqa: E402
+                               rotate, scale_of, visible)
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+# relative error of a weight on its way into P V: decode takes it in two parts of
+# the pool's type; prefill in two bf16 parts, the first truncated, or one fp16 part
+DECODE_WEIGHT = {"bf16": 2.0 ** -16, "f16": 2.0 ** -22}
+PREFILL_WEIGHT = {"bf16": 2.0 ** -15, "f16": F16_HALF_STEP}
+
+
+def new_status():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def build(lens, first_query, hkv, dim, dtype, window, sinks, seed, maxb=None, nan_hidden=True):
+    """Pools whose hidden tokens hold NaN and whose unseen blocks were given back."""
+    gen = torch.Generator().manual_seed(seed)
+    maxb = maxb or max(-(-n // 16) for n in lens) + 1
+    tables, nb = random_case(gen, lens, hkv, maxb)
+    k, v = (torch.randn((nb, hkv, 16, dim), generator=gen).to(DT[dtype]) for _ in range(2))
+    if nan_hidden:
+        keep = torch.zeros((nb, 16), dtype=torch.bool)
+        for s, n in enumerate(lens):
+            for q0 in range(first_query[s], n):
+                j = torch.tensor(visible(n, q0, window, sinks))
+                keep[tables[s].long()[j // 16], j % 16] = True
+        for p in (k, v):
+            p.permute(0, 2, 1, 3)[~keep] = float("nan")
+        for s, n in enumerate(lens):
+            for b in range(maxb):
+                if tables[s, b] >= 0 and not keep[tables[s, b]].any():
+                    tables[s, b] = -1
+    pool = KVPool(nb, hkv, dim, dtype, device="cuda")
+    pool.k_pool.copy_(k)
+    pool.v_pool.copy_(v)
+    return pool, k, v, tables, gen
+
+
+def expect(q, k, v, tables, lens, first_query, rows, window, sinks, dtype, weight, got):
+    """Every listed (row, sequence, position) of `got` against 64 bits."""
+    hq, hkv, dim = q.shape[1], k.shape[1], q.shape[2]
+    for row, s, pos in rows:
+        j = torch.tensor(visible(lens[s], pos, window, sinks))
+        blk, off = tables[s].long()[j // 16], j % 16
+        for h in range(hq):
+            kk, vv = (p[blk, h // (hq // hkv), off].double() for p in (k, v))
+            want, bound = attention(q[row, h].double(), kk, vv, scale_of(dim), DT[dtype], weight)
+            assert_within(got[row, h], want, bound, f"row {row} sequence {s} position {pos} head {h}")
+
+
+def run_decode(lens, hq, hkv, dim, dtype, window, sinks, seed, maxb=None):
+    first = [max(0, n - 1) for n in lens]
+    pool, k, v, tables, gen = build(lens, first, hkv, dim, dtype, window, sinks, seed, maxb)
+    q = torch.randn((len(lens), hq, dim), generator=gen).to(DT[dtype])
+    status = new_status()
+    out = paged_decode_attention_window(pool, q.cuda(), tables.cuda(),
+                                        torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                        scale_of(dim), window, sinks, status)
+    assert status_check(status) == (0, 0)
+    for s, n in enumerate(lens):
+        if n == 0:
+            assert not bool(out[s].any())
+    rows = [(s, s, n - 1) for s, n in enumerate(lens) if n]
+    expect(q, k, v, tables, lens, first, rows, window, sinks, dtype, DECODE_WEIGHT[dtype], out)
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (8, 2), (16, 1), (12, 1), (10, 2), (9, 1)])
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("f16", 128), ("bf16", 64), ("f16", 64)])
+def test_decode_head_layouts(dtype, dim, hq, hkv):
+    run_decode([1, 0, 16, 17, 130, 777], hq, hkv, dim, dtype, 100, 4, hq + dim)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 0), (16, 4), (17, 16), (33, 17), (64, 0),
+                                          (100, 200), (5000, 4), (2 ** 31 - 1, 2 ** 31 - 1)])
+@pytest.mark.parametrize("dtype,dim,hq,hkv", [("bf16", 128, 8, 2), ("f16", 64, 12, 1)])
+def test_decode_windows(dtype, dim, hq, hkv, window, sinks):
+    run_decode([1, 0, 15, 16, 33, 100, 600, 1111], hq, hkv, dim, dtype, window, sinks, sinks % 97)
+
+
+def test_decode_split_over_a_cluster():
+    """Long windows with few heads: several CTAs per (sequence, kv head)."""
+    run_decode([5003, 2, 400], 8, 1, 128, "bf16", 4000, 4, 31)
+    run_decode([5003], 2, 2, 64, "f16", 2 ** 31 - 1, 0, 32, maxb=900)
+
+
+def test_decode_bad_lengths_and_blocks():
+    pool, k, v, tables, gen = build([40] * 5, [0] * 5, 2, 128, "bf16", 99, 0, 33, maxb=4)
+    lens = [40, -1, 1000, 40, 40]
+    tables[3, 1] = pool.num_blocks
+    q = torch.randn((5, 8, 128), generator=gen).to(torch.bfloat16).cuda()
+    status = new_status()
+    dl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out = paged_decode_attention_window(pool, q, tables.cuda(), dl, 0.1, 99, 0, status)
+    assert status_check(status)[1] == DEV_BAD_LEN | DEV_BAD_BLOCK
+    assert not bool(out[1:4].any()) and bool(out[0].any()) and bool(out[4].any())
+    dl.fill_(40)
+    out = paged_decode_attention_window(pool, q, tables.cuda(), dl, 0.1, 8, 0, status)
+    assert status_check(status) == (0, 0) and bool(out[3].any())
+
+
+def test_decode_infinite_scores():
+    """A key of -inf products weighs nothing; the rest of the row is unharmed."""
+    pool, k, v, tables, gen = build([20], [19], 1, 64, "f16", 99, 0, 34, maxb=2)
+    q = torch.ones((1, 2, 64), dtype=torch.float16)
+    k[tables[0, 0], 0, 0] = float("-inf")
+    pool.k_pool.copy_(k)
+    status = new_status()
+    out = paged_decode_attention_window(pool, q.cuda(), tables.cuda(),
+                                        torch.tensor([20], dtype=torch.int32, device="cuda"), 0.125, 99, 0, status)
+    assert status_check(status) == (0, 0)
+    j = torch.arange(1, 20)
+    blk = tables[0].long()[j // 16]
+    for h in range(2):
+        want, bound = attention(q[0, h].double(), k[blk, 0, j % 16].double(), v[blk, 0, j % 16].double(),
+                                0.125, torch.float16, 2.0 ** -22)
+        assert_within(out[0, h], want, bound)
+
+
+def test_decode_repeated_captured_and_concurrent():
+    lens = [500, 33, 2000, 7]
+    pool, k, v, tables, gen = build(lens, [n - 1 for n in lens], 2, 128, "bf16", 600, 4, 35)
+    q = torch.randn((4, 8, 128), generator=gen).to(torch.bfloat16).cuda()
+    status = new_status()
+    args = (pool, q, tables.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), 0.1, 600, 4, status)
+    first = paged_decode_attention_window(*args)
+    graph, held = torch.cuda.CUDAGraph(), torch.zeros_like(q)
+    with torch.cuda.graph(graph):
+        paged_decode_attention_window(*args, out=held)
+    outs = [torch.empty_like(q) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, o in zip(streams, outs):
+            paged_decode_attention_window(*args, out=o, stream=s)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert status_check(status) == (0, 0)
+    for o in (*outs, held):
+        assert torch.equal(first, o)
+
+
+# ------------------------------------------------------------------------- prefill
+def run_prefill(lens, chunks, hq, hkv, dim, dtype, window, sinks, seed, sample=None):
+    first = [n - c for n, c in zip(lens, chunks)]
+    pool, k, v, tables, gen = build(lens, first, hkv, dim, dtype, window, sinks, seed)
+    T = sum(chunks)
+    q = torch.randn((T, hq, dim), generator=gen).to(DT[dtype])
+    start = torch.tensor([0] + list(np.cumsum(chunks)), dtype=torch.int32)
+    ws = torch.empty(prefill_workspace_bytes(len(lens), T, hq, hkv), dtype=torch.uint8, device="cuda")
+    status = new_status()
+    out = paged_prefill_attention_window(pool, q.cuda(), tables.cuda(), start.cuda(),
+                                         torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                         scale_of(dim), window, sinks, ws, status)
+    assert status_check(status) == (0, 0)
+    rows = [(int(start[s]) + i, s, first[s] + i) for s, c in enumerate(chunks) for i in range(c)]
+    if sample:
+        step = max(1, len(rows) // sample)
+        rows = rows[::step] + rows[-1:]
+    expect(q, k, v, tables, lens, first, rows, window, sinks, dtype, PREFILL_WEIGHT[dtype], out)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (16, 4), (63, 0), (64, 64), (65, 17), (257, 5),
+                                          (130, 100), (5000, 0)])
+@pytest.mark.parametrize("dtype,dim,hq,hkv", [("bf16", 128, 8, 2), ("f16", 64, 4, 4)])
+def test_prefill_windows(dtype, dim, hq, hkv, window, sinks):
+    run_prefill([700, 40, 1, 333], [90, 40, 1, 0], hq, hkv, dim, dtype, window, sinks, window, sample=50)
+
+
+@pytest.mark.parametrize("hq,hkv", [(16, 1), (12, 1), (10, 2), (3, 3)])
+@pytest.mark.parametrize("dtype,dim", [("bf16", 64), ("f16", 128)])
+def test_prefill_head_layouts(dtype, dim, hq, hkv):
+    run_prefill([500, 77], [60, 77], hq, hkv, dim, dtype, 100, 4, hq, sample=24)
+
+
+def test_prefill_long_chunk():
+    """Many tiles per item, whole tiles hidden from the item's later rows."""
+    run_prefill([4100], [600], 2, 2, 128, "bf16", 70, 4, 41, sample=40)
+    run_prefill([3000, 2500], [1500, 900], 8, 2, 128, "bf16", 1024, 4, 42, sample=24)
+
+
+def test_prefill_wide_window_is_the_causal_call():
+    lens, chunks = [300, 64], [100, 64]
+    pool, k, v, tables, gen = build(lens, [200, 0], 2, 128, "bf16", 10 ** 6, 0, 43)
+    q = torch.randn((164, 8, 128), generator=gen).to(torch.bfloat16).cuda()
+    start = torch.tensor([0, 100, 164], dtype=torch.int32, device="cuda")
+    dl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = torch.empty(prefill_workspace_bytes(2, 164, 8, 2), dtype=torch.uint8, device="cuda")
+    status = new_status()
+    a = paged_prefill_attention(pool, q, tables.cuda(), start, dl, 0.1, ws, status)
+    b = paged_prefill_attention_window(pool, q, tables.cuda(), start, dl, 0.1, 10 ** 6, 7, ws, status)
+    assert status_check(status) == (0, 0)
+    assert torch.equal(a, b)
+
+
+def test_prefill_bad_sequences():
+    pool, k, v, tables, gen = build([40, 40, 40], [0, 0, 0], 2, 64, "f16", 99, 0, 44)
+    q = torch.randn((30, 4, 64), generator=gen).to(torch.float16).cuda()
+    start = torch.tensor([0, 10, 20, 30], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([40, 5, 40], dtype=torch.int32, device="cuda")       # 5 < its chunk
+    tables[2, 2] = -1
+    ws = torch.empty(prefill_workspace_bytes(3, 30, 4, 2), dtype=torch.uint8, device="cuda")
+    status = new_status()
+    out = paged_prefill_attention_window(pool, q, tables.cuda(), start, lens, 0.1, 12, 0, ws, status)
+    assert status_check(status)[1] == DEV_BAD_LEN | DEV_BAD_BLOCK
+    assert bool(out[:10].any()) and not bool(out[10:].any())
+
+
+# ----------------------------------------------------------- as a server calls them
+@pytest.mark.parametrize("kind", ["bf16", "f16", "b8_bf16", "b8_f16"])
+def test_append_then_attend(kind):
+    """Prompts through the rotated append, the chunk's attention, then decode steps
+    (append, attend), every output against 64 bits computed from the unrotated rows."""
+    eight, dtype = kind.startswith("b8"), kind[-4:].lstrip("_")
+    dt, hq, hkv, dim, rot, window, sinks = DT[dtype], 8, 2, 64, 32, 40, 3
+    gen = torch.Generator().manual_seed(51)
+    prompts, steps = [70, 5, 33], 4
+    S, maxb, nb = 3, 8, 24
+    pool = KVPool(nb, hkv, dim, kind, free_order=torch.randperm(nb, generator=gen).numpy(), device="cuda")
+    if eight:
+        pool.kv.fill_(0xFF)
+    else:
+        pool.k_pool.fill_(float("nan"))
+        pool.v_pool.fill_(float("nan"))
+    tables, lens = np.full((S, maxb), -1, np.int32), np.zeros(S, np.int32)
+    table = rope_table(128, rot)
+    status = new_status()
+    past = [[torch.zeros((0, hkv, dim), dtype=torch.float64)] * 2 for _ in range(S)]
+    for step in range(1 + steps):
+        new = np.array(prompts if step == 0 else [1] * S, np.int32)
+        slots = pool.append_slots(lens, new, tables)
+        pos = np.concatenate([np.arange(a, a + n) for a, n in zip(lens, new)]).astype(np.int32)
+        lens += new
+        T = int(new.sum())
+        qkv = torch.randn((T, (hq + 2 * hkv) * dim), generator=gen).to(dt)
+        q, k, v = (p.view(T, -1, dim) for p in qkv.split([hq * dim, hkv * dim, hkv * dim], 1))
+        gq, gk, gv = (p.view(T, -1, dim) for p in qkv.cuda().split([hq * dim, hkv * dim, hkv * dim], 1))
+        q_rot = cache_write_rope(pool, gk, gv, torch.from_numpy(pos).cuda(), table.cuda(),
+                                 torch.from_numpy(slots).cuda(), status, q=gq)
+        dtab = torch.from_numpy(tables).cuda()
+        dl = torch.from_numpy(lens).cuda()
+        start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        if step == 0:
+            ws = torch.empty(prefill_workspace_bytes(S, T, hq, hkv), dtype=torch.uint8, device="cuda")
+            if eight:              # the 8-bit blocks as a 16-bit pool of the same numbering
+                view = KVPool(nb, hkv, dim, dtype, device="cuda")
+                dequantize_blocks(pool, torch.arange(nb, dtype=torch.int32, device="cuda"), view.k_pool,
+                                  view.v_pool, status)
+            out = paged_prefill_attention_window(view if eight else pool, q_rot, dtab,
+                                                 torch.from_numpy(start).cuda(), dl, scale_of(dim), window,
+                                                 sinks, ws, status)
+        elif eight:
+            out = paged_decode_attention_b8(pool, q_rot, dtab, dl, scale_of(dim), status, window=window,
+                                            sinks=sinks)
+        else:
+            out = paged_decode_attention_window(pool, q_rot, dtab, dl, scale_of(dim), window, sinks, status)
+        assert status_check(status) == (0, 0)
+        kd, _ = rotate(k.double(), table, torch.from_numpy(pos).long(), False)
+        qd, _ = rotate(q.double(), table, torch.from_numpy(pos).long(), False)
+        for s in range(S):
+            a, b = int(start[s]), int(start[s + 1])
+            past[s] = [torch.cat([past[s][0], kd[a:b]]), torch.cat([past[s][1], v[a:b].double()])]
+            for row in range(a, b, 7):
+                p = int(pos[row])
+                j = torch.tensor(visible(p + 1, p, window, sinks))
+                for h in range(hq):
+                    kk, vv = (x[j, h // (hq // hkv)] for x in past[s])
+                    want, bound = attention(qd[row, h], kk, vv, scale_of(dim), dt, F16_HALF_STEP)
+                    # what the cache rounds: a relative 2^-8 / 2^-11 of K and q, or half a step
+                    # of an 8-bit block (and one more for each time its scale grew, at most
+                    # the steps taken), at most 5 half steps of the largest value / 127
+                    half = {torch.bfloat16: 2.0 ** -8, torch.float16: F16_HALF_STEP}[dt]
+                    ek = kk.abs().max().item() / 127 * 2.5 if eight else 0.0
+                    ev = vv.abs().max().item() / 127 * 2.5 if eight else 0.0
+                    if eight:      # a block may also hold larger values that the window hides
+                        ek, ev = (x.abs().max().item() / 127 * 2.5 for x in past[s])
+                    dx = scale_of(dim) * (2 * half * (kk.abs() @ qd[row, h].abs()).max().item()
+                                          + ek * qd[row, h].abs().sum().item() * (1 + half))
+                    w = torch.softmax((kk @ qd[row, h]) * scale_of(dim), 0)
+                    bound = bound + 2 * np.expm1(2 * dx) / 2 * (w @ vv.abs()) + ev * np.exp(2 * dx) + half * (w @ vv.abs()) * (2 if eight else 0)
+                    assert_within(out[row, h], want, bound, f"step {step} row {row} head {h}")
