@@ -687,76 +687,69 @@ def paged_decode_attention_q8(pool: KVPool, q, block_tables, context_lens, scale
 
 # --------------------------------------- rotated append, 8-bit blocks, windows
 # The calls below are also made for a few rows at a time, where the host side is
-# most of their time: their checks read each attribute once.
-def _on_device(device, stream):
-    """(context, raw stream) of a launch: ``stream`` or the current stream of the
-    tensors' device, which is made current for the call if it is not."""
+# most of their time: each tensor is checked by one expression over its fields
+# (the message is worked out only when it fails), addresses go to the library as
+# plain integers, and torch is looked up once.
+_torch = None
+
+
+def _load_torch():
+    global _torch
     import torch
-    if device.type != "cuda":
-        raise ValueError(f"the call's tensors must be CUDA tensors, got {device}")
-    here = torch.cuda.current_device()
-    index = here if device.index is None else device.index
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        raw = stream if isinstance(stream, int) else stream.cuda_stream
-    return (None if here == index else torch.cuda.device(index)), raw
+    _torch = torch
+    return torch
 
 
-def _launch(name: str, device, stream, *args) -> None:
-    """Call the library's ``name`` with ``args`` and the stream as last argument."""
-    guard, raw = _on_device(device, stream)
-    fn = getattr(lib(), name)
-    if guard is None:
-        rc = fn(*args, raw)
-    else:
-        with guard:
-            rc = fn(*args, raw)
-    if rc:
-        check(rc, name)
-
-
-def _want(name: str, t, shape: tuple, dtype, device, contiguous: bool = True) -> int:
-    """Check a tensor of the call; its address."""
+def _refuse(name: str, t, shape: tuple, dtype, index: int, contiguous: bool):
+    """Raise for a tensor that failed its check."""
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}, got "
                         f"{str(t.dtype).replace('torch.', '')}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's rows are on {device}")
-    if contiguous and not t.is_contiguous():
+    if t.get_device() != index:
+        where = "the CPU" if index < 0 else f"cuda:{index}"
+        raise ValueError(f"{name} is on {t.device}, the call's rows are on {where}")
+    if contiguous:
         raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} was refused")
+
+
+def _want(name: str, t, shape: tuple, dtype, index: int) -> int:
+    """Check a contiguous tensor of the call; its address."""
+    if (t.shape != shape or t.dtype is not dtype or t.get_device() != index
+            or not t.is_contiguous()):
+        _refuse(name, t, shape, dtype, index, True)
     return t.data_ptr()
 
 
-def _want_rows(name: str, t, shape: tuple, dtype, device):
+def _want_rows(name: str, t, shape: tuple, dtype, index: int):
     """Check rows [T][H][D] whose tokens may lie apart (slices of a fused
     projection); their address and token stride in elements."""
-    ptr = _want(name, t, shape, dtype, device, False)
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        _refuse(name, t, shape, dtype, index, False)
     T, H, D = shape
     s, sh, sd = t.stride()
     if T > 0 and H > 0 and (sd != 1 or (sh != D and H > 1)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     if T <= 1:
-        return ptr, H * D
-    if s < H * D or s % 8:
+        s = H * D
+    elif s < H * D or s % 8:
         raise ValueError(f"{name}: the token stride must be a multiple of 8 and at least "
                          f"{H * D}, got {s}")
-    return ptr, s
+    return t.data_ptr(), s
 
 
-def _want_status(status, device) -> int:
-    if status.dtype != _torch_int32() or status.numel() < 1:
+def _want_status(status, index: int) -> int:
+    if status.dtype is not _torch.int32 or status.numel() < 1:
         raise TypeError("status must be an int32 tensor of at least one element")
-    if status.device != device:
-        raise ValueError(f"status is on {status.device}, the call's rows are on {device}")
+    if status.get_device() != index:
+        raise ValueError(f"status is on {status.device}, the call's rows are not")
     return status.data_ptr()
 
 
-def _want_pools(pool: KVPool, device, k_pool=None, v_pool=None, kv=None):
+def _want_pools(pool: KVPool, index: int, k_pool=None, v_pool=None, kv=None):
     """Addresses of the call's device pools: (K, V), or (records, 0)."""
-    import torch
     if pool.record_bytes:
         if not pool.is_b8:
             raise ValueError("the call takes 16-bit and block-scaled 8-bit pools")
@@ -764,14 +757,40 @@ def _want_pools(pool: KVPool, device, k_pool=None, v_pool=None, kv=None):
         if kv is None:
             raise ValueError("the pool has no device memory")
         return _want("kv", kv, (pool.num_blocks, pool.num_kv_heads, pool.record_bytes),
-                     torch.uint8, device), 0
+                     _torch.uint8, index), 0
     k_pool = pool.k_pool if k_pool is None else k_pool
     v_pool = pool.v_pool if v_pool is None else v_pool
     if k_pool is None or v_pool is None:
         raise ValueError("the pool has no device memory")
     shape = (pool.num_blocks, pool.num_kv_heads, pool.block_size, pool.head_dim)
-    dt = _torch_dtype(pool.dtype_code)
-    return _want("k_pool", k_pool, shape, dt, device), _want("v_pool", v_pool, shape, dt, device)
+    dt = _row_dtype(pool)
+    return _want("k_pool", k_pool, shape, dt, index), _want("v_pool", v_pool, shape, dt, index)
+
+
+def _row_dtype(pool: KVPool):
+    torch = _torch or _load_torch()
+    return _torch_dtype(pool.dtype_code) if pool.is_q8 else (
+        torch.bfloat16 if pool.dtype_code in (PKV_BF16, PKV_B8_BF16) else torch.float16)
+
+
+def _launch(name: str, index: int, stream, *args) -> None:
+    """Call the library's ``name`` with ``args`` and, last, ``stream`` or the current
+    stream of device ``index``, which is made current for the call if it is not."""
+    if index < 0:
+        raise ValueError("the call's tensors must be CUDA tensors, got cpu")
+    torch = _torch
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    fn = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, stream)
+    if rc:
+        check(rc, name)
 
 
 def rope_table(max_positions: int, rotary_dim: int, base: float = 10000.0, device=None):
@@ -800,35 +819,34 @@ def cache_write_rope(pool: KVPool, k_new, v_new, positions, cos_sin, slot_mappin
     (default: a new tensor; ``q`` itself: in place), which is returned.  Rows of
     skipped tokens in ``q_out`` are left as they were.  ``interleaved``: pairs of
     neighbouring dimensions instead of the halves' (i, i + rotary_dim / 2)."""
-    import torch
-    device = k_new.device
-    dt, D, Hkv = _torch_dtype(pool.dtype_code), pool.head_dim, pool.num_kv_heads
+    torch = _torch or _load_torch()
+    dev, dt, D, Hkv = k_new.get_device(), _row_dtype(pool), pool.head_dim, pool.num_kv_heads
     T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
-    slots = _want("slot_mapping", slot_mapping, (T,), torch.int64, device)
-    k, ks = _want_rows("k_new", k_new, (T, Hkv, D), dt, device)
-    v, vs = _want_rows("v_new", v_new, (T, Hkv, D), dt, device)
-    pos = _want("positions", positions, (T,), torch.int32, device)
+    slots = _want("slot_mapping", slot_mapping, (T,), torch.int64, dev)
+    k, ks = _want_rows("k_new", k_new, (T, Hkv, D), dt, dev)
+    v, vs = _want_rows("v_new", v_new, (T, Hkv, D), dt, dev)
+    pos = _want("positions", positions, (T,), torch.int32, dev)
     if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [max_positions][rotary_dim]")
     rows, rot = cos_sin.shape
-    table = _want("cos_sin", cos_sin, (rows, rot), torch.float32, device)
+    table = _want("cos_sin", cos_sin, (rows, rot), torch.float32, dev)
     qp = qs = qo = qos = hq = 0
     if q is not None:
         if q.dim() != 3:
             raise ValueError(f"q must be [{T}][h][{D}], got {list(q.shape)}")
         hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((T, hq, D), dtype=dt, device=device)
-        qp, qs = _want_rows("q", q, (T, hq, D), dt, device)
-        qo, qos = _want_rows("q_out", q_out, (T, hq, D), dt, device)
+            q_out = torch.empty((T, hq, D), dtype=dt, device=q.device)
+        qp, qs = _want_rows("q", q, (T, hq, D), dt, dev)
+        qo, qos = _want_rows("q_out", q_out, (T, hq, D), dt, dev)
         if qp == qo and qs != qos:
             raise ValueError("q_out over q needs the same token stride")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    kp, vp = _want_pools(pool, device, k_pool, v_pool, kv)
-    _launch("kv_cache_write_rope", device, stream, pool.handle, qo, qos, qp, qs, hq, k, ks, v, vs,
+    kp, vp = _want_pools(pool, dev, k_pool, v_pool, kv)
+    _launch("kv_cache_write_rope", dev, stream, pool.handle, qo, qos, qp, qs, hq, k, ks, v, vs,
             pos, table, rows, rot, 1 if interleaved else 0, slots, T, kp, vp,
-            _want_status(status, device))
+            _want_status(status, dev))
     return q_out
 
 
@@ -838,63 +856,63 @@ def cache_write_b8(pool: KVPool, k_new, v_new, slot_mapping, status, kv=None, st
     largest value written to it since its first token, and the codes before the new
     tokens are rounded to it when it grows.  The tokens of one block are neighbours
     in ``slot_mapping``, slots rising by one (as the ledger hands them out)."""
-    import torch
-    device = k_new.device
+    torch = _torch or _load_torch()
+    dev = k_new.get_device()
     if not pool.is_b8:
         raise ValueError("cache_write_b8 takes a block-scaled 8-bit pool")
-    dt, shape = _torch_dtype(pool.dtype_code), (pool.num_kv_heads, pool.head_dim)
+    dt, shape = _row_dtype(pool), (pool.num_kv_heads, pool.head_dim)
     T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
-    slots = _want("slot_mapping", slot_mapping, (T,), torch.int64, device)
-    k = _want("k_new", k_new, (T, *shape), dt, device)
-    v = _want("v_new", v_new, (T, *shape), dt, device)
-    rec, _ = _want_pools(pool, device, kv=kv)
-    _launch("kv_cache_write_b8", device, stream, pool.handle, k, v, slots, T, rec,
-            _want_status(status, device))
+    slots = _want("slot_mapping", slot_mapping, (T,), torch.int64, dev)
+    k = _want("k_new", k_new, (T, *shape), dt, dev)
+    v = _want("v_new", v_new, (T, *shape), dt, dev)
+    rec, _ = _want_pools(pool, dev, kv=kv)
+    _launch("kv_cache_write_b8", dev, stream, pool.handle, k, v, slots, T, rec,
+            _want_status(status, dev))
 
 
 def dequantize_blocks(pool: KVPool, ids, k_out, v_out, status, kv=None, stream=None):
     """Blocks ``ids`` (int32 device [n]) of a block-scaled 8-bit pool as 16-bit rows:
     ``k_out``/``v_out`` [n][Hkv][16][D] in the pool's row type (the layout of a 16-bit
     pool of n blocks).  Returns (k_out, v_out)."""
-    import torch
-    device = ids.device
+    torch = _torch or _load_torch()
+    dev = ids.get_device()
     if not pool.is_b8:
         raise ValueError("dequantize_blocks takes a block-scaled 8-bit pool")
     n = ids.shape[0] if ids.dim() == 1 else -1
-    i = _want("ids", ids, (n,), torch.int32, device)
-    dt, shape = _torch_dtype(pool.dtype_code), (n, pool.num_kv_heads, 16, pool.head_dim)
-    k = _want("k_out", k_out, shape, dt, device)
-    v = _want("v_out", v_out, shape, dt, device)
-    rec, _ = _want_pools(pool, device, kv=kv)
-    _launch("kv_dequantize_blocks", device, stream, pool.handle, i, n, rec, k, v,
-            _want_status(status, device))
+    i = _want("ids", ids, (n,), torch.int32, dev)
+    dt, shape = _row_dtype(pool), (n, pool.num_kv_heads, 16, pool.head_dim)
+    k = _want("k_out", k_out, shape, dt, dev)
+    v = _want("v_out", v_out, shape, dt, dev)
+    rec, _ = _want_pools(pool, dev, kv=kv)
+    _launch("kv_dequantize_blocks", dev, stream, pool.handle, i, n, rec, k, v,
+            _want_status(status, dev))
     return k_out, v_out
 
 
 def _decode_call(name: str, pool: KVPool, q, out, block_tables, context_lens, scale, window, sinks,
                  status, k_pool, v_pool, kv, stream):
-    """Checks and launch of the workspace-free decode calls."""
-    import torch
-    device, dt, D = q.device, _torch_dtype(pool.dtype_code), pool.head_dim
+    """Checks and launch of the windowed decode calls."""
+    torch = _torch or _load_torch()
+    dev, dt, D = q.get_device(), _row_dtype(pool), pool.head_dim
     if q.dim() != 3 or q.shape[2] != D:
         raise ValueError(f"q must be [n][h][{D}], got {list(q.shape)}")
     S, hq, _ = shape = tuple(q.shape)
     if hq % pool.num_kv_heads:
         raise ValueError(f"q has {hq} heads, not a multiple of the pool's "
                          f"{pool.num_kv_heads} kv heads")
-    qp = _want("q", q, shape, dt, device)
+    qp = _want("q", q, shape, dt, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=device)
-    op = _want("out", out, shape, dt, device)
+        out = torch.empty(shape, dtype=dt, device=q.device)
+    op = _want("out", out, shape, dt, dev)
     if block_tables.dim() != 2:
         raise ValueError("block_tables must have 2 dimensions")
     maxb = block_tables.shape[1]
-    tp = _want("block_tables", block_tables, (S, maxb), torch.int32, device)
-    lp = _want("context_lens", context_lens, (S,), torch.int32, device)
-    kp, vp = _want_pools(pool, device, k_pool, v_pool, kv)
+    tp = _want("block_tables", block_tables, (S, maxb), torch.int32, dev)
+    lp = _want("context_lens", context_lens, (S,), torch.int32, dev)
+    kp, vp = _want_pools(pool, dev, k_pool, v_pool, kv)
     pools = (kp,) if pool.is_b8 else (kp, vp)
-    _launch(name, device, stream, pool.handle, op, qp, *pools, tp, maxb, lp, S, hq, scale,
-            window, sinks, _want_status(status, device))
+    _launch(name, dev, stream, pool.handle, op, qp, *pools, tp, maxb, lp, S, hq, scale,
+            window, sinks, _want_status(status, dev))
     return out
 
 
@@ -944,32 +962,32 @@ def paged_prefill_attention_window(pool: KVPool, q, block_tables, query_start, c
     """``paged_prefill_attention`` where a query at position p attends to tokens p -
     window + 1 .. p and to the first ``sinks`` tokens (16-bit pools).  Workspace of
     ``prefill_workspace_bytes(S, T, Hq, Hkv)`` bytes."""
-    import torch
+    torch = _torch or _load_torch()
     if pool.record_bytes:
         raise ValueError("paged_prefill_attention_window takes a 16-bit pool")
     window, sinks = _window(window, sinks)
-    device, dt, D = q.device, _torch_dtype(pool.dtype_code), pool.head_dim
+    dev, dt, D = q.get_device(), _row_dtype(pool), pool.head_dim
     if q.dim() != 3 or q.shape[2] != D:
         raise ValueError(f"q must be [n][h][{D}], got {list(q.shape)}")
     T, hq, _ = shape = tuple(q.shape)
     if hq % pool.num_kv_heads:
         raise ValueError(f"q has {hq} heads, not a multiple of the pool's "
                          f"{pool.num_kv_heads} kv heads")
-    qp = _want("q", q, shape, dt, device)
+    qp = _want("q", q, shape, dt, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=device)
-    op = _want("out", out, shape, dt, device)
+        out = torch.empty(shape, dtype=dt, device=q.device)
+    op = _want("out", out, shape, dt, dev)
     if block_tables.dim() != 2:
         raise ValueError("block_tables must have 2 dimensions")
     S, maxb = block_tables.shape
-    tp = _want("block_tables", block_tables, (S, maxb), torch.int32, device)
-    lp = _want("context_lens", context_lens, (S,), torch.int32, device)
-    sp = _want("query_start", query_start, (S + 1,), torch.int32, device)
+    tp = _want("block_tables", block_tables, (S, maxb), torch.int32, dev)
+    lp = _want("context_lens", context_lens, (S,), torch.int32, dev)
+    sp = _want("query_start", query_start, (S + 1,), torch.int32, dev)
     nbytes = workspace.numel()
-    wp = _want("workspace", workspace, (nbytes,), torch.uint8, device)
-    kp, vp = _want_pools(pool, device, k_pool, v_pool)
-    _launch("paged_prefill_attention_window", device, stream, pool.handle, op, qp, kp, vp, tp, maxb,
-            sp, lp, S, T, hq, scale, window, sinks, wp, nbytes, _want_status(status, device))
+    wp = _want("workspace", workspace, (nbytes,), torch.uint8, dev)
+    kp, vp = _want_pools(pool, dev, k_pool, v_pool)
+    _launch("paged_prefill_attention_window", dev, stream, pool.handle, op, qp, kp, vp, tp, maxb,
+            sp, lp, S, T, hq, scale, window, sinks, wp, nbytes, _want_status(status, dev))
     return out
 
 

@@ -106,72 +106,99 @@ __device__ __forceinline__ void rotate16(float (&x)[16], int i, int half, const 
     }
 }
 
+// One thread's unit of append_rows: two chunks of one head's row.
+struct RowUnit {
+    const uint16_t *row;
+    int64_t t, slot;
+    int head, i, pos;
+    uint4 w0, w1;
+};
+
 // 16-bit pools (and, with heads_kv = 0, the queries of an 8-bit append): one
-// thread per (token, head, chunk pair), heads in the order q, k, v.  A thread
-// reads what it writes and nothing else, so q_out may be q itself.
+// thread per (token, head, chunk pair), heads in the order q, k, v; two units a
+// thread in flight.  A thread reads what it writes and nothing else of q, so
+// q_out may be q itself.
 template <bool BF16, bool NEIGHBOURS>
-__device__ __forceinline__ void append_rows(const Params &p, int D, int heads_kv, int64_t cta,
-                                            int64_t ctas)
+__device__ __forceinline__ void append_rows(const Params &p, int D, int heads_kv, int cta, int ctas)
 {
     const int lanes = D >> 4;                             // chunk pairs of a row
-    const int heads = p.num_q_heads + 2 * heads_kv;
-    const int per_token = heads * lanes;
-    const int64_t total = (int64_t)p.num_tokens * per_token;
-    const int half = p.rotary_dim >> 1;
-    for (int64_t base = cta * blockDim.x; base < total; base += ctas * blockDim.x) {
-        const int64_t t0 = base / per_token;
-        const int within0 = (int)(base - t0 * per_token) + threadIdx.x;
-        const int dt = within0 / per_token;
-        const int64_t t = t0 + dt;
-        if (t >= p.num_tokens) continue;
-        const int within = within0 - dt * per_token;
-        const int head = within / lanes, i = within - head * lanes;
-        const int64_t slot = __ldg(p.slots + t);
-        const int pos = __ldg(p.positions + t);
-        const bool is_q = head < p.num_q_heads;
-        const int kvh = is_q ? 0 : (head - p.num_q_heads) % max(heads_kv, 1);
-        const bool is_k = !is_q && head < p.num_q_heads + heads_kv;
-        const ChunkPair cp = chunk_pair<NEIGHBOURS>(i, p.rotary_dim);
-        const uint16_t *row =
-            is_q ? static_cast<const uint16_t *>(p.q) + t * p.q_stride + (int64_t)head * D
-                 : (is_k ? static_cast<const uint16_t *>(p.k) + t * p.k_stride
-                         : static_cast<const uint16_t *>(p.v) + t * p.v_stride) +
-                       (int64_t)kvh * D;
-        uint4 w0 = reinterpret_cast<const uint4 *>(row)[cp.c0];
-        uint4 w1 = reinterpret_cast<const uint4 *>(row)[cp.c1];
-        if (slot < 0) continue;                           // no token here
-        if (slot >= p.num_slots || pos < 0 || pos >= p.max_positions) {
-            if (within == 0)
-                atomicOr(p.status, slot >= p.num_slots ? PKV_DEV_BAD_SLOT : PKV_DEV_BAD_POS);
-            continue;
+    const int per_token = (p.num_q_heads + 2 * heads_kv) * lanes;
+    // units first, first + step, ...: the token and the rest advance by fixed amounts
+    const uint32_t first = (uint32_t)cta * blockDim.x + threadIdx.x;
+    const uint32_t step = (uint32_t)ctas * blockDim.x;
+    const int step_t = (int)(step / (uint32_t)per_token);
+    const int step_w = (int)(step - (uint32_t)step_t * per_token);
+    int64_t t = first / (uint32_t)per_token;
+    int within = (int)(first - (uint32_t)t * per_token);
+
+    auto load = [&](RowUnit &u) {                         // and advance
+        u.t = t;
+        if (t < p.num_tokens) {
+            u.head = within / lanes;
+            u.i = within - u.head * lanes;
+            const ChunkPair cp = chunk_pair<NEIGHBOURS>(u.i, p.rotary_dim);
+            const int h = u.head - p.num_q_heads;
+            u.row = h < 0 ? static_cast<const uint16_t *>(p.q) + t * p.q_stride + (int64_t)u.head * D
+                    : h < heads_kv
+                        ? static_cast<const uint16_t *>(p.k) + t * p.k_stride + (int64_t)h * D
+                        : static_cast<const uint16_t *>(p.v) + t * p.v_stride +
+                              (int64_t)(h - heads_kv) * D;
+            u.slot = __ldg(p.slots + t);
+            u.pos = __ldg(p.positions + t);
+            u.w0 = reinterpret_cast<const uint4 *>(u.row)[cp.c0];
+            u.w1 = reinterpret_cast<const uint4 *>(u.row)[cp.c1];
         }
-        if ((is_q || is_k) && cp.turned) {
+        t += step_t;
+        within += step_w;
+        if (within >= per_token) {
+            within -= per_token;
+            ++t;
+        }
+    };
+    auto finish = [&](RowUnit &u) {
+        if (u.t >= p.num_tokens || u.slot < 0) return;    // a negative slot: no token here
+        if (u.slot >= p.num_slots || u.pos < 0 || u.pos >= p.max_positions) {
+            if (u.head == 0 && u.i == 0)
+                atomicOr(p.status, u.slot >= p.num_slots ? PKV_DEV_BAD_SLOT : PKV_DEV_BAD_POS);
+            return;
+        }
+        const ChunkPair cp = chunk_pair<NEIGHBOURS>(u.i, p.rotary_dim);
+        const int h = u.head - p.num_q_heads;
+        if (h < heads_kv && cp.turned) {
             float x[16];
-            unpack8<BF16>(w0, x);
-            unpack8<BF16>(w1, x + 8);
-            rotate16<NEIGHBOURS>(x, i, half, p.cos_sin + (int64_t)pos * p.rotary_dim);
-            w0 = pack8<BF16>(x);
-            w1 = pack8<BF16>(x + 8);
+            unpack8<BF16>(u.w0, x);
+            unpack8<BF16>(u.w1, x + 8);
+            rotate16<NEIGHBOURS>(x, u.i, p.rotary_dim >> 1, p.cos_sin + (int64_t)u.pos * p.rotary_dim);
+            u.w0 = pack8<BF16>(x);
+            u.w1 = pack8<BF16>(x + 8);
         }
         uint4 *dst;
-        if (is_q) {
-            dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.q_out) + t * p.q_out_stride +
-                                            (int64_t)head * D);
+        if (h < 0) {
+            dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.q_out) + u.t * p.q_out_stride +
+                                            (int64_t)u.head * D);
         } else {
-            const int64_t block = slot / p.block_size;
-            const int64_t off = slot - block * p.block_size;
-            dst = (is_k ? p.k_pool : p.v_pool) +
+            const int64_t block = u.slot / p.block_size;
+            const int64_t off = u.slot - block * p.block_size;
+            const int kvh = h < heads_kv ? h : h - heads_kv;
+            dst = (h < heads_kv ? p.k_pool : p.v_pool) +
                   ((block * heads_kv + kvh) * p.block_size + off) * (D >> 3);
         }
-        dst[cp.c0] = w0;
-        dst[cp.c1] = w1;
+        dst[cp.c0] = u.w0;
+        dst[cp.c1] = u.w1;
+    };
+    while (t < p.num_tokens) {
+        RowUnit a, b;
+        load(a);
+        load(b);
+        finish(a);
+        finish(b);
     }
 }
 
 template <bool BF16, bool NEIGHBOURS>
-__global__ void __launch_bounds__(256) append_rope_kernel(const Params p, int D)
+__global__ void __launch_bounds__(256) append_rope_kernel(const Params p, int D, int heads_kv)
 {
-    append_rows<BF16, NEIGHBOURS>(p, D, p.num_kv_heads, blockIdx.x, gridDim.x);
+    append_rows<BF16, NEIGHBOURS>(p, D, heads_kv, blockIdx.x, gridDim.x);
 }
 
 // ------------------------------------------------------- block-scaled 8-bit pools
@@ -227,8 +254,11 @@ __device__ __forceinline__ uint32_t b8_rescale4(uint32_t w, float ratio)
 // where "scale before" counts only when the run does not start the block (off0
 // > 0).  When the scale grows, the codes of tokens 0 .. off0 - 1 are rounded to
 // it: rn(code * rn(old / new)).
-// A row is D / 16 lanes of 16 values; all rows of the run stay in registers
-// between the maximum and the codes, so each value is read once.
+// A row is D / 16 lanes of 16 values.  The rows of the run stay in registers,
+// packed, between the maximum and the codes, so each value is read once; K is
+// rotated for both (keeping the fp32 values instead took 154 registers, which
+// left too few warps to fill the memory pipe: 176 us against TIME on 16,700
+// tokens of 8 heads).
 template <bool BF16, bool NEIGHBOURS, int D>
 __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, int64_t t0, int n,
                                              int64_t block, int off0, int lane)
@@ -247,7 +277,7 @@ __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, i
                                 : ChunkPair{2 * i, 2 * i + 1, false};
     const float old = off0 > 0 ? *scale_at : 0.f;
     uint4 w[kPasses][2];
-    int pos[kPasses];
+    int pos[kPasses];                    // -1: no row, or one to skip
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
         const int j = k * kRows + r;
@@ -255,33 +285,34 @@ __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, i
         const uint4 *row = reinterpret_cast<const uint4 *>(rows + (t0 + (in ? j : 0)) * stride);
         w[k][0] = in ? row[cp.c0] : make_uint4(0u, 0u, 0u, 0u);
         w[k][1] = in ? row[cp.c1] : make_uint4(0u, 0u, 0u, 0u);
-        pos[k] = in && p.positions ? __ldg(p.positions + t0 + j) : 0;
+        pos[k] = !in ? -1 : p.positions ? __ldg(p.positions + t0 + j) : 0;
     }
-    float x[kPasses][16];
-    unsigned ok = 0;                     // bit k: row of pass k counts
+    auto values = [&](int k, float (&x)[16]) {
+        unpack8<BF16>(w[k][0], x);
+        unpack8<BF16>(w[k][1], x + 8);
+        if (cp.turned)
+            rotate16<NEIGHBOURS>(x, i, p.rotary_dim >> 1, p.cos_sin + (int64_t)pos[k] * p.rotary_dim);
+    };
     float amax = 0.f;
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
         if (k * kRows >= n) break;       // the same for the whole warp
         const int j = k * kRows + r;
-        const bool good = !p.positions || (pos[k] >= 0 && pos[k] < p.max_positions);
-        if (j < n && !good && i == 0) atomicOr(p.status, PKV_DEV_BAD_POS);
-        if (j >= n || !good) continue;
-        ok |= 1u << k;
-        unpack8<BF16>(w[k][0], x[k]);
-        unpack8<BF16>(w[k][1], x[k] + 8);
-        if (cp.turned)
-            rotate16<NEIGHBOURS>(x[k], i, p.rotary_dim >> 1,
-                                 p.cos_sin + (int64_t)pos[k] * p.rotary_dim);
+        if (p.positions && j < n && (pos[k] < 0 || pos[k] >= p.max_positions)) {
+            if (i == 0) atomicOr(p.status, PKV_DEV_BAD_POS);
+            pos[k] = -1;
+        }
+        if (pos[k] < 0) continue;
+        float x[16];
+        values(k, x);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[k][e]));   // ignores NaN
+        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));   // ignores NaN
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
     amax = amax < kB8Tiny ? 0.f : fminf(amax, 0x1.fep127f);   // an infinity takes the largest bf16
     constexpr float kRcp127 = 0x1.020408p-7f;                 // rn(1 / 127)
-    const float fresh = __fmul_rn(amax, kRcp127);
-    const float now = fmaxf(old, fresh);
+    const float now = fmaxf(old, __fmul_rn(amax, kRcp127));
     if (off0 > 0 && now > old) {
         const float ratio = __fdiv_rn(old, now);
         for (int c = lane; c < off0 * kLanes; c += 32) {
@@ -294,17 +325,19 @@ __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, i
             *at = v;
         }
     }
-    if (lane == 0 && now != old) *scale_at = now;
-    if (lane == 0 && off0 == 0 && now == old) *scale_at = 0.f;
+    if (lane == 0 && (off0 == 0 || now != old)) *scale_at = now;
     const float inv = now > 0.f ? __fdiv_rn(1.f, now) : 0.f;
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
-        if (!((ok >> k) & 1u)) continue;
+        if (k * kRows >= n) break;
+        if (pos[k] < 0) continue;
         const int t = off0 + k * kRows + r;
+        float x[16];
+        values(k, x);
         *reinterpret_cast<uint2 *>(codes + b8_chunk(t, cp.c0 >> 1, D) + 8 * (cp.c0 & 1)) =
-            make_uint2(b8_codes4(x[k], inv), b8_codes4(x[k] + 4, inv));
+            make_uint2(b8_codes4(x, inv), b8_codes4(x + 4, inv));
         *reinterpret_cast<uint2 *>(codes + b8_chunk(t, cp.c1 >> 1, D) + 8 * (cp.c1 & 1)) =
-            make_uint2(b8_codes4(x[k] + 8, inv), b8_codes4(x[k] + 12, inv));
+            make_uint2(b8_codes4(x + 8, inv), b8_codes4(x + 12, inv));
     }
 }
 
@@ -313,7 +346,7 @@ __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, i
 // follow one another inside a block; lane l looks at token tb - 1 + l, so a run
 // that begins at the span's last token is seen to its end.
 template <bool BF16, bool NEIGHBOURS, int D>
-__global__ void __launch_bounds__(128) append_b8_kernel(const Params p)
+__global__ void __launch_bounds__(128, 6) append_b8_kernel(const Params p)
 {
     if ((int)blockIdx.x >= p.write_blocks) {              // queries only
         append_rows<BF16, NEIGHBOURS>(p, D, 0, (int)blockIdx.x - p.write_blocks,
@@ -392,6 +425,15 @@ __global__ void __launch_bounds__(256)
 constexpr int64_t kSpanUnits = 8192;
 
 template <bool BF16, bool NEIGHBOURS>
+static int launch_rows(const Params &p, int D, int heads_kv, cudaStream_t st)
+{
+    const int64_t threads = (int64_t)p.num_tokens * (p.num_q_heads + 2 * heads_kv) * (D / 16);
+    const int64_t grid = std::min<int64_t>((threads + 511) / 512, 152 * 64);   // two units a thread
+    append_rope_kernel<BF16, NEIGHBOURS><<<(unsigned)grid, 256, 0, st>>>(p, D, heads_kv);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+template <bool BF16, bool NEIGHBOURS>
 static int launch_b8(const Params &p0, int D, bool queries, cudaStream_t st)
 {
     Params p = p0;
@@ -400,21 +442,16 @@ static int launch_b8(const Params &p0, int D, bool queries, cudaStream_t st)
     const int64_t units = p.span == 16 ? spans : (int64_t)p.num_tokens * 2 * p.num_kv_heads;
     p.write_blocks = (int32_t)std::min<int64_t>((units + 3) / 4, 152 * 64);
     int64_t grid = p.write_blocks;
-    if (queries) {
+    if (queries && p.span == 16) {
+        // many tokens: the queries in a launch of their own, at full occupancy
+        const int rc = launch_rows<BF16, NEIGHBOURS>(p, D, 0, st);
+        if (rc != PKV_OK) return rc;
+    } else if (queries) {
         const int64_t threads = (int64_t)p.num_tokens * p.num_q_heads * (D / 16);
-        grid += std::min<int64_t>((threads + 127) / 128, 152 * 64);
+        grid += std::min<int64_t>((threads + 255) / 256, 152 * 64);
     }
     if (D == 128) append_b8_kernel<BF16, NEIGHBOURS, 128><<<(unsigned)grid, 128, 0, st>>>(p);
     else append_b8_kernel<BF16, NEIGHBOURS, 64><<<(unsigned)grid, 128, 0, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
-}
-
-template <bool BF16, bool NEIGHBOURS>
-static int launch_16bit(const Params &p, int D, cudaStream_t st)
-{
-    const int64_t threads = (int64_t)p.num_tokens * (p.num_q_heads + 2 * p.num_kv_heads) * (D / 16);
-    const int64_t grid = std::min<int64_t>((threads + 255) / 256, 152 * 64);
-    append_rope_kernel<BF16, NEIGHBOURS><<<(unsigned)grid, 256, 0, st>>>(p, D);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -489,10 +526,10 @@ extern "C" int kv_cache_write_rope(const pkv_pool *pool, void *q_out, int64_t q_
                   : (nb ? launch_b8<false, true>(p, g.head_dim, q, st)
                         : launch_b8<false, false>(p, g.head_dim, q, st));
     }
-    return bf ? (nb ? launch_16bit<true, true>(p, g.head_dim, st)
-                    : launch_16bit<true, false>(p, g.head_dim, st))
-              : (nb ? launch_16bit<false, true>(p, g.head_dim, st)
-                    : launch_16bit<false, false>(p, g.head_dim, st));
+    return bf ? (nb ? launch_rows<true, true>(p, g.head_dim, g.num_kv_heads, st)
+                    : launch_rows<true, false>(p, g.head_dim, g.num_kv_heads, st))
+              : (nb ? launch_rows<false, true>(p, g.head_dim, g.num_kv_heads, st)
+                    : launch_rows<false, false>(p, g.head_dim, g.num_kv_heads, st));
 }
 
 extern "C" int kv_cache_write_b8(const pkv_pool *pool, const void *k_new, const void *v_new,

@@ -314,6 +314,12 @@ __device__ __forceinline__ uint64_t sub2f(uint64_t a, uint64_t b)
     return d;
 }
 
+// The n lowest of 64 bits (all for n >= 64, none for n <= 0).
+__device__ __forceinline__ uint64_t low_bits(int n)
+{
+    return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
+}
+
 // bf16 weights (p0, p1) (pp = the same pair packed) as a high and a low part,
 // the even index in the low half of each word: the high part is the weight
 // truncated to bf16 (its upper 16 bits, exact), the low part the remainder
@@ -652,10 +658,6 @@ __global__ void __launch_bounds__(kThreads)
                 first = valid ? pos - p.window + 1 - it.gap * kBlock : 0;
                 if (valid) pos -= it.gap * kBlock;
             }
-            // key n of the item hidden from this row
-            auto hidden = [&](int n) {
-                return n > pos || (WINDOW && n < first && n >= p.sinks);
-            };
             float m_ref = -INFINITY, l = 0.f;
             int bad = 0;
             for (int t = 0; t < it.ntiles; ++t, ++tg) {
@@ -682,14 +684,28 @@ __global__ void __launch_bounds__(kThreads)
                 // raw scores; the scale enters inside the exponent (one FFMA each).
                 // Hidden keys are kept out of the maximum here and get weight 0 below.
                 const int k0 = t * kKeys;
-                bool cross = k0 + kKeys - 1 > pos;         // the tile crosses this row's position
-                if constexpr (WINDOW)                      // or holds keys behind its window
-                    cross |= k0 < first && k0 + kKeys > p.sinks;
-                if (cross) {
+                const bool cross = k0 + kKeys - 1 > pos;   // the tile crosses this row's position
+                if constexpr (WINDOW) {
+                    // or holds keys behind its window.  Both edges of a window move
+                    // with the row, so many tiles cross some row of a warp: the test
+                    // is one bit per key, the branch the same for the warp, and
+                    // hidden scores reach weight 0 through the exponent (below)
+                    if (__any_sync(kFull, cross || (k0 < first && k0 + kKeys > p.sinks))) {
+                        const float hide = p.scale_log2 < 0.f ? INFINITY : -INFINITY;
+                        const uint64_t see = low_bits(pos - k0 + 1) &
+                                             (~low_bits(first - k0) | low_bits(p.sinks - k0));
+                        const uint32_t see0 = (uint32_t)see, see1 = (uint32_t)(see >> 32);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            if (!((see0 >> c) & 1u)) x[c] = hide;
+                            if (!((see1 >> c) & 1u)) x[32 + c] = hide;
+                        }
+                    }
+                } else if (cross) {
                     const float hide = p.scale_log2 < 0.f ? INFINITY : -INFINITY;
 #pragma unroll
                     for (int c = 0; c < kKeys; ++c)
-                        if (hidden(k0 + c)) x[c] = hide;
+                        if (k0 + c > pos) x[c] = hide;
                 }
                 float mx;
                 if (p.scale_log2 >= 0.f) {
@@ -714,7 +730,10 @@ __global__ void __launch_bounds__(kThreads)
                 // weights in pairs: packed fp32 arithmetic (f32x2), then a high and a
                 // low 16-bit part per weight
                 uint32_t hi[kKeys / 2], lo[kKeys / 2];
-                const uint64_t sc2 = pack2f(p.scale_log2, p.scale_log2), nm2 = pack2f(-m_ref, -m_ref);
+                // (a windowed row that has seen no key yet has m_ref = -inf; any finite
+                // reference gives its hidden scores weight 2^-inf = 0)
+                const float m_sub = WINDOW && m_ref == -INFINITY ? 0.f : m_ref;
+                const uint64_t sc2 = pack2f(p.scale_log2, p.scale_log2), nm2 = pack2f(-m_sub, -m_sub);
                 uint64_t lsum2 = pack2f(0.f, 0.f);
                 // two copies of the loop: only a tile that crosses the row's
                 // position pays for the per-key causal test
@@ -724,8 +743,8 @@ __global__ void __launch_bounds__(kThreads)
                         const float2 e = unpack2f(fma2f(pack2f(x[c], x[c + 1]), sc2, nm2));
                         float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
                         if constexpr (decltype(masked)::value) {
-                            if (hidden(k0 + c)) p0 = 0.f;
-                            if (hidden(k0 + c + 1)) p1 = 0.f;
+                            if (k0 + c > pos) p0 = 0.f;
+                            if (k0 + c + 1 > pos) p1 = 0.f;
                         }
                         const uint64_t pp = pack2f(p0, p1);
                         lsum2 = add2f(lsum2, pp);
@@ -735,7 +754,7 @@ __global__ void __launch_bounds__(kThreads)
                             hi[c / 2] = Elem<false>::pack(p0, p1);
                     }
                 };
-                if (cross) weights(std::true_type{});
+                if (!WINDOW && cross) weights(std::true_type{});
                 else weights(std::false_type{});
                 const float2 ls = unpack2f(lsum2);
                 l = l * f + (ls.x + ls.y);
@@ -1760,6 +1779,9 @@ static int prefill_call(const pkv_pool *pool, void *out, const void *q, const vo
     prm.window = window;
     prm.sinks = sinks;
     prm.scale_log2 = scale * 1.4426950408889634f;
+    // a windowed call hides scores by an infinity that the scale must carry into
+    // the exponent; at scale 0 the smallest normal number weighs all keys alike
+    if (window > 0 && scale == 0.f) prm.scale_log2 = 0x1p-126f;
     prm.header = static_cast<int32_t *>(workspace);
     prm.items = reinterpret_cast<int2 *>(static_cast<char *>(workspace) + 256);
     prm.max_items = max_items(num_seqs, num_tokens, prm.tile_tokens);

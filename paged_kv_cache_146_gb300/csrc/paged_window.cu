@@ -5,14 +5,15 @@
 //   x_j = scale <q, K_j>,  out = sum_j softmax(x)_j V_j   over the visible j:
 //   j < L  and  (j >= L - window  or  j < sinks)
 //
-// One launch, no workspace.  A (sequence, kv head) pair is one cluster of C
-// CTAs of four warps; its visible blocks -- the sinks' blocks, then the
-// window's, numbered without the gap between them -- are dealt to the C * 4
+// One launch, no workspace.  A (sequence, kv head) pair is one cluster of C CTAs
+// (C = 1: a plain CTA).  Its visible blocks -- the sinks' blocks, then the
+// window's, numbered without the gap between them -- are dealt to the cluster's
 // warps in turn.  Each warp is its own producer: it keeps a private ring of
 // stages, lane 0 copies block i + kStages (TMA) as soon as block i is consumed,
-// and block ids are fetched 32 at a time, one batch ahead.  The four warps'
-// (o, max, sum) meet in shared memory, the C CTAs' through distributed shared
-// memory, always in the same order, so results do not vary from run to run.
+// and block ids are fetched 32 at a time, one batch ahead.  The warps' (o, max,
+// sum) meet in shared memory, the CTAs' through distributed shared memory, always
+// in the same order, so results do not vary from run to run.  Where the grid is
+// more than one wave of ragged lengths, the longest pairs go first.
 //
 // Per 16-token block and warp, everything on mma.sync m16n8k16 with the tokens
 // (then the dimensions) as the 16 rows and eight query heads as the columns:
@@ -21,9 +22,15 @@
 //   O^T += V^T P^T     rows = dimensions; P^T comes from S^T's accumulator
 //                      layout through one 8x8 transpose (movmatrix) per half
 // so no half of a matrix instruction works on empty rows (G <= 8), and the
-// statistics and the accumulators of a head sit in the same lanes.
+// statistics and the accumulators of a head sit in the same lanes.  (tcgen05
+// takes 64 or 128 rows: with G <= 16 query rows per pair and a new K tile each
+// step it would idle; the tensor pipe is 25 % busy here.)
 //
-// The bytes of the visible K and V bound it; a block is read once.
+// The bytes of the visible K and V bound it, each read once: 256 sequences x 8
+// kv heads x window 1,024 (16-bit, 1.05 GB) 156 us, 6.7 TB/s; 160 ragged contexts
+// of up to 16,384 tokens (8-bit, 2.87 GB) 414 us, 6.9 TB/s.  Where a few pairs
+// leave SMs idle, an SM's own pace counts: 57 GB/s of 8-bit blocks (280
+// instructions per block and warp, the byte permutations half of the ALU pipe).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -40,8 +47,6 @@
 namespace pkv {
 namespace window {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kMaxHeads = 16;            // query heads per kv head
 // The reference maximum moves only when a score exceeds it by more than this
 // (log2 units): weights stay within 2^6, far inside fp16's and bf16's range.
@@ -58,6 +63,8 @@ struct Params {
     int32_t ctas;                        // cluster size C
     float scale_log2;
     int32_t *status;
+    int32_t num_seqs;
+    int32_t most;                        // > 0: pairs run longest first; the most blocks one can show
 };
 
 using KernelFn = void (*)(CUtensorMap, CUtensorMap, Params);
@@ -67,6 +74,12 @@ using KernelFn = void (*)(CUtensorMap, CUtensorMap, Params);
 struct Visible {
     int L, lo, sinks, sink_blocks, gap, n;
     __device__ __forceinline__ int block(int v) const { return v < sink_blocks ? v : v + gap; }
+    // some token of logical block b is hidden
+    __device__ __forceinline__ bool partial(int b) const
+    {
+        const int t0 = b * kBlock;
+        return t0 + kBlock > L || (t0 < lo && t0 + kBlock > sinks);
+    }
     // bit t: token t of logical block b is visible
     __device__ __forceinline__ uint32_t mask(int b) const
     {
@@ -126,18 +139,19 @@ __device__ __forceinline__ float2 cluster_load2(uint32_t addr)
 }
 
 // Shapes of one variant.  B8: block-scaled 8-bit records; else 16-bit pools.
-template <int D, bool B8, int NT>
+template <int D, bool B8, int NT, int W>
 struct Shape {
+    static constexpr int kThreads = 32 * W;
     static constexpr int kCopyBytes = B8 ? 32 * D + 16 : 64 * D;       // of one block and head
     static constexpr int kStageBytes = B8 ? (32 * D + 16 + 127) / 128 * 128 : 64 * D;
     // stages per warp: 16-bit 24 KB in flight, 2 CTAs per SM; 8-bit 16 KB, 3 CTAs per SM
     static constexpr int kStages = B8 ? (D == 128 ? 4 : 8) : (D == 128 ? 3 : 6);
-    static constexpr int kMinBlocks = B8 ? 3 : 2;
+    static constexpr int kMinBlocks = W > 4 ? 1 : B8 && NT == 1 ? 3 : 2;
     static constexpr int kWarpBytes = kStages * kStageBytes;
     static constexpr int kRow = D + 4;                                  // floats of a merge row
-    static constexpr int kBars = kWarps * kWarpBytes;
-    static constexpr int kMl = kBars + kWarps * 8 * 8;                  // [warps + 1][16] float2
-    static constexpr int kTotal = 1024 + kMl + (kWarps + 1) * kMaxHeads * 8;
+    static constexpr int kBars = W * kWarpBytes;
+    static constexpr int kMl = kBars + W * 8 * 8;                       // [warps + 1][16] float2
+    static constexpr int kTotal = 1024 + kMl + (W + 1) * kMaxHeads * 8;
     static_assert(kStages <= 8 && 8 * NT * kRow * 4 <= kWarpBytes, "merge rows fit a warp's ring");
 };
 
@@ -150,45 +164,108 @@ struct State {
     float m[NT][2], l[NT][2];
 };
 
-// Scores (log2 domain) of tokens r and r + 8 -> weights, with the lazy
-// reference maximum; x[nt] = (r, head 0), (r, head 1), (r + 8, head 0), (r + 8, head 1).
+// The query rows of a kv head as B operands (head r of tile nt); for 8-bit pools
+// also each row's scale and its offset (see codes_lo), for heads 2 q4 and 2 q4 + 1.
 template <int D, int NT>
-__device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&x)[NT][4])
+struct Queries {
+    uint32_t b[NT][D / 16][2];
+    float scale[NT][2], off[NT][2];
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void reset(State<D, NT> &st)
+{
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        st.m[nt][0] = st.m[nt][1] = -INFINITY;
+        st.l[nt][0] = st.l[nt][1] = 0.f;
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st.o[nt][t][e] = 0.f;
+    }
+}
+
+// Products x of tokens r and r + 8 of NB blocks -> weights 2^(x f - m), with the
+// lazy reference maximum m; x[b][nt] = (r, head 0), (r, head 1), (r + 8, head 0),
+// (r + 8, head 1), f[b][nt] = the heads' factors to the log2 domain, hidden
+// tokens' bits 0 in masks[b].
+template <int D, int NT, int NB>
+__device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&x)[NB][NT][4],
+                                             const float (&f)[NB][NT][2], const uint32_t (&masks)[NB],
+                                             int lane)
 {
     bool raise = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) raise |= x[nt][e] > st.m[nt][e & 1] + kLazy;
+        for (int h = 0; h < 2; ++h) {
+            raise |= st.m[nt][h] == -INFINITY;           // no token yet: x f is taken against 0
+            const float neg = st.m[nt][h] == -INFINITY ? 0.f : -st.m[nt][h];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    float &y = x[b][nt][2 * t + h];
+                    y = fmaf(y, f[b][nt][h], neg);
+                }
+        }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        if (masks[b] == 0xffffu) continue;               // the same for the warp
+        const bool v0 = (masks[b] >> (lane >> 2)) & 1u, v1 = (masks[b] >> ((lane >> 2) + 8)) & 1u;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (!(e < 2 ? v0 : v1)) x[b][nt][e] = -INFINITY;
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) raise |= x[b][nt][e] > kLazy;
     if (__any_sync(kFull, raise)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float mx = fmaxf(x[nt][h], x[nt][2 + h]);
-                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
-                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
-                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-                const float mn = fmaxf(st.m[nt][h], mx);
-                const float f = mn == -INFINITY ? 1.f : fast_exp2(st.m[nt][h] - mn);
-                st.m[nt][h] = mn;
-                st.l[nt][h] *= f;
+                float up = fmaxf(x[0][nt][h], x[0][nt][2 + h]);
+#pragma unroll
+                for (int b = 1; b < NB; ++b) up = fmaxf(up, fmaxf(x[b][nt][h], x[b][nt][2 + h]));
+                up = fmaxf(up, __shfl_xor_sync(kFull, up, 4));
+                up = fmaxf(up, __shfl_xor_sync(kFull, up, 8));
+                up = fmaxf(up, __shfl_xor_sync(kFull, up, 16));
+                // the reference moves up to the largest score (exactly to it at first)
+                const bool none = st.m[nt][h] == -INFINITY;
+                if (!none) up = fmaxf(up, 0.f);
+                const float s = none ? 1.f : fast_exp2(-up);
+                st.m[nt][h] = none ? up : st.m[nt][h] + up;
+                if (up == -INFINITY) up = 0.f;           // still no finite score
+                st.l[nt][h] *= s;
 #pragma unroll
                 for (int t = 0; t < D / 16; ++t) {
-                    st.o[nt][t][h] *= f;
-                    st.o[nt][t][2 + h] *= f;
+                    st.o[nt][t][h] *= s;
+                    st.o[nt][t][2 + h] *= s;
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    x[b][nt][h] -= up;
+                    x[b][nt][2 + h] -= up;
                 }
             }
         }
     }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float m = st.m[nt][e & 1];
-            x[nt][e] = fast_exp2(x[nt][e] - (m == -INFINITY ? 0.f : m));
-            st.l[nt][e & 1] += x[nt][e];
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[b][nt][e] = fast_exp2(x[b][nt][e]);
+                st.l[nt][e & 1] += x[b][nt][e];
+            }
 }
 
 // Weights x[4] of one head tile as the B operand of the P V product, in type E:
@@ -218,14 +295,16 @@ __device__ __forceinline__ void weights_lo(const float (&x)[4], const uint32_t (
 // P goes in as a high and a low part of the pool's type, which carries the
 // weights to ~2^-17 (a bf16 weight alone would be off by 2^-9).
 template <int D, bool BF16, int NT>
-__device__ __forceinline__ void consume_16bit(uint32_t kb, const uint32_t (&qb)[NT][D / 16][2],
+__device__ __forceinline__ void consume_16bit(uint32_t kb, const Queries<D, NT> &qs,
                                               State<D, NT> &st, uint32_t mask, float scale_log2,
                                               int lane)
 {
     using E = Elem<BF16>;
+    const auto &qb = qs.b;
     const int r = lane >> 2, q4 = lane & 3, mi = lane >> 3, r8 = lane & 7;
     const uint32_t vb = kb + 32 * D;
-    float c0[NT][4], c1[NT][4];          // two chains of products
+    float x[1][NT][4], c1[NT][4];        // two chains of products
+    float (&c0)[NT][4] = x[0];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -240,13 +319,16 @@ __device__ __forceinline__ void consume_16bit(uint32_t kb, const uint32_t (&qb)[
         for (int nt = 0; nt < NT; ++nt)
             E::mma(kk & 1 ? c1[nt] : c0[nt], a, qb[nt][kk][0], qb[nt][kk][1]);
     }
-    const bool v0 = (mask >> r) & 1u, v1 = (mask >> (r + 8)) & 1u;
+    float f[1][NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+        f[0][nt][0] = f[0][nt][1] = scale_log2;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            c0[nt][e] = (e < 2 ? v0 : v1) ? (c0[nt][e] + c1[nt][e]) * scale_log2 : -INFINITY;
-    softmax_step<D, NT>(st, c0);
+        for (int e = 0; e < 4; ++e) c0[nt][e] += c1[nt][e];
+    }
+    const bool edge = mask != 0xffffu;   // the same for the warp: an edge of the visible part
+    const uint32_t masks[1] = {mask};
+    softmax_step<D, NT, 1>(st, x, f, masks, lane);
     uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -264,10 +346,12 @@ __device__ __forceinline__ void consume_16bit(uint32_t kb, const uint32_t (&qb)[
         const int chunk = 2 * t + (mi & 1);
         uint32_t a[4];
         ldsm_x4_trans(a, vb + (chunk >> 3) * kBoxBytes + v_tok * 128 + (((chunk & 7) ^ r8) << 4));
-        a[0] &= keep_lo;
-        a[1] &= keep_lo;
-        a[2] &= keep_hi;
-        a[3] &= keep_hi;
+        if (edge) {
+            a[0] &= keep_lo;
+            a[1] &= keep_lo;
+            a[2] &= keep_hi;
+            a[3] &= keep_hi;
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             E::mma(st.o[nt][t], a, hi[nt][0], hi[nt][1]);
@@ -277,19 +361,35 @@ __device__ __forceinline__ void consume_16bit(uint32_t kb, const uint32_t (&qb)[
 }
 
 // ------------------------------------------------------------------- 8-bit block
-// Byte u = code + 128 is the low mantissa of fp16 1024 + u (bits 0x6400 | u);
-// minus 1152 that is the code, exactly.
+// Byte u = code + 128 is the low mantissa of fp16 1024 + u (bits 0x6400 | u), so
+// a byte pair becomes an fp16 pair by one byte permutation, each value carrying
+// an offset of 1152.  The products take it along and their accumulators start
+// from -1152 times the other operand's sum, which one product with a constant
+// operand gives.  A product of an fp16 value and 1152 + code (11 bits each) is
+// exact in fp32; the offset makes the terms of the fp32 sums up to ten times as
+// large (1279 against 127), and their rounding with them, still 2^-19 of the
+// operands' scale.  Subtracting the offset from every pair instead takes 64 more
+// instructions per block (305 against 280), 2 % where the SM is the limit.
+constexpr uint32_t kNegOffset = 0xE480E480u;                 // (-1152, -1152)
 __device__ __forceinline__ uint32_t codes_lo(uint32_t w)     // bytes 0 and 1
 {
-    uint32_t x = __byte_perm(w, 0x64646464u, 0x4140);
-    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0x64806480u));
-    return x;
+    return __byte_perm(w, 0x64646464u, 0x4140);
 }
 __device__ __forceinline__ uint32_t codes_hi(uint32_t w)     // bytes 2 and 3
 {
-    uint32_t x = __byte_perm(w, 0x64646464u, 0x4342);
-    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0x64806480u));
-    return x;
+    return __byte_perm(w, 0x64646464u, 0x4342);
+}
+
+// d = a b + c on fp16 operands.
+__device__ __forceinline__ void mma_from(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2],
+                                         const float (&c)[4])
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
 }
 
 // Offset of 16-byte chunk j of token t in the K or V codes (pagedkv.h).
@@ -308,21 +408,29 @@ __device__ __forceinline__ int chunk_at(int t, int j)
 // and the queries were laid out alike; of V it takes dimensions D/8 r ..
 // D/8 (r + 1) of its four tokens and pairs their bytes.
 // P: one fp16 part for bf16 rows (2^-12, below the output's 2^-9), two for fp16.
-template <int D, bool BF16, int NT>
-__device__ __forceinline__ void consume_b8(const uint8_t *rec, const uint32_t (&qb)[NT][D / 16][2],
-                                           const float (&scale_row)[NT][2], State<D, NT> &st,
-                                           uint32_t mask, int lane)
+// NB blocks at a time: their chains of dependent instructions overlap.
+template <int D, bool BF16, int NT, int NB>
+__device__ __forceinline__ void consume_b8(const uint8_t *const (&recs)[NB],
+                                           const Queries<D, NT> &qs, State<D, NT> &st,
+                                           const uint32_t (&masks)[NB], int lane)
 {
     using H = Elem<false>;
+    const auto &qb = qs.b;
+    const auto &k_off = qs.off;
+    const auto &scale_row = qs.scale;
     const int r = lane >> 2, q4 = lane & 3;
-    const float2 scales = *reinterpret_cast<const float2 *>(rec + 32 * D);
-    float x[NT][4];
-    {
-        float c0[NT][4], c1[NT][4];
+    float x[NB][NT][4], f[NB][NT][2];
+    float v_scale[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const uint8_t *rec = recs[b];
+        const float2 scales = *reinterpret_cast<const float2 *>(rec + 32 * D);
+        v_scale[b] = scales.y;
+        float c[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) c0[nt][e] = c1[nt][e] = 0.f;
+            for (int e = 0; e < 4; ++e) c[nt][e] = k_off[nt][e & 1];
 #pragma unroll
         for (int half = 0; half < D / 64; ++half) {
             const uint4 wa = *reinterpret_cast<const uint4 *>(rec + chunk_at<D>(r, q4 + 4 * half));
@@ -334,70 +442,201 @@ __device__ __forceinline__ void consume_b8(const uint8_t *rec, const uint32_t (&
                                        codes_hi(ub[i])};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    H::mma(i & 1 ? c1[nt] : c0[nt], a, qb[nt][4 * half + i][0],
-                           qb[nt][4 * half + i][1]);
+                    H::mma(c[nt], a, qb[nt][4 * half + i][0], qb[nt][4 * half + i][1]);
             }
         }
-        const bool v0 = (mask >> r) & 1u, v1 = (mask >> (r + 8)) & 1u;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float f[2] = {scales.x * scale_row[nt][0], scales.x * scale_row[nt][1]};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                x[nt][e] = (e < 2 ? v0 : v1) ? (c0[nt][e] + c1[nt][e]) * f[e & 1] : -INFINITY;
+            for (int h = 0; h < 2; ++h) f[b][nt][h] = scales.x * scale_row[nt][h];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[b][nt][e] = c[nt][e];
         }
     }
-    softmax_step<D, NT>(st, x);
-    uint32_t hi[NT][2], lo[NT][2];
+    softmax_step<D, NT, NB>(st, x, f, masks, lane);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        uint32_t raw[2];
-        weights_hi<H>(x[nt], hi[nt], raw);
-        if constexpr (!BF16) weights_lo<H>(x[nt], raw, lo[nt]);
-    }
-    // words of tokens 2q4, 2q4 + 1, 2q4 + 8, 2q4 + 9: four dimensions each
-    constexpr int kWords = D / 32;
-    uint32_t w[4][kWords];
+    for (int b = 0; b < NB; ++b) {
+        uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int t = 2 * q4 + (k & 1) + 8 * (k >> 1);
-        const uint8_t *at = rec + 16 * D;
-        if constexpr (D == 128) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(at + chunk_at<D>(t, r));
-            w[k][0] = v.x; w[k][1] = v.y; w[k][2] = v.z; w[k][3] = v.w;
-        } else {
-            const uint2 v = *reinterpret_cast<const uint2 *>(at + chunk_at<D>(t, r >> 1) + 8 * (r & 1));
-            w[k][0] = v.x; w[k][1] = v.y;
+        for (int nt = 0; nt < NT; ++nt) {
+            uint32_t raw[2];
+            weights_hi<H>(x[b][nt], hi[nt], raw);
+            if constexpr (!BF16) weights_lo<H>(x[b][nt], raw, lo[nt]);
         }
-    }
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-#pragma unroll
-        for (int pr = 0; pr < 2; ++pr) {          // dimensions 4i + 2 pr, 4i + 2 pr + 1
-            const uint32_t sel = pr ? 0x7362 : 0x5140;
-            const uint32_t p01 = __byte_perm(w[0][i], w[1][i], sel);
-            const uint32_t p89 = __byte_perm(w[2][i], w[3][i], sel);
-            const uint32_t a[4] = {codes_lo(p01), codes_hi(p01), codes_lo(p89), codes_hi(p89)};
+        float v_off[NT][4];              // -1152 x the weights' sums, every row alike
+        {
+            const uint32_t neg[4] = {kNegOffset, kNegOffset, kNegOffset, kNegOffset};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float c[4];
-                H::mma0(c, a, hi[nt][0], hi[nt][1]);
-                if constexpr (!BF16) H::mma(c, a, lo[nt][0], lo[nt][1]);
-                float *o = st.o[nt][2 * i + pr];
+                H::mma0(v_off[nt], neg, hi[nt][0], hi[nt][1]);
+                if constexpr (!BF16) H::mma(v_off[nt], neg, lo[nt][0], lo[nt][1]);
+            }
+        }
+        // words of tokens 2q4, 2q4 + 1, 2q4 + 8, 2q4 + 9: four dimensions each
+        constexpr int kWords = D / 32;
+        uint32_t w[4][kWords];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = fmaf(scales.y, c[e], o[e]);
+        for (int k = 0; k < 4; ++k) {
+            const int t = 2 * q4 + (k & 1) + 8 * (k >> 1);
+            const uint8_t *at = recs[b] + 16 * D;
+            if constexpr (D == 128) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(at + chunk_at<D>(t, r));
+                w[k][0] = v.x; w[k][1] = v.y; w[k][2] = v.z; w[k][3] = v.w;
+            } else {
+                const uint2 v =
+                    *reinterpret_cast<const uint2 *>(at + chunk_at<D>(t, r >> 1) + 8 * (r & 1));
+                w[k][0] = v.x; w[k][1] = v.y;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+#pragma unroll
+            for (int pr = 0; pr < 2; ++pr) {          // dimensions 4i + 2 pr, 4i + 2 pr + 1
+                const uint32_t sel = pr ? 0x7362 : 0x5140;
+                const uint32_t p01 = __byte_perm(w[0][i], w[1][i], sel);
+                const uint32_t p89 = __byte_perm(w[2][i], w[3][i], sel);
+                const uint32_t a[4] = {codes_lo(p01), codes_hi(p01), codes_lo(p89), codes_hi(p89)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float c[4];
+                    mma_from(c, a, hi[nt], v_off[nt]);
+                    if constexpr (!BF16) H::mma(c, a, lo[nt][0], lo[nt][1]);
+                    float *o = st.o[nt][2 * i + pr];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] = fmaf(v_scale[b], c[e], o[e]);
+                }
             }
         }
     }
 }
 
-// --------------------------------------------------------------------- the kernel
+// ------------------------------------------------------------------- query rows
+// `rows`: the G rows of the kv head, global or shared memory.
 template <int D, bool BF16, bool B8, int NT>
-__global__ void __launch_bounds__(kThreads, Shape<D, B8, NT>::kMinBlocks)
+__device__ __forceinline__ void load_queries(Queries<D, NT> &qs, const typename Elem<BF16>::T *rows,
+                                             int G, float scale_log2, int lane)
+{
+    using E = Elem<BF16>;
+    const int r = lane >> 2, q4 = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int h = 8 * nt + r;
+        qs.scale[nt][0] = qs.scale[nt][1] = scale_log2;
+        if constexpr (!B8) {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(rows + h * D);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                qs.b[nt][kk][0] = h < G ? w[8 * kk + q4] : 0u;
+                qs.b[nt][kk][1] = h < G ? w[8 * kk + 4 + q4] : 0u;
+            }
+        } else {
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {
+                const uint4 *w = reinterpret_cast<const uint4 *>(rows + h * D + 16 * (q4 + 4 * half));
+                const uint4 a = h < G ? w[0] : make_uint4(0u, 0u, 0u, 0u);
+                const uint4 b = h < G ? w[1] : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) qs.b[nt][4 * half + (i >> 1)][i & 1] = u[i];
+            }
+            if constexpr (BF16) {
+                // bf16 row -> fp16: times the power of two that puts its largest
+                // magnitude into [2^14, 2^15); every value within 2^28 of it
+                // converts exactly.  The inverse goes into the row's scale.
+                float amax = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 f = E::unpack(qs.b[nt][kk][e]);
+                        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+                const int ex = max(-112, ((__float_as_int(amax) >> 23) & 0xff) - 127 - 14);
+                const float down = __int_as_float((127 - ex) << 23);
+                const float up = __int_as_float((127 + ex) << 23);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 f = E::unpack(qs.b[nt][kk][e]);
+                        qs.b[nt][kk][e] = Elem<false>::pack(f.x * down, f.y * down);
+                    }
+                qs.scale[nt][0] *= __shfl_sync(kFull, up, 8 * q4);
+                qs.scale[nt][1] *= __shfl_sync(kFull, up, 8 * q4 + 4);
+            }
+            const uint32_t neg[4] = {kNegOffset, kNegOffset, kNegOffset, kNegOffset};
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                Elem<false>::mma(c, neg, qs.b[nt][kk][0], qs.b[nt][kk][1]);
+            qs.off[nt][0] = c[0];
+            qs.off[nt][1] = c[1];
+        }
+    }
+}
+
+// The sequence of place k when they are ordered by their visible blocks, longest
+// first, in 32 classes (index order inside a class).  A grid of several waves
+// then ends with its shortest pairs.  Every thread of the CTA calls it.
+template <int THREADS>
+__device__ __forceinline__ int longest_first(const Params &p, int k)
+{
+    __shared__ int count[32], found;
+    __shared__ int warp_hits[THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto class_of = [&](int s) {
+        const int L = __ldg(p.context_lens + s);
+        const int n = L < 0 || (int64_t)L > (int64_t)p.max_blocks_per_seq * kBlock
+                          ? 0
+                          : visible(L, p.window, p.sinks).n;
+        return 31 - (int)((int64_t)n * 31 / p.most);
+    };
+    if (tid < 32) count[tid] = 0;
+    if (tid == 0) found = 0;
+    __syncthreads();
+    for (int s = tid; s < p.num_seqs; s += THREADS) atomicAdd(&count[class_of(s)], 1);
+    __syncthreads();
+    // every warp for itself: the class that holds place k, and the place inside it
+    const int c = count[lane];
+    int inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += y;
+    }
+    const int cls = __ffs(__ballot_sync(kFull, inc > k)) - 1;
+    int left = k - __shfl_sync(kFull, inc - c, cls);
+    for (int s0 = 0; s0 < p.num_seqs; s0 += THREADS) {
+        const int s = s0 + tid;
+        const bool hit = s < p.num_seqs && class_of(s) == cls;
+        const unsigned hits = __ballot_sync(kFull, hit);
+        __syncthreads();
+        if (lane == 0) warp_hits[warp] = __popc(hits);
+        __syncthreads();
+        int before = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp) before += warp_hits[w];
+            all += warp_hits[w];
+        }
+        if (hit && before + __popc(hits & ((1u << lane) - 1u)) == left) found = s;
+        left -= all;
+        if (left < 0) break;             // the same for the CTA
+    }
+    __syncthreads();
+    return found;
+}
+
+// ------------------------------------------------------------ one cluster per pair
+template <int D, bool BF16, bool B8, int NT, int W>
+__global__ void __launch_bounds__(32 * W, Shape<D, B8, NT, W>::kMinBlocks)
     window_decode_kernel(const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const Params p)
 {
-    using SH = Shape<D, B8, NT>;
+    using SH = Shape<D, B8, NT, W>;
+    constexpr int kWarps = W, kThreads = 32 * W;
     using E = Elem<BF16>;
     using T = typename E::T;
     extern __shared__ uint8_t smem_raw[];
@@ -420,7 +659,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, B8, NT>::kMinBlocks)
     const int C = p.ctas;
     const int64_t pair = blockIdx.x / C;
     const int rank = (int)(blockIdx.x - pair * C);
-    const int s = (int)(pair / p.num_kv_heads), g = (int)(pair - (int64_t)s * p.num_kv_heads);
+    int s = (int)(pair / p.num_kv_heads);
+    const int g = (int)(pair - (int64_t)s * p.num_kv_heads);
+    if (p.most > 0) s = longest_first<32 * W>(p, s);
     const int G = p.group;
     int L = __ldg(p.context_lens + s);
     if (L < 0 || (int64_t)L > (int64_t)p.max_blocks_per_seq * kBlock) {
@@ -434,6 +675,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, B8, NT>::kMinBlocks)
     auto load_ids = [&](int i0) {
         const int i = i0 + lane;
         return i < count ? __ldg(row + vis.block(gw + i * stride)) : 0;
+    };
+    // bit l: the warp's block i0 + l holds hidden tokens
+    auto edges_from = [&](int i0) {
+        return __ballot_sync(kFull, vis.partial(vis.block(gw + (i0 + lane) * stride)));
     };
     int ids = load_ids(0), ids_next = load_ids(32);
     uint32_t bad = 0;
@@ -470,99 +715,73 @@ __global__ void __launch_bounds__(kThreads, Shape<D, B8, NT>::kMinBlocks)
     };
     for (int i = 0; i < SH::kStages; ++i) issue(i);
 
-    // query rows as B operands: head r of tile nt
-    uint32_t qb[NT][D / 16][2];
-    float scale_row[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int h = 8 * nt + r;
-        const T *qr = static_cast<const T *>(p.q) + ((int64_t)s * p.num_q_heads + (int64_t)g * G + h) * D;
-        scale_row[nt][0] = scale_row[nt][1] = p.scale_log2;
-        if constexpr (!B8) {
-            const uint32_t *w = reinterpret_cast<const uint32_t *>(qr);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                qb[nt][kk][0] = h < G ? __ldg(w + 8 * kk + q4) : 0u;
-                qb[nt][kk][1] = h < G ? __ldg(w + 8 * kk + 4 + q4) : 0u;
-            }
-        } else {
-#pragma unroll
-            for (int half = 0; half < D / 64; ++half) {
-                const uint4 *w = reinterpret_cast<const uint4 *>(qr + 16 * (q4 + 4 * half));
-                const uint4 a = h < G ? __ldg(w) : make_uint4(0u, 0u, 0u, 0u);
-                const uint4 b = h < G ? __ldg(w + 1) : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) qb[nt][4 * half + (i >> 1)][i & 1] = u[i];
-            }
-            if constexpr (BF16) {
-                // bf16 row -> fp16: times the power of two that puts its largest
-                // magnitude into [2^14, 2^15); every value within 2^28 of it
-                // converts exactly.  The inverse goes into the row's scale.
-                float amax = 0.f;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float2 f = E::unpack(qb[nt][kk][e]);
-                        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-                    }
-                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-                const int ex = max(-112, ((__float_as_int(amax) >> 23) & 0xff) - 127 - 14);
-                const float down = __int_as_float((127 - ex) << 23);
-                const float up = __int_as_float((127 + ex) << 23);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float2 f = E::unpack(qb[nt][kk][e]);
-                        qb[nt][kk][e] = Elem<false>::pack(f.x * down, f.y * down);
-                    }
-                scale_row[nt][0] *= __shfl_sync(kFull, up, 8 * q4);
-                scale_row[nt][1] *= __shfl_sync(kFull, up, 8 * q4 + 4);
-            }
-        }
-    }
-
+    Queries<D, NT> qs;
+    load_queries<D, BF16, B8, NT>(qs, static_cast<const T *>(p.q) +
+                                          ((int64_t)s * p.num_q_heads + (int64_t)g * G) * D,
+                                  G, p.scale_log2, lane);
     State<D, NT> st;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        st.m[nt][0] = st.m[nt][1] = -INFINITY;
-        st.l[nt][0] = st.l[nt][1] = 0.f;
-#pragma unroll
-        for (int t = 0; t < D / 16; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) st.o[nt][t][e] = 0.f;
-    }
-    for (int i = 0; i < count; ++i) {
-        const int slot = i % SH::kStages;
-        const bool landed = mbar_wait(smem_addr(&full[slot]), (uint32_t)(i / SH::kStages) & 1u,
-                                      abort_flag, p.status);
-        if (!__all_sync(kFull, landed)) {
-            // let the copies still in flight land, then give up
-            if (lane == 0) {
-                for (int k = i; k < min(i + SH::kStages, count); ++k) {
-                    const unsigned long long t0 = globaltimer();
-                    while (!mbar_try_wait(smem_addr(&full[k % SH::kStages]),
-                                          (uint32_t)(k / SH::kStages) & 1u))
-                        if (globaltimer() - t0 > kTimeoutNs) break;
-                }
+    reset(st);
+    // wait for the warp's i-th block; false (for the whole warp) when it gave up
+    auto wait_block = [&](int i) {
+        const bool landed = mbar_wait(smem_addr(&full[i % SH::kStages]),
+                                      (uint32_t)(i / SH::kStages) & 1u, abort_flag, p.status);
+        if (__all_sync(kFull, landed)) return true;
+        // let the copies still in flight land first
+        if (lane == 0) {
+            for (int k = i; k < min(i + SH::kStages, count); ++k) {
+                const unsigned long long t0 = globaltimer();
+                while (!mbar_try_wait(smem_addr(&full[k % SH::kStages]),
+                                      (uint32_t)(k / SH::kStages) & 1u))
+                    if (globaltimer() - t0 > kTimeoutNs) break;
             }
-            __syncwarp();
-            bad = 1u;
-            break;
         }
-        if (!bad) {
-            const uint32_t mask = vis.mask(vis.block(gw + i * stride));
-            uint8_t *stage = ring + slot * SH::kStageBytes;
-            if constexpr (B8) consume_b8<D, BF16, NT>(stage, qb, scale_row, st, mask, lane);
-            else consume_16bit<D, BF16, NT>(smem_addr(stage), qb, st, mask, p.scale_log2, lane);
-        }
-        // the stage's next contents come through the async proxy: order this
-        // warp's reads of it first
+        __syncwarp();
+        bad = 1u;
+        return false;
+    };
+    auto stage_of = [&](int i) { return ring + (i % SH::kStages) * SH::kStageBytes; };
+    uint32_t edges = 0;
+    auto mask_of = [&](int i) {
+        return (edges >> (i & 31)) & 1u ? vis.mask(vis.block(gw + i * stride)) : 0xffffu;
+    };
+    // the stages' next contents come through the async proxy: order this warp's
+    // reads of them first
+    auto released = [&]() {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
+    };
+    int i = 0;
+    bool alive = true;
+    if constexpr (B8 && NT == 1) {       // two blocks at a time (two head tiles: slower, 111 against
+                                         // 105 us on 200 pairs of 16 fp16 heads)
+        for (; i + 1 < count; i += 2) {
+            if ((i & 31) == 0) edges = edges_from(i);
+            alive = wait_block(i) && wait_block(i + 1);
+            if (!alive) break;
+            if (!bad) {
+                const uint8_t *const recs[2] = {stage_of(i), stage_of(i + 1)};
+                const uint32_t masks[2] = {mask_of(i), mask_of(i + 1)};
+                consume_b8<D, BF16, NT, 2>(recs, qs, st, masks, lane);
+            }
+            released();
+            issue(i + SH::kStages);
+            issue(i + 1 + SH::kStages);
+        }
+    }
+    for (; alive && i < count; ++i) {
+        if ((i & 31) == 0) edges = edges_from(i);
+        if (!wait_block(i)) break;
+        if (!bad) {
+            if constexpr (B8) {
+                const uint8_t *const recs[1] = {stage_of(i)};
+                const uint32_t masks[1] = {mask_of(i)};
+                consume_b8<D, BF16, NT, 1>(recs, qs, st, masks, lane);
+            } else {
+                consume_16bit<D, BF16, NT>(smem_addr(stage_of(i)), qs, st, mask_of(i), p.scale_log2,
+                                           lane);
+            }
+        }
+        released();
         issue(i + SH::kStages);
     }
 
@@ -660,42 +879,82 @@ __global__ void __launch_bounds__(kThreads, Shape<D, B8, NT>::kMinBlocks)
 // --------------------------------------------------------------------- host side
 struct Variant {
     KernelFn fn;
-    int smem;
+    int smem, warps;
+    int which;                 // index into the per-device cache
 };
 
-template <int D, bool B8>
+template <int D, bool B8, int W>
 static Variant variant(bool bf16, bool wide)
 {
+    const int which = (D == 128) | B8 << 1 | bf16 << 2 | wide << 3 | (W > 4) << 4;
     if (wide)
-        return bf16 ? Variant{&window_decode_kernel<D, true, B8, 2>, Shape<D, B8, 2>::kTotal}
-                    : Variant{&window_decode_kernel<D, false, B8, 2>, Shape<D, B8, 2>::kTotal};
-    return bf16 ? Variant{&window_decode_kernel<D, true, B8, 1>, Shape<D, B8, 1>::kTotal}
-                : Variant{&window_decode_kernel<D, false, B8, 1>, Shape<D, B8, 1>::kTotal};
+        return bf16 ? Variant{&window_decode_kernel<D, true, B8, 2, W>, Shape<D, B8, 2, W>::kTotal, W, which}
+                    : Variant{&window_decode_kernel<D, false, B8, 2, W>, Shape<D, B8, 2, W>::kTotal, W, which};
+    return bf16 ? Variant{&window_decode_kernel<D, true, B8, 1, W>, Shape<D, B8, 1, W>::kTotal, W, which}
+                : Variant{&window_decode_kernel<D, false, B8, 1, W>, Shape<D, B8, 1, W>::kTotal, W, which};
 }
 
-// CTAs of a variant that fit on the current device at once, cached per device.
-static int resident_ctas(int which, const Variant &v)
+template <bool B8, int W>
+static Variant variant(int D, bool bf16, bool wide)
 {
-    constexpr int kMaxDev = 64, kVariants = 16;
+    return D == 128 ? variant<128, B8, W>(bf16, wide) : variant<64, B8, W>(bf16, wide);
+}
+
+// What a variant can have on the current device, measured once per device.
+constexpr int kMaxCluster = 16;
+struct Limits {
+    int sms, resident;                   // SMs; CTAs of the variant that fit at once
+    int clusters[kMaxCluster + 1];       // clusters of c CTAs that fit at once (CTAs of 8 warps and more)
+};
+
+static bool limits(const Variant &v, Limits *out)
+{
+    constexpr int kMaxDev = 64, kVariants = 32;
     static std::mutex mu;
-    static int cache[kMaxDev][kVariants];
+    static Limits cache[kMaxDev][kVariants];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return false;
     std::lock_guard<std::mutex> lock(mu);
-    int &n = cache[dev][which];
-    if (n == 0) {
+    Limits &l = cache[dev][v.which];
+    if (l.resident == 0) {
         int sms = 0, per_sm = 0;
         const void *fn = reinterpret_cast<const void *>(v.fn);
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
             cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) !=
                 cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, v.smem) !=
+            cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, 32 * v.warps, v.smem) !=
                 cudaSuccess ||
             per_sm < 1)
-            return -1;
-        n = sms * per_sm;
+            return false;
+        for (int c = 1; c <= kMaxCluster && v.warps > 4; ++c) {
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = (unsigned)c;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)(c * sms));
+            cfg.blockDim = dim3(32u * (unsigned)v.warps);
+            cfg.dynamicSmemBytes = (size_t)v.smem;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess) l.clusters[c] = n;
+            else (void)cudaGetLastError();           // a size that cannot be scheduled: 0
+        }
+        l.sms = sms;
+        l.resident = sms * per_sm;
     }
-    return n;
+    *out = l;
+    return true;
+}
+
+// The most blocks a sequence can show (its length is known on the device only).
+static int64_t most_blocks(int32_t maxb, int32_t window, int32_t sinks)
+{
+    return std::min<int64_t>(
+        maxb, ((int64_t)window + 2 * kBlock - 2) / kBlock + ((int64_t)sinks + kBlock - 1) / kBlock);
 }
 
 static int launch(const pkv_pool *pool, bool want_b8, void *out, const void *q, const void *k_pool,
@@ -723,12 +982,36 @@ static int launch(const pkv_pool *pool, bool want_b8, void *out, const void *q, 
         ((uintptr_t)block_tables & 3u) || ((uintptr_t)context_lens & 3u) || ((uintptr_t)d_status & 3u))
         return PKV_ERR_INVALID_ARG;
     const bool bf = g.dtype == PKV_BF16 || g.dtype == PKV_B8_BF16, wide = G > 8;
-    const Variant v = g.head_dim == 128
-                          ? (want_b8 ? variant<128, true>(bf, wide) : variant<128, false>(bf, wide))
-                          : (want_b8 ? variant<64, true>(bf, wide) : variant<64, false>(bf, wide));
-    const int resident = resident_ctas((g.head_dim == 128) | want_b8 << 1 | bf << 2 | wide << 3, v);
-    if (resident < 1) return PKV_ERR_CUDA;
-
+    const int64_t pairs = (int64_t)num_seqs * g.num_kv_heads;
+    const int64_t most = most_blocks(maxb, window, sinks);
+    // Cluster size.  A cluster costs more to place the larger it is (a few
+    // microseconds per wave of eights), so a pair is split only
+    //  * while every CTA fits on the GPU at once and its warps have two blocks
+    //    each: 32 pairs of 1,000 tokens 12.8 us split by 4 to 8, 16.9 unsplit;
+    //    128 pairs 23 us split past one wave, 16.9 unsplit;
+    //  * or, where a pair may show long runs of blocks, into about one and a half
+    //    waves, for the GPU to stay busy to the end: 384 ragged pairs of up to
+    //    6,000 tokens 57.9 us split by 2, 74.2 unsplit; 512 pairs of 4,000
+    //    tokens 107 against 121; 1,280 pairs of up to 16,384 414 us unsplit,
+    //    422 split by 2.
+    // (All with 7 us of event and graph overhead, 8-bit pools, 128 dimensions.)
+    Variant v = want_b8 ? variant<true, 4>(g.head_dim, bf, wide) : variant<false, 4>(g.head_dim, bf, wide);
+    Limits lim;
+    if (!limits(v, &lim)) return PKV_ERR_CUDA;
+    int C = 1;
+    while (C < 8 && pairs * (C + 1) <= lim.resident && most >= 8 * (C + 1)) ++C;
+    if (most >= 96 * C)
+        while (C < 8 && 2 * pairs * C < 3 * lim.resident && most >= 48 * (C + 1)) ++C;
+    if (pairs * 8 <= lim.sms && most >= 256) {
+        // few long pairs: CTAs that take an SM each, in the largest clusters of
+        // which every pair gets one at once (8 pairs of 60,000 tokens: 33 us
+        // with 12 CTAs of 12 warps, 68 with 8 CTAs of four)
+        v = want_b8 ? variant<true, 12>(g.head_dim, bf, wide) : variant<false, 8>(g.head_dim, bf, wide);
+        if (!limits(v, &lim)) return PKV_ERR_CUDA;
+        C = 1;
+        for (int c = 2; c <= kMaxCluster; ++c)
+            if (lim.clusters[c] >= pairs && most >= 2 * v.warps * c) C = c;
+    }
     CUtensorMap tk = {}, tv = {};
     if (!want_b8 && (!decode::make_pool_map(&tk, k_pool, g) || !decode::make_pool_map(&tv, v_pool, g)))
         return PKV_ERR_CUDA;
@@ -748,16 +1031,11 @@ static int launch(const pkv_pool *pool, bool want_b8, void *out, const void *q, 
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = d_status;
 
-    // Cluster size: the most blocks a sequence can show is known here (its
-    // length is not).  Split a pair while the grid leaves SMs idle, and while a
-    // CTA would walk a long run of blocks by itself (the last pairs of a ragged
-    // batch then finish together); always leave each warp two blocks.
-    const int64_t pairs = (int64_t)num_seqs * g.num_kv_heads;
-    const int64_t most = std::min<int64_t>(
-        maxb, ((int64_t)window + 2 * kBlock - 2) / kBlock + ((int64_t)sinks + kBlock - 1) / kBlock);
-    int C = 1;
-    while (C < 8 && most > 2 * kWarps * C && (pairs * C < resident || most > 256 * C)) C *= 2;
+    p.num_seqs = num_seqs;
     p.ctas = C;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // more than one wave, lengths not levelled by a window: longest pairs first
+    p.most = pairs * C > lim.resident && most == maxb && most >= 64 ? (int)most : 0;
     if (pairs * C > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -765,9 +1043,9 @@ static int launch(const pkv_pool *pool, bool want_b8, void *out, const void *q, 
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pairs * C));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(32u * (unsigned)v.warps);
     cfg.dynamicSmemBytes = (size_t)v.smem;
-    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = C > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, v.fn, tk, tv, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;

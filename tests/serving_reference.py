@@ -17,9 +17,12 @@ def visible(L, q_pos, window, sinks):
     return [j for j in range(L) if j <= q_pos and (j > q_pos - window or j < sinks)]
 
 
-def attention(q, k, v, scale, dtype, weight_error):
+def attention(q, k, v, scale, dtype, weight_error, k_offset=None, v_offset=None):
     """One query row against its visible keys, fp64, and the bound on a kernel's
     error.  q [D], k and v [n][D] (fp64).
+
+    k_offset, v_offset [n]: what the kernel adds to every |k| and |v| of a token
+    inside its products and takes off again (8-bit pools: 1152 scales).
 
     The output is sum p v / sum p.  A weight's relative error is at most
     `weight_error` (its rounding on the way into the P V product) + 2^-20
@@ -29,14 +32,19 @@ def attention(q, k, v, scale, dtype, weight_error):
     and denominator then move by that much of sum p |v| and sum p; weights
     below fp16's normal range add 2^-25 |v| each (the largest weight is at
     least 1).  Last, one rounding to the output type."""
+    if k_offset is None:
+        k_offset = v_offset = torch.zeros(len(k), dtype=torch.float64)
     x = (k @ q) * scale
     p = torch.exp(x - x.max())
     total = p.sum()
     out = (p @ v) / total
-    score = scale * (k.abs() @ q.abs()).max().item()
+    # the offset counts twice: in the products and in the sum taken off
+    score = scale * (k.abs() @ q.abs() + 2 * k_offset * q.abs().sum()).max().item()
     rel = weight_error + 2.0 ** -20 + q.numel() * 2.0 ** -23 * score
     spread = (p @ v.abs()) / total
     tiny = 2.0 ** -25 * v.abs().sum(0) / total
+    # 16 tokens' products are added at a time
+    tiny = tiny + 16 * 2.0 ** -23 * 2 * (p @ v_offset) / total
     bound = 2 * rel * spread + tiny + HALF_STEP[dtype] * out.abs() + SUBNORMAL[dtype]
     return out, bound
 

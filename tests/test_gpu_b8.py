@@ -226,7 +226,8 @@ def run_attention(lens, hq, hkv, dim, dtype, window, sinks, seed, maxb=None, evi
         blk, off = tables[s].long()[j // 16], j % 16
         for h in range(hq):
             k, v = (x[blk, h // (hq // hkv), off] for x in kv)
-            want, bound = attention(q[s, h].double(), k, v, scale_of(dim), DT[dtype], WEIGHT[dtype])
+            offs = (1152 * torch.from_numpy(x[:, h // (hq // hkv)]).double()[blk] for x in ref.scales)
+            want, bound = attention(q[s, h].double(), k, v, scale_of(dim), DT[dtype], WEIGHT[dtype], *offs)
             assert_within(out[s, h], want, bound, f"sequence {s} ({n} tokens) head {h}")
     return out
 
@@ -269,7 +270,8 @@ def test_attention_scales_and_queries_of_any_size():
     j = torch.arange(200)
     k, v = (torch.from_numpy(ref.values(p))[tables[0].long()[j // 16], 0, j % 16] for p in range(2))
     for h in range(hq):
-        want, bound = attention(q[0, h].double(), k, v, 0.1, torch.bfloat16, F16_HALF_STEP)
+        offs = (1152 * torch.from_numpy(x[:, 0]).double()[tables[0].long()[j // 16]] for x in ref.scales)
+        want, bound = attention(q[0, h].double(), k, v, 0.1, torch.bfloat16, F16_HALF_STEP, *offs)
         assert_within(out[0, h], want, bound, f"head {h}")
 
 
