@@ -224,7 +224,7 @@ class KVPool:
                                    self.dtype_code, _np_ptr(order) if order is not None else None,
                                    ctypes.byref(h)), "kv_pool_create")
         self._h = h
-        self.k_pool = self.v_pool = self.kv = None
+        self.k_pool = self.v_pool = self.kv = self._rows = None
         if device is not None:
             import torch
             if self.record_bytes:
@@ -543,8 +543,11 @@ class CapturedDecode:
     will do): one untimed call on a side stream sets the kernels up first."""
 
     def __init__(self, pool: KVPool, q, block_tables, context_lens, scale: float, workspace,
-                 status, out, planned_prefix_items: int | None = None):
-        """``planned_prefix_items`` not None: capture the planned call
+                 status, out, planned_prefix_items: int | None = None,
+                 window: int | None = None, sinks: int = 0):
+        """``window``/``sinks``: capture the windowed call (16-bit and block-scaled
+        pools; ``workspace`` is then not used and may be None, as for every
+        block-scaled pool).  ``planned_prefix_items`` not None: capture the planned call
         (``paged_decode_attention_planned``, 16-bit pools): every replay then
         expects the workspace to begin with a host plan with that many
         shared-prefix items (the capture itself needs a valid plan there)."""
@@ -552,7 +555,13 @@ class CapturedDecode:
         self.torch = torch
 
         def call():
-            if pool.is_q8:
+            if pool.is_b8:
+                paged_decode_attention_b8(pool, q, block_tables, context_lens, scale, status,
+                                          window=window, sinks=sinks, out=out)
+            elif window is not None:
+                paged_decode_attention_window(pool, q, block_tables, context_lens, scale, window,
+                                              sinks, status, out=out)
+            elif pool.is_q8:
                 paged_decode_attention_q8(pool, q, block_tables, context_lens, scale, workspace,
                                           status, out=out)
             elif planned_prefix_items is not None:
@@ -687,9 +696,9 @@ def paged_decode_attention_q8(pool: KVPool, q, block_tables, context_lens, scale
 
 # --------------------------------------- rotated append, 8-bit blocks, windows
 # The calls below are also made for a few rows at a time, where the host side is
-# most of their time: each tensor is checked by one expression over its fields
-# (the message is worked out only when it fails), addresses go to the library as
-# plain integers, and torch is looked up once.
+# most of their time: the frequent ones check every tensor in one expression (when
+# it fails, the same checks run one by one for the message), addresses go to the
+# library as plain integers, and torch is looked up once.
 _torch = None
 
 
@@ -768,9 +777,12 @@ def _want_pools(pool: KVPool, index: int, k_pool=None, v_pool=None, kv=None):
 
 
 def _row_dtype(pool: KVPool):
-    torch = _torch or _load_torch()
-    return _torch_dtype(pool.dtype_code) if pool.is_q8 else (
-        torch.bfloat16 if pool.dtype_code in (PKV_BF16, PKV_B8_BF16) else torch.float16)
+    """Element type of the pool's rows (looked up once per pool)."""
+    dt = pool._rows
+    if dt is None:
+        _load_torch()
+        dt = pool._rows = _torch_dtype(pool.dtype_code)
+    return dt
 
 
 def _launch(name: str, index: int, stream, *args) -> None:
@@ -819,8 +831,9 @@ def cache_write_rope(pool: KVPool, k_new, v_new, positions, cos_sin, slot_mappin
     (default: a new tensor; ``q`` itself: in place), which is returned.  Rows of
     skipped tokens in ``q_out`` are left as they were.  ``interleaved``: pairs of
     neighbouring dimensions instead of the halves' (i, i + rotary_dim / 2)."""
-    torch = _torch or _load_torch()
-    dev, dt, D, Hkv = k_new.get_device(), _row_dtype(pool), pool.head_dim, pool.num_kv_heads
+    dt = pool._rows or _row_dtype(pool)
+    torch = _torch
+    dev, D, Hkv = k_new.get_device(), pool.head_dim, pool.num_kv_heads
     T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
     slots = _want("slot_mapping", slot_mapping, (T,), torch.int64, dev)
     k, ks = _want_rows("k_new", k_new, (T, Hkv, D), dt, dev)
@@ -838,7 +851,7 @@ def cache_write_rope(pool: KVPool, k_new, v_new, positions, cos_sin, slot_mappin
         if q_out is None:
             q_out = torch.empty((T, hq, D), dtype=dt, device=q.device)
         qp, qs = _want_rows("q", q, (T, hq, D), dt, dev)
-        qo, qos = _want_rows("q_out", q_out, (T, hq, D), dt, dev)
+        qo, qos = (qp, qs) if q_out is q else _want_rows("q_out", q_out, (T, hq, D), dt, dev)
         if qp == qo and qs != qos:
             raise ValueError("q_out over q needs the same token stride")
     elif q_out is not None:
@@ -892,26 +905,38 @@ def dequantize_blocks(pool: KVPool, ids, k_out, v_out, status, kv=None, stream=N
 def _decode_call(name: str, pool: KVPool, q, out, block_tables, context_lens, scale, window, sinks,
                  status, k_pool, v_pool, kv, stream):
     """Checks and launch of the windowed decode calls."""
-    torch = _torch or _load_torch()
-    dev, dt, D = q.get_device(), _row_dtype(pool), pool.head_dim
-    if q.dim() != 3 or q.shape[2] != D:
-        raise ValueError(f"q must be [n][h][{D}], got {list(q.shape)}")
-    S, hq, _ = shape = tuple(q.shape)
+    dt = pool._rows or _row_dtype(pool)
+    torch = _torch
+    dev, D, i32 = q.get_device(), pool.head_dim, torch.int32
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D:
+        raise ValueError(f"q must be [n][h][{D}], got {list(shape)}")
+    S, hq, _ = shape
     if hq % pool.num_kv_heads:
         raise ValueError(f"q has {hq} heads, not a multiple of the pool's "
                          f"{pool.num_kv_heads} kv heads")
-    qp = _want("q", q, shape, dt, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=q.device)
-    op = _want("out", out, shape, dt, dev)
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables must have 2 dimensions")
-    maxb = block_tables.shape[1]
-    tp = _want("block_tables", block_tables, (S, maxb), torch.int32, dev)
-    lp = _want("context_lens", context_lens, (S,), torch.int32, dev)
-    kp, vp = _want_pools(pool, dev, k_pool, v_pool, kv)
-    pools = (kp,) if pool.is_b8 else (kp, vp)
-    _launch(name, dev, stream, pool.handle, op, qp, *pools, tp, maxb, lp, S, hq, scale,
+        out = torch.empty_like(q)
+    if not (q.dtype is dt and q.is_contiguous()
+            and out.dtype is dt and out.shape == shape and out.get_device() == dev
+            and out.is_contiguous()
+            and block_tables.dtype is i32 and block_tables.dim() == 2
+            and block_tables.get_device() == dev and block_tables.is_contiguous()
+            and context_lens.dtype is i32 and context_lens.shape == (S,)
+            and context_lens.get_device() == dev and context_lens.is_contiguous()
+            and len(block_tables) == S):
+        shape = tuple(shape)
+        _want("q", q, shape, dt, dev)
+        _want("out", out, shape, dt, dev)
+        if block_tables.dim() != 2:
+            raise ValueError("block_tables must have 2 dimensions")
+        _want("block_tables", block_tables, (S, block_tables.shape[1]), i32, dev)
+        _want("context_lens", context_lens, (S,), i32, dev)
+    pools = _want_pools(pool, dev, k_pool, v_pool, kv)
+    if pool.is_b8:
+        pools = pools[:1]
+    _launch(name, dev, stream, pool.handle, out.data_ptr(), q.data_ptr(), *pools,
+            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), S, hq, scale,
             window, sinks, _want_status(status, dev))
     return out
 

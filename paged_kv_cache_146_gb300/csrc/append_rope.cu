@@ -40,8 +40,8 @@ struct Params {
     uint4 *k_pool, *v_pool;              // 16-bit pools
     uint8_t *kv;                         // 8-bit records
     int32_t *status;
-    int32_t span;                        // 8-bit write: tokens per warp (1 or 16)
-    int32_t write_blocks;                // 8-bit write: CTAs that write; the rest rotate queries
+    int32_t write_blocks;                // 8-bit write of few tokens: CTAs that write; the rest
+                                         // rotate queries
 };
 
 // A lane works on two 8-value chunks of a row.  Chunk pair i of the row: for
@@ -87,8 +87,9 @@ __device__ __forceinline__ void turn(float &a, float &b, float c, float s)
     b = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
 }
 
-// Rotate the 16 values of chunk pair i in place; cs = the position's table row.
-template <bool NEIGHBOURS>
+// Rotate the 16 values of chunk pair i in place; cs = the position's table row,
+// in global or (SHARED) shared memory.
+template <bool NEIGHBOURS, bool SHARED = false>
 __device__ __forceinline__ void rotate16(float (&x)[16], int i, int half, const float *cs)
 {
     // halves: values e and 8 + e are angle 8i + e; neighbours: values 2e and
@@ -96,7 +97,8 @@ __device__ __forceinline__ void rotate16(float (&x)[16], int i, int half, const 
     // entries 8i .. 8i + 7
     const float4 *c4 = reinterpret_cast<const float4 *>(cs + 8 * i);
     const float4 *s4 = reinterpret_cast<const float4 *>(cs + half + 8 * i);
-    const float4 ca = __ldg(c4), cb = __ldg(c4 + 1), sa = __ldg(s4), sb = __ldg(s4 + 1);
+    const float4 ca = SHARED ? c4[0] : __ldg(c4), cb = SHARED ? c4[1] : __ldg(c4 + 1);
+    const float4 sa = SHARED ? s4[0] : __ldg(s4), sb = SHARED ? s4[1] : __ldg(s4 + 1);
     const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
     const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
 #pragma unroll
@@ -221,18 +223,29 @@ __device__ __forceinline__ uint32_t round_bits(float x)
     return __float_as_uint(__fadd_rn(x, 12582912.0f));
 }
 
-// Four codes (clamped to [-127, 127]; NaN -> 0) of x * inv as stored bytes (code + 128).
+// Four codes of x * inv as stored bytes (code + 128).  ODD: the block holds an
+// infinity or a NaN, so codes are clamped to [-127, 127] and NaN gives 0; all
+// other values are at most 127 (1 + 2^-22) in size and round inside the range.
+template <bool ODD>
 __device__ __forceinline__ uint32_t b8_codes4(const float *x, float inv)
 {
     uint32_t b[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         float y = __fmul_rn(x[k], inv);
-        y = y == y ? y : 0.f;
-        b[k] = round_bits(fminf(fmaxf(y, -127.f), 127.f));
+        if (ODD) y = y == y ? fminf(fmaxf(y, -127.f), 127.f) : 0.f;
+        b[k] = round_bits(y);
     }
     return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410) ^
            0x80808080u;
+}
+
+// The larger of a and |x|; NaN if either is.
+__device__ __forceinline__ float max_abs_nan(float a, float x)
+{
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(fabsf(x)));
+    return m;
 }
 
 // Four stored bytes rounded to a larger scale (ratio = old / new <= 1).
@@ -256,13 +269,17 @@ __device__ __forceinline__ uint32_t b8_rescale4(uint32_t w, float ratio)
 // it: rn(code * rn(old / new)).
 // A row is D / 16 lanes of 16 values.  The rows of the run stay in registers,
 // packed, between the maximum and the codes, so each value is read once; K is
-// rotated for both (keeping the fp32 values instead took 154 registers, which
-// left too few warps to fill the memory pipe: 176 us against TIME on 16,700
-// tokens of 8 heads).
-template <bool BF16, bool NEIGHBOURS, int D>
+// rotated for both.  (Keeping the fp32 values took 154 registers and left too few
+// warps to fill the memory pipe: with the queries in the same launch, 20,500
+// tokens of 32 query and 8 kv heads took 176 us, against 59 + 49 us now; capping
+// this kernel's registers at 80 spilled, 69 us instead of 49.)
+template <bool BF16, bool NEIGHBOURS, int D, bool SHARED>
 __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, int64_t t0, int n,
-                                             int64_t block, int off0, int lane)
+                                             int64_t block, int off0, int lane,
+                                             const int *positions, const float *cos_sin, int cs_stride)
 {
+    // SHARED: positions and cos_sin hold the rows of tokens t0, t0 + 1, ... in
+    // shared memory; else they are the call's arrays
     constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPasses = 16 / kRows;
     constexpr int kRecord = PKV_B8_RECORD_BYTES(D);
     uint8_t *rec = p.kv + (block * p.num_kv_heads + h) * kRecord;
@@ -285,13 +302,15 @@ __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, i
         const uint4 *row = reinterpret_cast<const uint4 *>(rows + (t0 + (in ? j : 0)) * stride);
         w[k][0] = in ? row[cp.c0] : make_uint4(0u, 0u, 0u, 0u);
         w[k][1] = in ? row[cp.c1] : make_uint4(0u, 0u, 0u, 0u);
-        pos[k] = !in ? -1 : p.positions ? __ldg(p.positions + t0 + j) : 0;
+        pos[k] = !in ? -1 : !p.positions ? 0 : SHARED ? positions[j] : __ldg(positions + t0 + j);
     }
     auto values = [&](int k, float (&x)[16]) {
         unpack8<BF16>(w[k][0], x);
         unpack8<BF16>(w[k][1], x + 8);
         if (cp.turned)
-            rotate16<NEIGHBOURS>(x, i, p.rotary_dim >> 1, p.cos_sin + (int64_t)pos[k] * p.rotary_dim);
+            rotate16<NEIGHBOURS, SHARED>(
+                x, i, p.rotary_dim >> 1,
+                cos_sin + (SHARED ? (int64_t)(k * kRows + r) : (int64_t)pos[k]) * cs_stride);
     };
     float amax = 0.f;
 #pragma unroll
@@ -306,11 +325,26 @@ __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, i
         float x[16];
         values(k, x);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));   // ignores NaN
+        for (int e = 0; e < 16; ++e) amax = max_abs_nan(amax, x[e]);
+    }
+    constexpr float kMax = 0x1.fep127f;                       // the largest bf16
+    const bool odd = __any_sync(kFull, !(amax <= kMax));      // an infinity or a NaN
+    if (odd) {                           // once more: NaN ignored, an infinity as kMax
+        amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < kPasses; ++k) {
+            if (k * kRows >= n) break;
+            if (pos[k] < 0) continue;
+            float x[16];
+            values(k, x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
+        }
+        amax = fminf(amax, kMax);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-    amax = amax < kB8Tiny ? 0.f : fminf(amax, 0x1.fep127f);   // an infinity takes the largest bf16
+    if (amax < kB8Tiny) amax = 0.f;
     constexpr float kRcp127 = 0x1.020408p-7f;                 // rn(1 / 127)
     const float now = fmaxf(old, __fmul_rn(amax, kRcp127));
     if (off0 > 0 && now > old) {
@@ -334,17 +368,50 @@ __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, i
         const int t = off0 + k * kRows + r;
         float x[16];
         values(k, x);
-        *reinterpret_cast<uint2 *>(codes + b8_chunk(t, cp.c0 >> 1, D) + 8 * (cp.c0 & 1)) =
-            make_uint2(b8_codes4(x, inv), b8_codes4(x + 4, inv));
-        *reinterpret_cast<uint2 *>(codes + b8_chunk(t, cp.c1 >> 1, D) + 8 * (cp.c1 & 1)) =
-            make_uint2(b8_codes4(x + 8, inv), b8_codes4(x + 12, inv));
+        uint2 lo, hi;
+        if (odd) {
+            lo = make_uint2(b8_codes4<true>(x, inv), b8_codes4<true>(x + 4, inv));
+            hi = make_uint2(b8_codes4<true>(x + 8, inv), b8_codes4<true>(x + 12, inv));
+        } else {
+            lo = make_uint2(b8_codes4<false>(x, inv), b8_codes4<false>(x + 4, inv));
+            hi = make_uint2(b8_codes4<false>(x + 8, inv), b8_codes4<false>(x + 12, inv));
+        }
+        *reinterpret_cast<uint2 *>(codes + b8_chunk(t, cp.c0 >> 1, D) + 8 * (cp.c0 & 1)) = lo;
+        *reinterpret_cast<uint2 *>(codes + b8_chunk(t, cp.c1 >> 1, D) + 8 * (cp.c1 & 1)) = hi;
     }
 }
 
-// A warp takes `span` tokens (1 or 16), one kv head and K or V, and writes every
-// run that begins among its tokens.  A run is a chain of tokens whose slots
-// follow one another inside a block; lane l looks at token tb - 1 + l, so a run
-// that begins at the span's last token is seen to its end.
+// The runs that begin among `span` tokens from tb on.  A run is a chain of tokens
+// whose slots follow one another inside a block; lane l looks at token tb - 1 + l,
+// so a run that begins at the span's last token is seen to its end.
+struct Runs {
+    int64_t slot;            // of token tb - 1 + lane
+    unsigned links, leads;   // bit l: token tb - 1 + l goes on with a run, begins one
+    __device__ __forceinline__ int length(int l) const     // of the run that token l begins
+    {
+        return __ffs(l < 31 ? ~(links >> (l + 1)) : ~0u);  // 1 + the links that follow
+    }
+};
+
+__device__ __forceinline__ Runs find_runs(const Params &p, int64_t tb, int span, int lane, bool report)
+{
+    Runs r;
+    const int64_t t = tb - 1 + lane;
+    r.slot = t >= 0 && t < p.num_tokens ? __ldg(p.slots + t) : -1;
+    const int64_t prev = __shfl_up_sync(kFull, r.slot, 1);
+    const bool valid = r.slot >= 0 && r.slot < p.num_slots;
+    const unsigned mine = span == 16 ? 0x1fffeu : 0x2u;
+    if ((__ballot_sync(kFull, r.slot >= p.num_slots) & mine) && lane == 0 && report)
+        atomicOr(p.status, PKV_DEV_BAD_SLOT);
+    const bool linked =
+        lane > 0 && valid && prev >= 0 && prev + 1 == r.slot && r.slot % kBlock != 0;
+    r.links = __ballot_sync(kFull, linked);
+    r.leads = __ballot_sync(kFull, valid && !linked) & mine;
+    return r;
+}
+
+// Few tokens: a warp takes one token, one kv head and K or V, and writes the run
+// that begins there, if one does.
 template <bool BF16, bool NEIGHBOURS, int D>
 __global__ void __launch_bounds__(128, 6) append_b8_kernel(const Params p)
 {
@@ -354,75 +421,113 @@ __global__ void __launch_bounds__(128, 6) append_b8_kernel(const Params p)
         return;
     }
     const int lane = threadIdx.x & 31;
-    const int per_span = 2 * p.num_kv_heads;
-    const int64_t units = ((int64_t)p.num_tokens + p.span - 1) / p.span * per_span;
+    const int per_token = 2 * p.num_kv_heads;
+    const int64_t units = (int64_t)p.num_tokens * per_token;
     for (int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); u < units;
          u += (int64_t)p.write_blocks * 4) {
-        const int64_t w = u / per_span;
-        const int rest = (int)(u - w * per_span);
-        const int part = rest & 1, h = rest >> 1;
-        const int64_t tb = w * p.span, t = tb - 1 + lane;
-        const int64_t slot = t >= 0 && t < p.num_tokens ? __ldg(p.slots + t) : -1;
-        const int64_t prev = __shfl_up_sync(kFull, slot, 1);
-        const bool valid = slot >= 0 && slot < p.num_slots;
-        const unsigned mine = p.span == 16 ? 0x1fffeu : 0x2u;
-        if ((__ballot_sync(kFull, slot >= p.num_slots) & mine) && lane == 0)
-            atomicOr(p.status, PKV_DEV_BAD_SLOT);
-        const bool linked = lane > 0 && valid && prev >= 0 && prev + 1 == slot && slot % kBlock != 0;
-        const unsigned links = __ballot_sync(kFull, linked);
-        unsigned leads = __ballot_sync(kFull, valid && !linked) & mine;
-        while (leads) {
-            const int l = __ffs(leads) - 1;
-            leads &= leads - 1;
-            const int64_t s0 = __shfl_sync(kFull, slot, l);
-            // links of the tokens after l: the run's length
-            const unsigned after = l < 31 ? ~(links >> (l + 1)) : ~0u;
-            const int n = __ffs(after);                   // 1 + trailing ones (bit 31 - l on is 0 links)
-            b8_write_run<BF16, NEIGHBOURS, D>(p, part, h, tb - 1 + l, n, s0 / kBlock,
-                                              (int)(s0 % kBlock), lane);
+        const int64_t t = u / per_token;
+        const int rest = (int)(u - t * per_token);
+        const Runs runs = find_runs(p, t, 1, lane, rest == 0);
+        if (!runs.leads) continue;
+        const int64_t s0 = __shfl_sync(kFull, runs.slot, 1);
+        b8_write_run<BF16, NEIGHBOURS, D, false>(p, rest & 1, rest >> 1, t, runs.length(1),
+                                                 s0 / kBlock, (int)(s0 % kBlock), lane,
+                                                 p.positions, p.cos_sin, p.rotary_dim);
+    }
+}
+
+// Many tokens: a CTA takes a span of 16 and writes every run that begins there,
+// the (run, kv head, K or V) units dealt to its warps.  The table rows of the
+// tokens it may reach (31) come to shared memory once, for all heads.
+constexpr int kSpanWarps = 8;
+constexpr int kSpanTokens = 31;
+
+template <bool BF16, bool NEIGHBOURS, int D>
+__global__ void __launch_bounds__(32 * kSpanWarps, 2) append_b8_span_kernel(const Params p)
+{
+    constexpr int kStride = D + 4;                        // floats of a staged table row
+    __shared__ __align__(16) float table[kSpanTokens * kStride];
+    __shared__ int positions[kSpanTokens + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t spans = ((int64_t)p.num_tokens + 15) / 16;
+    for (int64_t w = blockIdx.x; w < spans; w += gridDim.x) {
+        const int64_t tb = w * 16;
+        const Runs runs = find_runs(p, tb, 16, lane, warp == 0);
+        if (p.positions) {
+            const int n = (int)min((int64_t)kSpanTokens, p.num_tokens - tb);
+            const int per_row = p.rotary_dim / 4;
+            for (int e = threadIdx.x; e < n * per_row; e += 32 * kSpanWarps) {
+                const int t = e / per_row, c = e - t * per_row;
+                const int pos = __ldg(p.positions + tb + t);
+                if (c == 0) positions[t] = pos;
+                if (pos >= 0 && pos < p.max_positions)
+                    *reinterpret_cast<float4 *>(table + t * kStride + 4 * c) = __ldg(
+                        reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * p.rotary_dim) + c);
+            }
+            __syncthreads();
         }
+        const int n_leads = __popc(runs.leads), units = n_leads * 2 * p.num_kv_heads;
+        for (int u = warp; u < units; u += kSpanWarps) {
+            const int rest = u / n_leads, k = u - rest * n_leads;
+            unsigned left = runs.leads;                   // the k-th run's first token
+            for (int i = 0; i < k; ++i) left &= left - 1;
+            const int l = __ffs(left) - 1;
+            const int64_t s0 = __shfl_sync(kFull, runs.slot, l);
+            b8_write_run<BF16, NEIGHBOURS, D, true>(p, rest & 1, rest >> 1, tb - 1 + l,
+                                                    runs.length(l), s0 / kBlock,
+                                                    (int)(s0 % kBlock), lane, positions + l - 1,
+                                                    table + (l - 1) * kStride, kStride);
+        }
+        __syncthreads();                                  // the table may be filled anew
     }
 }
 
 // Records of blocks ids[0 .. n) as K and V rows [n][Hkv][16][D] of the row type:
-// one thread per 16-byte code chunk (two 16-byte stores).
+// a thread takes one 16-byte code chunk of K and the same of V (four 16-byte
+// stores).
 template <bool BF16, int D>
 __global__ void __launch_bounds__(256)
     dequantize_kernel(const uint8_t *__restrict__ kv, const int32_t *__restrict__ ids, int32_t n,
                       int32_t num_kv_heads, int32_t num_blocks, uint4 *__restrict__ k_out,
                       uint4 *__restrict__ v_out, int32_t *__restrict__ status)
 {
-    constexpr int kChunks = D;                            // chunks of one part of a record
-    const int per_block = num_kv_heads * 2 * kChunks;
+    constexpr int kChunks = D;                            // chunks of K (or V) of a record
+    const uint32_t per_block = (uint32_t)num_kv_heads * kChunks;
     const int64_t total = (int64_t)n * per_block;
     for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < total;
          e += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t b = e / per_block;
+        const int64_t b = total <= UINT32_MAX ? (int64_t)((uint32_t)e / per_block) : e / per_block;
         const int within = (int)(e - b * per_block);
-        const int h = within / (2 * kChunks), c = within % (2 * kChunks);
-        const int part = c / kChunks, t = (c % kChunks) / (D / 16), j = c % (D / 16);
+        const int h = within / kChunks, c = within % kChunks;
+        const int t = c / (D / 16), j = c % (D / 16);
         const int32_t id = __ldg(ids + b);
         if (id < 0 || id >= num_blocks) {
             if (within == 0) atomicOr(status, PKV_DEV_BAD_BLOCK);
             continue;
         }
         const uint8_t *rec = kv + ((int64_t)id * num_kv_heads + h) * PKV_B8_RECORD_BYTES(D);
-        const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(rec + 16 * D * part + b8_chunk(t, j, D)));
-        const float scale = __ldg(reinterpret_cast<const float *>(rec + 32 * D) + part);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        float x[16];
+        const uint4 w[2] = {__ldcs(reinterpret_cast<const uint4 *>(rec + b8_chunk(t, j, D))),
+                            __ldcs(reinterpret_cast<const uint4 *>(rec + 16 * D + b8_chunk(t, j, D)))};
+        const float2 scales = __ldg(reinterpret_cast<const float2 *>(rec + 32 * D));
+        const int64_t at = (((b * num_kv_heads + h) * kBlock + t) * D + 16 * j) / 8;
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-            x[k] = __fmul_rn((float)((int)((u[k >> 2] >> (8 * (k & 3))) & 0xffu) - 128), scale);
-        uint4 *out = (part ? v_out : k_out) + (((b * num_kv_heads + h) * kBlock + t) * D + 16 * j) / 8;
-        out[0] = pack8<BF16>(x);
-        out[1] = pack8<BF16>(x + 8);
+        for (int part = 0; part < 2; ++part) {
+            const float scale = part ? scales.y : scales.x;
+            const uint32_t u[4] = {w[part].x, w[part].y, w[part].z, w[part].w};
+            float x[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                x[k] = __fmul_rn((float)((int)((u[k >> 2] >> (8 * (k & 3))) & 0xffu) - 128), scale);
+            uint4 *out = (part ? v_out : k_out) + at;
+            out[0] = pack8<BF16>(x);
+            out[1] = pack8<BF16>(x + 8);
+        }
     }
 }
 
-// Spans of 16 tokens per warp once that still gives every resident warp work;
-// below that one warp per token.
-constexpr int64_t kSpanUnits = 8192;
+// From this many spans of 16 tokens on, a CTA per span; below, a warp per token
+// (8 kv heads: 2,000 tokens 14 us by spans, 18 by tokens; 500 tokens 14 and 8).
+constexpr int64_t kSpans = 100;
 
 template <bool BF16, bool NEIGHBOURS>
 static int launch_rows(const Params &p, int D, int heads_kv, cudaStream_t st)
@@ -437,16 +542,21 @@ template <bool BF16, bool NEIGHBOURS>
 static int launch_b8(const Params &p0, int D, bool queries, cudaStream_t st)
 {
     Params p = p0;
-    const int64_t spans = ((int64_t)p.num_tokens + 15) / 16 * 2 * p.num_kv_heads;
-    p.span = spans >= kSpanUnits ? 16 : 1;
-    const int64_t units = p.span == 16 ? spans : (int64_t)p.num_tokens * 2 * p.num_kv_heads;
+    const int64_t spans = ((int64_t)p.num_tokens + 15) / 16;
+    if (spans >= kSpans) {
+        if (queries) {               // in a launch of their own, at full occupancy
+            const int rc = launch_rows<BF16, NEIGHBOURS>(p, D, 0, st);
+            if (rc != PKV_OK) return rc;
+        }
+        const unsigned grid = (unsigned)std::min<int64_t>(spans, 152 * 64);
+        if (D == 128) append_b8_span_kernel<BF16, NEIGHBOURS, 128><<<grid, 32 * kSpanWarps, 0, st>>>(p);
+        else append_b8_span_kernel<BF16, NEIGHBOURS, 64><<<grid, 32 * kSpanWarps, 0, st>>>(p);
+        return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    }
+    const int64_t units = (int64_t)p.num_tokens * 2 * p.num_kv_heads;
     p.write_blocks = (int32_t)std::min<int64_t>((units + 3) / 4, 152 * 64);
     int64_t grid = p.write_blocks;
-    if (queries && p.span == 16) {
-        // many tokens: the queries in a launch of their own, at full occupancy
-        const int rc = launch_rows<BF16, NEIGHBOURS>(p, D, 0, st);
-        if (rc != PKV_OK) return rc;
-    } else if (queries) {
+    if (queries) {
         const int64_t threads = (int64_t)p.num_tokens * p.num_q_heads * (D / 16);
         grid += std::min<int64_t>((threads + 255) / 256, 152 * 64);
     }
@@ -574,7 +684,7 @@ extern "C" int kv_dequantize_blocks(const pkv_pool *pool, const int32_t *ids, in
     if (!pkv::aligned16(kv_b8) || !pkv::aligned16(k_out) || !pkv::aligned16(v_out) ||
         ((uintptr_t)ids & 3u) || ((uintptr_t)d_status & 3u))
         return PKV_ERR_INVALID_ARG;
-    const int64_t total = (int64_t)n * g.num_kv_heads * 2 * g.head_dim;
+    const int64_t total = (int64_t)n * g.num_kv_heads * g.head_dim;
     const unsigned grid = (unsigned)std::min<int64_t>((total + 255) / 256, 152 * 64);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool bf = g.dtype == PKV_B8_BF16;

@@ -8,8 +8,11 @@ reads every sequence's blocks through its table.  Finished sequences release
 their blocks ("vLLM-and-PagedAttention-KR", "가장 기본적인 decoding", step 5).
 
 The pool may be 16-bit (fp16/bf16 K and V) or an 8-bit cache ("kv-cache-by-model",
-section 1: one-byte codes, one fp16 scale per 32 values); the engine picks the
-matching cache-write and attention calls.
+section 1: one-byte codes, one fp16 scale per 32 values; or one scale per block
+and head); the engine picks the matching cache-write and attention calls.  With
+``rope`` (a table from ``rope_table``) the write also rotates K and the queries by
+their positions, with ``window`` the attention reaches back that far only, and to
+the first ``sinks`` tokens (16-bit and block-scaled pools).
 
 Hand-off to the GPU: the device copies of the ledger arrays (table, lengths,
 slots) come in two sets.  Step t's arrays are copied on a copy stream into the
@@ -23,21 +26,24 @@ The attention call's work plan (partition size, work list, shared-prefix
 runs) is built on the host from the ledger's lengths and tables
 (``decode_plan``) and travels with them, into the workspace of the same device
 set, so the call starts with its main kernel (16-bit pools, automatic
-partition size; the 8-bit path and a fixed partition size plan on the device).
+partition size; the 8-bit path and a fixed partition size plan on the device; windowed and
+block-scaled calls need no plan).
 """
 from __future__ import annotations
 
 import numpy as np
 
-from . import (KVPool, cache_write, cache_write_q8, decode_plan, decode_plan_bytes,
-               decode_workspace_bytes, paged_decode_attention, paged_decode_attention_planned,
-               paged_decode_attention_q8, status_check)
+from . import (KVPool, cache_write, cache_write_b8, cache_write_q8, cache_write_rope, decode_plan,
+               decode_plan_bytes, decode_workspace_bytes, paged_decode_attention,
+               paged_decode_attention_b8, paged_decode_attention_planned,
+               paged_decode_attention_q8, paged_decode_attention_window, status_check)
 
 
 class DecodeEngine:
     def __init__(self, pool: KVPool, num_seqs: int, num_q_heads: int, max_blocks_per_seq: int,
                  scale: float, device, blocks_per_split: int | None = None,
-                 plan_on_host: bool = True):
+                 plan_on_host: bool = True, rope=None, rope_interleaved: bool = False,
+                 window: int | None = None, sinks: int = 0):
         import torch
         self.torch = torch
         self.pool = pool
@@ -47,17 +53,29 @@ class DecodeEngine:
         self.split = blocks_per_split
         if pool.is_q8 and blocks_per_split is not None:
             raise ValueError("the 8-bit path uses the default partition size")
+        if pool.is_q8 and (rope is not None or window is not None):
+            raise ValueError("rope and window take 16-bit and block-scaled 8-bit pools")
+        if window is None and sinks:
+            raise ValueError("sinks without a window")
+        self.rope, self.rope_interleaved = rope, rope_interleaved
+        self.window, self.sinks = window, sinks
+        # calls that take neither a plan nor a workspace
+        self.plain_call = pool.is_b8 or window is not None
+        if self.plain_call and blocks_per_split is not None:
+            raise ValueError("windowed and block-scaled calls choose their own split")
         pin = dict(pin_memory=True)
         self.h_tables = torch.full((num_seqs, max_blocks_per_seq), -1, dtype=torch.int32, **pin)
         self.h_lens = torch.zeros(num_seqs, dtype=torch.int32, **pin)
         self.h_slots = torch.zeros(num_seqs, dtype=torch.int64, **pin)
+        self.h_positions = torch.zeros(num_seqs, dtype=torch.int32, **pin)   # rope only
         self.tables = self.h_tables.numpy()      # ledger writes here directly
         self.lens = self.h_lens.numpy()
         # two device sets of the ledger arrays (see the module docstring)
         self._sets = [{"tables": torch.full((num_seqs, max_blocks_per_seq), -1,
                                             dtype=torch.int32, device=device),
                        "lens": torch.zeros(num_seqs, dtype=torch.int32, device=device),
-                       "slots": torch.zeros(num_seqs, dtype=torch.int64, device=device)}
+                       "slots": torch.zeros(num_seqs, dtype=torch.int64, device=device),
+                       "positions": torch.zeros(num_seqs, dtype=torch.int32, device=device)}
                       for _ in range(2)]
         self._set = 0
         self._h2d = torch.cuda.Stream(device=device)
@@ -68,11 +86,14 @@ class DecodeEngine:
         self._loaded = [torch.cuda.Event() for _ in range(2)]
         self._used = [torch.cuda.Event() for _ in range(2)]
         self._io = None                              # q/k/v/out sets of decode_step_host
-        nbytes = decode_workspace_bytes(num_seqs, num_q_heads, pool.num_kv_heads, pool.head_dim,
-                                        max_blocks_per_seq, blocks_per_split)
+        nbytes = 0
+        if not self.plain_call:
+            nbytes = decode_workspace_bytes(num_seqs, num_q_heads, pool.num_kv_heads, pool.head_dim,
+                                            max_blocks_per_seq, blocks_per_split)
         # host-planned calls: one workspace per device set (a set's plan lands
         # while the other set's kernels run) and a pinned plan buffer per set
-        self.planned = plan_on_host and not pool.is_q8 and blocks_per_split is None
+        self.planned = (plan_on_host and not pool.is_q8 and not self.plain_call
+                        and blocks_per_split is None)
         for st in self._sets[:2 if self.planned else 1]:
             st["workspace"] = torch.empty(nbytes, dtype=torch.uint8, device=device)
         if not self.planned:
@@ -85,7 +106,7 @@ class DecodeEngine:
                 st["h_plan"] = torch.zeros(pb, dtype=torch.uint8, pin_memory=True)
                 st["prefix_items"] = 0
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
-        tdt = torch.bfloat16 if pool.dtype in ("bf16", "q8_bf16") else torch.float16
+        tdt = (torch.bfloat16 if pool.dtype in ("bf16", "q8_bf16", "b8_bf16") else torch.float16)
         self.out = torch.empty((num_seqs, num_q_heads, pool.head_dim), dtype=tdt, device=device)
         self._ones = np.ones(num_seqs, dtype=np.int32)
         self._copied = None                          # event: last H2D of the pinned ledger
@@ -113,15 +134,22 @@ class DecodeEngine:
         return self._sets[self._set]["prefix_items"]
 
     # ------------------------------------------------------------------ prompt
-    def prefill(self, k_rows, v_rows, num_new) -> np.ndarray:
+    def prefill(self, k_rows, v_rows, num_new, q_rows=None) -> np.ndarray:
         """Write prompt tokens: ``num_new[s]`` rows per sequence, sequence after
-        sequence in ``k_rows``/``v_rows`` (device [sum][Hkv][D]).  Returns the slots."""
+        sequence in ``k_rows``/``v_rows`` (device [sum][Hkv][D]).  Returns the slots.
+        With ``rope``, K is rotated on the way and so are ``q_rows``, in place."""
         torch = self.torch
         self._wait_copy()
         num_new = np.ascontiguousarray(num_new, dtype=np.int32)
         slots = self.pool.append_slots(self.lens, num_new, self.tables)
         if len(slots):
-            self.write(k_rows, v_rows, torch.from_numpy(slots).to(self.device))
+            positions = None
+            if self.rope is not None:
+                positions = torch.from_numpy(np.concatenate(
+                    [np.arange(n, n + m, dtype=np.int32) for n, m in zip(self.lens, num_new)]
+                )).to(self.device)
+            self.write(k_rows, v_rows, torch.from_numpy(slots).to(self.device), q=q_rows,
+                       positions=positions)
         self.lens += num_new
         return slots
 
@@ -152,6 +180,8 @@ class DecodeEngine:
         block table, context lengths and slot mapping in the pinned buffers."""
         self._wait_copy()
         self.h_slots.numpy()[:] = self.pool.append_slots(self.lens, self._ones, self.tables)
+        if self.rope is not None:
+            self.h_positions.numpy()[:] = self.lens
         self.lens += 1
 
     def _stage(self, extra=()) -> int:
@@ -170,6 +200,8 @@ class DecodeEngine:
             dst["tables"].copy_(self.h_tables, non_blocking=True)
             dst["lens"].copy_(self.h_lens, non_blocking=True)
             dst["slots"].copy_(self.h_slots, non_blocking=True)
+            if self.rope is not None:
+                dst["positions"].copy_(self.h_positions, non_blocking=True)
             if self.planned:
                 dst["workspace"][:self.plan_bytes].copy_(dst["h_plan"], non_blocking=True)
             for d, h in extra:
@@ -187,10 +219,19 @@ class DecodeEngine:
         """The ledger step and the hand-off of its arrays to the device."""
         self._stage()
 
-    def write(self, k_new, v_new, d_slots=None) -> None:
-        """Cache write of K/V rows into their slots (this step's by default)."""
+    def write(self, k_new, v_new, d_slots=None, q=None, positions=None) -> None:
+        """Cache write of K/V rows into their slots (this step's by default).  With
+        ``rope``, K is rotated by ``positions`` (this step's by default) on the way,
+        and ``q``, if given, in place."""
         d_slots = self.d_slots if d_slots is None else d_slots
-        if self.pool.is_q8:
+        if self.rope is not None:
+            if positions is None:
+                positions = self._sets[self._set]["positions"]
+            cache_write_rope(self.pool, k_new, v_new, positions, self.rope, d_slots, self.status,
+                             q=q, q_out=q, interleaved=self.rope_interleaved)
+        elif self.pool.is_b8:
+            cache_write_b8(self.pool, k_new, v_new, d_slots, self.status)
+        elif self.pool.is_q8:
             cache_write_q8(self.pool, k_new, v_new, d_slots, self.status)
         else:
             cache_write(self.pool, k_new, v_new, d_slots, self.status)
@@ -201,7 +242,14 @@ class DecodeEngine:
         return self._attend_into(q, self.out)
 
     def _attend_into(self, q, out):
-        if self.pool.is_q8:
+        if self.pool.is_b8:
+            r = paged_decode_attention_b8(self.pool, q, self.d_tables, self.d_lens, self.scale,
+                                          self.status, window=self.window, sinks=self.sinks,
+                                          out=out)
+        elif self.window is not None:
+            r = paged_decode_attention_window(self.pool, q, self.d_tables, self.d_lens, self.scale,
+                                              self.window, self.sinks, self.status, out=out)
+        elif self.pool.is_q8:
             r = paged_decode_attention_q8(self.pool, q, self.d_tables, self.d_lens, self.scale,
                                           self.workspace, self.status, out=out)
         elif self.planned:
@@ -221,8 +269,9 @@ class DecodeEngine:
         return self.split
 
     def device_step(self, q, k_new, v_new):
-        """Cache write of this step's K/V, then paged attention."""
-        self.write(k_new, v_new)
+        """Cache write of this step's K/V, then paged attention (with ``rope``, ``q``
+        is rotated in place)."""
+        self.write(k_new, v_new, q=q)
         return self.attend(q)
 
     def decode_step(self, q, k_new, v_new):
@@ -249,7 +298,7 @@ class DecodeEngine:
         b = self._stage([(io["q"][nb], q_h), (io["k"][nb], k_h), (io["v"][nb], v_h)])
         cur = torch.cuda.current_stream()
         cur.wait_event(io["sent"][b])           # out set b's previous contents have left
-        self.write(io["k"][b], io["v"][b])
+        self.write(io["k"][b], io["v"][b], q=io["q"][b])
         self._attend_into(io["q"][b], io["out"][b])
         self._d2h.wait_event(self._used[b])
         with torch.cuda.stream(self._d2h):
@@ -306,7 +355,15 @@ class DecodeEngine:
         p = self.pool
         elem = 2
         per_head = 2 * (p.head_dim + p.head_dim // 32 * 2) if p.is_q8 else 2 * p.head_dim * elem
-        kv = int(self.lens.astype(np.int64).sum()) * p.num_kv_heads * per_head
+        lens = self.lens.astype(np.int64)
+        if self.window is not None:              # visible tokens
+            low = np.maximum(lens - self.window, 0)
+            lens = lens - low + np.minimum(self.sinks, low)
+        if p.is_b8:                              # codes, and the blocks' two scales
+            kv = p.num_kv_heads * (int(lens.sum()) * 2 * p.head_dim
+                                   + 8 * int((-(-lens // p.block_size)).sum()))
+        else:
+            kv = int(lens.sum()) * p.num_kv_heads * per_head
         qo = 2 * self.S * self.hq * p.head_dim * elem
-        meta = 4 * int(sum(-(-int(n) // p.block_size) for n in self.lens)) + 4 * self.S
+        meta = 4 * int((-(-lens // p.block_size)).sum()) + 4 * self.S
         return kv + qo + meta
