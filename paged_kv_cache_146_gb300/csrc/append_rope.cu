@@ -13,7 +13,8 @@
 //
 // Every value is read once and written once, so the kernels are bound by HBM
 // (and, for a decode step's few rows, by the chain slot -> position -> table
-// row -> store and the launch).
+// row -> store and the launch): 13,300 tokens of 8 + 8 heads of 64 (84 MB) 16 us,
+// 5.2 TB/s with the launch; the queries of 20,500 tokens (337 MB) 59 us, 5.7 TB/s.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -248,6 +249,11 @@ __device__ __forceinline__ float max_abs_nan(float a, float x)
     return m;
 }
 
+__device__ __forceinline__ void copy16(uint4 *dst, const uint4 *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+
 // Four stored bytes rounded to a larger scale (ratio = old / new <= 1).
 __device__ __forceinline__ uint32_t b8_rescale4(uint32_t w, float ratio)
 {
@@ -267,19 +273,21 @@ __device__ __forceinline__ uint32_t b8_rescale4(uint32_t w, float ratio)
 // where "scale before" counts only when the run does not start the block (off0
 // > 0).  When the scale grows, the codes of tokens 0 .. off0 - 1 are rounded to
 // it: rn(code * rn(old / new)).
-// A row is D / 16 lanes of 16 values.  The rows of the run stay in registers,
-// packed, between the maximum and the codes, so each value is read once; K is
-// rotated for both.  (Keeping the fp32 values took 154 registers and left too few
-// warps to fill the memory pipe: with the queries in the same launch, 20,500
-// tokens of 32 query and 8 kv heads took 176 us, against 59 + 49 us now; capping
-// this kernel's registers at 80 spilled, 69 us instead of 49.)
+// A row is D / 16 lanes of 16 values.  The run's rows wait, packed, between the
+// maximum and the codes (in registers for few tokens; many tokens stage them in
+// shared memory, which leaves registers for 32 warps an SM), so each value is read
+// once; K is rotated for both.  Measured on 20,500 tokens of 32 query and 8 kv
+// heads of 128: fp32 values kept in registers (154 of them), the queries in the
+// same launch: 176 us; packed in registers 59 (queries) + 49; staged 59 + 43.
 template <bool BF16, bool NEIGHBOURS, int D, bool SHARED>
 __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, int64_t t0, int n,
                                              int64_t block, int off0, int lane,
-                                             const int *positions, const float *cos_sin, int cs_stride)
+                                             const int *positions, const float *cos_sin, int cs_stride,
+                                             uint4 *stage)
 {
     // SHARED: positions and cos_sin hold the rows of tokens t0, t0 + 1, ... in
-    // shared memory; else they are the call's arrays
+    // shared memory, and the run's rows wait in `stage`; else these are the call's
+    // arrays, and the rows wait in registers
     constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPasses = 16 / kRows;
     constexpr int kRecord = PKV_B8_RECORD_BYTES(D);
     uint8_t *rec = p.kv + (block * p.num_kv_heads + h) * kRecord;
@@ -293,20 +301,28 @@ __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, i
     const ChunkPair cp = rotate ? chunk_pair<NEIGHBOURS>(i, p.rotary_dim)
                                 : ChunkPair{2 * i, 2 * i + 1, false};
     const float old = off0 > 0 ? *scale_at : 0.f;
-    uint4 w[kPasses][2];
+    uint4 w[SHARED ? 1 : kPasses][2];
     int pos[kPasses];                    // -1: no row, or one to skip
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
         const int j = k * kRows + r;
         const bool in = j < n;
         const uint4 *row = reinterpret_cast<const uint4 *>(rows + (t0 + (in ? j : 0)) * stride);
-        w[k][0] = in ? row[cp.c0] : make_uint4(0u, 0u, 0u, 0u);
-        w[k][1] = in ? row[cp.c1] : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (SHARED) {          // a lane stages what it will read itself
+            if (in) {
+                copy16(stage + 64 * k + lane, row + cp.c0);
+                copy16(stage + 64 * k + 32 + lane, row + cp.c1);
+            }
+        } else {
+            w[k][0] = in ? row[cp.c0] : make_uint4(0u, 0u, 0u, 0u);
+            w[k][1] = in ? row[cp.c1] : make_uint4(0u, 0u, 0u, 0u);
+        }
         pos[k] = !in ? -1 : !p.positions ? 0 : SHARED ? positions[j] : __ldg(positions + t0 + j);
     }
+    if constexpr (SHARED) asm volatile("cp.async.wait_all;" ::: "memory");
     auto values = [&](int k, float (&x)[16]) {
-        unpack8<BF16>(w[k][0], x);
-        unpack8<BF16>(w[k][1], x + 8);
+        unpack8<BF16>(SHARED ? stage[64 * k + lane] : w[SHARED ? 0 : k][0], x);
+        unpack8<BF16>(SHARED ? stage[64 * k + 32 + lane] : w[SHARED ? 0 : k][1], x + 8);
         if (cp.turned)
             rotate16<NEIGHBOURS, SHARED>(
                 x, i, p.rotary_dim >> 1,
@@ -432,7 +448,7 @@ __global__ void __launch_bounds__(128, 6) append_b8_kernel(const Params p)
         const int64_t s0 = __shfl_sync(kFull, runs.slot, 1);
         b8_write_run<BF16, NEIGHBOURS, D, false>(p, rest & 1, rest >> 1, t, runs.length(1),
                                                  s0 / kBlock, (int)(s0 % kBlock), lane,
-                                                 p.positions, p.cos_sin, p.rotary_dim);
+                                                 p.positions, p.cos_sin, p.rotary_dim, nullptr);
     }
 }
 
@@ -443,12 +459,14 @@ constexpr int kSpanWarps = 8;
 constexpr int kSpanTokens = 31;
 
 template <bool BF16, bool NEIGHBOURS, int D>
-__global__ void __launch_bounds__(32 * kSpanWarps, 2) append_b8_span_kernel(const Params p)
+__global__ void __launch_bounds__(32 * kSpanWarps, 4) append_b8_span_kernel(const Params p)
 {
     constexpr int kStride = D + 4;                        // floats of a staged table row
+    extern __shared__ uint4 stages[];                     // [warps][16 rows x D / 8]
     __shared__ __align__(16) float table[kSpanTokens * kStride];
     __shared__ int positions[kSpanTokens + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint4 *stage = stages + warp * 2 * D;
     const int64_t spans = ((int64_t)p.num_tokens + 15) / 16;
     for (int64_t w = blockIdx.x; w < spans; w += gridDim.x) {
         const int64_t tb = w * 16;
@@ -476,7 +494,7 @@ __global__ void __launch_bounds__(32 * kSpanWarps, 2) append_b8_span_kernel(cons
             b8_write_run<BF16, NEIGHBOURS, D, true>(p, rest & 1, rest >> 1, tb - 1 + l,
                                                     runs.length(l), s0 / kBlock,
                                                     (int)(s0 % kBlock), lane, positions + l - 1,
-                                                    table + (l - 1) * kStride, kStride);
+                                                    table + (l - 1) * kStride, kStride, stage);
         }
         __syncthreads();                                  // the table may be filled anew
     }
@@ -525,9 +543,11 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// From this many spans of 16 tokens on, a CTA per span; below, a warp per token
-// (8 kv heads: 2,000 tokens 14 us by spans, 18 by tokens; 500 tokens 14 and 8).
-constexpr int64_t kSpans = 100;
+// From this many spans of 16 tokens on, a CTA per span and the queries in a launch
+// of their own; below, a warp per token and one launch.  With 32 query and 8 kv
+// heads, the append and its read-back: 2,000 tokens 28 us by spans, 24 by tokens;
+// 4,000 tokens 38 and 39; 8,000 tokens 57 and 73.
+constexpr int64_t kSpans = 200;
 
 template <bool BF16, bool NEIGHBOURS>
 static int launch_rows(const Params &p, int D, int heads_kv, cudaStream_t st)
@@ -549,8 +569,14 @@ static int launch_b8(const Params &p0, int D, bool queries, cudaStream_t st)
             if (rc != PKV_OK) return rc;
         }
         const unsigned grid = (unsigned)std::min<int64_t>(spans, 152 * 64);
-        if (D == 128) append_b8_span_kernel<BF16, NEIGHBOURS, 128><<<grid, 32 * kSpanWarps, 0, st>>>(p);
-        else append_b8_span_kernel<BF16, NEIGHBOURS, 64><<<grid, 32 * kSpanWarps, 0, st>>>(p);
+        const int smem = kSpanWarps * 32 * D;
+        void (*fn)(Params) = D == 128 ? &append_b8_span_kernel<BF16, NEIGHBOURS, 128>
+                                      : &append_b8_span_kernel<BF16, NEIGHBOURS, 64>;
+        // with the static part a little over the 48 KB of a plain launch
+        if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return PKV_ERR_CUDA;
+        fn<<<grid, 32 * kSpanWarps, smem, st>>>(p);
         return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
     }
     const int64_t units = (int64_t)p.num_tokens * 2 * p.num_kv_heads;
