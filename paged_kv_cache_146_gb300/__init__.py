@@ -936,8 +936,8 @@ def _decode_call(name: str, pool: KVPool, q, out, block_tables, context_lens, sc
     if pool.is_b8:
         pools = pools[:1]
     _launch(name, dev, stream, pool.handle, out.data_ptr(), q.data_ptr(), *pools,
-            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), S, hq, scale,
-            window, sinks, _want_status(status, dev))
+            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), S, hq,
+            float(scale), window, sinks, _want_status(status, dev))
     return out
 
 
@@ -1012,7 +1012,7 @@ def paged_prefill_attention_window(pool: KVPool, q, block_tables, query_start, c
     wp = _want("workspace", workspace, (nbytes,), torch.uint8, dev)
     kp, vp = _want_pools(pool, dev, k_pool, v_pool)
     _launch("paged_prefill_attention_window", dev, stream, pool.handle, op, qp, kp, vp, tp, maxb,
-            sp, lp, S, T, hq, scale, window, sinks, wp, nbytes, _want_status(status, dev))
+            sp, lp, S, T, hq, float(scale), window, sinks, wp, nbytes, _want_status(status, dev))
     return out
 
 

@@ -1035,7 +1035,9 @@ static int launch(const pkv_pool *pool, bool want_b8, void *out, const void *q, 
     p.ctas = C;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // more than one wave, lengths not levelled by a window: longest pairs first
-    p.most = pairs * C > lim.resident && most == maxb && most >= 64 ? (int)most : 0;
+    // (every CTA looks at every length for it, so not for thousands of sequences,
+    // whose many waves even out by themselves)
+    p.most = pairs * C > lim.resident && most == maxb && most >= 64 && num_seqs <= 512 ? (int)most : 0;
     if (pairs * C > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -251,6 +251,32 @@ def test_attention_long_and_wide_tables():
     run_attention([9001], 4, 1, 64, "f16", None, 0, 22, maxb=600)
 
 
+@pytest.mark.parametrize("seqs,hq,hkv,top", [(130, 4, 4, 1100), (45, 4, 2, 760), (600, 1, 1, 40)])
+def test_attention_many_ragged_sequences(seqs, hq, hkv, top):
+    """More CTAs than fit at once (longest first), odd cluster sizes, many short rows."""
+    lens = [(37 * i * i + 11 * i) % top for i in range(seqs)]
+    run_attention(lens, hq, hkv, 64, "bf16", None, 0, seqs, maxb=-(-top // 16) + 2)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1])
+def test_attention_zero_and_negative_scale(scale):
+    gen = torch.Generator().manual_seed(30)
+    tables, nb = random_case(gen, [90], 1, 6)
+    pool, ref = random_pool(nb, 1, 64, "f16", 31)
+    q = torch.randn((1, 4, 64), generator=gen).to(torch.float16)
+    status = new_status()
+    out = paged_decode_attention_b8(pool, q.cuda(), tables.cuda(), torch.tensor([90], dtype=torch.int32, device="cuda"),
+                                    scale, status, window=30, sinks=5)
+    assert status_check(status) == (0, 0)
+    j = torch.tensor(visible(90, 89, 30, 5))
+    k, v = (torch.from_numpy(ref.values(p))[tables[0].long()[j // 16], 0, j % 16] for p in range(2))
+    offs = [1152 * torch.from_numpy(x[:, 0]).double()[tables[0].long()[j // 16]] for x in ref.scales]
+    for h in range(4):
+        # the bound counts the score's size: take the scale's
+        want, bound = attention(-q[0, h].double(), k, v, -scale, torch.float16, F16_HALF_STEP ** 2, *offs)
+        assert_within(out[0, h], want, bound, f"head {h}")
+
+
 def test_attention_scales_and_queries_of_any_size():
     """Blocks whose scales differ by 2^40, and queries far outside fp16's range."""
     dim, hkv, hq = 128, 1, 4

@@ -207,6 +207,33 @@ def test_prefill_wide_window_is_the_causal_call():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.125])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_zero_and_negative_scales(dtype, scale):
+    """Scale 0 weighs every visible token alike; a negative one prefers small products."""
+    lens, chunks, window, sinks = [200, 90], [140, 7], 33, 6
+    first = [n - c for n, c in zip(lens, chunks)]
+    pool, k, v, tables, gen = build(lens, first, 2, 64, dtype, window, sinks, 46)
+    q = torch.randn((147, 4, 64), generator=gen).to(DT[dtype])
+    start = torch.tensor([0, 140, 147], dtype=torch.int32, device="cuda")
+    dl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = torch.empty(prefill_workspace_bytes(2, 147, 4, 2), dtype=torch.uint8, device="cuda")
+    status = new_status()
+    out = paged_prefill_attention_window(pool, q.cuda(), tables.cuda(), start, dl, scale, window, sinks, ws, status)
+    last = q[[139, 146]].cuda()
+    dec = paged_decode_attention_window(pool, last, tables.cuda(), dl, scale, window, sinks, status)
+    assert status_check(status) == (0, 0)
+    for row, s, pos in [(0, 0, 60), (77, 0, 137), (139, 0, 199), (146, 1, 89)]:
+        j = torch.tensor(visible(lens[s], pos, window, sinks))
+        blk, off = tables[s].long()[j // 16], j % 16
+        for h in range(4):
+            kk, vv = (p[blk, h // 2, off].double() for p in (k, v))
+            want, bound = attention(-q[row, h].double(), kk, vv, -scale, DT[dtype], PREFILL_WEIGHT[dtype])
+            assert_within(out[row, h], want, bound, f"row {row} head {h}")
+            if row in (139, 146):
+                assert_within(dec[s, h], want, bound, f"decode {s} head {h}")
+
+
 def test_prefill_bad_sequences():
     pool, k, v, tables, gen = build([40, 40, 40], [0, 0, 0], 2, 64, "f16", 99, 0, 44)
     q = torch.randn((30, 4, 64), generator=gen).to(torch.float16).cuda()
