@@ -13,6 +13,12 @@ Typical decode step (the flow of "LLM 추론 배칭 전략 정리", section 5):
     cache_write(pool, k_new, v_new, d_slots, status)          # device: write new K/V
     paged_decode_attention(pool, q, d_tables, d_lens, scale, ws, status, out=out)
     pool.free(finished_blocks)                                # host: release
+
+A model that rotates K and its queries by position, and attends to a window:
+
+    table = rope_table(max_positions, rotary_dim, device="cuda")
+    q = cache_write_rope(pool, k_new, v_new, d_positions, table, d_slots, status, q=q)
+    paged_decode_attention_window(pool, q, d_tables, d_lens, scale, window, sinks, status)
 """
 from __future__ import annotations
 
