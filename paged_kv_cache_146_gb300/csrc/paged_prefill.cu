@@ -38,6 +38,7 @@ struct Params {
     int32_t num_seqs, num_tokens, num_q_heads, num_kv_heads, group, max_blocks_per_seq;
     int32_t num_blocks, tile_tokens;
     int32_t window, sinks;          // windowed calls only (tcp kernel, WINDOW)
+    int32_t group_tokens;           // windowed: tokens of a query tile (an item has one or two)
     float scale_log2;
     int32_t *header;                // [0] = number of (sequence, tile) pairs
     int2 *items;                    // (sequence, tile)
@@ -366,17 +367,22 @@ struct Item {
     int sink_blocks, gap, hide0, hide1;
 };
 
-// Keys an item of a windowed call reads: its first query (token t0) reaches
-// back furthest, to position lo; later ones see less of the front.
-__device__ __forceinline__ void item_window(Item &it, int window, int sinks)
+// An item of a windowed call: its tokens (one or two query tiles, QT tokens each)
+// and the keys that it reads: its first query (token t0) reaches back furthest, to
+// position lo; later ones see less of the front.
+__device__ __forceinline__ void item_window(Item &it, const Params &p, int QT)
 {
-    const int lo = max(0, it.L - it.C + it.t0 - window + 1);
-    const int seen = min(sinks, it.nkeys);                 // sinks up to the last query
+    it.t0 = it.t0 / (kGroups * QT) * p.tile_tokens;
+    it.t1 = min(it.t0 + p.tile_tokens, it.C);
+    it.nkeys = it.L - it.C + it.t1;
+    const int lo = max(0, it.L - it.C + it.t0 - p.window + 1);
+    const int seen = min(p.sinks, it.nkeys);               // sinks up to the last query
     it.sink_blocks = (seen + kBlock - 1) / kBlock;
     it.gap = max(0, lo / kBlock - it.sink_blocks);
     it.nkeys -= it.gap * kBlock;
     it.hide0 = seen;
     it.hide1 = lo - it.gap * kBlock;
+    it.ntiles = (it.nkeys + kKeys - 1) / kKeys;
 }
 
 template <bool PREFIX, int KEYS = kKeys>
@@ -479,7 +485,8 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t tmem = *tslot;
     griddep_wait();
 
-    const int Hkv = p.num_kv_heads, G = p.group, QT = p.tile_tokens / kGroups;   // one query tile
+    // tokens of one query tile
+    const int Hkv = p.num_kv_heads, G = p.group, QT = WINDOW ? p.group_tokens : p.tile_tokens / kGroups;
     const int total = (PREFIX ? *p.prefix_count : p.header[0]) * Hkv;
 
     if (warp == kProducer) {
@@ -489,10 +496,7 @@ __global__ void __launch_bounds__(kThreads)
             for (int k = 0; k < LY::kStages; ++k) last_par[k] = -1;
             for (int i = blockIdx.x; i < total && !*abort_flag; i += gridDim.x, ++it_cnt) {
                 Item it = load_item<PREFIX>(p, i, total, QT);
-                if constexpr (WINDOW) {
-                    item_window(it, p.window, p.sinks);
-                    it.ntiles = (it.nkeys + kKeys - 1) / kKeys;
-                }
+                if constexpr (WINDOW) item_window(it, p, QT);
                 if (it_cnt > 0 &&
                     !mbar_wait(smem_addr(q_empty), (it_cnt - 1) & 1u, abort_flag, p.status))
                     break;
@@ -572,11 +576,13 @@ __global__ void __launch_bounds__(kThreads)
             // issuing thread's instruction stream short -- it shares its
             // scheduler with two softmax warps.
             const uint64_t qa_d = tc::desc_sw128(q_a, 16, 1024);
-            uint32_t tg = 0, it_cnt = 0;
+            // tg counts this query tile's key tiles, lag those that passed it by (a
+            // windowed call's items with one query tile): the stages count both
+            uint32_t tg = 0, lag = 0, it_cnt = 0;
             bool ok = true;
             // P V of tile t for this group, then its share of freeing the stage
             auto issue_pv = [&](uint32_t t, bool first) {
-                const uint32_t vs = st_a + (t % LY::kStages) * LY::kStageBytes + LY::kKVBytes;
+                const uint32_t vs = st_a + ((t + lag) % LY::kStages) * LY::kStageBytes + LY::kKVBytes;
                 if (!mbar_wait(smem_addr(&p_full[2 * gr + (t & 1u)]), (t >> 1) & 1u, abort_flag,
                                p.status)) {
                     ok = false;
@@ -594,18 +600,27 @@ __global__ void __launch_bounds__(kThreads)
                                        !(first && part == 0 && kk == 0));
                     }
                 tc::mma_commit(smem_addr(&o_full[2 * gr + (t & 1u)]));
-                tc::mma_commit(smem_addr(&kv_empty[t % LY::kStages]));
+                tc::mma_commit(smem_addr(&kv_empty[(t + lag) % LY::kStages]));
             };
             for (int i = blockIdx.x; i < total && ok; i += gridDim.x, ++it_cnt) {
                 Item it = load_item<PREFIX>(p, i, total, QT);
-                if constexpr (WINDOW) {
-                    item_window(it, p.window, p.sinks);
-                    it.ntiles = (it.nkeys + kKeys - 1) / kKeys;
-                }
+                if constexpr (WINDOW) item_window(it, p, QT);
                 if (!mbar_wait(smem_addr(q_full), it_cnt & 1u, abort_flag, p.status)) break;
+                if constexpr (WINDOW) {
+                    if (gr == 1 && it.t0 + QT >= it.t1) {   // no rows: only give the buffers back
+                        mbar_arrive(smem_addr(q_empty));
+                        for (int t = 0; t < it.ntiles && ok; ++t, ++lag) {
+                            const uint32_t st = (tg + lag) % LY::kStages;
+                            ok = mbar_wait(smem_addr(&kv_full[st]), ((tg + lag) / LY::kStages) & 1u,
+                                           abort_flag, p.status);
+                            if (ok) mbar_arrive(smem_addr(&kv_empty[st]));
+                        }
+                        continue;
+                    }
+                }
                 for (int t = 0; t < it.ntiles && ok; ++t, ++tg) {
-                    const uint32_t st = tg % LY::kStages, sb = tg & 1u;
-                    if (!mbar_wait(smem_addr(&kv_full[st]), (tg / LY::kStages) & 1u, abort_flag,
+                    const uint32_t st = (tg + lag) % LY::kStages, sb = tg & 1u;
+                    if (!mbar_wait(smem_addr(&kv_full[st]), ((tg + lag) / LY::kStages) & 1u, abort_flag,
                                    p.status)) {
                         ok = false;
                         break;
@@ -641,13 +656,16 @@ __global__ void __launch_bounds__(kThreads)
         const int r = threadIdx.x - kRows * gr;     // row = tensor-memory lane
         const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t s_col = 64 * 2 * gr, o_col = 256 + 128 * gr;
-        uint32_t tg = 0, it_cnt = 0;
+        uint32_t tg = 0, lag = 0, it_cnt = 0;      // as the issuer counts them
         bool alive = true;
         for (int i = blockIdx.x; i < total && alive; i += gridDim.x, ++it_cnt) {
             Item it = load_item<PREFIX>(p, i, total, QT);
+            if constexpr (WINDOW) item_window(it, p, QT);
             if constexpr (WINDOW) {
-                item_window(it, p.window, p.sinks);
-                it.ntiles = (it.nkeys + kKeys - 1) / kKeys;
+                if (gr == 1 && it.t0 + QT >= it.t1) {
+                    lag += (uint32_t)it.ntiles;
+                    continue;
+                }
             }
             const int jj = r / G, h = r - (r / G) * G;
             const int tg0 = it.t0 + gr * QT;            // this group's first token
@@ -661,9 +679,12 @@ __global__ void __launch_bounds__(kThreads)
             float m_ref = -INFINITY, l = 0.f;
             int bad = 0;
             for (int t = 0; t < it.ntiles; ++t, ++tg) {
-                const uint32_t st = tg % LY::kStages, sb = tg & 1u;
-                const bool ok1 = mbar_wait(smem_addr(&kv_full[st]), (tg / LY::kStages) & 1u, abort_flag,
-                                           p.status);
+                const uint32_t st = (tg + lag) % LY::kStages, sb = tg & 1u;
+                // (windowed: a query tile that passed items by may be more than a phase
+                // away from this barrier; S is issued only after its stage has landed,
+                // so the wait for S stands for both)
+                const bool ok1 = WINDOW || mbar_wait(smem_addr(&kv_full[st]), (tg / LY::kStages) & 1u,
+                                                     abort_flag, p.status);
                 const bool ok2 = ok1 && mbar_wait(smem_addr(&s_full[2 * gr + sb]), (tg >> 1) & 1u,
                                                   abort_flag, p.status);
                 if (!__all_sync(kFull, ok2)) { alive = false; break; }
@@ -1519,9 +1540,10 @@ static int64_t max_items(int64_t S, int64_t T, int64_t QT) { return T / QT + S +
 // tokens of one item: kGroups query tiles of kRows / G tokens each
 static int tile_tokens(int G) { return tcp::kGroups * (tcp::kRows / G); }
 
+// (room for items of a single query tile, as small windowed calls have them)
 static size_t ws_bytes(int64_t S, int64_t T, int64_t G)
 {
-    return 256 + align256((size_t)max_items(S, T, tile_tokens((int)G)) * 8);
+    return 256 + align256((size_t)max_items(S, T, tcp::kRows / G) * 8);
 }
 
 // The workspace with room for the fp16 copy of V after the work list: the
@@ -1778,20 +1800,27 @@ static int prefill_call(const pkv_pool *pool, void *out, const void *q, const vo
     prm.tile_tokens = tile_tokens(G);
     prm.window = window;
     prm.sinks = sinks;
+    prm.group_tokens = tcp::kRows / G;
     prm.scale_log2 = scale * 1.4426950408889634f;
     // a windowed call hides scores by an infinity that the scale must carry into
     // the exponent; at scale 0 the smallest normal number weighs all keys alike
     if (window > 0 && scale == 0.f) prm.scale_log2 = 0x1p-126f;
     prm.header = static_cast<int32_t *>(workspace);
     prm.items = reinterpret_cast<int2 *>(static_cast<char *>(workspace) + 256);
+    int sms = 0;
+    const int per_sm = resident(reinterpret_cast<const void *>(kp.fn), kp.smem, kp.threads, &sms);
+    if (per_sm < 1 || (kp.reg_split && !launch_regs_ok(kp.fn))) return PKV_ERR_CUDA;
+    // a windowed call of few items gives each a single query tile: a key tile then
+    // costs a CTA one softmax and one pair of products instead of two of each (one
+    // chunk of 64 to 512 tokens, window 1,024: 29 against 37 us; from more items than
+    // SMs on, two tiles share every key tile)
+    if (window > 0 && max_items(num_seqs, num_tokens, prm.group_tokens) * g.num_kv_heads <= sms)
+        prm.tile_tokens = prm.group_tokens;
     prm.max_items = max_items(num_seqs, num_tokens, prm.tile_tokens);
     prm.status = d_status;
     prm.v16 = staged ? reinterpret_cast<uint16_t *>(ws + sl.v16) : nullptr;
     prm.v_emax = staged ? reinterpret_cast<int32_t *>(ws + sl.emax) : nullptr;
 
-    int sms = 0;
-    const int per_sm = resident(reinterpret_cast<const void *>(kp.fn), kp.smem, kp.threads, &sms);
-    if (per_sm < 1 || (kp.reg_split && !launch_regs_ok(kp.fn))) return PKV_ERR_CUDA;
     int64_t grid = (int64_t)per_sm * sms;
     const int64_t upper = prm.max_items * g.num_kv_heads;
     if (grid > upper) grid = upper;

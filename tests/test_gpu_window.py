@@ -187,6 +187,14 @@ def test_prefill_head_layouts(dtype, dim, hq, hkv):
     run_prefill([500, 77], [60, 77], hq, hkv, dim, dtype, 100, 4, hq, sample=24)
 
 
+@pytest.mark.parametrize("window,sinks", [(1, 0), (70, 4), (200, 33), (10 ** 6, 0)])
+@pytest.mark.parametrize("dtype,dim,hq,hkv", [("bf16", 64, 32, 16), ("f16", 128, 20, 20)])
+def test_prefill_many_items(dtype, dim, hq, hkv, window, sinks):
+    """More items than SMs: two query tiles to an item, the second of some empty."""
+    run_prefill([700, 400, 333, 64, 900], [300, 400, 100, 64, 130], hq, hkv, dim, dtype, window, sinks,
+                window % 89, sample=16)
+
+
 def test_prefill_long_chunk():
     """Many tiles per item, whole tiles hidden from the item's later rows."""
     run_prefill([4100], [600], 2, 2, 128, "bf16", 70, 4, 41, sample=40)
