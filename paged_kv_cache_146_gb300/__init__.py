@@ -840,15 +840,22 @@ def cache_write_rope(pool: KVPool, k_new, v_new, positions, cos_sin, slot_mappin
     dt = pool._rows or _row_dtype(pool)
     torch = _torch
     dev, D, Hkv = k_new.get_device(), pool.head_dim, pool.num_kv_heads
-    T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
-    slots = _want("slot_mapping", slot_mapping, (T,), torch.int64, dev)
+    if not (slot_mapping.dtype is torch.int64 and slot_mapping.dim() == 1
+            and slot_mapping.get_device() == dev and slot_mapping.is_contiguous()
+            and positions.dtype is torch.int32 and positions.shape == slot_mapping.shape
+            and positions.get_device() == dev and positions.is_contiguous()
+            and cos_sin.dtype is torch.float32 and cos_sin.dim() == 2
+            and cos_sin.get_device() == dev and cos_sin.is_contiguous()):
+        T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
+        _want("slot_mapping", slot_mapping, (T,), torch.int64, dev)
+        _want("positions", positions, (T,), torch.int32, dev)
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_positions][rotary_dim]")
+        _want("cos_sin", cos_sin, tuple(cos_sin.shape), torch.float32, dev)
+    T = slot_mapping.shape[0]
+    rows, rot = cos_sin.shape
     k, ks = _want_rows("k_new", k_new, (T, Hkv, D), dt, dev)
     v, vs = _want_rows("v_new", v_new, (T, Hkv, D), dt, dev)
-    pos = _want("positions", positions, (T,), torch.int32, dev)
-    if cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be [max_positions][rotary_dim]")
-    rows, rot = cos_sin.shape
-    table = _want("cos_sin", cos_sin, (rows, rot), torch.float32, dev)
     qp = qs = qo = qos = hq = 0
     if q is not None:
         if q.dim() != 3:
@@ -864,8 +871,8 @@ def cache_write_rope(pool: KVPool, k_new, v_new, positions, cos_sin, slot_mappin
         raise ValueError("q_out without q")
     kp, vp = _want_pools(pool, dev, k_pool, v_pool, kv)
     _launch("kv_cache_write_rope", dev, stream, pool.handle, qo, qos, qp, qs, hq, k, ks, v, vs,
-            pos, table, rows, rot, 1 if interleaved else 0, slots, T, kp, vp,
-            _want_status(status, dev))
+            positions.data_ptr(), cos_sin.data_ptr(), rows, rot, 1 if interleaved else 0,
+            slot_mapping.data_ptr(), T, kp, vp, _want_status(status, dev))
     return q_out
 
 

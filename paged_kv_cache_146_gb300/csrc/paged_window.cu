@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(32 * W, Shape<D, B8, NT, W>::kMinBlocks)
     }
     __syncthreads();
 
-    // ---- the four warps: factors 2^(m_w - M), sums; a bad piece has sum -1
+    // ---- the CTA's warps: factors 2^(m_w - M), sums; a bad piece has sum -1
     T *out = static_cast<T *>(p.out) + ((int64_t)s * p.num_q_heads + (int64_t)g * G) * D;
     auto factor = [](float m, float M) { return m == -INFINITY ? 0.f : fast_exp2(m - M); };
     auto store = [&](int u, float4 a, float l, bool poisoned) {
