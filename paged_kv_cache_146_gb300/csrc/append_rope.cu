@@ -37,6 +37,7 @@ struct Params {
     const int64_t *slots;
     int32_t num_tokens, num_q_heads, num_kv_heads, max_positions, rotary_dim;
     int32_t block_size;
+    int32_t block_shift, lane_shift;     // log2 of block_size and of head_dim / 16; -1: no power of two
     int64_t num_slots;
     uint4 *k_pool, *v_pool;              // 16-bit pools
     uint8_t *kv;                         // 8-bit records
@@ -137,7 +138,7 @@ __device__ __forceinline__ void append_rows(const Params &p, int D, int heads_kv
     auto load = [&](RowUnit &u) {                         // and advance
         u.t = t;
         if (t < p.num_tokens) {
-            u.head = within / lanes;
+            u.head = p.lane_shift >= 0 ? within >> p.lane_shift : within / lanes;
             u.i = within - u.head * lanes;
             const ChunkPair cp = chunk_pair<NEIGHBOURS>(u.i, p.rotary_dim);
             const int h = u.head - p.num_q_heads;
@@ -180,7 +181,8 @@ __device__ __forceinline__ void append_rows(const Params &p, int D, int heads_kv
             dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.q_out) + u.t * p.q_out_stride +
                                             (int64_t)u.head * D);
         } else {
-            const int64_t block = u.slot / p.block_size;
+            const int64_t block =
+                p.block_shift >= 0 ? u.slot >> p.block_shift : u.slot / p.block_size;
             const int64_t off = u.slot - block * p.block_size;
             const int kvh = h < heads_kv ? h : h - heads_kv;
             dst = (h < heads_kv ? p.k_pool : p.v_pool) +
@@ -591,6 +593,13 @@ static int launch_b8(const Params &p0, int D, bool queries, cudaStream_t st)
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
+static int32_t log2_or_none(int32_t x)
+{
+    for (int32_t k = 0; k < 31; ++k)
+        if (x == 1 << k) return k;
+    return -1;
+}
+
 static bool rows_ok(const void *p, int64_t stride, int64_t width)
 {
     return p && aligned16(p) && stride >= width && stride % 8 == 0;
@@ -648,6 +657,8 @@ extern "C" int kv_cache_write_rope(const pkv_pool *pool, void *q_out, int64_t q_
     p.max_positions = max_positions;
     p.rotary_dim = rotary_dim;
     p.block_size = g.block_size;
+    p.block_shift = log2_or_none(g.block_size);
+    p.lane_shift = log2_or_none(g.head_dim / 16);
     p.num_slots = (int64_t)g.num_blocks * g.block_size;
     p.k_pool = static_cast<uint4 *>(k_pool);
     p.v_pool = static_cast<uint4 *>(v_pool);
