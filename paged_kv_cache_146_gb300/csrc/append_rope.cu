@@ -13,8 +13,8 @@
 //
 // Every value is read once and written once, so the kernels are bound by HBM
 // (and, for a decode step's few rows, by the chain slot -> position -> table
-// row -> store and the launch): 13,300 tokens of 8 + 8 heads of 64 (84 MB) 16 us,
-// 5.2 TB/s with the launch; the queries of 20,500 tokens (337 MB) 59 us, 5.7 TB/s.
+// row -> store and the launch): 13,300 tokens of 8 + 8 heads of 64 (84 MB) 14.8 us,
+// 5.7 TB/s with its ramp; the queries of 20,500 tokens (337 MB) 57 us, 5.9 TB/s.
 #include <algorithm>
 
 #include <cuda_bf16.h>
