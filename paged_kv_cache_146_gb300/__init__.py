@@ -230,6 +230,10 @@ class KVPool:
                                    self.dtype_code, _np_ptr(order) if order is not None else None,
                                    ctypes.byref(h)), "kv_pool_create")
         self._h = h
+        # what the compiled call checks need to know of the pool (see _load_torch)
+        self._meta = (h.value, num_blocks, num_kv_heads, block_size, head_dim,
+                      int(self.dtype_code in (PKV_BF16, PKV_B8_BF16)),
+                      32 * head_dim + 32 if self.dtype_code in (PKV_B8_BF16, PKV_B8_F16) else 0)
         self.k_pool = self.v_pool = self.kv = self._rows = None
         if device is not None:
             import torch
@@ -250,7 +254,7 @@ class KVPool:
     def close(self):
         if getattr(self, "_h", None) is not None:
             lib().kv_pool_destroy(self._h)
-            self._h = None
+            self._h = self._meta = None
 
     def __del__(self):
         try:
@@ -702,17 +706,34 @@ def paged_decode_attention_q8(pool: KVPool, q, block_tables, context_lens, scale
 
 # --------------------------------------- rotated append, 8-bit blocks, windows
 # The calls below are also made for a few rows at a time, where the host side is
-# most of their time: the frequent ones check every tensor in one expression (when
-# it fails, the same checks run one by one for the message), addresses go to the
-# library as plain integers, and torch is looked up once.
-_torch = None
+# most of their time.  Their argument checks exist twice: compiled (_fastcall,
+# csrc/fastcall.cpp), which calls the library when every check holds, and here,
+# which says what is wrong when one does not (and makes the call where the
+# compiled form does not: a library built without torch's headers, tensors on
+# another device than the current one).
+_torch = _fast = None
 
 
 def _load_torch():
-    global _torch
+    global _torch, _fast
     import torch
-    _torch = torch
+    try:
+        from . import _fastcall
+    except ImportError:
+        _fastcall = None
+    if _fastcall is not None and _fastcall.torch_version != torch.__version__.split("+")[0]:
+        _fastcall = None                    # built against the headers of another torch
+    if _fastcall is not None:
+        _fastcall.bind(*(ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in (
+            "paged_decode_attention_window", "paged_decode_attention_b8", "kv_cache_write_rope",
+            "kv_dequantize_blocks", "paged_prefill_attention_window")))
+    _torch, _fast = torch, _fastcall
     return torch
+
+
+def _raw(stream):
+    """A call's ``stream`` argument as the compiled checks take it."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def _refuse(name: str, t, shape: tuple, dtype, index: int, contiguous: bool):
@@ -786,7 +807,8 @@ def _row_dtype(pool: KVPool):
     """Element type of the pool's rows (looked up once per pool)."""
     dt = pool._rows
     if dt is None:
-        _load_torch()
+        if _torch is None:
+            _load_torch()
         dt = pool._rows = _torch_dtype(pool.dtype_code)
     return dt
 
@@ -839,21 +861,26 @@ def cache_write_rope(pool: KVPool, k_new, v_new, positions, cos_sin, slot_mappin
     neighbouring dimensions instead of the halves' (i, i + rotary_dim / 2)."""
     dt = pool._rows or _row_dtype(pool)
     torch = _torch
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if _fast is not None:
+        a, b = ((pool.kv if kv is None else kv, None) if pool.record_bytes else
+                (pool.k_pool if k_pool is None else k_pool, pool.v_pool if v_pool is None else v_pool))
+        rc = None if pool.is_q8 else _fast.rope(
+            pool._meta, k_new, v_new, positions, cos_sin, slot_mapping, status, q, q_out,
+            1 if interleaved else 0, a, b, _raw(stream))
+        if rc is not None:
+            if rc:
+                check(rc, "kv_cache_write_rope")
+            return q_out
     dev, D, Hkv = k_new.get_device(), pool.head_dim, pool.num_kv_heads
-    if not (slot_mapping.dtype is torch.int64 and slot_mapping.dim() == 1
-            and slot_mapping.get_device() == dev and slot_mapping.is_contiguous()
-            and positions.dtype is torch.int32 and positions.shape == slot_mapping.shape
-            and positions.get_device() == dev and positions.is_contiguous()
-            and cos_sin.dtype is torch.float32 and cos_sin.dim() == 2
-            and cos_sin.get_device() == dev and cos_sin.is_contiguous()):
-        T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
-        _want("slot_mapping", slot_mapping, (T,), torch.int64, dev)
-        _want("positions", positions, (T,), torch.int32, dev)
-        if cos_sin.dim() != 2:
-            raise ValueError("cos_sin must be [max_positions][rotary_dim]")
-        _want("cos_sin", cos_sin, tuple(cos_sin.shape), torch.float32, dev)
-    T = slot_mapping.shape[0]
+    T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
+    slots = _want("slot_mapping", slot_mapping, (T,), torch.int64, dev)
+    pos = _want("positions", positions, (T,), torch.int32, dev)
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [max_positions][rotary_dim]")
     rows, rot = cos_sin.shape
+    table = _want("cos_sin", cos_sin, (rows, rot), torch.float32, dev)
     k, ks = _want_rows("k_new", k_new, (T, Hkv, D), dt, dev)
     v, vs = _want_rows("v_new", v_new, (T, Hkv, D), dt, dev)
     qp = qs = qo = qos = hq = 0
@@ -861,8 +888,6 @@ def cache_write_rope(pool: KVPool, k_new, v_new, positions, cos_sin, slot_mappin
         if q.dim() != 3:
             raise ValueError(f"q must be [{T}][h][{D}], got {list(q.shape)}")
         hq = q.shape[1]
-        if q_out is None:
-            q_out = torch.empty((T, hq, D), dtype=dt, device=q.device)
         qp, qs = _want_rows("q", q, (T, hq, D), dt, dev)
         qo, qos = (qp, qs) if q_out is q else _want_rows("q_out", q_out, (T, hq, D), dt, dev)
         if qp == qo and qs != qos:
@@ -871,8 +896,8 @@ def cache_write_rope(pool: KVPool, k_new, v_new, positions, cos_sin, slot_mappin
         raise ValueError("q_out without q")
     kp, vp = _want_pools(pool, dev, k_pool, v_pool, kv)
     _launch("kv_cache_write_rope", dev, stream, pool.handle, qo, qos, qp, qs, hq, k, ks, v, vs,
-            positions.data_ptr(), cos_sin.data_ptr(), rows, rot, 1 if interleaved else 0,
-            slot_mapping.data_ptr(), T, kp, vp, _want_status(status, dev))
+            pos, table, rows, rot, 1 if interleaved else 0, slots, T, kp, vp,
+            _want_status(status, dev))
     return q_out
 
 
@@ -901,9 +926,16 @@ def dequantize_blocks(pool: KVPool, ids, k_out, v_out, status, kv=None, stream=N
     ``k_out``/``v_out`` [n][Hkv][16][D] in the pool's row type (the layout of a 16-bit
     pool of n blocks).  Returns (k_out, v_out)."""
     torch = _torch or _load_torch()
-    dev = ids.get_device()
     if not pool.is_b8:
         raise ValueError("dequantize_blocks takes a block-scaled 8-bit pool")
+    if _fast is not None:
+        rc = _fast.dequantize(pool._meta, ids, k_out, v_out, status, pool.kv if kv is None else kv,
+                              _raw(stream))
+        if rc is not None:
+            if rc:
+                check(rc, "kv_dequantize_blocks")
+            return k_out, v_out
+    dev = ids.get_device()
     n = ids.shape[0] if ids.dim() == 1 else -1
     i = _want("ids", ids, (n,), torch.int32, dev)
     dt, shape = _row_dtype(pool), (n, pool.num_kv_heads, 16, pool.head_dim)
@@ -920,37 +952,36 @@ def _decode_call(name: str, pool: KVPool, q, out, block_tables, context_lens, sc
     """Checks and launch of the windowed decode calls."""
     dt = pool._rows or _row_dtype(pool)
     torch = _torch
-    dev, D, i32 = q.get_device(), pool.head_dim, torch.int32
-    shape = q.shape
-    if len(shape) != 3 or shape[2] != D:
-        raise ValueError(f"q must be [n][h][{D}], got {list(shape)}")
-    S, hq, _ = shape
+    if out is None:
+        out = torch.empty_like(q)
+    if _fast is not None:
+        a, b = ((pool.kv if kv is None else kv, None) if pool.is_b8 else
+                (pool.k_pool if k_pool is None else k_pool, pool.v_pool if v_pool is None else v_pool))
+        rc = _fast.decode(pool._meta, q, out, block_tables, context_lens, float(scale), window, sinks,
+                          status, a, b, _raw(stream))
+        if rc is not None:
+            if rc:
+                check(rc, name)
+            return out
+    dev, D = q.get_device(), pool.head_dim
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError(f"q must be [n][h][{D}], got {list(q.shape)}")
+    S, hq, _ = shape = tuple(q.shape)
     if hq % pool.num_kv_heads:
         raise ValueError(f"q has {hq} heads, not a multiple of the pool's "
                          f"{pool.num_kv_heads} kv heads")
-    if out is None:
-        out = torch.empty_like(q)
-    if not (q.dtype is dt and q.is_contiguous()
-            and out.dtype is dt and out.shape == shape and out.get_device() == dev
-            and out.is_contiguous()
-            and block_tables.dtype is i32 and block_tables.dim() == 2
-            and block_tables.get_device() == dev and block_tables.is_contiguous()
-            and context_lens.dtype is i32 and context_lens.shape == (S,)
-            and context_lens.get_device() == dev and context_lens.is_contiguous()
-            and len(block_tables) == S):
-        shape = tuple(shape)
-        _want("q", q, shape, dt, dev)
-        _want("out", out, shape, dt, dev)
-        if block_tables.dim() != 2:
-            raise ValueError("block_tables must have 2 dimensions")
-        _want("block_tables", block_tables, (S, block_tables.shape[1]), i32, dev)
-        _want("context_lens", context_lens, (S,), i32, dev)
+    qp = _want("q", q, shape, dt, dev)
+    op = _want("out", out, shape, dt, dev)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must have 2 dimensions")
+    maxb = block_tables.shape[1]
+    tp = _want("block_tables", block_tables, (S, maxb), torch.int32, dev)
+    lp = _want("context_lens", context_lens, (S,), torch.int32, dev)
     pools = _want_pools(pool, dev, k_pool, v_pool, kv)
     if pool.is_b8:
         pools = pools[:1]
-    _launch(name, dev, stream, pool.handle, out.data_ptr(), q.data_ptr(), *pools,
-            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), S, hq,
-            float(scale), window, sinks, _want_status(status, dev))
+    _launch(name, dev, stream, pool.handle, op, qp, *pools, tp, maxb, lp, S, hq, float(scale),
+            window, sinks, _want_status(status, dev))
     return out
 
 
@@ -1004,6 +1035,17 @@ def paged_prefill_attention_window(pool: KVPool, q, block_tables, query_start, c
     if pool.record_bytes:
         raise ValueError("paged_prefill_attention_window takes a 16-bit pool")
     window, sinks = _window(window, sinks)
+    if out is None:
+        out = torch.empty_like(q)
+    if _fast is not None:
+        rc = _fast.prefill(pool._meta, q, out, block_tables, query_start, context_lens, float(scale),
+                           window, sinks, workspace, status,
+                           pool.k_pool if k_pool is None else k_pool,
+                           pool.v_pool if v_pool is None else v_pool, _raw(stream))
+        if rc is not None:
+            if rc:
+                check(rc, "paged_prefill_attention_window")
+            return out
     dev, dt, D = q.get_device(), _row_dtype(pool), pool.head_dim
     if q.dim() != 3 or q.shape[2] != D:
         raise ValueError(f"q must be [n][h][{D}], got {list(q.shape)}")
@@ -1012,8 +1054,6 @@ def paged_prefill_attention_window(pool: KVPool, q, block_tables, query_start, c
         raise ValueError(f"q has {hq} heads, not a multiple of the pool's "
                          f"{pool.num_kv_heads} kv heads")
     qp = _want("q", q, shape, dt, dev)
-    if out is None:
-        out = torch.empty(shape, dtype=dt, device=q.device)
     op = _want("out", out, shape, dt, dev)
     if block_tables.dim() != 2:
         raise ValueError("block_tables must have 2 dimensions")

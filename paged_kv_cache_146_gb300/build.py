@@ -2,15 +2,18 @@
 
 Usage: ``python -m paged_kv_cache_146_gb300.build`` (or ``__graft_entry__.build()``).
 Each translation unit compiles in parallel; the shared library links the CUDA
-runtime statically, so it only needs the driver at run time.
+runtime statically, so it only needs the driver at run time.  _fastcall.so beside
+it holds the binding's compiled argument checks.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
+FASTCALL = os.path.join(PKG, "_fastcall.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["ledger.cpp", "cache_write.cu", "paged_decode.cu", "paged_decode_q8.cu",
@@ -48,6 +52,30 @@ def _compile(src: str, verbose: bool, build_dir: str = BUILD, defines=()) -> str
     return obj
 
 
+def _build_fastcall() -> None:
+    """_fastcall.so: the compiled argument checks, against torch's and Python's headers.
+    Where those are not installed none is built, and the binding's own checks serve."""
+    spec = importlib.util.find_spec("torch")
+    python = sysconfig.get_paths()["include"]
+    torch = spec.submodule_search_locations[0] if spec is not None else ""
+    if not (os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so"))
+            and os.path.exists(os.path.join(python, "Python.h"))):
+        return
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = FASTCALL + ".tmp"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-I", INCLUDE,
+           "-isystem", os.path.join(torch, "include"),
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-isystem", python,
+           "-isystem", os.path.join(cuda, "include"),
+           os.path.join(CSRC, "fastcall.cpp"), "-o", tmp, "-L", os.path.join(torch, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on fastcall.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, FASTCALL)
+
+
 def build(verbose: bool = False, checked: bool = False, out: str | None = None) -> str:
     """Build the library.  ``checked=True`` compiles the kernels' bounds and
     alignment checks in (-DPKV_DEBUG_CHECKS) into ``out`` (a separate file)."""
@@ -55,8 +83,11 @@ def build(verbose: bool = False, checked: bool = False, out: str | None = None) 
     build_dir = BUILD + ("_checked" if checked else "")
     defines = ("PKV_DEBUG_CHECKS",) if checked else ()
     os.makedirs(build_dir, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        fast = None if checked or out else ex.submit(_build_fastcall)
         objs = list(ex.map(lambda s: _compile(s, verbose, build_dir, defines), SOURCES))
+        if fast is not None:
+            fast.result()
     tmp = lib + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
