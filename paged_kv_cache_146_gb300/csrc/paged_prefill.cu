@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(1024) prefill_prep_kernel(Params p, int32_t he
     __shared__ int carry;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     griddep_launch_dependents();
+    griddep_wait();                // a launch may overlap the end of the kernel before it
     if (tid == 0) carry = 0;
     if (p.v_emax)       // the staging kernels that follow take maxima into these
         for (int i = tid; i < p.num_seqs * p.num_kv_heads; i += 1024) p.v_emax[i] = 0;
@@ -758,10 +759,14 @@ __global__ void __launch_bounds__(kThreads)
                 uint64_t lsum2 = pack2f(0.f, 0.f);
                 // two copies of the loop: only a tile that crosses the row's
                 // position pays for the per-key causal test
-                auto weights = [&](auto masked) {
+                auto weights = [&](auto masked, auto wide) {
 #pragma unroll
                     for (int c = 0; c < kKeys; c += 2) {
-                        const float2 e = unpack2f(fma2f(pack2f(x[c], x[c + 1]), sc2, nm2));
+                        const float2 e =
+                            decltype(wide)::value
+                                ? make_float2(__fsub_rn(__fmul_rn(x[c], p.scale_log2), m_sub),
+                                              __fsub_rn(__fmul_rn(x[c + 1], p.scale_log2), m_sub))
+                                : unpack2f(fma2f(pack2f(x[c], x[c + 1]), sc2, nm2));
                         float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
                         if constexpr (decltype(masked)::value) {
                             if (k0 + c > pos) p0 = 0.f;
@@ -775,8 +780,20 @@ __global__ void __launch_bounds__(kThreads)
                             hi[c / 2] = Elem<false>::pack(p0, p1);
                     }
                 };
-                if (!WINDOW && cross) weights(std::true_type{});
-                else weights(std::false_type{});
+                if constexpr (WINDOW) {
+                    // the reference is a rounded product: against it, the unrounded
+                    // products of the fused form come out up to half its spacing too
+                    // large or too small, the same for the whole row, which cancels;
+                    // from 2^25 on that is 2 or more and grows past the range of the
+                    // weights, so there the products are rounded alike, by scalar
+                    // operations that stay apart (the largest weight is then exactly 1)
+                    if (__any_sync(kFull, fabsf(m_sub) > 0x1p24f))
+                        weights(std::false_type{}, std::true_type{});
+                    else weights(std::false_type{}, std::false_type{});
+                } else {
+                    if (cross) weights(std::true_type{}, std::false_type{});
+                    else weights(std::false_type{}, std::false_type{});
+                }
                 const float2 ls = unpack2f(lsum2);
                 l = l * f + (ls.x + ls.y);
                 // O is rescaled before P V of this tile, once P V of the previous
@@ -1825,8 +1842,17 @@ static int prefill_call(const pkv_pool *pool, void *out, const void *q, const vo
     const int64_t upper = prm.max_items * g.num_kv_heads;
     if (grid > upper) grid = upper;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    prefill_prep_kernel<<<1, 1024, 0, st>>>(prm, g.head_dim);
-    if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t pcfg = {};
+    pcfg.gridDim = dim3(1);
+    pcfg.blockDim = dim3(1024);
+    pcfg.stream = st;
+    pcfg.attrs = pdl;
+    pcfg.numAttrs = window > 0 ? 1 : 0;
+    if (cudaLaunchKernelEx(&pcfg, prefill_prep_kernel, prm, (int32_t)g.head_dim) != cudaSuccess)
+        return PKV_ERR_CUDA;
     if (staged) {       // exponent maxima, then the fp16 copy of V
         const int64_t units = (int64_t)num_seqs * g.num_kv_heads *
                               ((max_blocks_per_seq * pkv::kBlock + kStageTokens - 1) / kStageTokens);
@@ -1841,9 +1867,6 @@ static int prefill_call(const pkv_pool *pool, void *out, const void *q, const vo
         }
         if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
     }
-    cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kp.threads);

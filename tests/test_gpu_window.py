@@ -7,7 +7,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
-from paged_kv_cache_146_gb300 import (DEV_BAD_BLOCK, DEV_BAD_LEN, KVPool, cache_write_rope,  # noqa: E402
+from paged_kv_cache_146_gb300 import (DEV_BAD_BLOCK, DEV_BAD_LEN, KVPool, cache_write_b8, cache_write_rope,  # noqa: E402
                                       dequantize_blocks, paged_decode_attention_b8,
                                       paged_decode_attention_window, paged_prefill_attention,
                                       paged_prefill_attention_window, prefill_workspace_bytes,
@@ -328,3 +328,69 @@ def test_append_then_attend(kind):
                     w = torch.softmax((kk @ qd[row, h]) * scale_of(dim), 0)
                     bound = bound + 2 * np.expm1(2 * dx) / 2 * (w @ vv.abs()) + ev * np.exp(2 * dx) + half * (w @ vv.abs()) * (2 if eight else 0)
                     assert_within(out[row, h], want, bound, f"step {step} row {row} head {h}")
+
+
+@pytest.mark.parametrize("exponent", [0, 8, 15, 45])
+@pytest.mark.parametrize("kind", ["bf16", "f16", "b8_bf16", "b8_f16"])
+def test_large_scores(kind, exponent):
+    """Scores of 2^16 to 2^64, exact in fp32 and far apart: only the largest visible
+    keys count.  Prefill takes every key of a row against one reference, so those count
+    alike and the row is the mean of their V; its roundings: a weight's on its way into
+    P V (the sum takes it unrounded), the sum and the quotient in fp32 (2^-20 leaves
+    room) and the result's own, half a step.  Decode's reference moves
+    from block to block and the scale's product is rounded when it does: a weight is off
+    by a factor of up to 2^(|score| 2^-23), so equal scores of 2^18 count alike to 2 % and
+    the largest ones in any proportion, where the row is some mean of their V."""
+    dtype = kind.split("_")[-1]
+    if exponent > 15 and dtype == "f16":
+        exponent, unit = 15, 2.0 ** 10           # fp16 ends at 2^16
+    else:
+        unit = 2.0 ** 12
+    hkv, hq, dim, n, window, sinks, chunk = 2, 4, 64, 300, 90, 3, 150
+    gen = torch.Generator().manual_seed(exponent)
+    tables, nb = random_case(gen, [n], hkv, 20)
+    level = torch.randint(1, 6, (nb, hkv, 16, 1), generator=gen).double()
+    k = (level * unit).expand(nb, hkv, 16, dim).to(DT[dtype])
+    v = torch.randn((nb, hkv, 16, dim), generator=gen).to(DT[dtype])
+    q = torch.full((chunk, hq, dim), 2.0 ** exponent).to(DT[dtype])
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    status = new_status()
+    pool = KVPool(nb, hkv, dim, kind, device="cuda")
+    if pool.is_b8:
+        slots = torch.arange(nb * 16, device="cuda")
+        cache_write_b8(pool, *(t.permute(0, 2, 1, 3).reshape(-1, hkv, dim).contiguous().cuda()
+                               for t in (k, v)), slots, status)
+        kb, vb = torch.empty((2, nb, hkv, 16, dim), dtype=DT[dtype], device="cuda")
+        dequantize_blocks(pool, torch.arange(nb, dtype=torch.int32, device="cuda"), kb, vb, status)
+        outs = [(n - 1, paged_decode_attention_b8(pool, q[:1].cuda(), tables.cuda(), lens, 0.125, status,
+                                                  window=window, sinks=sinks)[0])]
+        v = vb.cpu()
+    else:
+        pool.k_pool.copy_(k)
+        pool.v_pool.copy_(v)
+        out = paged_decode_attention_window(pool, q[:1].cuda(), tables.cuda(), lens, 0.125, window, sinks,
+                                            status)
+        ws = torch.empty(prefill_workspace_bytes(1, chunk, hq, hkv), dtype=torch.uint8, device="cuda")
+        start = torch.tensor([0, chunk], dtype=torch.int32, device="cuda")
+        rows = paged_prefill_attention_window(pool, q.cuda(), tables.cuda(), start, lens, 0.125, window,
+                                              sinks, ws, status)
+        outs = [(n - 1, out[0])] + [(n - chunk + i, rows[i]) for i in range(chunk)]
+    assert status_check(status) == (0, 0)
+    for pos, got in outs:
+        j = torch.tensor(visible(n, pos, window, sinks))
+        blk, off = tables[0].long()[j // 16], j % 16
+        for h in range(hq):
+            lv = level[blk, h // 2, off, 0]
+            top = lv == lv.max()
+            vv = v[blk, h // 2, off].double()
+            half = torch.finfo(DT[dtype]).eps / 2
+            if got is outs[0][1]:        # decode: any mix of the largest
+                lo, hi = vv[top].min(0).values, vv[top].max(0).values
+                # the result's rounding and, of an 8-bit pool's V, the read-back's: half a step each
+                room = 2 * half * (1 + half) * vv[top].abs().max(0).values + 1e-6
+                g = got[h].double().cpu()
+                assert ((g >= lo - room) & (g <= hi + room)).all(), (pos, h)
+            else:
+                want = vv[top].mean(0)
+                room = half * want.abs() + (PREFILL_WEIGHT[dtype] + 2.0 ** -20) * vv[top].abs().max(0).values
+                assert ((got[h].double().cpu() - want).abs() <= room).all(), (pos, h)
