@@ -46,6 +46,39 @@ struct Params {
                                          // rotate queries
 };
 
+// Every kernel here is launched with the programmatic attribute: it may be set up
+// while the kernel before it in the stream ends, lets the next one do the same, and
+// waits for the end of the one before it ahead of its first access to memory.
+// Arrays that earlier kernels may have written are read by plain loads, or through a
+// pointer that passed here: neither moves above the wait.
+__device__ __forceinline__ void begin()
+{
+    griddep_launch_dependents();
+    griddep_wait();
+}
+
+template <typename T>
+__device__ __forceinline__ void after_wait(T *&pointer)
+{
+    asm volatile("" : "+l"(pointer));
+}
+
+template <typename... P, typename... A>
+static int launch(void (*fn)(P...), int64_t grid, int threads, int smem, cudaStream_t st, const A &...args)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
 // A lane works on two 8-value chunks of a row.  Chunk pair i of the row: for
 // the halves form the pairs' two sides (i and i + rotary_dim / 16) while i
 // falls inside the rotated part, else two neighbouring chunks.
@@ -147,8 +180,8 @@ __device__ __forceinline__ void append_rows(const Params &p, int D, int heads_kv
                         ? static_cast<const uint16_t *>(p.k) + t * p.k_stride + (int64_t)h * D
                         : static_cast<const uint16_t *>(p.v) + t * p.v_stride +
                               (int64_t)(h - heads_kv) * D;
-            u.slot = __ldg(p.slots + t);
-            u.pos = __ldg(p.positions + t);
+            u.slot = p.slots[t];
+            u.pos = p.positions[t];
             u.w0 = reinterpret_cast<const uint4 *>(u.row)[cp.c0];
             u.w1 = reinterpret_cast<const uint4 *>(u.row)[cp.c1];
         }
@@ -201,8 +234,10 @@ __device__ __forceinline__ void append_rows(const Params &p, int D, int heads_kv
 }
 
 template <bool BF16, bool NEIGHBOURS>
-__global__ void __launch_bounds__(256) append_rope_kernel(const Params p, int D, int heads_kv)
+__global__ void __launch_bounds__(256) append_rope_kernel(Params p, int D, int heads_kv)
 {
+    begin();
+    after_wait(p.cos_sin);
     append_rows<BF16, NEIGHBOURS>(p, D, heads_kv, blockIdx.x, gridDim.x);
 }
 
@@ -319,7 +354,7 @@ __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, i
             w[k][0] = in ? row[cp.c0] : make_uint4(0u, 0u, 0u, 0u);
             w[k][1] = in ? row[cp.c1] : make_uint4(0u, 0u, 0u, 0u);
         }
-        pos[k] = !in ? -1 : !p.positions ? 0 : SHARED ? positions[j] : __ldg(positions + t0 + j);
+        pos[k] = !in ? -1 : !p.positions ? 0 : positions[(SHARED ? 0 : t0) + j];
     }
     if constexpr (SHARED) asm volatile("cp.async.wait_all;" ::: "memory");
     auto values = [&](int k, float (&x)[16]) {
@@ -415,7 +450,7 @@ __device__ __forceinline__ Runs find_runs(const Params &p, int64_t tb, int span,
 {
     Runs r;
     const int64_t t = tb - 1 + lane;
-    r.slot = t >= 0 && t < p.num_tokens ? __ldg(p.slots + t) : -1;
+    r.slot = t >= 0 && t < p.num_tokens ? p.slots[t] : -1;
     const int64_t prev = __shfl_up_sync(kFull, r.slot, 1);
     const bool valid = r.slot >= 0 && r.slot < p.num_slots;
     const unsigned mine = span == 16 ? 0x1fffeu : 0x2u;
@@ -431,8 +466,10 @@ __device__ __forceinline__ Runs find_runs(const Params &p, int64_t tb, int span,
 // Few tokens: a warp takes one token, one kv head and K or V, and writes the run
 // that begins there, if one does.
 template <bool BF16, bool NEIGHBOURS, int D>
-__global__ void __launch_bounds__(128, 6) append_b8_kernel(const Params p)
+__global__ void __launch_bounds__(128, 6) append_b8_kernel(Params p)
 {
+    begin();
+    after_wait(p.cos_sin);
     if ((int)blockIdx.x >= p.write_blocks) {              // queries only
         append_rows<BF16, NEIGHBOURS>(p, D, 0, (int)blockIdx.x - p.write_blocks,
                                       (int)gridDim.x - p.write_blocks);
@@ -461,7 +498,7 @@ constexpr int kSpanWarps = 8;
 constexpr int kSpanTokens = 31;
 
 template <bool BF16, bool NEIGHBOURS, int D>
-__global__ void __launch_bounds__(32 * kSpanWarps, 4) append_b8_span_kernel(const Params p)
+__global__ void __launch_bounds__(32 * kSpanWarps, 4) append_b8_span_kernel(Params p)
 {
     constexpr int kStride = D + 4;                        // floats of a staged table row
     extern __shared__ uint4 stages[];                     // [warps][16 rows x D / 8]
@@ -469,6 +506,8 @@ __global__ void __launch_bounds__(32 * kSpanWarps, 4) append_b8_span_kernel(cons
     __shared__ int positions[kSpanTokens + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint4 *stage = stages + warp * 2 * D;
+    begin();
+    after_wait(p.cos_sin);
     const int64_t spans = ((int64_t)p.num_tokens + 15) / 16;
     for (int64_t w = blockIdx.x; w < spans; w += gridDim.x) {
         const int64_t tb = w * 16;
@@ -478,7 +517,7 @@ __global__ void __launch_bounds__(32 * kSpanWarps, 4) append_b8_span_kernel(cons
             const int per_row = p.rotary_dim / 4;
             for (int e = threadIdx.x; e < n * per_row; e += 32 * kSpanWarps) {
                 const int t = e / per_row, c = e - t * per_row;
-                const int pos = __ldg(p.positions + tb + t);
+                const int pos = p.positions[tb + t];
                 if (c == 0) positions[t] = pos;
                 if (pos >= 0 && pos < p.max_positions)
                     *reinterpret_cast<float4 *>(table + t * kStride + 4 * c) = __ldg(
@@ -507,10 +546,12 @@ __global__ void __launch_bounds__(32 * kSpanWarps, 4) append_b8_span_kernel(cons
 // stores).
 template <bool BF16, int D>
 __global__ void __launch_bounds__(256)
-    dequantize_kernel(const uint8_t *__restrict__ kv, const int32_t *__restrict__ ids, int32_t n,
-                      int32_t num_kv_heads, int32_t num_blocks, uint4 *__restrict__ k_out,
-                      uint4 *__restrict__ v_out, int32_t *__restrict__ status)
+    dequantize_kernel(const uint8_t *kv, const int32_t *ids, int32_t n, int32_t num_kv_heads,
+                      int32_t num_blocks, uint4 *k_out, uint4 *v_out, int32_t *status)
 {
+    begin();
+    after_wait(kv);
+    after_wait(ids);
     constexpr int kChunks = D;                            // chunks of K (or V) of a record
     const uint32_t per_block = (uint32_t)num_kv_heads * kChunks;
     const int64_t total = (int64_t)n * per_block;
@@ -556,8 +597,7 @@ static int launch_rows(const Params &p, int D, int heads_kv, cudaStream_t st)
 {
     const int64_t threads = (int64_t)p.num_tokens * (p.num_q_heads + 2 * heads_kv) * (D / 16);
     const int64_t grid = std::min<int64_t>((threads + 511) / 512, 152 * 64);   // two units a thread
-    append_rope_kernel<BF16, NEIGHBOURS><<<(unsigned)grid, 256, 0, st>>>(p, D, heads_kv);
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return launch(&append_rope_kernel<BF16, NEIGHBOURS>, grid, 256, 0, st, p, D, heads_kv);
 }
 
 template <bool BF16, bool NEIGHBOURS>
@@ -570,7 +610,7 @@ static int launch_b8(const Params &p0, int D, bool queries, cudaStream_t st)
             const int rc = launch_rows<BF16, NEIGHBOURS>(p, D, 0, st);
             if (rc != PKV_OK) return rc;
         }
-        const unsigned grid = (unsigned)std::min<int64_t>(spans, 152 * 64);
+        const int64_t grid = std::min<int64_t>(spans, 152 * 64);
         const int smem = kSpanWarps * 32 * D;
         void (*fn)(Params) = D == 128 ? &append_b8_span_kernel<BF16, NEIGHBOURS, 128>
                                       : &append_b8_span_kernel<BF16, NEIGHBOURS, 64>;
@@ -578,8 +618,7 @@ static int launch_b8(const Params &p0, int D, bool queries, cudaStream_t st)
         if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
             return PKV_ERR_CUDA;
-        fn<<<grid, 32 * kSpanWarps, smem, st>>>(p);
-        return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+        return launch(fn, grid, 32 * kSpanWarps, smem, st, p);
     }
     const int64_t units = (int64_t)p.num_tokens * 2 * p.num_kv_heads;
     p.write_blocks = (int32_t)std::min<int64_t>((units + 3) / 4, 152 * 64);
@@ -588,9 +627,9 @@ static int launch_b8(const Params &p0, int D, bool queries, cudaStream_t st)
         const int64_t threads = (int64_t)p.num_tokens * p.num_q_heads * (D / 16);
         grid += std::min<int64_t>((threads + 255) / 256, 152 * 64);
     }
-    if (D == 128) append_b8_kernel<BF16, NEIGHBOURS, 128><<<(unsigned)grid, 128, 0, st>>>(p);
-    else append_b8_kernel<BF16, NEIGHBOURS, 64><<<(unsigned)grid, 128, 0, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return launch(D == 128 ? &append_b8_kernel<BF16, NEIGHBOURS, 128>
+                           : &append_b8_kernel<BF16, NEIGHBOURS, 64>,
+                  grid, 128, 0, st, p);
 }
 
 static int32_t log2_or_none(int32_t x)
@@ -722,17 +761,11 @@ extern "C" int kv_dequantize_blocks(const pkv_pool *pool, const int32_t *ids, in
         ((uintptr_t)ids & 3u) || ((uintptr_t)d_status & 3u))
         return PKV_ERR_INVALID_ARG;
     const int64_t total = (int64_t)n * g.num_kv_heads * g.head_dim;
-    const unsigned grid = (unsigned)std::min<int64_t>((total + 255) / 256, 152 * 64);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int64_t grid = std::min<int64_t>((total + 255) / 256, 152 * 64);
     const bool bf = g.dtype == PKV_B8_BF16;
-    const uint8_t *kv = static_cast<const uint8_t *>(kv_b8);
-    uint4 *ko = static_cast<uint4 *>(k_out), *vo = static_cast<uint4 *>(v_out);
-    if (g.head_dim == 128) {
-        if (bf) dequantize_kernel<true, 128><<<grid, 256, 0, st>>>(kv, ids, n, g.num_kv_heads, g.num_blocks, ko, vo, d_status);
-        else dequantize_kernel<false, 128><<<grid, 256, 0, st>>>(kv, ids, n, g.num_kv_heads, g.num_blocks, ko, vo, d_status);
-    } else {
-        if (bf) dequantize_kernel<true, 64><<<grid, 256, 0, st>>>(kv, ids, n, g.num_kv_heads, g.num_blocks, ko, vo, d_status);
-        else dequantize_kernel<false, 64><<<grid, 256, 0, st>>>(kv, ids, n, g.num_kv_heads, g.num_blocks, ko, vo, d_status);
-    }
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    auto fn = g.head_dim == 128 ? (bf ? &dequantize_kernel<true, 128> : &dequantize_kernel<false, 128>)
+                                : (bf ? &dequantize_kernel<true, 64> : &dequantize_kernel<false, 64>);
+    return launch(fn, grid, 256, 0, static_cast<cudaStream_t>(stream),
+                  static_cast<const uint8_t *>(kv_b8), ids, n, g.num_kv_heads, g.num_blocks,
+                  static_cast<uint4 *>(k_out), static_cast<uint4 *>(v_out), d_status);
 }

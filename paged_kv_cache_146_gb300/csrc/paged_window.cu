@@ -587,7 +587,7 @@ __device__ __forceinline__ int longest_first(const Params &p, int k)
     __shared__ int warp_hits[THREADS / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto class_of = [&](int s) {
-        const int L = __ldg(p.context_lens + s);
+        const int L = p.context_lens[s];
         const int n = L < 0 || (int64_t)L > (int64_t)p.max_blocks_per_seq * kBlock
                           ? 0
                           : visible(L, p.window, p.sinks).n;
@@ -655,6 +655,10 @@ __global__ void __launch_bounds__(32 * W, Shape<D, B8, NT, W>::kMinBlocks)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncwarp();
+    // a launch may overlap the end of the kernel before it: nothing of the call is
+    // read above the wait (and by plain loads below it, which do not move above)
+    griddep_launch_dependents();
+    griddep_wait();
 
     const int C = p.ctas;
     const int64_t pair = blockIdx.x / C;
@@ -663,7 +667,7 @@ __global__ void __launch_bounds__(32 * W, Shape<D, B8, NT, W>::kMinBlocks)
     const int g = (int)(pair - (int64_t)s * p.num_kv_heads);
     if (p.most > 0) s = longest_first<32 * W>(p, s);
     const int G = p.group;
-    int L = __ldg(p.context_lens + s);
+    int L = p.context_lens[s];
     if (L < 0 || (int64_t)L > (int64_t)p.max_blocks_per_seq * kBlock) {
         if (threadIdx.x == 0) atomicOr(p.status, PKV_DEV_BAD_LEN);
         L = 0;
@@ -674,7 +678,7 @@ __global__ void __launch_bounds__(32 * W, Shape<D, B8, NT, W>::kMinBlocks)
     const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
     auto load_ids = [&](int i0) {
         const int i = i0 + lane;
-        return i < count ? __ldg(row + vis.block(gw + i * stride)) : 0;
+        return i < count ? row[vis.block(gw + i * stride)] : 0;
     };
     // bit l: the warp's block i0 + l holds hidden tokens
     auto edges_from = [&](int i0) {
@@ -1039,17 +1043,19 @@ static int launch(const pkv_pool *pool, bool want_b8, void *out, const void *q, 
     // whose many waves even out by themselves)
     p.most = pairs * C > lim.resident && most == maxb && most >= 64 && num_seqs <= 512 ? (int)most : 0;
     if (pairs * C > INT32_MAX) return PKV_ERR_UNSUPPORTED;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)C;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pairs * C));
     cfg.blockDim = dim3(32u * (unsigned)v.warps);
     cfg.dynamicSmemBytes = (size_t)v.smem;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = C > 1 ? 1 : 0;
+    cfg.numAttrs = C > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, v.fn, tk, tv, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
