@@ -394,3 +394,34 @@ def test_large_scores(kind, exponent):
                 want = vv[top].mean(0)
                 room = half * want.abs() + (PREFILL_WEIGHT[dtype] + 2.0 ** -20) * vv[top].abs().max(0).values
                 assert ((got[h].double().cpu() - want).abs() <= room).all(), (pos, h)
+
+
+@pytest.mark.parametrize("n", [1, 31, 32, 33, 70])
+def test_prefill_numbers_of_sequences(n):
+    """Around the number of sequences up to which each CTA lists the items for itself;
+    a third of them without a row, every seventh with a length that does not fit."""
+    gen = torch.Generator().manual_seed(n)
+    chunks = [0 if i % 3 == 1 else 1 + (37 * i) % 90 for i in range(n)]
+    lens = [c + (i * 29) % 200 for i, c in enumerate(chunks)]
+    bad = [i for i in range(n) if i % 7 == 3]
+    first = [a - c for a, c in zip(lens, chunks)]
+    pool, k, v, tables, gen = build(lens, first, 2, 64, "bf16", 60, 3, n)
+    T = sum(chunks) + 5                                  # rows behind the last sequence
+    q = torch.randn((T, 8, 64), generator=gen).to(torch.bfloat16)
+    start = torch.tensor([0] + list(np.cumsum(chunks)), dtype=torch.int32)
+    given = torch.tensor([(-1 if i % 2 else chunks[i] - 1) if i in bad else lens[i] for i in range(n)],
+                         dtype=torch.int32)
+    ws = torch.empty(prefill_workspace_bytes(n, T, 8, 2), dtype=torch.uint8, device="cuda")
+    status = new_status()
+    out = torch.full((T, 8, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    paged_prefill_attention_window(pool, q.cuda(), tables.cuda(), start.cuda(), given.cuda(), scale_of(64),
+                                   60, 3, ws, status, out=out)
+    assert status_check(status)[1] == (DEV_BAD_LEN if bad else 0)
+    assert bool((out[T - 5:] == 7).all())
+    rows = []
+    for s, c in enumerate(chunks):
+        if s in bad:
+            assert not bool(out[start[s]:start[s + 1]].any())
+        elif c:
+            rows += [(int(start[s]) + i, s, first[s] + i) for i in {0, c // 2, c - 1}]
+    expect(q, k, v, tables, lens, first, rows, 60, 3, "bf16", PREFILL_WEIGHT["bf16"], out)
