@@ -44,6 +44,7 @@ struct Params {
     int32_t *status;
     int32_t write_blocks;                // 8-bit write of few tokens: CTAs that write; the rest
                                          // rotate queries
+    uint64_t minus_zeros;                // see mul2
 };
 
 // Every kernel here is launched with the programmatic attribute: it may be set up
@@ -122,9 +123,8 @@ __device__ __forceinline__ void turn(float &a, float &b, float c, float s)
     b = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
 }
 
-// Rotate the 16 values of chunk pair i in place; cs = the position's table row,
-// in global or (SHARED) shared memory.
-template <bool NEIGHBOURS, bool SHARED = false>
+// Rotate the 16 values of chunk pair i in place; cs = the position's table row.
+template <bool NEIGHBOURS>
 __device__ __forceinline__ void rotate16(float (&x)[16], int i, int half, const float *cs)
 {
     // halves: values e and 8 + e are angle 8i + e; neighbours: values 2e and
@@ -132,8 +132,7 @@ __device__ __forceinline__ void rotate16(float (&x)[16], int i, int half, const 
     // entries 8i .. 8i + 7
     const float4 *c4 = reinterpret_cast<const float4 *>(cs + 8 * i);
     const float4 *s4 = reinterpret_cast<const float4 *>(cs + half + 8 * i);
-    const float4 ca = SHARED ? c4[0] : __ldg(c4), cb = SHARED ? c4[1] : __ldg(c4 + 1);
-    const float4 sa = SHARED ? s4[0] : __ldg(s4), sb = SHARED ? s4[1] : __ldg(s4 + 1);
+    const float4 ca = __ldg(c4), cb = __ldg(c4 + 1), sa = __ldg(s4), sb = __ldg(s4 + 1);
     const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
     const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
 #pragma unroll
@@ -254,6 +253,69 @@ __device__ __forceinline__ int b8_chunk(int t, int j, int D)
 // reciprocal scale would leave the fp32 range.
 constexpr float kB8Tiny = 0x1p-100f;
 
+constexpr uint64_t kMinusZeros = 0x8000000080000000ull;
+
+// The 8-bit append works on pairs of fp32 values in packed operations, half as many
+// instructions.  A product and a sum are rounded each by itself; the compiler joins a
+// packed product with the sum it feeds, so the product is written as a fused one whose
+// addend, -0, it does not know: x y + (-0) is x y rounded once, signed zeros included.
+__device__ __forceinline__ uint64_t mul2(const Params &p, uint64_t a, uint64_t b)
+{
+    return fma2f(a, b, p.minus_zeros);
+}
+
+// The 16 values of a chunk pair so that (a, b) are the pairs that a rotation turns.
+// halves: a = the first chunk's values in order, b = the second's; neighbours: a = the
+// even values of both chunks, b = the odd ones.  Entry m turns by angles 8i + 2m, + 1.
+struct Values {
+    uint64_t a[4], b[4];
+};
+
+template <bool BF16, bool NEIGHBOURS>
+__device__ __forceinline__ Values unpack16(const uint4 &w0, const uint4 &w1)
+{
+    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    Values v;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const float2 f = Elem<BF16>::unpack(w[NEIGHBOURS ? 2 * m : m]);
+        const float2 g = Elem<BF16>::unpack(w[NEIGHBOURS ? 2 * m + 1 : 4 + m]);
+        v.a[m] = NEIGHBOURS ? pack2f(f.x, g.x) : pack2f(f.x, f.y);
+        v.b[m] = NEIGHBOURS ? pack2f(f.y, g.y) : pack2f(g.x, g.y);
+    }
+    return v;
+}
+
+template <bool SHARED>
+__device__ __forceinline__ void turn16(const Params &p, Values &v, int i, int half, const float *cs)
+{
+    const ulonglong2 *c2 = reinterpret_cast<const ulonglong2 *>(cs + 8 * i);
+    const ulonglong2 *s2 = reinterpret_cast<const ulonglong2 *>(cs + half + 8 * i);
+    const ulonglong2 ca = SHARED ? c2[0] : __ldg(c2), cb = SHARED ? c2[1] : __ldg(c2 + 1);
+    const ulonglong2 sa = SHARED ? s2[0] : __ldg(s2), sb = SHARED ? s2[1] : __ldg(s2 + 1);
+    const uint64_t c[4] = {ca.x, ca.y, cb.x, cb.y}, s[4] = {sa.x, sa.y, sb.x, sb.y};
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const uint64_t x = v.a[m], y = v.b[m];
+        v.a[m] = sub2f(mul2(p, x, c[m]), mul2(p, y, s[m]));
+        v.b[m] = add2f(mul2(p, y, c[m]), mul2(p, x, s[m]));
+    }
+}
+
+// The values of the two chunks in order.
+template <bool NEIGHBOURS>
+__device__ __forceinline__ void in_order(const Values &v, float (&x)[16])
+{
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const float2 a = unpack2f(v.a[m]), b = unpack2f(v.b[m]);
+        x[NEIGHBOURS ? 4 * m : 2 * m] = a.x;
+        x[NEIGHBOURS ? 4 * m + 2 : 2 * m + 1] = a.y;
+        x[NEIGHBOURS ? 4 * m + 1 : 8 + 2 * m] = b.x;
+        x[NEIGHBOURS ? 4 * m + 3 : 8 + 2 * m + 1] = b.y;
+    }
+}
+
 // Rounding to an integer, ties to even, of |x| <= 2^22: adding 1.5 * 2^23 puts
 // the sum where the fp32 spacing is 1; its low byte is the integer's.
 __device__ __forceinline__ uint32_t round_bits(float x)
@@ -261,29 +323,68 @@ __device__ __forceinline__ uint32_t round_bits(float x)
     return __float_as_uint(__fadd_rn(x, 12582912.0f));
 }
 
-// Four codes of x * inv as stored bytes (code + 128).  ODD: the block holds an
-// infinity or a NaN, so codes are clamped to [-127, 127] and NaN gives 0; all
-// other values are at most 127 (1 + 2^-22) in size and round inside the range.
-template <bool ODD>
-__device__ __forceinline__ uint32_t b8_codes4(const float *x, float inv)
+__device__ __forceinline__ uint32_t low_bytes(uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3)
 {
-    uint32_t b[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        float y = __fmul_rn(x[k], inv);
-        if (ODD) y = y == y ? fminf(fmaxf(y, -127.f), 127.f) : 0.f;
-        b[k] = round_bits(y);
-    }
-    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410) ^
-           0x80808080u;
+    return __byte_perm(__byte_perm(b0, b1, 0x0040), __byte_perm(b2, b3, 0x0040), 0x5410);
 }
 
-// The larger of a and |x|; NaN if either is.
-__device__ __forceinline__ float max_abs_nan(float a, float x)
+// Codes of 16 values times inv as stored bytes (code + 128, where the sum that rounds
+// puts the 128).  All values are at most 127 (1 + 2^-22) in size and round inside the
+// range; in a block that holds an infinity or a NaN (odd) codes are clamped to
+// [-127, 127] and NaN gives 0.
+template <bool NEIGHBOURS>
+__device__ __forceinline__ uint4 b8_codes16(const Params &p, const Values &v, float inv, bool odd)
 {
-    float m;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(fabsf(x)));
-    return m;
+    constexpr float kRound = 12582912.0f + 128.0f;
+    uint32_t b[16];
+    if (!odd) {
+        const uint64_t inv2 = pack2f(inv, inv), round2 = pack2f(kRound, kRound);
+        Values y;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            y.a[m] = add2f(mul2(p, v.a[m], inv2), round2);
+            y.b[m] = add2f(mul2(p, v.b[m], inv2), round2);
+        }
+        float x[16];
+        in_order<NEIGHBOURS>(y, x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) b[e] = __float_as_uint(x[e]);
+    } else {
+        float x[16];
+        in_order<NEIGHBOURS>(v, x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            float y = __fmul_rn(x[e], inv);
+            y = y == y ? fminf(fmaxf(y, -127.f), 127.f) : 0.f;
+            b[e] = __float_as_uint(__fadd_rn(y, kRound));
+        }
+    }
+    return make_uint4(low_bytes(b[0], b[1], b[2], b[3]), low_bytes(b[4], b[5], b[6], b[7]),
+                      low_bytes(b[8], b[9], b[10], b[11]), low_bytes(b[12], b[13], b[14], b[15]));
+}
+
+// The largest of a and the values' sizes; NaN if any is.
+__device__ __forceinline__ float max_abs_nan(float a, const Values &v)
+{
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const float2 x = unpack2f(v.a[m]), y = unpack2f(v.b[m]);
+        asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(a), "f"(x.x), "f"(x.y));
+        asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(a), "f"(y.x), "f"(y.y));
+    }
+    return a;
+}
+
+// The same of two chunks of 16-bit values, which need no unpacking for it: their bits
+// without the sign are ordered as their sizes are, infinity and NaN last.  a = such
+// bits, two to a word.
+__device__ __forceinline__ uint32_t max_abs_bits(uint32_t a, const uint4 &w0, const uint4 &w1)
+{
+    constexpr uint32_t kSize = 0x7fff7fffu;
+    a = __vimax3_u16x2(a, w0.x & kSize, w0.y & kSize);
+    a = __vimax3_u16x2(a, w0.z & kSize, w0.w & kSize);
+    a = __vimax3_u16x2(a, w1.x & kSize, w1.y & kSize);
+    return __vimax3_u16x2(a, w1.z & kSize, w1.w & kSize);
 }
 
 __device__ __forceinline__ void copy16(uint4 *dst, const uint4 *src)
@@ -322,9 +423,8 @@ __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, i
                                              const int *positions, const float *cos_sin, int cs_stride,
                                              uint4 *stage)
 {
-    // SHARED: positions and cos_sin hold the rows of tokens t0, t0 + 1, ... in
-    // shared memory, and the run's rows wait in `stage`; else these are the call's
-    // arrays, and the rows wait in registers
+    // the run's rows wait in `stage`.  SHARED: positions and cos_sin hold the rows of
+    // tokens t0, t0 + 1, ... in shared memory; else these are the call's arrays
     constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPasses = 16 / kRows;
     constexpr int kRecord = PKV_B8_RECORD_BYTES(D);
     uint8_t *rec = p.kv + (block * p.num_kv_heads + h) * kRecord;
@@ -338,34 +438,28 @@ __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, i
     const ChunkPair cp = rotate ? chunk_pair<NEIGHBOURS>(i, p.rotary_dim)
                                 : ChunkPair{2 * i, 2 * i + 1, false};
     const float old = off0 > 0 ? *scale_at : 0.f;
-    uint4 w[SHARED ? 1 : kPasses][2];
     int pos[kPasses];                    // -1: no row, or one to skip
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
         const int j = k * kRows + r;
         const bool in = j < n;
         const uint4 *row = reinterpret_cast<const uint4 *>(rows + (t0 + (in ? j : 0)) * stride);
-        if constexpr (SHARED) {          // a lane stages what it will read itself
-            if (in) {
-                copy16(stage + 64 * k + lane, row + cp.c0);
-                copy16(stage + 64 * k + 32 + lane, row + cp.c1);
-            }
-        } else {
-            w[k][0] = in ? row[cp.c0] : make_uint4(0u, 0u, 0u, 0u);
-            w[k][1] = in ? row[cp.c1] : make_uint4(0u, 0u, 0u, 0u);
+        if (in) {                        // a lane stages what it will read itself
+            copy16(stage + 64 * k + lane, row + cp.c0);
+            copy16(stage + 64 * k + 32 + lane, row + cp.c1);
         }
         pos[k] = !in ? -1 : !p.positions ? 0 : positions[(SHARED ? 0 : t0) + j];
     }
-    if constexpr (SHARED) asm volatile("cp.async.wait_all;" ::: "memory");
-    auto values = [&](int k, float (&x)[16]) {
-        unpack8<BF16>(SHARED ? stage[64 * k + lane] : w[SHARED ? 0 : k][0], x);
-        unpack8<BF16>(SHARED ? stage[64 * k + 32 + lane] : w[SHARED ? 0 : k][1], x + 8);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    auto values = [&](int k) {
+        Values v = unpack16<BF16, NEIGHBOURS>(stage[64 * k + lane], stage[64 * k + 32 + lane]);
         if (cp.turned)
-            rotate16<NEIGHBOURS, SHARED>(
-                x, i, p.rotary_dim >> 1,
-                cos_sin + (SHARED ? (int64_t)(k * kRows + r) : (int64_t)pos[k]) * cs_stride);
+            turn16<SHARED>(p, v, i, p.rotary_dim >> 1,
+                           cos_sin + (SHARED ? (int64_t)(k * kRows + r) : (int64_t)pos[k]) * cs_stride);
+        return v;
     };
     float amax = 0.f;
+    uint32_t bits = 0u;
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
         if (k * kRows >= n) break;       // the same for the whole warp
@@ -375,10 +469,12 @@ __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, i
             pos[k] = -1;
         }
         if (pos[k] < 0) continue;
-        float x[16];
-        values(k, x);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) amax = max_abs_nan(amax, x[e]);
+        if (rotate) amax = max_abs_nan(amax, values(k));
+        else bits = max_abs_bits(bits, stage[64 * k + lane], stage[64 * k + 32 + lane]);
+    }
+    if (!rotate) {
+        const float2 f = Elem<BF16>::unpack(bits);
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(amax) : "f"(f.x), "f"(f.y));
     }
     constexpr float kMax = 0x1.fep127f;                       // the largest bf16
     const bool odd = __any_sync(kFull, !(amax <= kMax));      // an infinity or a NaN
@@ -389,7 +485,7 @@ __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, i
             if (k * kRows >= n) break;
             if (pos[k] < 0) continue;
             float x[16];
-            values(k, x);
+            in_order<NEIGHBOURS>(values(k), x);
 #pragma unroll
             for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
         }
@@ -419,18 +515,11 @@ __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, i
         if (k * kRows >= n) break;
         if (pos[k] < 0) continue;
         const int t = off0 + k * kRows + r;
-        float x[16];
-        values(k, x);
-        uint2 lo, hi;
-        if (odd) {
-            lo = make_uint2(b8_codes4<true>(x, inv), b8_codes4<true>(x + 4, inv));
-            hi = make_uint2(b8_codes4<true>(x + 8, inv), b8_codes4<true>(x + 12, inv));
-        } else {
-            lo = make_uint2(b8_codes4<false>(x, inv), b8_codes4<false>(x + 4, inv));
-            hi = make_uint2(b8_codes4<false>(x + 8, inv), b8_codes4<false>(x + 12, inv));
-        }
-        *reinterpret_cast<uint2 *>(codes + b8_chunk(t, cp.c0 >> 1, D) + 8 * (cp.c0 & 1)) = lo;
-        *reinterpret_cast<uint2 *>(codes + b8_chunk(t, cp.c1 >> 1, D) + 8 * (cp.c1 & 1)) = hi;
+        const uint4 b = b8_codes16<NEIGHBOURS>(p, values(k), inv, odd);
+        *reinterpret_cast<uint2 *>(codes + b8_chunk(t, cp.c0 >> 1, D) + 8 * (cp.c0 & 1)) =
+            make_uint2(b.x, b.y);
+        *reinterpret_cast<uint2 *>(codes + b8_chunk(t, cp.c1 >> 1, D) + 8 * (cp.c1 & 1)) =
+            make_uint2(b.z, b.w);
     }
 }
 
@@ -475,7 +564,9 @@ __global__ void __launch_bounds__(128, 6) append_b8_kernel(Params p)
                                       (int)gridDim.x - p.write_blocks);
         return;
     }
+    __shared__ uint4 stages[4 * 2 * D];
     const int lane = threadIdx.x & 31;
+    uint4 *stage = stages + (threadIdx.x >> 5) * 2 * D;
     const int per_token = 2 * p.num_kv_heads;
     const int64_t units = (int64_t)p.num_tokens * per_token;
     for (int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); u < units;
@@ -487,7 +578,7 @@ __global__ void __launch_bounds__(128, 6) append_b8_kernel(Params p)
         const int64_t s0 = __shfl_sync(kFull, runs.slot, 1);
         b8_write_run<BF16, NEIGHBOURS, D, false>(p, rest & 1, rest >> 1, t, runs.length(1),
                                                  s0 / kBlock, (int)(s0 % kBlock), lane,
-                                                 p.positions, p.cos_sin, p.rotary_dim, nullptr);
+                                                 p.positions, p.cos_sin, p.rotary_dim, stage);
     }
 }
 
@@ -703,6 +794,7 @@ extern "C" int kv_cache_write_rope(const pkv_pool *pool, void *q_out, int64_t q_
     p.v_pool = static_cast<uint4 *>(v_pool);
     p.kv = static_cast<uint8_t *>(k_pool);
     p.status = d_status;
+    p.minus_zeros = kMinusZeros;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool bf = g.dtype == PKV_BF16 || g.dtype == PKV_B8_BF16, nb = interleaved != 0;
     if (b8) {
@@ -742,6 +834,7 @@ extern "C" int kv_cache_write_b8(const pkv_pool *pool, const void *k_new, const 
     p.num_slots = (int64_t)g.num_blocks * g.block_size;
     p.kv = static_cast<uint8_t *>(kv_b8);
     p.status = d_status;
+    p.minus_zeros = kMinusZeros;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return g.dtype == PKV_B8_BF16 ? launch_b8<true, false>(p, g.head_dim, false, st)
                                   : launch_b8<false, false>(p, g.head_dim, false, st);

@@ -289,43 +289,6 @@ __device__ __forceinline__ float min3f(float a, float b, float c)
     asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ __forceinline__ uint64_t pack2f(float a, float b)
-{
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-    return d;
-}
-__device__ __forceinline__ float2 unpack2f(uint64_t v)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2f(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2f(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul2f(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t sub2f(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // The n lowest of 64 bits (all for n >= 64, none for n <= 0).
 __device__ __forceinline__ uint64_t low_bits(int n)
 {
@@ -1026,16 +989,11 @@ __global__ void __launch_bounds__(kThreads)
 // Every wait is bounded; on expiry the kernel flags PKV_DEV_TIMEOUT and stops.
 namespace tcw {
 
-using tcp::add2f;
-using tcp::fma2f;
 using tcp::Item;
 using tcp::kGroups;
 using tcp::kRows;
 using tcp::max3f;
 using tcp::min3f;
-using tcp::mul2f;
-using tcp::pack2f;
-using tcp::unpack2f;
 
 constexpr int kKeys = 128;             // keys per KV tile (N of S = Q K^T)
 constexpr int kTileBlocks = kKeys / kBlock;
