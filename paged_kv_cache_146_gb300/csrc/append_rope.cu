@@ -65,13 +65,13 @@ __device__ __forceinline__ void after_wait(T *&pointer)
 }
 
 template <typename... P, typename... A>
-static int launch(void (*fn)(P...), int64_t grid, int threads, int smem, cudaStream_t st, const A &...args)
+static int launch(void (*fn)(P...), dim3 grid, int threads, int smem, cudaStream_t st, const A &...args)
 {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = st;
@@ -244,10 +244,12 @@ __global__ void __launch_bounds__(256) append_rope_kernel(Params p, int D, int h
 // Byte of 16-byte chunk j of token t inside a record's K (or V) codes (see the
 // layout in pagedkv.h): lines of 128 bytes, chunk positions rotated so that the
 // attention kernel's wide shared-memory reads of either operand touch all banks.
-__device__ __forceinline__ int b8_chunk(int t, int j, int D)
-{
-    return ((t * D) >> 7) * 128 + ((j ^ ((t & 1) << 2) ^ (((t >> 1) & 3) << 1)) << 4);
-}
+__device__ __forceinline__ int b8_line(int t, int D) { return ((t * D) >> 7) * 128; }
+__device__ __forceinline__ int b8_swizzle(int t) { return ((t & 1) << 6) ^ (((t >> 1) & 3) << 5); }
+__device__ __forceinline__ int b8_chunk(int t, int j, int D) { return b8_line(t, D) + ((j * 16) ^ b8_swizzle(t)); }
+
+// A table row staged in shared memory: this many floats apart beyond its own.
+constexpr int kTablePad = 4;
 
 // Values whose block maximum is below this store as zeros (scale 0): their
 // reciprocal scale would leave the fp32 range.
@@ -263,6 +265,11 @@ __device__ __forceinline__ uint64_t mul2(const Params &p, uint64_t a, uint64_t b
 {
     return fma2f(a, b, p.minus_zeros);
 }
+
+// A lane's two chunks of a row.
+struct Chunks {
+    uint4 w0, w1;
+};
 
 // The 16 values of a chunk pair so that (a, b) are the pairs that a rotation turns.
 // halves: a = the first chunk's values in order, b = the second's; neighbours: a = the
@@ -286,13 +293,23 @@ __device__ __forceinline__ Values unpack16(const uint4 &w0, const uint4 &w1)
     return v;
 }
 
+// cs = the position's table row, in global memory or (SHARED) staged: there the cosines'
+// float4s 0, 2, 4, ... come before 1, 3, 5, ..., the sines' likewise, so that
+// neighbouring lanes read neighbouring float4s (other banks).
+__device__ __forceinline__ int staged_at(int c, int half)     // place of a row's c-th float4
+{
+    const int quarter = half / 8, part = c >= 2 * quarter, e = c - 2 * quarter * part;
+    return 2 * quarter * part + (e & 1) * quarter + (e >> 1);
+}
+
 template <bool SHARED>
 __device__ __forceinline__ void turn16(const Params &p, Values &v, int i, int half, const float *cs)
 {
-    const ulonglong2 *c2 = reinterpret_cast<const ulonglong2 *>(cs + 8 * i);
-    const ulonglong2 *s2 = reinterpret_cast<const ulonglong2 *>(cs + half + 8 * i);
-    const ulonglong2 ca = SHARED ? c2[0] : __ldg(c2), cb = SHARED ? c2[1] : __ldg(c2 + 1);
-    const ulonglong2 sa = SHARED ? s2[0] : __ldg(s2), sb = SHARED ? s2[1] : __ldg(s2 + 1);
+    const ulonglong2 *c2 = reinterpret_cast<const ulonglong2 *>(cs) + (SHARED ? i : 2 * i);
+    const ulonglong2 *s2 = c2 + half / 4;
+    const int next = SHARED ? half / 8 : 1;
+    const ulonglong2 ca = SHARED ? c2[0] : __ldg(c2), cb = SHARED ? c2[next] : __ldg(c2 + 1);
+    const ulonglong2 sa = SHARED ? s2[0] : __ldg(s2), sb = SHARED ? s2[next] : __ldg(s2 + 1);
     const uint64_t c[4] = {ca.x, ca.y, cb.x, cb.y}, s[4] = {sa.x, sa.y, sb.x, sb.y};
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -375,16 +392,24 @@ __device__ __forceinline__ float max_abs_nan(float a, const Values &v)
     return a;
 }
 
-// The same of two chunks of 16-bit values, which need no unpacking for it: their bits
-// without the sign are ordered as their sizes are, infinity and NaN last.  a = such
-// bits, two to a word.
-__device__ __forceinline__ uint32_t max_abs_bits(uint32_t a, const uint4 &w0, const uint4 &w1)
+// The same of two chunks of 16-bit values, which need no unpacking for it.  a = two
+// such maxima; their signs mean nothing.
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_abs_nan16(uint32_t a, uint32_t b)
 {
-    constexpr uint32_t kSize = 0x7fff7fffu;
-    a = __vimax3_u16x2(a, w0.x & kSize, w0.y & kSize);
-    a = __vimax3_u16x2(a, w0.z & kSize, w0.w & kSize);
-    a = __vimax3_u16x2(a, w1.x & kSize, w1.y & kSize);
-    return __vimax3_u16x2(a, w1.z & kSize, w1.w & kSize);
+    uint32_t m;
+    if constexpr (BF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    else asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_abs_nan16(uint32_t a, const uint4 &w0, const uint4 &w1)
+{
+    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+    for (int m = 0; m < 8; ++m) a = max_abs_nan16<BF16>(a, w[m]);
+    return a;
 }
 
 __device__ __forceinline__ void copy16(uint4 *dst, const uint4 *src)
@@ -405,101 +430,95 @@ __device__ __forceinline__ uint32_t b8_rescale4(uint32_t w, float ratio)
            0x80808080u;
 }
 
-// Write K (part 0) or V (part 1) of one run of tokens t0 .. t0 + n - 1, whose
-// slots are off0, off0 + 1, ... of one block, by one warp.
+// One run of tokens t0 .. t0 + n - 1, whose slots are off0, off0 + 1, ... of one block,
+// for one kv head, as a warp writes it: a row is D / 16 lanes of 16 values, a pass
+// kRows rows.
+template <int D>
+struct Run {
+    static constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPasses = 16 / kRows;
+    int t0, n, off0, h;
+    int r, i;                            // the lane's row of a pass and its place in it
+    uint8_t *rec;
+    __device__ __forceinline__ Run(const Params &p, int t0_, int n_, int64_t slot, int h_, int lane)
+        : t0(t0_), n(n_), off0((int)slot & (kBlock - 1)), h(h_), r(lane / kLanes), i(lane % kLanes),
+          rec(p.kv + ((slot / kBlock) * p.num_kv_heads + h_) * PKV_B8_RECORD_BYTES(D))
+    {
+    }
+    // call f(pass, the row's two chunks) for the lane's rows
+    template <typename F>
+    __device__ __forceinline__ void rows(const void *base, int64_t stride, const ChunkPair &cp, F &&f) const
+    {
+        const uint16_t *at = static_cast<const uint16_t *>(base) + (t0 + r) * stride + h * D;
+#pragma unroll
+        for (int k = 0; k < kPasses; ++k, at += kRows * stride)
+            if (k * kRows + r < n)
+                f(k, reinterpret_cast<const uint4 *>(at) + cp.c0, reinterpret_cast<const uint4 *>(at) + cp.c1);
+    }
+};
+
+// Write K (part 0) or V (part 1) of a run.
 //   scale = max(scale before, amax * rn(1 / 127)),  code = rn(x * rn(1 / scale))
 // where "scale before" counts only when the run does not start the block (off0
 // > 0).  When the scale grows, the codes of tokens 0 .. off0 - 1 are rounded to
 // it: rn(code * rn(old / new)).
-// A row is D / 16 lanes of 16 values.  The run's rows wait, packed, between the
-// maximum and the codes (in registers for few tokens; many tokens stage them in
-// shared memory, which leaves registers for 32 warps an SM), so each value is read
-// once; K is rotated for both.  Measured on 20,500 tokens of 32 query and 8 kv
-// heads of 128: fp32 values kept in registers (154 of them), the queries in the
-// same launch: 176 us; packed in registers 59 (queries) + 49; staged 59 + 43.
-template <bool BF16, bool NEIGHBOURS, int D, bool SHARED>
-__device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, int64_t t0, int n,
-                                             int64_t block, int off0, int lane,
-                                             const int *positions, const float *cos_sin, int cs_stride,
-                                             uint4 *stage)
+// raw(k) gives the two chunks of the lane's row of pass k, turn(k, values) rotates them
+// (ROTATE), `keep` has the bits of the passes whose row is written.  A row stays packed
+// between the maximum and the codes and is rotated for both.
+template <bool BF16, bool NEIGHBOURS, bool ROTATE, int D, typename Raw, typename Turn>
+__device__ __forceinline__ void b8_write_part(const Params &p, const Run<D> &u, int part,
+                                              const ChunkPair &cp, uint32_t keep, int lane, Raw &&raw,
+                                              Turn &&turn)
 {
-    // the run's rows wait in `stage`.  SHARED: positions and cos_sin hold the rows of
-    // tokens t0, t0 + 1, ... in shared memory; else these are the call's arrays
-    constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPasses = 16 / kRows;
-    constexpr int kRecord = PKV_B8_RECORD_BYTES(D);
-    uint8_t *rec = p.kv + (block * p.num_kv_heads + h) * kRecord;
-    uint8_t *codes = rec + 16 * D * part;
-    float *scale_at = reinterpret_cast<float *>(rec + 32 * D) + part;
-    const int r = lane / kLanes, i = lane % kLanes;
-    const uint16_t *rows = part ? static_cast<const uint16_t *>(p.v) + (int64_t)h * D
-                                : static_cast<const uint16_t *>(p.k) + (int64_t)h * D;
-    const int64_t stride = part ? p.v_stride : p.k_stride;
-    const bool rotate = part == 0 && p.positions != nullptr;
-    const ChunkPair cp = rotate ? chunk_pair<NEIGHBOURS>(i, p.rotary_dim)
-                                : ChunkPair{2 * i, 2 * i + 1, false};
-    const float old = off0 > 0 ? *scale_at : 0.f;
-    int pos[kPasses];                    // -1: no row, or one to skip
-#pragma unroll
-    for (int k = 0; k < kPasses; ++k) {
-        const int j = k * kRows + r;
-        const bool in = j < n;
-        const uint4 *row = reinterpret_cast<const uint4 *>(rows + (t0 + (in ? j : 0)) * stride);
-        if (in) {                        // a lane stages what it will read itself
-            copy16(stage + 64 * k + lane, row + cp.c0);
-            copy16(stage + 64 * k + 32 + lane, row + cp.c1);
-        }
-        pos[k] = !in ? -1 : !p.positions ? 0 : positions[(SHARED ? 0 : t0) + j];
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    constexpr int kPasses = Run<D>::kPasses;
+    uint8_t *codes = u.rec + 16 * D * part;
+    float *scale_at = reinterpret_cast<float *>(u.rec + 32 * D) + part;
+    const float old = u.off0 > 0 ? *scale_at : 0.f;
     auto values = [&](int k) {
-        Values v = unpack16<BF16, NEIGHBOURS>(stage[64 * k + lane], stage[64 * k + 32 + lane]);
-        if (cp.turned)
-            turn16<SHARED>(p, v, i, p.rotary_dim >> 1,
-                           cos_sin + (SHARED ? (int64_t)(k * kRows + r) : (int64_t)pos[k]) * cs_stride);
+        const Chunks c = raw(k);
+        Values v = unpack16<BF16, NEIGHBOURS>(c.w0, c.w1);
+        if (ROTATE) turn(k, v);
         return v;
     };
     float amax = 0.f;
-    uint32_t bits = 0u;
+    uint32_t amax16 = 0u;
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
-        if (k * kRows >= n) break;       // the same for the whole warp
-        const int j = k * kRows + r;
-        if (p.positions && j < n && (pos[k] < 0 || pos[k] >= p.max_positions)) {
-            if (i == 0) atomicOr(p.status, PKV_DEV_BAD_POS);
-            pos[k] = -1;
+        if (!((keep >> k) & 1u)) continue;
+        if constexpr (ROTATE) {
+            amax = max_abs_nan(amax, values(k));
+        } else {
+            const Chunks c = raw(k);
+            amax16 = max_abs_nan16<BF16>(amax16, c.w0, c.w1);
         }
-        if (pos[k] < 0) continue;
-        if (rotate) amax = max_abs_nan(amax, values(k));
-        else bits = max_abs_bits(bits, stage[64 * k + lane], stage[64 * k + 32 + lane]);
     }
-    if (!rotate) {
-        const float2 f = Elem<BF16>::unpack(bits);
-        asm("max.NaN.f32 %0, %1, %2;" : "=f"(amax) : "f"(f.x), "f"(f.y));
+    if constexpr (!ROTATE) {
+        const float2 f = Elem<BF16>::unpack(amax16);
+        asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(amax) : "f"(0.f), "f"(f.x), "f"(f.y));
     }
+    // sizes are ordered as their bits are, infinity and NaN last
     constexpr float kMax = 0x1.fep127f;                       // the largest bf16
-    const bool odd = __any_sync(kFull, !(amax <= kMax));      // an infinity or a NaN
+    amax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(amax)));
+    const bool odd = !(amax <= kMax);                         // an infinity or a NaN
     if (odd) {                           // once more: NaN ignored, an infinity as kMax
         amax = 0.f;
 #pragma unroll
         for (int k = 0; k < kPasses; ++k) {
-            if (k * kRows >= n) break;
-            if (pos[k] < 0) continue;
+            if (!((keep >> k) & 1u)) continue;
             float x[16];
             in_order<NEIGHBOURS>(values(k), x);
 #pragma unroll
             for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
         }
-        amax = fminf(amax, kMax);
+        amax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fminf(amax, kMax))));
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
     if (amax < kB8Tiny) amax = 0.f;
     constexpr float kRcp127 = 0x1.020408p-7f;                 // rn(1 / 127)
     const float now = fmaxf(old, __fmul_rn(amax, kRcp127));
-    if (off0 > 0 && now > old) {
+    if (u.off0 > 0 && now > old) {
         const float ratio = __fdiv_rn(old, now);
-        for (int c = lane; c < off0 * kLanes; c += 32) {
-            uint4 *at = reinterpret_cast<uint4 *>(codes + b8_chunk(c / kLanes, c % kLanes, D));
+        for (int c = lane; c < u.off0 * Run<D>::kLanes; c += 32) {
+            uint4 *at = reinterpret_cast<uint4 *>(
+                codes + b8_chunk(c / Run<D>::kLanes, c % Run<D>::kLanes, D));
             uint4 v = *at;
             v.x = b8_rescale4(v.x, ratio);
             v.y = b8_rescale4(v.y, ratio);
@@ -508,19 +527,79 @@ __device__ __forceinline__ void b8_write_run(const Params &p, int part, int h, i
             *at = v;
         }
     }
-    if (lane == 0 && (off0 == 0 || now != old)) *scale_at = now;
+    if (lane == 0 && (u.off0 == 0 || now != old)) *scale_at = now;
     const float inv = now > 0.f ? __fdiv_rn(1.f, now) : 0.f;
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
-        if (k * kRows >= n) break;
-        if (pos[k] < 0) continue;
-        const int t = off0 + k * kRows + r;
+        if (!((keep >> k) & 1u)) continue;
+        const int t = u.off0 + k * Run<D>::kRows + u.r, swizzle = b8_swizzle(t);
+        uint8_t *line = codes + b8_line(t, D);
         const uint4 b = b8_codes16<NEIGHBOURS>(p, values(k), inv, odd);
-        *reinterpret_cast<uint2 *>(codes + b8_chunk(t, cp.c0 >> 1, D) + 8 * (cp.c0 & 1)) =
-            make_uint2(b.x, b.y);
-        *reinterpret_cast<uint2 *>(codes + b8_chunk(t, cp.c1 >> 1, D) + 8 * (cp.c1 & 1)) =
-            make_uint2(b.z, b.w);
+        if (NEIGHBOURS || !ROTATE) {     // the two chunks are one of codes
+            *reinterpret_cast<uint4 *>(line + ((cp.c0 * 8) ^ swizzle)) = b;
+        } else {
+            *reinterpret_cast<uint2 *>(line + (((cp.c0 >> 1) * 16) ^ swizzle) + 8 * (cp.c0 & 1)) =
+                make_uint2(b.x, b.y);
+            *reinterpret_cast<uint2 *>(line + (((cp.c1 >> 1) * 16) ^ swizzle) + 8 * (cp.c1 & 1)) =
+                make_uint2(b.z, b.w);
+        }
     }
+}
+
+// Write K and V of a run, or one of them (PARTS: bit 0 K, bit 1 V).  The rows wait in
+// `stage`, those of V beside K in registers, all loaded before any is worked on.  SHARED:
+// positions and cos_sin hold the rows of tokens t0, t0 + 1, ... in shared memory; else
+// these are the call's arrays.  `ready` is called between the loads and the rest.
+template <bool BF16, bool NEIGHBOURS, int D, bool SHARED, int PARTS, typename Ready>
+__device__ __forceinline__ void b8_write_run(const Params &p, const Run<D> &u, int lane,
+                                             const int *positions, const float *cos_sin, uint4 *stage,
+                                             Ready &&ready)
+{
+    constexpr int kPasses = Run<D>::kPasses, kRows = Run<D>::kRows;
+    const bool rotate = p.positions != nullptr;
+    const ChunkPair plain = {2 * u.i, 2 * u.i + 1, false};
+    const ChunkPair cp = rotate ? chunk_pair<NEIGHBOURS>(u.i, p.rotary_dim) : plain;
+    auto to_stage = [&](int k, const uint4 *a, const uint4 *b) {
+        copy16(stage + 64 * k + lane, a);                 // a lane stages what it will read itself
+        copy16(stage + 64 * k + 32 + lane, b);
+    };
+    auto staged = [&](int k) { return Chunks{stage[64 * k + lane], stage[64 * k + 32 + lane]}; };
+    if constexpr (PARTS & 1) u.rows(p.k, p.k_stride, cp, to_stage);
+    Chunks v[kPasses];
+    if constexpr (PARTS == 2) u.rows(p.v, p.v_stride, plain, to_stage);
+    if constexpr (PARTS == 3)
+        u.rows(p.v, p.v_stride, plain, [&](int k, const uint4 *a, const uint4 *b) { v[k] = {*a, *b}; });
+    ready();
+    uint32_t keep = 0u;                                   // rows to write
+    int pos[kPasses];
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) {
+        const int j = k * kRows + u.r;
+        pos[k] = j < u.n && rotate ? positions[(SHARED ? 0 : u.t0) + j] : 0;
+        if (j < u.n) {
+            if (pos[k] >= 0 && pos[k] < max(p.max_positions, 1)) keep |= 1u << k;
+            else if (u.i == 0) atomicOr(p.status, PKV_DEV_BAD_POS);
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if constexpr (PARTS & 1) {
+        if (rotate)
+            b8_write_part<BF16, NEIGHBOURS, true>(p, u, 0, cp, keep, lane, staged, [&](int k, Values &x) {
+                const float *cs = cos_sin + (SHARED ? (int64_t)((k * kRows + u.r) * (D + kTablePad))
+                                                    : (int64_t)pos[k] * p.rotary_dim);
+                if (cp.turned) turn16<SHARED>(p, x, u.i, p.rotary_dim >> 1, cs);
+            });
+        else
+            b8_write_part<BF16, NEIGHBOURS, false>(p, u, 0, cp, keep, lane, staged, [](int, Values &) {});
+    }
+    if constexpr (PARTS & 2)
+        b8_write_part<BF16, NEIGHBOURS, false>(
+            p, u, 1, plain, keep, lane,
+            [&](int k) {
+                if constexpr (PARTS == 3) return v[k];
+                else return staged(k);
+            },
+            [](int, Values &) {});
 }
 
 // The runs that begin among `span` tokens from tb on.  A run is a chain of tokens
@@ -576,22 +655,25 @@ __global__ void __launch_bounds__(128, 6) append_b8_kernel(Params p)
         const Runs runs = find_runs(p, t, 1, lane, rest == 0);
         if (!runs.leads) continue;
         const int64_t s0 = __shfl_sync(kFull, runs.slot, 1);
-        b8_write_run<BF16, NEIGHBOURS, D, false>(p, rest & 1, rest >> 1, t, runs.length(1),
-                                                 s0 / kBlock, (int)(s0 % kBlock), lane,
-                                                 p.positions, p.cos_sin, p.rotary_dim, stage);
+        const Run<D> run(p, (int)t, runs.length(1), s0, rest >> 1, lane);
+        if (rest & 1)
+            b8_write_run<BF16, NEIGHBOURS, D, false, 2>(p, run, lane, p.positions, p.cos_sin, stage, [] {});
+        else
+            b8_write_run<BF16, NEIGHBOURS, D, false, 1>(p, run, lane, p.positions, p.cos_sin, stage, [] {});
     }
 }
 
-// Many tokens: a CTA takes a span of 16 and writes every run that begins there,
-// the (run, kv head, K or V) units dealt to its warps.  The table rows of the
-// tokens it may reach (31) come to shared memory once, for all heads.
+// Many tokens: a CTA takes a span of 16 and writes every run that begins there, the
+// (run, kv head) units dealt to its warps.  The table rows of the tokens that they
+// reach (up to 31) come to shared memory once, for all heads, while the rows of the
+// warps' first units are on their way.
 constexpr int kSpanWarps = 8;
 constexpr int kSpanTokens = 31;
 
 template <bool BF16, bool NEIGHBOURS, int D>
-__global__ void __launch_bounds__(32 * kSpanWarps, 4) append_b8_span_kernel(Params p)
+__global__ void __launch_bounds__(32 * kSpanWarps, 3) append_b8_span_kernel(Params p)
 {
-    constexpr int kStride = D + 4;                        // floats of a staged table row
+    constexpr int kStride = D + kTablePad;                // floats of a staged table row
     extern __shared__ uint4 stages[];                     // [warps][16 rows x D / 8]
     __shared__ __align__(16) float table[kSpanTokens * kStride];
     __shared__ int positions[kSpanTokens + 1];
@@ -599,34 +681,41 @@ __global__ void __launch_bounds__(32 * kSpanWarps, 4) append_b8_span_kernel(Para
     uint4 *stage = stages + warp * 2 * D;
     begin();
     after_wait(p.cos_sin);
-    const int64_t spans = ((int64_t)p.num_tokens + 15) / 16;
-    for (int64_t w = blockIdx.x; w < spans; w += gridDim.x) {
-        const int64_t tb = w * 16;
+    const int spans = (p.num_tokens + 15) / 16;
+    for (int w = blockIdx.x; w < spans; w += gridDim.x) {
+        const int tb = w * 16;
         const Runs runs = find_runs(p, tb, 16, lane, warp == 0);
-        if (p.positions) {
-            const int n = (int)min((int64_t)kSpanTokens, p.num_tokens - tb);
+        const int n_leads = __popc(runs.leads), units = n_leads * p.num_kv_heads;
+        // of token tb - 1 + lane, asked for together with the slots
+        const int at = tb - 1 + lane;
+        const int lane_pos = p.positions && at >= 0 && at < p.num_tokens ? p.positions[at] : -1;
+        auto fill = [&] {                                 // the table, up to the end of the last run
+            if (!p.positions) return;
+            const int last = 31 - __clz(runs.leads | 1u);
+            const int n = runs.leads ? last - 1 + runs.length(last) : 0;
             const int per_row = p.rotary_dim / 4;
-            for (int e = threadIdx.x; e < n * per_row; e += 32 * kSpanWarps) {
-                const int t = e / per_row, c = e - t * per_row;
-                const int pos = p.positions[tb + t];
-                if (c == 0) positions[t] = pos;
-                if (pos >= 0 && pos < p.max_positions)
-                    *reinterpret_cast<float4 *>(table + t * kStride + 4 * c) = __ldg(
-                        reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * p.rotary_dim) + c);
+            for (int e0 = 32 * warp; e0 < n * per_row; e0 += 32 * kSpanWarps) {
+                const int e = e0 + lane, t = e / per_row, c = e - t * per_row;
+                const int pos = __shfl_sync(kFull, lane_pos, (t + 1) & 31);
+                if (t < n && pos >= 0 && pos < p.max_positions)
+                    *reinterpret_cast<float4 *>(table + t * kStride + 4 * staged_at(c, p.rotary_dim >> 1)) =
+                        __ldg(reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * p.rotary_dim) + c);
             }
+            if (warp == 0 && lane > 0) positions[lane - 1] = lane_pos;
             __syncthreads();
-        }
-        const int n_leads = __popc(runs.leads), units = n_leads * 2 * p.num_kv_heads;
+        };
+        if (warp >= units) fill();
         for (int u = warp; u < units; u += kSpanWarps) {
-            const int rest = u / n_leads, k = u - rest * n_leads;
+            const int h = n_leads == 1 ? u : u / n_leads, k = u - h * n_leads;
             unsigned left = runs.leads;                   // the k-th run's first token
             for (int i = 0; i < k; ++i) left &= left - 1;
             const int l = __ffs(left) - 1;
             const int64_t s0 = __shfl_sync(kFull, runs.slot, l);
-            b8_write_run<BF16, NEIGHBOURS, D, true>(p, rest & 1, rest >> 1, tb - 1 + l,
-                                                    runs.length(l), s0 / kBlock,
-                                                    (int)(s0 % kBlock), lane, positions + l - 1,
-                                                    table + (l - 1) * kStride, kStride, stage);
+            const Run<D> run(p, tb - 1 + l, runs.length(l), s0, h, lane);
+            b8_write_run<BF16, NEIGHBOURS, D, true, 3>(p, run, lane, positions + l - 1,
+                                                       table + (l - 1) * kStride, stage, [&] {
+                                                           if (u == warp) fill();
+                                                       });
         }
         __syncthreads();                                  // the table may be filled anew
     }
@@ -688,7 +777,7 @@ static int launch_rows(const Params &p, int D, int heads_kv, cudaStream_t st)
 {
     const int64_t threads = (int64_t)p.num_tokens * (p.num_q_heads + 2 * heads_kv) * (D / 16);
     const int64_t grid = std::min<int64_t>((threads + 511) / 512, 152 * 64);   // two units a thread
-    return launch(&append_rope_kernel<BF16, NEIGHBOURS>, grid, 256, 0, st, p, D, heads_kv);
+    return launch(&append_rope_kernel<BF16, NEIGHBOURS>, dim3((unsigned)grid), 256, 0, st, p, D, heads_kv);
 }
 
 template <bool BF16, bool NEIGHBOURS>
@@ -701,7 +790,7 @@ static int launch_b8(const Params &p0, int D, bool queries, cudaStream_t st)
             const int rc = launch_rows<BF16, NEIGHBOURS>(p, D, 0, st);
             if (rc != PKV_OK) return rc;
         }
-        const int64_t grid = std::min<int64_t>(spans, 152 * 64);
+        const dim3 grid((unsigned)std::min<int64_t>(spans, 152 * 64));
         const int smem = kSpanWarps * 32 * D;
         void (*fn)(Params) = D == 128 ? &append_b8_span_kernel<BF16, NEIGHBOURS, 128>
                                       : &append_b8_span_kernel<BF16, NEIGHBOURS, 64>;
@@ -720,7 +809,7 @@ static int launch_b8(const Params &p0, int D, bool queries, cudaStream_t st)
     }
     return launch(D == 128 ? &append_b8_kernel<BF16, NEIGHBOURS, 128>
                            : &append_b8_kernel<BF16, NEIGHBOURS, 64>,
-                  grid, 128, 0, st, p);
+                  dim3((unsigned)grid), 128, 0, st, p);
 }
 
 static int32_t log2_or_none(int32_t x)
@@ -858,7 +947,7 @@ extern "C" int kv_dequantize_blocks(const pkv_pool *pool, const int32_t *ids, in
     const bool bf = g.dtype == PKV_B8_BF16;
     auto fn = g.head_dim == 128 ? (bf ? &dequantize_kernel<true, 128> : &dequantize_kernel<false, 128>)
                                 : (bf ? &dequantize_kernel<true, 64> : &dequantize_kernel<false, 64>);
-    return launch(fn, grid, 256, 0, static_cast<cudaStream_t>(stream),
+    return launch(fn, dim3((unsigned)grid), 256, 0, static_cast<cudaStream_t>(stream),
                   static_cast<const uint8_t *>(kv_b8), ids, n, g.num_kv_heads, g.num_blocks,
                   static_cast<uint4 *>(k_out), static_cast<uint4 *>(v_out), d_status);
 }
