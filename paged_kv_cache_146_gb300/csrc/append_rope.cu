@@ -97,18 +97,6 @@ __device__ __forceinline__ ChunkPair chunk_pair(int i, int rotary_dim)
 }
 
 template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4 &w, float *x)
-{
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float2 f = Elem<BF16>::unpack(u[k]);
-        x[2 * k] = f.x;
-        x[2 * k + 1] = f.y;
-    }
-}
-
-template <bool BF16>
 __device__ __forceinline__ uint4 pack8(const float *x)
 {
     using E = Elem<BF16>;
@@ -116,148 +104,9 @@ __device__ __forceinline__ uint4 pack8(const float *x)
                       E::pack(x[6], x[7]));
 }
 
-__device__ __forceinline__ void turn(float &a, float &b, float c, float s)
-{
-    const float x = a, y = b;
-    a = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
-    b = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
-}
-
-// Rotate the 16 values of chunk pair i in place; cs = the position's table row.
-template <bool NEIGHBOURS>
-__device__ __forceinline__ void rotate16(float (&x)[16], int i, int half, const float *cs)
-{
-    // halves: values e and 8 + e are angle 8i + e; neighbours: values 2e and
-    // 2e + 1 are angle 8i + e: either way the pair of chunks takes the table's
-    // entries 8i .. 8i + 7
-    const float4 *c4 = reinterpret_cast<const float4 *>(cs + 8 * i);
-    const float4 *s4 = reinterpret_cast<const float4 *>(cs + half + 8 * i);
-    const float4 ca = __ldg(c4), cb = __ldg(c4 + 1), sa = __ldg(s4), sb = __ldg(s4 + 1);
-    const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
-    const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        if (NEIGHBOURS) turn(x[2 * e], x[2 * e + 1], c[e], s[e]);
-        else turn(x[e], x[8 + e], c[e], s[e]);
-    }
-}
-
-// One thread's unit of append_rows: two chunks of one head's row.
-struct RowUnit {
-    const uint16_t *row;
-    int64_t t, slot;
-    int head, i, pos;
-    uint4 w0, w1;
-};
-
-// 16-bit pools (and, with heads_kv = 0, the queries of an 8-bit append): one
-// thread per (token, head, chunk pair), heads in the order q, k, v; two units a
-// thread in flight.  A thread reads what it writes and nothing else of q, so
-// q_out may be q itself.
-template <bool BF16, bool NEIGHBOURS>
-__device__ __forceinline__ void append_rows(const Params &p, int D, int heads_kv, int cta, int ctas)
-{
-    const int lanes = D >> 4;                             // chunk pairs of a row
-    const int per_token = (p.num_q_heads + 2 * heads_kv) * lanes;
-    // units first, first + step, ...: the token and the rest advance by fixed amounts
-    const uint32_t first = (uint32_t)cta * blockDim.x + threadIdx.x;
-    const uint32_t step = (uint32_t)ctas * blockDim.x;
-    const int step_t = (int)(step / (uint32_t)per_token);
-    const int step_w = (int)(step - (uint32_t)step_t * per_token);
-    int64_t t = first / (uint32_t)per_token;
-    int within = (int)(first - (uint32_t)t * per_token);
-
-    auto load = [&](RowUnit &u) {                         // and advance
-        u.t = t;
-        if (t < p.num_tokens) {
-            u.head = p.lane_shift >= 0 ? within >> p.lane_shift : within / lanes;
-            u.i = within - u.head * lanes;
-            const ChunkPair cp = chunk_pair<NEIGHBOURS>(u.i, p.rotary_dim);
-            const int h = u.head - p.num_q_heads;
-            u.row = h < 0 ? static_cast<const uint16_t *>(p.q) + t * p.q_stride + (int64_t)u.head * D
-                    : h < heads_kv
-                        ? static_cast<const uint16_t *>(p.k) + t * p.k_stride + (int64_t)h * D
-                        : static_cast<const uint16_t *>(p.v) + t * p.v_stride +
-                              (int64_t)(h - heads_kv) * D;
-            u.slot = p.slots[t];
-            u.pos = p.positions[t];
-            u.w0 = reinterpret_cast<const uint4 *>(u.row)[cp.c0];
-            u.w1 = reinterpret_cast<const uint4 *>(u.row)[cp.c1];
-        }
-        t += step_t;
-        within += step_w;
-        if (within >= per_token) {
-            within -= per_token;
-            ++t;
-        }
-    };
-    auto finish = [&](RowUnit &u) {
-        if (u.t >= p.num_tokens || u.slot < 0) return;    // a negative slot: no token here
-        if (u.slot >= p.num_slots || u.pos < 0 || u.pos >= p.max_positions) {
-            if (u.head == 0 && u.i == 0)
-                atomicOr(p.status, u.slot >= p.num_slots ? PKV_DEV_BAD_SLOT : PKV_DEV_BAD_POS);
-            return;
-        }
-        const ChunkPair cp = chunk_pair<NEIGHBOURS>(u.i, p.rotary_dim);
-        const int h = u.head - p.num_q_heads;
-        if (h < heads_kv && cp.turned) {
-            float x[16];
-            unpack8<BF16>(u.w0, x);
-            unpack8<BF16>(u.w1, x + 8);
-            rotate16<NEIGHBOURS>(x, u.i, p.rotary_dim >> 1, p.cos_sin + (int64_t)u.pos * p.rotary_dim);
-            u.w0 = pack8<BF16>(x);
-            u.w1 = pack8<BF16>(x + 8);
-        }
-        uint4 *dst;
-        if (h < 0) {
-            dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.q_out) + u.t * p.q_out_stride +
-                                            (int64_t)u.head * D);
-        } else {
-            const int64_t block =
-                p.block_shift >= 0 ? u.slot >> p.block_shift : u.slot / p.block_size;
-            const int64_t off = u.slot - block * p.block_size;
-            const int kvh = h < heads_kv ? h : h - heads_kv;
-            dst = (h < heads_kv ? p.k_pool : p.v_pool) +
-                  ((block * heads_kv + kvh) * p.block_size + off) * (D >> 3);
-        }
-        dst[cp.c0] = u.w0;
-        dst[cp.c1] = u.w1;
-    };
-    while (t < p.num_tokens) {
-        RowUnit a, b;
-        load(a);
-        load(b);
-        finish(a);
-        finish(b);
-    }
-}
-
-template <bool BF16, bool NEIGHBOURS>
-__global__ void __launch_bounds__(256) append_rope_kernel(Params p, int D, int heads_kv)
-{
-    begin();
-    after_wait(p.cos_sin);
-    append_rows<BF16, NEIGHBOURS>(p, D, heads_kv, blockIdx.x, gridDim.x);
-}
-
-// ------------------------------------------------------- block-scaled 8-bit pools
-// Byte of 16-byte chunk j of token t inside a record's K (or V) codes (see the
-// layout in pagedkv.h): lines of 128 bytes, chunk positions rotated so that the
-// attention kernel's wide shared-memory reads of either operand touch all banks.
-__device__ __forceinline__ int b8_line(int t, int D) { return ((t * D) >> 7) * 128; }
-__device__ __forceinline__ int b8_swizzle(int t) { return ((t & 1) << 6) ^ (((t >> 1) & 3) << 5); }
-__device__ __forceinline__ int b8_chunk(int t, int j, int D) { return b8_line(t, D) + ((j * 16) ^ b8_swizzle(t)); }
-
-// A table row staged in shared memory: this many floats apart beyond its own.
-constexpr int kTablePad = 4;
-
-// Values whose block maximum is below this store as zeros (scale 0): their
-// reciprocal scale would leave the fp32 range.
-constexpr float kB8Tiny = 0x1p-100f;
-
 constexpr uint64_t kMinusZeros = 0x8000000080000000ull;
 
-// The 8-bit append works on pairs of fp32 values in packed operations, half as many
+// The kernels work on pairs of fp32 values in packed operations, half as many
 // instructions.  A product and a sum are rounded each by itself; the compiler joins a
 // packed product with the sum it feeds, so the product is written as a fused one whose
 // addend, -0, it does not know: x y + (-0) is x y rounded once, signed zeros included.
@@ -332,6 +181,130 @@ __device__ __forceinline__ void in_order(const Values &v, float (&x)[16])
         x[NEIGHBOURS ? 4 * m + 3 : 8 + 2 * m + 1] = b.y;
     }
 }
+
+// The 16-bit words of the two chunks.
+template <bool BF16, bool NEIGHBOURS>
+__device__ __forceinline__ Chunks pack16(const Values &v)
+{
+    using E = Elem<BF16>;
+    uint32_t w[8];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const float2 a = unpack2f(v.a[m]), b = unpack2f(v.b[m]);
+        w[NEIGHBOURS ? 2 * m : m] = NEIGHBOURS ? E::pack(a.x, b.x) : E::pack(a.x, a.y);
+        w[NEIGHBOURS ? 2 * m + 1 : 4 + m] = NEIGHBOURS ? E::pack(a.y, b.y) : E::pack(b.x, b.y);
+    }
+    return {make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])};
+}
+
+// One thread's unit of append_rows: two chunks of one head's row.
+struct RowUnit {
+    const uint16_t *row;
+    int64_t t, slot;
+    int head, i, pos;
+    Chunks w;
+};
+
+// 16-bit pools (and, with heads_kv = 0, the queries of an 8-bit append): one
+// thread per (token, head, chunk pair), heads in the order q, k, v; two units a
+// thread in flight.  A thread reads what it writes and nothing else of q, so
+// q_out may be q itself.
+template <bool BF16, bool NEIGHBOURS>
+__device__ __forceinline__ void append_rows(const Params &p, int D, int heads_kv, int cta, int ctas)
+{
+    const int lanes = D >> 4;                             // chunk pairs of a row
+    const int per_token = (p.num_q_heads + 2 * heads_kv) * lanes;
+    // units first, first + step, ...: the token and the rest advance by fixed amounts
+    const uint32_t first = (uint32_t)cta * blockDim.x + threadIdx.x;
+    const uint32_t step = (uint32_t)ctas * blockDim.x;
+    const int step_t = (int)(step / (uint32_t)per_token);
+    const int step_w = (int)(step - (uint32_t)step_t * per_token);
+    int64_t t = first / (uint32_t)per_token;
+    int within = (int)(first - (uint32_t)t * per_token);
+
+    auto load = [&](RowUnit &u) {                         // and advance
+        u.t = t;
+        if (t < p.num_tokens) {
+            u.head = p.lane_shift >= 0 ? within >> p.lane_shift : within / lanes;
+            u.i = within - u.head * lanes;
+            const ChunkPair cp = chunk_pair<NEIGHBOURS>(u.i, p.rotary_dim);
+            const int h = u.head - p.num_q_heads;
+            u.row = h < 0 ? static_cast<const uint16_t *>(p.q) + t * p.q_stride + (int64_t)u.head * D
+                    : h < heads_kv
+                        ? static_cast<const uint16_t *>(p.k) + t * p.k_stride + (int64_t)h * D
+                        : static_cast<const uint16_t *>(p.v) + t * p.v_stride +
+                              (int64_t)(h - heads_kv) * D;
+            u.slot = p.slots[t];
+            u.pos = p.positions[t];
+            u.w = {reinterpret_cast<const uint4 *>(u.row)[cp.c0], reinterpret_cast<const uint4 *>(u.row)[cp.c1]};
+        }
+        t += step_t;
+        within += step_w;
+        if (within >= per_token) {
+            within -= per_token;
+            ++t;
+        }
+    };
+    auto finish = [&](RowUnit &u) {
+        if (u.t >= p.num_tokens || u.slot < 0) return;    // a negative slot: no token here
+        if (u.slot >= p.num_slots || u.pos < 0 || u.pos >= p.max_positions) {
+            if (u.head == 0 && u.i == 0)
+                atomicOr(p.status, u.slot >= p.num_slots ? PKV_DEV_BAD_SLOT : PKV_DEV_BAD_POS);
+            return;
+        }
+        const ChunkPair cp = chunk_pair<NEIGHBOURS>(u.i, p.rotary_dim);
+        const int h = u.head - p.num_q_heads;
+        if (h < heads_kv && cp.turned) {
+            Values x = unpack16<BF16, NEIGHBOURS>(u.w.w0, u.w.w1);
+            turn16<false>(p, x, u.i, p.rotary_dim >> 1, p.cos_sin + (int64_t)u.pos * p.rotary_dim);
+            u.w = pack16<BF16, NEIGHBOURS>(x);
+        }
+        uint4 *dst;
+        if (h < 0) {
+            dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.q_out) + u.t * p.q_out_stride +
+                                            (int64_t)u.head * D);
+        } else {
+            const int64_t block =
+                p.block_shift >= 0 ? u.slot >> p.block_shift : u.slot / p.block_size;
+            const int64_t off = u.slot - block * p.block_size;
+            const int kvh = h < heads_kv ? h : h - heads_kv;
+            dst = (h < heads_kv ? p.k_pool : p.v_pool) +
+                  ((block * heads_kv + kvh) * p.block_size + off) * (D >> 3);
+        }
+        dst[cp.c0] = u.w.w0;
+        dst[cp.c1] = u.w.w1;
+    };
+    while (t < p.num_tokens) {
+        RowUnit a, b;
+        load(a);
+        load(b);
+        finish(a);
+        finish(b);
+    }
+}
+
+template <bool BF16, bool NEIGHBOURS>
+__global__ void __launch_bounds__(256) append_rope_kernel(Params p, int D, int heads_kv)
+{
+    begin();
+    after_wait(p.cos_sin);
+    append_rows<BF16, NEIGHBOURS>(p, D, heads_kv, blockIdx.x, gridDim.x);
+}
+
+// ------------------------------------------------------- block-scaled 8-bit pools
+// Byte of 16-byte chunk j of token t inside a record's K (or V) codes (see the
+// layout in pagedkv.h): lines of 128 bytes, chunk positions rotated so that the
+// attention kernel's wide shared-memory reads of either operand touch all banks.
+__device__ __forceinline__ int b8_line(int t, int D) { return ((t * D) >> 7) * 128; }
+__device__ __forceinline__ int b8_swizzle(int t) { return ((t & 1) << 6) ^ (((t >> 1) & 3) << 5); }
+__device__ __forceinline__ int b8_chunk(int t, int j, int D) { return b8_line(t, D) + ((j * 16) ^ b8_swizzle(t)); }
+
+// A table row staged in shared memory: this many floats apart beyond its own.
+constexpr int kTablePad = 4;
+
+// Values whose block maximum is below this store as zeros (scale 0): their
+// reciprocal scale would leave the fp32 range.
+constexpr float kB8Tiny = 0x1p-100f;
 
 // Rounding to an integer, ties to even, of |x| <= 2^22: adding 1.5 * 2^23 puts
 // the sum where the fp32 spacing is 1; its low byte is the integer's.
@@ -681,8 +654,15 @@ __global__ void __launch_bounds__(32 * kSpanWarps, 3) append_b8_span_kernel(Para
     uint4 *stage = stages + warp * 2 * D;
     begin();
     after_wait(p.cos_sin);
+    // write_blocks CTAs write, the others rotate queries, evenly mixed: an SM's writers
+    // compute while its others wait for memory
+    const int64_t before = (int64_t)blockIdx.x * p.write_blocks / gridDim.x;
+    if ((int64_t)(blockIdx.x + 1) * p.write_blocks / gridDim.x == before) {
+        append_rows<BF16, NEIGHBOURS>(p, D, 0, (int)(blockIdx.x - before), (int)gridDim.x - p.write_blocks);
+        return;
+    }
     const int spans = (p.num_tokens + 15) / 16;
-    for (int w = blockIdx.x; w < spans; w += gridDim.x) {
+    for (int w = (int)before; w < spans; w += p.write_blocks) {
         const int tb = w * 16;
         const Runs runs = find_runs(p, tb, 16, lane, warp == 0);
         const int n_leads = __popc(runs.leads), units = n_leads * p.num_kv_heads;
@@ -786,11 +766,14 @@ static int launch_b8(const Params &p0, int D, bool queries, cudaStream_t st)
     Params p = p0;
     const int64_t spans = ((int64_t)p.num_tokens + 15) / 16;
     if (spans >= kSpans) {
-        if (queries) {               // in a launch of their own, at full occupancy
-            const int rc = launch_rows<BF16, NEIGHBOURS>(p, D, 0, st);
-            if (rc != PKV_OK) return rc;
+        p.write_blocks = (int32_t)std::min<int64_t>(spans, 152 * 64);
+        int64_t grid = p.write_blocks;
+        if (queries) {
+            // units a thread (20,500 and 4,000 tokens): 2 101 and 23.0 us, 4 95 and 21.5,
+            // 8 93 and 19.8, 16 97 and 24.8; in a launch of their own before 96 and 23.1
+            const int64_t units = (int64_t)p.num_tokens * p.num_q_heads * (D / 16);
+            grid += std::min<int64_t>((units + 256 * 8 - 1) / (256 * 8), 152 * 64);
         }
-        const dim3 grid((unsigned)std::min<int64_t>(spans, 152 * 64));
         const int smem = kSpanWarps * 32 * D;
         void (*fn)(Params) = D == 128 ? &append_b8_span_kernel<BF16, NEIGHBOURS, 128>
                                       : &append_b8_span_kernel<BF16, NEIGHBOURS, 64>;
@@ -798,7 +781,7 @@ static int launch_b8(const Params &p0, int D, bool queries, cudaStream_t st)
         if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
             return PKV_ERR_CUDA;
-        return launch(fn, grid, 32 * kSpanWarps, smem, st, p);
+        return launch(fn, dim3((unsigned)grid), 32 * kSpanWarps, smem, st, p);
     }
     const int64_t units = (int64_t)p.num_tokens * 2 * p.num_kv_heads;
     p.write_blocks = (int32_t)std::min<int64_t>((units + 3) / 4, 152 * 64);
