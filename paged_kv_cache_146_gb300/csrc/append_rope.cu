@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(32 * kSpanWarps, 3) append_b8_span_kernel(Para
         append_rows<BF16, NEIGHBOURS>(p, D, 0, (int)(blockIdx.x - before), (int)gridDim.x - p.write_blocks);
         return;
     }
-    const int spans = (p.num_tokens + 15) / 16;
+    const int spans = (int)(((int64_t)p.num_tokens + 15) / 16);
     for (int w = (int)before; w < spans; w += p.write_blocks) {
         const int tb = w * 16;
         const Runs runs = find_runs(p, tb, 16, lane, warp == 0);
@@ -746,10 +746,11 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// From this many spans of 16 tokens on, a CTA per span and the queries in a launch
-// of their own; below, a warp per token and one launch.  With 32 query and 8 kv
-// heads, the append and its read-back: 2,000 tokens 28 us by spans, 24 by tokens;
-// 4,000 tokens 38 and 39; 8,000 tokens 57 and 73.
+// From this many spans of 16 tokens on, a CTA per span; below, a warp per token.  With
+// 32 query and 8 kv heads, tokens of prompts: 1,000 10.3 us by spans, 9.3 by tokens;
+// 2,000 10.8 and 14.6; tokens of as many sequences (a CTA then writes 128 runs): 1,000
+// 48 and 14, 3,000 62 and 36, 6,000 92 and 74.  The limit lies above the numbers of
+// sequences that decode together.
 constexpr int64_t kSpans = 200;
 
 template <bool BF16, bool NEIGHBOURS>

@@ -366,3 +366,54 @@ def test_repeated_captured_and_concurrent_calls_agree():
     assert status_check(status) == (0, 0)
     for o in (*outs, held):
         assert torch.equal(first, o)
+
+
+@pytest.mark.parametrize("dtype,dim,rot,hq,hkv,interleaved", [
+    ("bf16", 128, 128, 4, 8, False), ("f16", 128, 64, 2, 3, True), ("f16", 64, 64, 3, 1, False),
+    ("bf16", 64, 16, 0, 9, True), ("bf16", 128, 112, 5, 2, False)])
+def test_many_tokens_with_gaps_and_odd_values(dtype, dim, rot, hq, hkv, interleaved):
+    """Thousands of tokens of ragged sequences, some blocks cut short, some tokens
+    refused, infinities and NaN among the values, queries turned in place."""
+    rng = np.random.default_rng(dim + rot)
+    prior = rng.integers(0, 40, 60).astype(np.int32)
+    news = np.where(np.arange(60) % 7 == 0, 1, rng.integers(40, 110, 60)).astype(np.int32)
+    nb = int(sum(-(-int(a + b) // 16) for a, b in zip(prior, news))) + 3
+    pool, ref = random_pool(nb, hkv, dim, dtype, 21)
+    ledger = KVPool(nb, hkv, dim, "b8_" + dtype, free_order=rng.permutation(nb))
+    tables = np.full((60, 12), -1, np.int32)
+    ledger.append_slots(np.zeros(60, np.int32), prior, tables)
+    slots = np.asarray(ledger.append_slots(prior, news, tables)).copy()
+    tokens = len(slots)
+    assert tokens >= 3200
+    pos = np.concatenate([np.arange(a, a + n) for a, n in zip(prior, news)]).astype(np.int32)
+    table = rope_table(200, rot)
+    for t in range(100, tokens, 97):                       # the rest of a block is left out
+        slots[t:t + 16][slots[t:t + 16] // 16 == slots[t] // 16] = -1
+    refused = [t for t in range(60, tokens - 1, 113)
+               if slots[t] > 0 and slots[t] % 16 and slots[t - 1] == slots[t] - 1]
+    pos[refused[::2]] = 200
+    pos[refused[1::2]] = -1
+    qkv = torch.randn((tokens, (hq + 2 * hkv) * dim), generator=torch.Generator().manual_seed(22)).to(DT[dtype])
+    q, k, v = (p.view(tokens, -1, dim) for p in qkv.split([hq * dim, hkv * dim, hkv * dim], 1))
+    for i, odd in enumerate([float("inf"), float("-inf"), float("nan")] * 4):
+        k[37 + 211 * i, i % hkv, (5 * i) % dim] = odd
+        v[90 + 173 * i, i % hkv, (7 * i) % dim] = odd
+    gpu = qkv.cuda()
+    gq, gk, gv = (p.view(tokens, -1, dim) for p in gpu.split([hq * dim, hkv * dim, hkv * dim], 1))
+    status = new_status()
+    dev = dict(q=gq, q_out=gq) if hq else {}
+    cache_write_rope(pool, gk, gv, torch.from_numpy(pos).cuda(), table.cuda(), torch.from_numpy(slots).cuda(),
+                     status, interleaved=interleaved, **dev)
+    assert status_check(status)[1] == DEV_BAD_POS
+    kept = slots.copy()
+    kept[refused] = -1
+    safe = np.where(kept < 0, 0, pos)
+    with np.errstate(invalid="ignore"):
+        ref.append(0, rotate_f32(k.float().numpy(), table, safe, interleaved), kept)
+        ref.append(1, v.float().numpy(), kept)
+    same_records(pool, ref)
+    if hq:
+        want = torch.from_numpy(rotate_f32(q.float().numpy(), table, safe, interleaved)).to(DT[dtype])
+        want[torch.from_numpy(kept < 0)] = q[torch.from_numpy(kept < 0)]
+        assert torch.equal(gq.cpu(), want)
+    assert torch.equal(gk.cpu().view(torch.int16), k.contiguous().view(torch.int16))
