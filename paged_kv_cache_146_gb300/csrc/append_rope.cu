@@ -151,20 +151,28 @@ __device__ __forceinline__ int staged_at(int c, int half)     // place of a row'
     return 2 * quarter * part + (e & 1) * quarter + (e >> 1);
 }
 
+struct Angles {
+    uint64_t c[4], s[4];
+};
+
 template <bool SHARED>
-__device__ __forceinline__ void turn16(const Params &p, Values &v, int i, int half, const float *cs)
+__device__ __forceinline__ Angles angles(int i, int half, const float *cs)
 {
     const ulonglong2 *c2 = reinterpret_cast<const ulonglong2 *>(cs) + (SHARED ? i : 2 * i);
     const ulonglong2 *s2 = c2 + half / 4;
     const int next = SHARED ? half / 8 : 1;
     const ulonglong2 ca = SHARED ? c2[0] : __ldg(c2), cb = SHARED ? c2[next] : __ldg(c2 + 1);
     const ulonglong2 sa = SHARED ? s2[0] : __ldg(s2), sb = SHARED ? s2[next] : __ldg(s2 + 1);
-    const uint64_t c[4] = {ca.x, ca.y, cb.x, cb.y}, s[4] = {sa.x, sa.y, sb.x, sb.y};
+    return {{ca.x, ca.y, cb.x, cb.y}, {sa.x, sa.y, sb.x, sb.y}};
+}
+
+__device__ __forceinline__ void turn16(const Params &p, Values &v, const Angles &w)
+{
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
         const uint64_t x = v.a[m], y = v.b[m];
-        v.a[m] = sub2f(mul2(p, x, c[m]), mul2(p, y, s[m]));
-        v.b[m] = add2f(mul2(p, y, c[m]), mul2(p, x, s[m]));
+        v.a[m] = sub2f(mul2(p, x, w.c[m]), mul2(p, y, w.s[m]));
+        v.b[m] = add2f(mul2(p, y, w.c[m]), mul2(p, x, w.s[m]));
     }
 }
 
@@ -197,23 +205,24 @@ __device__ __forceinline__ Chunks pack16(const Values &v)
     return {make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])};
 }
 
-// One thread's unit of append_rows: two chunks of one head's row.
-struct RowUnit {
-    const uint16_t *row;
-    int64_t t, slot;
-    int head, i, pos;
-    Chunks w;
-};
+// 16-bit pools (and, with heads_kv = 0, the queries of an 8-bit append): one thread per
+// (token, R heads, chunk pair), heads in the order q, k, v: the R rows are under way
+// together and share slot, position and the table's entries.  A thread reads what it
+// writes and nothing else of q, so q_out may be q itself.
+// R by measurement (R = 1, 2, 4): 20,500 tokens of 32/8 heads of 128, halves, 83, 79,
+// 82 us, 4,000 18.7, 16.0, 15.8, 40,000 of 8/8 heads of 64 45.5, 42.0, 39.8; too few
+// threads to fill the GPU at 4, 800 of 32/8 heads 4.3, 3.8, 4.9.  Neighbours (a thread's
+// two chunks adjoin, so each of its accesses takes half a sector): 13,300 of 8/8 heads of
+// 64 11.8, 12.9, 13.8, 20,000 of 32/8 41.8, 41.2, 42.4.
+constexpr int kRowHeads = 4;
+constexpr int64_t kRowHeadsFrom = 152 * 1024;             // threads with kRowHeads
 
-// 16-bit pools (and, with heads_kv = 0, the queries of an 8-bit append): one
-// thread per (token, head, chunk pair), heads in the order q, k, v; two units a
-// thread in flight.  A thread reads what it writes and nothing else of q, so
-// q_out may be q itself.
-template <bool BF16, bool NEIGHBOURS>
+template <bool BF16, bool NEIGHBOURS, int R>
 __device__ __forceinline__ void append_rows(const Params &p, int D, int heads_kv, int cta, int ctas)
 {
     const int lanes = D >> 4;                             // chunk pairs of a row
-    const int per_token = (p.num_q_heads + 2 * heads_kv) * lanes;
+    const int turned_heads = p.num_q_heads + heads_kv, heads = turned_heads + heads_kv;
+    const int groups = (heads + R - 1) / R, per_token = groups * lanes;
     // units first, first + step, ...: the token and the rest advance by fixed amounts
     const uint32_t first = (uint32_t)cta * blockDim.x + threadIdx.x;
     const uint32_t step = (uint32_t)ctas * blockDim.x;
@@ -221,74 +230,68 @@ __device__ __forceinline__ void append_rows(const Params &p, int D, int heads_kv
     const int step_w = (int)(step - (uint32_t)step_t * per_token);
     int64_t t = first / (uint32_t)per_token;
     int within = (int)(first - (uint32_t)t * per_token);
-
-    auto load = [&](RowUnit &u) {                         // and advance
-        u.t = t;
-        if (t < p.num_tokens) {
-            u.head = p.lane_shift >= 0 ? within >> p.lane_shift : within / lanes;
-            u.i = within - u.head * lanes;
-            const ChunkPair cp = chunk_pair<NEIGHBOURS>(u.i, p.rotary_dim);
-            const int h = u.head - p.num_q_heads;
-            u.row = h < 0 ? static_cast<const uint16_t *>(p.q) + t * p.q_stride + (int64_t)u.head * D
-                    : h < heads_kv
-                        ? static_cast<const uint16_t *>(p.k) + t * p.k_stride + (int64_t)h * D
-                        : static_cast<const uint16_t *>(p.v) + t * p.v_stride +
-                              (int64_t)(h - heads_kv) * D;
-            u.slot = p.slots[t];
-            u.pos = p.positions[t];
-            u.w = {reinterpret_cast<const uint4 *>(u.row)[cp.c0], reinterpret_cast<const uint4 *>(u.row)[cp.c1]};
-        }
-        t += step_t;
-        within += step_w;
+    for (; t < p.num_tokens; t += step_t, within += step_w) {
         if (within >= per_token) {
             within -= per_token;
-            ++t;
+            if (++t >= p.num_tokens) break;
         }
-    };
-    auto finish = [&](RowUnit &u) {
-        if (u.t >= p.num_tokens || u.slot < 0) return;    // a negative slot: no token here
-        if (u.slot >= p.num_slots || u.pos < 0 || u.pos >= p.max_positions) {
-            if (u.head == 0 && u.i == 0)
-                atomicOr(p.status, u.slot >= p.num_slots ? PKV_DEV_BAD_SLOT : PKV_DEV_BAD_POS);
-            return;
+        const int group = p.lane_shift >= 0 ? within >> p.lane_shift : within / lanes;
+        const int i = within - group * lanes;
+        const ChunkPair cp = chunk_pair<NEIGHBOURS>(i, p.rotary_dim);
+        const int64_t slot = p.slots[t];
+        const int pos = p.positions[t];
+        Chunks w[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const int h = group + j * groups;             // neighbouring threads, neighbouring heads
+            if (R > 1 && h >= heads) break;
+            const uint16_t *row =
+                h < p.num_q_heads ? static_cast<const uint16_t *>(p.q) + t * p.q_stride + h * D
+                : h < turned_heads
+                    ? static_cast<const uint16_t *>(p.k) + t * p.k_stride + (h - p.num_q_heads) * D
+                    : static_cast<const uint16_t *>(p.v) + t * p.v_stride + (h - turned_heads) * D;
+            w[j] = {reinterpret_cast<const uint4 *>(row)[cp.c0], reinterpret_cast<const uint4 *>(row)[cp.c1]};
         }
-        const ChunkPair cp = chunk_pair<NEIGHBOURS>(u.i, p.rotary_dim);
-        const int h = u.head - p.num_q_heads;
-        if (h < heads_kv && cp.turned) {
-            Values x = unpack16<BF16, NEIGHBOURS>(u.w.w0, u.w.w1);
-            turn16<false>(p, x, u.i, p.rotary_dim >> 1, p.cos_sin + (int64_t)u.pos * p.rotary_dim);
-            u.w = pack16<BF16, NEIGHBOURS>(x);
+        if (slot < 0) continue;                           // no token here
+        if (slot >= p.num_slots || pos < 0 || pos >= p.max_positions) {
+            if (within == 0) atomicOr(p.status, slot >= p.num_slots ? PKV_DEV_BAD_SLOT : PKV_DEV_BAD_POS);
+            continue;
         }
-        uint4 *dst;
-        if (h < 0) {
-            dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.q_out) + u.t * p.q_out_stride +
-                                            (int64_t)u.head * D);
-        } else {
-            const int64_t block =
-                p.block_shift >= 0 ? u.slot >> p.block_shift : u.slot / p.block_size;
-            const int64_t off = u.slot - block * p.block_size;
-            const int kvh = h < heads_kv ? h : h - heads_kv;
-            dst = (h < heads_kv ? p.k_pool : p.v_pool) +
-                  ((block * heads_kv + kvh) * p.block_size + off) * (D >> 3);
+        if (cp.turned && group < turned_heads) {
+            const Angles a =
+                angles<false>(i, p.rotary_dim >> 1, p.cos_sin + (int64_t)pos * p.rotary_dim);
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                if (R > 1 && group + j * groups >= turned_heads) break;
+                Values x = unpack16<BF16, NEIGHBOURS>(w[j].w0, w[j].w1);
+                turn16(p, x, a);
+                w[j] = pack16<BF16, NEIGHBOURS>(x);
+            }
         }
-        dst[cp.c0] = u.w.w0;
-        dst[cp.c1] = u.w.w1;
-    };
-    while (t < p.num_tokens) {
-        RowUnit a, b;
-        load(a);
-        load(b);
-        finish(a);
-        finish(b);
+        const int64_t block = p.block_shift >= 0 ? slot >> p.block_shift : slot / p.block_size;
+        const int off = (int)(slot - block * p.block_size);
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const int h = group + j * groups, kh = h - p.num_q_heads, vh = h - turned_heads;
+            if (R > 1 && h >= heads) break;
+            uint4 *dst;
+            if (kh < 0)
+                dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.q_out) + t * p.q_out_stride + h * D);
+            else
+                dst = (vh < 0 ? p.k_pool : p.v_pool) +
+                      ((block * heads_kv + (vh < 0 ? kh : vh)) * p.block_size + off) * (D >> 3);
+            dst[cp.c0] = w[j].w0;
+            dst[cp.c1] = w[j].w1;
+        }
     }
 }
 
-template <bool BF16, bool NEIGHBOURS>
+template <bool BF16, bool NEIGHBOURS, int R>
 __global__ void __launch_bounds__(256) append_rope_kernel(Params p, int D, int heads_kv)
 {
     begin();
     after_wait(p.cos_sin);
-    append_rows<BF16, NEIGHBOURS>(p, D, heads_kv, blockIdx.x, gridDim.x);
+    append_rows<BF16, NEIGHBOURS, R>(p, D, heads_kv, blockIdx.x, gridDim.x);
 }
 
 // ------------------------------------------------------- block-scaled 8-bit pools
@@ -560,7 +563,7 @@ __device__ __forceinline__ void b8_write_run(const Params &p, const Run<D> &u, i
             b8_write_part<BF16, NEIGHBOURS, true>(p, u, 0, cp, keep, lane, staged, [&](int k, Values &x) {
                 const float *cs = cos_sin + (SHARED ? (int64_t)((k * kRows + u.r) * (D + kTablePad))
                                                     : (int64_t)pos[k] * p.rotary_dim);
-                if (cp.turned) turn16<SHARED>(p, x, u.i, p.rotary_dim >> 1, cs);
+                if (cp.turned) turn16(p, x, angles<SHARED>(u.i, p.rotary_dim >> 1, cs));
             });
         else
             b8_write_part<BF16, NEIGHBOURS, false>(p, u, 0, cp, keep, lane, staged, [](int, Values &) {});
@@ -612,8 +615,8 @@ __global__ void __launch_bounds__(128, 6) append_b8_kernel(Params p)
     begin();
     after_wait(p.cos_sin);
     if ((int)blockIdx.x >= p.write_blocks) {              // queries only
-        append_rows<BF16, NEIGHBOURS>(p, D, 0, (int)blockIdx.x - p.write_blocks,
-                                      (int)gridDim.x - p.write_blocks);
+        append_rows<BF16, NEIGHBOURS, 1>(p, D, 0, (int)blockIdx.x - p.write_blocks,
+                                         (int)gridDim.x - p.write_blocks);
         return;
     }
     __shared__ uint4 stages[4 * 2 * D];
@@ -658,7 +661,8 @@ __global__ void __launch_bounds__(32 * kSpanWarps, 3) append_b8_span_kernel(Para
     // compute while its others wait for memory
     const int64_t before = (int64_t)blockIdx.x * p.write_blocks / gridDim.x;
     if ((int64_t)(blockIdx.x + 1) * p.write_blocks / gridDim.x == before) {
-        append_rows<BF16, NEIGHBOURS>(p, D, 0, (int)(blockIdx.x - before), (int)gridDim.x - p.write_blocks);
+        append_rows<BF16, NEIGHBOURS, kRowHeads>(p, D, 0, (int)(blockIdx.x - before),
+                                                 (int)gridDim.x - p.write_blocks);
         return;
     }
     const int spans = (int)(((int64_t)p.num_tokens + 15) / 16);
@@ -756,9 +760,13 @@ constexpr int64_t kSpans = 200;
 template <bool BF16, bool NEIGHBOURS>
 static int launch_rows(const Params &p, int D, int heads_kv, cudaStream_t st)
 {
-    const int64_t threads = (int64_t)p.num_tokens * (p.num_q_heads + 2 * heads_kv) * (D / 16);
-    const int64_t grid = std::min<int64_t>((threads + 511) / 512, 152 * 64);   // two units a thread
-    return launch(&append_rope_kernel<BF16, NEIGHBOURS>, dim3((unsigned)grid), 256, 0, st, p, D, heads_kv);
+    const int heads = p.num_q_heads + 2 * heads_kv;
+    const int64_t rows = (int64_t)p.num_tokens * (D / 16), many = rows * ((heads + kRowHeads - 1) / kRowHeads);
+    const bool by_four = !NEIGHBOURS && many >= kRowHeadsFrom;
+    const int64_t grid = std::min<int64_t>(((by_four ? many : rows * heads) + 255) / 256, 152 * 64);
+    return launch(by_four ? &append_rope_kernel<BF16, NEIGHBOURS, NEIGHBOURS ? 1 : kRowHeads>
+                          : &append_rope_kernel<BF16, NEIGHBOURS, 1>,
+                  dim3((unsigned)grid), 256, 0, st, p, D, heads_kv);
 }
 
 template <bool BF16, bool NEIGHBOURS>
@@ -770,10 +778,12 @@ static int launch_b8(const Params &p0, int D, bool queries, cudaStream_t st)
         p.write_blocks = (int32_t)std::min<int64_t>(spans, 152 * 64);
         int64_t grid = p.write_blocks;
         if (queries) {
-            // units a thread (20,500 and 4,000 tokens): 2 101 and 23.0 us, 4 95 and 21.5,
-            // 8 93 and 19.8, 16 97 and 24.8; in a launch of their own before 96 and 23.1
-            const int64_t units = (int64_t)p.num_tokens * p.num_q_heads * (D / 16);
-            grid += std::min<int64_t>((units + 256 * 8 - 1) / (256 * 8), 152 * 64);
+            // kRowHeads rows at a time, four times a thread: 3,300, 8,000 and 20,500 tokens
+            // 12.9, 34.5, 75.6 us; once 15.6, 36.7, 80.4; two rows 15.3, 37.8, 85.9; one
+            // row 18.0, 43.6, 101
+            const int64_t units =
+                (int64_t)p.num_tokens * ((p.num_q_heads + kRowHeads - 1) / kRowHeads) * (D / 16);
+            grid += std::min<int64_t>((units + 1023) / 1024, 152 * 64);
         }
         const int smem = kSpanWarps * 32 * D;
         void (*fn)(Params) = D == 128 ? &append_b8_span_kernel<BF16, NEIGHBOURS, 128>
