@@ -96,14 +96,6 @@ __device__ __forceinline__ ChunkPair chunk_pair(int i, int rotary_dim)
     return ChunkPair{2 * i, 2 * i + 1, false};
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float *x)
-{
-    using E = Elem<BF16>;
-    return make_uint4(E::pack(x[0], x[1]), E::pack(x[2], x[3]), E::pack(x[4], x[5]),
-                      E::pack(x[6], x[7]));
-}
-
 constexpr uint64_t kMinusZeros = 0x8000000080000000ull;
 
 // The kernels work on pairs of fp32 values in packed operations, half as many
@@ -705,9 +697,34 @@ __global__ void __launch_bounds__(32 * kSpanWarps, 3) append_b8_span_kernel(Para
     }
 }
 
-// Records of blocks ids[0 .. n) as K and V rows [n][Hkv][16][D] of the row type:
-// a thread takes one 16-byte code chunk of K and the same of V (four 16-byte
-// stores).
+// Records of blocks ids[0 .. n) as K and V rows [n][Hkv][16][D] of the row type: a unit
+// is 8 codes of K and the same 8 of V, the e-th unit the e-th 16 bytes of either result;
+// a thread has two units under way.  A code becomes fp32 as the low byte of 2^23 + byte.
+// 203, 800 and 5,000 blocks of 8 heads of 128: 4.1, 10.3, 76 us (4.9, 7.7 from L2, 6.5
+// TB/s); by 16 codes and integer conversions, one unit at a time, 6.2, 13.3, 78.
+struct RecordUnit {
+    int64_t e;
+    uint2 k, v;
+    float2 scales;
+};
+
+template <bool BF16>
+__device__ __forceinline__ uint4 b8_values8(const uint2 &w, float scale)
+{
+    constexpr float kFirst = 8388608.0f;                  // 2^23
+    const uint64_t zero2 = pack2f(-(kFirst + 128.f), -(kFirst + 128.f)), scale2 = pack2f(scale, scale);
+    uint32_t out[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const uint32_t u = m < 2 ? w.x : w.y;
+        const uint64_t x = pack2f(__uint_as_float(__byte_perm(u, __float_as_uint(kFirst), m & 1 ? 0x7652 : 0x7650)),
+                                  __uint_as_float(__byte_perm(u, __float_as_uint(kFirst), m & 1 ? 0x7653 : 0x7651)));
+        const float2 y = unpack2f(mul2f(add2f(x, zero2), scale2));
+        out[m] = Elem<BF16>::pack(y.x, y.y);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
 template <bool BF16, int D>
 __global__ void __launch_bounds__(256)
     dequantize_kernel(const uint8_t *kv, const int32_t *ids, int32_t n, int32_t num_kv_heads,
@@ -716,37 +733,39 @@ __global__ void __launch_bounds__(256)
     begin();
     after_wait(kv);
     after_wait(ids);
-    constexpr int kChunks = D;                            // chunks of K (or V) of a record
-    const uint32_t per_block = (uint32_t)num_kv_heads * kChunks;
-    const int64_t total = (int64_t)n * per_block;
-    for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < total;
-         e += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t b = total <= UINT32_MAX ? (int64_t)((uint32_t)e / per_block) : e / per_block;
-        const int within = (int)(e - b * per_block);
-        const int h = within / kChunks, c = within % kChunks;
-        const int t = c / (D / 16), j = c % (D / 16);
+    constexpr int kUnits = 2 * D;                         // of a record
+    const int64_t total = (int64_t)n * num_kv_heads * kUnits;
+    auto load = [&](RecordUnit &u, int64_t e) {
+        u.e = -1;
+        if (e >= total) return;
+        const int64_t record = e / kUnits;
+        const int within = (int)(e % kUnits), t = within / (D / 8), half = within % (D / 8);
+        const int64_t b = record <= UINT32_MAX ? (int64_t)((uint32_t)record / (uint32_t)num_kv_heads)
+                                               : record / num_kv_heads;
+        const int h = (int)(record - b * num_kv_heads);
         const int32_t id = __ldg(ids + b);
         if (id < 0 || id >= num_blocks) {
-            if (within == 0) atomicOr(status, PKV_DEV_BAD_BLOCK);
-            continue;
+            if (within == 0 && h == 0) atomicOr(status, PKV_DEV_BAD_BLOCK);
+            return;
         }
+        u.e = e;
         const uint8_t *rec = kv + ((int64_t)id * num_kv_heads + h) * PKV_B8_RECORD_BYTES(D);
-        const uint4 w[2] = {__ldcs(reinterpret_cast<const uint4 *>(rec + b8_chunk(t, j, D))),
-                            __ldcs(reinterpret_cast<const uint4 *>(rec + 16 * D + b8_chunk(t, j, D)))};
-        const float2 scales = __ldg(reinterpret_cast<const float2 *>(rec + 32 * D));
-        const int64_t at = (((b * num_kv_heads + h) * kBlock + t) * D + 16 * j) / 8;
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-            const float scale = part ? scales.y : scales.x;
-            const uint32_t u[4] = {w[part].x, w[part].y, w[part].z, w[part].w};
-            float x[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-                x[k] = __fmul_rn((float)((int)((u[k >> 2] >> (8 * (k & 3))) & 0xffu) - 128), scale);
-            uint4 *out = (part ? v_out : k_out) + at;
-            out[0] = pack8<BF16>(x);
-            out[1] = pack8<BF16>(x + 8);
-        }
+        const uint8_t *codes = rec + b8_chunk(t, half >> 1, D) + 8 * (half & 1);
+        u.k = __ldcs(reinterpret_cast<const uint2 *>(codes));
+        u.v = __ldcs(reinterpret_cast<const uint2 *>(codes + 16 * D));
+        u.scales = __ldg(reinterpret_cast<const float2 *>(rec + 32 * D));
+    };
+    auto finish = [&](const RecordUnit &u) {
+        if (u.e < 0) return;
+        k_out[u.e] = b8_values8<BF16>(u.k, u.scales.x);
+        v_out[u.e] = b8_values8<BF16>(u.v, u.scales.y);
+    };
+    for (int64_t e = (int64_t)blockIdx.x * 512 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 512) {
+        RecordUnit a, c;
+        load(a, e);
+        load(c, e + 256);
+        finish(a);
+        finish(c);
     }
 }
 
@@ -936,8 +955,8 @@ extern "C" int kv_dequantize_blocks(const pkv_pool *pool, const int32_t *ids, in
     if (!pkv::aligned16(kv_b8) || !pkv::aligned16(k_out) || !pkv::aligned16(v_out) ||
         ((uintptr_t)ids & 3u) || ((uintptr_t)d_status & 3u))
         return PKV_ERR_INVALID_ARG;
-    const int64_t total = (int64_t)n * g.num_kv_heads * g.head_dim;
-    const int64_t grid = std::min<int64_t>((total + 255) / 256, 152 * 64);
+    const int64_t total = (int64_t)n * g.num_kv_heads * g.head_dim * 2;      // units
+    const int64_t grid = std::min<int64_t>((total + 511) / 512, 152 * 64);
     const bool bf = g.dtype == PKV_B8_BF16;
     auto fn = g.head_dim == 128 ? (bf ? &dequantize_kernel<true, 128> : &dequantize_kernel<false, 128>)
                                 : (bf ? &dequantize_kernel<true, 64> : &dequantize_kernel<false, 64>);
