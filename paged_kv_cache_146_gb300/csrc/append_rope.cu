@@ -13,8 +13,8 @@
 //
 // Every value is read once and written once, so the kernels are bound by HBM
 // (and, for a decode step's few rows, by the chain slot -> position -> table
-// row -> store and the launch): 13,300 tokens of 8 + 8 heads of 64 (84 MB) 14.8 us,
-// 5.7 TB/s with its ramp; the queries of 20,500 tokens (337 MB) 57 us, 5.9 TB/s.
+// row -> store and the launch): 20,500 tokens of 32 query and 8 kv heads of 128 (505 MB)
+// 78 to 81 us, 6.2 to 6.5 TB/s; into 8-bit blocks (463 MB) 75 us, 6.2 TB/s.
 #include <algorithm>
 
 #include <cuda_bf16.h>
