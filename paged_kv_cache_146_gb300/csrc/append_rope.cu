@@ -44,6 +44,7 @@ struct Params {
     int32_t *status;
     int32_t write_blocks;                // 8-bit write of few tokens: CTAs that write; the rest
                                          // rotate queries
+    int32_t parts;                       // of many tokens: CTAs that share a span's heads
     uint64_t minus_zeros;                // see mul2
 };
 
@@ -631,10 +632,10 @@ __global__ void __launch_bounds__(128, 6) append_b8_kernel(Params p)
     }
 }
 
-// Many tokens: a CTA takes a span of 16 and writes every run that begins there, the
-// (run, kv head) units dealt to its warps.  The table rows of the tokens that they
-// reach (up to 31) come to shared memory once, for all heads, while the rows of the
-// warps' first units are on their way.
+// Many tokens: a CTA takes a span of 16 and some of the kv heads (all, or a share of
+// `parts`) and writes every run that begins there, the (run, kv head) units dealt to
+// its warps.  The table rows of the tokens that they reach (up to 31) come to shared
+// memory once for its heads, while the rows of the warps' first units are on their way.
 constexpr int kSpanWarps = 8;
 constexpr int kSpanTokens = 31;
 
@@ -658,10 +659,12 @@ __global__ void __launch_bounds__(32 * kSpanWarps, 3) append_b8_span_kernel(Para
         return;
     }
     const int spans = (int)(((int64_t)p.num_tokens + 15) / 16);
-    for (int w = (int)before; w < spans; w += p.write_blocks) {
-        const int tb = w * 16;
-        const Runs runs = find_runs(p, tb, 16, lane, warp == 0);
-        const int n_leads = __popc(runs.leads), units = n_leads * p.num_kv_heads;
+    for (int64_t w = before; w < (int64_t)spans * p.parts; w += p.write_blocks) {
+        const int part = (int)(w % p.parts), tb = (int)(w / p.parts) * 16;
+        const int head0 = p.num_kv_heads * part / p.parts;
+        const int heads = p.num_kv_heads * (part + 1) / p.parts - head0;
+        const Runs runs = find_runs(p, tb, 16, lane, part == 0 && warp == 0);
+        const int n_leads = __popc(runs.leads), units = n_leads * heads;
         // of token tb - 1 + lane, asked for together with the slots
         const int at = tb - 1 + lane;
         const int lane_pos = p.positions && at >= 0 && at < p.num_tokens ? p.positions[at] : -1;
@@ -687,7 +690,7 @@ __global__ void __launch_bounds__(32 * kSpanWarps, 3) append_b8_span_kernel(Para
             for (int i = 0; i < k; ++i) left &= left - 1;
             const int l = __ffs(left) - 1;
             const int64_t s0 = __shfl_sync(kFull, runs.slot, l);
-            const Run<D> run(p, tb - 1 + l, runs.length(l), s0, h, lane);
+            const Run<D> run(p, tb - 1 + l, runs.length(l), s0, head0 + h, lane);
             b8_write_run<BF16, NEIGHBOURS, D, true, 3>(p, run, lane, positions + l - 1,
                                                        table + (l - 1) * kStride, stage, [&] {
                                                            if (u == warp) fill();
@@ -769,12 +772,16 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// From this many spans of 16 tokens on, a CTA per span; below, a warp per token.  With
-// 32 query and 8 kv heads, tokens of prompts: 1,000 10.3 us by spans, 9.3 by tokens;
-// 2,000 10.8 and 14.6; tokens of as many sequences (a CTA then writes 128 runs): 1,000
-// 48 and 14, 3,000 62 and 36, 6,000 92 and 74.  The limit lies above the numbers of
-// sequences that decode together.
-constexpr int64_t kSpans = 200;
+// From this many values of K on, by spans of 16 tokens; below, a warp per token, head and
+// part.  Prompts, by tokens and by spans: 32/8 heads of 128 1,500 tokens 12.1 and 12.6 us,
+// 2,000 15.2 and 15.2, 3,000 20.9 and 16.9; 40/40 heads 320 tokens 11.2 and 11.4, 1,000
+// 23.2 and 15.0; 8/2 heads of 64 6,000 tokens 9.8 and 11.2, 20,500 21.5 and 20.2.
+constexpr int64_t kSpanValues = 1 << 21;
+// A span's heads are shared by as many CTAs as fit at once (3 an SM): tokens of as many
+// sequences as there are tokens make 16 runs a span, and one CTA for all heads takes long
+// over them: 2,000 such tokens of 32/8 heads 55 us, 27.9 so (by tokens 26.5), 3,000 57.8
+// and 38.3 (39.5); of 40/40 heads 1,000 212 and 50 (50).
+constexpr int64_t kSpanCtas = 152 * 3;
 
 template <bool BF16, bool NEIGHBOURS>
 static int launch_rows(const Params &p, int D, int heads_kv, cudaStream_t st)
@@ -793,8 +800,9 @@ static int launch_b8(const Params &p0, int D, bool queries, cudaStream_t st)
 {
     Params p = p0;
     const int64_t spans = ((int64_t)p.num_tokens + 15) / 16;
-    if (spans >= kSpans) {
-        p.write_blocks = (int32_t)std::min<int64_t>(spans, 152 * 64);
+    if ((int64_t)p.num_tokens * p.num_kv_heads * D >= kSpanValues) {
+        p.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>(kSpanCtas / spans, p.num_kv_heads));
+        p.write_blocks = (int32_t)std::min<int64_t>(spans * p.parts, 152 * 64);
         int64_t grid = p.write_blocks;
         if (queries) {
             // kRowHeads rows at a time, four times a thread: 3,300, 8,000 and 20,500 tokens

@@ -370,7 +370,10 @@ def test_repeated_captured_and_concurrent_calls_agree():
 
 @pytest.mark.parametrize("dtype,dim,rot,hq,hkv,interleaved", [
     ("bf16", 128, 128, 4, 8, False), ("f16", 128, 64, 2, 3, True), ("f16", 64, 64, 3, 1, False),
-    ("bf16", 64, 16, 0, 9, True), ("bf16", 128, 112, 5, 2, False)])
+    ("bf16", 64, 16, 0, 9, True), ("bf16", 128, 112, 5, 2, False),
+    # values enough for spans of tokens
+    ("f16", 128, 64, 2, 6, True), ("f16", 64, 64, 3, 11, False), ("bf16", 64, 16, 0, 13, True),
+    ("bf16", 128, 112, 5, 7, False), ("f16", 128, 128, 3, 40, True)])
 def test_many_tokens_with_gaps_and_odd_values(dtype, dim, rot, hq, hkv, interleaved):
     """Thousands of tokens of ragged sequences, some blocks cut short, some tokens
     refused, infinities and NaN among the values, queries turned in place."""
@@ -417,3 +420,28 @@ def test_many_tokens_with_gaps_and_odd_values(dtype, dim, rot, hq, hkv, interlea
         want[torch.from_numpy(kept < 0)] = q[torch.from_numpy(kept < 0)]
         assert torch.equal(gq.cpu(), want)
     assert torch.equal(gk.cpu().view(torch.int16), k.contiguous().view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype,dim,hq,hkv,tokens", [("bf16", 128, 3, 33, 520), ("f16", 64, 2, 80, 421)])
+def test_many_heads_and_one_token_per_sequence(dtype, dim, hq, hkv, tokens):
+    """Enough values for spans of tokens, every token a run of its own."""
+    rng = np.random.default_rng(tokens)
+    nb = tokens + 5
+    pool, ref = random_pool(nb, hkv, dim, dtype, 31)
+    slots = (rng.permutation(nb)[:tokens] * 16 + rng.integers(0, 16, tokens)).astype(np.int64)
+    slots[::41] = -1
+    pos = rng.integers(0, 90, tokens).astype(np.int32)
+    table = rope_table(90, dim)
+    gen = torch.Generator().manual_seed(32)
+    q, k, v = (torch.randn((tokens, h, dim), generator=gen).to(DT[dtype]) for h in (hq, hkv, hkv))
+    status = new_status()
+    out = torch.zeros_like(q).cuda()
+    cache_write_rope(pool, k.cuda(), v.cuda(), torch.from_numpy(pos).cuda(), table.cuda(),
+                     torch.from_numpy(slots).cuda(), status, q=q.cuda(), q_out=out)
+    assert status_check(status) == (0, 0)
+    ref.append(0, rotate_f32(k.float().numpy(), table, pos, False), slots)
+    ref.append(1, v.float().numpy(), slots)
+    same_records(pool, ref)
+    want = torch.from_numpy(rotate_f32(q.float().numpy(), table, pos, False)).to(DT[dtype])
+    want[torch.from_numpy(slots < 0)] = 0
+    assert torch.equal(out.cpu(), want)
