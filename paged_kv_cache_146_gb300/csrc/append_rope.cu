@@ -42,8 +42,7 @@ struct Params {
     uint4 *k_pool, *v_pool;              // 16-bit pools
     uint8_t *kv;                         // 8-bit records
     int32_t *status;
-    int32_t write_blocks;                // 8-bit write of few tokens: CTAs that write; the rest
-                                         // rotate queries
+    int32_t write_blocks;                // 8-bit write: CTAs that write; the rest rotate queries
     int32_t parts;                       // of many tokens: CTAs that share a span's heads
     uint64_t minus_zeros;                // see mul2
 };
