@@ -178,3 +178,42 @@ def test_captured_and_on_another_stream():
     graph.replay()
     assert status_check(status) == (0, 0)
     check(pool, q, k, v, slots, pos, table, q_out, False)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype,dim,rot,hq,hkv,T", [
+    ("bf16", 128, 128, 5, 3, 9000), ("f16", 96, 48, 7, 2, 9100), ("bf16", 256, 240, 1, 1, 11000),
+    ("f16", 64, 64, 0, 3, 40000), ("bf16", 256, 256, 24, 2, 24000)])
+def test_many_tokens_equal_few_at_a_time(dtype, dim, rot, hq, hkv, T, interleaved):
+    """One large call gives the bits of many small ones: heads that do not divide into
+    groups, more work than the grid has threads, padding and refused positions."""
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    dt = {"bf16": torch.bfloat16, "f16": torch.float16}[dtype]
+    qkv = torch.randn((T, (hq + 2 * hkv) * dim), device="cuda", generator=gen).to(dt)
+    q, k, v = (p.view(T, -1, dim) for p in qkv.split([hq * dim, hkv * dim, hkv * dim], 1))
+    nb = T // 16 + 2
+    slots = torch.randperm(nb * 16, device="cuda", generator=gen)[:T]
+    slots[::97] = -1
+    pos = torch.randint(0, 700, (T,), device="cuda", generator=gen, dtype=torch.int32)
+    pos[5::1013] = 700
+    table = rope_table(700, rot).cuda()
+    got = []
+    for step in (T, 997):
+        pool = KVPool(nb, hkv, dim, dtype, device="cuda")
+        for p in (pool.k_pool, pool.v_pool):
+            p.fill_(7.0)
+        q_out = torch.full((T, max(hq, 1), dim), 9.0, dtype=dt, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        for t in range(0, T, step):
+            part = slice(t, t + step)
+            cache_write_rope(pool, k[part], v[part], pos[part], table, slots[part], status,
+                             interleaved=interleaved,
+                             **(dict(q=q[part], q_out=q_out[part]) if hq else {}))
+        assert status_check(status)[1] == DEV_BAD_POS
+        got.append((pool.k_pool, pool.v_pool, q_out))
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    kept = (slots >= 0) & (pos < 700)
+    assert torch.equal(got[0][1][slots[kept] // 16, :, slots[kept] % 16], v[kept])
+    if hq:
+        assert bool((got[0][2][~kept] == 9).all()) and not bool((got[0][2][kept] == 9).all(-1).any())

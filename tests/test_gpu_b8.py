@@ -445,3 +445,33 @@ def test_many_heads_and_one_token_per_sequence(dtype, dim, hq, hkv, tokens):
     want = torch.from_numpy(rotate_f32(q.float().numpy(), table, pos, False)).to(DT[dtype])
     want[torch.from_numpy(slots < 0)] = 0
     assert torch.equal(out.cpu(), want)
+
+
+@pytest.mark.parametrize("dtype,dim,hkv,n", [("bf16", 128, 8, 2700), ("f16", 64, 7, 5900)])
+def test_many_blocks_read_back_equal_few_at_a_time(dtype, dim, hkv, n):
+    """More blocks than one round of the grid takes, some refused."""
+    nb = 900
+    pool = KVPool(nb, hkv, dim, "b8_" + dtype, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    pool.kv.random_(0, 256, generator=gen)
+    pool.kv[:, :, 32 * dim:].view(torch.float32).uniform_(0.01, 3.0, generator=gen)
+    ids = torch.randint(0, nb, (n,), device="cuda", generator=gen, dtype=torch.int32)
+    ids[7::501], ids[9::501] = -1, nb
+    got = []
+    for step in (n, 61):
+        out = [torch.full((n, hkv, 16, dim), 5.0, dtype=DT[dtype], device="cuda") for _ in "kv"]
+        status = new_status()
+        for i in range(0, n, step):
+            dequantize_blocks(pool, ids[i:i + step], out[0][i:i + step], out[1][i:i + step], status)
+        assert status_check(status)[1] == DEV_BAD_BLOCK
+        got.append(out)
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    bad = (ids < 0) | (ids >= nb)
+    assert bool((got[0][0][bad] == 5).all())
+    # K of one block by the formula: byte - 128 times the scale, rounded once
+    i = int((~bad).nonzero()[3])
+    scale = pool.kv[ids[i], :, 32 * dim:].view(torch.float32)[:, 0]
+    codes = Records.from_bytes(pool.kv[ids[i]:ids[i] + 1].cpu().numpy()).codes[0, 0]
+    want = (torch.from_numpy(codes).float().cuda() * scale[:, None, None]).to(DT[dtype])
+    assert torch.equal(got[0][0][i], want)
