@@ -50,6 +50,7 @@ struct Params {
     float *part_o;              // [pairs * Hkv * G * D]: unnormalised partition output
     int32_t *status;
     const uint8_t *kv_q8;       // 8-bit pool: one record of kQ8Slab bytes per (block, kv head)
+    int32_t planned;            // the plan came with the call: no prep kernel before the main one
     int64_t max_pairs;          // capacity of items / partial arrays (checked builds)
     int32_t *debug;             // first failed check: site << 24 | value (checked builds)
 };
@@ -98,9 +99,13 @@ Q8KernelInfo q8_kernel_info(bool bf16_queries);
 #ifdef __CUDACC__
 // Output rows of sequences with no context, or with a length the table cannot
 // hold, are zeros.  context_lens is an input of the call, not something the
-// prep kernel writes, so each main kernel's CTAs store these rows before they
-// wait for the prep kernel's work list, while it still runs (grid-stride over
-// sequences, the CTA's threads over the row's 16-byte pieces).  Not inlined,
+// prep kernel writes, so behind a prep kernel each main kernel's CTAs store these
+// rows before they wait for its work list, while it still runs (grid-stride over
+// sequences, the CTA's threads over the row's 16-byte pieces).  That is sound
+// because the prep kernel, launched without the programmatic attribute, starts
+// only when everything before it has ended.  A planned call has no prep kernel:
+// the kernel before its main kernel may be any other call's, one that still reads
+// or writes this call's `out`, so there the wait comes first.  Not inlined,
 // so it leaves the main loop's register allocation alone; its arguments are
 // values, so no copy of the kernel's parameters is taken.
 static __device__ __noinline__ void zero_idle_rows(void *out, const int32_t *context_lens,

@@ -487,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
+    if (p.planned) griddep_wait(); // another call's kernel may still use `out`
     zero_idle_rows(p.out, p.context_lens, p.num_seqs, p.num_q_heads * D * 2,
                    (int64_t)p.max_blocks_per_seq * kBlock);
     griddep_wait();                // the work list comes from the prep kernel
@@ -1179,6 +1180,7 @@ static int launch(const pkv_pool *pool, void *out, const void *q, const void *k_
     prm.multi = reinterpret_cast<int32_t *>(ws + w.multi);
     prm.status = d_status;
     prm.kv_q8 = want_8bit ? static_cast<const uint8_t *>(k_pool) : nullptr;
+    prm.planned = planned >= 0;
     prm.max_pairs = w.max_pairs;
     prm.debug = prm.header + 1;
     // (a plan without shared-prefix items has zero skips: the kernels need not read them)
