@@ -50,8 +50,15 @@ struct Params {
 // Every kernel here is launched with the programmatic attribute: it may be set up
 // while the kernel before it in the stream ends, lets the next one do the same, and
 // waits for the end of the one before it ahead of its first access to memory.
-// Arrays that earlier kernels may have written are read by plain loads, or through a
-// pointer that passed here: neither moves above the wait.
+// What a call of this library may have written (rows, pools, scales) is read by plain
+// or streaming loads (ld, ld.cs), not by __ldg: that one wants its data unchanged for
+// the whole life of the kernel, and this life begins before the wait, while an append
+// may still raise the scales that a read-back needs.  The cos/sin table is no call's
+// output, and a kernel that does not let its successor start early (any other that
+// fills the table) has ended before this life begins, so __ldg may read it (plain
+// loads there: 13,300 tokens 17.8 us against 16.2, 20,500 into 8-bit blocks 103.5
+// against 97.9).  A plain load does not move above the wait, the others when their
+// pointer passed here.
 __device__ __forceinline__ void begin()
 {
     griddep_launch_dependents();
@@ -734,7 +741,6 @@ __global__ void __launch_bounds__(256)
 {
     begin();
     after_wait(kv);
-    after_wait(ids);
     constexpr int kUnits = 2 * D;                         // of a record
     const int64_t total = (int64_t)n * num_kv_heads * kUnits;
     auto load = [&](RecordUnit &u, int64_t e) {
@@ -745,7 +751,7 @@ __global__ void __launch_bounds__(256)
         const int64_t b = record <= UINT32_MAX ? (int64_t)((uint32_t)record / (uint32_t)num_kv_heads)
                                                : record / num_kv_heads;
         const int h = (int)(record - b * num_kv_heads);
-        const int32_t id = __ldg(ids + b);
+        const int32_t id = ids[b];
         if (id < 0 || id >= num_blocks) {
             if (within == 0 && h == 0) atomicOr(status, PKV_DEV_BAD_BLOCK);
             return;
@@ -755,7 +761,7 @@ __global__ void __launch_bounds__(256)
         const uint8_t *codes = rec + b8_chunk(t, half >> 1, D) + 8 * (half & 1);
         u.k = __ldcs(reinterpret_cast<const uint2 *>(codes));
         u.v = __ldcs(reinterpret_cast<const uint2 *>(codes + 16 * D));
-        u.scales = __ldg(reinterpret_cast<const float2 *>(rec + 32 * D));
+        u.scales = *reinterpret_cast<const float2 *>(rec + 32 * D);
     };
     auto finish = [&](const RecordUnit &u) {
         if (u.e < 0) return;
