@@ -162,6 +162,8 @@ template <int D, int NT>
 struct State {
     float o[NT][D / 16][4];
     float m[NT][2], l[NT][2];
+    // the same for the warp: some head has no finite m yet; some |m| > 2^24 (see softmax_step)
+    bool none, wide;
 };
 
 // The query rows of a kv head as B operands (head r of tile nt); for 8-bit pools
@@ -175,6 +177,8 @@ struct Queries {
 template <int D, int NT>
 __device__ __forceinline__ void reset(State<D, NT> &st)
 {
+    st.none = true;
+    st.wide = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         st.m[nt][0] = st.m[nt][1] = -INFINITY;
@@ -190,72 +194,107 @@ __device__ __forceinline__ void reset(State<D, NT> &st)
 // lazy reference maximum m; x[b][nt] = (r, head 0), (r, head 1), (r + 8, head 0),
 // (r + 8, head 1), f[b][nt] = the heads' factors to the log2 domain, hidden
 // tokens' bits 0 in masks[b].
+// A weight depends on its product and on m alone, whatever the block and the path by
+// which m came about: the exponent is taken from the product itself (one fma, the
+// product not rounded), also when this block moves m, and what was summed before is
+// scaled by the exact step of m.  Products beyond 2^24, whose spacing is a unit and
+// more, are rounded like the maximum that m was taken from (`wide`): unrounded ones
+// would lie up to half that spacing above it.
 template <int D, int NT, int NB>
 __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&x)[NB][NT][4],
                                              const float (&f)[NB][NT][2], const uint32_t (&masks)[NB],
                                              int lane)
 {
-    bool raise = false;
+    float y[NB][NT][4];                  // exponents, -inf for hidden tokens
+    auto is_wide = [](float m) { return m != -INFINITY && fabsf(m) > 0x1p24f; };
+    auto hide = [&]() {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+        for (int b = 0; b < NB; ++b) {
+            if (masks[b] == 0xffffu) continue;           // the same for the warp
+            const bool v0 = (masks[b] >> (lane >> 2)) & 1u, v1 = (masks[b] >> ((lane >> 2) + 8)) & 1u;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            raise |= st.m[nt][h] == -INFINITY;           // no token yet: x f is taken against 0
-            const float neg = st.m[nt][h] == -INFINITY ? 0.f : -st.m[nt][h];
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!(e < 2 ? v0 : v1)) y[b][nt][e] = -INFINITY;
+        }
+    };
+    auto exponents = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                // (no token yet: any finite reference, nothing visible has a weight)
+                const float neg = st.m[nt][h] == -INFINITY ? 0.f : -st.m[nt][h];
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        y[b][nt][2 * t + h] = fmaf(x[b][nt][2 * t + h], f[b][nt][h], neg);
+            }
+        if (st.wide) {                   // the same for the warp
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!is_wide(st.m[nt][h])) continue;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+                            y[b][nt][2 * t + h] = __fsub_rn(
+                                __fmul_rn(x[b][nt][2 * t + h], f[b][nt][h]), st.m[nt][h]);
+                }
+        }
+        hide();
+    };
+    bool raise = st.none;
+    if (!raise) {
+        exponents();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    float &y = x[b][nt][2 * t + h];
-                    y = fmaf(y, f[b][nt][h], neg);
-                }
-        }
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        if (masks[b] == 0xffffu) continue;               // the same for the warp
-        const bool v0 = (masks[b] >> (lane >> 2)) & 1u, v1 = (masks[b] >> ((lane >> 2) + 8)) & 1u;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (!(e < 2 ? v0 : v1)) x[b][nt][e] = -INFINITY;
+                for (int e = 0; e < 4; ++e) raise |= y[b][nt][e] > kLazy;
+        raise = __any_sync(kFull, raise);
     }
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
+    if (raise) {
+        bool none = false, wide = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) raise |= x[b][nt][e] > kLazy;
-    if (__any_sync(kFull, raise)) {
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[b][nt][e] = __fmul_rn(x[b][nt][e], f[b][nt][e & 1]);
+        hide();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float up = fmaxf(x[0][nt][h], x[0][nt][2 + h]);
+                float up = fmaxf(y[0][nt][h], y[0][nt][2 + h]);
 #pragma unroll
-                for (int b = 1; b < NB; ++b) up = fmaxf(up, fmaxf(x[b][nt][h], x[b][nt][2 + h]));
+                for (int b = 1; b < NB; ++b) up = fmaxf(up, fmaxf(y[b][nt][h], y[b][nt][2 + h]));
                 up = fmaxf(up, __shfl_xor_sync(kFull, up, 4));
                 up = fmaxf(up, __shfl_xor_sync(kFull, up, 8));
                 up = fmaxf(up, __shfl_xor_sync(kFull, up, 16));
-                // the reference moves up to the largest score (exactly to it at first)
-                const bool none = st.m[nt][h] == -INFINITY;
-                if (!none) up = fmaxf(up, 0.f);
-                const float s = none ? 1.f : fast_exp2(-up);
-                st.m[nt][h] = none ? up : st.m[nt][h] + up;
-                if (up == -INFINITY) up = 0.f;           // still no finite score
+                // the reference moves up to the largest score
+                const float old = st.m[nt][h], now = fmaxf(old, up);
+                const float s = old == -INFINITY ? 1.f : fast_exp2(old - now);
+                st.m[nt][h] = now;
+                none |= now == -INFINITY;
+                wide |= is_wide(now);
                 st.l[nt][h] *= s;
 #pragma unroll
                 for (int t = 0; t < D / 16; ++t) {
                     st.o[nt][t][h] *= s;
                     st.o[nt][t][2 + h] *= s;
                 }
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    x[b][nt][h] -= up;
-                    x[b][nt][2 + h] -= up;
-                }
             }
         }
+        st.none = __any_sync(kFull, none);
+        st.wide = __any_sync(kFull, wide);
+        exponents();
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -263,7 +302,7 @@ __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&x)[NB][NT
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                x[b][nt][e] = fast_exp2(x[b][nt][e]);
+                x[b][nt][e] = fast_exp2(y[b][nt][e]);
                 st.l[nt][e & 1] += x[b][nt][e];
             }
 }
