@@ -446,9 +446,10 @@ __device__ __forceinline__ int chunk_at(int t, int j)
 // (and q4 + 4) of tokens r and r + 8 as its A words, four dimensions to a step,
 // and the queries were laid out alike; of V it takes dimensions D/8 r ..
 // D/8 (r + 1) of its four tokens and pairs their bytes.
-// P: one fp16 part for bf16 rows (2^-12, below the output's 2^-9), two for fp16.
+// P: two fp16 parts, which carry a weight to 2^-22 (one part, 2^-11, would show in a
+// bf16 result: 8 of 10,000 of its norm against one rounded from 64 bits).
 // NB blocks at a time: their chains of dependent instructions overlap.
-template <int D, bool BF16, int NT, int NB>
+template <int D, int NT, int NB>
 __device__ __forceinline__ void consume_b8(const uint8_t *const (&recs)[NB],
                                            const Queries<D, NT> &qs, State<D, NT> &st,
                                            const uint32_t (&masks)[NB], int lane)
@@ -500,7 +501,7 @@ __device__ __forceinline__ void consume_b8(const uint8_t *const (&recs)[NB],
         for (int nt = 0; nt < NT; ++nt) {
             uint32_t raw[2];
             weights_hi<H>(x[b][nt], hi[nt], raw);
-            if constexpr (!BF16) weights_lo<H>(x[b][nt], raw, lo[nt]);
+            weights_lo<H>(x[b][nt], raw, lo[nt]);
         }
         float v_off[NT][4];              // -1152 x the weights' sums, every row alike
         {
@@ -508,7 +509,7 @@ __device__ __forceinline__ void consume_b8(const uint8_t *const (&recs)[NB],
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 H::mma0(v_off[nt], neg, hi[nt][0], hi[nt][1]);
-                if constexpr (!BF16) H::mma(v_off[nt], neg, lo[nt][0], lo[nt][1]);
+                H::mma(v_off[nt], neg, lo[nt][0], lo[nt][1]);
             }
         }
         // words of tokens 2q4, 2q4 + 1, 2q4 + 8, 2q4 + 9: four dimensions each
@@ -539,7 +540,7 @@ __device__ __forceinline__ void consume_b8(const uint8_t *const (&recs)[NB],
                 for (int nt = 0; nt < NT; ++nt) {
                     float c[4];
                     mma_from(c, a, hi[nt], v_off[nt]);
-                    if constexpr (!BF16) H::mma(c, a, lo[nt][0], lo[nt][1]);
+                    H::mma(c, a, lo[nt][0], lo[nt][1]);
                     float *o = st.o[nt][2 * i + pr];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[e] = fmaf(v_scale[b], c[e], o[e]);
@@ -804,7 +805,7 @@ __global__ void __launch_bounds__(32 * W, Shape<D, B8, NT, W>::kMinBlocks)
             if (!bad) {
                 const uint8_t *const recs[2] = {stage_of(i), stage_of(i + 1)};
                 const uint32_t masks[2] = {mask_of(i), mask_of(i + 1)};
-                consume_b8<D, BF16, NT, 2>(recs, qs, st, masks, lane);
+                consume_b8<D, NT, 2>(recs, qs, st, masks, lane);
             }
             released();
             issue(i + SH::kStages);
@@ -818,7 +819,7 @@ __global__ void __launch_bounds__(32 * W, Shape<D, B8, NT, W>::kMinBlocks)
             if constexpr (B8) {
                 const uint8_t *const recs[1] = {stage_of(i)};
                 const uint32_t masks[1] = {mask_of(i)};
-                consume_b8<D, BF16, NT, 1>(recs, qs, st, masks, lane);
+                consume_b8<D, NT, 1>(recs, qs, st, masks, lane);
             } else {
                 consume_16bit<D, BF16, NT>(smem_addr(stage_of(i)), qs, st, mask_of(i), p.scale_log2,
                                            lane);

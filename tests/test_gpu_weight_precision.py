@@ -1,0 +1,73 @@
+"""How precisely the attention calls carry a softmax weight into the product with V."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from paged_kv_cache_146_gb300 import KVPool, paged_decode_attention_b8, status_check  # noqa: E402
+from serving_reference import Records  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+HKV, NB = 2, 6                               # the pool is one sequence of 96 tokens
+
+
+def cancelling(kind, dim, c0, c1):
+    """A pool whose even tokens have score 0 and value c0 / 64, the odd ones a score of -scale and
+    the value -c1 / 64; with a window of two and scale = ln(c1 / c0) they cancel."""
+    pool = KVPool(NB, HKV, dim, kind, device="cuda")
+    if pool.is_b8:
+        r = Records(NB, HKV, dim)
+        r.scales[:] = 2.0 ** -6
+        r.codes[0, :, :, 1::2, 0] = -64
+        r.codes[1, :, :, 0::2], r.codes[1, :, :, 1::2] = c0, -c1
+        pool.kv.copy_(torch.from_numpy(r.to_bytes()))
+    else:
+        pool.k_pool.zero_()
+        pool.k_pool[:, :, 1::2, 0] = -1
+        pool.v_pool[:, :, 0::2], pool.v_pool[:, :, 1::2] = c0 / 64, -c1 / 64
+    return pool
+
+
+def query(rows, hq, dim, dt):
+    q = torch.zeros((rows, hq, dim), dtype=dt, device="cuda")
+    q[..., 0] = 1
+    return q
+
+
+def check(out, c0, c1, scale, weight, steps):
+    """The error of a weight is at most `weight` (its way into the product) + 2^-22 (exp2) + 2^-23
+    (its argument: the scale's product with log2 e) + 2^-22 (joining two warps' sums); the sums of
+    up to three products and the quotient add 5 2^-24; in all 2^-20 beside `weight`.  8-bit pools
+    add and take off 1152 steps of V (`steps` of them to a c0): four sums of up to 2304 steps with
+    an error of 2^-23 each.  The result's rounding is of a value near zero."""
+    w = math.exp(-float(torch.tensor(scale, dtype=torch.float32)))
+    room = (c0 / 64) * (weight + 2.0 ** -20 + steps * 4 * 2304 * 2.0 ** -23 / c0) / (1 + w)
+    want = (c0 - w * c1) / 64 / (1 + w)
+    half = torch.finfo(out.dtype).eps / 2
+    tiny = torch.finfo(out.dtype).smallest_normal * torch.finfo(out.dtype).eps / 2
+    worst = (out.double().cpu() - want).abs().max().item()
+    assert worst <= room + half * (abs(want) + room) + tiny, (c0, c1, worst / room)
+
+
+RATIOS = [(64 + i, 127 - i // 3) for i in range(0, 60, 4)]
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hq", [4, 24])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_8bit_decode(dtype, dim, hq):
+    """Two fp16 parts: 2^-22."""
+    lens = torch.arange(2, 96, dtype=torch.int32, device="cuda")
+    tables = torch.arange(NB, dtype=torch.int32, device="cuda").repeat(len(lens), 1)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for c0, c1 in RATIOS:
+        pool = cancelling("b8_" + dtype, dim, c0, c1)
+        scale = math.log(c1 / c0)
+        out = paged_decode_attention_b8(pool, query(len(lens), hq, dim, DT[dtype]), tables, lens, scale,
+                                        status, window=2)
+        check(out, c0, c1, scale, 2.0 ** -22, 1)
+    assert status_check(status) == (0, 0)
