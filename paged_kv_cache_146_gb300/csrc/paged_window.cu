@@ -48,9 +48,12 @@ namespace pkv {
 namespace window {
 
 constexpr int kMaxHeads = 16;            // query heads per kv head
-// The reference maximum moves only when a score exceeds it by more than this
-// (log2 units): weights stay within 2^6, far inside fp16's and bf16's range.
-constexpr float kLazy = 6.f;
+// The reference maximum moves only when a score exceeds it by more than kLazy (log2
+// units).  Where weights become fp16 (fp16 and 8-bit pools) it is taken kTop below the
+// largest score: weights stay within 2^14, the largest is at least 2^8, and those down
+// to 2^-22 of it are normal numbers in fp16 (2^-14 with the reference at the maximum: a
+// long context far below a few dominant tokens would lose its weights' bits).
+constexpr float kLazy = 6.f, kTop = 8.f, kTopInverse = 0x1p-8f;
 
 struct Params {
     void *out;
@@ -199,11 +202,11 @@ __device__ __forceinline__ void reset(State<D, NT> &st)
 // product not rounded), also when this block moves m, and what was summed before is
 // scaled by the exact step of m.  Products beyond 2^24, whose spacing is a unit and
 // more, are rounded like the maximum that m was taken from (`wide`): unrounded ones
-// would lie up to half that spacing above it.
+// would lie up to half that spacing above it.  top = kTop where weights become fp16, else 0.
 template <int D, int NT, int NB>
 __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&x)[NB][NT][4],
                                              const float (&f)[NB][NT][2], const uint32_t (&masks)[NB],
-                                             int lane)
+                                             float top, int lane)
 {
     float y[NB][NT][4];                  // exponents, -inf for hidden tokens
     auto is_wide = [](float m) { return m != -INFINITY && fabsf(m) > 0x1p24f; };
@@ -256,7 +259,7 @@ __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&x)[NB][NT
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) raise |= y[b][nt][e] > kLazy;
+                for (int e = 0; e < 4; ++e) raise |= y[b][nt][e] > top + kLazy;
         raise = __any_sync(kFull, raise);
     }
     if (raise) {
@@ -278,8 +281,10 @@ __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&x)[NB][NT
                 up = fmaxf(up, __shfl_xor_sync(kFull, up, 4));
                 up = fmaxf(up, __shfl_xor_sync(kFull, up, 8));
                 up = fmaxf(up, __shfl_xor_sync(kFull, up, 16));
-                // the reference moves up to the largest score
-                const float old = st.m[nt][h], now = fmaxf(old, up);
+                // the reference moves up with the largest score (from 2^24 on, where
+                // the spacing nears kTop, to it)
+                const float old = st.m[nt][h];
+                const float now = fmaxf(old, fabsf(up) > 0x1p24f ? up : up - top);
                 const float s = old == -INFINITY ? 1.f : fast_exp2(old - now);
                 st.m[nt][h] = now;
                 none |= now == -INFINITY;
@@ -367,7 +372,7 @@ __device__ __forceinline__ void consume_16bit(uint32_t kb, const Queries<D, NT> 
     }
     const bool edge = mask != 0xffffu;   // the same for the warp: an edge of the visible part
     const uint32_t masks[1] = {mask};
-    softmax_step<D, NT, 1>(st, x, f, masks, lane);
+    softmax_step<D, NT, 1>(st, x, f, masks, BF16 ? 0.f : kTop, lane);
     uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -440,8 +445,9 @@ __device__ __forceinline__ int chunk_at(int t, int j)
 
 // Codes are exact in fp16, so both products run on fp16 operands; the block's
 // two scales stay out of them: K's multiplies the scores, V's the block's
-// product as it is added to the accumulator (weights of at most 2^6 then keep
-// fp16's full precision whatever the scale).  The reduction over dimensions
+// product as it is added to the accumulator (weights then keep fp16's full
+// precision whatever the scale), less the 2^kTop of the weights, which values
+// near the largest bf16 leave no room for.  The reduction over dimensions
 // may take them in any order, so lane (r, q4) takes whole 16-byte chunks q4
 // (and q4 + 4) of tokens r and r + 8 as its A words, four dimensions to a step,
 // and the queries were laid out alike; of V it takes dimensions D/8 r ..
@@ -465,7 +471,7 @@ __device__ __forceinline__ void consume_b8(const uint8_t *const (&recs)[NB],
     for (int b = 0; b < NB; ++b) {
         const uint8_t *rec = recs[b];
         const float2 scales = *reinterpret_cast<const float2 *>(rec + 32 * D);
-        v_scale[b] = scales.y;
+        v_scale[b] = scales.y * kTopInverse;
         float c[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -493,7 +499,7 @@ __device__ __forceinline__ void consume_b8(const uint8_t *const (&recs)[NB],
             for (int e = 0; e < 4; ++e) x[b][nt][e] = c[nt][e];
         }
     }
-    softmax_step<D, NT, NB>(st, x, f, masks, lane);
+    softmax_step<D, NT, NB>(st, x, f, masks, kTop, lane);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         uint32_t hi[NT][2], lo[NT][2];
@@ -839,6 +845,7 @@ __global__ void __launch_bounds__(32 * W, Shape<D, B8, NT, W>::kMinBlocks)
             l += __shfl_xor_sync(kFull, l, 4);
             l += __shfl_xor_sync(kFull, l, 8);
             l += __shfl_xor_sync(kFull, l, 16);
+            if constexpr (B8) l *= kTopInverse;          // as the accumulators
             const int head = 8 * nt + 2 * q4 + h;
             if (r == 0) ml[warp * kMaxHeads + head] = make_float2(st.m[nt][h], bad ? -1.f : l);
             float *dst = piece + head * SH::kRow;

@@ -7,7 +7,8 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
-from paged_kv_cache_146_gb300 import KVPool, paged_decode_attention_b8, status_check  # noqa: E402
+from paged_kv_cache_146_gb300 import (KVPool, paged_decode_attention_b8,  # noqa: E402
+                                      paged_decode_attention_window, status_check)
 from serving_reference import Records  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -70,4 +71,65 @@ def test_8bit_decode(dtype, dim, hq):
         out = paged_decode_attention_b8(pool, query(len(lens), hq, dim, DT[dtype]), tables, lens, scale,
                                         status, window=2)
         check(out, c0, c1, scale, 2.0 ** -22, 1)
+    assert status_check(status) == (0, 0)
+
+
+# ------------------------------------------------------------- a few dominant tokens
+def dominated(kind, dim, n, first):
+    """A pool of one sequence of n tokens: the first ones have score 0 and value 0, the others a
+    score of -1 times the scale and the value 1."""
+    nb = -(-n // 16)
+    pool = KVPool(nb, HKV, dim, kind, device="cuda")
+    late = (torch.arange(nb * 16) >= first).view(nb, 1, 16)
+    if pool.is_b8:
+        r = Records(nb, HKV, dim)
+        r.scales[:] = 2.0 ** -6
+        r.codes[0, :, :, :, 0] = torch.where(late, -64, 0).numpy()
+        r.codes[1] = torch.where(late, 64, 0)[..., None].numpy()
+        pool.kv.copy_(torch.from_numpy(r.to_bytes()))
+    else:
+        pool.k_pool.zero_()
+        pool.k_pool[..., 0] = torch.where(late, -1.0, 0.0).to(pool.k_pool)
+        pool.v_pool.copy_(torch.where(late, 1.0, 0.0)[..., None].expand_as(pool.v_pool))
+    return pool, nb
+
+
+def check_dominated(out, n, first, bits, scale, weight, late, offset):
+    """n - first equal weights of 2^-bits against one.  Numerator and denominator are off by the
+    error of a weight (`weight` and 2^-20, see `check`), the numerator also by what fp16 cannot
+    hold of the late weights (`late`: with the largest weight 2^8 and a step of 2^-24 at the
+    small end, 2^-25 2^-8 2^bits) and by the sums' own error (some hundred additions a warp:
+    2^-16; of 8-bit pools with the offset, 1152 / 64 times that at most: 2^-14 is below the
+    former's rounding).  8-bit pools also add and take off 1152 steps times the dominant weight,
+    although its value is 0: the four sums of up to 2304 steps of `check`, 64 to a value, with a
+    weight of 1 here, so an absolute error of 4 2304 2^-23 / 64 = 2^-15.8 of the late tokens' value,
+    in the one block that holds the dominant token."""
+    w = math.exp(-float(torch.tensor(scale, dtype=torch.float32))) * (n - first)
+    want = w / (first + w)
+    rel = 2 * (weight + 2.0 ** -20) + late + 2.0 ** -14 + torch.finfo(out.dtype).eps / 2
+    rel += offset * 4 * 2304 * 2.0 ** -23 / 64 / want
+    worst = (out.double().cpu() / want - 1).abs().max().item()
+    assert worst <= rel, (bits, worst / rel)
+
+
+@pytest.mark.parametrize("kind,dim,hq", [("bf16", 128, 8), ("f16", 64, 4), ("f16", 128, 24), ("b8_bf16", 128, 8),
+                                         ("b8_f16", 64, 24)])
+@pytest.mark.parametrize("n", [1000, 24000])
+def test_decode_far_below_a_few_tokens(kind, dim, hq, n):
+    """The dominant tokens sit among the late ones' blocks of one warp, and alone in others'."""
+    dt = DT[kind.split("_")[-1]]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    pool, nb = dominated(kind, dim, n, 1)
+    tables = torch.arange(nb, dtype=torch.int32, device="cuda").view(1, nb)
+    for bits in (19.0, 20.37, 21.5, 22.0):
+        scale = bits * math.log(2.0)
+        q = query(1, hq, dim, dt)
+        if pool.is_b8:
+            out = paged_decode_attention_b8(pool, q, tables, lens, scale, status)
+        else:
+            out = paged_decode_attention_window(pool, q, tables, lens, scale, n, 0, status)
+        half = kind != "bf16"                        # weights become fp16
+        check_dominated(out, n, 1, bits, scale, 2.0 ** -22 if half else 2.0 ** -17,
+                        2.0 ** (bits - 33) if half else 0.0, pool.is_b8)
     assert status_check(status) == (0, 0)
