@@ -312,32 +312,30 @@ __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&x)[NB][NT
             }
 }
 
-// Weights x[4] of one head tile as the B operand of the P V product, in type E:
-// (b0, b1) = tokens 2 q4, 2 q4 + 1 and 8 + those, head r.
-template <typename E>
-__device__ __forceinline__ void weights_hi(const float (&x)[4], uint32_t (&b)[2], uint32_t (&raw)[2])
+// Weights x[4] of one head tile as B operands of the P V product, in PARTS parts of
+// type E, each the last ones' remainder rounded: (b0, b1) = tokens 2 q4, 2 q4 + 1 and
+// 8 + those, head r.  The remainders are exact.
+template <typename E, int PARTS>
+__device__ __forceinline__ void weight_parts(const float (&x)[4], uint32_t (&b)[PARTS][2])
 {
-    raw[0] = E::pack(x[0], x[1]);
-    raw[1] = E::pack(x[2], x[3]);
-    b[0] = transpose8x8(raw[0]);
-    b[1] = transpose8x8(raw[1]);
-}
-
-// The weights' remainders after weights_hi, rounded to the same type.
-template <typename E>
-__device__ __forceinline__ void weights_lo(const float (&x)[4], const uint32_t (&raw)[2],
-                                           uint32_t (&b)[2])
-{
-    const float2 h0 = E::unpack(raw[0]), h1 = E::unpack(raw[1]);
-    b[0] = transpose8x8(E::pack(x[0] - h0.x, x[1] - h0.y));
-    b[1] = transpose8x8(E::pack(x[2] - h1.x, x[3] - h1.y));
+    float rest[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+    for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t w = E::pack(rest[2 * k], rest[2 * k + 1]);
+            b[part][k] = transpose8x8(w);
+            const float2 f = E::unpack(w);
+            rest[2 * k] -= f.x;
+            rest[2 * k + 1] -= f.y;
+        }
 }
 
 // ------------------------------------------------------------------ 16-bit block
 // K and V slabs as TMA leaves them: boxes of 64 columns x 16 rows, 16-byte chunk
 // c of row t at position c ^ (t % 8).  qb = the query rows as B operands.
-// P goes in as a high and a low part of the pool's type, which carries the
-// weights to ~2^-17 (a bf16 weight alone would be off by 2^-9).
+// P goes in as parts of the pool's type: three of bf16 (2^-27; two, 2^-18, would show
+// in the last bits of a result), two of fp16 (2^-22).
 template <int D, bool BF16, int NT>
 __device__ __forceinline__ void consume_16bit(uint32_t kb, const Queries<D, NT> &qs,
                                               State<D, NT> &st, uint32_t mask, float scale_log2,
@@ -373,13 +371,10 @@ __device__ __forceinline__ void consume_16bit(uint32_t kb, const Queries<D, NT> 
     const bool edge = mask != 0xffffu;   // the same for the warp: an edge of the visible part
     const uint32_t masks[1] = {mask};
     softmax_step<D, NT, 1>(st, x, f, masks, BF16 ? 0.f : kTop, lane);
-    uint32_t hi[NT][2], lo[NT][2];
+    constexpr int kParts = BF16 ? 3 : 2;
+    uint32_t w[NT][kParts][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        uint32_t raw[2];
-        weights_hi<E>(c0[nt], hi[nt], raw);
-        weights_lo<E>(c0[nt], raw, lo[nt]);
-    }
+    for (int nt = 0; nt < NT; ++nt) weight_parts<E, kParts>(c0[nt], w[nt]);
     // hidden tokens: their V rows may hold anything, and 0 * NaN is NaN
     const uint32_t two_lo = mask >> (2 * q4), two_hi = mask >> (2 * q4 + 8);
     const uint32_t keep_lo = (two_lo & 1u ? 0xffffu : 0u) | (two_lo & 2u ? 0xffff0000u : 0u);
@@ -397,10 +392,10 @@ __device__ __forceinline__ void consume_16bit(uint32_t kb, const Queries<D, NT> 
             a[3] &= keep_hi;
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            E::mma(st.o[nt][t], a, hi[nt][0], hi[nt][1]);
-            E::mma(st.o[nt][t], a, lo[nt][0], lo[nt][1]);
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int part = 0; part < kParts; ++part)
+                E::mma(st.o[nt][t], a, w[nt][part][0], w[nt][part][1]);
     }
 }
 
@@ -502,20 +497,16 @@ __device__ __forceinline__ void consume_b8(const uint8_t *const (&recs)[NB],
     softmax_step<D, NT, NB>(st, x, f, masks, kTop, lane);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        uint32_t hi[NT][2], lo[NT][2];
+        uint32_t p[NT][2][2];            // the weights' parts
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            uint32_t raw[2];
-            weights_hi<H>(x[b][nt], hi[nt], raw);
-            weights_lo<H>(x[b][nt], raw, lo[nt]);
-        }
+        for (int nt = 0; nt < NT; ++nt) weight_parts<H, 2>(x[b][nt], p[nt]);
         float v_off[NT][4];              // -1152 x the weights' sums, every row alike
         {
             const uint32_t neg[4] = {kNegOffset, kNegOffset, kNegOffset, kNegOffset};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                H::mma0(v_off[nt], neg, hi[nt][0], hi[nt][1]);
-                H::mma(v_off[nt], neg, lo[nt][0], lo[nt][1]);
+                H::mma0(v_off[nt], neg, p[nt][0][0], p[nt][0][1]);
+                H::mma(v_off[nt], neg, p[nt][1][0], p[nt][1][1]);
             }
         }
         // words of tokens 2q4, 2q4 + 1, 2q4 + 8, 2q4 + 9: four dimensions each
@@ -545,8 +536,8 @@ __device__ __forceinline__ void consume_b8(const uint8_t *const (&recs)[NB],
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float c[4];
-                    mma_from(c, a, hi[nt], v_off[nt]);
-                    H::mma(c, a, lo[nt][0], lo[nt][1]);
+                    mma_from(c, a, p[nt][0], v_off[nt]);
+                    H::mma(c, a, p[nt][1][0], p[nt][1][1]);
                     float *o = st.o[nt][2 * i + pr];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[e] = fmaf(v_scale[b], c[e], o[e]);

@@ -74,6 +74,22 @@ def test_8bit_decode(dtype, dim, hq):
     assert status_check(status) == (0, 0)
 
 
+@pytest.mark.parametrize("dim,hq", [(64, 4), (128, 8), (128, 24)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_16bit_decode(dtype, dim, hq):
+    """Three bf16 parts (2^-27) or two fp16 parts (2^-22)."""
+    lens = torch.arange(2, 96, dtype=torch.int32, device="cuda")
+    tables = torch.arange(NB, dtype=torch.int32, device="cuda").repeat(len(lens), 1)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for c0, c1 in RATIOS:
+        pool = cancelling(dtype, dim, c0, c1)
+        scale = math.log(c1 / c0)
+        out = paged_decode_attention_window(pool, query(len(lens), hq, dim, DT[dtype]), tables, lens, scale,
+                                            2, 0, status)
+        check(out, c0, c1, scale, 2.0 ** -27 if dtype == "bf16" else 2.0 ** -22, 0)
+    assert status_check(status) == (0, 0)
+
+
 # ------------------------------------------------------------- a few dominant tokens
 def dominated(kind, dim, n, first):
     """A pool of one sequence of n tokens: the first ones have score 0 and value 0, the others a
