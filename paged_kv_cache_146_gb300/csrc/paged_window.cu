@@ -170,11 +170,11 @@ struct State {
 };
 
 // The query rows of a kv head as B operands (head r of tile nt); for 8-bit pools
-// also each row's scale and its offset (see codes_lo), for heads 2 q4 and 2 q4 + 1.
+// also each row's scale, for heads 2 q4 and 2 q4 + 1.
 template <int D, int NT>
 struct Queries {
     uint32_t b[NT][D / 16][2];
-    float scale[NT][2], off[NT][2];
+    float scale[NT][2];
 };
 
 template <int D, int NT>
@@ -400,35 +400,26 @@ __device__ __forceinline__ void consume_16bit(uint32_t kb, const Queries<D, NT> 
 }
 
 // ------------------------------------------------------------------- 8-bit block
-// Byte u = code + 128 is the low mantissa of fp16 1024 + u (bits 0x6400 | u), so
-// a byte pair becomes an fp16 pair by one byte permutation, each value carrying
-// an offset of 1152.  The products take it along and their accumulators start
-// from -1152 times the other operand's sum, which one product with a constant
-// operand gives.  A product of an fp16 value and 1152 + code (11 bits each) is
-// exact in fp32; the offset makes the terms of the fp32 sums up to ten times as
-// large (1279 against 127), and their rounding with them, still 2^-19 of the
-// operands' scale.  Subtracting the offset from every pair instead takes 64 more
-// instructions per block (305 against 280), 2 % where the SM is the limit.
-constexpr uint32_t kNegOffset = 0xE480E480u;                 // (-1152, -1152)
+// Byte u = code + 128 is the low mantissa of fp16 1024 + u (bits 0x6400 | u), so one
+// byte permutation and one subtraction of 1152 make an fp16 pair of a byte pair.
+// (Products that take the 1152 along, their sums starting from -1152 times the other
+// operand's sum, need 64 instructions less per block, 280 against 305 of them, and
+// were 2 % faster where the SM is the limit; but they round at ten times the
+// size of the terms, which showed in the last bits: 1.2 to 2 of 10,000 of a bf16
+// result's norm against 64 bits.)
+__device__ __forceinline__ uint32_t centred(uint32_t w)
+{
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(0x64806480u));   // (1152, 1152)
+    return d;
+}
 __device__ __forceinline__ uint32_t codes_lo(uint32_t w)     // bytes 0 and 1
 {
-    return __byte_perm(w, 0x64646464u, 0x4140);
+    return centred(__byte_perm(w, 0x64646464u, 0x4140));
 }
 __device__ __forceinline__ uint32_t codes_hi(uint32_t w)     // bytes 2 and 3
 {
-    return __byte_perm(w, 0x64646464u, 0x4342);
-}
-
-// d = a b + c on fp16 operands.
-__device__ __forceinline__ void mma_from(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2],
-                                         const float (&c)[4])
-{
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(c[0]), "f"(c[1]),
-          "f"(c[2]), "f"(c[3]));
+    return centred(__byte_perm(w, 0x64646464u, 0x4342));
 }
 
 // Offset of 16-byte chunk j of token t in the K or V codes (pagedkv.h).
@@ -457,7 +448,6 @@ __device__ __forceinline__ void consume_b8(const uint8_t *const (&recs)[NB],
 {
     using H = Elem<false>;
     const auto &qb = qs.b;
-    const auto &k_off = qs.off;
     const auto &scale_row = qs.scale;
     const int r = lane >> 2, q4 = lane & 3;
     float x[NB][NT][4], f[NB][NT][2];
@@ -471,7 +461,7 @@ __device__ __forceinline__ void consume_b8(const uint8_t *const (&recs)[NB],
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) c[nt][e] = k_off[nt][e & 1];
+            for (int e = 0; e < 4; ++e) c[nt][e] = 0.f;
 #pragma unroll
         for (int half = 0; half < D / 64; ++half) {
             const uint4 wa = *reinterpret_cast<const uint4 *>(rec + chunk_at<D>(r, q4 + 4 * half));
@@ -500,15 +490,6 @@ __device__ __forceinline__ void consume_b8(const uint8_t *const (&recs)[NB],
         uint32_t p[NT][2][2];            // the weights' parts
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) weight_parts<H, 2>(x[b][nt], p[nt]);
-        float v_off[NT][4];              // -1152 x the weights' sums, every row alike
-        {
-            const uint32_t neg[4] = {kNegOffset, kNegOffset, kNegOffset, kNegOffset};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                H::mma0(v_off[nt], neg, p[nt][0][0], p[nt][0][1]);
-                H::mma(v_off[nt], neg, p[nt][1][0], p[nt][1][1]);
-            }
-        }
         // words of tokens 2q4, 2q4 + 1, 2q4 + 8, 2q4 + 9: four dimensions each
         constexpr int kWords = D / 32;
         uint32_t w[4][kWords];
@@ -536,7 +517,7 @@ __device__ __forceinline__ void consume_b8(const uint8_t *const (&recs)[NB],
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float c[4];
-                    mma_from(c, a, p[nt][0], v_off[nt]);
+                    H::mma0(c, a, p[nt][0][0], p[nt][0][1]);
                     H::mma(c, a, p[nt][1][0], p[nt][1][1]);
                     float *o = st.o[nt][2 * i + pr];
 #pragma unroll
@@ -603,13 +584,6 @@ __device__ __forceinline__ void load_queries(Queries<D, NT> &qs, const typename 
                 qs.scale[nt][0] *= __shfl_sync(kFull, up, 8 * q4);
                 qs.scale[nt][1] *= __shfl_sync(kFull, up, 8 * q4 + 4);
             }
-            const uint32_t neg[4] = {kNegOffset, kNegOffset, kNegOffset, kNegOffset};
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                Elem<false>::mma(c, neg, qs.b[nt][kk][0], qs.b[nt][kk][1]);
-            qs.off[nt][0] = c[0];
-            qs.off[nt][1] = c[1];
         }
     }
 }
