@@ -254,8 +254,9 @@ __global__ void __launch_bounds__(256) prefill_v16_kernel(const uint16_t *__rest
 //   warps 9 and 10, lane 0 (MMA issuers, one per query tile): S = Q K^T into
 //     one of two tensor-memory buffers (M 128, N 64), then O += P V for the
 //     previous tile (M 128, N D, V as an MN-major operand), P as a high and a
-//     low bf16 part (bf16 pools) or one fp16 part (fp16 pools, and bf16 pools
-//     whose V was copied to fp16 for the call).  One issuer
+//     low part (bf16 pools, and fp16 pools of a windowed call) or one fp16 part
+//     (fp16 pools otherwise, and bf16 pools whose V was copied to fp16 for the
+//     call).  One issuer
 //     per query tile lets each group's S and P V go out as soon as that
 //     group's inputs are ready, without waiting behind the other group's.
 //   warps 0-3 and 4-7 (softmax, one warpgroup per query tile, ping-pong on the
@@ -298,14 +299,21 @@ __device__ __forceinline__ uint64_t low_bits(int n)
 // bf16 weights (p0, p1) (pp = the same pair packed) as a high and a low part,
 // the even index in the low half of each word: the high part is the weight
 // truncated to bf16 (its upper 16 bits, exact), the low part the remainder
-// rounded to bf16, so high + low carries the weight to ~2^-16.  (fp16 pools
-// keep a single fp16 part: its relative error, <= 2^-11, is inside the
+// rounded to bf16, so high + low carries the weight to ~2^-16.  fp16 weights:
+// the high part rounded, high + low to 2^-22.  (The plain call on fp16 pools
+// keeps a single fp16 part: its relative error, <= 2^-11, is inside the
 // tolerance, where a single bf16 part's 2^-9 is not.)
 template <bool BF16>
 __device__ __forceinline__ void split_hi_lo(float p0, float p1, uint64_t pp, uint32_t &hi,
                                             uint32_t &lo)
 {
-    static_assert(BF16, "fp16 weights take one part");
+    if constexpr (!BF16) {
+        hi = Elem<false>::pack(p0, p1);
+        const float2 h = Elem<false>::unpack(hi);
+        const float2 d = unpack2f(sub2f(pp, pack2f(h.x, h.y)));
+        lo = Elem<false>::pack(d.x, d.y);
+        return;
+    }
     const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
     hi = __byte_perm(b0, b1, 0x7632);
     const float2 d = unpack2f(sub2f(pp, pack2f(__uint_as_float(b0 & 0xffff0000u),
@@ -460,7 +468,8 @@ __global__ void __launch_bounds__(kThreads)
     static_assert(BF16 || !VS, "fp16 pools take V as it is");
     static_assert(!(VS && PREFIX), "the shared-prefix mode reads V from the pool");
     static_assert(!(WINDOW && (VS || PREFIX)), "windowed calls read V from the pool");
-    constexpr bool kTwoParts = BF16 && !VS;    // P as bf16 high + low parts
+    constexpr bool kPBf16 = BF16 && !VS;       // P and V of the P V product as bf16, else fp16
+    constexpr bool kTwoParts = kPBf16 || WINDOW;     // P as a high and a low part
     using E = Elem<BF16>;
     using T = typename E::T;
     using LY = Layout<D>;
@@ -599,7 +608,7 @@ __global__ void __launch_bounds__(kThreads)
         if (lane == 0) {
             const int gr = warp - kIssuer;
             const uint32_t id_qk = tc::idesc_f16(BF16, kRows, kKeys, 0, 0);
-            const uint32_t id_pv = tc::idesc_f16(kTwoParts, kRows, D, 0, 1);   // P and V: same type
+            const uint32_t id_pv = tc::idesc_f16(kPBf16, kRows, D, 0, 1);   // P and V: same type
             const uint32_t q_a = smem_addr(q_s) + gr * LY::kQBytes, st_a = smem_addr(stage_s);
             const uint32_t o_t = tmem + 256 + 128 * gr;
             // Descriptors are built once per operand base; each MMA adds its
@@ -806,7 +815,7 @@ __global__ void __launch_bounds__(kThreads)
                         const uint64_t pp = pack2f(p0, p1);
                         lsum2 = add2f(lsum2, pp);
                         if constexpr (kTwoParts)
-                            split_hi_lo<true>(p0, p1, pp, hi[c / 2], lo[c / 2]);
+                            split_hi_lo<kPBf16>(p0, p1, pp, hi[c / 2], lo[c / 2]);
                         else                   // fp16 (relative error <= 2^-11): one part
                             hi[c / 2] = Elem<false>::pack(p0, p1);
                     }

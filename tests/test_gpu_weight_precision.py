@@ -8,7 +8,8 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 from paged_kv_cache_146_gb300 import (KVPool, paged_decode_attention_b8,  # noqa: E402
-                                      paged_decode_attention_window, status_check)
+                                      paged_decode_attention_window, paged_prefill_attention_window,
+                                      prefill_workspace_bytes, status_check)
 from serving_reference import Records  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -87,6 +88,31 @@ def test_16bit_decode(dtype, dim, hq):
                                             2, 0, status)
         check(out, c0, c1, scale, 2.0 ** -27 if dtype == "bf16" else 2.0 ** -22)
     assert status_check(status) == (0, 0)
+
+
+def prefill(pool, q, tables, lens, scale, window):
+    """One chunk a sequence, of equal size."""
+    seqs, rows, hq = len(lens), q.shape[0], q.shape[1]
+    start = torch.arange(seqs + 1, dtype=torch.int32, device="cuda") * (rows // seqs)
+    ws = torch.empty(prefill_workspace_bytes(seqs, rows, hq, HKV), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = paged_prefill_attention_window(pool, q, tables, start, lens, scale, window, 0, ws, status)
+    assert status_check(status) == (0, 0)
+    return out
+
+
+@pytest.mark.parametrize("dim,hq", [(64, 2), (64, 8), (128, 8), (128, 24)])
+@pytest.mark.parametrize("seqs", [1, 70])
+@pytest.mark.parametrize("dtype", ["f16"])
+def test_prefill(dtype, seqs, dim, hq):
+    """Two fp16 parts: 2^-22."""
+    lens = torch.full((seqs,), 96, dtype=torch.int32, device="cuda")
+    tables = torch.arange(NB, dtype=torch.int32, device="cuda").repeat(seqs, 1)
+    for c0, c1 in RATIOS:
+        pool = cancelling(dtype, dim, c0, c1)
+        scale = math.log(c1 / c0)
+        out = prefill(pool, query(seqs * 95, hq, dim, DT[dtype]), tables, lens, scale, 2)
+        check(out, c0, c1, scale, 2.0 ** -22)
 
 
 # ------------------------------------------------------------- a few dominant tokens
