@@ -299,8 +299,9 @@ __device__ __forceinline__ uint64_t low_bits(int n)
 // bf16 weights (p0, p1) (pp = the same pair packed) as a high and a low part,
 // the even index in the low half of each word: the high part is the weight
 // truncated to bf16 (its upper 16 bits, exact), the low part the remainder
-// rounded to bf16, so high + low carries the weight to ~2^-16.  fp16 weights:
-// the high part rounded, high + low to 2^-22.  (The plain call on fp16 pools
+// rounded to bf16, so high + low carries the weight to 2^-15 (a windowed call as
+// the plain one: a window as long as the context gives the plain call's bits).
+// fp16 weights: the high part rounded, high + low to 2^-22.  (The plain call on fp16 pools
 // keeps a single fp16 part: its relative error, <= 2^-11, is inside the
 // tolerance, where a single bf16 part's 2^-9 is not.)
 template <bool BF16>

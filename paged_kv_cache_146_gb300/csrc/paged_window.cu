@@ -334,7 +334,7 @@ __device__ __forceinline__ void weight_parts(const float (&x)[4], uint32_t (&b)[
 // ------------------------------------------------------------------ 16-bit block
 // K and V slabs as TMA leaves them: boxes of 64 columns x 16 rows, 16-byte chunk
 // c of row t at position c ^ (t % 8).  qb = the query rows as B operands.
-// P goes in as parts of the pool's type: three of bf16 (2^-27; two, 2^-18, would show
+// P goes in as parts of the pool's type: three of bf16 (2^-24; two, 2^-16, would show
 // in the last bits of a result), two of fp16 (2^-22).
 template <int D, bool BF16, int NT>
 __device__ __forceinline__ void consume_16bit(uint32_t kb, const Queries<D, NT> &qs,
