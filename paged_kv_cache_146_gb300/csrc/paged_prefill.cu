@@ -471,6 +471,11 @@ __global__ void __launch_bounds__(kThreads)
     static_assert(!(WINDOW && (VS || PREFIX)), "windowed calls read V from the pool");
     constexpr bool kPBf16 = BF16 && !VS;       // P and V of the P V product as bf16, else fp16
     constexpr bool kTwoParts = kPBf16 || WINDOW;     // P as a high and a low part
+    // Windowed calls on fp16 pools take the reference this much below a row's largest
+    // score: weights stay within 2^15, and those down to 2^-21 of the largest are normal
+    // numbers in fp16 (2^-14 without: a row far below a few dominant keys, sinks for one,
+    // would lose its weights' bits).
+    constexpr float kTop = WINDOW && !kPBf16 ? 7.f : 0.f;
     using E = Elem<BF16>;
     using T = typename E::T;
     using LY = Layout<D>;
@@ -783,12 +788,14 @@ __global__ void __launch_bounds__(kThreads)
                 mx *= p.scale_log2;
                 float f = 1.f;
                 bool resc = false;
-                if (mx > m_ref + kLazy) {          // also the first tile: m_ref = -inf
+                if (mx > m_ref + (kLazy + kTop)) {     // also the first tile: m_ref = -inf
+                    // (from 2^24 on, where the spacing nears kTop, the largest score itself)
+                    const float now = kTop == 0.f || fabsf(mx) > 0x1p24f ? mx : mx - kTop;
                     if (m_ref != -INFINITY) {
-                        f = fast_exp2(m_ref - mx);
+                        f = fast_exp2(m_ref - now);
                         resc = true;
                     }
-                    m_ref = mx;
+                    m_ref = now;
                 }
                 // weights in pairs: packed fp32 arithmetic (f32x2), then a high and a
                 // low 16-bit part per weight

@@ -170,3 +170,26 @@ def test_decode_far_below_a_few_tokens(kind, dim, hq, n):
         check_dominated(out, n, 1, bits, scale, 2.0 ** -22 if half else 2.0 ** -24,
                         2.0 ** (bits - 33) if half else 0.0)
     assert status_check(status) == (0, 0)
+
+
+@pytest.mark.parametrize("dim,hq", [(64, 4), (128, 8), (128, 24)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("n,rows", [(1000, 60), (6000, 300)])
+def test_prefill_far_below_a_few_tokens(dtype, dim, hq, n, rows):
+    """A row has one reference for all its keys, so a dominant sink stands against every late one.
+    With the largest weight 2^7, what fp16 cannot hold of a weight of 2^-bits is 2^-25 2^-7 2^bits of
+    it; sums of n products in order round to n 2^-24 at worst, most of it in the same direction."""
+    pool, nb = dominated(dtype, dim, n, 1)
+    tables = torch.arange(nb, dtype=torch.int32, device="cuda").view(1, nb)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    for bits in (18.0, 19.37, 20.5, 21.0):
+        scale = bits * math.log(2.0)
+        out = prefill(pool, query(rows, hq, dim, DT[dtype]), tables, lens, scale, n)
+        w = math.exp(-float(torch.tensor(scale, dtype=torch.float32)))
+        late = torch.arange(n - rows, n, dtype=torch.float64) * w      # the query itself is late
+        want = (late / (1 + late))[:, None, None]
+        rel = (2 * ((2.0 ** -22 if dtype == "f16" else 2.0 ** -15) + 2.0 ** -20) + n * 2.0 ** -24
+               + (2.0 ** (bits - 32) if dtype == "f16" else 0.0) + torch.finfo(DT[dtype]).eps / 2)
+        # (an output of 2^-11 and up is a normal number of either type)
+        worst = (out.double().cpu() / want - 1).abs().max().item()
+        assert worst <= rel, (bits, worst / rel)
