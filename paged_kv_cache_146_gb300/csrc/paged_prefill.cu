@@ -803,6 +803,7 @@ __global__ void __launch_bounds__(kThreads)
                 // (a windowed row that has seen no key yet has m_ref = -inf; any finite
                 // reference gives its hidden scores weight 2^-inf = 0)
                 const float m_sub = WINDOW && m_ref == -INFINITY ? 0.f : m_ref;
+                const bool big = fabsf(m_sub) > 0x1p24f;       // (windowed calls, below)
                 const uint64_t sc2 = pack2f(p.scale_log2, p.scale_log2), nm2 = pack2f(-m_sub, -m_sub);
                 uint64_t lsum2 = pack2f(0.f, 0.f);
                 // two copies of the loop: only a tile that crosses the row's
@@ -810,11 +811,10 @@ __global__ void __launch_bounds__(kThreads)
                 auto weights = [&](auto masked, auto wide) {
 #pragma unroll
                     for (int c = 0; c < kKeys; c += 2) {
-                        const float2 e =
-                            decltype(wide)::value
-                                ? make_float2(__fsub_rn(__fmul_rn(x[c], p.scale_log2), m_sub),
-                                              __fsub_rn(__fmul_rn(x[c + 1], p.scale_log2), m_sub))
-                                : unpack2f(fma2f(pack2f(x[c], x[c + 1]), sc2, nm2));
+                        float2 e = unpack2f(fma2f(pack2f(x[c], x[c + 1]), sc2, nm2));
+                        if (decltype(wide)::value && big)
+                            e = make_float2(__fsub_rn(__fmul_rn(x[c], p.scale_log2), m_sub),
+                                            __fsub_rn(__fmul_rn(x[c + 1], p.scale_log2), m_sub));
                         float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
                         if constexpr (decltype(masked)::value) {
                             if (k0 + c > pos) p0 = 0.f;
@@ -834,8 +834,9 @@ __global__ void __launch_bounds__(kThreads)
                     // large or too small, the same for the whole row, which cancels;
                     // from 2^25 on that is 2 or more and grows past the range of the
                     // weights, so there the products are rounded alike, by scalar
-                    // operations that stay apart (the largest weight is then exactly 1)
-                    if (__any_sync(kFull, fabsf(m_sub) > 0x1p24f))
+                    // operations that stay apart (the largest weight is then exactly 1);
+                    // of such rows only: the others' keys of earlier tiles were not
+                    if (__any_sync(kFull, big))
                         weights(std::false_type{}, std::true_type{});
                     else weights(std::false_type{}, std::false_type{});
                 } else {

@@ -8,7 +8,8 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 from paged_kv_cache_146_gb300 import (KVPool, cache_write_b8, paged_decode_attention_b8,  # noqa: E402
-                                      paged_decode_attention_window, status_check)
+                                      paged_decode_attention_window, paged_prefill_attention_window,
+                                      prefill_workspace_bytes, status_check)
 from serving_reference import Records, random_case, visible  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -72,3 +73,44 @@ def test_largest_keys_count_alike(kind, n, window, sinks, exponent):
         want = vv.mean(0)
         room = half * want.abs() + (2 * WEIGHT[kind] + 2.0 ** -18) * vv.abs().mean(0) + tiny + n * 2.0 ** -32
         assert ((got[0, h].double().cpu() - want).abs() <= room).all(), h
+
+
+@pytest.mark.parametrize("call", ["prefill", "decode"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_a_neighbour_of_huge_scores_changes_nothing(dtype, call):
+    """Two heads of a kv head: the second sees keys of one score, near 2^20, and its row is the mean
+    of V; the first head's scores pass 2^24 from the second key tile on.  Roundings as above (prefill:
+    two bf16 parts, the first truncated, 2^-15; two fp16 parts, 2^-22)."""
+    n, chunk, dim = 300, 40 if call == "prefill" else 1, 64
+    gen = torch.Generator().manual_seed(6)
+    tables, nb = random_case(gen, [n], 1, 20)
+    dt, half = DT[dtype], torch.finfo(DT[dtype]).eps / 2
+    v = torch.randn((nb, 1, 16, dim), generator=gen).to(dt)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, chunk], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    ws = torch.empty(prefill_workspace_bytes(1, chunk, 2, 1), dtype=torch.uint8, device="cuda")
+    pool = KVPool(nb, 1, dim, dtype, device="cuda")
+    pool.v_pool.copy_(v)
+    for factor in (1.0, 1.0078125, 1.2421875, 1.6640625, 1.9921875):
+        k = torch.zeros((nb, 1, 16, dim))
+        for j in range(n):
+            k[tables[0, j // 16], 0, j % 16, 0] = 1.0 if j < 64 else 2.0 ** 14
+        k[..., 1] = 2.0 ** 13 * 1.2421875
+        q = torch.zeros((chunk, 2, dim))
+        q[:, 0, 0] = 2.0 ** 15
+        q[:, 1, 1] = 2.0 ** 10 * factor
+        pool.k_pool.copy_(k)
+        if call == "prefill":
+            got = paged_prefill_attention_window(pool, q.to(dt).cuda(), tables.cuda(), start, lens, 0.1,
+                                                 10 ** 6, 0, ws, status)
+        else:
+            got = paged_decode_attention_window(pool, q.to(dt).cuda(), tables.cuda(), lens, 0.1, 10 ** 6, 0,
+                                                status)
+        assert status_check(status) == (0, 0)
+        for row in range(chunk):
+            j = torch.arange(n - chunk + row + 1)
+            vv = v[tables[0].long()[j // 16], 0, j % 16].double()
+            want = vv.mean(0)
+            room = half * want.abs() + (2 * (2.0 ** -15 if dtype == "bf16" else 2.0 ** -22) + 2.0 ** -18) * vv.abs().mean(0)
+            assert ((got[row, 1].double().cpu() - want).abs() <= room).all(), (factor, row)
