@@ -334,13 +334,33 @@ class DecodeEngine:
             }
         return self._io
 
+    def release_hidden(self) -> int:
+        """With ``window``: the blocks that neither the last token of their sequence nor
+        any later one sees are given back, their table entries become -1.  May be called
+        between any two steps; returns the number of blocks.  (Such a sequence cannot be
+        forked, nor its prefix shared, any more: the ledger wants every entry there.)"""
+        if self.window is None:
+            raise ValueError("without a window every token stays visible")
+        self._wait_copy()
+        bs, count = self.pool.block_size, 0
+        for s in range(self.S):
+            first, last = -(-self.sinks // bs), max(int(self.lens[s]) - self.window, 0) // bs
+            row = self.tables[s, first:max(first, last)]
+            ids = row[row >= 0]
+            self.pool.free(ids)
+            row[:] = -1
+            count += len(ids)
+        return count
+
     def release(self, seqs) -> None:
-        """Finished sequences give back their blocks."""
+        """Finished sequences give back their blocks (with ``window``: those that they
+        still have)."""
         self._wait_copy()
         bs = self.pool.block_size
         for s in seqs:
             nb = -(-int(self.lens[s]) // bs)
-            self.pool.free(self.tables[s, :nb])
+            row = self.tables[s, :nb]
+            self.pool.free(row if self.window is None else row[row >= 0])
             self.tables[s, :] = -1
             self.lens[s] = 0
 
