@@ -714,15 +714,25 @@ def paged_decode_attention_q8(pool: KVPool, q, block_tables, context_lens, scale
 _torch = _fast = None
 
 
+def _load_fastcall(torch):
+    """The module of compiled checks, or None: not built, or built for another torch, another
+    Python or another interface of the library."""
+    import sys
+    from .build import interface_hash
+    try:
+        from . import _fastcall
+        made_for = (_fastcall.torch_version, _fastcall.python_version, _fastcall.interface)
+        here = (torch.__version__.split("+")[0], sys.version_info[0] * 100 + sys.version_info[1],
+                interface_hash())
+    except (ImportError, AttributeError, OSError):
+        return None
+    return _fastcall if made_for == here else None
+
+
 def _load_torch():
     global _torch, _fast
     import torch
-    try:
-        from . import _fastcall
-    except ImportError:
-        _fastcall = None
-    if _fastcall is not None and _fastcall.torch_version != torch.__version__.split("+")[0]:
-        _fastcall = None                    # built against the headers of another torch
+    _fastcall = _load_fastcall(torch)
     if _fastcall is not None:
         _fastcall.bind(*(ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in (
             "paged_decode_attention_window", "paged_decode_attention_b8", "kv_cache_write_rope",

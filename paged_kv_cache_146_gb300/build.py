@@ -8,12 +8,14 @@ it holds the binding's compiled argument checks.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import hashlib
 import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -52,18 +54,42 @@ def _compile(src: str, verbose: bool, build_dir: str = BUILD, defines=()) -> str
     return obj
 
 
-def _build_fastcall() -> None:
+def interface_hash() -> str:
+    """Of the entry points that _fastcall.so calls and of its own functions: the binding
+    takes it only when it was built from the sources that are there now."""
+    h = hashlib.sha256()
+    for path in (os.path.join(INCLUDE, "pagedkv.h"), os.path.join(CSRC, "fastcall.cpp")):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()[:16]
+
+
+def _fastcall() -> None:
+    """Build _fastcall.so if that can be done.  The library does not need it and the
+    binding's own checks serve without it, so a failure is a warning; what an earlier
+    build left is removed, as it may have been made for other signatures."""
+    try:
+        if _build_fastcall():
+            return
+    except Exception as e:                    # no compiler, headers that it cannot take
+        warnings.warn(f"_fastcall.so was not built (calls of a few rows take longer): {e}")
+    if os.path.exists(FASTCALL):
+        os.remove(FASTCALL)
+
+
+def _build_fastcall() -> bool:
     """_fastcall.so: the compiled argument checks, against torch's and Python's headers.
-    Where those are not installed none is built, and the binding's own checks serve."""
+    False where those are not installed."""
     spec = importlib.util.find_spec("torch")
     python = sysconfig.get_paths()["include"]
     torch = spec.submodule_search_locations[0] if spec is not None else ""
     if not (os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so"))
             and os.path.exists(os.path.join(python, "Python.h"))):
-        return
+        return False
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     tmp = FASTCALL + ".tmp"
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-I", INCLUDE,
+           f'-DPKV_INTERFACE="{interface_hash()}"',
            "-isystem", os.path.join(torch, "include"),
            "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            "-isystem", python,
@@ -74,6 +100,7 @@ def _build_fastcall() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on fastcall.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, FASTCALL)
+    return True
 
 
 def build(verbose: bool = False, checked: bool = False, out: str | None = None) -> str:
@@ -84,7 +111,7 @@ def build(verbose: bool = False, checked: bool = False, out: str | None = None) 
     defines = ("PKV_DEBUG_CHECKS",) if checked else ()
     os.makedirs(build_dir, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        fast = None if checked or out else ex.submit(_build_fastcall)
+        fast = None if checked or out else ex.submit(_fastcall)
         objs = list(ex.map(lambda s: _compile(s, verbose, build_dir, defines), SOURCES))
         if fast is not None:
             fast.result()

@@ -316,8 +316,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, methods};
 
 PyMODINIT_FUNC PyInit__fastcall(void)
 {
+    // what the binding compares before it takes the module
     PyObject *m = PyModule_Create(&module);
-    if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) {
+    if (m && (PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0 ||
+              PyModule_AddIntConstant(m, "python_version", PY_MAJOR_VERSION * 100 + PY_MINOR_VERSION) < 0 ||
+              PyModule_AddStringConstant(m, "interface", PKV_INTERFACE) < 0)) {
         Py_DECREF(m);
         return nullptr;
     }
