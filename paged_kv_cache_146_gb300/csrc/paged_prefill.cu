@@ -1601,10 +1601,9 @@ static int64_t max_items(int64_t S, int64_t T, int64_t QT) { return T / QT + S +
 // tokens of one item: kGroups query tiles of kRows / G tokens each
 static int tile_tokens(int G) { return tcp::kGroups * (tcp::kRows / G); }
 
-// (room for items of a single query tile, as small windowed calls have them)
 static size_t ws_bytes(int64_t S, int64_t T, int64_t G)
 {
-    return 256 + align256((size_t)max_items(S, T, tcp::kRows / G) * 8);
+    return 256 + align256((size_t)max_items(S, T, tile_tokens((int)G)) * 8);
 }
 
 // The workspace with room for the fp16 copy of V after the work list: the
@@ -1874,11 +1873,14 @@ static int prefill_call(const pkv_pool *pool, void *out, const void *q, const vo
     // a windowed call of few items gives each a single query tile: a key tile then
     // costs a CTA one softmax and one pair of products instead of two of each (one
     // chunk of 64 to 512 tokens, window 1,024: 29 against 37 us; from more items than
-    // SMs on, two tiles share every key tile)
-    if (window > 0 && max_items(num_seqs, num_tokens, prm.group_tokens) * g.num_kv_heads <= sms)
+    // SMs on, two tiles share every key tile), if their list fits the workspace, whose
+    // size counts two tiles to an item; few sequences need no list there
+    prm.few = window > 0 && num_seqs <= tcp::kFewSeqs;
+    const int64_t single = max_items(num_seqs, num_tokens, prm.group_tokens);
+    if (window > 0 && single * g.num_kv_heads <= sms &&
+        (prm.few || workspace_bytes >= 256 + (size_t)single * 8))
         prm.tile_tokens = prm.group_tokens;
     prm.max_items = max_items(num_seqs, num_tokens, prm.tile_tokens);
-    prm.few = window > 0 && num_seqs <= tcp::kFewSeqs;
     prm.status = d_status;
     prm.v16 = staged ? reinterpret_cast<uint16_t *>(ws + sl.v16) : nullptr;
     prm.v_emax = staged ? reinterpret_cast<int32_t *>(ws + sl.emax) : nullptr;
