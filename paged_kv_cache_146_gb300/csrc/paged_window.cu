@@ -164,9 +164,15 @@ struct Shape {
 template <int D, int NT>
 struct State {
     float o[NT][D / 16][4];
-    float m[NT][2], l[NT][2];
-    // the same for the warp: some head has no finite m yet; some |m| > 2^24 (see softmax_step)
-    bool none, wide;
+    // reference maximum m = -neg; 0 and bit 2 nt + h of `unset` before a head's first
+    // finite score (m = -inf)
+    float neg[NT][2], l[NT][2];
+    uint32_t unset;
+    bool special;                        // some head of the warp is unset or has |m| > 2^24
+    __device__ __forceinline__ float m(int nt, int h) const
+    {
+        return (unset >> (2 * nt + h)) & 1u ? -INFINITY : -neg[nt][h];
+    }
 };
 
 // The query rows of a kv head as B operands (head r of tile nt); for 8-bit pools
@@ -180,11 +186,11 @@ struct Queries {
 template <int D, int NT>
 __device__ __forceinline__ void reset(State<D, NT> &st)
 {
-    st.none = true;
-    st.wide = false;
+    st.unset = ~0u;
+    st.special = true;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        st.m[nt][0] = st.m[nt][1] = -INFINITY;
+        st.neg[nt][0] = st.neg[nt][1] = 0.f;
         st.l[nt][0] = st.l[nt][1] = 0.f;
 #pragma unroll
         for (int t = 0; t < D / 16; ++t)
@@ -209,7 +215,6 @@ __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&x)[NB][NT
                                              float top, int lane)
 {
     float y[NB][NT][4];                  // exponents, -inf for hidden tokens
-    auto is_wide = [](float m) { return m != -INFINITY && fabsf(m) > 0x1p24f; };
     auto hide = [&]() {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -222,55 +227,28 @@ __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&x)[NB][NT
                     if (!(e < 2 ? v0 : v1)) y[b][nt][e] = -INFINITY;
         }
     };
-    auto exponents = [&]() {
+    auto each = [&](auto exponent) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                // (no token yet: any finite reference, nothing visible has a weight)
-                const float neg = st.m[nt][h] == -INFINITY ? 0.f : -st.m[nt][h];
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        y[b][nt][2 * t + h] = fmaf(x[b][nt][2 * t + h], f[b][nt][h], neg);
-            }
-        if (st.wide) {                   // the same for the warp
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!is_wide(st.m[nt][h])) continue;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-#pragma unroll
-                        for (int t = 0; t < 2; ++t)
-                            y[b][nt][2 * t + h] = __fsub_rn(
-                                __fmul_rn(x[b][nt][2 * t + h], f[b][nt][h]), st.m[nt][h]);
-                }
-        }
+                for (int e = 0; e < 4; ++e) y[b][nt][e] = exponent(x[b][nt][e], f[b][nt][e & 1], nt, e & 1);
         hide();
     };
-    bool raise = st.none;
-    if (!raise) {
-        exponents();
+    each([&](float p, float factor, int nt, int h) { return fmaf(p, factor, st.neg[nt][h]); });
+    bool raise = st.special;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) raise |= y[b][nt][e] > top + kLazy;
-        raise = __any_sync(kFull, raise);
-    }
-    if (raise) {
-        bool none = false, wide = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[b][nt][e] = __fmul_rn(x[b][nt][e], f[b][nt][e & 1]);
-        hide();
+            for (int e = 0; e < 4; ++e) raise |= y[b][nt][e] > top + kLazy;
+    if (__any_sync(kFull, raise)) {      // m moves, or the warp is special: products of their own
+        each([&](float p, float factor, int, int) { return __fmul_rn(p, factor); });
+        auto is_wide = [](float m) { return m != -INFINITY && fabsf(m) > 0x1p24f; };
+        bool special = false;
+        uint32_t wide = 0u;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -283,12 +261,15 @@ __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&x)[NB][NT
                 up = fmaxf(up, __shfl_xor_sync(kFull, up, 16));
                 // the reference moves up with the largest score (from 2^24 on, where
                 // the spacing nears kTop, to it)
-                const float old = st.m[nt][h];
+                const float old = st.m(nt, h);
                 const float now = fmaxf(old, fabsf(up) > 0x1p24f ? up : up - top);
                 const float s = old == -INFINITY ? 1.f : fast_exp2(old - now);
-                st.m[nt][h] = now;
-                none |= now == -INFINITY;
-                wide |= is_wide(now);
+                if (now != -INFINITY) {
+                    st.neg[nt][h] = -now;
+                    st.unset &= ~(1u << (2 * nt + h));
+                }
+                if (is_wide(now)) wide |= 1u << (2 * nt + h);
+                special |= now == -INFINITY || is_wide(now);
                 st.l[nt][h] *= s;
 #pragma unroll
                 for (int t = 0; t < D / 16; ++t) {
@@ -297,9 +278,11 @@ __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&x)[NB][NT
                 }
             }
         }
-        st.none = __any_sync(kFull, none);
-        st.wide = __any_sync(kFull, wide);
-        exponents();
+        st.special = __any_sync(kFull, special);
+        each([&](float p, float factor, int nt, int h) {
+            return (wide >> (2 * nt + h)) & 1u ? __fadd_rn(__fmul_rn(p, factor), st.neg[nt][h])
+                                               : fmaf(p, factor, st.neg[nt][h]);
+        });
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -812,7 +795,7 @@ __global__ void __launch_bounds__(32 * W, Shape<D, B8, NT, W>::kMinBlocks)
             l += __shfl_xor_sync(kFull, l, 16);
             if constexpr (B8) l *= kTopInverse;          // as the accumulators
             const int head = 8 * nt + 2 * q4 + h;
-            if (r == 0) ml[warp * kMaxHeads + head] = make_float2(st.m[nt][h], bad ? -1.f : l);
+            if (r == 0) ml[warp * kMaxHeads + head] = make_float2(st.m(nt, h), bad ? -1.f : l);
             float *dst = piece + head * SH::kRow;
 #pragma unroll
             for (int t = 0; t < D / 16; ++t) {
