@@ -626,8 +626,9 @@ int paged_decode_attention_b8(const pkv_pool *pool, void *out, const void *q, co
  *   j <= p  and  (j > p - window  or  j < sinks)
  * window >= 1, sinks >= 0; a window as long as the context is plain attention.
  * Table entries of blocks without a visible token are not read (a program may
- * have given those blocks back), and nothing that hidden tokens hold, NaN
- * included, reaches a result. */
+ * have given those blocks back; kv_seq_fork and kv_block_free still want an
+ * allocated block in every entry that they are given), and nothing that hidden
+ * tokens hold, NaN included, reaches a result. */
 
 /* paged_decode_attention under that mask (the query of sequence s sits at
  * position context_lens[s] - 1).  16-bit pools, head_dim 64 or 128, block_size

@@ -352,7 +352,7 @@ struct Item {
 
 // A windowed call of up to this many sequences has no launch of the prep kernel before
 // it: every CTA lists the items for itself, a sequence per lane (one chunk of 300
-// tokens: 10.3 us back to back with the prep kernel, 7.5 without).
+// tokens: 13.3 us back to back with the prep kernel, 12.0 without).
 constexpr int kFewSeqs = 32;
 
 // The list: items before each sequence's, first[kFewSeqs] = all of them.  By the
@@ -1872,7 +1872,7 @@ static int prefill_call(const pkv_pool *pool, void *out, const void *q, const vo
     if (per_sm < 1 || (kp.reg_split && !launch_regs_ok(kp.fn))) return PKV_ERR_CUDA;
     // a windowed call of few items gives each a single query tile: a key tile then
     // costs a CTA one softmax and one pair of products instead of two of each (one
-    // chunk of 64 to 512 tokens, window 1,024: 29 against 37 us; from more items than
+    // chunk of 64 to 512 tokens, window 1,024: 23 against 31 us; from more items than
     // SMs on, two tiles share every key tile), if their list fits the workspace, whose
     // size counts two tiles to an item; few sequences need no list there
     prm.few = window > 0 && num_seqs <= tcp::kFewSeqs;

@@ -24,13 +24,14 @@
 // so no half of a matrix instruction works on empty rows (G <= 8), and the
 // statistics and the accumulators of a head sit in the same lanes.  (tcgen05
 // takes 64 or 128 rows: with G <= 16 query rows per pair and a new K tile each
-// step it would idle; the tensor pipe is 25 % busy here.)
+// step it would idle; the tensor pipe is 18 to 28 % busy here.)
 //
 // The bytes of the visible K and V bound it, each read once: 256 sequences x 8
-// kv heads x window 1,024 (16-bit, 1.05 GB) 156 us, 6.7 TB/s; 160 ragged contexts
-// of up to 16,384 tokens (8-bit, 2.87 GB) 414 us, 6.9 TB/s.  Where a few pairs
-// leave SMs idle, an SM's own pace counts: 57 GB/s of 8-bit blocks (280
-// instructions per block and warp, the byte permutations half of the ALU pipe).
+// kv heads x window 1,024 (16-bit, 1.05 GB) 155 us, 6.8 TB/s; 160 ragged contexts
+// of up to 16,384 tokens (8-bit, 2.87 GB) 422 us, 6.8 TB/s.  Where a few pairs
+// leave SMs idle, an SM's own pace counts: 46 GB/s of 8-bit blocks (360
+// instructions per block and warp, half of the issue slots; 57 GB/s and 280 with
+// weights in one part and codes that kept their offset, see consume_b8).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -386,10 +387,11 @@ __device__ __forceinline__ void consume_16bit(uint32_t kb, const Queries<D, NT> 
 // Byte u = code + 128 is the low mantissa of fp16 1024 + u (bits 0x6400 | u), so one
 // byte permutation and one subtraction of 1152 make an fp16 pair of a byte pair.
 // (Products that take the 1152 along, their sums starting from -1152 times the other
-// operand's sum, need 64 instructions less per block, 280 against 305 of them, and
-// were 2 % faster where the SM is the limit; but they round at ten times the
-// size of the terms, which showed in the last bits: 1.2 to 2 of 10,000 of a bf16
-// result's norm against 64 bits.)
+// operand's sum, need 64 instructions less per block and were 3 % faster where the SM
+// is the limit; but they round at ten times the size of the terms, which showed in
+// the last bits: 1.2 to 2 of 10,000 of a bf16 result's norm against the plain form's.
+// The bytes as fp16 subnormals, u 2^-24, with an offset of 128: as exact as the
+// subtraction but where one weight is far above the rest, and 1 to 3 % faster.)
 __device__ __forceinline__ uint32_t centred(uint32_t w)
 {
     uint32_t d;
@@ -422,7 +424,8 @@ __device__ __forceinline__ int chunk_at(int t, int j)
 // and the queries were laid out alike; of V it takes dimensions D/8 r ..
 // D/8 (r + 1) of its four tokens and pairs their bytes.
 // P: two fp16 parts, which carry a weight to 2^-22 (one part, 2^-11, would show in a
-// bf16 result: 8 of 10,000 of its norm against one rounded from 64 bits).
+// bf16 result: 8 of 10,000 of its norm against the plain form's; it was 2 % faster on
+// grids that fill the GPU and 9 % where the SM is the limit).
 // NB blocks at a time: their chains of dependent instructions overlap.
 template <int D, int NT, int NB>
 __device__ __forceinline__ void consume_b8(const uint8_t *const (&recs)[NB],
@@ -750,8 +753,8 @@ __global__ void __launch_bounds__(32 * W, Shape<D, B8, NT, W>::kMinBlocks)
     };
     int i = 0;
     bool alive = true;
-    if constexpr (B8 && NT == 1) {       // two blocks at a time (two head tiles: slower, 111 against
-                                         // 105 us on 200 pairs of 16 fp16 heads)
+    if constexpr (B8 && NT == 1) {       // two blocks at a time (two head tiles: slower, 49.3 against
+                                         // 48.3 us on 200 pairs of 16 fp16 heads)
         for (; i + 1 < count; i += 2) {
             if ((i & 31) == 0) edges = edges_from(i);
             alive = wait_block(i) && wait_block(i + 1);
@@ -986,14 +989,14 @@ static int launch(const pkv_pool *pool, bool want_b8, void *out, const void *q, 
     // Cluster size.  A cluster costs more to place the larger it is (a few
     // microseconds per wave of eights), so a pair is split only
     //  * while every CTA fits on the GPU at once and its warps have two blocks
-    //    each: 32 pairs of 1,000 tokens 12.8 us split by 4 to 8, 16.9 unsplit;
-    //    128 pairs 23 us split past one wave, 16.9 unsplit;
+    //    each: 32 pairs of 1,000 tokens 12.9 us split by 4 or 8, 19.1 unsplit;
+    //    128 pairs 19.1 us unsplit to split by 3, 25 by 4 (past one wave), 31 by 8;
     //  * or, where a pair may show long runs of blocks, into about one and a half
     //    waves, for the GPU to stay busy to the end: 384 ragged pairs of up to
-    //    6,000 tokens 57.9 us split by 2, 74.2 unsplit; 512 pairs of 4,000
-    //    tokens 107 against 121; 1,280 pairs of up to 16,384 414 us unsplit,
-    //    422 split by 2.
-    // (All with 7 us of event and graph overhead, 8-bit pools, 128 dimensions.)
+    //    6,000 tokens 68 us split by 2, 91 unsplit; 512 pairs of 4,000 tokens 126
+    //    against 146; 1,280 pairs of up to 16,384 445 us unsplit, 455 split by 2.
+    // (All with 9 us of event overhead, the L2 full of written data, 8-bit pools, 128
+    // dimensions.)
     Variant v = want_b8 ? variant<true, 4>(g.head_dim, bf, wide) : variant<false, 4>(g.head_dim, bf, wide);
     Limits lim;
     if (!limits(v, &lim)) return PKV_ERR_CUDA;
@@ -1003,8 +1006,8 @@ static int launch(const pkv_pool *pool, bool want_b8, void *out, const void *q, 
         while (C < 8 && 2 * pairs * C < 3 * lim.resident && most >= 48 * (C + 1)) ++C;
     if (pairs * 8 <= lim.sms && most >= 256) {
         // few long pairs: CTAs that take an SM each, in the largest clusters of
-        // which every pair gets one at once (8 pairs of 60,000 tokens: 33 us
-        // with 12 CTAs of 12 warps, 68 with 8 CTAs of four)
+        // which every pair gets one at once (8 pairs of 60,000 tokens, as above:
+        // 40 us with 12 CTAs of 12 warps, 50 with 8, 83 with 8 CTAs of four)
         v = want_b8 ? variant<true, 12>(g.head_dim, bf, wide) : variant<false, 8>(g.head_dim, bf, wide);
         if (!limits(v, &lim)) return PKV_ERR_CUDA;
         C = 1;
@@ -1035,7 +1038,8 @@ static int launch(const pkv_pool *pool, bool want_b8, void *out, const void *q, 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // more than one wave, lengths not levelled by a window: longest pairs first
     // (every CTA looks at every length for it, so not for thousands of sequences,
-    // whose many waves even out by themselves)
+    // whose many waves even out by themselves): the 1,280 pairs 445 us against 519 in
+    // index order, the 384 68 against 89
     p.most = pairs * C > lim.resident && most == maxb && most >= 64 && num_seqs <= 512 ? (int)most : 0;
     if (pairs * C > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     cudaLaunchAttribute attr[2];
