@@ -89,6 +89,8 @@ typedef enum pkv_status {
 #define PKV_DEV_BAD_LEN   0x4   /* attention: context_len < 0 or longer than table  */
 #define PKV_DEV_TIMEOUT   0x8   /* a bounded wait inside a kernel ran out           */
 #define PKV_DEV_BAD_POS   0x10  /* rotated append: position outside the cos/sin table */
+#define PKV_DEV_BAD_TREE  0x20  /* a drafted token's parent does not come before it, or
+                                 * kept positions that do not rise                    */
 
 typedef struct pkv_pool pkv_pool;
 
@@ -657,6 +659,96 @@ int paged_prefill_attention_window(const pkv_pool *pool, void *out, const void *
                                    int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
                                    float scale, int32_t window, int32_t sinks, void *workspace,
                                    size_t workspace_bytes, int32_t *d_status, void *stream);
+
+/* ------------------------------------------------ trees of drafted tokens
+ * (An addition of this library: the source pages have no counterpart.)
+ *
+ * A step that checks several drafted continuations of each sequence at once.
+ * Sequence s has n_s = query_start[s + 1] - query_start[s] drafted tokens in the
+ * order of a tree: node 0 is the root (the token that the last step gave), a
+ * node's parent comes before it.  Their K and V are written to the cache behind
+ * the sequence's own tokens (node i at position base + i, base = context_lens[s]
+ * - n_s; a rotation goes by depth, which is the caller's business), all nodes
+ * attend at once, the path that the model agrees with is found, and its tokens
+ * are moved together.  Per-node arrays are [num_tokens], sequence s's nodes in
+ * rows query_start[s] .. query_start[s + 1] - 1; query_start is device int32
+ * [num_seqs + 1].  Rows behind the last sequence's are neither read nor written. */
+
+/* Scratch bytes of paged_tree_attention for num_tokens rows; 0 on a bad argument. */
+size_t paged_tree_workspace_bytes(int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                  int32_t head_dim);
+
+/* Attention of drafted tokens.  Row r of q and out ([num_tokens][num_q_heads]
+ * [head_dim], the pool's type) is drafted token i = r - query_start[s] of its
+ * sequence; it attends to positions j < base and to drafted token d (position
+ * base + d) where bit d % 32 of tree_mask[r][d / 32] is set (int32
+ * [num_tokens][mask_words]; a token sees itself only if its own bit is set; bits
+ * from n_s on count for nothing).  n_s <= 32 * mask_words, mask_words 1 .. 32.
+ * context_lens[s] includes the drafted tokens.  A row that sees nothing is zero.
+ * What a row does not see cannot reach it, whatever it holds, NaN and infinities
+ * included.  A sequence whose lengths do not fit (PKV_DEV_BAD_LEN) or that has a
+ * bad table entry among its ceil(context_lens[s] / 16) blocks (PKV_DEV_BAD_BLOCK)
+ * gets zero rows.
+ *   workspace  paged_tree_workspace_bytes(...) bytes, 256-byte aligned, contents
+ *              of no account before and after; calls that may run at the same
+ *              time need one each
+ * 16-bit pools, head_dim 64 or 128, block_size 16, num_q_heads / num_kv_heads
+ * <= 16; results do not vary from run to run.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA. */
+int paged_tree_attention(const pkv_pool *pool, void *out, const void *q, const void *k_pool,
+                         const void *v_pool, const int32_t *block_tables,
+                         int32_t max_blocks_per_seq, const int32_t *query_start,
+                         const int32_t *context_lens, const int32_t *tree_mask, int32_t mask_words,
+                         int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads, float scale,
+                         void *workspace, size_t workspace_bytes, int32_t *d_status, void *stream);
+
+/* The path of each tree that the model agrees with, token by token: node 0 is
+ * kept; then, as long as some child of the last kept node holds the token
+ * targets[last kept node] (what the model answered there), the first such child
+ * in the tree's order.
+ *   tokens, targets  device [num_tokens], int32 (token_bytes 4) or int64 (8)
+ *   parents          device int32 [num_tokens]: index of the parent among the
+ *                    sequence's nodes, -1 for node 0; other nodes of parent -1
+ *                    are on no path
+ *   first            device int32 [num_seqs]: position of node 0 in the sequence
+ *   kept             device int32 [num_tokens], written: positions first + i of
+ *                    the kept nodes, in order, then -1 up to the sequence's end
+ *   num_kept         device int32 [num_seqs], written
+ *   next_tokens      device [num_seqs] of the tokens' type, written: the target
+ *                    at the last kept node, -1 where num_kept is 0
+ * A sequence without nodes keeps none.  A tree with a parent that does not come
+ * before its node (PKV_DEV_BAD_TREE), or a sequence whose row range does not fit
+ * or whose positions leave int32 (PKV_DEV_BAD_LEN) keeps none either.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_CUDA. */
+int kv_tree_accept(const void *tokens, const int32_t *parents, const void *targets,
+                   int32_t token_bytes, const int32_t *query_start, const int32_t *first,
+                   int32_t num_seqs, int32_t num_tokens, int32_t *kept, int32_t *num_kept,
+                   void *next_tokens, int32_t *d_status, void *stream);
+
+/* Move kept tokens together, in place: for i < num_kept[s], K and V (all kv
+ * heads, bit for bit) of sequence s's position kept[kept_start[s] + i] go to its
+ * position first[s] + i, as if all were read before the first is written.  The
+ * positions rise, none is below its destination.  For the path of a tree
+ * (kv_tree_accept's kept, num_kept and first, kept_start = query_start), and for
+ * any other choice of tokens to keep; blocks behind the last token are the
+ * ledger's to give back (kv_block_free).  Blocks that are written must not be
+ * shared with another sequence.
+ *   block_tables  device int32 [num_seqs][max_blocks_per_seq]
+ *   kept          device int32 [num_entries]; sequence s's begin at
+ *                 kept_start[s] (device int32 [num_seqs + 1])
+ *   num_kept      device int32 [num_seqs], at most kept_start[s + 1] - kept_start[s]
+ *   first         device int32 [num_seqs]
+ * A sequence whose ranges do not fit is left as it is (PKV_DEV_BAD_LEN); from the
+ * first position that does not rise, lies below its destination or outside the
+ * table row on, the rest of the sequence's stay where they are
+ * (PKV_DEV_BAD_TREE); a token whose own or destination block is not in the pool
+ * is skipped (PKV_DEV_BAD_BLOCK).  16-bit pools, rows of a multiple of 16 bytes.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA. */
+int kv_cache_compact(const pkv_pool *pool, const int32_t *block_tables,
+                     int32_t max_blocks_per_seq, const int32_t *kept, const int32_t *kept_start,
+                     const int32_t *num_kept, const int32_t *first, int32_t num_seqs,
+                     int32_t num_entries, void *k_pool, void *v_pool, int32_t *d_status,
+                     void *stream);
 
 /* ------------------------------------------------------------ status word */
 

@@ -19,6 +19,15 @@ A model that rotates K and its queries by position, and attends to a window:
     table = rope_table(max_positions, rotary_dim, device="cuda")
     q = cache_write_rope(pool, k_new, v_new, d_positions, table, d_slots, status, q=q)
     paged_decode_attention_window(pool, q, d_tables, d_lens, scale, window, sinks, status)
+
+A step that checks a tree of drafted tokens for each sequence (their K and V appended behind
+the sequence's own, in the tree's order, node 0 the token that the last step gave):
+
+    mask = tree_mask(d_parents, d_start)
+    out = paged_tree_attention(pool, q, d_tables, d_start, d_lens, mask, scale, ws, status)
+    # ... the model's answer at every node: d_targets
+    kept, num_kept, next_tokens = tree_accept(d_tokens, d_parents, d_targets, d_start, d_first, status)
+    cache_compact(pool, d_tables, kept, d_start, num_kept, d_first, status)   # in every layer
 """
 from __future__ import annotations
 
@@ -27,7 +36,7 @@ import ctypes
 import numpy as np
 
 from . import _native
-from ._native import (DEV_BAD_BLOCK, DEV_BAD_LEN, DEV_BAD_POS, DEV_BAD_SLOT, DEV_TIMEOUT,
+from ._native import (DEV_BAD_BLOCK, DEV_BAD_LEN, DEV_BAD_POS, DEV_BAD_SLOT, DEV_BAD_TREE, DEV_TIMEOUT,
                       PKV_B8_BF16, PKV_B8_F16, PKV_BF16, PKV_F16, PKV_Q8_BF16, PKV_Q8_F16,
                       PagedKVError, check, lib)
 
@@ -38,11 +47,13 @@ __all__ = ["KVPool", "PagedKVError", "cache_write", "block_copy", "gather_blocks
            "cache_write_q8", "paged_decode_attention_q8",
            "cache_write_rope", "rope_table", "cache_write_b8", "dequantize_blocks",
            "paged_decode_attention_b8", "paged_decode_attention_window",
-           "paged_prefill_attention_window",
+           "paged_prefill_attention_window", "paged_tree_attention", "tree_mask", "tree_accept",
+           "tree_workspace_bytes", "cache_compact",
            "prefill_workspace_bytes",
            "decode_workspace_bytes", "status_check", "kv_bytes_per_token",
            "kv_blocks_for_tokens", "kv_pool_bytes", "default_split", "lib",
-           "DEV_BAD_SLOT", "DEV_BAD_BLOCK", "DEV_BAD_LEN", "DEV_TIMEOUT", "DEV_BAD_POS"]
+           "DEV_BAD_SLOT", "DEV_BAD_BLOCK", "DEV_BAD_LEN", "DEV_TIMEOUT", "DEV_BAD_POS",
+           "DEV_BAD_TREE"]
 
 _DTYPES = {"f16": PKV_F16, "fp16": PKV_F16, "float16": PKV_F16,
            "bf16": PKV_BF16, "bfloat16": PKV_BF16,
@@ -736,7 +747,8 @@ def _load_torch():
     if _fastcall is not None:
         _fastcall.bind(*(ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in (
             "paged_decode_attention_window", "paged_decode_attention_b8", "kv_cache_write_rope",
-            "kv_dequantize_blocks", "paged_prefill_attention_window")))
+            "kv_dequantize_blocks", "paged_prefill_attention_window", "paged_tree_attention",
+            "kv_tree_accept", "kv_cache_compact")))
     _torch, _fast = torch, _fastcall
     return torch
 
@@ -1077,6 +1089,175 @@ def paged_prefill_attention_window(pool: KVPool, q, block_tables, query_start, c
     _launch("paged_prefill_attention_window", dev, stream, pool.handle, op, qp, kp, vp, tp, maxb,
             sp, lp, S, T, hq, float(scale), window, sinks, wp, nbytes, _want_status(status, dev))
     return out
+
+
+# ------------------------------------------------------- trees of drafted tokens
+def tree_workspace_bytes(num_tokens: int, num_q_heads: int, num_kv_heads: int,
+                         head_dim: int) -> int:
+    """Workspace bytes of ``paged_tree_attention`` for up to ``num_tokens`` rows; 0 for a
+    shape that it does not take."""
+    return lib().paged_tree_workspace_bytes(num_tokens, num_q_heads, num_kv_heads, head_dim)
+
+
+def tree_mask(parents, query_start, words: int | None = None):
+    """Bit masks of ``paged_tree_attention``, int32 [T][words], from the trees' ``parents``
+    (int32 [T], index among the sequence's nodes, -1 for a root; rows by ``query_start`` int32
+    [S + 1]): every node sees itself and the nodes above it.  Rows behind the last sequence are
+    zero.  ``words`` (room for 32 nodes of a sequence each) is read from ``query_start`` when
+    it is not given, which waits for the device.  Plain tensor operations on the parents'
+    device."""
+    import torch
+    T = parents.shape[0]
+    start = query_start.long()
+    if words is None:
+        words = max(1, -(-int((start[1:] - start[:-1]).max()) // 32)) if len(start) > 1 else 1
+    if not 1 <= words <= 32:
+        raise ValueError(f"1 to 32 words of 32 nodes, got {words}")
+    if T == 0:
+        return torch.zeros((0, words), dtype=torch.int32, device=parents.device)
+    t = torch.arange(T, device=parents.device)
+    s = (torch.searchsorted(start, t, right=True) - 1).clamp(0, len(start) - 2)
+    node = t - start[s]
+    inside = (t >= start[0]) & (t < start[-1])
+    up = torch.where((parents >= 0) & inside, start[s] + parents, t)
+    up = torch.where((up >= 0) & (up < t), up, t)              # anything else: no parent
+    bit = torch.where(inside, 1 << (node % 32), 0)
+    mask = torch.where(torch.arange(words, device=parents.device) == (node // 32)[:, None],
+                       bit[:, None], 0)
+    for _ in range((32 * words - 1).bit_length()):             # twice as far up each time
+        mask = mask | mask[up]
+        up = up[up]
+    # a word's 32 bits as int32
+    return torch.where(mask >= 1 << 31, mask - (1 << 32), mask).to(torch.int32)
+
+
+def paged_tree_attention(pool: KVPool, q, block_tables, query_start, context_lens, tree_mask,
+                         scale: float, workspace, status, out=None, k_pool=None, v_pool=None,
+                         stream=None):
+    """Attention of each sequence's drafted tokens over its cache and over those drafted tokens
+    that their masks name (16-bit pools).
+
+    ``q`` [T][Hq][D]: the drafted tokens of all sequences, sequence s's in rows
+    ``query_start[s]`` .. ``query_start[s + 1] - 1`` (int32 device [S + 1]); their K and V
+    stand at its last positions, ``context_lens`` (int32 device [S]) includes them.
+    ``tree_mask`` int32 [T][words]: bit j of a row, bit j % 32 of word j // 32, lets it see
+    drafted token j of its sequence (``tree_mask`` makes it of a tree's parents); all see the
+    cache before the drafted tokens.  A row that sees nothing is zero.  ``workspace`` a uint8 device
+    tensor of ``tree_workspace_bytes(...)`` bytes, one for each call that may run at the same time.
+    Returns ``out`` [T][Hq][D]."""
+    torch = _torch or _load_torch()
+    if pool.record_bytes:
+        raise ValueError("paged_tree_attention takes a 16-bit pool")
+    if out is None:
+        out = torch.empty_like(q)
+    if _fast is not None:
+        rc = _fast.tree(pool._meta, q, out, block_tables, query_start, context_lens, tree_mask,
+                        float(scale), workspace, status, pool.k_pool if k_pool is None else k_pool,
+                        pool.v_pool if v_pool is None else v_pool, _raw(stream))
+        if rc is not None:
+            if rc:
+                check(rc, "paged_tree_attention")
+            return out
+    dev, dt, D = q.get_device(), _row_dtype(pool), pool.head_dim
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError(f"q must be [n][h][{D}], got {list(q.shape)}")
+    T, hq, _ = shape = tuple(q.shape)
+    if hq % pool.num_kv_heads:
+        raise ValueError(f"q has {hq} heads, not a multiple of the pool's "
+                         f"{pool.num_kv_heads} kv heads")
+    qp = _want("q", q, shape, dt, dev)
+    op = _want("out", out, shape, dt, dev)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must have 2 dimensions")
+    S, maxb = block_tables.shape
+    tp = _want("block_tables", block_tables, (S, maxb), torch.int32, dev)
+    lp = _want("context_lens", context_lens, (S,), torch.int32, dev)
+    sp = _want("query_start", query_start, (S + 1,), torch.int32, dev)
+    if tree_mask.dim() != 2:
+        raise ValueError("tree_mask must be [n][words]")
+    words = tree_mask.shape[1]
+    mp = _want("tree_mask", tree_mask, (T, words), torch.int32, dev)
+    nbytes = workspace.numel()
+    wp = _want("workspace", workspace, (nbytes,), torch.uint8, dev)
+    kp, vp = _want_pools(pool, dev, k_pool, v_pool)
+    _launch("paged_tree_attention", dev, stream, pool.handle, op, qp, kp, vp, tp, maxb, sp, lp, mp,
+            words, S, T, hq, float(scale), wp, nbytes, _want_status(status, dev))
+    return out
+
+
+def tree_accept(tokens, parents, targets, query_start, first, status, kept=None, num_kept=None,
+                next_tokens=None, stream=None):
+    """The path of each drafted tree that the model agrees with: its root, then, as long as a
+    child of the last kept node holds the token that the model answered there, the first such
+    child.
+
+    ``tokens`` and ``targets`` (the model's answers) [T], both int32 or both int64; ``parents``
+    int32 [T], -1 for a sequence's root, its node 0; ``query_start`` int32 [S + 1] as in
+    ``paged_tree_attention``; ``first`` int32 [S]: position of each root in its sequence.
+    Returns ``kept`` int32 [T] (the path's positions in each sequence's rows, then -1),
+    ``num_kept`` int32 [S] and ``next_tokens`` [S] (the model's answer at the path's end, -1
+    without one); buffers that are given are used."""
+    torch = _torch or _load_torch()
+    if kept is None:
+        kept = torch.full((tokens.shape[0],), -1, dtype=torch.int32, device=tokens.device)
+    if num_kept is None:
+        num_kept = torch.empty_like(first)
+    if next_tokens is None:
+        next_tokens = torch.empty((first.shape[0],), dtype=tokens.dtype, device=tokens.device)
+    if _fast is not None:
+        rc = _fast.accept(tokens, parents, targets, query_start, first, kept, num_kept,
+                          next_tokens, status, _raw(stream))
+        if rc is not None:
+            if rc:
+                check(rc, "kv_tree_accept")
+            return kept, num_kept, next_tokens
+    dev, dt = tokens.get_device(), tokens.dtype
+    if dt not in (torch.int32, torch.int64):
+        raise TypeError(f"tokens must be int32 or int64, got {str(dt).replace('torch.', '')}")
+    T = tokens.shape[0] if tokens.dim() == 1 else -1
+    S = first.shape[0] if first.dim() == 1 else -1
+    ptrs = [_want(name, t, shape, want, dev) for name, t, shape, want in (
+        ("tokens", tokens, (T,), dt), ("parents", parents, (T,), torch.int32),
+        ("targets", targets, (T,), dt), ("query_start", query_start, (S + 1,), torch.int32),
+        ("first", first, (S,), torch.int32), ("kept", kept, (T,), torch.int32),
+        ("num_kept", num_kept, (S,), torch.int32), ("next_tokens", next_tokens, (S,), dt))]
+    _launch("kv_tree_accept", dev, stream, *ptrs[:3], dt.itemsize, *ptrs[3:5], S, T, *ptrs[5:],
+            _want_status(status, dev))
+    return kept, num_kept, next_tokens
+
+
+def cache_compact(pool: KVPool, block_tables, kept, kept_start, num_kept, first, status,
+                  k_pool=None, v_pool=None, stream=None) -> None:
+    """Move kept tokens of the cache together, in place (16-bit pools): K and V of position
+    ``kept[kept_start[s] + i]`` of sequence s go to its position ``first[s] + i``, i <
+    ``num_kept[s]``.  A sequence's positions rise, none is below its destination; blocks that
+    are written must not be shared.  ``kept`` int32 [N], ``kept_start`` int32 [S + 1],
+    ``num_kept`` and ``first`` int32 [S], ``block_tables`` int32 [S][max_blocks], all on the
+    device: for trees ``tree_accept``'s results with ``kept_start`` = ``query_start``, for a policy
+    of leaving out tokens whatever it keeps.  The ledger's blocks behind the last token are then
+    the caller's to give back (``pool.free``)."""
+    torch = _torch or _load_torch()
+    if pool.record_bytes:
+        raise ValueError("cache_compact takes a 16-bit pool")
+    if _fast is not None:
+        rc = _fast.compact(pool._meta, block_tables, kept, kept_start, num_kept, first, status,
+                           pool.k_pool if k_pool is None else k_pool,
+                           pool.v_pool if v_pool is None else v_pool, _raw(stream))
+        if rc is not None:
+            if rc:
+                check(rc, "kv_cache_compact")
+            return
+    dev = kept.get_device()
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must have 2 dimensions")
+    S, maxb = block_tables.shape
+    N = kept.shape[0] if kept.dim() == 1 else -1
+    ptrs = [_want(name, t, shape, torch.int32, dev) for name, t, shape in (
+        ("block_tables", block_tables, (S, maxb)), ("kept", kept, (N,)),
+        ("kept_start", kept_start, (S + 1,)), ("num_kept", num_kept, (S,)), ("first", first, (S,)))]
+    kp, vp = _want_pools(pool, dev, k_pool, v_pool)
+    _launch("kv_cache_compact", dev, stream, pool.handle, ptrs[0], maxb, *ptrs[1:], S, N, kp, vp,
+            _want_status(status, dev))
 
 
 def status_check(status, stream=None):

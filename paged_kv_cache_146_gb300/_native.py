@@ -20,7 +20,8 @@ STATUS_NAMES = {
     -3: "PKV_ERR_BAD_BLOCK", -4: "PKV_ERR_CUDA", -5: "PKV_ERR_DEVICE_BOUNDS",
     -6: "PKV_ERR_DEVICE_TIMEOUT", -7: "PKV_ERR_SHARED_BLOCK", -8: "PKV_ERR_UNSUPPORTED",
 }
-DEV_BAD_SLOT, DEV_BAD_BLOCK, DEV_BAD_LEN, DEV_TIMEOUT, DEV_BAD_POS = 0x1, 0x2, 0x4, 0x8, 0x10
+DEV_BAD_SLOT, DEV_BAD_BLOCK, DEV_BAD_LEN, DEV_TIMEOUT, DEV_BAD_POS, DEV_BAD_TREE = (
+    0x1, 0x2, 0x4, 0x8, 0x10, 0x20)
 
 # (name, restype, argtypes) of every symbol the header declares
 _i32, _i64, _sz, _f32, _p = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float, ctypes.c_void_p
@@ -78,6 +79,13 @@ SIGNATURES = [
      [_p, _p, _p, _p, _p, _p, _i32, _p, _i32, _i32, _f32, _i32, _i32, _p, _p]),
     ("paged_prefill_attention_window", ctypes.c_int,
      [_p, _p, _p, _p, _p, _p, _i32, _p, _p, _i32, _i32, _i32, _f32, _i32, _i32, _p, _sz, _p, _p]),
+    ("paged_tree_workspace_bytes", _sz, [_i32, _i32, _i32, _i32]),
+    ("paged_tree_attention", ctypes.c_int,
+     [_p, _p, _p, _p, _p, _p, _i32, _p, _p, _p, _i32, _i32, _i32, _i32, _f32, _p, _sz, _p, _p]),
+    ("kv_tree_accept", ctypes.c_int,
+     [_p, _p, _p, _i32, _p, _p, _i32, _i32, _p, _p, _p, _p, _p]),
+    ("kv_cache_compact", ctypes.c_int,
+     [_p, _p, _i32, _p, _p, _p, _p, _i32, _i32, _p, _p, _p, _p]),
     ("kv_status_check", ctypes.c_int, [_p, _p, _pi32]),
 ]
 

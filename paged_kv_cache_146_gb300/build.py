@@ -27,7 +27,7 @@ FASTCALL = os.path.join(PKG, "_fastcall.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["ledger.cpp", "cache_write.cu", "paged_decode.cu", "paged_decode_q8.cu",
-           "paged_prefill.cu", "append_rope.cu", "paged_window.cu"]
+           "paged_prefill.cu", "append_rope.cu", "paged_window.cu", "paged_tree.cu", "cache_compact.cu"]
 
 
 def nvcc() -> str:

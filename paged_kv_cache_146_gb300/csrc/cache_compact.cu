@@ -1,0 +1,244 @@
+// The accepted path of a tree of drafted tokens, and moving kept tokens of the cache
+// together.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "pagedkv.h"
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+namespace compact {
+
+// Every kernel here is launched with the programmatic attribute: it may be set up while
+// the kernel before it ends, and waits for that end ahead of its first access to memory.
+template <typename... P, typename... A>
+static int launch(void (*fn)(P...), dim3 grid, int threads, cudaStream_t st, const A &...args)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------- accepted path
+struct Trees {
+    const void *tokens, *targets;
+    const int32_t *parents, *query_start, *first;
+    int32_t num_seqs, num_tokens;
+    int32_t *kept, *num_kept;
+    void *next_tokens;
+    int32_t *status;
+};
+
+// A warp per sequence.  A step of the path asks 32 nodes at a time whether their parent is
+// the last kept node and their token its target; what it reads was read by the check of
+// the parents before, so a step costs a few accesses to L1.
+constexpr int kAcceptWarps = 4;
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kAcceptWarps) tree_accept_kernel(const Trees p)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int s = blockIdx.x * kAcceptWarps + (threadIdx.x >> 5);
+    if (s >= p.num_seqs) return;
+    const int r0 = p.query_start[s], r1 = p.query_start[s + 1], first = p.first[s];
+    const bool rows_ok = 0 <= r0 && r0 <= r1 && r1 <= p.num_tokens;
+    const int n = rows_ok ? r1 - r0 : 0;
+    const bool fits = rows_ok && first >= 0 && first <= INT32_MAX - n;
+    const T *tokens = static_cast<const T *>(p.tokens) + (n ? r0 : 0);
+    const T *targets = static_cast<const T *>(p.targets) + (n ? r0 : 0);
+    const int32_t *parents = p.parents + (n ? r0 : 0);
+    int32_t *kept = p.kept + (n ? r0 : 0);
+    bool bad = false;
+    for (int i = lane; i < n; i += 32) {
+        const int up = parents[i];
+        bad |= up < -1 || up >= i;                   // node 0: -1
+        kept[i] = -1;
+    }
+    bad = __any_sync(kFull, bad);
+    if (lane == 0 && (!fits || bad)) atomicOr(p.status, fits ? PKV_DEV_BAD_TREE : PKV_DEV_BAD_LEN);
+    int num = 0;
+    T next = (T)-1;
+    if (fits && !bad && n > 0) {
+        __syncwarp();                                // the -1 before the positions
+        int at = 0;
+        for (;;) {
+            if (lane == 0) kept[num] = first + at;
+            ++num;
+            next = targets[at];
+            int found = -1;
+            for (int i0 = (at + 1) & ~31; i0 < n; i0 += 32) {
+                const int i = i0 + lane;
+                const bool hit = i > at && i < n && parents[i] == at && tokens[i] == next;
+                const unsigned hits = __ballot_sync(kFull, hit);
+                if (hits) {
+                    found = i0 + __ffs(hits) - 1;
+                    break;
+                }
+            }
+            if (found < 0) break;
+            at = found;
+        }
+    }
+    if (lane == 0) {
+        p.num_kept[s] = num;
+        static_cast<T *>(p.next_tokens)[s] = next;
+    }
+}
+
+// ------------------------------------------------------------------- moving tokens
+struct Moves {
+    const int32_t *block_tables, *kept, *kept_start, *num_kept, *first;
+    int32_t max_blocks_per_seq, num_entries, num_kv_heads, block_size, num_blocks;
+    int32_t chunks;                      // 16-byte chunks of a row
+    int32_t parts, part_chunks;          // CTAs that share a row, chunks of each
+    uint4 *k_pool, *v_pool;
+    int32_t *status;
+};
+
+constexpr int kMoveThreads = 256, kMoveDepth = 8;
+
+// A CTA takes a sequence, a kv head, K or V, and a share of each row; nothing else reads or
+// writes these bytes.  It goes through the kept tokens in order, a batch at a time: all of
+// the batch's rows are read, then written.  A destination is never above its source and
+// sources rise, so what a batch writes is no source of a later one.
+__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const Moves p)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int s = blockIdx.y, tid = threadIdx.x;
+    const int start = p.kept_start[s], end = p.kept_start[s + 1], n = p.num_kept[s], first = p.first[s];
+    if (!(0 <= start && start <= end && end <= p.num_entries && 0 <= n && n <= end - start && first >= 0)) {
+        if (blockIdx.x == 0 && tid == 0) atomicOr(p.status, PKV_DEV_BAD_LEN);
+        return;
+    }
+    const int part = blockIdx.x % p.parts, rest = blockIdx.x / p.parts;
+    const int g = rest >> 1;
+    uint4 *pool = rest & 1 ? p.v_pool : p.k_pool;
+    const int c0 = part * p.part_chunks, nc = min(p.part_chunks, p.chunks - c0);
+    if (nc <= 0) return;
+    const int per_pass = kMoveThreads / nc;              // tokens of one pass of the threads
+    const int c = tid % nc, k = tid / nc;
+    const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
+    const int32_t *kept = p.kept + start;
+    const int64_t limit = (int64_t)p.max_blocks_per_seq * p.block_size;
+    auto place = [&](int pos) -> int64_t {               // chunk index in the pool, -1: bad block
+        const int id = row[pos / p.block_size];
+        if (id < 0 || id >= p.num_blocks) return -1;
+        return (((int64_t)id * p.num_kv_heads + g) * p.block_size + pos % p.block_size) * p.chunks + c0 + c;
+    };
+    bool ok = true;
+    for (int i0 = 0; i0 < n && ok; i0 += per_pass * kMoveDepth) {
+        uint4 v[kMoveDepth];
+        int64_t to[kMoveDepth];
+        int stop = n;                                    // first entry that may not move
+        bool lost = false;
+#pragma unroll
+        for (int d = 0; d < kMoveDepth; ++d) {
+            const int i = i0 + d * per_pass + k;
+            to[d] = -1;
+            if (k >= per_pass || i >= n) continue;
+            const int pos = kept[i];
+            const int64_t dst = (int64_t)first + i;
+            if (pos < dst || (i > 0 && kept[i - 1] >= pos) || pos >= limit) {
+                stop = min(stop, i);
+                continue;
+            }
+            if (pos == dst) continue;
+            const int64_t from = place(pos), there = place((int)dst);
+            lost |= from < 0 || there < 0;
+            if (from < 0 || there < 0) continue;
+            v[d] = pool[from];
+            to[d] = there;
+        }
+        __shared__ int stops;
+        if (tid == 0) stops = n;
+        __syncthreads();
+        if (stop < n) atomicMin(&stops, stop);
+        if (lost && blockIdx.x == 0) atomicOr(p.status, PKV_DEV_BAD_BLOCK);
+        __syncthreads();                                 // and every row of the batch is read
+        stop = stops;
+#pragma unroll
+        for (int d = 0; d < kMoveDepth; ++d)
+            if (to[d] >= 0 && i0 + d * per_pass + k < stop) pool[to[d]] = v[d];
+        ok = stop >= n;
+        if (!ok && blockIdx.x == 0 && tid == 0) atomicOr(p.status, PKV_DEV_BAD_TREE);
+        __syncthreads();
+    }
+}
+
+}  // namespace compact
+}  // namespace pkv
+
+extern "C" int kv_tree_accept(const void *tokens, const int32_t *parents, const void *targets,
+                              int32_t token_bytes, const int32_t *query_start,
+                              const int32_t *first, int32_t num_seqs, int32_t num_tokens,
+                              int32_t *kept, int32_t *num_kept, void *next_tokens,
+                              int32_t *d_status, void *stream)
+{
+    using namespace pkv::compact;
+    if ((token_bytes != 4 && token_bytes != 8) || num_seqs < 0 || num_tokens < 0)
+        return PKV_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PKV_OK;
+    if (!query_start || !first || !num_kept || !next_tokens || !d_status) return PKV_ERR_INVALID_ARG;
+    if (num_tokens > 0 && (!tokens || !parents || !targets || !kept)) return PKV_ERR_INVALID_ARG;
+    const uintptr_t wide = (uintptr_t)tokens | (uintptr_t)targets | (uintptr_t)next_tokens;
+    const uintptr_t words = (uintptr_t)parents | (uintptr_t)query_start | (uintptr_t)first |
+                            (uintptr_t)kept | (uintptr_t)num_kept | (uintptr_t)d_status;
+    if ((wide & (uintptr_t)(token_bytes - 1)) || (words & 3u)) return PKV_ERR_INVALID_ARG;
+    const Trees p = {tokens, targets, parents, query_start, first, num_seqs, num_tokens,
+                     kept, num_kept, next_tokens, d_status};
+    const dim3 grid((unsigned)((num_seqs + kAcceptWarps - 1) / kAcceptWarps));
+    return launch(token_bytes == 8 ? &tree_accept_kernel<int64_t> : &tree_accept_kernel<int32_t>, grid,
+                  32 * kAcceptWarps, (cudaStream_t)stream, p);
+}
+
+extern "C" int kv_cache_compact(const pkv_pool *pool, const int32_t *block_tables,
+                                int32_t max_blocks_per_seq, const int32_t *kept,
+                                const int32_t *kept_start, const int32_t *num_kept,
+                                const int32_t *first, int32_t num_seqs, int32_t num_entries,
+                                void *k_pool, void *v_pool, int32_t *d_status, void *stream)
+{
+    using namespace pkv::compact;
+    pkv::PoolGeometry g;
+    if (!pkv::pool_geometry(pool, &g) || !pkv::is_16bit(g)) return PKV_ERR_INVALID_ARG;
+    if (num_seqs < 0 || num_entries < 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
+    if (g.head_dim % 8) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_entries == 0) return PKV_OK;
+    if (!block_tables || !kept || !kept_start || !num_kept || !first || !k_pool || !v_pool || !d_status)
+        return PKV_ERR_INVALID_ARG;
+    if (!pkv::aligned16(k_pool) || !pkv::aligned16(v_pool) || ((uintptr_t)block_tables & 3u) ||
+        ((uintptr_t)kept & 3u) || ((uintptr_t)kept_start & 3u) || ((uintptr_t)num_kept & 3u) ||
+        ((uintptr_t)first & 3u) || ((uintptr_t)d_status & 3u))
+        return PKV_ERR_INVALID_ARG;
+    Moves p;
+    p.block_tables = block_tables;
+    p.kept = kept;
+    p.kept_start = kept_start;
+    p.num_kept = num_kept;
+    p.first = first;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.num_entries = num_entries;
+    p.num_kv_heads = g.num_kv_heads;
+    p.block_size = g.block_size;
+    p.num_blocks = g.num_blocks;
+    p.chunks = g.head_dim / 8;
+    p.part_chunks = std::min(p.chunks, 16);
+    p.parts = (p.chunks + p.part_chunks - 1) / p.part_chunks;
+    p.k_pool = static_cast<uint4 *>(k_pool);
+    p.v_pool = static_cast<uint4 *>(v_pool);
+    p.status = d_status;
+    if (num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)(g.num_kv_heads * 2 * p.parts), (unsigned)num_seqs);
+    return launch(&compact_kernel, grid, kMoveThreads, (cudaStream_t)stream, p);
+}

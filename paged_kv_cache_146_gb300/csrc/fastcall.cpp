@@ -27,6 +27,9 @@ decltype(&paged_decode_attention_b8) decode_b8 = nullptr;
 decltype(&kv_cache_write_rope) write_rope = nullptr;
 decltype(&kv_dequantize_blocks) dequantize = nullptr;
 decltype(&paged_prefill_attention_window) prefill_window = nullptr;
+decltype(&paged_tree_attention) tree_attention = nullptr;
+decltype(&kv_tree_accept) tree_accept = nullptr;
+decltype(&kv_cache_compact) cache_compact = nullptr;
 
 // The library is called without the interpreter lock, like through ctypes: a launch
 // waits while the driver's queue is full.
@@ -277,15 +280,104 @@ PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// (pool, q, out, tables, query_start, lens, mask, scale, workspace, status, k_pool, v_pool, stream)
+PyObject *tree(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> long {
+        want(n == 13 && tree_attention);
+        const Pool p = pool_of(a[0]);
+        const at::Tensor &q = tensor(a[1]);
+        want(!p.record && q.is_cuda() && q.dim() == 3 && q.scalar_type() == p.rows &&
+             q.is_contiguous());
+        const auto dev = static_cast<c10::DeviceIndex>(q.get_device());
+        const int64_t T = q.size(0), hq = q.size(1);
+        want(q.size(2) == p.dim && hq % p.heads == 0 && T <= INT32_MAX && hq <= INT32_MAX);
+        void *out = dense(a[2], q.sizes(), p.rows, dev);
+        const at::Tensor &tables = tensor(a[3]), &mask = tensor(a[6]), &ws = tensor(a[8]);
+        want(tables.dim() == 2 && tables.size(0) < INT32_MAX && tables.size(1) <= INT32_MAX &&
+             mask.dim() == 2 && mask.size(1) <= INT32_MAX && ws.dim() == 1);
+        const int64_t S = tables.size(0), maxb = tables.size(1), words = mask.size(1);
+        const int64_t ts[2] = {S, maxb}, ls[1] = {S}, qs[1] = {S + 1}, ms[2] = {T, words};
+        const auto *tp = static_cast<const int32_t *>(dense(a[3], ts, at::kInt, dev));
+        const auto *sp = static_cast<const int32_t *>(dense(a[4], qs, at::kInt, dev));
+        const auto *lp = static_cast<const int32_t *>(dense(a[5], ls, at::kInt, dev));
+        const auto *mp = static_cast<const int32_t *>(dense(a[6], ms, at::kInt, dev));
+        want(PyFloat_Check(a[7]));
+        const float scale = static_cast<float>(PyFloat_AS_DOUBLE(a[7]));
+        void *wp = dense(a[8], ws.sizes(), at::kByte, dev);
+        auto *status = static_cast<int32_t *>(status_word(a[9], dev));
+        const Pools pools = pools_of(p, a[10], a[11], dev);
+        void *stream = stream_of(a[12], dev);
+        const Unlocked unlocked;
+        return tree_attention(p.handle, out, q.data_ptr(), pools.a, pools.b, tp, (int32_t)maxb, sp, lp,
+                              mp, (int32_t)words, (int32_t)S, (int32_t)T, (int32_t)hq, scale, wp,
+                              (size_t)ws.numel(), status, stream);
+    });
+}
+
+// (tokens, parents, targets, query_start, first, kept, num_kept, next_tokens, status, stream)
+PyObject *accept(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> long {
+        want(n == 10 && tree_accept);
+        const at::Tensor &tokens = tensor(a[0]), &first = tensor(a[4]);
+        const at::ScalarType type = tokens.scalar_type();
+        want(tokens.is_cuda() && tokens.dim() == 1 && first.dim() == 1 &&
+             (type == at::kInt || type == at::kLong) && tokens.size(0) <= INT32_MAX &&
+             first.size(0) < INT32_MAX);
+        const auto dev = static_cast<c10::DeviceIndex>(tokens.get_device());
+        const int64_t S = first.size(0), ts[1] = {tokens.size(0)}, ss[1] = {S}, qs[1] = {S + 1};
+        const void *tp = dense(a[0], ts, type, dev), *gp = dense(a[2], ts, type, dev);
+        const auto *pp = static_cast<const int32_t *>(dense(a[1], ts, at::kInt, dev));
+        const auto *sp = static_cast<const int32_t *>(dense(a[3], qs, at::kInt, dev));
+        const auto *fp = static_cast<const int32_t *>(dense(a[4], ss, at::kInt, dev));
+        auto *kp = static_cast<int32_t *>(dense(a[5], ts, at::kInt, dev));
+        auto *np = static_cast<int32_t *>(dense(a[6], ss, at::kInt, dev));
+        void *xp = dense(a[7], ss, type, dev);
+        auto *status = static_cast<int32_t *>(status_word(a[8], dev));
+        void *stream = stream_of(a[9], dev);
+        const Unlocked unlocked;
+        return tree_accept(tp, pp, gp, type == at::kLong ? 8 : 4, sp, fp, (int32_t)S, (int32_t)ts[0], kp,
+                           np, xp, status, stream);
+    });
+}
+
+// (pool, tables, kept, kept_start, num_kept, first, status, k_pool, v_pool, stream)
+PyObject *compact(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> long {
+        want(n == 10 && cache_compact);
+        const Pool p = pool_of(a[0]);
+        const at::Tensor &tables = tensor(a[1]), &kept = tensor(a[2]);
+        want(!p.record && kept.is_cuda() && kept.dim() == 1 && kept.size(0) <= INT32_MAX &&
+             tables.dim() == 2 && tables.size(0) < INT32_MAX && tables.size(1) <= INT32_MAX);
+        const auto dev = static_cast<c10::DeviceIndex>(kept.get_device());
+        const int64_t S = tables.size(0), maxb = tables.size(1);
+        const int64_t ts[2] = {S, maxb}, ks[1] = {kept.size(0)}, ss[1] = {S}, qs[1] = {S + 1};
+        const auto *tp = static_cast<const int32_t *>(dense(a[1], ts, at::kInt, dev));
+        const auto *kp = static_cast<const int32_t *>(dense(a[2], ks, at::kInt, dev));
+        const auto *sp = static_cast<const int32_t *>(dense(a[3], qs, at::kInt, dev));
+        const auto *np = static_cast<const int32_t *>(dense(a[4], ss, at::kInt, dev));
+        const auto *fp = static_cast<const int32_t *>(dense(a[5], ss, at::kInt, dev));
+        auto *status = static_cast<int32_t *>(status_word(a[6], dev));
+        const Pools pools = pools_of(p, a[7], a[8], dev);
+        void *stream = stream_of(a[9], dev);
+        const Unlocked unlocked;
+        return cache_compact(p.handle, tp, (int32_t)maxb, kp, sp, np, fp, (int32_t)S, (int32_t)ks[0],
+                             pools.a, pools.b, status, stream);
+    });
+}
+
 // Addresses of the library's entry points, in the order of the variables above.
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    if (n != 5) {
-        PyErr_SetString(PyExc_TypeError, "bind takes five addresses");
+    constexpr int kEntries = 8;
+    if (n != kEntries) {
+        PyErr_SetString(PyExc_TypeError, "bind takes eight addresses");
         return nullptr;
     }
-    void *p[5];
-    for (int i = 0; i < 5; ++i) {
+    void *p[kEntries];
+    for (int i = 0; i < kEntries; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (!p[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
@@ -297,6 +389,9 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
     write_rope = reinterpret_cast<decltype(write_rope)>(p[2]);
     dequantize = reinterpret_cast<decltype(dequantize)>(p[3]);
     prefill_window = reinterpret_cast<decltype(prefill_window)>(p[4]);
+    tree_attention = reinterpret_cast<decltype(tree_attention)>(p[5]);
+    tree_accept = reinterpret_cast<decltype(tree_accept)>(p[6]);
+    cache_compact = reinterpret_cast<decltype(cache_compact)>(p[7]);
     Py_RETURN_NONE;
 }
 
@@ -307,7 +402,8 @@ PyMethodDef method(const char *name)
 }
 
 PyMethodDef methods[] = {method<decode>("decode"), method<rope>("rope"), method<dequant>("dequantize"),
-                         method<prefill>("prefill"), method<bind>("bind"),
+                         method<prefill>("prefill"), method<tree>("tree"), method<accept>("accept"),
+                         method<compact>("compact"), method<bind>("bind"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, methods};
