@@ -4,87 +4,1015 @@
 //   x_j = scale <q, K_j>,  out = sum_j softmax(x)_j V_j   over the j that it sees:
 //   j < base,  or  base <= j < L and bit j - base of its mask is set.
 //
-// One warp per row and query head, a key at a time.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+// All n G rows of a (sequence, kv head) share its keys, so K and V are read once for up to
+// NG * 128 rows, one row to a lane of tensor memory, and both products run on tcgen05.
+// Work items are (sequence, kv head, NG query tiles); their key tiles (64 keys), written one
+// after the other with kItemCost tiles' worth of overhead before each item, are cut into
+// equal ranges, one to a CTA: every CTA has the same work, whatever the lengths, and an item
+// is cut where a range ends.  A cut item's pieces (unnormalised output, reference maximum,
+// sum; fp32) meet in the workspace and a second kernel joins them, always in the same order.
+//
+//   NG = 1 (rows fit one query tile): two CTAs to an SM, 256 columns of tensor memory each;
+//     while one waits for its softmax or begins an item, the other keeps copies and
+//     products going.
+//   NG = 2: one CTA to an SM, two query tiles against the same K and V.
+//
+// Roles of a CTA's warps:
+//   softmax (4 NG): thread r of a query tile owns row r.  Weights are taken against a lazy
+//     reference maximum (it moves when a score exceeds it by more than kLazy, in log2
+//     units), as two 16-bit parts each, into tensor memory.
+//   producer: a ring of K tiles and one of V tiles, one TMA box to each block and 64 columns;
+//     the item's query rows.
+//   issuers (NG): S = Q K^T into one of two buffers, then O += P V of the tile before.
+//   cleaner: V of keys that no row may be reached by.  A weight of zero does not stop a NaN
+//     or an infinity in V, so in tiles that hold drafted tokens or the end of the sequence V
+//     behind the end becomes zero, and so do V's odd values; rows that see such a key get
+//     them added by hand (rare).
+// Every wait is bounded; on expiry the kernel flags PKV_DEV_TIMEOUT and stops.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
 
 #include "pagedkv.h"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "tc_device.cuh"
 
 namespace pkv {
 namespace tree {
 
+constexpr int kRows = 128;             // M: rows of a query tile
+constexpr int kKeys = 64;              // keys of a tile
 constexpr int kMaxWords = 32;
+constexpr int kTilesKnown = 16;
+constexpr float kLazy = 8.f;
+constexpr int kItemCost = 2;           // an item's beginning and end, in tiles
+constexpr int kMinRange = 4;           // a range has at least so many
+constexpr int kSnap = 2;               // no piece shorter than this is cut off an item
+constexpr int kMaxRanges = 304;        // CTAs of a call, at most
 
 struct Params {
     void *out;
-    const void *q, *k_pool, *v_pool;
+    const void *v_pool;
     const int32_t *block_tables, *query_start, *context_lens;
     const uint32_t *mask;
-    int32_t words, num_seqs, num_tokens, num_q_heads, num_kv_heads, max_blocks_per_seq, num_blocks;
+    int32_t words, num_seqs, num_tokens, num_q_heads, num_kv_heads, group;
+    int32_t max_blocks_per_seq, num_blocks;
+    int32_t tile_tokens;               // tokens of a query tile
+    int32_t box_tokens;                // and of one box of query rows
+    int32_t piece_rows;                // rows of a piece's place in the workspace
     float scale_log2;
+    int32_t *header;                   // [0] = ranges
+    int4 *ranges;                      // see Range
+    float2 *part_ml;                   // [2 ranges][piece_rows]: (reference, sum); sum < 0: bad block
+    float4 *part_o;                    // [2 ranges][D / 4][piece_rows]
     int32_t *status;
 };
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(256) tree_rows_kernel(const Params p)
+// What a range's CTA leaves for the joining kernel: x = 1 it holds the continuation of an item
+// that began in an earlier range (piece 2 b), + 2 up to the item's end, + 4 it begins an item that
+// ends in a later range (piece 2 b + 1): sequence y, item z.
+constexpr int kContinues = 1, kEnds = 2, kBegins = 4;
+
+// One sequence of a call.
+struct Seq {
+    int r0, n, base, L, tiles, sets;   // rows; key tiles; sets of NG query tiles
+    bool rows_ok, bad;
+    __device__ __forceinline__ int items(const Params &p) const { return sets * p.num_kv_heads; }
+};
+
+template <int NG>
+__device__ __forceinline__ Seq seq_of(const Params &p, int s)
+{
+    Seq q;
+    q.r0 = p.query_start[s];
+    const int r1 = p.query_start[s + 1];
+    q.L = p.context_lens[s];
+    q.rows_ok = 0 <= q.r0 && q.r0 <= r1 && r1 <= p.num_tokens;
+    q.n = q.rows_ok ? r1 - q.r0 : 0;
+    q.bad = !q.rows_ok || q.L < q.n || (int64_t)q.L > (int64_t)p.max_blocks_per_seq * kBlock ||
+            q.n > 32 * p.words;
+    q.base = q.L - q.n;
+    q.tiles = (q.L + kKeys - 1) / kKeys;
+    q.sets = q.bad ? 0 : (q.n + NG * p.tile_tokens - 1) / (NG * p.tile_tokens);
+    return q;
+}
+
+// A place in the order of all tiles: tile t of item `it` of sequence s.
+struct Place {
+    int s, it, t;
+};
+
+// A CTA's range.
+struct Plan {
+    Place from, to;
+    int ranges;
+};
+
+// An item's part in a range: tiles [t0, t1).
+struct Item {
+    int s, g, first;                   // first: its first token in the sequence
+    int it, t0, t1;
+};
+
+// Goes through a range's items; every role walks for itself.
+template <int NG>
+struct Walk {
+    Place at;
+    Seq seq;
+    bool loaded = false;
+    __device__ __forceinline__ explicit Walk(const Plan &plan) : at(plan.from) {}
+    __device__ __forceinline__ bool next(const Params &p, const Plan &plan, Item &item)
+    {
+        for (;;) {
+            if (at.s >= p.num_seqs || at.s > plan.to.s) return false;
+            if (!loaded) {
+                seq = seq_of<NG>(p, at.s);
+                loaded = true;
+            }
+            const bool last = at.s == plan.to.s;
+            if (at.it < seq.items(p) && (!last || at.it <= plan.to.it)) {
+                item.s = at.s;
+                item.it = at.it;
+                item.g = at.it / seq.sets;
+                item.first = (at.it - item.g * seq.sets) * NG * p.tile_tokens;
+                item.t0 = at.t;
+                item.t1 = last && at.it == plan.to.it ? plan.to.t : seq.tiles;
+                ++at.it;
+                at.t = 0;
+                if (item.t0 < item.t1) return true;
+                continue;
+            }
+            ++at.s;
+            at.it = at.t = 0;
+            loaded = false;
+        }
+    }
+};
+
+// The place where a range ends that would end `off` units into sequence s's: not inside an
+// item's overhead, and not so near an end of the item that a short piece would be left.
+__device__ __forceinline__ Place cut(const Params &p, int s, const Seq &q, int64_t off, int snap)
+{
+    const int per = q.tiles + kItemCost;
+    Place c = {s, (int)(off / per), 0};
+    const int t = (int)(off - (int64_t)c.it * per) - kItemCost;
+    c.t = t < snap ? 0 : t;
+    if (t > q.tiles - snap) {
+        c.t = 0;
+        ++c.it;
+    }
+    if (c.it >= q.items(p)) {
+        ++c.s;
+        c.it = 0;
+    }
+    return c;
+}
+
+// The ranges, by the whole CTA: units of all sequences are counted (a slice of them to a
+// thread), and the two ends of this CTA's range looked up.  CTA s % gridDim also reports and
+// clears sequences whose lengths do not fit.
+template <int NG, int D, int THREADS>
+__device__ __forceinline__ void make_plan(const Params &p, Plan *plan, int64_t *warp_sum)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int slice = (p.num_seqs + THREADS - 1) / THREADS;
+    const int s0 = min(tid * slice, p.num_seqs), s1 = min(s0 + slice, p.num_seqs);
+    int64_t mine = 0;
+    for (int s = s0; s < s1; ++s) {
+        const Seq q = seq_of<NG>(p, s);
+        mine += (int64_t)q.items(p) * (q.tiles + kItemCost);
+        if (q.bad && s % gridDim.x == blockIdx.x) {
+            atomicOr(p.status, PKV_DEV_BAD_LEN);
+            uint4 *o = static_cast<uint4 *>(p.out) + (int64_t)q.r0 * p.num_q_heads * (D / 8);
+            for (int64_t i = 0; i < (int64_t)q.n * p.num_q_heads * (D / 8); ++i) o[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(kFull, upto, o);
+        if (lane >= o) upto += y;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    int64_t before = upto - mine, all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        all += warp_sum[w];
+    }
+    const int ranges = (int)max((int64_t)1, min((int64_t)gridDim.x, all / kMinRange));
+    const int snap = (int)min((int64_t)kSnap, all / ranges / 4);
+    const int64_t ends[2] = {all * blockIdx.x / ranges, all * (blockIdx.x + 1) / ranges};
+    if (tid == 0) {
+        plan->ranges = ranges;
+        plan->from = plan->to = Place{p.num_seqs, 0, 0};
+    }
+    __syncthreads();
+    if (blockIdx.x < ranges) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (ends[e] < before || ends[e] >= before + mine) continue;
+            int64_t off = ends[e] - before;
+            for (int s = s0; s < s1; ++s) {
+                const Seq q = seq_of<NG>(p, s);
+                const int64_t units = (int64_t)q.items(p) * (q.tiles + kItemCost);
+                if (off < units) {
+                    (e ? plan->to : plan->from) = cut(p, s, q, off, snap);
+                    break;
+                }
+                off -= units;
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// The n lowest of 64 bits (all for n >= 64, none for n <= 0).
+__device__ __forceinline__ uint64_t low_bits(int n)
+{
+    return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
+}
+
+// Keys k0 .. k0 + 63 that a drafted token sees; `words` its mask, two = its first two words.
+__device__ __forceinline__ uint64_t seen_keys(const Params &p, const uint32_t *words, uint64_t two,
+                                              int k0, int base, int L)
+{
+    const int d = k0 - base;                     // drafted token of key k0
+    uint64_t bits;
+    if (d <= 0) {
+        bits = two << -d | low_bits(-d);         // (base - k0 < 64: the tile holds drafted tokens)
+    } else {
+        const int w = d >> 5, sh = d & 31;
+        const uint64_t a = w < p.words ? words[w] : 0u, b = w + 1 < p.words ? words[w + 1] : 0u;
+        const uint64_t c = w + 2 < p.words ? words[w + 2] : 0u;
+        bits = (a | b << 32) >> sh;
+        if (sh) bits |= c << (64 - sh);
+    }
+    return bits & low_bits(L - k0);
+}
+
+// Weights (p0, p1), pp = the same pair packed, as two 16-bit parts, the even key in the low
+// half of each word.  bf16: truncated (its upper 16 bits, exact), then the remainder rounded:
+// to 2^-15.  fp16: rounded, then the remainder rounded: to 2^-22.
+template <bool BF16>
+__device__ __forceinline__ void two_parts(float p0, float p1, uint64_t pp, uint32_t &hi, uint32_t &lo)
+{
+    float2 h;
+    if constexpr (BF16) {
+        const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+        hi = __byte_perm(b0, b1, 0x7632);
+        h = make_float2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u));
+    } else {
+        hi = Elem<false>::pack(p0, p1);
+        h = Elem<false>::unpack(hi);
+    }
+    const float2 d = unpack2f(sub2f(pp, pack2f(h.x, h.y)));
+    lo = Elem<BF16>::pack(d.x, d.y);
+}
+
+// One of a word's two values is an infinity or a NaN: their halves as a mask.
+template <bool BF16>
+__device__ __forceinline__ uint32_t odd_halves(uint32_t w)
+{
+    constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
+    return ((w & kExp) == kExp ? 0xffffu : 0u) | ((w >> 16 & kExp) == kExp ? 0xffff0000u : 0u);
+}
+
+template <int D, int NG>
+struct Layout {
+    static constexpr int kRegions = D / 64;
+    // K and V tiles in flight, a ring each
+    static constexpr int kK = NG == 1 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
+    static constexpr int kV = NG == 1 ? (D == 128 ? 2 : 6) : (D == 128 ? 5 : 10);
+    static constexpr int kQBytes = kRegions * kRows * 128;     // a query tile: [region][row][128 B]
+    static constexpr int kTileBytes = kRegions * kKeys * 128;  // a K or V tile
+    static constexpr int kKRing = NG * kQBytes, kVRing = kKRing + kK * kTileBytes;
+    static constexpr int kMisc = kVRing + kV * kTileBytes;
+    static constexpr int kTotal = kMisc + 1024;
+    static constexpr int kWarps = 4 * NG + 2 + NG, kThreads = 32 * kWarps;
+    static constexpr int kProducer = 4 * NG, kIssuer = 4 * NG + 1, kCleaner = 5 * NG + 1;
+    static constexpr uint32_t kColumns = 256 * NG;             // per query tile: S, S, O
+};
+
+template <int D, bool BF16, int NG>
+__global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                const __grid_constant__ CUtensorMap tmQ, const Params p)
 {
     using E = Elem<BF16>;
     using T = typename E::T;
-    constexpr int kPer = D / 32;
-    const int s = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int r0 = p.query_start[s], r1 = p.query_start[s + 1], L = p.context_lens[s], n = r1 - r0;
-    if (!(0 <= r0 && r0 <= r1 && r1 <= p.num_tokens)) {
-        if (threadIdx.x == 0) atomicOr(p.status, PKV_DEV_BAD_LEN);
+    using LY = Layout<D, NG>;
+    constexpr int NK = LY::kK, NV = LY::kV;
+    // fp16 pools take the reference this much below a row's largest score: weights stay
+    // within 2^15, and those down to 2^-21 of the largest are normal numbers in fp16 (a row
+    // far below a few dominant keys would lose its weights' bits).
+    constexpr float kTop = BF16 ? 0.f : 7.f;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + LY::kMisc);
+    uint64_t *q_full = bars, *q_empty = bars + 1;
+    uint64_t *k_full = bars + 2, *k_empty = k_full + NK;
+    uint64_t *v_full = k_empty + NK, *v_empty = v_full + NV, *clean = v_empty + NV;
+    // S of a query tile out; P out; P V done, each for even and odd tiles
+    uint64_t *s_full = clean + NV, *p_full = s_full + 2 * NG, *o_full = p_full + 2 * NG;
+    uint64_t *done = o_full + 2 * NG;                          // [NG]
+    uint64_t *odd_keys = done + NG;                            // [NV]: keys whose V held odd values
+    int64_t *sums = reinterpret_cast<int64_t *>(odd_keys + NV);         // [warps], see make_plan
+    Plan &plan = *reinterpret_cast<Plan *>(sums + LY::kWarps);
+    // tile's bad blocks: a K tile's slot is free once S is out, before the softmax reads this, so
+    // these have places of their own, more than there are tiles under way
+    uint8_t *bad_blocks = reinterpret_cast<uint8_t *>(&plan + 1);       // [kTilesKnown]
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bad_blocks + kTilesKnown);
+    volatile int *abort_flag = reinterpret_cast<int *>(tslot + 1);
+    static_assert((2 + 2 * NK + 4 * NV + 7 * NG + LY::kWarps) * 8 + sizeof(Plan) + kTilesKnown + 8 <= 1024 &&
+                      NK + 3 <= kTilesKnown && NV + 3 <= kTilesKnown && sizeof(Plan) % 4 == 0,
+                  "barriers and flags");
+
+    if (smem_addr(smem) & 1023u) {       // the swizzle's atoms; no launch has been seen to do this
+        if (threadIdx.x == 0) atomicOr(p.status, PKV_DEV_TIMEOUT);
         return;
     }
-    const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
-    bool dead = L < n || (int64_t)L > (int64_t)p.max_blocks_per_seq * kBlock || n > 32 * p.words;
-    if (dead && threadIdx.x == 0) atomicOr(p.status, PKV_DEV_BAD_LEN);
-    if (!dead && n > 0) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_addr(q_full), 1);
+        mbar_init(smem_addr(q_empty), NG);
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(smem_addr(&k_full[i]), 1);
+            mbar_init(smem_addr(&k_empty[i]), NG);
+        }
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(smem_addr(&v_full[i]), 1);
+            mbar_init(smem_addr(&v_empty[i]), NG);
+            mbar_init(smem_addr(&clean[i]), 1);
+        }
+        for (int i = 0; i < 2 * NG; ++i) {
+            mbar_init(smem_addr(&s_full[i]), 1);
+            mbar_init(smem_addr(&p_full[i]), 4);
+            mbar_init(smem_addr(&o_full[i]), 1);
+        }
+        for (int i = 0; i < NG; ++i) mbar_init(smem_addr(&done[i]), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) tc::tmem_alloc(tslot, LY::kColumns);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tslot;
+    // a launch may overlap the end of the kernel before it, and the joining kernel the end
+    // of this one
+    griddep_launch_dependents();
+    griddep_wait();
+    make_plan<NG, D, LY::kThreads>(p, &plan, sums);
+    const int Hkv = p.num_kv_heads, G = p.group, QT = p.tile_tokens;
+    if (threadIdx.x == 0 && blockIdx.x < plan.ranges) {
+        const bool same = plan.from.s == plan.to.s && plan.from.it == plan.to.it;
+        int4 r = make_int4(0, plan.to.s, plan.to.it, 0);
+        if (plan.from.t > 0) r.x |= kContinues | (same ? 0 : kEnds);
+        if (plan.to.t > 0 && !(same && plan.from.t > 0)) r.x |= kBegins;
+        p.ranges[blockIdx.x] = r;
+        if (blockIdx.x == 0) p.header[0] = plan.ranges;
+    }
+
+    Walk<NG> walk(plan);
+    Item it;
+    if (warp == LY::kProducer) {
+        uint32_t kt = 0, vt = 0, items = 0;      // K tiles, V tiles and items under way or done
+        bool ok = true;
+        while (ok && walk.next(p, plan, it)) {
+            const int32_t *row = p.block_tables + (int64_t)it.s * p.max_blocks_per_seq;
+            const int nb = (walk.seq.L + kBlock - 1) / kBlock;
+            // 32 block ids, 8 tiles, at a time, one batch ahead; behind the end any block will do
+            auto ids_from = [&](int t) { return 4 * t + lane < nb ? row[4 * t + lane] : 0; };
+            int ids = ids_from(it.t0), ids_next = ids_from(it.t0 + 8);
+            // the first row of the four blocks of tile t in the pools; all lanes call it
+            auto rows_of = [&](int t, int (&y)[4]) {
+                bool bad = false;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    int id = __shfl_sync(kFull, ids, ((t - it.t0) & 7) * 4 + b);
+                    if (id < 0 || id >= p.num_blocks) {
+                        bad = true;
+                        id = 0;
+                    }
+                    y[b] = (id * Hkv + it.g) * kBlock;
+                }
+                return bad;
+            };
+            auto copy = [&](const CUtensorMap *map, int at, uint64_t *bar, const int (&y)[4]) {
+                const uint32_t fb = smem_addr(bar), dst = smem_addr(smem + at);
+                mbar_arrive_expect_tx(fb, LY::kTileBytes);
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int rg = 0; rg < LY::kRegions; ++rg)
+                        tma_load_2d(dst + rg * kKeys * 128 + b * kBlock * 128, map, rg * 64, y[b], fb);
+            };
+            // K of a tile goes out before V of the tile before it
+            int y_v[4] = {};
+            for (int t = it.t0; t <= it.t1 && ok; ++t) {
+                int y[4] = {};
+                if (t < it.t1) {
+                    if (((t - it.t0) & 7) == 0 && t > it.t0) {
+                        ids = ids_next;
+                        ids_next = ids_from(t + 8);
+                    }
+                    const bool bad = rows_of(t, y);
+                    if (kt >= NK)
+                        ok = mbar_wait(smem_addr(&k_empty[kt % NK]), (kt / NK - 1) & 1u, abort_flag, p.status);
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (bad) atomicOr(p.status, PKV_DEV_BAD_BLOCK);
+                        bad_blocks[kt % kTilesKnown] = (uint8_t)bad;
+                        copy(&tmK, LY::kKRing + (kt % NK) * LY::kTileBytes, &k_full[kt % NK], y);
+                    }
+                    ++kt;
+                }
+                if (t == it.t0) {
+                    // the item's query rows, once its first K tile is under way
+                    if (items > 0) ok = mbar_wait(smem_addr(q_empty), (items - 1) & 1u, abort_flag, p.status);
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                    ++items;
+                    if (lane == 0) {
+                        const int left = walk.seq.n - it.first;
+                        int boxes = 0;
+                        for (int gr = 0; gr < NG; ++gr)
+                            boxes += (max(0, min(QT, left - gr * QT)) + p.box_tokens - 1) / p.box_tokens;
+                        const uint32_t qb = smem_addr(q_full);
+                        mbar_arrive_expect_tx(qb, (uint32_t)(boxes * LY::kRegions * p.box_tokens * G * 128));
+                        for (int gr = 0; gr < NG; ++gr)
+                            for (int i = 0; i < min(QT, left - gr * QT); i += p.box_tokens)
+                                for (int rg = 0; rg < LY::kRegions; ++rg)
+                                    tc::tma_load_4d(
+                                        smem_addr(smem + gr * LY::kQBytes + rg * kRows * 128 + i * G * 128),
+                                        &tmQ, rg * 64, 0, it.g, walk.seq.r0 + it.first + gr * QT + i, qb);
+                    }
+                } else {
+                    if (vt >= NV)
+                        ok = mbar_wait(smem_addr(&v_empty[vt % NV]), (vt / NV - 1) & 1u, abort_flag, p.status);
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                    if (lane == 0)
+                        copy(&tmV, LY::kVRing + (vt % NV) * LY::kTileBytes, &v_full[vt % NV], y_v);
+                    ++vt;
+                }
+#pragma unroll
+                for (int b = 0; b < 4; ++b) y_v[b] = y[b];
+            }
+        }
+        // after a timed-out wait: let the copies still in flight land first
+        if (*abort_flag && lane == 0) {
+            auto drain = [&](uint64_t *bar, uint32_t parity) {
+                const unsigned long long t0 = globaltimer();
+                while (!mbar_try_wait(smem_addr(bar), parity))
+                    if (globaltimer() - t0 > kTimeoutNs) break;
+            };
+            for (uint32_t i = kt > NK ? kt - NK : 0; i < kt; ++i) drain(&k_full[i % NK], (i / NK) & 1u);
+            for (uint32_t i = vt > NV ? vt - NV : 0; i < vt; ++i) drain(&v_full[i % NV], (i / NV) & 1u);
+            if (items > 0) drain(q_full, (items - 1) & 1u);
+        }
+    } else if (warp >= LY::kIssuer && warp < LY::kIssuer + NG) {
+        if (lane == 0) {
+            const int gr = warp - LY::kIssuer;
+            const uint32_t id_qk = tc::idesc_f16(BF16, kRows, kKeys, 0, 0);
+            const uint32_t id_pv = tc::idesc_f16(BF16, kRows, D, 0, 1);
+            const uint32_t t_s = tmem + 256 * gr, t_o = t_s + 128;
+            const uint64_t qa_d = tc::desc_sw128(smem_addr(smem) + gr * LY::kQBytes, 16, 1024);
+            uint32_t kt = 0;             // key tiles of the CTA
+            uint32_t tp = 0, items = 0;  // those that this query tile took part in
+            bool ok = true;
+            // P V of tile tp - 1, the CTA's tile vt
+            auto issue_pv = [&](uint32_t vt) {
+                const uint32_t slot = vt % NV, par = (vt / NV) & 1u, b = (tp - 1) & 1u;
+                ok = mbar_wait(smem_addr(&clean[slot]), par, abort_flag, p.status) &&
+                     mbar_wait(smem_addr(&v_full[slot]), par, abort_flag, p.status) &&
+                     mbar_wait(smem_addr(&p_full[2 * gr + b]), ((tp - 1) >> 1) & 1u, abort_flag, p.status);
+                if (!ok) return;
+                tc::fence_after_sync();
+                const uint64_t vb_d =
+                    tc::desc_sw128(smem_addr(smem + LY::kVRing + slot * LY::kTileBytes), kKeys * 128, 1024);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        tc::mma_f16_ts(t_o, t_s + 64 * b + part * 32 + kk * 8,
+                                       vb_d + (uint64_t)((kk * 16 * 128) >> 4), id_pv, true);
+                tc::mma_commit(smem_addr(&o_full[2 * gr + b]));
+                tc::mma_commit(smem_addr(&v_empty[slot]));
+            };
+            while (ok && walk.next(p, plan, it)) {
+                ok = mbar_wait(smem_addr(q_full), items & 1u, abort_flag, p.status);
+                if (!ok) break;
+                ++items;
+                if (it.first + gr * QT >= walk.seq.n) {          // no rows: only give the buffers back
+                    mbar_arrive(smem_addr(q_empty));
+                    for (int t = it.t0; t < it.t1 && ok; ++t, ++kt) {
+                        ok = mbar_wait(smem_addr(&k_full[kt % NK]), (kt / NK) & 1u, abort_flag, p.status);
+                        if (ok) mbar_arrive(smem_addr(&k_empty[kt % NK]));
+                        ok = ok && mbar_wait(smem_addr(&v_full[kt % NV]), (kt / NV) & 1u, abort_flag, p.status);
+                        if (ok) mbar_arrive(smem_addr(&v_empty[kt % NV]));
+                    }
+                    continue;
+                }
+                for (int t = it.t0; t < it.t1 && ok; ++t, ++kt) {
+                    const uint32_t slot = kt % NK;
+                    ok = mbar_wait(smem_addr(&k_full[slot]), (kt / NK) & 1u, abort_flag, p.status);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const uint64_t kb_d = tc::desc_sw128(smem_addr(smem + LY::kKRing + slot * LY::kTileBytes), 16, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk & 3) * 32;      // 16 values inside the row
+                        tc::mma_f16(t_s + 64 * (tp & 1u), qa_d + (uint64_t)(((kk >> 2) * kRows * 128 + off) >> 4),
+                                    kb_d + (uint64_t)(((kk >> 2) * kKeys * 128 + off) >> 4), id_qk, kk > 0);
+                    }
+                    tc::mma_commit(smem_addr(&s_full[2 * gr + (tp & 1u)]));
+                    tc::mma_commit(smem_addr(&k_empty[slot]));
+                    if (t == it.t1 - 1) tc::mma_commit(smem_addr(q_empty));
+                    if (t > it.t0) issue_pv(kt - 1);
+                    ++tp;
+                }
+                if (ok) issue_pv(kt - 1);
+            }
+            // every MMA this thread issued has completed before the columns are freed
+            tc::mma_commit(smem_addr(&done[gr]));
+            const unsigned long long t0 = globaltimer();
+            while (!mbar_try_wait(smem_addr(&done[gr]), 0)) {
+                if (globaltimer() - t0 > kTimeoutNs) {
+                    atomicOr(p.status, PKV_DEV_TIMEOUT);
+                    break;
+                }
+            }
+        }
+    } else if (warp == LY::kCleaner) {
+        uint32_t vt = 0;
+        bool ok = true;
+        while (ok && walk.next(p, plan, it)) {
+            const int base = walk.seq.base, L = walk.seq.L;
+            for (int t = it.t0; t < it.t1; ++t, ++vt) {
+                const uint32_t slot = vt % NV;
+                ok = __all_sync(kFull, mbar_wait(smem_addr(&v_full[slot]), (vt / NV) & 1u, abort_flag, p.status));
+                if (!ok) break;
+                const int k0 = t * kKeys;
+                if (k0 + kKeys > base) {
+                    uint8_t *v = smem + LY::kVRing + slot * LY::kTileBytes;
+                    constexpr int kChunks = LY::kRegions * 8;
+                    const int r0 = max(base - k0, 0), r1 = min(L - k0, kKeys);
+                    uint32_t odd[2] = {0u, 0u};
+                    for (int e = r0 * kChunks + lane; e < kKeys * kChunks; e += 32) {
+                        const int r = e / kChunks, c = e % kChunks;
+                        uint4 *at = reinterpret_cast<uint4 *>(v + (c >> 3) * kKeys * 128 + r * 128 + (c & 7) * 16);
+                        if (r >= r1) {
+                            *at = make_uint4(0u, 0u, 0u, 0u);
+                            continue;
+                        }
+                        uint4 w = *at;
+                        const uint32_t o[4] = {odd_halves<BF16>(w.x), odd_halves<BF16>(w.y),
+                                               odd_halves<BF16>(w.z), odd_halves<BF16>(w.w)};
+                        if (o[0] | o[1] | o[2] | o[3]) {
+                            w.x &= ~o[0];
+                            w.y &= ~o[1];
+                            w.z &= ~o[2];
+                            w.w &= ~o[3];
+                            *at = w;
+                            odd[r >> 5] |= 1u << (r & 31);
+                        }
+                    }
+                    odd[0] = __reduce_or_sync(kFull, odd[0]);
+                    odd[1] = __reduce_or_sync(kFull, odd[1]);
+                    if (lane == 0) odd_keys[slot] = odd[0] | (uint64_t)odd[1] << 32;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(smem_addr(&clean[slot]));
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- softmax
+        const int gr = warp >> 2, r = threadIdx.x - kRows * gr;
+        const uint32_t t_s = tmem + 256 * gr + ((uint32_t)(32 * (warp & 3)) << 16), t_o = t_s + 128;
+        const int jj = r / G, h = r - jj * G;
+        uint32_t kt = 0, tp = 0;         // key tiles of the CTA; those with rows of this query tile
+        bool alive = true;
+        while (alive && walk.next(p, plan, it)) {
+            const int n = walk.seq.n, base = walk.seq.base, L = walk.seq.L;
+            const int token = it.first + gr * QT + jj;
+            if (it.first + gr * QT >= n) {               // no rows in this query tile
+                kt += (uint32_t)(it.t1 - it.t0);
+                continue;
+            }
+            const bool valid = r < QT * G && token < n;
+            const bool busy = __any_sync(kFull, valid);  // some row of the warp counts
+            const uint32_t *words = p.mask + (int64_t)(walk.seq.r0 + (valid ? token : it.first)) * p.words;
+            const uint64_t two = words[0] | (uint64_t)(p.words > 1 ? words[1] : 0u) << 32;
+            float m_ref = -INFINITY, l = 0.f;
+            int bad = 0;
+            if (busy) {
+                uint32_t z[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) z[c] = 0u;
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 32) tc::tmem_st32(t_o + c0, z);
+            }
+            for (int t = it.t0; t < it.t1; ++t, ++tp, ++kt) {
+                const uint32_t b = tp & 1u, vslot = kt % NV;
+                const bool got = mbar_wait(smem_addr(&s_full[2 * gr + b]), (tp >> 1) & 1u, abort_flag, p.status);
+                if (!__all_sync(kFull, got)) { alive = false; break; }
+                if (!busy) {
+                    if (lane == 0) mbar_arrive(smem_addr(&p_full[2 * gr + b]));
+                    continue;
+                }
+                tc::fence_after_sync();
+                bad |= bad_blocks[kt % kTilesKnown];
+                float x[kKeys];
+                {
+                    uint32_t v[2][32];
+                    tc::tmem_ld32(t_s + 64 * b, v[0]);
+                    tc::tmem_ld32(t_s + 64 * b + 32, v[1]);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        x[c] = __uint_as_float(v[0][c]);
+                        x[32 + c] = __uint_as_float(v[1][c]);
+                    }
+                }
+                const int k0 = t * kKeys;
+                const bool edge = k0 + kKeys > base;     // drafted tokens or the end: masks
+                uint64_t see = ~0ull;
+                if (edge) {
+                    if (valid) see = seen_keys(p, words, two, k0, base, L);
+                    // (the scale is never zero, see the host)
+                    const float hide = p.scale_log2 < 0.f ? INFINITY : -INFINITY;
+                    const uint32_t see0 = (uint32_t)see, see1 = (uint32_t)(see >> 32);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        if (!((see0 >> c) & 1u)) x[c] = hide;
+                        if (!((see1 >> c) & 1u)) x[32 + c] = hide;
+                    }
+                }
+                // the tile's largest scaled score
+                float mx;
+                if (p.scale_log2 >= 0.f) {
+                    mx = fmaxf(x[0], x[1]);
+#pragma unroll
+                    for (int c = 2; c < kKeys; c += 2) mx = fmaxf(mx, fmaxf(x[c], x[c + 1]));
+                } else {
+                    mx = fminf(x[0], x[1]);
+#pragma unroll
+                    for (int c = 2; c < kKeys; c += 2) mx = fminf(mx, fminf(x[c], x[c + 1]));
+                }
+                mx *= p.scale_log2;
+                float f = 1.f;
+                bool resc = false;
+                if (valid && mx > m_ref + (kLazy + kTop)) {      // also the first tile: m_ref = -inf
+                    // (from 2^24 on, where the spacing nears kTop, the largest score itself)
+                    const float now = kTop == 0.f || fabsf(mx) > 0x1p24f ? mx : mx - kTop;
+                    if (m_ref != -INFINITY) {
+                        f = fast_exp2(m_ref - now);
+                        resc = true;
+                    }
+                    m_ref = now;
+                }
+                // (a row that has seen no key yet has m_ref = -inf; any finite reference gives
+                // its hidden scores weight 2^-inf = 0)
+                const float m_sub = m_ref == -INFINITY ? 0.f : m_ref;
+                const bool big = fabsf(m_sub) > 0x1p24f;
+                const uint64_t sc2 = pack2f(p.scale_log2, p.scale_log2), nm2 = pack2f(-m_sub, -m_sub);
+                uint64_t lsum2 = pack2f(0.f, 0.f);
+                uint64_t zero = 0ull;                    // (rare path) weights that are zero
+                // 32 keys at a time: weights, their parts over the tile's S columns (already
+                // read), high parts in the first 32, low parts in the next
+                auto weights = [&](auto wide) {
+#pragma unroll
+                    for (int c0 = 0; c0 < kKeys; c0 += 32) {
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int c = c0; c < c0 + 32; c += 2) {
+                            float2 e = unpack2f(fma2f(pack2f(x[c], x[c + 1]), sc2, nm2));
+                            if (decltype(wide)::value && big)
+                                e = make_float2(__fsub_rn(__fmul_rn(x[c], p.scale_log2), m_sub),
+                                                __fsub_rn(__fmul_rn(x[c + 1], p.scale_log2), m_sub));
+                            const float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
+                            const uint64_t pp = pack2f(p0, p1);
+                            lsum2 = add2f(lsum2, pp);
+                            two_parts<BF16>(p0, p1, pp, hi[(c - c0) / 2], lo[(c - c0) / 2]);
+                            if (decltype(wide)::value)
+                                zero |= (uint64_t)(p0 == 0.f) << c | (uint64_t)(p1 == 0.f) << (c + 1);
+                        }
+                        tc::tmem_st16(t_s + 64 * b + c0 / 2, hi);
+                        tc::tmem_st16(t_s + 64 * b + 32 + c0 / 2, lo);
+                    }
+                };
+                uint64_t odd = 0ull;                     // keys whose V held odd values
+                if (edge) {
+                    const bool swept = mbar_wait(smem_addr(&clean[vslot]), (kt / NV) & 1u, abort_flag, p.status);
+                    if (!__all_sync(kFull, swept)) { alive = false; break; }
+                    odd = odd_keys[vslot];
+                }
+                // the reference is a rounded product: against it, the unrounded products of the
+                // fused form come out up to half its spacing too large or too small, the same for
+                // the whole row, which cancels; from 2^25 on that is 2 or more and grows past the
+                // range of the weights, so from 2^24 on the products are rounded alike, by scalar
+                // operations that stay apart (the largest weight is then exactly 1)
+                if (__any_sync(kFull, big) || odd) weights(std::true_type{});
+                else weights(std::false_type{});
+                const float2 ls = unpack2f(lsum2);
+                l = l * f + (ls.x + ls.y);
+                // O changes before P V of this tile, once P V of the one before has ended; the
+                // wait for that consumes its o_full phase either here or after P is out
+                const bool touch = __any_sync(kFull, resc) || odd;
+                if (touch && t > it.t0) {
+                    const bool ended = mbar_wait(smem_addr(&o_full[2 * gr + (b ^ 1u)]), ((tp - 1) >> 1) & 1u, abort_flag, p.status);
+                    if (!__all_sync(kFull, ended)) { alive = false; break; }
+                    tc::fence_after_sync();
+                }
+                if (touch) {
+                    tc::tmem_wait_st();                  // (O's zeros, in an item's first tile)
+                    const int32_t *row = p.block_tables + (int64_t)it.s * p.max_blocks_per_seq;
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t v[32];
+                        tc::tmem_ld32(t_o + c0, v);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * f);
+                        for (uint64_t left = valid ? odd & see : 0ull; left; left &= left - 1) {
+                            const int c = __ffsll((long long)left) - 1, pos = k0 + c;
+                            int id = row[pos / kBlock];
+                            if (id < 0 || id >= p.num_blocks) id = 0;        // (the result is zero anyway)
+                            const T *vp = static_cast<const T *>(p.v_pool) +
+                                          (((int64_t)id * Hkv + it.g) * kBlock + pos % kBlock) * D + c0;
+                            const bool none = zero >> c & 1u;                // 0 * infinity
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float y = (float)vp[e];
+                                if (!(fabsf(y) < INFINITY))
+                                    v[e] = __float_as_uint(__uint_as_float(v[e]) + (none ? NAN : y));
+                            }
+                        }
+                        tc::tmem_st32(t_o + c0, v);
+                    }
+                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&p_full[2 * gr + b]));
+                if (!touch && t > it.t0) {
+                    const bool ended = mbar_wait(smem_addr(&o_full[2 * gr + (b ^ 1u)]), ((tp - 1) >> 1) & 1u, abort_flag, p.status);
+                    if (!__all_sync(kFull, ended)) { alive = false; break; }
+                }
+            }
+            if (!alive) break;
+            // ---- the part's result, once its last P V is done (which writes the lanes of warps
+            // without rows too: they wait before another item's zeros)
+            const bool ended = mbar_wait(smem_addr(&o_full[2 * gr + ((tp - 1) & 1u)]), ((tp - 1) >> 1) & 1u, abort_flag, p.status);
+            if (!__all_sync(kFull, ended)) break;
+            tc::fence_after_sync();
+            if (!busy) continue;
+            if (it.t0 > 0 || it.t1 < walk.seq.tiles) {
+                const int64_t piece = 2 * blockIdx.x + (it.t0 == 0);
+                const int rr = gr * kRows + r;
+                if (valid) p.part_ml[piece * p.piece_rows + rr] = make_float2(m_ref, bad ? -1.f : l);
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t v[32];
+                    tc::tmem_ld32(t_o + c0, v);
+                    tc::tmem_wait_ld();
+                    if (valid) {
+                        float4 *dst = p.part_o + (piece * (D / 4) + c0 / 4) * p.piece_rows + rr;
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            dst[(int64_t)(c / 4) * p.piece_rows] =
+                                make_float4(__uint_as_float(v[c]), __uint_as_float(v[c + 1]),
+                                            __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+                    }
+                }
+            } else {
+                const bool none = bad || l == 0.f;       // a bad block, or nothing seen
+                const float inv = none ? 0.f : 1.f / l;
+                T *out = static_cast<T *>(p.out) +
+                         ((int64_t)(walk.seq.r0 + token) * p.num_q_heads + (int64_t)it.g * G + h) * D;
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t v[32];
+                    tc::tmem_ld32(t_o + c0, v);
+                    tc::tmem_wait_ld();
+                    if (valid) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 8) {
+                            auto two_of = [&](int k) {
+                                return none ? 0u : E::pack(__uint_as_float(v[c + k]) * inv, __uint_as_float(v[c + k + 1]) * inv);
+                            };
+                            *reinterpret_cast<uint4 *>(out + c0 + c) =
+                                make_uint4(two_of(0), two_of(2), two_of(4), two_of(6));
+                        }
+                    }
+                }
+            }
+            tc::fence_before_sync();
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 0) tc::tmem_dealloc(tmem, LY::kColumns);
+}
+
+// ------------------------------------------------------------------ joining the pieces
+// A row of CTAs per cut item (the x-th range that begins one it does not end); a warp takes
+// 32 rows and 8 columns.
+constexpr int kJoinThreads = 256;
+
+template <int D, bool BF16, int NG>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const Params p)
+{
+    using E = Elem<BF16>;
+    using T = typename E::T;
+    __shared__ int kinds[kMaxRanges], found[2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int ranges = min(p.header[0], kMaxRanges);
+    for (int i = tid; i < ranges; i += kJoinThreads) kinds[i] = p.ranges[i].x;
+    __syncthreads();
+    if (warp == 0) {
+        int begin = -1, end = -1, left = blockIdx.x;
+        for (int i0 = 0; i0 < ranges && end < 0; i0 += 32) {
+            const int kind = i0 + lane < ranges ? kinds[i0 + lane] : 0;
+            unsigned ends = __ballot_sync(kFull, kind & kEnds);
+            if (begin < 0) {
+                unsigned begins = __ballot_sync(kFull, kind & kBegins);
+                if (__popc(begins) <= left) {
+                    left -= __popc(begins);
+                    continue;
+                }
+                for (; left > 0; --left) begins &= begins - 1;
+                begin = i0 + __ffs(begins) - 1;
+                ends &= ~((2u << (begin - i0)) - 1u);
+            }
+            if (ends) end = i0 + __ffs(ends) - 1;
+        }
+        if (lane == 0) {
+            found[0] = begin;
+            found[1] = end;
+        }
+    }
+    __syncthreads();
+    const int begin = found[0], end = found[1];
+    if (begin < 0 || end < 0) return;
+    const int4 what = p.ranges[begin];
+    const Seq q = seq_of<NG>(p, what.y);
+    const int g = what.z / q.sets, first = (what.z - g * q.sets) * NG * p.tile_tokens;
+    const int G = p.group, pieces = end - begin + 1;
+    auto piece = [&](int k) -> int64_t { return k == 0 ? 2 * begin + 1 : 2 * (begin + k); };
+    // rows that count: those of full query tiles before the last one's
+    const int tokens = min(NG * p.tile_tokens, q.n - first);
+    const int tiles = (tokens + p.tile_tokens - 1) / p.tile_tokens;
+    const int rows = (tiles - 1) * kRows + (tokens - (tiles - 1) * p.tile_tokens) * G;
+    const int tasks = (rows + 31) / 32 * (D / 8);
+    for (int task = blockIdx.y * (kJoinThreads / 32) + warp; task < tasks; task += gridDim.y * (kJoinThreads / 32)) {
+        const int rr = task / (D / 8) * 32 + lane, c8 = task % (D / 8);
+        const int gr = rr / kRows, jj = (rr - gr * kRows) / G, h = rr - gr * kRows - jj * G;
+        const int token = first + gr * p.tile_tokens + jj;
+        if (jj >= p.tile_tokens || token >= q.n) continue;
+        float m = -INFINITY;
         bool bad = false;
-        for (int b = threadIdx.x; b < (L + kBlock - 1) / kBlock; b += blockDim.x)
-            bad |= row[b] < 0 || row[b] >= p.num_blocks;
-        if (__syncthreads_or(bad)) {
-            dead = true;
-            if (threadIdx.x == 0) atomicOr(p.status, PKV_DEV_BAD_BLOCK);
+#pragma unroll 4
+        for (int k = 0; k < pieces; ++k) {
+            const float2 ml = p.part_ml[piece(k) * p.piece_rows + rr];
+            m = ml.y == 0.f ? m : fmaxf(m, ml.x);        // (a sum of zero: it saw nothing there)
+            bad |= ml.y < 0.f;
         }
+        float l = 0.f, o[8] = {};
+#pragma unroll 4
+        for (int k = 0; k < pieces; ++k) {
+            const int64_t at = piece(k);
+            const float2 ml = p.part_ml[at * p.piece_rows + rr];
+            const float w = ml.y == 0.f ? 0.f : fast_exp2(ml.x - m);
+            const float4 *src = p.part_o + (at * (D / 4) + 2 * c8) * p.piece_rows + rr;
+            const float4 a = src[0], b = src[p.piece_rows];
+            l += w * ml.y;
+            const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] += w * v[e];
+        }
+        const bool none = bad || l == 0.f;
+        const float inv = none ? 0.f : 1.f / l;
+        auto two_of = [&](int k) { return none ? 0u : E::pack(o[k] * inv, o[k + 1] * inv); };
+        T *out = static_cast<T *>(p.out) +
+                 ((int64_t)(q.r0 + token) * p.num_q_heads + (int64_t)g * G + h) * D + 8 * c8;
+        *reinterpret_cast<uint4 *>(out) = make_uint4(two_of(0), two_of(2), two_of(4), two_of(6));
     }
-    const int G = p.num_q_heads / p.num_kv_heads;
-    for (int e = blockIdx.y * 8 + warp; e < n * p.num_q_heads; e += gridDim.y * 8) {
-        const int i = e / p.num_q_heads, h = e - i * p.num_q_heads, g = h / G;
-        const int64_t at = ((int64_t)(r0 + i) * p.num_q_heads + h) * D + lane * kPer;
-        float q[kPer], o[kPer], m = -INFINITY, l = 0.f;
-#pragma unroll
-        for (int d = 0; d < kPer; ++d) {
-            q[d] = (float)static_cast<const T *>(p.q)[at + d];
-            o[d] = 0.f;
-        }
-        for (int j = 0; j < (dead ? 0 : L); ++j) {
-            const int d0 = j - (L - n);
-            if (d0 >= 0 && !((p.mask[(int64_t)(r0 + i) * p.words + (d0 >> 5)] >> (d0 & 31)) & 1u)) continue;
-            const int64_t kv =
-                (((int64_t)row[j / kBlock] * p.num_kv_heads + g) * kBlock + j % kBlock) * D + lane * kPer;
-            float x = 0.f;
-#pragma unroll
-            for (int d = 0; d < kPer; ++d) x = fmaf(q[d], (float)static_cast<const T *>(p.k_pool)[kv + d], x);
-#pragma unroll
-            for (int f = 16; f > 0; f >>= 1) x += __shfl_xor_sync(kFull, x, f);
-            x *= p.scale_log2;
-            const float now = x != x ? x : fmaxf(m, x), f = m == now ? 1.f : exp2f(m - now);
-            const float w = x == -INFINITY ? 0.f : exp2f(x - now);
-            l = l * f + w;
-#pragma unroll
-            for (int d = 0; d < kPer; ++d)
-                o[d] = fmaf(w, (float)static_cast<const T *>(p.v_pool)[kv + d], o[d] * f);
-            m = now;
-        }
-#pragma unroll
-        for (int d = 0; d < kPer; ++d)
-            static_cast<T *>(p.out)[at + d] = E::from_float(l == 0.f ? 0.f : o[d] / l);
+}
+
+// --------------------------------------------------------------------- host side
+using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
+
+static EncodeFn encode_fn()
+{
+    static EncodeFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeFn>(ptr);
+    });
+    return fn;
+}
+
+static bool make_map(CUtensorMap *map, const void *base, bool bf16, int rank, const cuuint64_t *dims,
+                     const cuuint64_t *strides, const cuuint32_t *box)
+{
+    const EncodeFn enc = encode_fn();
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    return enc && enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                      (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, step,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tokens of a box of query rows: whole groups of 8 rows (the swizzle's atom), about 32 rows.
+static int box_tokens(int G)
+{
+    const int unit = G % 8 == 0 ? 1 : G % 4 == 0 ? 2 : G % 2 == 0 ? 4 : 8;
+    return unit * std::max(1, 32 / (unit * G));
+}
+
+static int tile_tokens(int G) { return kRows / (box_tokens(G) * G) * box_tokens(G); }
+
+static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Rows of a piece's place: a call whose rows fit less than a query tile needs less.
+static int64_t piece_rows(int64_t T, int G) { return std::min<int64_t>(kRows, (T * G + 31) / 32 * 32); }
+
+struct Workspace {
+    size_t ranges, ml, o, total;
+};
+static Workspace workspace_of(int64_t T, int G, int D)
+{
+    const size_t rows = 2 * kMaxRanges * (size_t)piece_rows(T, G);
+    Workspace w;
+    w.ranges = 256;
+    w.ml = w.ranges + align256(kMaxRanges * sizeof(int4));
+    w.o = w.ml + align256(rows * sizeof(float2));
+    w.total = w.o + rows * D * sizeof(float);
+    return w;
+}
+
+using KernelFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, Params);
+using JoinFn = void (*)(Params);
+
+struct Pick {
+    KernelFn fn;
+    JoinFn join;
+    int smem, threads;
+};
+
+template <int D, bool BF16, int NG>
+static Pick pick_of()
+{
+    return {&tree_kernel<D, BF16, NG>, &tree_join_kernel<D, BF16, NG>, Layout<D, NG>::kTotal,
+            Layout<D, NG>::kThreads};
+}
+
+template <int NG>
+static Pick pick(int D, bool bf16)
+{
+    if (D == 128) return bf16 ? pick_of<128, true, NG>() : pick_of<128, false, NG>();
+    return bf16 ? pick_of<64, true, NG>() : pick_of<64, false, NG>();
+}
+
+// CTAs of a kernel that fit the current device at once, cached per device and kernel.
+static int resident(const Pick &k, int slot)
+{
+    constexpr int kMaxDev = 64, kSlots = 8;
+    static std::mutex mu;
+    static int ctas[kMaxDev][kSlots];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return -1;
+    std::lock_guard<std::mutex> lock(mu);
+    int &n = ctas[dev][slot];
+    if (n == 0) {
+        const void *fn = reinterpret_cast<const void *>(k.fn);
+        int sms = 0, per = 0;
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, fn, k.threads, (size_t)k.smem) != cudaSuccess ||
+            per < 1)
+            return -1;
+        n = sms * per;
     }
+    return n;
 }
 
 }  // namespace tree
@@ -96,7 +1024,7 @@ extern "C" size_t paged_tree_workspace_bytes(int32_t num_tokens, int32_t num_q_h
     if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads ||
         num_q_heads / num_kv_heads > 16 || (head_dim != 64 && head_dim != 128))
         return 0;
-    return 256;
+    return pkv::tree::workspace_of(num_tokens, num_q_heads / num_kv_heads, head_dim).total;
 }
 
 extern "C" int paged_tree_attention(const pkv_pool *pool, void *out, const void *q,
@@ -115,9 +1043,8 @@ extern "C" int paged_tree_attention(const pkv_pool *pool, void *out, const void 
         mask_words < 1 || mask_words > kMaxWords || num_q_heads % g.num_kv_heads)
         return PKV_ERR_INVALID_ARG;
     if (!(scale == scale) || scale == INFINITY || scale == -INFINITY) return PKV_ERR_INVALID_ARG;
-    if (g.block_size != pkv::kBlock || num_q_heads / g.num_kv_heads > 16 ||
-        (g.head_dim != 64 && g.head_dim != 128))
-        return PKV_ERR_UNSUPPORTED;
+    const int G = num_q_heads / g.num_kv_heads, D = g.head_dim;
+    if (g.block_size != pkv::kBlock || G > 16 || (D != 64 && D != 128)) return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
     if (!out || !q || !k_pool || !v_pool || !block_tables || !query_start || !context_lens ||
         !tree_mask || !workspace || !d_status)
@@ -127,15 +1054,17 @@ extern "C" int paged_tree_attention(const pkv_pool *pool, void *out, const void 
         ((uintptr_t)block_tables & 3u) || ((uintptr_t)query_start & 3u) ||
         ((uintptr_t)context_lens & 3u) || ((uintptr_t)tree_mask & 3u) || ((uintptr_t)d_status & 3u))
         return PKV_ERR_INVALID_ARG;
-    if (workspace_bytes <
-        paged_tree_workspace_bytes(num_tokens, num_q_heads, g.num_kv_heads, g.head_dim))
-        return PKV_ERR_INVALID_ARG;
+    const Workspace ws = workspace_of(num_tokens, G, D);
+    if (workspace_bytes < ws.total) return PKV_ERR_INVALID_ARG;
     if ((int64_t)g.num_blocks * g.num_kv_heads * g.block_size > (int64_t)1 << 31)
         return PKV_ERR_UNSUPPORTED;
+    const bool bf16 = g.dtype == PKV_BF16;
+    // two query tiles to a CTA where the rows of an average sequence need more than one
+    const bool two = (int64_t)num_tokens * G > (int64_t)kRows * num_seqs;
+    const Pick k = two ? pick<2>(D, bf16) : pick<1>(D, bf16);
+
     Params prm;
     prm.out = out;
-    prm.q = q;
-    prm.k_pool = k_pool;
     prm.v_pool = v_pool;
     prm.block_tables = block_tables;
     prm.query_start = query_start;
@@ -146,13 +1075,52 @@ extern "C" int paged_tree_attention(const pkv_pool *pool, void *out, const void 
     prm.num_tokens = num_tokens;
     prm.num_q_heads = num_q_heads;
     prm.num_kv_heads = g.num_kv_heads;
+    prm.group = G;
     prm.max_blocks_per_seq = max_blocks_per_seq;
     prm.num_blocks = g.num_blocks;
-    prm.scale_log2 = scale * 1.4426950408889634f;
+    prm.tile_tokens = tile_tokens(G);
+    prm.box_tokens = box_tokens(G);
+    prm.piece_rows = two ? 2 * kRows : (int32_t)piece_rows(num_tokens, G);
+    // scores are hidden by an infinity that the scale must carry into the exponent; at scale 0
+    // the smallest normal number weighs all keys alike
+    prm.scale_log2 = scale == 0.f ? 0x1p-126f : scale * 1.4426950408889634f;
+    char *w = static_cast<char *>(workspace);
+    prm.header = reinterpret_cast<int32_t *>(w);
+    prm.ranges = reinterpret_cast<int4 *>(w + ws.ranges);
+    prm.part_ml = reinterpret_cast<float2 *>(w + ws.ml);
+    prm.part_o = reinterpret_cast<float4 *>(w + ws.o);
     prm.status = d_status;
-    const bool bf16 = g.dtype == PKV_BF16;
-    auto fn = g.head_dim == 128 ? (bf16 ? &tree_rows_kernel<128, true> : &tree_rows_kernel<128, false>)
-                                : (bf16 ? &tree_rows_kernel<64, true> : &tree_rows_kernel<64, false>);
-    fn<<<dim3((unsigned)num_seqs, 32), 256, 0, (cudaStream_t)stream>>>(prm);
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+
+    CUtensorMap tk, tv, tq;
+    const cuuint64_t rows[2] = {(cuuint64_t)D, (cuuint64_t)g.num_blocks * g.num_kv_heads * g.block_size};
+    const cuuint64_t row_bytes[1] = {(cuuint64_t)D * 2};
+    const cuuint32_t block[2] = {64u, (cuuint32_t)pkv::kBlock};
+    // query rows as (D, G, Hkv, T): a box brings G rows of each of its tokens
+    const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)G, (cuuint64_t)g.num_kv_heads, (cuuint64_t)num_tokens};
+    const cuuint64_t qs[3] = {(cuuint64_t)D * 2, (cuuint64_t)G * D * 2, (cuuint64_t)num_q_heads * D * 2};
+    const cuuint32_t qb[4] = {64u, (cuuint32_t)G, 1u, (cuuint32_t)prm.box_tokens};
+    if (!make_map(&tk, k_pool, bf16, 2, rows, row_bytes, block) ||
+        !make_map(&tv, v_pool, bf16, 2, rows, row_bytes, block) || !make_map(&tq, q, bf16, 4, qd, qs, qb))
+        return PKV_ERR_CUDA;
+    const int fit = resident(k, (D == 128) * 4 + bf16 * 2 + two);
+    if (fit < 1) return PKV_ERR_CUDA;
+
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min(fit, two ? kMaxRanges / 2 : kMaxRanges));
+    cfg.blockDim = dim3((unsigned)k.threads);
+    cfg.dynamicSmemBytes = (size_t)k.smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, k.fn, tk, tv, tq, prm) != cudaSuccess) return PKV_ERR_CUDA;
+    // items that can be cut: no more than there are, nor than ranges
+    const int64_t sets = (int64_t)num_tokens / ((two ? 2 : 1) * prm.tile_tokens) + num_seqs;
+    const int64_t cuts = std::min<int64_t>(cfg.gridDim.x, sets * g.num_kv_heads);
+    cfg.gridDim = dim3((unsigned)cuts, (unsigned)std::min<int64_t>(16, std::max<int64_t>(1, 1216 / cuts)));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, k.join, prm) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
