@@ -293,7 +293,8 @@ struct Layout {
     static constexpr int kTileBytes = kRegions * kKeys * 128;  // a K or V tile
     static constexpr int kKRing = NG * kQBytes, kVRing = kKRing + kK * kTileBytes;
     static constexpr int kMisc = kVRing + kV * kTileBytes;
-    static constexpr int kTotal = kMisc + 1024;
+    static constexpr int kMiscBytes = NG == 1 ? 512 : 1024;
+    static constexpr int kTotal = kMisc + kMiscBytes;
     static constexpr int kWarps = 4 * NG + 2 + NG, kThreads = 32 * kWarps;
     static constexpr int kProducer = 4 * NG, kIssuer = 4 * NG + 1, kCleaner = 5 * NG + 1;
     static constexpr uint32_t kColumns = 256 * NG;             // per query tile: S, S, O
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
     uint8_t *bad_blocks = reinterpret_cast<uint8_t *>(&plan + 1);       // [kTilesKnown]
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bad_blocks + kTilesKnown);
     volatile int *abort_flag = reinterpret_cast<int *>(tslot + 1);
-    static_assert((2 + 2 * NK + 4 * NV + 7 * NG + LY::kWarps) * 8 + sizeof(Plan) + kTilesKnown + 8 <= 1024 &&
+    static_assert((2 + 2 * NK + 4 * NV + 7 * NG + LY::kWarps) * 8 + sizeof(Plan) + kTilesKnown + 8 <= LY::kMiscBytes &&
                       NK + 3 <= kTilesKnown && NV + 3 <= kTilesKnown && sizeof(Plan) % 4 == 0,
                   "barriers and flags");
 
@@ -975,14 +976,14 @@ using JoinFn = void (*)(Params);
 struct Pick {
     KernelFn fn;
     JoinFn join;
-    int smem, threads;
+    int smem, threads, ctas;           // ctas: to an SM
 };
 
 template <int D, bool BF16, int NG>
 static Pick pick_of()
 {
     return {&tree_kernel<D, BF16, NG>, &tree_join_kernel<D, BF16, NG>, Layout<D, NG>::kTotal,
-            Layout<D, NG>::kThreads};
+            Layout<D, NG>::kThreads, NG == 1 ? 2 : 1};
 }
 
 template <int NG>
@@ -992,7 +993,9 @@ static Pick pick(int D, bool bf16)
     return bf16 ? pick_of<64, true, NG>() : pick_of<64, false, NG>();
 }
 
-// CTAs of a kernel that fit the current device at once, cached per device and kernel.
+// CTAs of a kernel that fit the current device at once, cached per device and kernel.  (The
+// runtime's own count is one to an SM for every kernel that allocates tensor memory; two of
+// NG = 1 take 512 columns, all there are.)
 static int resident(const Pick &k, int slot)
 {
     constexpr int kMaxDev = 64, kSlots = 8;
@@ -1004,13 +1007,15 @@ static int resident(const Pick &k, int slot)
     int &n = ctas[dev][slot];
     if (n == 0) {
         const void *fn = reinterpret_cast<const void *>(k.fn);
-        int sms = 0, per = 0;
+        int sms = 0, shared = 0, reserved = 0;
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&shared, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev) != cudaSuccess ||
             cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, fn, k.threads, (size_t)k.smem) != cudaSuccess ||
-            per < 1)
+            cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared) != cudaSuccess)
             return -1;
-        n = sms * per;
+        n = sms * (k.ctas == 2 && 2 * (k.smem + reserved) <= shared ? 2 : 1);
     }
     return n;
 }
