@@ -48,6 +48,7 @@ constexpr int kRows = 128;             // M: rows of a query tile
 constexpr int kKeys = 64;              // keys of a tile
 constexpr int kMaxWords = 32;
 constexpr int kTilesKnown = 16;
+constexpr int kTasks = 8;               // items under way, at most
 constexpr float kLazy = 8.f;
 constexpr int kItemCost = 2;           // an item's beginning and end, in tiles
 constexpr int kMinRange = 4;           // a range has at least so many
@@ -85,12 +86,11 @@ struct Seq {
 };
 
 template <int NG>
-__device__ __forceinline__ Seq seq_of(const Params &p, int s)
+__device__ __forceinline__ Seq seq_of(const Params &p, int r0, int r1, int L)
 {
     Seq q;
-    q.r0 = p.query_start[s];
-    const int r1 = p.query_start[s + 1];
-    q.L = p.context_lens[s];
+    q.r0 = r0;
+    q.L = L;
     q.rows_ok = 0 <= q.r0 && q.r0 <= r1 && r1 <= p.num_tokens;
     q.n = q.rows_ok ? r1 - q.r0 : 0;
     q.bad = !q.rows_ok || q.L < q.n || (int64_t)q.L > (int64_t)p.max_blocks_per_seq * kBlock ||
@@ -99,6 +99,12 @@ __device__ __forceinline__ Seq seq_of(const Params &p, int s)
     q.tiles = (q.L + kKeys - 1) / kKeys;
     q.sets = q.bad ? 0 : (q.n + NG * p.tile_tokens - 1) / (NG * p.tile_tokens);
     return q;
+}
+
+template <int NG>
+__device__ __forceinline__ Seq seq_of(const Params &p, int s)
+{
+    return seq_of<NG>(p, p.query_start[s], p.query_start[s + 1], p.context_lens[s]);
 }
 
 // A place in the order of all tiles: tile t of item `it` of sequence s.
@@ -112,43 +118,54 @@ struct Plan {
     int ranges;
 };
 
-// An item's part in a range: tiles [t0, t1).
-struct Item {
-    int s, g, first;                   // first: its first token in the sequence
-    int it, t0, t1;
+// An item's part in a range: tiles [t0, t1) of kv head g and the query tiles from token `first`
+// on, of sequence s.  t0 == t1: there are no more.
+struct alignas(16) Task {
+    int s, g, first, t0, t1;
+    int r0, n, base;                   // the sequence's rows, drafted tokens and tokens before them
+    __device__ __forceinline__ int L() const { return base + n; }
 };
 
-// Goes through a range's items; every role walks for itself.
+// Goes through a range's items; the producer's warp does it for the CTA.  Lane i holds the
+// lengths of sequence `held` + i.
 template <int NG>
 struct Walk {
     Place at;
-    Seq seq;
-    bool loaded = false;
-    __device__ __forceinline__ explicit Walk(const Plan &plan) : at(plan.from) {}
-    __device__ __forceinline__ bool next(const Params &p, const Plan &plan, Item &item)
+    int held, r0, r1, L;
+    __device__ __forceinline__ explicit Walk(const Params &p, const Plan &plan) : at(plan.from) { hold(p, at.s); }
+    __device__ __forceinline__ void hold(const Params &p, int s)
     {
+        held = s;
+        const int i = s + (int)(threadIdx.x & 31);
+        r0 = i < p.num_seqs ? p.query_start[i] : 0;
+        r1 = i < p.num_seqs ? p.query_start[i + 1] : 0;
+        L = i < p.num_seqs ? p.context_lens[i] : 0;
+    }
+    __device__ __forceinline__ Task next(const Params &p, const Plan &plan)
+    {
+        Task k = {};
         for (;;) {
-            if (at.s >= p.num_seqs || at.s > plan.to.s) return false;
-            if (!loaded) {
-                seq = seq_of<NG>(p, at.s);
-                loaded = true;
-            }
+            if (at.s >= p.num_seqs || at.s > plan.to.s) return k;
+            if (at.s >= held + 32) hold(p, at.s);
+            const int i = at.s - held;
+            const Seq q = seq_of<NG>(p, __shfl_sync(kFull, r0, i), __shfl_sync(kFull, r1, i), __shfl_sync(kFull, L, i));
             const bool last = at.s == plan.to.s;
-            if (at.it < seq.items(p) && (!last || at.it <= plan.to.it)) {
-                item.s = at.s;
-                item.it = at.it;
-                item.g = at.it / seq.sets;
-                item.first = (at.it - item.g * seq.sets) * NG * p.tile_tokens;
-                item.t0 = at.t;
-                item.t1 = last && at.it == plan.to.it ? plan.to.t : seq.tiles;
+            while (at.it < q.items(p) && (!last || at.it <= plan.to.it)) {
+                k.s = at.s;
+                k.g = at.it / q.sets;
+                k.first = (at.it - k.g * q.sets) * NG * p.tile_tokens;
+                k.t0 = at.t;
+                k.t1 = last && at.it == plan.to.it ? plan.to.t : q.tiles;
+                k.r0 = q.r0;
+                k.n = q.n;
+                k.base = q.base;
                 ++at.it;
                 at.t = 0;
-                if (item.t0 < item.t1) return true;
-                continue;
+                if (k.t0 < k.t1) return k;
             }
+            k = {};
             ++at.s;
             at.it = at.t = 0;
-            loaded = false;
         }
     }
 };
@@ -232,20 +249,50 @@ __device__ __forceinline__ void make_plan(const Params &p, Plan *plan, int64_t *
     __syncthreads();
 }
 
+__device__ __forceinline__ float max3f(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float min3f(float a, float b, float c)
+{
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// One tensor-memory column of this thread's lane.
+__device__ __forceinline__ uint32_t column(uint32_t taddr)
+{
+    uint32_t v;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr));
+    tc::tmem_wait_ld();
+    return v;
+}
+__device__ __forceinline__ void set_column(uint32_t taddr, uint32_t v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
+    tc::tmem_wait_st();
+}
+
 // The n lowest of 64 bits (all for n >= 64, none for n <= 0).
 __device__ __forceinline__ uint64_t low_bits(int n)
 {
     return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
 }
 
-// Keys k0 .. k0 + 63 that a drafted token sees; `words` its mask, two = its first two words.
-__device__ __forceinline__ uint64_t seen_keys(const Params &p, const uint32_t *words, uint64_t two,
-                                              int k0, int base, int L)
+// Keys k0 .. k0 + 63 that a drafted token sees; `words` its mask, w0 and w1 its first two words.
+__device__ __forceinline__ uint64_t seen_keys(const Params &p, const uint32_t *words, uint32_t w0,
+                                              uint32_t w1, int k0, int base, int L)
 {
     const int d = k0 - base;                     // drafted token of key k0
+    const uint64_t two = w0 | (uint64_t)w1 << 32;
     uint64_t bits;
     if (d <= 0) {
         bits = two << -d | low_bits(-d);         // (base - k0 < 64: the tile holds drafted tokens)
+    } else if (p.words <= 2) {
+        bits = two >> (d & 63);                  // (d < 64: the tile holds a drafted token)
     } else {
         const int w = d >> 5, sh = d & 31;
         const uint64_t a = w < p.words ? words[w] : 0u, b = w + 1 < p.words ? words[w + 1] : 0u;
@@ -283,19 +330,34 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t w)
     return ((w & kExp) == kExp ? 0xffffu : 0u) | ((w >> 16 & kExp) == kExp ? 0xffff0000u : 0u);
 }
 
+// The sum with 0 w added: NaN from the first infinity or NaN on.
+template <bool BF16>
+__device__ __forceinline__ void add_odd(uint32_t &sum, uint32_t w)
+{
+    if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w), "r"(0u));
+    else asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w), "r"(0u));
+}
+
 template <int D, int NG>
 struct Layout {
     static constexpr int kRegions = D / 64;
     // K and V tiles in flight, a ring each
-    static constexpr int kK = NG == 1 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
-    static constexpr int kV = NG == 1 ? (D == 128 ? 2 : 6) : (D == 128 ? 5 : 10);
+    static constexpr int kK = NG == 1 ? (D == 128 ? 2 : 6) : (D == 128 ? 5 : 10);
+    static constexpr int kV = NG == 1 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
     static constexpr int kQBytes = kRegions * kRows * 128;     // a query tile: [region][row][128 B]
     static constexpr int kTileBytes = kRegions * kKeys * 128;  // a K or V tile
     static constexpr int kKRing = NG * kQBytes, kVRing = kKRing + kK * kTileBytes;
     static constexpr int kMisc = kVRing + kV * kTileBytes;
-    static constexpr int kMiscBytes = NG == 1 ? 512 : 1024;
+    static constexpr int kMiscBytes = 1024 * NG;
     static constexpr int kTotal = kMisc + kMiscBytes;
-    static constexpr int kWarps = 4 * NG + 2 + NG, kThreads = 32 * kWarps;
+    // (the copy and issue warps are a warpgroup; NG = 1 has a warp without a role)
+    static constexpr int kWarps = 4 * NG + 4, kThreads = 32 * kWarps;
+    // Registers of a thread: the launch gives kLaunchRegs, the copy and issue warpgroup keeps
+    // kRegsIo and hands the rest to the softmax warpgroups.  A launch with fewer would leave
+    // setmaxnreg.inc waiting for ever, so the host launches only kernels of exactly kLaunchRegs.
+    static constexpr int kLaunchRegs = NG == 1 ? 128 : 168;
+    static constexpr int kRegsIo = 104, kRegsSoftmax = NG == 1 ? 152 : 200;
+    static_assert(NG * kRegsSoftmax + kRegsIo == (NG + 1) * kLaunchRegs, "register split of the launch");
     static constexpr int kProducer = 4 * NG, kIssuer = 4 * NG + 1, kCleaner = 5 * NG + 1;
     static constexpr uint32_t kColumns = 256 * NG;             // per query tile: S, S, O
 };
@@ -309,8 +371,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
     using T = typename E::T;
     using LY = Layout<D, NG>;
     constexpr int NK = LY::kK, NV = LY::kV;
-    // fp16 pools take the reference this much below a row's largest score: weights stay
-    // within 2^15, and those down to 2^-21 of the largest are normal numbers in fp16 (a row
+    // fp16 pools take their weights times 2^kTop: they stay within 2^15, and those down to 2^-21 of the largest are normal numbers in fp16 (a row
     // far below a few dominant keys would lose its weights' bits).
     constexpr float kTop = BF16 ? 0.f : 7.f;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -321,7 +382,8 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
     // S of a query tile out; P out; P V done, each for even and odd tiles
     uint64_t *s_full = clean + NV, *p_full = s_full + 2 * NG, *o_full = p_full + 2 * NG;
     uint64_t *done = o_full + 2 * NG;                          // [NG]
-    uint64_t *odd_keys = done + NG;                            // [NV]: keys whose V held odd values
+    uint64_t *task_full = done + NG, *task_empty = task_full + kTasks;
+    uint64_t *odd_keys = task_empty + kTasks;                            // [NV]: keys whose V held odd values
     int64_t *sums = reinterpret_cast<int64_t *>(odd_keys + NV);         // [warps], see make_plan
     Plan &plan = *reinterpret_cast<Plan *>(sums + LY::kWarps);
     // tile's bad blocks: a K tile's slot is free once S is out, before the softmax reads this, so
@@ -329,7 +391,9 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
     uint8_t *bad_blocks = reinterpret_cast<uint8_t *>(&plan + 1);       // [kTilesKnown]
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bad_blocks + kTilesKnown);
     volatile int *abort_flag = reinterpret_cast<int *>(tslot + 1);
-    static_assert((2 + 2 * NK + 4 * NV + 7 * NG + LY::kWarps) * 8 + sizeof(Plan) + kTilesKnown + 8 <= LY::kMiscBytes &&
+    Task *tasks = reinterpret_cast<Task *>(smem + LY::kTotal) - kTasks;
+    static_assert((2 + 2 * NK + 4 * NV + 7 * NG + 2 * kTasks + LY::kWarps) * 8 + sizeof(Plan) + kTilesKnown + 8 +
+                          kTasks * sizeof(Task) <= LY::kMiscBytes &&
                       NK + 3 <= kTilesKnown && NV + 3 <= kTilesKnown && sizeof(Plan) % 4 == 0,
                   "barriers and flags");
 
@@ -356,10 +420,18 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
             mbar_init(smem_addr(&o_full[i]), 1);
         }
         for (int i = 0; i < NG; ++i) mbar_init(smem_addr(&done[i]), 1);
+        for (int i = 0; i < kTasks; ++i) {
+            mbar_init(smem_addr(&task_full[i]), 1);
+            mbar_init(smem_addr(&task_empty[i]), 5 * NG + 1);   // softmax warps, issuers, cleaner
+        }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) tc::tmem_alloc(tslot, LY::kColumns);
+    if (warp == 1 && lane < 3) {
+        const CUtensorMap *map = lane == 0 ? &tmK : lane == 1 ? &tmV : &tmQ;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+    }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -379,17 +451,50 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
         if (blockIdx.x == 0) p.header[0] = plan.ranges;
     }
 
-    Walk<NG> walk(plan);
-    Item it;
+    // (the register split is taken inside each role's branch, so that all of a role's code
+    // lies under one limit)
+    uint32_t nt = 0;                     // items that this role has taken
+    // the next item's task, false once there is none or a wait ran out
+    Task it;
+    auto next_task = [&]() {
+        if (!mbar_wait(smem_addr(&task_full[nt % kTasks]), (nt / kTasks) & 1u, abort_flag, p.status)) return false;
+        it = tasks[nt % kTasks];
+        return it.t0 < it.t1;
+    };
+    if (warp >= LY::kProducer) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LY::kRegsIo));
     if (warp == LY::kProducer) {
         uint32_t kt = 0, vt = 0, items = 0;      // K tiles, V tiles and items under way or done
         bool ok = true;
-        while (ok && walk.next(p, plan, it)) {
-            const int32_t *row = p.block_tables + (int64_t)it.s * p.max_blocks_per_seq;
-            const int nb = (walk.seq.L + kBlock - 1) / kBlock;
-            // 32 block ids, 8 tiles, at a time, one batch ahead; behind the end any block will do
-            auto ids_from = [&](int t) { return 4 * t + lane < nb ? row[4 * t + lane] : 0; };
-            int ids = ids_from(it.t0), ids_next = ids_from(it.t0 + 8);
+        Walk<NG> walk(p, plan);
+        // 32 block ids, 8 tiles, at a time, one batch ahead; behind the end any block will do
+        auto ids_from = [&](const Task &k, int t) {
+            const int b = 4 * t + lane;
+            return b < (k.L() + kBlock - 1) / kBlock ? p.block_tables[(int64_t)k.s * p.max_blocks_per_seq + b] : 0;
+        };
+        // the boxes of an item's query rows
+        auto each_box = [&](const Task &k, auto &&box) {
+            for (int gr = 0; gr < NG; ++gr)
+                for (int i = 0; i < min(QT, k.n - k.first - gr * QT); i += p.box_tokens)
+                    for (int rg = 0; rg < LY::kRegions; ++rg)
+                        box(gr * LY::kQBytes + rg * kRows * 128 + i * G * 128, rg * 64, k.g,
+                            k.r0 + k.first + gr * QT + i);
+        };
+        Task after = walk.next(p, plan);
+        int ids_after = after.t0 < after.t1 ? ids_from(after, after.t0) : 0;
+        for (;;) {
+            it = after;
+            if (nt >= kTasks)
+                ok = mbar_wait(smem_addr(&task_empty[nt % kTasks]), (nt / kTasks - 1) & 1u, abort_flag, p.status);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                tasks[nt % kTasks] = it;
+                mbar_arrive(smem_addr(&task_full[nt % kTasks]));
+            }
+            ++nt;
+            if (it.t0 >= it.t1) break;
+            int ids = ids_after, ids_next = ids_from(it, it.t0 + 8);
             // the first row of the four blocks of tile t in the pools; all lanes call it
             auto rows_of = [&](int t, int (&y)[4]) {
                 bool bad = false;
@@ -420,7 +525,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                 if (t < it.t1) {
                     if (((t - it.t0) & 7) == 0 && t > it.t0) {
                         ids = ids_next;
-                        ids_next = ids_from(t + 8);
+                        ids_next = ids_from(it, t + 8);
                     }
                     const bool bad = rows_of(t, y);
                     if (kt >= NK)
@@ -441,18 +546,13 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                     if (!ok) break;
                     ++items;
                     if (lane == 0) {
-                        const int left = walk.seq.n - it.first;
                         int boxes = 0;
-                        for (int gr = 0; gr < NG; ++gr)
-                            boxes += (max(0, min(QT, left - gr * QT)) + p.box_tokens - 1) / p.box_tokens;
+                        each_box(it, [&](int, int, int, int) { ++boxes; });
                         const uint32_t qb = smem_addr(q_full);
-                        mbar_arrive_expect_tx(qb, (uint32_t)(boxes * LY::kRegions * p.box_tokens * G * 128));
-                        for (int gr = 0; gr < NG; ++gr)
-                            for (int i = 0; i < min(QT, left - gr * QT); i += p.box_tokens)
-                                for (int rg = 0; rg < LY::kRegions; ++rg)
-                                    tc::tma_load_4d(
-                                        smem_addr(smem + gr * LY::kQBytes + rg * kRows * 128 + i * G * 128),
-                                        &tmQ, rg * 64, 0, it.g, walk.seq.r0 + it.first + gr * QT + i, qb);
+                        mbar_arrive_expect_tx(qb, (uint32_t)(boxes * p.box_tokens * G * 128));
+                        each_box(it, [&](int at, int x, int g, int token) {
+                            tc::tma_load_4d(smem_addr(smem + at), &tmQ, x, 0, g, token, qb);
+                        });
                     }
                 } else {
                     if (vt >= NV)
@@ -465,7 +565,19 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                 }
 #pragma unroll
                 for (int b = 0; b < 4; ++b) y_v[b] = y[b];
+                if (t == min(it.t0 + 2, it.t1)) {
+                    // the item after this one: its first block ids, its query rows into L2
+                    after = walk.next(p, plan);
+                    if (after.t0 < after.t1) {
+                        ids_after = ids_from(after, after.t0);
+                        if (lane == 0)
+                            each_box(after, [&](int, int x, int g, int token) {
+                                tc::tma_prefetch_4d(&tmQ, x, 0, g, token);
+                            });
+                    }
+                }
             }
+            if (!ok) break;
         }
         // after a timed-out wait: let the copies still in flight land first
         if (*abort_flag && lane == 0) {
@@ -486,7 +598,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
             const uint32_t t_s = tmem + 256 * gr, t_o = t_s + 128;
             const uint64_t qa_d = tc::desc_sw128(smem_addr(smem) + gr * LY::kQBytes, 16, 1024);
             uint32_t kt = 0;             // key tiles of the CTA
-            uint32_t tp = 0, items = 0;  // those that this query tile took part in
+            uint32_t tp = 0;             // those that this query tile took part in
             bool ok = true;
             // P V of tile tp - 1, the CTA's tile vt
             auto issue_pv = [&](uint32_t vt) {
@@ -502,16 +614,15 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int kk = 0; kk < kKeys / 16; ++kk)
-                        tc::mma_f16_ts(t_o, t_s + 64 * b + part * 32 + kk * 8,
+                        tc::mma_f16_ts(t_o, t_s + 64 * b + 32 * (kk >> 1) + 16 * part + 8 * (kk & 1),
                                        vb_d + (uint64_t)((kk * 16 * 128) >> 4), id_pv, true);
                 tc::mma_commit(smem_addr(&o_full[2 * gr + b]));
                 tc::mma_commit(smem_addr(&v_empty[slot]));
             };
-            while (ok && walk.next(p, plan, it)) {
-                ok = mbar_wait(smem_addr(q_full), items & 1u, abort_flag, p.status);
+            for (; ok && next_task(); mbar_arrive(smem_addr(&task_empty[nt++ % kTasks]))) {
+                ok = mbar_wait(smem_addr(q_full), nt & 1u, abort_flag, p.status);
                 if (!ok) break;
-                ++items;
-                if (it.first + gr * QT >= walk.seq.n) {          // no rows: only give the buffers back
+                if (it.first + gr * QT >= it.n) {          // no rows: only give the buffers back
                     mbar_arrive(smem_addr(q_empty));
                     for (int t = it.t0; t < it.t1 && ok; ++t, ++kt) {
                         ok = mbar_wait(smem_addr(&k_full[kt % NK]), (kt / NK) & 1u, abort_flag, p.status);
@@ -554,65 +665,86 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
     } else if (warp == LY::kCleaner) {
         uint32_t vt = 0;
         bool ok = true;
-        while (ok && walk.next(p, plan, it)) {
-            const int base = walk.seq.base, L = walk.seq.L;
+        for (; ok && next_task(); ++nt) {
             for (int t = it.t0; t < it.t1; ++t, ++vt) {
                 const uint32_t slot = vt % NV;
                 ok = __all_sync(kFull, mbar_wait(smem_addr(&v_full[slot]), (vt / NV) & 1u, abort_flag, p.status));
                 if (!ok) break;
                 const int k0 = t * kKeys;
-                if (k0 + kKeys > base) {
-                    uint8_t *v = smem + LY::kVRing + slot * LY::kTileBytes;
+                if (k0 + kKeys > it.base) {
                     constexpr int kChunks = LY::kRegions * 8;
-                    const int r0 = max(base - k0, 0), r1 = min(L - k0, kKeys);
-                    uint32_t odd[2] = {0u, 0u};
-                    for (int e = r0 * kChunks + lane; e < kKeys * kChunks; e += 32) {
+                    // chunk e of the tile's rows
+                    auto chunk = [&](int e) -> uint4 & {
                         const int r = e / kChunks, c = e % kChunks;
-                        uint4 *at = reinterpret_cast<uint4 *>(v + (c >> 3) * kKeys * 128 + r * 128 + (c & 7) * 16);
-                        if (r >= r1) {
-                            *at = make_uint4(0u, 0u, 0u, 0u);
-                            continue;
-                        }
-                        uint4 w = *at;
-                        const uint32_t o[4] = {odd_halves<BF16>(w.x), odd_halves<BF16>(w.y),
-                                               odd_halves<BF16>(w.z), odd_halves<BF16>(w.w)};
-                        if (o[0] | o[1] | o[2] | o[3]) {
-                            w.x &= ~o[0];
-                            w.y &= ~o[1];
-                            w.z &= ~o[2];
-                            w.w &= ~o[3];
-                            *at = w;
-                            odd[r >> 5] |= 1u << (r & 31);
-                        }
+                        return *reinterpret_cast<uint4 *>(smem + LY::kVRing + slot * LY::kTileBytes +
+                                                          (c >> 3) * kKeys * 128 + r * 128 + (c & 7) * 16);
+                    };
+                    const int e0 = max(it.base - k0, 0) * kChunks, e1 = min(it.L() - k0, kKeys) * kChunks;
+                    uint32_t sum[4] = {0u, 0u, 0u, 0u}, odd[2] = {0u, 0u};
+#pragma unroll 4
+                    for (int e = e0 + lane; e < e1; e += 32) {
+                        const uint4 w = chunk(e);
+                        add_odd<BF16>(sum[0], w.x);
+                        add_odd<BF16>(sum[1], w.y);
+                        add_odd<BF16>(sum[2], w.z);
+                        add_odd<BF16>(sum[3], w.w);
                     }
-                    odd[0] = __reduce_or_sync(kFull, odd[0]);
-                    odd[1] = __reduce_or_sync(kFull, odd[1]);
+#pragma unroll 4
+                    for (int e = e1 + lane; e < kKeys * kChunks; e += 32) chunk(e) = make_uint4(0u, 0u, 0u, 0u);
+                    if (__any_sync(kFull, odd_halves<BF16>(sum[0]) | odd_halves<BF16>(sum[1]) |
+                                              odd_halves<BF16>(sum[2]) | odd_halves<BF16>(sum[3]))) {
+                        for (int e = e0 + lane; e < e1; e += 32) {
+                            uint4 &w = chunk(e);
+                            const uint4 o = make_uint4(odd_halves<BF16>(w.x), odd_halves<BF16>(w.y),
+                                                       odd_halves<BF16>(w.z), odd_halves<BF16>(w.w));
+                            if (o.x | o.y | o.z | o.w) {
+                                w = make_uint4(w.x & ~o.x, w.y & ~o.y, w.z & ~o.z, w.w & ~o.w);
+                                const int r = e / kChunks;
+                                odd[r >> 5] |= 1u << (r & 31);
+                            }
+                        }
+                        odd[0] = __reduce_or_sync(kFull, odd[0]);
+                        odd[1] = __reduce_or_sync(kFull, odd[1]);
+                    }
                     if (lane == 0) odd_keys[slot] = odd[0] | (uint64_t)odd[1] << 32;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
                 if (lane == 0) mbar_arrive(smem_addr(&clean[slot]));
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&task_empty[nt % kTasks]));
         }
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LY::kRegsSoftmax));
         // ---------------------------------------------------------- softmax
         const int gr = warp >> 2, r = threadIdx.x - kRows * gr;
         const uint32_t t_s = tmem + 256 * gr + ((uint32_t)(32 * (warp & 3)) << 16), t_o = t_s + 128;
         const int jj = r / G, h = r - jj * G;
+        // product of a hidden key: the scale carries it to -inf (it is never zero, see the host)
+        const float hide = p.scale_log2 < 0.f ? INFINITY : -INFINITY;
         uint32_t kt = 0, tp = 0;         // key tiles of the CTA; those with rows of this query tile
         bool alive = true;
-        while (alive && walk.next(p, plan, it)) {
-            const int n = walk.seq.n, base = walk.seq.base, L = walk.seq.L;
+        // the item is done with
+        auto leave = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&task_empty[nt % kTasks]));
+            ++nt;
+        };
+        while (alive && __all_sync(kFull, next_task())) {
+            const int n = it.n, base = it.base, L = it.L();
             const int token = it.first + gr * QT + jj;
             if (it.first + gr * QT >= n) {               // no rows in this query tile
                 kt += (uint32_t)(it.t1 - it.t0);
+                leave();
                 continue;
             }
             const bool valid = r < QT * G && token < n;
             const bool busy = __any_sync(kFull, valid);  // some row of the warp counts
-            const uint32_t *words = p.mask + (int64_t)(walk.seq.r0 + (valid ? token : it.first)) * p.words;
-            const uint64_t two = words[0] | (uint64_t)(p.words > 1 ? words[1] : 0u) << 32;
-            float m_ref = -INFINITY, l = 0.f;
+            const uint32_t *words = p.mask + (int64_t)(it.r0 + (valid ? token : it.first)) * p.words;
+            const uint32_t w0 = words[0], w1 = p.words > 1 ? words[1] : 0u;
+            float ref = hide, l = 0.f;
             int bad = 0;
             if (busy) {
                 uint32_t z[32];
@@ -631,100 +763,84 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                 }
                 tc::fence_after_sync();
                 bad |= bad_blocks[kt % kTilesKnown];
-                float x[kKeys];
-                {
-                    uint32_t v[2][32];
-                    tc::tmem_ld32(t_s + 64 * b, v[0]);
-                    tc::tmem_ld32(t_s + 64 * b + 32, v[1]);
-                    tc::tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        x[c] = __uint_as_float(v[0][c]);
-                        x[32 + c] = __uint_as_float(v[1][c]);
-                    }
-                }
                 const int k0 = t * kKeys;
                 const bool edge = k0 + kKeys > base;     // drafted tokens or the end: masks
                 uint64_t see = ~0ull;
-                if (edge) {
-                    if (valid) see = seen_keys(p, words, two, k0, base, L);
-                    // (the scale is never zero, see the host)
-                    const float hide = p.scale_log2 < 0.f ? INFINITY : -INFINITY;
-                    const uint32_t see0 = (uint32_t)see, see1 = (uint32_t)(see >> 32);
+                if (edge && valid) see = seen_keys(p, words, w0, w1, k0, base, L);
+                // products of 32 keys (the scale is in the exponents), those that the row does not
+                // see hidden; the columns are read twice, so that the loop below stays a loop: all
+                // roles' code has to stay near (instruction fetches were what it waited for)
+                auto products = [&](int c0, float (&x)[32]) {
+                    uint32_t v[32];
+                    tc::tmem_ld32(t_s + 64 * b + c0, v);
+                    tc::tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        if (!((see0 >> c) & 1u)) x[c] = hide;
-                        if (!((see1 >> c) & 1u)) x[32 + c] = hide;
-                    }
-                }
-                // the tile's largest scaled score
-                float mx;
-                if (p.scale_log2 >= 0.f) {
-                    mx = fmaxf(x[0], x[1]);
+                    for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(v[c]);
+                    if (edge) {
+                        const uint32_t bits = (uint32_t)(see >> c0);
 #pragma unroll
-                    for (int c = 2; c < kKeys; c += 2) mx = fmaxf(mx, fmaxf(x[c], x[c + 1]));
-                } else {
-                    mx = fminf(x[0], x[1]);
-#pragma unroll
-                    for (int c = 2; c < kKeys; c += 2) mx = fminf(mx, fminf(x[c], x[c + 1]));
-                }
-                mx *= p.scale_log2;
-                float f = 1.f;
-                bool resc = false;
-                if (valid && mx > m_ref + (kLazy + kTop)) {      // also the first tile: m_ref = -inf
-                    // (from 2^24 on, where the spacing nears kTop, the largest score itself)
-                    const float now = kTop == 0.f || fabsf(mx) > 0x1p24f ? mx : mx - kTop;
-                    if (m_ref != -INFINITY) {
-                        f = fast_exp2(m_ref - now);
-                        resc = true;
-                    }
-                    m_ref = now;
-                }
-                // (a row that has seen no key yet has m_ref = -inf; any finite reference gives
-                // its hidden scores weight 2^-inf = 0)
-                const float m_sub = m_ref == -INFINITY ? 0.f : m_ref;
-                const bool big = fabsf(m_sub) > 0x1p24f;
-                const uint64_t sc2 = pack2f(p.scale_log2, p.scale_log2), nm2 = pack2f(-m_sub, -m_sub);
-                uint64_t lsum2 = pack2f(0.f, 0.f);
-                uint64_t zero = 0ull;                    // (rare path) weights that are zero
-                // 32 keys at a time: weights, their parts over the tile's S columns (already
-                // read), high parts in the first 32, low parts in the next
-                auto weights = [&](auto wide) {
-#pragma unroll
-                    for (int c0 = 0; c0 < kKeys; c0 += 32) {
-                        uint32_t hi[16], lo[16];
-#pragma unroll
-                        for (int c = c0; c < c0 + 32; c += 2) {
-                            float2 e = unpack2f(fma2f(pack2f(x[c], x[c + 1]), sc2, nm2));
-                            if (decltype(wide)::value && big)
-                                e = make_float2(__fsub_rn(__fmul_rn(x[c], p.scale_log2), m_sub),
-                                                __fsub_rn(__fmul_rn(x[c + 1], p.scale_log2), m_sub));
-                            const float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
-                            const uint64_t pp = pack2f(p0, p1);
-                            lsum2 = add2f(lsum2, pp);
-                            two_parts<BF16>(p0, p1, pp, hi[(c - c0) / 2], lo[(c - c0) / 2]);
-                            if (decltype(wide)::value)
-                                zero |= (uint64_t)(p0 == 0.f) << c | (uint64_t)(p1 == 0.f) << (c + 1);
-                        }
-                        tc::tmem_st16(t_s + 64 * b + c0 / 2, hi);
-                        tc::tmem_st16(t_s + 64 * b + 32 + c0 / 2, lo);
+                        for (int c = 0; c < 32; ++c)
+                            if (!((bits >> c) & 1u)) x[c] = hide;
                     }
                 };
+                // the tile's product of the largest score
+                float mx = hide;
+#pragma unroll 1
+                for (int c0 = 0; c0 < kKeys; c0 += 32) {
+                    float x[32];
+                    products(c0, x);
+                    if (p.scale_log2 >= 0.f) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) mx = max3f(mx, x[c], x[c + 1]);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) mx = min3f(mx, x[c], x[c + 1]);
+                    }
+                }
+                // The reference is a product: a weight is 2^((x - ref) scale + kTop), so products
+                // that agree weigh alike whatever their size, and nothing is lost to the rounding
+                // of a scaled reference.
+                float f = 1.f;
+                bool resc = false;
+                const bool unset = ref == hide;          // no key seen yet
+                if (valid && mx != hide && (unset || (mx - ref) * p.scale_log2 > kLazy)) {
+                    if (!unset) {
+                        f = fast_exp2((ref - mx) * p.scale_log2);
+                        resc = true;
+                    }
+                    ref = mx;
+                }
+                // (any finite reference gives hidden products weight 2^-inf = 0)
+                const float sub = ref == hide ? 0.f : ref;
+                const uint64_t sc2 = pack2f(p.scale_log2, p.scale_log2), sub2 = pack2f(-sub, -sub);
+                const uint64_t top2 = pack2f(kTop, kTop);
+                uint64_t lsum2 = pack2f(0.f, 0.f);
+                // weights over the products' columns: 16 of high parts, 16 of low parts
+#pragma unroll 1
+                for (int c0 = 0; c0 < kKeys; c0 += 32) {
+                    float x[32];
+                    products(c0, x);
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        const uint64_t d2 = add2f(pack2f(x[c], x[c + 1]), sub2);
+                        const float2 e = unpack2f(kTop == 0.f ? mul2f(d2, sc2) : fma2f(d2, sc2, top2));
+                        const float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
+                        const uint64_t pp = pack2f(p0, p1);
+                        lsum2 = add2f(lsum2, pp);
+                        two_parts<BF16>(p0, p1, pp, hi[c / 2], lo[c / 2]);
+                    }
+                    tc::tmem_st16(t_s + 64 * b + c0, hi);
+                    tc::tmem_st16(t_s + 64 * b + c0 + 16, lo);
+                }
+                const float2 ls = unpack2f(lsum2);
+                l = l * f + (ls.x + ls.y);
                 uint64_t odd = 0ull;                     // keys whose V held odd values
                 if (edge) {
                     const bool swept = mbar_wait(smem_addr(&clean[vslot]), (kt / NV) & 1u, abort_flag, p.status);
                     if (!__all_sync(kFull, swept)) { alive = false; break; }
                     odd = odd_keys[vslot];
                 }
-                // the reference is a rounded product: against it, the unrounded products of the
-                // fused form come out up to half its spacing too large or too small, the same for
-                // the whole row, which cancels; from 2^25 on that is 2 or more and grows past the
-                // range of the weights, so from 2^24 on the products are rounded alike, by scalar
-                // operations that stay apart (the largest weight is then exactly 1)
-                if (__any_sync(kFull, big) || odd) weights(std::true_type{});
-                else weights(std::false_type{});
-                const float2 ls = unpack2f(lsum2);
-                l = l * f + (ls.x + ls.y);
                 // O changes before P V of this tile, once P V of the one before has ended; the
                 // wait for that consumes its o_full phase either here or after P is out
                 const bool touch = __any_sync(kFull, resc) || odd;
@@ -734,30 +850,36 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                     tc::fence_after_sync();
                 }
                 if (touch) {
-                    tc::tmem_wait_st();                  // (O's zeros, in an item's first tile)
-                    const int32_t *row = p.block_tables + (int64_t)it.s * p.max_blocks_per_seq;
-#pragma unroll
+                    tc::tmem_wait_st();                  // (O's zeros, in an item's first tile; P)
+#pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 32) {
                         uint32_t v[32];
                         tc::tmem_ld32(t_o + c0, v);
                         tc::tmem_wait_ld();
 #pragma unroll
                         for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * f);
-                        for (uint64_t left = valid ? odd & see : 0ull; left; left &= left - 1) {
-                            const int c = __ffsll((long long)left) - 1, pos = k0 + c;
-                            int id = row[pos / kBlock];
-                            if (id < 0 || id >= p.num_blocks) id = 0;        // (the result is zero anyway)
-                            const T *vp = static_cast<const T *>(p.v_pool) +
-                                          (((int64_t)id * Hkv + it.g) * kBlock + pos % kBlock) * D + c0;
-                            const bool none = zero >> c & 1u;                // 0 * infinity
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float y = (float)vp[e];
-                                if (!(fabsf(y) < INFINITY))
-                                    v[e] = __float_as_uint(__uint_as_float(v[e]) + (none ? NAN : y));
-                            }
-                        }
                         tc::tmem_st32(t_o + c0, v);
+                    }
+                    tc::tmem_wait_st();
+                    // the odd values of a key's V go to the rows that see it, times their weights
+                    // (an infinity, or NaN; 0 * infinity is NaN)
+#pragma unroll 1
+                    for (uint64_t left = odd; left; left &= left - 1) {
+                        const int c = __ffsll((long long)left) - 1, pos = k0 + c;
+                        const uint32_t word = t_s + 64 * b + (c & 32) + (c & 31) / 2;
+                        const uint32_t both = column(word) | column(word + 16);
+                        const bool some = (both >> (16 * (c & 1)) & 0x7fffu) != 0u;
+                        int id = p.block_tables[(int64_t)it.s * p.max_blocks_per_seq + pos / kBlock];
+                        if (id < 0 || id >= p.num_blocks) id = 0;            // (the result is zero anyway)
+                        const T *vp = static_cast<const T *>(p.v_pool) +
+                                      (((int64_t)id * Hkv + it.g) * kBlock + pos % kBlock) * D;
+#pragma unroll 1
+                        for (int d = 0; d < D; ++d) {
+                            const float y = (float)vp[d];
+                            if (fabsf(y) < INFINITY) continue;               // the same for the warp
+                            const float o = __uint_as_float(column(t_o + d));
+                            set_column(t_o + d, __float_as_uint(see >> c & 1u ? o + (some ? y : NAN) : o));
+                        }
                     }
                 }
                 tc::tmem_wait_st();
@@ -775,12 +897,15 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
             const bool ended = mbar_wait(smem_addr(&o_full[2 * gr + ((tp - 1) & 1u)]), ((tp - 1) >> 1) & 1u, abort_flag, p.status);
             if (!__all_sync(kFull, ended)) break;
             tc::fence_after_sync();
-            if (!busy) continue;
-            if (it.t0 > 0 || it.t1 < walk.seq.tiles) {
+            if (!busy) {
+                leave();
+                continue;
+            }
+            if (it.t0 > 0 || it.t1 * kKeys < L) {
                 const int64_t piece = 2 * blockIdx.x + (it.t0 == 0);
                 const int rr = gr * kRows + r;
-                if (valid) p.part_ml[piece * p.piece_rows + rr] = make_float2(m_ref, bad ? -1.f : l);
-#pragma unroll
+                if (valid) p.part_ml[piece * p.piece_rows + rr] = make_float2(ref, bad ? -1.f : l);
+#pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t v[32];
                     tc::tmem_ld32(t_o + c0, v);
@@ -798,8 +923,8 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                 const bool none = bad || l == 0.f;       // a bad block, or nothing seen
                 const float inv = none ? 0.f : 1.f / l;
                 T *out = static_cast<T *>(p.out) +
-                         ((int64_t)(walk.seq.r0 + token) * p.num_q_heads + (int64_t)it.g * G + h) * D;
-#pragma unroll
+                         ((int64_t)(it.r0 + token) * p.num_q_heads + (int64_t)it.g * G + h) * D;
+#pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t v[32];
                     tc::tmem_ld32(t_o + c0, v);
@@ -817,6 +942,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                 }
             }
             tc::fence_before_sync();
+            leave();
         }
     }
     tc::fence_before_sync();
@@ -882,12 +1008,12 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const Params p)
         const int gr = rr / kRows, jj = (rr - gr * kRows) / G, h = rr - gr * kRows - jj * G;
         const int token = first + gr * p.tile_tokens + jj;
         if (jj >= p.tile_tokens || token >= q.n) continue;
-        float m = -INFINITY;
+        float m = p.scale_log2 < 0.f ? INFINITY : -INFINITY;
         bool bad = false;
 #pragma unroll 4
         for (int k = 0; k < pieces; ++k) {
             const float2 ml = p.part_ml[piece(k) * p.piece_rows + rr];
-            m = ml.y == 0.f ? m : fmaxf(m, ml.x);        // (a sum of zero: it saw nothing there)
+            if (ml.y != 0.f) m = p.scale_log2 < 0.f ? fminf(m, ml.x) : fmaxf(m, ml.x);   // (0: it saw nothing)
             bad |= ml.y < 0.f;
         }
         float l = 0.f, o[8] = {};
@@ -895,7 +1021,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const Params p)
         for (int k = 0; k < pieces; ++k) {
             const int64_t at = piece(k);
             const float2 ml = p.part_ml[at * p.piece_rows + rr];
-            const float w = ml.y == 0.f ? 0.f : fast_exp2(ml.x - m);
+            const float w = ml.y == 0.f ? 0.f : fast_exp2((ml.x - m) * p.scale_log2);
             const float4 *src = p.part_o + (at * (D / 4) + 2 * c8) * p.piece_rows + rr;
             const float4 a = src[0], b = src[p.piece_rows];
             l += w * ml.y;
@@ -976,14 +1102,14 @@ using JoinFn = void (*)(Params);
 struct Pick {
     KernelFn fn;
     JoinFn join;
-    int smem, threads, ctas;           // ctas: to an SM
+    int smem, threads, ctas, regs;     // ctas: to an SM
 };
 
 template <int D, bool BF16, int NG>
 static Pick pick_of()
 {
     return {&tree_kernel<D, BF16, NG>, &tree_join_kernel<D, BF16, NG>, Layout<D, NG>::kTotal,
-            Layout<D, NG>::kThreads, NG == 1 ? 2 : 1};
+            Layout<D, NG>::kThreads, NG == 1 ? 2 : 1, Layout<D, NG>::kLaunchRegs};
 }
 
 template <int NG>
@@ -1008,6 +1134,8 @@ static int resident(const Pick &k, int slot)
     if (n == 0) {
         const void *fn = reinterpret_cast<const void *>(k.fn);
         int sms = 0, shared = 0, reserved = 0;
+        cudaFuncAttributes a;
+        if (cudaFuncGetAttributes(&a, fn) != cudaSuccess || a.numRegs != k.regs) return -1;
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&shared, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev) != cudaSuccess ||
