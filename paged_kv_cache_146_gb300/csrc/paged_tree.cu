@@ -64,6 +64,7 @@ struct Params {
     int32_t max_blocks_per_seq, num_blocks;
     int32_t tile_tokens;               // tokens of a query tile
     int32_t box_tokens;                // and of one box of query rows
+    int32_t set_tokens, set_inverse;   // of NG query tiles; ceil(2^20 / that)
     int32_t piece_rows;                // rows of a piece's place in the workspace
     float scale_log2;
     int32_t *header;                   // [0] = ranges
@@ -85,7 +86,6 @@ struct Seq {
     __device__ __forceinline__ int items(const Params &p) const { return sets * p.num_kv_heads; }
 };
 
-template <int NG>
 __device__ __forceinline__ Seq seq_of(const Params &p, int r0, int r1, int L)
 {
     Seq q;
@@ -97,14 +97,14 @@ __device__ __forceinline__ Seq seq_of(const Params &p, int r0, int r1, int L)
             q.n > 32 * p.words;
     q.base = q.L - q.n;
     q.tiles = (q.L + kKeys - 1) / kKeys;
-    q.sets = q.bad ? 0 : (q.n + NG * p.tile_tokens - 1) / (NG * p.tile_tokens);
+    // ceil(n / set_tokens): n + set_tokens < 1280 here, so 2^20 is enough for the inverse
+    q.sets = q.bad ? 0 : (q.n + p.set_tokens - 1) * p.set_inverse >> 20;
     return q;
 }
 
-template <int NG>
 __device__ __forceinline__ Seq seq_of(const Params &p, int s)
 {
-    return seq_of<NG>(p, p.query_start[s], p.query_start[s + 1], p.context_lens[s]);
+    return seq_of(p, p.query_start[s], p.query_start[s + 1], p.context_lens[s]);
 }
 
 // A place in the order of all tiles: tile t of item `it` of sequence s.
@@ -128,11 +128,18 @@ struct alignas(16) Task {
 
 // Goes through a range's items; the producer's warp does it for the CTA.  Lane i holds the
 // lengths of sequence `held` + i.
-template <int NG>
 struct Walk {
     Place at;
+    Seq q;                             // sequence at.s
+    int g, set;                        // item at.it
     int held, r0, r1, L;
-    __device__ __forceinline__ explicit Walk(const Params &p, const Plan &plan) : at(plan.from) { hold(p, at.s); }
+    __device__ __forceinline__ Walk(const Params &p, const Plan &plan) : at(plan.from)
+    {
+        hold(p, at.s);
+        q = sequence(p);
+        g = q.sets ? at.it / q.sets : 0;
+        set = at.it - g * q.sets;
+    }
     __device__ __forceinline__ void hold(const Params &p, int s)
     {
         held = s;
@@ -141,41 +148,62 @@ struct Walk {
         r1 = i < p.num_seqs ? p.query_start[i + 1] : 0;
         L = i < p.num_seqs ? p.context_lens[i] : 0;
     }
+    __device__ __forceinline__ Seq sequence(const Params &p) const
+    {
+        const int i = at.s - held;
+        return seq_of(p, __shfl_sync(kFull, r0, i), __shfl_sync(kFull, r1, i), __shfl_sync(kFull, L, i));
+    }
     __device__ __forceinline__ Task next(const Params &p, const Plan &plan)
     {
         Task k = {};
-        for (;;) {
-            if (at.s >= p.num_seqs || at.s > plan.to.s) return k;
-            if (at.s >= held + 32) hold(p, at.s);
-            const int i = at.s - held;
-            const Seq q = seq_of<NG>(p, __shfl_sync(kFull, r0, i), __shfl_sync(kFull, r1, i), __shfl_sync(kFull, L, i));
+        while (at.s < p.num_seqs && at.s <= plan.to.s) {
             const bool last = at.s == plan.to.s;
-            while (at.it < q.items(p) && (!last || at.it <= plan.to.it)) {
+            if (g < p.num_kv_heads && q.sets > 0 && (!last || at.it <= plan.to.it)) {
+                const int t1 = last && at.it == plan.to.it ? plan.to.t : q.tiles;
+                const int t0 = at.t;
                 k.s = at.s;
-                k.g = at.it / q.sets;
-                k.first = (at.it - k.g * q.sets) * NG * p.tile_tokens;
-                k.t0 = at.t;
-                k.t1 = last && at.it == plan.to.it ? plan.to.t : q.tiles;
+                k.g = g;
+                k.first = set * p.set_tokens;
                 k.r0 = q.r0;
                 k.n = q.n;
                 k.base = q.base;
                 ++at.it;
                 at.t = 0;
-                if (k.t0 < k.t1) return k;
+                if (++set == q.sets) {
+                    set = 0;
+                    ++g;
+                }
+                if (t0 < t1) {
+                    k.t0 = t0;
+                    k.t1 = t1;
+                    return k;
+                }
+            } else {
+                ++at.s;
+                at.it = at.t = g = set = 0;
+                if (at.s >= held + 32) hold(p, at.s);
+                q = sequence(p);
             }
-            k = {};
-            ++at.s;
-            at.it = at.t = 0;
         }
+        return k;
     }
 };
+
+// floor(a / b) for 0 <= a, 0 < b, by an estimate in fp32 that is then put right.
+__device__ __forceinline__ int64_t quotient(int64_t a, int b)
+{
+    int64_t q = (int64_t)((float)a / (float)b), r = a - q * b;
+    for (; r < 0; r += b) --q;
+    for (; r >= b; r -= b) ++q;
+    return q;
+}
 
 // The place where a range ends that would end `off` units into sequence s's: not inside an
 // item's overhead, and not so near an end of the item that a short piece would be left.
 __device__ __forceinline__ Place cut(const Params &p, int s, const Seq &q, int64_t off, int snap)
 {
     const int per = q.tiles + kItemCost;
-    Place c = {s, (int)(off / per), 0};
+    Place c = {s, (int)quotient(off, per), 0};
     const int t = (int)(off - (int64_t)c.it * per) - kItemCost;
     c.t = t < snap ? 0 : t;
     if (t > q.tiles - snap) {
@@ -200,7 +228,7 @@ __device__ __forceinline__ void make_plan(const Params &p, Plan *plan, int64_t *
     const int s0 = min(tid * slice, p.num_seqs), s1 = min(s0 + slice, p.num_seqs);
     int64_t mine = 0;
     for (int s = s0; s < s1; ++s) {
-        const Seq q = seq_of<NG>(p, s);
+        const Seq q = seq_of(p, s);
         mine += (int64_t)q.items(p) * (q.tiles + kItemCost);
         if (q.bad && s % gridDim.x == blockIdx.x) {
             atomicOr(p.status, PKV_DEV_BAD_LEN);
@@ -223,20 +251,23 @@ __device__ __forceinline__ void make_plan(const Params &p, Plan *plan, int64_t *
         all += warp_sum[w];
     }
     const int ranges = (int)max((int64_t)1, min((int64_t)gridDim.x, all / kMinRange));
-    const int snap = (int)min((int64_t)kSnap, all / ranges / 4);
-    const int64_t ends[2] = {all * blockIdx.x / ranges, all * (blockIdx.x + 1) / ranges};
+    // the first `more` ranges have a unit more
+    const int64_t size = quotient(all, ranges), more = all - size * ranges;
+    const int snap = (int)min((int64_t)kSnap, size / 4);
+    const int64_t begin = size * blockIdx.x + min((int64_t)blockIdx.x, more);
+    const int64_t ends[2] = {begin, begin + size + (blockIdx.x < more)};
     if (tid == 0) {
         plan->ranges = ranges;
         plan->from = plan->to = Place{p.num_seqs, 0, 0};
     }
     __syncthreads();
     if (blockIdx.x < ranges) {
-#pragma unroll
+#pragma unroll 1
         for (int e = 0; e < 2; ++e) {
-            if (ends[e] < before || ends[e] >= before + mine) continue;
-            int64_t off = ends[e] - before;
+            int64_t off = (e ? ends[1] : ends[0]) - before;
+            if (off < 0 || off >= mine) continue;
             for (int s = s0; s < s1; ++s) {
-                const Seq q = seq_of<NG>(p, s);
+                const Seq q = seq_of(p, s);
                 const int64_t units = (int64_t)q.items(p) * (q.tiles + kItemCost);
                 if (off < units) {
                     (e ? plan->to : plan->from) = cut(p, s, q, off, snap);
@@ -274,6 +305,17 @@ __device__ __forceinline__ void set_column(uint32_t taddr, uint32_t v)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
     tc::tmem_wait_st();
+}
+
+// One lane of the warp, always the same.  Code that only it runs, in a branch of the whole warp,
+// keeps the operands of matrix instructions and copies in uniform registers; in a branch by
+// lane number each operand goes through a move of its own, and the issue of a tile's products
+// took as long as its softmax.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
 }
 
 // The n lowest of 64 bits (all for n >= 64, none for n <= 0).
@@ -466,7 +508,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
     if (warp == LY::kProducer) {
         uint32_t kt = 0, vt = 0, items = 0;      // K tiles, V tiles and items under way or done
         bool ok = true;
-        Walk<NG> walk(p, plan);
+        Walk walk(p, plan);
         // 32 block ids, 8 tiles, at a time, one batch ahead; behind the end any block will do
         auto ids_from = [&](const Task &k, int t) {
             const int b = 4 * t + lane;
@@ -480,21 +522,32 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                         box(gr * LY::kQBytes + rg * kRows * 128 + i * G * 128, rg * 64, k.g,
                             k.r0 + k.first + gr * QT + i);
         };
-        Task after = walk.next(p, plan);
-        int ids_after = after.t0 < after.t1 ? ids_from(after, after.t0) : 0;
-        for (;;) {
+        Task after = {};
+        int ids_after = 0;
+        // the item after `it`: its first block ids, its query rows into L2
+        for (bool begun = false;; begun = true) {
             it = after;
+            after = walk.next(p, plan);
+            const int ids_now = ids_after;
+            if (after.t0 < after.t1) {
+                ids_after = ids_from(after, after.t0);
+                if (begun && elect_one())
+                    each_box(after, [&](int, int x, int g, int token) {
+                        tc::tma_prefetch_4d(&tmQ, x, 0, g, token);
+                    });
+            }
+            if (!begun) continue;
             if (nt >= kTasks)
                 ok = mbar_wait(smem_addr(&task_empty[nt % kTasks]), (nt / kTasks - 1) & 1u, abort_flag, p.status);
             ok = __all_sync(kFull, ok);
             if (!ok) break;
-            if (lane == 0) {
+            if (elect_one()) {
                 tasks[nt % kTasks] = it;
                 mbar_arrive(smem_addr(&task_full[nt % kTasks]));
             }
             ++nt;
             if (it.t0 >= it.t1) break;
-            int ids = ids_after, ids_next = ids_from(it, it.t0 + 8);
+            int ids = ids_now, ids_next = ids_from(it, it.t0 + 8);
             // the first row of the four blocks of tile t in the pools; all lanes call it
             auto rows_of = [&](int t, int (&y)[4]) {
                 bool bad = false;
@@ -532,7 +585,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                         ok = mbar_wait(smem_addr(&k_empty[kt % NK]), (kt / NK - 1) & 1u, abort_flag, p.status);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
-                    if (lane == 0) {
+                    if (elect_one()) {
                         if (bad) atomicOr(p.status, PKV_DEV_BAD_BLOCK);
                         bad_blocks[kt % kTilesKnown] = (uint8_t)bad;
                         copy(&tmK, LY::kKRing + (kt % NK) * LY::kTileBytes, &k_full[kt % NK], y);
@@ -545,7 +598,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
                     ++items;
-                    if (lane == 0) {
+                    if (elect_one()) {
                         int boxes = 0;
                         each_box(it, [&](int, int, int, int) { ++boxes; });
                         const uint32_t qb = smem_addr(q_full);
@@ -559,23 +612,12 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                         ok = mbar_wait(smem_addr(&v_empty[vt % NV]), (vt / NV - 1) & 1u, abort_flag, p.status);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
-                    if (lane == 0)
+                    if (elect_one())
                         copy(&tmV, LY::kVRing + (vt % NV) * LY::kTileBytes, &v_full[vt % NV], y_v);
                     ++vt;
                 }
 #pragma unroll
                 for (int b = 0; b < 4; ++b) y_v[b] = y[b];
-                if (t == min(it.t0 + 2, it.t1)) {
-                    // the item after this one: its first block ids, its query rows into L2
-                    after = walk.next(p, plan);
-                    if (after.t0 < after.t1) {
-                        ids_after = ids_from(after, after.t0);
-                        if (lane == 0)
-                            each_box(after, [&](int, int x, int g, int token) {
-                                tc::tma_prefetch_4d(&tmQ, x, 0, g, token);
-                            });
-                    }
-                }
             }
             if (!ok) break;
         }
@@ -591,68 +633,83 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
             if (items > 0) drain(q_full, (items - 1) & 1u);
         }
     } else if (warp >= LY::kIssuer && warp < LY::kIssuer + NG) {
-        if (lane == 0) {
-            const int gr = warp - LY::kIssuer;
-            const uint32_t id_qk = tc::idesc_f16(BF16, kRows, kKeys, 0, 0);
-            const uint32_t id_pv = tc::idesc_f16(BF16, kRows, D, 0, 1);
-            const uint32_t t_s = tmem + 256 * gr, t_o = t_s + 128;
-            const uint64_t qa_d = tc::desc_sw128(smem_addr(smem) + gr * LY::kQBytes, 16, 1024);
-            uint32_t kt = 0;             // key tiles of the CTA
-            uint32_t tp = 0;             // those that this query tile took part in
-            bool ok = true;
-            // P V of tile tp - 1, the CTA's tile vt
-            auto issue_pv = [&](uint32_t vt) {
-                const uint32_t slot = vt % NV, par = (vt / NV) & 1u, b = (tp - 1) & 1u;
-                ok = mbar_wait(smem_addr(&clean[slot]), par, abort_flag, p.status) &&
-                     mbar_wait(smem_addr(&v_full[slot]), par, abort_flag, p.status) &&
-                     mbar_wait(smem_addr(&p_full[2 * gr + b]), ((tp - 1) >> 1) & 1u, abort_flag, p.status);
-                if (!ok) return;
-                tc::fence_after_sync();
-                const uint64_t vb_d =
-                    tc::desc_sw128(smem_addr(smem + LY::kVRing + slot * LY::kTileBytes), kKeys * 128, 1024);
+        const int gr = __shfl_sync(kFull, warp, 0) - LY::kIssuer;
+        const uint32_t id_qk = tc::idesc_f16(BF16, kRows, kKeys, 0, 0);
+        const uint32_t id_pv = tc::idesc_f16(BF16, kRows, D, 0, 1);
+        const uint32_t t_s = __shfl_sync(kFull, tmem, 0) + 256 * gr, t_o = t_s + 128;
+        const uint64_t qa_d = tc::desc_sw128(smem_addr(smem) + gr * LY::kQBytes, 16, 1024);
+        uint32_t kt = 0;                 // key tiles of the CTA
+        uint32_t tp = 0;                 // those that this query tile took part in
+        bool ok = true;
+        auto reach = [&](uint64_t *bar, uint32_t parity) {
+            ok = __all_sync(kFull, mbar_wait(smem_addr(bar), parity, abort_flag, p.status));
+            return ok;
+        };
+        // P V of tile tp - 1, the CTA's tile vt
+        auto issue_pv = [&](uint32_t vt) {
+            const uint32_t slot = vt % NV, par = (vt / NV) & 1u, b = (tp - 1) & 1u;
+            if (!reach(&clean[slot], par) || !reach(&v_full[slot], par) ||
+                !reach(&p_full[2 * gr + b], ((tp - 1) >> 1) & 1u))
+                return;
+            tc::fence_after_sync();
+            const uint64_t vb_d = tc::desc_sw128(smem_addr(smem + LY::kVRing + slot * LY::kTileBytes), kKeys * 128, 1024);
+            if (elect_one()) {
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        tc::mma_f16_ts(t_o, t_s + 64 * b + 32 * (kk >> 1) + 16 * part + 8 * (kk & 1),
-                                       vb_d + (uint64_t)((kk * 16 * 128) >> 4), id_pv, true);
+                for (int i = 0; i < 2 * kKeys / 16; ++i) {       // 16 keys, high or low parts
+                    const int kk = 2 * (i >> 2) + (i & 1);
+                    tc::mma_f16_ts(t_o, t_s + 64 * b + 8 * i, vb_d + (uint64_t)((kk * 16 * 128) >> 4), id_pv, true);
+                }
                 tc::mma_commit(smem_addr(&o_full[2 * gr + b]));
                 tc::mma_commit(smem_addr(&v_empty[slot]));
-            };
-            for (; ok && next_task(); mbar_arrive(smem_addr(&task_empty[nt++ % kTasks]))) {
-                ok = mbar_wait(smem_addr(q_full), nt & 1u, abort_flag, p.status);
-                if (!ok) break;
-                if (it.first + gr * QT >= it.n) {          // no rows: only give the buffers back
-                    mbar_arrive(smem_addr(q_empty));
-                    for (int t = it.t0; t < it.t1 && ok; ++t, ++kt) {
-                        ok = mbar_wait(smem_addr(&k_full[kt % NK]), (kt / NK) & 1u, abort_flag, p.status);
-                        if (ok) mbar_arrive(smem_addr(&k_empty[kt % NK]));
-                        ok = ok && mbar_wait(smem_addr(&v_full[kt % NV]), (kt / NV) & 1u, abort_flag, p.status);
-                        if (ok) mbar_arrive(smem_addr(&v_empty[kt % NV]));
-                    }
-                    continue;
-                }
-                for (int t = it.t0; t < it.t1 && ok; ++t, ++kt) {
-                    const uint32_t slot = kt % NK;
-                    ok = mbar_wait(smem_addr(&k_full[slot]), (kt / NK) & 1u, abort_flag, p.status);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    const uint64_t kb_d = tc::desc_sw128(smem_addr(smem + LY::kKRing + slot * LY::kTileBytes), 16, 1024);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk & 3) * 32;      // 16 values inside the row
-                        tc::mma_f16(t_s + 64 * (tp & 1u), qa_d + (uint64_t)(((kk >> 2) * kRows * 128 + off) >> 4),
-                                    kb_d + (uint64_t)(((kk >> 2) * kKeys * 128 + off) >> 4), id_qk, kk > 0);
-                    }
-                    tc::mma_commit(smem_addr(&s_full[2 * gr + (tp & 1u)]));
-                    tc::mma_commit(smem_addr(&k_empty[slot]));
-                    if (t == it.t1 - 1) tc::mma_commit(smem_addr(q_empty));
-                    if (t > it.t0) issue_pv(kt - 1);
-                    ++tp;
-                }
-                if (ok) issue_pv(kt - 1);
             }
-            // every MMA this thread issued has completed before the columns are freed
+            __syncwarp();
+        };
+        while (ok && __all_sync(kFull, next_task()) && reach(q_full, nt & 1u)) {
+            if (it.first + gr * QT >= it.n) {                // no rows: only give the buffers back
+                if (lane == 0) mbar_arrive(smem_addr(q_empty));
+#pragma unroll 1
+                for (int t = it.t0; t < it.t1; ++t, ++kt) {
+                    if (!reach(&k_full[kt % NK], (kt / NK) & 1u)) break;
+                    if (lane == 0) mbar_arrive(smem_addr(&k_empty[kt % NK]));
+                    if (!reach(&v_full[kt % NV], (kt / NV) & 1u)) break;
+                    if (lane == 0) mbar_arrive(smem_addr(&v_empty[kt % NV]));
+                }
+            } else {
+#pragma unroll 1
+                for (int t = it.t0; t <= it.t1; ++t) {
+                    if (t < it.t1) {
+                        const uint32_t slot = kt % NK;
+                        if (!reach(&k_full[slot], (kt / NK) & 1u)) break;
+                        tc::fence_after_sync();
+                        const uint64_t kb_d = tc::desc_sw128(smem_addr(smem + LY::kKRing + slot * LY::kTileBytes), 16, 1024);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t off = (kk & 3) * 32;          // 16 values inside the row
+                                tc::mma_f16(t_s + 64 * (tp & 1u),
+                                            qa_d + (uint64_t)(((kk >> 2) * kRows * 128 + off) >> 4),
+                                            kb_d + (uint64_t)(((kk >> 2) * kKeys * 128 + off) >> 4), id_qk, kk > 0);
+                            }
+                            tc::mma_commit(smem_addr(&s_full[2 * gr + (tp & 1u)]));
+                            tc::mma_commit(smem_addr(&k_empty[slot]));
+                            if (t == it.t1 - 1) tc::mma_commit(smem_addr(q_empty));
+                        }
+                        __syncwarp();
+                    }
+                    if (t > it.t0) issue_pv(kt - 1);
+                    if (!ok) break;
+                    if (t < it.t1) {
+                        ++tp;
+                        ++kt;
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&task_empty[nt % kTasks]));
+            ++nt;
+        }
+        // every MMA this warp issued has completed before the columns are freed
+        if (elect_one()) {
             tc::mma_commit(smem_addr(&done[gr]));
             const unsigned long long t0 = globaltimer();
             while (!mbar_try_wait(smem_addr(&done[gr]), 0)) {
@@ -662,6 +719,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                 }
             }
         }
+        __syncwarp();
     } else if (warp == LY::kCleaner) {
         uint32_t vt = 0;
         bool ok = true;
@@ -681,7 +739,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                     };
                     const int e0 = max(it.base - k0, 0) * kChunks, e1 = min(it.L() - k0, kKeys) * kChunks;
                     uint32_t sum[4] = {0u, 0u, 0u, 0u}, odd[2] = {0u, 0u};
-#pragma unroll 4
+#pragma unroll 2
                     for (int e = e0 + lane; e < e1; e += 32) {
                         const uint4 w = chunk(e);
                         add_odd<BF16>(sum[0], w.x);
@@ -689,7 +747,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                         add_odd<BF16>(sum[2], w.z);
                         add_odd<BF16>(sum[3], w.w);
                     }
-#pragma unroll 4
+#pragma unroll 1
                     for (int e = e1 + lane; e < kKeys * kChunks; e += 32) chunk(e) = make_uint4(0u, 0u, 0u, 0u);
                     if (__any_sync(kFull, odd_halves<BF16>(sum[0]) | odd_halves<BF16>(sum[1]) |
                                               odd_halves<BF16>(sum[2]) | odd_halves<BF16>(sum[3]))) {
@@ -732,7 +790,9 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
             if (lane == 0) mbar_arrive(smem_addr(&task_empty[nt % kTasks]));
             ++nt;
         };
-        while (alive && __all_sync(kFull, next_task())) {
+        while (alive && __all_sync(kFull, mbar_wait(smem_addr(&task_full[nt % kTasks]), (nt / kTasks) & 1u, abort_flag, p.status))) {
+            it = tasks[nt % kTasks];
+            if (it.t0 >= it.t1) break;
             const int n = it.n, base = it.base, L = it.L();
             const int token = it.first + gr * QT + jj;
             if (it.first + gr * QT >= n) {               // no rows in this query tile
@@ -994,7 +1054,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const Params p)
     const int begin = found[0], end = found[1];
     if (begin < 0 || end < 0) return;
     const int4 what = p.ranges[begin];
-    const Seq q = seq_of<NG>(p, what.y);
+    const Seq q = seq_of(p, what.y);
     const int g = what.z / q.sets, first = (what.z - g * q.sets) * NG * p.tile_tokens;
     const int G = p.group, pieces = end - begin + 1;
     auto piece = [&](int k) -> int64_t { return k == 0 ? 2 * begin + 1 : 2 * (begin + k); };
@@ -1213,6 +1273,8 @@ extern "C" int paged_tree_attention(const pkv_pool *pool, void *out, const void 
     prm.num_blocks = g.num_blocks;
     prm.tile_tokens = tile_tokens(G);
     prm.box_tokens = box_tokens(G);
+    prm.set_tokens = (two ? 2 : 1) * prm.tile_tokens;
+    prm.set_inverse = ((1 << 20) + prm.set_tokens - 1) / prm.set_tokens;
     prm.piece_rows = two ? 2 * kRows : (int32_t)piece_rows(num_tokens, G);
     // scores are hidden by an infinity that the scale must carry into the exponent; at scale 0
     // the smallest normal number weighs all keys alike
