@@ -67,16 +67,16 @@ struct Params {
     int32_t set_tokens, set_inverse;   // of NG query tiles; ceil(2^20 / that)
     int32_t piece_rows;                // rows of a piece's place in the workspace
     float scale_log2;
-    int32_t *header;                   // [0] = ranges
-    int4 *ranges;                      // see Range
+    int32_t grid;                      // CTAs of the call
+    int4 *ranges;                      // [grid], see kContinues
     float2 *part_ml;                   // [2 ranges][piece_rows]: (reference, sum); sum < 0: bad block
     float4 *part_o;                    // [2 ranges][D / 4][piece_rows]
     int32_t *status;
 };
 
-// What a range's CTA leaves for the joining kernel: x = 1 it holds the continuation of an item
-// that began in an earlier range (piece 2 b), + 2 up to the item's end, + 4 it begins an item that
-// ends in a later range (piece 2 b + 1): sequence y, item z.
+// What CTA b leaves for the joining kernel: x = 1 it holds the continuation of an item that began
+// in an earlier range (piece 2 b), + 2 up to the item's end, + 4 it begins an item that ends in a
+// later range (piece 2 b + 1), of y tokens from row z on, kv head w.
 constexpr int kContinues = 1, kEnds = 2, kBegins = 4;
 
 // One sequence of a call.
@@ -112,81 +112,12 @@ struct Place {
     int s, it, t;
 };
 
-// A CTA's range.
-struct Plan {
-    Place from, to;
-    int ranges;
-};
-
 // An item's part in a range: tiles [t0, t1) of kv head g and the query tiles from token `first`
 // on, of sequence s.  t0 == t1: there are no more.
 struct alignas(16) Task {
     int s, g, first, t0, t1;
     int r0, n, base;                   // the sequence's rows, drafted tokens and tokens before them
     __device__ __forceinline__ int L() const { return base + n; }
-};
-
-// Goes through a range's items; the producer's warp does it for the CTA.  Lane i holds the
-// lengths of sequence `held` + i.
-struct Walk {
-    Place at;
-    Seq q;                             // sequence at.s
-    int g, set;                        // item at.it
-    int held, r0, r1, L;
-    __device__ __forceinline__ Walk(const Params &p, const Plan &plan) : at(plan.from)
-    {
-        hold(p, at.s);
-        q = sequence(p);
-        g = q.sets ? at.it / q.sets : 0;
-        set = at.it - g * q.sets;
-    }
-    __device__ __forceinline__ void hold(const Params &p, int s)
-    {
-        held = s;
-        const int i = s + (int)(threadIdx.x & 31);
-        r0 = i < p.num_seqs ? p.query_start[i] : 0;
-        r1 = i < p.num_seqs ? p.query_start[i + 1] : 0;
-        L = i < p.num_seqs ? p.context_lens[i] : 0;
-    }
-    __device__ __forceinline__ Seq sequence(const Params &p) const
-    {
-        const int i = at.s - held;
-        return seq_of(p, __shfl_sync(kFull, r0, i), __shfl_sync(kFull, r1, i), __shfl_sync(kFull, L, i));
-    }
-    __device__ __forceinline__ Task next(const Params &p, const Plan &plan)
-    {
-        Task k = {};
-        while (at.s < p.num_seqs && at.s <= plan.to.s) {
-            const bool last = at.s == plan.to.s;
-            if (g < p.num_kv_heads && q.sets > 0 && (!last || at.it <= plan.to.it)) {
-                const int t1 = last && at.it == plan.to.it ? plan.to.t : q.tiles;
-                const int t0 = at.t;
-                k.s = at.s;
-                k.g = g;
-                k.first = set * p.set_tokens;
-                k.r0 = q.r0;
-                k.n = q.n;
-                k.base = q.base;
-                ++at.it;
-                at.t = 0;
-                if (++set == q.sets) {
-                    set = 0;
-                    ++g;
-                }
-                if (t0 < t1) {
-                    k.t0 = t0;
-                    k.t1 = t1;
-                    return k;
-                }
-            } else {
-                ++at.s;
-                at.it = at.t = g = set = 0;
-                if (at.s >= held + 32) hold(p, at.s);
-                q = sequence(p);
-            }
-        }
-        return k;
-    }
 };
 
 // floor(a / b) for 0 <= a, 0 < b, by an estimate in fp32 that is then put right.
@@ -217,68 +148,135 @@ __device__ __forceinline__ Place cut(const Params &p, int s, const Seq &q, int64
     return c;
 }
 
-// The ranges, by the whole CTA: units of all sequences are counted (a slice of them to a
-// thread), and the two ends of this CTA's range looked up.  CTA s % gridDim also reports and
-// clears sequences whose lengths do not fit.
-template <int NG, int D, int THREADS>
-__device__ __forceinline__ void make_plan(const Params &p, Plan *plan, int64_t *warp_sum)
-{
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int slice = (p.num_seqs + THREADS - 1) / THREADS;
-    const int s0 = min(tid * slice, p.num_seqs), s1 = min(s0 + slice, p.num_seqs);
-    int64_t mine = 0;
-    for (int s = s0; s < s1; ++s) {
-        const Seq q = seq_of(p, s);
-        mine += (int64_t)q.items(p) * (q.tiles + kItemCost);
-        if (q.bad && s % gridDim.x == blockIdx.x) {
-            atomicOr(p.status, PKV_DEV_BAD_LEN);
-            uint4 *o = static_cast<uint4 *>(p.out) + (int64_t)q.r0 * p.num_q_heads * (D / 8);
-            for (int64_t i = 0; i < (int64_t)q.n * p.num_q_heads * (D / 8); ++i) o[i] = make_uint4(0, 0, 0, 0);
-        }
+// A CTA's range and the way through its items; the producer's warp makes it and goes it for the
+// CTA.  Lane i holds the lengths of sequence `held` + i.
+struct Walk {
+    Place at, to;
+    int ranges;
+    Seq q;                             // sequence at.s
+    int g, set;                        // item at.it
+    int held, r0, r1, L;
+
+    __device__ __forceinline__ void hold(const Params &p, int s)
+    {
+        held = s;
+        const int i = s + (int)(threadIdx.x & 31);
+        r0 = i < p.num_seqs ? p.query_start[i] : 0;
+        r1 = i < p.num_seqs ? p.query_start[i + 1] : 0;
+        L = i < p.num_seqs ? p.context_lens[i] : 0;
     }
-    int64_t upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(kFull, upto, o);
-        if (lane >= o) upto += y;
+    __device__ __forceinline__ void at_sequence(const Params &p)
+    {
+        const int i = at.s - held;
+        q = seq_of(p, __shfl_sync(kFull, r0, i), __shfl_sync(kFull, r1, i), __shfl_sync(kFull, L, i));
     }
-    if (lane == 31) warp_sum[warp] = upto;
-    __syncthreads();
-    int64_t before = upto - mine, all = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) before += warp_sum[w];
-        all += warp_sum[w];
-    }
-    const int ranges = (int)max((int64_t)1, min((int64_t)gridDim.x, all / kMinRange));
-    // the first `more` ranges have a unit more
-    const int64_t size = quotient(all, ranges), more = all - size * ranges;
-    const int snap = (int)min((int64_t)kSnap, size / 4);
-    const int64_t begin = size * blockIdx.x + min((int64_t)blockIdx.x, more);
-    const int64_t ends[2] = {begin, begin + size + (blockIdx.x < more)};
-    if (tid == 0) {
-        plan->ranges = ranges;
-        plan->from = plan->to = Place{p.num_seqs, 0, 0};
-    }
-    __syncthreads();
-    if (blockIdx.x < ranges) {
+
+    // The ranges: the units of all sequences are counted, and the two ends of this CTA's range
+    // looked up.  CTA s % gridDim also reports and clears sequences whose lengths do not fit.
+    template <int D>
+    __device__ __forceinline__ void plan(const Params &p)
+    {
+        const int lane = threadIdx.x & 31;
+        auto units_of = [&](const Seq &x) { return (int64_t)x.items(p) * (x.tiles + kItemCost); };
+        int64_t all = 0;
 #pragma unroll 1
-        for (int e = 0; e < 2; ++e) {
-            int64_t off = (e ? ends[1] : ends[0]) - before;
-            if (off < 0 || off >= mine) continue;
-            for (int s = s0; s < s1; ++s) {
-                const Seq q = seq_of(p, s);
-                const int64_t units = (int64_t)q.items(p) * (q.tiles + kItemCost);
-                if (off < units) {
-                    (e ? plan->to : plan->from) = cut(p, s, q, off, snap);
-                    break;
-                }
-                off -= units;
+        for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+            hold(p, s0);
+            const Seq x = seq_of(p, r0, r1, L);
+            all += units_of(x);
+            if (x.bad && (s0 + lane) % gridDim.x == blockIdx.x) {
+                atomicOr(p.status, PKV_DEV_BAD_LEN);
+                uint4 *o = static_cast<uint4 *>(p.out) + (int64_t)x.r0 * p.num_q_heads * (D / 8);
+                for (int64_t i = 0; i < (int64_t)x.n * p.num_q_heads * (D / 8); ++i) o[i] = make_uint4(0, 0, 0, 0);
             }
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
+        ranges = (int)max((int64_t)1, min((int64_t)gridDim.x, all / kMinRange));
+        // the first `more` ranges have a unit more
+        const int64_t size = quotient(all, ranges), more = all - size * ranges;
+        const int snap = (int)min((int64_t)kSnap, size / 4);
+        const int64_t begin = size * blockIdx.x + min((int64_t)blockIdx.x, more);
+        const int64_t end = begin + size + (blockIdx.x < more);
+        at = to = Place{p.num_seqs, 0, 0};
+        int4 left = make_int4(0, 0, 0, 0);               // for the joining kernel
+        int64_t before = 0;
+#pragma unroll 1
+        for (int s0 = 0; s0 < p.num_seqs && blockIdx.x < ranges && before <= end; s0 += 32) {
+            if (s0 != held) hold(p, s0);
+            const Seq x = seq_of(p, r0, r1, L);
+            const int64_t units = units_of(x);
+            int64_t upto = units;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(kFull, upto, o);
+                if (lane >= o) upto += y;
+            }
+#pragma unroll 1
+            for (int e = 0; e < 2; ++e) {
+                const int64_t off = (e ? end : begin) - before - (upto - units);
+                const bool here = off >= 0 && off < units;
+                Place c = {0, 0, 0};
+                if (here) c = cut(p, s0 + lane, x, off, snap);
+                const unsigned who = __ballot_sync(kFull, here);
+                if (!who) continue;
+                const int src = __ffs(who) - 1;
+                c = {__shfl_sync(kFull, c.s, src), __shfl_sync(kFull, c.it, src), __shfl_sync(kFull, c.t, src)};
+                if (!e) {
+                    at = c;
+                    continue;
+                }
+                to = c;
+                const int n = __shfl_sync(kFull, x.n, src), sets = __shfl_sync(kFull, x.sets, src);
+                const int head = c.it / sets, first = (c.it - head * sets) * p.set_tokens;
+                left = make_int4(0, min(p.set_tokens, n - first), __shfl_sync(kFull, x.r0, src) + first, head);
+            }
+            before += __shfl_sync(kFull, upto, 31);
+        }
+        const bool same = at.s == to.s && at.it == to.it;
+        if (at.t > 0) left.x |= kContinues | (same ? 0 : kEnds);
+        if (to.t > 0 && !(same && at.t > 0)) left.x |= kBegins;
+        if (lane == 0) p.ranges[blockIdx.x] = left;
+        if (at.s < held || at.s >= held + 32) hold(p, at.s);
+        at_sequence(p);
+        g = q.sets > 1 ? at.it / q.sets : at.it;
+        set = at.it - g * q.sets;
     }
-    __syncthreads();
-}
+    __device__ __forceinline__ Task next(const Params &p)
+    {
+        Task k = {};
+        while (at.s < p.num_seqs && at.s <= to.s) {
+            const bool last = at.s == to.s;
+            if (g < p.num_kv_heads && q.sets > 0 && (!last || at.it <= to.it)) {
+                const int t1 = last && at.it == to.it ? to.t : q.tiles;
+                const int t0 = at.t;
+                k.s = at.s;
+                k.g = g;
+                k.first = set * p.set_tokens;
+                k.r0 = q.r0;
+                k.n = q.n;
+                k.base = q.base;
+                ++at.it;
+                at.t = 0;
+                if (++set == q.sets) {
+                    set = 0;
+                    ++g;
+                }
+                if (t0 < t1) {
+                    k.t0 = t0;
+                    k.t1 = t1;
+                    return k;
+                }
+            } else {
+                ++at.s;
+                at.it = at.t = g = set = 0;
+                if (at.s >= held + 32) hold(p, at.s);
+                at_sequence(p);
+            }
+        }
+        return k;
+    }
+};
 
 __device__ __forceinline__ float max3f(float a, float b, float c)
 {
@@ -426,17 +424,14 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
     uint64_t *done = o_full + 2 * NG;                          // [NG]
     uint64_t *task_full = done + NG, *task_empty = task_full + kTasks;
     uint64_t *odd_keys = task_empty + kTasks;                            // [NV]: keys whose V held odd values
-    int64_t *sums = reinterpret_cast<int64_t *>(odd_keys + NV);         // [warps], see make_plan
-    Plan &plan = *reinterpret_cast<Plan *>(sums + LY::kWarps);
     // tile's bad blocks: a K tile's slot is free once S is out, before the softmax reads this, so
     // these have places of their own, more than there are tiles under way
-    uint8_t *bad_blocks = reinterpret_cast<uint8_t *>(&plan + 1);       // [kTilesKnown]
+    uint8_t *bad_blocks = reinterpret_cast<uint8_t *>(odd_keys + NV);   // [kTilesKnown]
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bad_blocks + kTilesKnown);
     volatile int *abort_flag = reinterpret_cast<int *>(tslot + 1);
     Task *tasks = reinterpret_cast<Task *>(smem + LY::kTotal) - kTasks;
-    static_assert((2 + 2 * NK + 4 * NV + 7 * NG + 2 * kTasks + LY::kWarps) * 8 + sizeof(Plan) + kTilesKnown + 8 +
-                          kTasks * sizeof(Task) <= LY::kMiscBytes &&
-                      NK + 3 <= kTilesKnown && NV + 3 <= kTilesKnown && sizeof(Plan) % 4 == 0,
+    static_assert((2 + 2 * NK + 4 * NV + 7 * NG + 2 * kTasks) * 8 + kTilesKnown + 8 + kTasks * sizeof(Task) <=
+                          LY::kMiscBytes && NK + 3 <= kTilesKnown && NV + 3 <= kTilesKnown,
                   "barriers and flags");
 
     if (smem_addr(smem) & 1023u) {       // the swizzle's atoms; no launch has been seen to do this
@@ -482,16 +477,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
     // of this one
     griddep_launch_dependents();
     griddep_wait();
-    make_plan<NG, D, LY::kThreads>(p, &plan, sums);
     const int Hkv = p.num_kv_heads, G = p.group, QT = p.tile_tokens;
-    if (threadIdx.x == 0 && blockIdx.x < plan.ranges) {
-        const bool same = plan.from.s == plan.to.s && plan.from.it == plan.to.it;
-        int4 r = make_int4(0, plan.to.s, plan.to.it, 0);
-        if (plan.from.t > 0) r.x |= kContinues | (same ? 0 : kEnds);
-        if (plan.to.t > 0 && !(same && plan.from.t > 0)) r.x |= kBegins;
-        p.ranges[blockIdx.x] = r;
-        if (blockIdx.x == 0) p.header[0] = plan.ranges;
-    }
 
     // (the register split is taken inside each role's branch, so that all of a role's code
     // lies under one limit)
@@ -508,7 +494,8 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
     if (warp == LY::kProducer) {
         uint32_t kt = 0, vt = 0, items = 0;      // K tiles, V tiles and items under way or done
         bool ok = true;
-        Walk walk(p, plan);
+        Walk walk;
+        walk.plan<D>(p);
         // 32 block ids, 8 tiles, at a time, one batch ahead; behind the end any block will do
         auto ids_from = [&](const Task &k, int t) {
             const int b = 4 * t + lane;
@@ -522,21 +509,10 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                         box(gr * LY::kQBytes + rg * kRows * 128 + i * G * 128, rg * 64, k.g,
                             k.r0 + k.first + gr * QT + i);
         };
-        Task after = {};
-        int ids_after = 0;
-        // the item after `it`: its first block ids, its query rows into L2
-        for (bool begun = false;; begun = true) {
+        Task after = walk.next(p);
+        int ids_after = after.t0 < after.t1 ? ids_from(after, after.t0) : 0;
+        for (;;) {
             it = after;
-            after = walk.next(p, plan);
-            const int ids_now = ids_after;
-            if (after.t0 < after.t1) {
-                ids_after = ids_from(after, after.t0);
-                if (begun && elect_one())
-                    each_box(after, [&](int, int x, int g, int token) {
-                        tc::tma_prefetch_4d(&tmQ, x, 0, g, token);
-                    });
-            }
-            if (!begun) continue;
             if (nt >= kTasks)
                 ok = mbar_wait(smem_addr(&task_empty[nt % kTasks]), (nt / kTasks - 1) & 1u, abort_flag, p.status);
             ok = __all_sync(kFull, ok);
@@ -547,7 +523,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
             }
             ++nt;
             if (it.t0 >= it.t1) break;
-            int ids = ids_now, ids_next = ids_from(it, it.t0 + 8);
+            int ids = ids_after, ids_next = ids_from(it, it.t0 + 8);
             // the first row of the four blocks of tile t in the pools; all lanes call it
             auto rows_of = [&](int t, int (&y)[4]) {
                 bool bad = false;
@@ -618,6 +594,17 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                 }
 #pragma unroll
                 for (int b = 0; b < 4; ++b) y_v[b] = y[b];
+                if (t == min(it.t0 + 1, it.t1)) {
+                    // the item after this one: its first block ids, its query rows into L2
+                    after = walk.next(p);
+                    if (after.t0 < after.t1) {
+                        ids_after = ids_from(after, after.t0);
+                        if (elect_one())
+                            each_box(after, [&](int, int x, int g, int token) {
+                                tc::tma_prefetch_4d(&tmQ, x, 0, g, token);
+                            });
+                    }
+                }
             }
             if (!ok) break;
         }
@@ -1013,87 +1000,88 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
 
 // ------------------------------------------------------------------ joining the pieces
 // A row of CTAs per cut item (the x-th range that begins one it does not end); a warp takes
-// 32 rows and 8 columns.
+// 32 rows and 8 columns, the pieces in their order, four under way at a time.
 constexpr int kJoinThreads = 256;
 
-template <int D, bool BF16, int NG>
+template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const Params p)
 {
     using E = Elem<BF16>;
     using T = typename E::T;
-    __shared__ int kinds[kMaxRanges], found[2];
+    __shared__ int4 ranges[kMaxRanges];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     griddep_launch_dependents();
     griddep_wait();
-    const int ranges = min(p.header[0], kMaxRanges);
-    for (int i = tid; i < ranges; i += kJoinThreads) kinds[i] = p.ranges[i].x;
+#pragma unroll
+    for (int i = tid; i < kMaxRanges; i += kJoinThreads)
+        if (i < p.grid) ranges[i] = p.ranges[i];
     __syncthreads();
-    if (warp == 0) {
-        int begin = -1, end = -1, left = blockIdx.x;
-        for (int i0 = 0; i0 < ranges && end < 0; i0 += 32) {
-            const int kind = i0 + lane < ranges ? kinds[i0 + lane] : 0;
-            unsigned ends = __ballot_sync(kFull, kind & kEnds);
-            if (begin < 0) {
-                unsigned begins = __ballot_sync(kFull, kind & kBegins);
-                if (__popc(begins) <= left) {
-                    left -= __popc(begins);
-                    continue;
-                }
-                for (; left > 0; --left) begins &= begins - 1;
-                begin = i0 + __ffs(begins) - 1;
-                ends &= ~((2u << (begin - i0)) - 1u);
+    int begin = -1, end = -1, left = blockIdx.x;         // (every warp for itself)
+    for (int i0 = 0; i0 < p.grid && end < 0; i0 += 32) {
+        const int kind = i0 + lane < p.grid ? ranges[i0 + lane].x : 0;
+        unsigned ends = __ballot_sync(kFull, kind & kEnds);
+        if (begin < 0) {
+            unsigned begins = __ballot_sync(kFull, kind & kBegins);
+            if (__popc(begins) <= left) {
+                left -= __popc(begins);
+                continue;
             }
-            if (ends) end = i0 + __ffs(ends) - 1;
+            for (; left > 0; --left) begins &= begins - 1;
+            begin = i0 + __ffs(begins) - 1;
+            ends &= ~((2u << (begin - i0)) - 1u);
         }
-        if (lane == 0) {
-            found[0] = begin;
-            found[1] = end;
-        }
+        if (ends) end = i0 + __ffs(ends) - 1;
     }
-    __syncthreads();
-    const int begin = found[0], end = found[1];
     if (begin < 0 || end < 0) return;
-    const int4 what = p.ranges[begin];
-    const Seq q = seq_of(p, what.y);
-    const int g = what.z / q.sets, first = (what.z - g * q.sets) * NG * p.tile_tokens;
-    const int G = p.group, pieces = end - begin + 1;
-    auto piece = [&](int k) -> int64_t { return k == 0 ? 2 * begin + 1 : 2 * (begin + k); };
+    const int tokens = ranges[begin].y, r0 = ranges[begin].z, g = ranges[begin].w;
+    const int G = p.group, QT = p.tile_tokens, pieces = end - begin + 1;
     // rows that count: those of full query tiles before the last one's
-    const int tokens = min(NG * p.tile_tokens, q.n - first);
-    const int tiles = (tokens + p.tile_tokens - 1) / p.tile_tokens;
-    const int rows = (tiles - 1) * kRows + (tokens - (tiles - 1) * p.tile_tokens) * G;
+    const int before = (tokens - 1) / QT;
+    const int rows = before * kRows + (tokens - before * QT) * G;
     const int tasks = (rows + 31) / 32 * (D / 8);
+    const float sc = p.scale_log2, hide = sc < 0.f ? INFINITY : -INFINITY;
     for (int task = blockIdx.y * (kJoinThreads / 32) + warp; task < tasks; task += gridDim.y * (kJoinThreads / 32)) {
         const int rr = task / (D / 8) * 32 + lane, c8 = task % (D / 8);
         const int gr = rr / kRows, jj = (rr - gr * kRows) / G, h = rr - gr * kRows - jj * G;
-        const int token = first + gr * p.tile_tokens + jj;
-        if (jj >= p.tile_tokens || token >= q.n) continue;
-        float m = p.scale_log2 < 0.f ? INFINITY : -INFINITY;
+        const int token = gr * QT + jj;
+        if (jj >= QT || token >= tokens) continue;
+        float ref = hide, l = 0.f, o[8] = {};
         bool bad = false;
-#pragma unroll 4
-        for (int k = 0; k < pieces; ++k) {
-            const float2 ml = p.part_ml[piece(k) * p.piece_rows + rr];
-            if (ml.y != 0.f) m = p.scale_log2 < 0.f ? fminf(m, ml.x) : fmaxf(m, ml.x);   // (0: it saw nothing)
+        auto add = [&](float2 ml, float4 a, float4 b) {
             bad |= ml.y < 0.f;
-        }
-        float l = 0.f, o[8] = {};
-#pragma unroll 4
-        for (int k = 0; k < pieces; ++k) {
-            const int64_t at = piece(k);
-            const float2 ml = p.part_ml[at * p.piece_rows + rr];
-            const float w = ml.y == 0.f ? 0.f : fast_exp2((ml.x - m) * p.scale_log2);
-            const float4 *src = p.part_o + (at * (D / 4) + 2 * c8) * p.piece_rows + rr;
-            const float4 a = src[0], b = src[p.piece_rows];
-            l += w * ml.y;
+            if (ml.y == 0.f) return;                     // nothing seen there
+            const float now = sc < 0.f ? fminf(ref, ml.x) : fmaxf(ref, ml.x);
+            const float f = ref == hide ? 0.f : fast_exp2((ref - now) * sc);
+            const float w = fast_exp2((ml.x - now) * sc);
             const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            ref = now;
+            l = l * f + w * ml.y;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] += w * v[e];
+            for (int e = 0; e < 8; ++e) o[e] = o[e] * f + w * v[e];
+        };
+        const float2 *ml_at = p.part_ml + rr;
+        const float4 *o_at = p.part_o + (int64_t)2 * c8 * p.piece_rows + rr;
+        for (int k0 = 0; k0 < pieces; k0 += 4) {
+            float2 ml[4];
+            float4 a[4], b[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k0 + k >= pieces) break;
+                const int64_t piece = k0 + k == 0 ? 2 * begin + 1 : 2 * (begin + k0 + k);
+                const float4 *src = o_at + piece * (D / 4) * p.piece_rows;
+                ml[k] = ml_at[piece * p.piece_rows];
+                a[k] = src[0];
+                b[k] = src[p.piece_rows];
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k0 + k < pieces) add(ml[k], a[k], b[k]);
         }
         const bool none = bad || l == 0.f;
         const float inv = none ? 0.f : 1.f / l;
         auto two_of = [&](int k) { return none ? 0u : E::pack(o[k] * inv, o[k + 1] * inv); };
         T *out = static_cast<T *>(p.out) +
-                 ((int64_t)(q.r0 + token) * p.num_q_heads + (int64_t)g * G + h) * D + 8 * c8;
+                 ((int64_t)(r0 + token) * p.num_q_heads + (int64_t)g * G + h) * D + 8 * c8;
         *reinterpret_cast<uint4 *>(out) = make_uint4(two_of(0), two_of(2), two_of(4), two_of(6));
     }
 }
@@ -1149,7 +1137,7 @@ static Workspace workspace_of(int64_t T, int G, int D)
 {
     const size_t rows = 2 * kMaxRanges * (size_t)piece_rows(T, G);
     Workspace w;
-    w.ranges = 256;
+    w.ranges = 0;
     w.ml = w.ranges + align256(kMaxRanges * sizeof(int4));
     w.o = w.ml + align256(rows * sizeof(float2));
     w.total = w.o + rows * D * sizeof(float);
@@ -1168,7 +1156,7 @@ struct Pick {
 template <int D, bool BF16, int NG>
 static Pick pick_of()
 {
-    return {&tree_kernel<D, BF16, NG>, &tree_join_kernel<D, BF16, NG>, Layout<D, NG>::kTotal,
+    return {&tree_kernel<D, BF16, NG>, &tree_join_kernel<D, BF16>, Layout<D, NG>::kTotal,
             Layout<D, NG>::kThreads, NG == 1 ? 2 : 1, Layout<D, NG>::kLaunchRegs};
 }
 
@@ -1280,7 +1268,6 @@ extern "C" int paged_tree_attention(const pkv_pool *pool, void *out, const void 
     // the smallest normal number weighs all keys alike
     prm.scale_log2 = scale == 0.f ? 0x1p-126f : scale * 1.4426950408889634f;
     char *w = static_cast<char *>(workspace);
-    prm.header = reinterpret_cast<int32_t *>(w);
     prm.ranges = reinterpret_cast<int4 *>(w + ws.ranges);
     prm.part_ml = reinterpret_cast<float2 *>(w + ws.ml);
     prm.part_o = reinterpret_cast<float4 *>(w + ws.o);
@@ -1304,7 +1291,8 @@ extern "C" int paged_tree_attention(const pkv_pool *pool, void *out, const void 
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min(fit, two ? kMaxRanges / 2 : kMaxRanges));
+    prm.grid = std::min(fit, two ? kMaxRanges / 2 : kMaxRanges);
+    cfg.gridDim = dim3((unsigned)prm.grid);
     cfg.blockDim = dim3((unsigned)k.threads);
     cfg.dynamicSmemBytes = (size_t)k.smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
