@@ -101,19 +101,35 @@ struct Moves {
     const int32_t *block_tables, *kept, *kept_start, *num_kept, *first;
     int32_t max_blocks_per_seq, num_entries, num_kv_heads, block_size, num_blocks;
     int32_t chunks;                      // 16-byte chunks of a row
-    int32_t parts, part_chunks;          // CTAs that share a row, chunks of each
+    int32_t part_chunks, parts;          // of them a CTA's, and CTAs that share a row
+    int32_t pairs;                       // (kv head, K or V) of a CTA
+    int32_t batch;                       // tokens of a batch
     uint4 *k_pool, *v_pool;
     int32_t *status;
 };
 
-constexpr int kMoveThreads = 256, kMoveDepth = 8;
-
-// A CTA takes a sequence, a kv head, K or V, and a share of each row; nothing else reads or
-// writes these bytes.  It goes through the kept tokens in order, a batch at a time: all of
-// the batch's rows are read, then written.  A destination is never above its source and
+// A CTA takes a sequence, some of its (kv head, K or V) pairs, and a share of each row; nothing
+// else reads or writes these bytes.  It goes through the kept tokens in order, a batch at a time:
+// all of the batch's rows are read, then written.  A destination is never above its source and
 // sources rise, so what a batch writes is no source of a later one.
-__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const Moves p)
+// The chain list -> table -> row -> store bounds it, and how many rows are under way at
+// once: places are looked up once for a CTA and a batch ahead of the rows, the list is read two
+// ahead.  Nine caches of up to 16,384 tokens that keep 40,000 in all (305 MB moved): 68 us,
+// 4.5 TB/s (floor 45; the longest list's 8,000 tokens set the end); 155 us with whole rows to a
+// CTA (64 bytes here, so that few sequences fill the GPU), 280 before places were looked up ahead.
+constexpr int kMoveThreads = 256, kMoveDepth = 8, kMoveBatch = 512;
+constexpr int kMoveCtas = 608;           // four to an SM
+
+struct Place {
+    int64_t from, to;                    // token rows of kv head 0 in the pool, -1: does not move
+};
+
+__global__ void __launch_bounds__(kMoveThreads, 3) compact_kernel(const Moves p)
 {
+    // of three batches: a thread may look up the one after the next while another still writes
+    // this one's rows
+    __shared__ Place places[3][kMoveBatch];
+    __shared__ int stops[3];             // first entry that may not move, n: none
     griddep_launch_dependents();
     griddep_wait();
     const int s = blockIdx.y, tid = threadIdx.x;
@@ -122,58 +138,83 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const Moves p)
         if (blockIdx.x == 0 && tid == 0) atomicOr(p.status, PKV_DEV_BAD_LEN);
         return;
     }
-    const int part = blockIdx.x % p.parts, rest = blockIdx.x / p.parts;
-    const int g = rest >> 1;
-    uint4 *pool = rest & 1 ? p.v_pool : p.k_pool;
+    const int part = blockIdx.x % p.parts, pair0 = blockIdx.x / p.parts * p.pairs;
+    const int pairs = min(p.pairs, 2 * p.num_kv_heads - pair0);
     const int c0 = part * p.part_chunks, nc = min(p.part_chunks, p.chunks - c0);
-    if (nc <= 0) return;
-    const int per_pass = kMoveThreads / nc;              // tokens of one pass of the threads
+    const int per_pass = kMoveThreads / nc;              // rows of one pass of the threads
     const int c = tid % nc, k = tid / nc;
     const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
     const int32_t *kept = p.kept + start;
     const int64_t limit = (int64_t)p.max_blocks_per_seq * p.block_size;
-    auto place = [&](int pos) -> int64_t {               // chunk index in the pool, -1: bad block
+    auto place = [&](int pos) -> int64_t {
         const int id = row[pos / p.block_size];
-        if (id < 0 || id >= p.num_blocks) return -1;
-        return (((int64_t)id * p.num_kv_heads + g) * p.block_size + pos % p.block_size) * p.chunks + c0 + c;
+        return id < 0 || id >= p.num_blocks ? -1 : (int64_t)id * p.num_kv_heads * p.block_size + pos % p.block_size;
     };
-    bool ok = true;
-    for (int i0 = 0; i0 < n && ok; i0 += per_pass * kMoveDepth) {
-        uint4 v[kMoveDepth];
-        int64_t to[kMoveDepth];
-        int stop = n;                                    // first entry that may not move
-        bool lost = false;
+    // The list runs two batches ahead of the rows, the places one: `fetch` takes a thread's entries
+    // of the batch from i0 on, `look_up` finds their places.
+    constexpr int kEntries = kMoveBatch / kMoveThreads;
+    int pos[kEntries], before[kEntries];
+    auto fetch = [&](int i0) {
 #pragma unroll
-        for (int d = 0; d < kMoveDepth; ++d) {
-            const int i = i0 + d * per_pass + k;
-            to[d] = -1;
-            if (k >= per_pass || i >= n) continue;
-            const int pos = kept[i];
-            const int64_t dst = (int64_t)first + i;
-            if (pos < dst || (i > 0 && kept[i - 1] >= pos) || pos >= limit) {
-                stop = min(stop, i);
-                continue;
-            }
-            if (pos == dst) continue;
-            const int64_t from = place(pos), there = place((int)dst);
-            lost |= from < 0 || there < 0;
-            if (from < 0 || there < 0) continue;
-            v[d] = pool[from];
-            to[d] = there;
+        for (int j = 0; j < kEntries; ++j) {
+            const int e = j * kMoveThreads + tid, i = i0 + e;
+            const bool mine = e < p.batch && i < n;
+            pos[j] = mine ? kept[i] : 0;
+            before[j] = mine && i > 0 ? kept[i - 1] : -1;
         }
-        __shared__ int stops;
-        if (tid == 0) stops = n;
-        __syncthreads();
-        if (stop < n) atomicMin(&stops, stop);
-        if (lost && blockIdx.x == 0) atomicOr(p.status, PKV_DEV_BAD_BLOCK);
-        __syncthreads();                                 // and every row of the batch is read
-        stop = stops;
+    };
+    auto look_up = [&](int i0, int buffer) {
+#pragma unroll
+        for (int j = 0; j < kEntries; ++j) {
+            const int e = j * kMoveThreads + tid, i = i0 + e;
+            if (e >= p.batch || i >= n) continue;
+            const int64_t dst = (int64_t)first + i;
+            Place x = {-1, -1};
+            if (pos[j] < dst || before[j] >= pos[j] || pos[j] >= limit) {
+                atomicMin(&stops[buffer], i);
+            } else if (pos[j] != dst) {
+                x = {place(pos[j]), place((int)dst)};
+                if (x.from < 0 || x.to < 0) {
+                    x = {-1, -1};
+                    if (blockIdx.x == 0) atomicOr(p.status, PKV_DEV_BAD_BLOCK);
+                }
+            }
+            places[buffer][e] = x;
+        }
+    };
+    if (tid < 3) stops[tid] = n;
+    __syncthreads();
+    fetch(0);
+    look_up(0, 0);
+    fetch(p.batch);
+    __syncthreads();
+    for (int i0 = 0, buffer = 0; i0 < n; i0 += p.batch, buffer = buffer == 2 ? 0 : buffer + 1) {
+        const int count = min(p.batch, n - i0), stop = stops[buffer];
+        uint4 v[kMoveDepth];
+        // the thread's d-th chunk of the batch: where it comes from and goes to, null: nowhere
+        auto chunk = [&](int d, bool source) -> uint4 * {
+            const int r = d * per_pass + k, pair = pairs == 1 ? 0 : r / p.batch, e = r - pair * p.batch;
+            if (k >= per_pass || pair >= pairs || e >= count || i0 + e >= stop) return nullptr;
+            const int64_t at = source ? places[buffer][e].from : places[buffer][e].to;
+            if (at < 0) return nullptr;
+            return ((pair0 + pair) & 1 ? p.v_pool : p.k_pool) + c0 + c +
+                   (at + (int64_t)((pair0 + pair) >> 1) * p.block_size) * p.chunks;
+        };
 #pragma unroll
         for (int d = 0; d < kMoveDepth; ++d)
-            if (to[d] >= 0 && i0 + d * per_pass + k < stop) pool[to[d]] = v[d];
-        ok = stop >= n;
-        if (!ok && blockIdx.x == 0 && tid == 0) atomicOr(p.status, PKV_DEV_BAD_TREE);
-        __syncthreads();
+            if (const uint4 *from = chunk(d, true)) v[d] = *from;
+        if (stop >= n) {
+            look_up(i0 + p.batch, buffer == 2 ? 0 : buffer + 1);
+            fetch(i0 + 2 * p.batch);
+        }
+        __syncthreads();                                 // every row of the batch is read
+#pragma unroll
+        for (int d = 0; d < kMoveDepth; ++d)
+            if (uint4 *to = chunk(d, false)) *to = v[d];
+        if (stop < n) {                                  // the same for the CTA
+            if (blockIdx.x == 0 && tid == 0) atomicOr(p.status, PKV_DEV_BAD_TREE);
+            return;
+        }
     }
 }
 
@@ -233,12 +274,19 @@ extern "C" int kv_cache_compact(const pkv_pool *pool, const int32_t *block_table
     p.block_size = g.block_size;
     p.num_blocks = g.num_blocks;
     p.chunks = g.head_dim / 8;
-    p.part_chunks = std::min(p.chunks, 16);
+    const int64_t average = std::max<int64_t>(1, num_entries / num_seqs);
+    // long lists of few sequences share each row among CTAs, down to 64 bytes
+    const int64_t ctas = (int64_t)num_seqs * g.num_kv_heads * 2;
+    const int parts = average <= 128 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(p.chunks / 4, kMoveCtas / ctas));
+    p.part_chunks = std::min((p.chunks + parts - 1) / parts, kMoveThreads);
     p.parts = (p.chunks + p.part_chunks - 1) / p.part_chunks;
+    const int rows = kMoveThreads / p.part_chunks * kMoveDepth;      // of a batch
+    p.pairs = (int32_t)std::max<int64_t>(1, std::min<int64_t>(rows / average, 2 * g.num_kv_heads));
+    p.batch = std::min(rows / p.pairs, kMoveBatch);
     p.k_pool = static_cast<uint4 *>(k_pool);
     p.v_pool = static_cast<uint4 *>(v_pool);
     p.status = d_status;
     if (num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)(g.num_kv_heads * 2 * p.parts), (unsigned)num_seqs);
+    const dim3 grid((unsigned)((g.num_kv_heads * 2 + p.pairs - 1) / p.pairs * p.parts), (unsigned)num_seqs);
     return launch(&compact_kernel, grid, kMoveThreads, (cudaStream_t)stream, p);
 }
