@@ -51,7 +51,7 @@ constexpr int kTilesKnown = 16;
 constexpr int kTasks = 8;               // items under way, at most
 constexpr float kLazy = 8.f;
 constexpr int kItemCost = 2;           // an item's beginning and end, in tiles
-constexpr int kMinRange = 4;           // a range has at least so many
+constexpr int kMinRange = 2;           // a range has at least so many
 constexpr int kSnap = 2;               // no piece shorter than this is cut off an item
 constexpr int kMaxRanges = 304;        // CTAs of a call, at most
 
@@ -131,6 +131,8 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int b)
 
 // The place where a range ends that would end `off` units into sequence s's: not inside an
 // item's overhead, and not so near an end of the item that a short piece would be left.
+// (Leaving short items whole where a cut's pieces cost more bytes than it saves made no case
+// faster: 24 trees of 64 157 -> 176 us, 12 sequences of 16 heads 17 -> 27.)
 __device__ __forceinline__ Place cut(const Params &p, int s, const Seq &q, int64_t off, int snap)
 {
     const int per = q.tiles + kItemCost;
@@ -999,61 +1001,87 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
 }
 
 // ------------------------------------------------------------------ joining the pieces
-// A row of CTAs per cut item (the x-th range that begins one it does not end); a warp takes
-// 32 rows and 8 columns, the pieces in their order, four under way at a time.
-constexpr int kJoinThreads = 256;
+// A task is 32 rows and 8 columns of a cut item; one, two, four or eight warps share its pieces
+// (in turn, so that the order of a sum does not vary), four pieces under way at a time, and
+// meet in shared memory.  Every CTA lists the cut items and their passes (as many tasks as a CTA
+// takes at once), and takes every gridDim-th pass.
+constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32, kJoinCtas = 152;
+static_assert(kJoinThreads >= kMaxRanges, "a thread for each range");
+
+__device__ __forceinline__ int ways_of(int pieces) { return pieces > 16 ? 8 : pieces > 8 ? 4 : pieces > 4 ? 2 : 1; }
+
+// Rows of an item that count: those of full query tiles before the last one's.
+__device__ __forceinline__ int tasks_of(const Params &p, int D, int tokens)
+{
+    const int before = (tokens - 1) / p.tile_tokens;
+    const int rows = before * kRows + (tokens - before * p.tile_tokens) * p.group;
+    return (rows + 31) / 32 * (D / 8);
+}
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const Params p)
+__global__ void __launch_bounds__(kJoinThreads, 1) tree_join_kernel(const Params p)
 {
     using E = Elem<BF16>;
     using T = typename E::T;
     __shared__ int4 ranges[kMaxRanges];
+    __shared__ int begins[kMaxRanges], ends[kMaxRanges], passes[kMaxRanges + 1], sums[kJoinWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     griddep_launch_dependents();
     griddep_wait();
-#pragma unroll
-    for (int i = tid; i < kMaxRanges; i += kJoinThreads)
-        if (i < p.grid) ranges[i] = p.ranges[i];
+    // the sum of the warps' totals before this one, and of all
+    auto across = [&](int total, int &all) {
+        if (lane == 0) sums[warp] = total;
+        __syncthreads();
+        const int x = lane < kJoinWarps ? sums[lane] : 0;
+        all = __reduce_add_sync(kFull, x);
+        return (int)__reduce_add_sync(kFull, lane < warp ? x : 0);
+    };
+    int4 range = make_int4(0, 0, 0, 0);
+    if (tid < p.grid) ranges[tid] = range = p.ranges[tid];
+    const unsigned begun = __ballot_sync(kFull, range.x & kBegins);
+    int items;
+    const int rank = across(__popc(begun), items) + __popc(begun & ((1u << lane) - 1u));
+    if (range.x & kBegins) begins[rank] = tid;
+    if (range.x & kEnds) ends[rank - 1] = tid;           // the item begun before this range's own
     __syncthreads();
-    int begin = -1, end = -1, left = blockIdx.x;         // (every warp for itself)
-    for (int i0 = 0; i0 < p.grid && end < 0; i0 += 32) {
-        const int kind = i0 + lane < p.grid ? ranges[i0 + lane].x : 0;
-        unsigned ends = __ballot_sync(kFull, kind & kEnds);
-        if (begin < 0) {
-            unsigned begins = __ballot_sync(kFull, kind & kBegins);
-            if (__popc(begins) <= left) {
-                left -= __popc(begins);
-                continue;
-            }
-            for (; left > 0; --left) begins &= begins - 1;
-            begin = i0 + __ffs(begins) - 1;
-            ends &= ~((2u << (begin - i0)) - 1u);
-        }
-        if (ends) end = i0 + __ffs(ends) - 1;
+    int n = 0;
+    if (tid < items) {
+        const int per_pass = kJoinWarps / ways_of(ends[tid] - begins[tid] + 1);
+        n = (tasks_of(p, D, ranges[begins[tid]].y) + per_pass - 1) / per_pass;
     }
-    if (begin < 0 || end < 0) return;
-    const int tokens = ranges[begin].y, r0 = ranges[begin].z, g = ranges[begin].w;
-    const int G = p.group, QT = p.tile_tokens, pieces = end - begin + 1;
-    // rows that count: those of full query tiles before the last one's
-    const int before = (tokens - 1) / QT;
-    const int rows = before * kRows + (tokens - before * QT) * G;
-    const int tasks = (rows + 31) / 32 * (D / 8);
+    int upto = n, all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, upto, o);
+        if (lane >= o) upto += y;
+    }
+    upto += across(__shfl_sync(kFull, upto, 31), all);
+    if (tid < items) passes[tid] = upto - n;
+    if (tid == 0) passes[items] = all;
+    __syncthreads();
+    const int G = p.group, QT = p.tile_tokens;
     const float sc = p.scale_log2, hide = sc < 0.f ? INFINITY : -INFINITY;
-    for (int task = blockIdx.y * (kJoinThreads / 32) + warp; task < tasks; task += gridDim.y * (kJoinThreads / 32)) {
+    __shared__ float shares[kJoinWarps][11][32];
+    for (int pass = blockIdx.x; pass < passes[items]; pass += gridDim.x) {
+        int item = 0;                                    // the last item that begins at or before the pass
+        for (int step = 256; step > 0; step >>= 1)
+            if (item + step < items && passes[item + step] <= pass) item += step;
+        const int begin = begins[item], pieces = ends[item] - begin + 1;
+        const int tokens = ranges[begin].y, row0 = ranges[begin].z, g = ranges[begin].w;
+        const int tasks = tasks_of(p, D, tokens), ways = ways_of(pieces), mine = warp % ways;
+        const int task = (pass - passes[item]) * (kJoinWarps / ways) + warp / ways;
         const int rr = task / (D / 8) * 32 + lane, c8 = task % (D / 8);
         const int gr = rr / kRows, jj = (rr - gr * kRows) / G, h = rr - gr * kRows - jj * G;
         const int token = gr * QT + jj;
-        if (jj >= QT || token >= tokens) continue;
+        const bool valid = task < tasks && jj < QT && token < tokens;
         float ref = hide, l = 0.f, o[8] = {};
         bool bad = false;
-        auto add = [&](float2 ml, float4 a, float4 b) {
+        auto add = [&](float2 ml, const float (&v)[8]) {
             bad |= ml.y < 0.f;
             if (ml.y == 0.f) return;                     // nothing seen there
             const float now = sc < 0.f ? fminf(ref, ml.x) : fmaxf(ref, ml.x);
             const float f = ref == hide ? 0.f : fast_exp2((ref - now) * sc);
             const float w = fast_exp2((ml.x - now) * sc);
-            const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
             ref = now;
             l = l * f + w * ml.y;
 #pragma unroll
@@ -1061,13 +1089,14 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const Params p)
         };
         const float2 *ml_at = p.part_ml + rr;
         const float4 *o_at = p.part_o + (int64_t)2 * c8 * p.piece_rows + rr;
-        for (int k0 = 0; k0 < pieces; k0 += 4) {
+        for (int k0 = mine; k0 < pieces && valid; k0 += 4 * ways) {
             float2 ml[4];
             float4 a[4], b[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                if (k0 + k >= pieces) break;
-                const int64_t piece = k0 + k == 0 ? 2 * begin + 1 : 2 * (begin + k0 + k);
+                const int at = k0 + k * ways;
+                if (at >= pieces) break;
+                const int64_t piece = at == 0 ? 2 * begin + 1 : 2 * (begin + at);
                 const float4 *src = o_at + piece * (D / 4) * p.piece_rows;
                 ml[k] = ml_at[piece * p.piece_rows];
                 a[k] = src[0];
@@ -1075,13 +1104,38 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const Params p)
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (k0 + k < pieces) add(ml[k], a[k], b[k]);
+                if (k0 + k * ways < pieces)
+                    add(ml[k], {a[k].x, a[k].y, a[k].z, a[k].w, b[k].x, b[k].y, b[k].z, b[k].w});
         }
+        if (ways > 1) {                                  // the same for the CTA
+            float (&share)[11][32] = shares[warp];
+            if (mine) {
+                share[0][lane] = ref;
+                share[1][lane] = l;
+                share[2][lane] = bad ? 1.f : 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) share[3 + e][lane] = o[e];
+            }
+            __syncthreads();
+            if (mine == 0) {
+                for (int w = 1; w < ways; ++w) {
+                    const float (&other)[11][32] = shares[warp + w];
+                    bad |= other[2][lane] != 0.f;
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = other[3 + e][lane];
+                    // (its output is in terms of its own reference and sum)
+                    add(make_float2(other[0][lane], other[1][lane]), v);
+                }
+            }
+            __syncthreads();
+        }
+        if (!valid || mine) continue;
         const bool none = bad || l == 0.f;
         const float inv = none ? 0.f : 1.f / l;
         auto two_of = [&](int k) { return none ? 0u : E::pack(o[k] * inv, o[k + 1] * inv); };
         T *out = static_cast<T *>(p.out) +
-                 ((int64_t)(r0 + token) * p.num_q_heads + (int64_t)g * G + h) * D + 8 * c8;
+                 ((int64_t)(row0 + token) * p.num_q_heads + (int64_t)g * G + h) * D + 8 * c8;
         *reinterpret_cast<uint4 *>(out) = make_uint4(two_of(0), two_of(2), two_of(4), two_of(6));
     }
 }
@@ -1299,10 +1353,7 @@ extern "C" int paged_tree_attention(const pkv_pool *pool, void *out, const void 
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, k.fn, tk, tv, tq, prm) != cudaSuccess) return PKV_ERR_CUDA;
-    // items that can be cut: no more than there are, nor than ranges
-    const int64_t sets = (int64_t)num_tokens / ((two ? 2 : 1) * prm.tile_tokens) + num_seqs;
-    const int64_t cuts = std::min<int64_t>(cfg.gridDim.x, sets * g.num_kv_heads);
-    cfg.gridDim = dim3((unsigned)cuts, (unsigned)std::min<int64_t>(16, std::max<int64_t>(1, 1216 / cuts)));
+    cfg.gridDim = dim3(kJoinCtas);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, k.join, prm) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
