@@ -49,6 +49,7 @@ constexpr int kKeys = 64;              // keys of a tile
 constexpr int kMaxWords = 32;
 constexpr int kTilesKnown = 16;
 constexpr int kTasks = 8;               // items under way, at most
+constexpr int kAhead = 2;               // lengths of so many 32 sequences are read at once
 constexpr float kLazy = 8.f;
 constexpr int kItemCost = 2;           // an item's beginning and end, in tiles
 constexpr int kMinRange = 2;           // a range has at least so many
@@ -62,6 +63,7 @@ struct Params {
     const uint32_t *mask;
     int32_t words, num_seqs, num_tokens, num_q_heads, num_kv_heads, group;
     int32_t max_blocks_per_seq, num_blocks;
+    int32_t max_tokens;                // that a table row holds
     int32_t tile_tokens;               // tokens of a query tile
     int32_t box_tokens;                // and of one box of query rows
     int32_t set_tokens, set_inverse;   // of NG query tiles; ceil(2^20 / that)
@@ -93,8 +95,7 @@ __device__ __forceinline__ Seq seq_of(const Params &p, int r0, int r1, int L)
     q.L = L;
     q.rows_ok = 0 <= q.r0 && q.r0 <= r1 && r1 <= p.num_tokens;
     q.n = q.rows_ok ? r1 - q.r0 : 0;
-    q.bad = !q.rows_ok || q.L < q.n || (int64_t)q.L > (int64_t)p.max_blocks_per_seq * kBlock ||
-            q.n > 32 * p.words;
+    q.bad = !q.rows_ok || q.L < q.n || q.L > p.max_tokens || q.n > 32 * p.words;
     q.base = q.L - q.n;
     q.tiles = (q.L + kKeys - 1) / kKeys;
     // ceil(n / set_tokens): n + set_tokens < 1280 here, so 2^20 is enough for the inverse
@@ -120,24 +121,15 @@ struct alignas(16) Task {
     __device__ __forceinline__ int L() const { return base + n; }
 };
 
-// floor(a / b) for 0 <= a, 0 < b, by an estimate in fp32 that is then put right.
-__device__ __forceinline__ int64_t quotient(int64_t a, int b)
-{
-    int64_t q = (int64_t)((float)a / (float)b), r = a - q * b;
-    for (; r < 0; r += b) --q;
-    for (; r >= b; r -= b) ++q;
-    return q;
-}
-
 // The place where a range ends that would end `off` units into sequence s's: not inside an
 // item's overhead, and not so near an end of the item that a short piece would be left.
 // (Leaving short items whole where a cut's pieces cost more bytes than it saves made no case
 // faster: 24 trees of 64 157 -> 176 us, 12 sequences of 16 heads 17 -> 27.)
-__device__ __forceinline__ Place cut(const Params &p, int s, const Seq &q, int64_t off, int snap)
+__device__ __forceinline__ Place cut(const Params &p, int s, const Seq &q, uint32_t off, int snap)
 {
-    const int per = q.tiles + kItemCost;
-    Place c = {s, (int)quotient(off, per), 0};
-    const int t = (int)(off - (int64_t)c.it * per) - kItemCost;
+    const uint32_t per = q.tiles + kItemCost;
+    Place c = {s, (int)(off / per), 0};
+    const int t = (int)(off - c.it * per) - kItemCost;
     c.t = t < snap ? 0 : t;
     if (t > q.tiles - snap) {
         c.t = 0;
@@ -151,10 +143,10 @@ __device__ __forceinline__ Place cut(const Params &p, int s, const Seq &q, int64
 }
 
 // A CTA's range and the way through its items; the producer's warp makes it and goes it for the
-// CTA.  Lane i holds the lengths of sequence `held` + i.
+// CTA.  Lane i holds the lengths of sequence `held` + i.  (The host sees to it that all units of a
+// call fit 32 bits.)
 struct Walk {
     Place at, to;
-    int ranges;
     Seq q;                             // sequence at.s
     int g, set;                        // item at.it
     int held, r0, r1, L;
@@ -167,10 +159,9 @@ struct Walk {
         r1 = i < p.num_seqs ? p.query_start[i + 1] : 0;
         L = i < p.num_seqs ? p.context_lens[i] : 0;
     }
-    __device__ __forceinline__ void at_sequence(const Params &p)
+    __device__ __forceinline__ Seq sequence(const Params &p, int i) const
     {
-        const int i = at.s - held;
-        q = seq_of(p, __shfl_sync(kFull, r0, i), __shfl_sync(kFull, r1, i), __shfl_sync(kFull, L, i));
+        return seq_of(p, __shfl_sync(kFull, r0, i), __shfl_sync(kFull, r1, i), __shfl_sync(kFull, L, i));
     }
 
     // The ranges: the units of all sequences are counted, and the two ends of this CTA's range
@@ -179,59 +170,74 @@ struct Walk {
     __device__ __forceinline__ void plan(const Params &p)
     {
         const int lane = threadIdx.x & 31;
-        auto units_of = [&](const Seq &x) { return (int64_t)x.items(p) * (x.tiles + kItemCost); };
-        int64_t all = 0;
+        auto units_of = [&](const Seq &x) { return (uint32_t)x.items(p) * (uint32_t)(x.tiles + kItemCost); };
+        uint32_t all = 0;
 #pragma unroll 1
-        for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
-            hold(p, s0);
-            const Seq x = seq_of(p, r0, r1, L);
-            all += units_of(x);
-            if (x.bad && (s0 + lane) % gridDim.x == blockIdx.x) {
-                atomicOr(p.status, PKV_DEV_BAD_LEN);
-                uint4 *o = static_cast<uint4 *>(p.out) + (int64_t)x.r0 * p.num_q_heads * (D / 8);
-                for (int64_t i = 0; i < (int64_t)x.n * p.num_q_heads * (D / 8); ++i) o[i] = make_uint4(0, 0, 0, 0);
+        for (int s0 = 0; s0 < p.num_seqs; s0 += 32 * kAhead) {
+            int a[kAhead], b[kAhead], len[kAhead];       // the loads of several steps at once
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = s0 + 32 * k + lane;
+                a[k] = i < p.num_seqs ? p.query_start[i] : 0;
+                b[k] = i < p.num_seqs ? p.query_start[i + 1] : 0;
+                len[k] = i < p.num_seqs ? p.context_lens[i] : 0;
+            }
+            held = s0;
+            r0 = a[0];
+            r1 = b[0];
+            L = len[0];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const Seq x = seq_of(p, a[k], b[k], len[k]);
+                all += units_of(x);
+                if (x.bad && (s0 + 32 * k + lane) % gridDim.x == blockIdx.x) {
+                    atomicOr(p.status, PKV_DEV_BAD_LEN);
+                    uint4 *o = static_cast<uint4 *>(p.out) + (int64_t)x.r0 * p.num_q_heads * (D / 8);
+                    for (int64_t i = 0; i < (int64_t)x.n * p.num_q_heads * (D / 8); ++i) o[i] = make_uint4(0, 0, 0, 0);
+                }
             }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
-        ranges = (int)max((int64_t)1, min((int64_t)gridDim.x, all / kMinRange));
+        all = __reduce_add_sync(kFull, all);
+        const uint32_t ranges = max(1u, min(gridDim.x, all / kMinRange));
         // the first `more` ranges have a unit more
-        const int64_t size = quotient(all, ranges), more = all - size * ranges;
-        const int snap = (int)min((int64_t)kSnap, size / 4);
-        const int64_t begin = size * blockIdx.x + min((int64_t)blockIdx.x, more);
-        const int64_t end = begin + size + (blockIdx.x < more);
+        const uint32_t size = all / ranges, more = all - size * ranges;
+        const int snap = min(kSnap, (int)(size / 4));
+        const uint32_t begin = size * blockIdx.x + min(blockIdx.x, more);
+        const uint32_t end = begin + size + (blockIdx.x < more);
         at = to = Place{p.num_seqs, 0, 0};
+        q = Seq{};
         int4 left = make_int4(0, 0, 0, 0);               // for the joining kernel
-        int64_t before = 0;
+        uint32_t before = 0;
 #pragma unroll 1
         for (int s0 = 0; s0 < p.num_seqs && blockIdx.x < ranges && before <= end; s0 += 32) {
             if (s0 != held) hold(p, s0);
-            const Seq x = seq_of(p, r0, r1, L);
-            const int64_t units = units_of(x);
-            int64_t upto = units;
+            const uint32_t units = units_of(seq_of(p, r0, r1, L));
+            uint32_t upto = units;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(kFull, upto, o);
+                const uint32_t y = __shfl_up_sync(kFull, upto, o);
                 if (lane >= o) upto += y;
             }
 #pragma unroll 1
             for (int e = 0; e < 2; ++e) {
-                const int64_t off = (e ? end : begin) - before - (upto - units);
-                const bool here = off >= 0 && off < units;
-                Place c = {0, 0, 0};
-                if (here) c = cut(p, s0 + lane, x, off, snap);
-                const unsigned who = __ballot_sync(kFull, here);
+                const uint32_t off = (e ? end : begin) - before;     // (wraps below `before`)
+                const unsigned who = __ballot_sync(kFull, off >= upto - units && off < upto);
                 if (!who) continue;
                 const int src = __ffs(who) - 1;
-                c = {__shfl_sync(kFull, c.s, src), __shfl_sync(kFull, c.it, src), __shfl_sync(kFull, c.t, src)};
+                const Seq x = sequence(p, src);
+                const Place c = cut(p, s0 + src, x, off - __shfl_sync(kFull, upto - units, src), snap);
+                const int head = c.s == s0 + src && x.sets > 1 ? c.it / x.sets : c.it;
+                const int mine = c.it - head * x.sets;               // query tiles of that head
                 if (!e) {
                     at = c;
-                    continue;
+                    q = x;
+                    g = head;
+                    set = mine;
+                } else {
+                    to = c;
+                    const int first = mine * p.set_tokens;
+                    left = make_int4(0, min(p.set_tokens, x.n - first), x.r0 + first, head);
                 }
-                to = c;
-                const int n = __shfl_sync(kFull, x.n, src), sets = __shfl_sync(kFull, x.sets, src);
-                const int head = c.it / sets, first = (c.it - head * sets) * p.set_tokens;
-                left = make_int4(0, min(p.set_tokens, n - first), __shfl_sync(kFull, x.r0, src) + first, head);
             }
             before += __shfl_sync(kFull, upto, 31);
         }
@@ -240,9 +246,10 @@ struct Walk {
         if (to.t > 0 && !(same && at.t > 0)) left.x |= kBegins;
         if (lane == 0) p.ranges[blockIdx.x] = left;
         if (at.s < held || at.s >= held + 32) hold(p, at.s);
-        at_sequence(p);
-        g = q.sets > 1 ? at.it / q.sets : at.it;
-        set = at.it - g * q.sets;
+        if (at.it == 0) {                                // (the cut may have led to the next sequence)
+            g = set = 0;
+            q = sequence(p, at.s - held);
+        }
     }
     __device__ __forceinline__ Task next(const Params &p)
     {
@@ -273,7 +280,7 @@ struct Walk {
                 ++at.s;
                 at.it = at.t = g = set = 0;
                 if (at.s >= held + 32) hold(p, at.s);
-                at_sequence(p);
+                q = sequence(p, at.s - held);
             }
         }
         return k;
@@ -1312,12 +1319,17 @@ extern "C" int paged_tree_attention(const pkv_pool *pool, void *out, const void 
     prm.num_kv_heads = g.num_kv_heads;
     prm.group = G;
     prm.max_blocks_per_seq = max_blocks_per_seq;
+    prm.max_tokens = (int32_t)std::min<int64_t>((int64_t)max_blocks_per_seq * pkv::kBlock, INT32_MAX);
     prm.num_blocks = g.num_blocks;
     prm.tile_tokens = tile_tokens(G);
     prm.box_tokens = box_tokens(G);
     prm.set_tokens = (two ? 2 : 1) * prm.tile_tokens;
     prm.set_inverse = ((1 << 20) + prm.set_tokens - 1) / prm.set_tokens;
     prm.piece_rows = two ? 2 * kRows : (int32_t)piece_rows(num_tokens, G);
+    // the ranges are counted in 32 bits
+    const double most = ((double)num_tokens / prm.set_tokens + num_seqs) * g.num_kv_heads *
+                        (prm.max_tokens / kKeys + 1 + kItemCost);
+    if (most > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     // scores are hidden by an infinity that the scale must carry into the exponent; at scale 0
     // the smallest normal number weighs all keys alike
     prm.scale_log2 = scale == 0.f ? 0x1p-126f : scale * 1.4426950408889634f;
