@@ -4,27 +4,27 @@
 //   x_j = scale <q, K_j>,  out = sum_j softmax(x)_j V_j   over the j that it sees:
 //   j < base,  or  base <= j < L and bit j - base of its mask is set.
 //
-// All n G rows of a (sequence, kv head) share its keys, so K and V are read once for up to
-// NG * 128 rows, one row to a lane of tensor memory, and both products run on tcgen05.
-// Work items are (sequence, kv head, NG query tiles); their key tiles (64 keys), written one
-// after the other with kItemCost tiles' worth of overhead before each item, are cut into
-// equal ranges, one to a CTA: every CTA has the same work, whatever the lengths, and an item
-// is cut where a range ends.  A cut item's pieces (unnormalised output, reference maximum,
-// sum; fp32) meet in the workspace and a second kernel joins them, always in the same order.
+// All n G rows of a (sequence, kv head) share its keys: K and V are read once for each query
+// tile of up to 128 rows, one row to a lane of tensor memory, and both products run on
+// tcgen05.  An item is a query tile of a (sequence, kv head); the key tiles (64 keys) of all items,
+// written one after the other with kItemCost tiles' worth of overhead before each, are cut into
+// equal ranges, one to a CTA: every CTA has the same work, whatever the lengths, and an item is
+// cut where a range ends.  A cut item's pieces (unnormalised output, reference, sum; fp32) meet
+// in the workspace and a second kernel joins them, always in the same order.
 //
-//   NG = 1 (rows fit one query tile): two CTAs to an SM, 256 columns of tensor memory each;
-//     while one waits for its softmax or begins an item, the other keeps copies and
-//     products going.
-//   NG = 2: one CTA to an SM, two query tiles against the same K and V.
+// Items go first query tiles first, by sequence and kv head, then the second ones, and so on:
+// where trees need two tiles, two CTAs read the same keys at about the same time, one of
+// them from L2.  Two CTAs fit an SM, with 256 columns of tensor memory each; while one waits for
+// its softmax or begins an item, the other keeps copies and products going.
 //
 // Roles of a CTA's warps:
-//   softmax (4 NG): thread r of a query tile owns row r.  Weights are taken against a lazy
-//     reference maximum (it moves when a score exceeds it by more than kLazy, in log2
-//     units), as two 16-bit parts each, into tensor memory.
-//   producer: a ring of K tiles and one of V tiles, one TMA box to each block and 64 columns;
-//     the item's query rows.
-//   issuers (NG): S = Q K^T into one of two buffers, then O += P V of the tile before.
-//   cleaner: V of keys that no row may be reached by.  A weight of zero does not stop a NaN
+//   0-3, softmax: thread r owns row r.  Weights are taken against a lazy reference (it moves
+//     when a score exceeds it by more than kLazy, in log2 units), as two 16-bit parts each,
+//     into tensor memory.
+//   4, producer: makes the plan and hands out the items; a ring of K tiles and one of V tiles,
+//     one TMA box to each block and 64 columns; the items' query rows.
+//   5, issuer: S = Q K^T into one of two buffers, then O += P V of the tile before.
+//   6, cleaner: V of keys that no row may be reached by.  A weight of zero does not stop a NaN
 //     or an infinity in V, so in tiles that hold drafted tokens or the end of the sequence V
 //     behind the end becomes zero, and so do V's odd values; rows that see such a key get
 //     them added by hand (rare).
@@ -66,7 +66,7 @@ struct Params {
     int32_t max_tokens;                // that a table row holds
     int32_t tile_tokens;               // tokens of a query tile
     int32_t box_tokens;                // and of one box of query rows
-    int32_t set_tokens, set_inverse;   // of NG query tiles; ceil(2^20 / that)
+    int32_t tile_inverse;              // ceil(2^20 / tile_tokens)
     int32_t piece_rows;                // rows of a piece's place in the workspace
     float scale_log2;
     int32_t grid;                      // CTAs of the call
@@ -83,9 +83,8 @@ constexpr int kContinues = 1, kEnds = 2, kBegins = 4;
 
 // One sequence of a call.
 struct Seq {
-    int r0, n, base, L, tiles, sets;   // rows; key tiles; sets of NG query tiles
+    int r0, n, base, L, tiles, parts;  // rows; key tiles; query tiles
     bool rows_ok, bad;
-    __device__ __forceinline__ int items(const Params &p) const { return sets * p.num_kv_heads; }
 };
 
 __device__ __forceinline__ Seq seq_of(const Params &p, int r0, int r1, int L)
@@ -98,19 +97,20 @@ __device__ __forceinline__ Seq seq_of(const Params &p, int r0, int r1, int L)
     q.bad = !q.rows_ok || q.L < q.n || q.L > p.max_tokens || q.n > 32 * p.words;
     q.base = q.L - q.n;
     q.tiles = (q.L + kKeys - 1) / kKeys;
-    // ceil(n / set_tokens): n + set_tokens < 1280 here, so 2^20 is enough for the inverse
-    q.sets = q.bad ? 0 : (q.n + p.set_tokens - 1) * p.set_inverse >> 20;
+    // ceil(n / tile_tokens): n + tile_tokens < 1280 here, so 2^20 is enough for the inverse
+    q.parts = q.bad ? 0 : (q.n + p.tile_tokens - 1) * p.tile_inverse >> 20;
     return q;
 }
 
-__device__ __forceinline__ Seq seq_of(const Params &p, int s)
-{
-    return seq_of(p, p.query_start[s], p.query_start[s + 1], p.context_lens[s]);
-}
-
-// A place in the order of all tiles: tile t of item `it` of sequence s.
+// A place in the order of all tiles: key tile t of query tile k of sequence s and kv head g.
 struct Place {
-    int s, it, t;
+    int k, s, g, t;
+    // the items that the places are in
+    __device__ __forceinline__ bool operator==(const Place &o) const { return k == o.k && s == o.s && g == o.g; }
+    __device__ __forceinline__ bool operator<(const Place &o) const
+    {
+        return k != o.k ? k < o.k : s != o.s ? s < o.s : g < o.g;
+    }
 };
 
 // An item's part in a range: tiles [t0, t1) of kv head g and the query tiles from token `first`
@@ -125,19 +125,18 @@ struct alignas(16) Task {
 // item's overhead, and not so near an end of the item that a short piece would be left.
 // (Leaving short items whole where a cut's pieces cost more bytes than it saves made no case
 // faster: 24 trees of 64 157 -> 176 us, 12 sequences of 16 heads 17 -> 27.)
-__device__ __forceinline__ Place cut(const Params &p, int s, const Seq &q, uint32_t off, int snap)
+__device__ __forceinline__ Place cut(const Params &p, int k, int s, const Seq &q, uint32_t off, int snap)
 {
     const uint32_t per = q.tiles + kItemCost;
-    Place c = {s, (int)(off / per), 0};
-    const int t = (int)(off - c.it * per) - kItemCost;
+    Place c = {k, s, (int)(off / per), 0};
+    const int t = (int)(off - c.g * per) - kItemCost;
     c.t = t < snap ? 0 : t;
     if (t > q.tiles - snap) {
         c.t = 0;
-        ++c.it;
-    }
-    if (c.it >= q.items(p)) {
-        ++c.s;
-        c.it = 0;
+        if (++c.g == p.num_kv_heads) {
+            c.g = 0;
+            ++c.s;
+        }
     }
     return c;
 }
@@ -148,7 +147,7 @@ __device__ __forceinline__ Place cut(const Params &p, int s, const Seq &q, uint3
 struct Walk {
     Place at, to;
     Seq q;                             // sequence at.s
-    int g, set;                        // item at.it
+    int most;                          // query tiles of a sequence, at most
     int held, r0, r1, L;
 
     __device__ __forceinline__ void hold(const Params &p, int s)
@@ -170,8 +169,10 @@ struct Walk {
     __device__ __forceinline__ void plan(const Params &p)
     {
         const int lane = threadIdx.x & 31;
-        auto units_of = [&](const Seq &x) { return (uint32_t)x.items(p) * (uint32_t)(x.tiles + kItemCost); };
+        // of one query tile
+        auto units_of = [&](const Seq &x) { return (uint32_t)p.num_kv_heads * (uint32_t)(x.tiles + kItemCost); };
         uint32_t all = 0;
+        most = 0;
 #pragma unroll 1
         for (int s0 = 0; s0 < p.num_seqs; s0 += 32 * kAhead) {
             int a[kAhead], b[kAhead], len[kAhead];       // the loads of several steps at once
@@ -189,7 +190,8 @@ struct Walk {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const Seq x = seq_of(p, a[k], b[k], len[k]);
-                all += units_of(x);
+                all += x.parts * units_of(x);
+                most = max(most, x.parts);
                 if (x.bad && (s0 + 32 * k + lane) % gridDim.x == blockIdx.x) {
                     atomicOr(p.status, PKV_DEV_BAD_LEN);
                     uint4 *o = static_cast<uint4 *>(p.out) + (int64_t)x.r0 * p.num_q_heads * (D / 8);
@@ -198,92 +200,86 @@ struct Walk {
             }
         }
         all = __reduce_add_sync(kFull, all);
+        most = __reduce_max_sync(kFull, most);
         const uint32_t ranges = max(1u, min(gridDim.x, all / kMinRange));
         // the first `more` ranges have a unit more
         const uint32_t size = all / ranges, more = all - size * ranges;
         const int snap = min(kSnap, (int)(size / 4));
         const uint32_t begin = size * blockIdx.x + min(blockIdx.x, more);
         const uint32_t end = begin + size + (blockIdx.x < more);
-        at = to = Place{p.num_seqs, 0, 0};
-        q = Seq{};
+        at = to = Place{most, 0, 0, 0};
         int4 left = make_int4(0, 0, 0, 0);               // for the joining kernel
         uint32_t before = 0;
 #pragma unroll 1
-        for (int s0 = 0; s0 < p.num_seqs && blockIdx.x < ranges && before <= end; s0 += 32) {
-            if (s0 != held) hold(p, s0);
-            const uint32_t units = units_of(seq_of(p, r0, r1, L));
-            uint32_t upto = units;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(kFull, upto, o);
-                if (lane >= o) upto += y;
-            }
+        for (int k = 0; k < most && blockIdx.x < ranges && before <= end; ++k) {
 #pragma unroll 1
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t off = (e ? end : begin) - before;     // (wraps below `before`)
-                const unsigned who = __ballot_sync(kFull, off >= upto - units && off < upto);
-                if (!who) continue;
-                const int src = __ffs(who) - 1;
-                const Seq x = sequence(p, src);
-                const Place c = cut(p, s0 + src, x, off - __shfl_sync(kFull, upto - units, src), snap);
-                const int head = c.s == s0 + src && x.sets > 1 ? c.it / x.sets : c.it;
-                const int mine = c.it - head * x.sets;               // query tiles of that head
-                if (!e) {
-                    at = c;
-                    q = x;
-                    g = head;
-                    set = mine;
-                } else {
-                    to = c;
-                    const int first = mine * p.set_tokens;
-                    left = make_int4(0, min(p.set_tokens, x.n - first), x.r0 + first, head);
+            for (int s0 = 0; s0 < p.num_seqs && before <= end; s0 += 32) {
+                if (s0 != held) hold(p, s0);
+                const Seq mine = seq_of(p, r0, r1, L);
+                const uint32_t units = mine.parts > k ? units_of(mine) : 0u;
+                uint32_t upto = units;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(kFull, upto, o);
+                    if (lane >= o) upto += y;
                 }
+#pragma unroll 1
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t off = (e ? end : begin) - before;         // (wraps below `before`)
+                    const unsigned who = __ballot_sync(kFull, off >= upto - units && off < upto);
+                    if (!who) continue;
+                    const int src = __ffs(who) - 1;
+                    const Seq x = sequence(p, src);
+                    const Place c = cut(p, k, s0 + src, x, off - __shfl_sync(kFull, upto - units, src), snap);
+                    if (!e) {
+                        at = c;
+                        continue;
+                    }
+                    to = c;
+                    const int first = k * p.tile_tokens;
+                    left = make_int4(0, min(p.tile_tokens, x.n - first), x.r0 + first, c.g);
+                }
+                before += __shfl_sync(kFull, upto, 31);
             }
-            before += __shfl_sync(kFull, upto, 31);
         }
-        const bool same = at.s == to.s && at.it == to.it;
+        const bool same = at == to;
         if (at.t > 0) left.x |= kContinues | (same ? 0 : kEnds);
         if (to.t > 0 && !(same && at.t > 0)) left.x |= kBegins;
         if (lane == 0) p.ranges[blockIdx.x] = left;
         if (at.s < held || at.s >= held + 32) hold(p, at.s);
-        if (at.it == 0) {                                // (the cut may have led to the next sequence)
-            g = set = 0;
-            q = sequence(p, at.s - held);
-        }
+        q = sequence(p, at.s - held);
     }
     __device__ __forceinline__ Task next(const Params &p)
     {
-        Task k = {};
-        while (at.s < p.num_seqs && at.s <= to.s) {
-            const bool last = at.s == to.s;
-            if (g < p.num_kv_heads && q.sets > 0 && (!last || at.it <= to.it)) {
-                const int t1 = last && at.it == to.it ? to.t : q.tiles;
-                const int t0 = at.t;
-                k.s = at.s;
-                k.g = g;
-                k.first = set * p.set_tokens;
-                k.r0 = q.r0;
-                k.n = q.n;
-                k.base = q.base;
-                ++at.it;
+        Task task = {};
+        while (at < to || (at == to && at.t < to.t)) {
+            if (at.s >= p.num_seqs) {                    // the next query tiles
+                ++at.k;
+                at.s = at.g = 0;
+                hold(p, 0);
+                q = sequence(p, 0);
+                continue;
+            }
+            if (q.parts > at.k) {
+                task.s = at.s;
+                task.g = at.g;
+                task.first = at.k * p.tile_tokens;
+                task.t0 = at.t;
+                task.t1 = at == to ? to.t : q.tiles;
+                task.r0 = q.r0;
+                task.n = q.n;
+                task.base = q.base;
                 at.t = 0;
-                if (++set == q.sets) {
-                    set = 0;
-                    ++g;
-                }
-                if (t0 < t1) {
-                    k.t0 = t0;
-                    k.t1 = t1;
-                    return k;
-                }
-            } else {
-                ++at.s;
-                at.it = at.t = g = set = 0;
+                if (++at.g < p.num_kv_heads) return task;
+            }
+            at.g = 0;
+            if (++at.s < p.num_seqs) {
                 if (at.s >= held + 32) hold(p, at.s);
                 q = sequence(p, at.s - held);
             }
+            if (task.t0 < task.t1) return task;
         }
-        return k;
+        return task;
     }
 };
 
@@ -387,38 +383,36 @@ __device__ __forceinline__ void add_odd(uint32_t &sum, uint32_t w)
     else asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w), "r"(0u));
 }
 
-template <int D, int NG>
+template <int D>
 struct Layout {
     static constexpr int kRegions = D / 64;
-    // K and V tiles in flight, a ring each
-    static constexpr int kK = NG == 1 ? (D == 128 ? 2 : 6) : (D == 128 ? 5 : 10);
-    static constexpr int kV = NG == 1 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
+    // K and V tiles in flight, a ring each (V waits for the softmax, K does not)
+    static constexpr int kK = D == 128 ? 2 : 6, kV = D == 128 ? 3 : 6;
     static constexpr int kQBytes = kRegions * kRows * 128;     // a query tile: [region][row][128 B]
     static constexpr int kTileBytes = kRegions * kKeys * 128;  // a K or V tile
-    static constexpr int kKRing = NG * kQBytes, kVRing = kKRing + kK * kTileBytes;
-    static constexpr int kMisc = kVRing + kV * kTileBytes;
-    static constexpr int kMiscBytes = 1024 * NG;
-    static constexpr int kTotal = kMisc + kMiscBytes;
-    // (the copy and issue warps are a warpgroup; NG = 1 has a warp without a role)
-    static constexpr int kWarps = 4 * NG + 4, kThreads = 32 * kWarps;
-    // Registers of a thread: the launch gives kLaunchRegs, the copy and issue warpgroup keeps
-    // kRegsIo and hands the rest to the softmax warpgroups.  A launch with fewer would leave
-    // setmaxnreg.inc waiting for ever, so the host launches only kernels of exactly kLaunchRegs.
-    static constexpr int kLaunchRegs = NG == 1 ? 128 : 168;
-    static constexpr int kRegsIo = 104, kRegsSoftmax = NG == 1 ? 152 : 200;
-    static_assert(NG * kRegsSoftmax + kRegsIo == (NG + 1) * kLaunchRegs, "register split of the launch");
-    static constexpr int kProducer = 4 * NG, kIssuer = 4 * NG + 1, kCleaner = 5 * NG + 1;
-    static constexpr uint32_t kColumns = 256 * NG;             // per query tile: S, S, O
+    static constexpr int kKRing = kQBytes, kVRing = kKRing + kK * kTileBytes;
+    static constexpr int kMisc = kVRing + kV * kTileBytes, kMiscBytes = 1024;
+    static constexpr int kTotal = kMisc + kMiscBytes;          // two CTAs to an SM: at most 113 KB
 };
 
-template <int D, bool BF16, int NG>
-__global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
+// Warps: softmax, copies and products, and one without a role (the register split goes by
+// warpgroups).
+constexpr int kProducer = 4, kIssuer = 5, kCleaner = 6, kThreads = 256;
+// Registers of a thread: the launch gives kLaunchRegs, the copy and issue warpgroup keeps
+// kRegsIo and hands the rest to the softmax warpgroup.  A launch with fewer would leave
+// setmaxnreg.inc waiting for ever, so the host launches only kernels of exactly kLaunchRegs.
+constexpr int kLaunchRegs = 128, kRegsIo = 104, kRegsSoftmax = 152;
+static_assert(kRegsSoftmax + kRegsIo == 2 * kLaunchRegs, "register split of the launch");
+constexpr uint32_t kColumns = 256;     // tensor memory: S, S, O
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 2)
     tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                 const __grid_constant__ CUtensorMap tmQ, const Params p)
 {
     using E = Elem<BF16>;
     using T = typename E::T;
-    using LY = Layout<D, NG>;
+    using LY = Layout<D>;
     constexpr int NK = LY::kK, NV = LY::kV;
     // fp16 pools take their weights times 2^kTop: they stay within 2^15, and those down to 2^-21 of the largest are normal numbers in fp16 (a row
     // far below a few dominant keys would lose its weights' bits).
@@ -428,10 +422,9 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
     uint64_t *q_full = bars, *q_empty = bars + 1;
     uint64_t *k_full = bars + 2, *k_empty = k_full + NK;
     uint64_t *v_full = k_empty + NK, *v_empty = v_full + NV, *clean = v_empty + NV;
-    // S of a query tile out; P out; P V done, each for even and odd tiles
-    uint64_t *s_full = clean + NV, *p_full = s_full + 2 * NG, *o_full = p_full + 2 * NG;
-    uint64_t *done = o_full + 2 * NG;                          // [NG]
-    uint64_t *task_full = done + NG, *task_empty = task_full + kTasks;
+    // S out; P out; P V done, each for even and odd tiles
+    uint64_t *s_full = clean + NV, *p_full = s_full + 2, *o_full = p_full + 2, *done = o_full + 2;
+    uint64_t *task_full = done + 1, *task_empty = task_full + kTasks;
     uint64_t *odd_keys = task_empty + kTasks;                            // [NV]: keys whose V held odd values
     // tile's bad blocks: a K tile's slot is free once S is out, before the softmax reads this, so
     // these have places of their own, more than there are tiles under way
@@ -439,7 +432,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bad_blocks + kTilesKnown);
     volatile int *abort_flag = reinterpret_cast<int *>(tslot + 1);
     Task *tasks = reinterpret_cast<Task *>(smem + LY::kTotal) - kTasks;
-    static_assert((2 + 2 * NK + 4 * NV + 7 * NG + 2 * kTasks) * 8 + kTilesKnown + 8 + kTasks * sizeof(Task) <=
+    static_assert((9 + 2 * NK + 4 * NV + 2 * kTasks) * 8 + kTilesKnown + 8 + kTasks * sizeof(Task) <=
                           LY::kMiscBytes && NK + 3 <= kTilesKnown && NV + 3 <= kTilesKnown,
                   "barriers and flags");
 
@@ -450,30 +443,30 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         mbar_init(smem_addr(q_full), 1);
-        mbar_init(smem_addr(q_empty), NG);
+        mbar_init(smem_addr(q_empty), 1);
         for (int i = 0; i < NK; ++i) {
             mbar_init(smem_addr(&k_full[i]), 1);
-            mbar_init(smem_addr(&k_empty[i]), NG);
+            mbar_init(smem_addr(&k_empty[i]), 1);
         }
         for (int i = 0; i < NV; ++i) {
             mbar_init(smem_addr(&v_full[i]), 1);
-            mbar_init(smem_addr(&v_empty[i]), NG);
+            mbar_init(smem_addr(&v_empty[i]), 1);
             mbar_init(smem_addr(&clean[i]), 1);
         }
-        for (int i = 0; i < 2 * NG; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&s_full[i]), 1);
             mbar_init(smem_addr(&p_full[i]), 4);
             mbar_init(smem_addr(&o_full[i]), 1);
         }
-        for (int i = 0; i < NG; ++i) mbar_init(smem_addr(&done[i]), 1);
+        mbar_init(smem_addr(done), 1);
         for (int i = 0; i < kTasks; ++i) {
             mbar_init(smem_addr(&task_full[i]), 1);
-            mbar_init(smem_addr(&task_empty[i]), 5 * NG + 1);   // softmax warps, issuers, cleaner
+            mbar_init(smem_addr(&task_empty[i]), 6);        // softmax warps, issuer, cleaner
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) tc::tmem_alloc(tslot, LY::kColumns);
+    if (warp == 0) tc::tmem_alloc(tslot, kColumns);
     if (warp == 1 && lane < 3) {
         const CUtensorMap *map = lane == 0 ? &tmK : lane == 1 ? &tmV : &tmQ;
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -498,9 +491,9 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
         it = tasks[nt % kTasks];
         return it.t0 < it.t1;
     };
-    if (warp >= LY::kProducer) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LY::kRegsIo));
-    if (warp == LY::kProducer) {
+    if (warp >= kProducer) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIo));
+    if (warp == kProducer) {
         uint32_t kt = 0, vt = 0, items = 0;      // K tiles, V tiles and items under way or done
         bool ok = true;
         Walk walk;
@@ -512,11 +505,9 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
         };
         // the boxes of an item's query rows
         auto each_box = [&](const Task &k, auto &&box) {
-            for (int gr = 0; gr < NG; ++gr)
-                for (int i = 0; i < min(QT, k.n - k.first - gr * QT); i += p.box_tokens)
-                    for (int rg = 0; rg < LY::kRegions; ++rg)
-                        box(gr * LY::kQBytes + rg * kRows * 128 + i * G * 128, rg * 64, k.g,
-                            k.r0 + k.first + gr * QT + i);
+            for (int i = 0; i < min(QT, k.n - k.first); i += p.box_tokens)
+                for (int rg = 0; rg < LY::kRegions; ++rg)
+                    box(rg * kRows * 128 + i * G * 128, rg * 64, k.g, k.r0 + k.first + i);
         };
         Task after = walk.next(p);
         int ids_after = after.t0 < after.t1 ? ids_from(after, after.t0) : 0;
@@ -628,25 +619,21 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
             for (uint32_t i = vt > NV ? vt - NV : 0; i < vt; ++i) drain(&v_full[i % NV], (i / NV) & 1u);
             if (items > 0) drain(q_full, (items - 1) & 1u);
         }
-    } else if (warp >= LY::kIssuer && warp < LY::kIssuer + NG) {
-        const int gr = __shfl_sync(kFull, warp, 0) - LY::kIssuer;
+    } else if (warp == kIssuer) {
         const uint32_t id_qk = tc::idesc_f16(BF16, kRows, kKeys, 0, 0);
         const uint32_t id_pv = tc::idesc_f16(BF16, kRows, D, 0, 1);
-        const uint32_t t_s = __shfl_sync(kFull, tmem, 0) + 256 * gr, t_o = t_s + 128;
-        const uint64_t qa_d = tc::desc_sw128(smem_addr(smem) + gr * LY::kQBytes, 16, 1024);
-        uint32_t kt = 0;                 // key tiles of the CTA
-        uint32_t tp = 0;                 // those that this query tile took part in
+        const uint32_t t_s = __shfl_sync(kFull, tmem, 0), t_o = t_s + 128;
+        const uint64_t qa_d = tc::desc_sw128(smem_addr(smem), 16, 1024);
+        uint32_t kt = 0;                 // key tiles
         bool ok = true;
         auto reach = [&](uint64_t *bar, uint32_t parity) {
             ok = __all_sync(kFull, mbar_wait(smem_addr(bar), parity, abort_flag, p.status));
             return ok;
         };
-        // P V of tile tp - 1, the CTA's tile vt
+        // P V of tile vt
         auto issue_pv = [&](uint32_t vt) {
-            const uint32_t slot = vt % NV, par = (vt / NV) & 1u, b = (tp - 1) & 1u;
-            if (!reach(&clean[slot], par) || !reach(&v_full[slot], par) ||
-                !reach(&p_full[2 * gr + b], ((tp - 1) >> 1) & 1u))
-                return;
+            const uint32_t slot = vt % NV, par = (vt / NV) & 1u, b = vt & 1u;
+            if (!reach(&clean[slot], par) || !reach(&v_full[slot], par) || !reach(&p_full[b], (vt >> 1) & 1u)) return;
             tc::fence_after_sync();
             const uint64_t vb_d = tc::desc_sw128(smem_addr(smem + LY::kVRing + slot * LY::kTileBytes), kKeys * 128, 1024);
             if (elect_one()) {
@@ -655,50 +642,35 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                     const int kk = 2 * (i >> 2) + (i & 1);
                     tc::mma_f16_ts(t_o, t_s + 64 * b + 8 * i, vb_d + (uint64_t)((kk * 16 * 128) >> 4), id_pv, true);
                 }
-                tc::mma_commit(smem_addr(&o_full[2 * gr + b]));
+                tc::mma_commit(smem_addr(&o_full[b]));
                 tc::mma_commit(smem_addr(&v_empty[slot]));
             }
             __syncwarp();
         };
         while (ok && __all_sync(kFull, next_task()) && reach(q_full, nt & 1u)) {
-            if (it.first + gr * QT >= it.n) {                // no rows: only give the buffers back
-                if (lane == 0) mbar_arrive(smem_addr(q_empty));
 #pragma unroll 1
-                for (int t = it.t0; t < it.t1; ++t, ++kt) {
-                    if (!reach(&k_full[kt % NK], (kt / NK) & 1u)) break;
-                    if (lane == 0) mbar_arrive(smem_addr(&k_empty[kt % NK]));
-                    if (!reach(&v_full[kt % NV], (kt / NV) & 1u)) break;
-                    if (lane == 0) mbar_arrive(smem_addr(&v_empty[kt % NV]));
-                }
-            } else {
-#pragma unroll 1
-                for (int t = it.t0; t <= it.t1; ++t) {
-                    if (t < it.t1) {
-                        const uint32_t slot = kt % NK;
-                        if (!reach(&k_full[slot], (kt / NK) & 1u)) break;
-                        tc::fence_after_sync();
-                        const uint64_t kb_d = tc::desc_sw128(smem_addr(smem + LY::kKRing + slot * LY::kTileBytes), 16, 1024);
-                        if (elect_one()) {
+            for (int t = it.t0; t <= it.t1; ++t) {
+                if (t < it.t1) {
+                    const uint32_t slot = kt % NK;
+                    if (!reach(&k_full[slot], (kt / NK) & 1u)) break;
+                    tc::fence_after_sync();
+                    const uint64_t kb_d = tc::desc_sw128(smem_addr(smem + LY::kKRing + slot * LY::kTileBytes), 16, 1024);
+                    if (elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint32_t off = (kk & 3) * 32;          // 16 values inside the row
-                                tc::mma_f16(t_s + 64 * (tp & 1u),
-                                            qa_d + (uint64_t)(((kk >> 2) * kRows * 128 + off) >> 4),
-                                            kb_d + (uint64_t)(((kk >> 2) * kKeys * 128 + off) >> 4), id_qk, kk > 0);
-                            }
-                            tc::mma_commit(smem_addr(&s_full[2 * gr + (tp & 1u)]));
-                            tc::mma_commit(smem_addr(&k_empty[slot]));
-                            if (t == it.t1 - 1) tc::mma_commit(smem_addr(q_empty));
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = (kk & 3) * 32;              // 16 values inside the row
+                            tc::mma_f16(t_s + 64 * (kt & 1u), qa_d + (uint64_t)(((kk >> 2) * kRows * 128 + off) >> 4),
+                                        kb_d + (uint64_t)(((kk >> 2) * kKeys * 128 + off) >> 4), id_qk, kk > 0);
                         }
-                        __syncwarp();
+                        tc::mma_commit(smem_addr(&s_full[kt & 1u]));
+                        tc::mma_commit(smem_addr(&k_empty[slot]));
+                        if (t == it.t1 - 1) tc::mma_commit(smem_addr(q_empty));
                     }
-                    if (t > it.t0) issue_pv(kt - 1);
-                    if (!ok) break;
-                    if (t < it.t1) {
-                        ++tp;
-                        ++kt;
-                    }
+                    __syncwarp();
                 }
+                if (t > it.t0) issue_pv(kt - 1);
+                if (!ok) break;
+                if (t < it.t1) ++kt;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&task_empty[nt % kTasks]));
@@ -706,9 +678,9 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
         }
         // every MMA this warp issued has completed before the columns are freed
         if (elect_one()) {
-            tc::mma_commit(smem_addr(&done[gr]));
+            tc::mma_commit(smem_addr(done));
             const unsigned long long t0 = globaltimer();
-            while (!mbar_try_wait(smem_addr(&done[gr]), 0)) {
+            while (!mbar_try_wait(smem_addr(done), 0)) {
                 if (globaltimer() - t0 > kTimeoutNs) {
                     atomicOr(p.status, PKV_DEV_TIMEOUT);
                     break;
@@ -716,7 +688,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
             }
         }
         __syncwarp();
-    } else if (warp == LY::kCleaner) {
+    } else if (warp == kCleaner) {
         uint32_t vt = 0;
         bool ok = true;
         for (; ok && next_task(); ++nt) {
@@ -771,14 +743,14 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
         }
     }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LY::kRegsSoftmax));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---------------------------------------------------------- softmax
-        const int gr = warp >> 2, r = threadIdx.x - kRows * gr;
-        const uint32_t t_s = tmem + 256 * gr + ((uint32_t)(32 * (warp & 3)) << 16), t_o = t_s + 128;
+        const int r = threadIdx.x;
+        const uint32_t t_s = tmem + ((uint32_t)(32 * warp) << 16), t_o = t_s + 128;
         const int jj = r / G, h = r - jj * G;
         // product of a hidden key: the scale carries it to -inf (it is never zero, see the host)
         const float hide = p.scale_log2 < 0.f ? INFINITY : -INFINITY;
-        uint32_t kt = 0, tp = 0;         // key tiles of the CTA; those with rows of this query tile
+        uint32_t kt = 0;                 // key tiles
         bool alive = true;
         // the item is done with
         auto leave = [&]() {
@@ -790,12 +762,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
             it = tasks[nt % kTasks];
             if (it.t0 >= it.t1) break;
             const int n = it.n, base = it.base, L = it.L();
-            const int token = it.first + gr * QT + jj;
-            if (it.first + gr * QT >= n) {               // no rows in this query tile
-                kt += (uint32_t)(it.t1 - it.t0);
-                leave();
-                continue;
-            }
+            const int token = it.first + jj;
             const bool valid = r < QT * G && token < n;
             const bool busy = __any_sync(kFull, valid);  // some row of the warp counts
             const uint32_t *words = p.mask + (int64_t)(it.r0 + (valid ? token : it.first)) * p.words;
@@ -809,12 +776,12 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
 #pragma unroll
                 for (int c0 = 0; c0 < D; c0 += 32) tc::tmem_st32(t_o + c0, z);
             }
-            for (int t = it.t0; t < it.t1; ++t, ++tp, ++kt) {
-                const uint32_t b = tp & 1u, vslot = kt % NV;
-                const bool got = mbar_wait(smem_addr(&s_full[2 * gr + b]), (tp >> 1) & 1u, abort_flag, p.status);
+            for (int t = it.t0; t < it.t1; ++t, ++kt) {
+                const uint32_t b = kt & 1u, vslot = kt % NV;
+                const bool got = mbar_wait(smem_addr(&s_full[b]), (kt >> 1) & 1u, abort_flag, p.status);
                 if (!__all_sync(kFull, got)) { alive = false; break; }
                 if (!busy) {
-                    if (lane == 0) mbar_arrive(smem_addr(&p_full[2 * gr + b]));
+                    if (lane == 0) mbar_arrive(smem_addr(&p_full[b]));
                     continue;
                 }
                 tc::fence_after_sync();
@@ -901,7 +868,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                 // wait for that consumes its o_full phase either here or after P is out
                 const bool touch = __any_sync(kFull, resc) || odd;
                 if (touch && t > it.t0) {
-                    const bool ended = mbar_wait(smem_addr(&o_full[2 * gr + (b ^ 1u)]), ((tp - 1) >> 1) & 1u, abort_flag, p.status);
+                    const bool ended = mbar_wait(smem_addr(&o_full[b ^ 1u]), ((kt - 1) >> 1) & 1u, abort_flag, p.status);
                     if (!__all_sync(kFull, ended)) { alive = false; break; }
                     tc::fence_after_sync();
                 }
@@ -941,16 +908,16 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&p_full[2 * gr + b]));
+                if (lane == 0) mbar_arrive(smem_addr(&p_full[b]));
                 if (!touch && t > it.t0) {
-                    const bool ended = mbar_wait(smem_addr(&o_full[2 * gr + (b ^ 1u)]), ((tp - 1) >> 1) & 1u, abort_flag, p.status);
+                    const bool ended = mbar_wait(smem_addr(&o_full[b ^ 1u]), ((kt - 1) >> 1) & 1u, abort_flag, p.status);
                     if (!__all_sync(kFull, ended)) { alive = false; break; }
                 }
             }
             if (!alive) break;
             // ---- the part's result, once its last P V is done (which writes the lanes of warps
             // without rows too: they wait before another item's zeros)
-            const bool ended = mbar_wait(smem_addr(&o_full[2 * gr + ((tp - 1) & 1u)]), ((tp - 1) >> 1) & 1u, abort_flag, p.status);
+            const bool ended = mbar_wait(smem_addr(&o_full[(kt - 1) & 1u]), ((kt - 1) >> 1) & 1u, abort_flag, p.status);
             if (!__all_sync(kFull, ended)) break;
             tc::fence_after_sync();
             if (!busy) {
@@ -959,15 +926,14 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
             }
             if (it.t0 > 0 || it.t1 * kKeys < L) {
                 const int64_t piece = 2 * blockIdx.x + (it.t0 == 0);
-                const int rr = gr * kRows + r;
-                if (valid) p.part_ml[piece * p.piece_rows + rr] = make_float2(ref, bad ? -1.f : l);
+                if (valid) p.part_ml[piece * p.piece_rows + r] = make_float2(ref, bad ? -1.f : l);
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t v[32];
                     tc::tmem_ld32(t_o + c0, v);
                     tc::tmem_wait_ld();
                     if (valid) {
-                        float4 *dst = p.part_o + (piece * (D / 4) + c0 / 4) * p.piece_rows + rr;
+                        float4 *dst = p.part_o + (piece * (D / 4) + c0 / 4) * p.piece_rows + r;
 #pragma unroll
                         for (int c = 0; c < 32; c += 4)
                             dst[(int64_t)(c / 4) * p.piece_rows] =
@@ -1004,7 +970,7 @@ __global__ void __launch_bounds__(Layout<D, NG>::kThreads, NG == 1 ? 2 : 1)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 0) tc::tmem_dealloc(tmem, LY::kColumns);
+    if (warp == 0) tc::tmem_dealloc(tmem, kColumns);
 }
 
 // ------------------------------------------------------------------ joining the pieces
@@ -1017,12 +983,9 @@ static_assert(kJoinThreads >= kMaxRanges, "a thread for each range");
 
 __device__ __forceinline__ int ways_of(int pieces) { return pieces > 16 ? 8 : pieces > 8 ? 4 : pieces > 4 ? 2 : 1; }
 
-// Rows of an item that count: those of full query tiles before the last one's.
 __device__ __forceinline__ int tasks_of(const Params &p, int D, int tokens)
 {
-    const int before = (tokens - 1) / p.tile_tokens;
-    const int rows = before * kRows + (tokens - before * p.tile_tokens) * p.group;
-    return (rows + 31) / 32 * (D / 8);
+    return (tokens * p.group + 31) / 32 * (D / 8);
 }
 
 template <int D, bool BF16>
@@ -1066,7 +1029,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1) tree_join_kernel(const Params
     if (tid < items) passes[tid] = upto - n;
     if (tid == 0) passes[items] = all;
     __syncthreads();
-    const int G = p.group, QT = p.tile_tokens;
+    const int G = p.group;
     const float sc = p.scale_log2, hide = sc < 0.f ? INFINITY : -INFINITY;
     __shared__ float shares[kJoinWarps][11][32];
     for (int pass = blockIdx.x; pass < passes[items]; pass += gridDim.x) {
@@ -1078,9 +1041,8 @@ __global__ void __launch_bounds__(kJoinThreads, 1) tree_join_kernel(const Params
         const int tasks = tasks_of(p, D, tokens), ways = ways_of(pieces), mine = warp % ways;
         const int task = (pass - passes[item]) * (kJoinWarps / ways) + warp / ways;
         const int rr = task / (D / 8) * 32 + lane, c8 = task % (D / 8);
-        const int gr = rr / kRows, jj = (rr - gr * kRows) / G, h = rr - gr * kRows - jj * G;
-        const int token = gr * QT + jj;
-        const bool valid = task < tasks && jj < QT && token < tokens;
+        const int token = rr / G, h = rr - token * G;
+        const bool valid = task < tasks && token < tokens;
         float ref = hide, l = 0.f, o[8] = {};
         bool bad = false;
         auto add = [&](float2 ml, const float (&v)[8]) {
@@ -1211,29 +1173,21 @@ using JoinFn = void (*)(Params);
 struct Pick {
     KernelFn fn;
     JoinFn join;
-    int smem, threads, ctas, regs;     // ctas: to an SM
+    int smem;
 };
 
-template <int D, bool BF16, int NG>
+template <int D, bool BF16>
 static Pick pick_of()
 {
-    return {&tree_kernel<D, BF16, NG>, &tree_join_kernel<D, BF16>, Layout<D, NG>::kTotal,
-            Layout<D, NG>::kThreads, NG == 1 ? 2 : 1, Layout<D, NG>::kLaunchRegs};
-}
-
-template <int NG>
-static Pick pick(int D, bool bf16)
-{
-    if (D == 128) return bf16 ? pick_of<128, true, NG>() : pick_of<128, false, NG>();
-    return bf16 ? pick_of<64, true, NG>() : pick_of<64, false, NG>();
+    return {&tree_kernel<D, BF16>, &tree_join_kernel<D, BF16>, Layout<D>::kTotal};
 }
 
 // CTAs of a kernel that fit the current device at once, cached per device and kernel.  (The
 // runtime's own count is one to an SM for every kernel that allocates tensor memory; two of
-// NG = 1 take 512 columns, all there are.)
+// these take 512 columns, all there are.)
 static int resident(const Pick &k, int slot)
 {
-    constexpr int kMaxDev = 64, kSlots = 8;
+    constexpr int kMaxDev = 64, kSlots = 4;
     static std::mutex mu;
     static int ctas[kMaxDev][kSlots];
     int dev = 0;
@@ -1244,7 +1198,7 @@ static int resident(const Pick &k, int slot)
         const void *fn = reinterpret_cast<const void *>(k.fn);
         int sms = 0, shared = 0, reserved = 0;
         cudaFuncAttributes a;
-        if (cudaFuncGetAttributes(&a, fn) != cudaSuccess || a.numRegs != k.regs) return -1;
+        if (cudaFuncGetAttributes(&a, fn) != cudaSuccess || a.numRegs != kLaunchRegs) return -1;
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&shared, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev) != cudaSuccess ||
@@ -1252,7 +1206,7 @@ static int resident(const Pick &k, int slot)
             cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
                                  cudaSharedmemCarveoutMaxShared) != cudaSuccess)
             return -1;
-        n = sms * (k.ctas == 2 && 2 * (k.smem + reserved) <= shared ? 2 : 1);
+        n = sms * (2 * (k.smem + reserved) <= shared ? 2 : 1);
     }
     return n;
 }
@@ -1301,9 +1255,8 @@ extern "C" int paged_tree_attention(const pkv_pool *pool, void *out, const void 
     if ((int64_t)g.num_blocks * g.num_kv_heads * g.block_size > (int64_t)1 << 31)
         return PKV_ERR_UNSUPPORTED;
     const bool bf16 = g.dtype == PKV_BF16;
-    // two query tiles to a CTA where the rows of an average sequence need more than one
-    const bool two = (int64_t)num_tokens * G > (int64_t)kRows * num_seqs;
-    const Pick k = two ? pick<2>(D, bf16) : pick<1>(D, bf16);
+    const Pick k = D == 128 ? (bf16 ? pick_of<128, true>() : pick_of<128, false>())
+                            : (bf16 ? pick_of<64, true>() : pick_of<64, false>());
 
     Params prm;
     prm.out = out;
@@ -1323,11 +1276,10 @@ extern "C" int paged_tree_attention(const pkv_pool *pool, void *out, const void 
     prm.num_blocks = g.num_blocks;
     prm.tile_tokens = tile_tokens(G);
     prm.box_tokens = box_tokens(G);
-    prm.set_tokens = (two ? 2 : 1) * prm.tile_tokens;
-    prm.set_inverse = ((1 << 20) + prm.set_tokens - 1) / prm.set_tokens;
-    prm.piece_rows = two ? 2 * kRows : (int32_t)piece_rows(num_tokens, G);
+    prm.tile_inverse = ((1 << 20) + prm.tile_tokens - 1) / prm.tile_tokens;
+    prm.piece_rows = (int32_t)piece_rows(num_tokens, G);
     // the ranges are counted in 32 bits
-    const double most = ((double)num_tokens / prm.set_tokens + num_seqs) * g.num_kv_heads *
+    const double most = ((double)num_tokens / prm.tile_tokens + num_seqs) * g.num_kv_heads *
                         (prm.max_tokens / kKeys + 1 + kItemCost);
     if (most > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     // scores are hidden by an infinity that the scale must carry into the exponent; at scale 0
@@ -1350,16 +1302,16 @@ extern "C" int paged_tree_attention(const pkv_pool *pool, void *out, const void 
     if (!make_map(&tk, k_pool, bf16, 2, rows, row_bytes, block) ||
         !make_map(&tv, v_pool, bf16, 2, rows, row_bytes, block) || !make_map(&tq, q, bf16, 4, qd, qs, qb))
         return PKV_ERR_CUDA;
-    const int fit = resident(k, (D == 128) * 4 + bf16 * 2 + two);
+    const int fit = resident(k, (D == 128) * 2 + bf16);
     if (fit < 1) return PKV_ERR_CUDA;
 
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    prm.grid = std::min(fit, two ? kMaxRanges / 2 : kMaxRanges);
+    prm.grid = std::min(fit, kMaxRanges);
     cfg.gridDim = dim3((unsigned)prm.grid);
-    cfg.blockDim = dim3((unsigned)k.threads);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = (size_t)k.smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = pdl;
