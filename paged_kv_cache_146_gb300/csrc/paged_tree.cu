@@ -202,11 +202,12 @@ struct Walk {
         all = __reduce_add_sync(kFull, all);
         most = __reduce_max_sync(kFull, most);
         const uint32_t ranges = max(1u, min(gridDim.x, all / kMinRange));
-        // the first `more` ranges have a unit more
+        // range b begins at all b / ranges: the rest is spread evenly, so that CTAs at the same
+        // place among first and among second query tiles keep in step
         const uint32_t size = all / ranges, more = all - size * ranges;
         const int snap = min(kSnap, (int)(size / 4));
-        const uint32_t begin = size * blockIdx.x + min(blockIdx.x, more);
-        const uint32_t end = begin + size + (blockIdx.x < more);
+        const uint32_t begin = size * blockIdx.x + more * blockIdx.x / ranges;
+        const uint32_t end = size * (blockIdx.x + 1) + more * (blockIdx.x + 1) / ranges;
         at = to = Place{most, 0, 0, 0};
         int4 left = make_int4(0, 0, 0, 0);               // for the joining kernel
         uint32_t before = 0;
