@@ -40,8 +40,8 @@ struct Trees {
 
 // A warp per sequence.  Trees of up to kHeld nodes are read at once, one latency for all, and
 // walked in registers: a step takes the target from the lane that holds the last kept node and
-// asks all nodes whether they are its child and hold that token.  256 trees of 21 to 64 nodes: 3.2
-// us back to back (5.7 when each step read its nodes from L1), of which the launch is most.
+// asks all nodes whether they are its child and hold that token.  256 trees of 21 to 64 nodes: 3.9
+// us back to back (6.4 when each step read its nodes from L1; one small tree 2.5, the launch).
 constexpr int kAcceptWarps = 4, kSteps = 4, kHeld = 32 * kSteps;
 
 template <typename T>
@@ -143,23 +143,42 @@ struct Moves {
 // else reads or writes these bytes.  It goes through the kept tokens in order, a batch at a time:
 // all of the batch's rows are read, then written.  A destination is never above its source and
 // sources rise, so what a batch writes is no source of a later one.
-// The chain list -> table -> row -> store bounds it, and how many rows are under way at
-// once: places are looked up once for a CTA and a batch ahead of the rows, the list is read two
-// ahead.  Nine caches of up to 16,384 tokens that keep 40,000 in all (305 MB moved): 68 us,
-// 4.5 TB/s (floor 45; the longest list's 8,000 tokens set the end); 155 us with whole rows to a
-// CTA (64 bytes here, so that few sequences fill the GPU), 280 before places were looked up ahead.
-constexpr int kMoveThreads = 256, kMoveDepth = 8, kMoveBatch = 512;
-constexpr int kMoveCtas = 608;           // four to an SM
+// The chain list -> table -> row -> store bounds it, and how many rows are under way at once:
+// places are looked up once for a CTA and a batch ahead of the rows, the list is read two ahead.
+// Nine caches of up to 16,384 tokens that keep 40,000 in all (305 MB moved): 71 us, 4.3 TB/s
+// (floor 45; the longest list's 8,000 tokens set the end); 93 us with whole rows to a CTA, four
+// times as long when each thread looked up its rows' places.
+//
+// Threads, chunks of a thread under way, tokens of a batch at most, CTAs to an SM.  What is under
+// way on an SM is the same for all; larger CTAs wait for their slowest row and end later, so they
+// are only for calls with no more CTAs than SMs (a cache of 16,000 tokens: 64 of them, 31 us
+// against 63 with Many; 100 caches of 300 to 900 tokens, 1,600 CTAs: 77 against 59).  Lists that
+// end within a batch want the fewer steps of Brief (96 lists of up to 60: 4.5 us against 6.2; the
+// nine caches: 81 against 71).
+struct Few {
+    static constexpr int kThreads = 1024, kDepth = 4, kBatch = 960, kCtas = 1;   // 46 KB of places
+};
+struct Brief {
+    static constexpr int kThreads = 256, kDepth = 4, kBatch = 512, kCtas = 3;
+};
+struct Many {
+    static constexpr int kThreads = 256, kDepth = 8, kBatch = 512, kCtas = 3;
+};
+constexpr int kFewCtas = 152, kBriefList = 128;
+constexpr int kMoveCtas = 608;           // rows are shared until there are four CTAs for an SM (the nine caches
+                                         // 104 us with two, 71 with eight; 5 caches of 40 heads 65)
 
 struct Place {
     int64_t from, to;                    // token rows of kv head 0 in the pool, -1: does not move
 };
 
-__global__ void __launch_bounds__(kMoveThreads, 3) compact_kernel(const Moves p)
+template <typename C>
+__global__ void __launch_bounds__(C::kThreads, C::kCtas) compact_kernel(const Moves p)
 {
+    constexpr int kThreads = C::kThreads, kDepth = C::kDepth;
     // of three batches: a thread may look up the one after the next while another still writes
     // this one's rows
-    __shared__ Place places[3][kMoveBatch];
+    __shared__ Place places[3][C::kBatch];
     __shared__ int stops[3];             // first entry that may not move, n: none
     griddep_launch_dependents();
     griddep_wait();
@@ -172,7 +191,7 @@ __global__ void __launch_bounds__(kMoveThreads, 3) compact_kernel(const Moves p)
     const int part = blockIdx.x % p.parts, pair0 = blockIdx.x / p.parts * p.pairs;
     const int pairs = min(p.pairs, 2 * p.num_kv_heads - pair0);
     const int c0 = part * p.part_chunks, nc = min(p.part_chunks, p.chunks - c0);
-    const int per_pass = kMoveThreads / nc;              // rows of one pass of the threads
+    const int per_pass = kThreads / nc;              // rows of one pass of the threads
     const int c = tid % nc, k = tid / nc;
     const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
     const int32_t *kept = p.kept + start;
@@ -183,12 +202,12 @@ __global__ void __launch_bounds__(kMoveThreads, 3) compact_kernel(const Moves p)
     };
     // The list runs two batches ahead of the rows, the places one: `fetch` takes a thread's entries
     // of the batch from i0 on, `look_up` finds their places.
-    constexpr int kEntries = kMoveBatch / kMoveThreads;
+    constexpr int kEntries = (C::kBatch + kThreads - 1) / kThreads;
     int pos[kEntries], before[kEntries];
     auto fetch = [&](int i0) {
 #pragma unroll
         for (int j = 0; j < kEntries; ++j) {
-            const int e = j * kMoveThreads + tid, i = i0 + e;
+            const int e = j * kThreads + tid, i = i0 + e;
             const bool mine = e < p.batch && i < n;
             pos[j] = mine ? kept[i] : 0;
             before[j] = mine && i > 0 ? kept[i - 1] : -1;
@@ -197,7 +216,7 @@ __global__ void __launch_bounds__(kMoveThreads, 3) compact_kernel(const Moves p)
     auto look_up = [&](int i0, int buffer) {
 #pragma unroll
         for (int j = 0; j < kEntries; ++j) {
-            const int e = j * kMoveThreads + tid, i = i0 + e;
+            const int e = j * kThreads + tid, i = i0 + e;
             if (e >= p.batch || i >= n) continue;
             const int64_t dst = (int64_t)first + i;
             Place x = {-1, -1};
@@ -221,7 +240,7 @@ __global__ void __launch_bounds__(kMoveThreads, 3) compact_kernel(const Moves p)
     __syncthreads();
     for (int i0 = 0, buffer = 0; i0 < n; i0 += p.batch, buffer = buffer == 2 ? 0 : buffer + 1) {
         const int count = min(p.batch, n - i0), stop = stops[buffer];
-        uint4 v[kMoveDepth];
+        uint4 v[kDepth];
         // the thread's d-th chunk of the batch: where it comes from and goes to, null: nowhere
         auto chunk = [&](int d, bool source) -> uint4 * {
             const int r = d * per_pass + k, pair = pairs == 1 ? 0 : r / p.batch, e = r - pair * p.batch;
@@ -232,7 +251,7 @@ __global__ void __launch_bounds__(kMoveThreads, 3) compact_kernel(const Moves p)
                    (at + (int64_t)((pair0 + pair) >> 1) * p.block_size) * p.chunks;
         };
 #pragma unroll
-        for (int d = 0; d < kMoveDepth; ++d)
+        for (int d = 0; d < kDepth; ++d)
             if (const uint4 *from = chunk(d, true)) v[d] = *from;
         if (stop >= n) {
             look_up(i0 + p.batch, buffer == 2 ? 0 : buffer + 1);
@@ -240,13 +259,26 @@ __global__ void __launch_bounds__(kMoveThreads, 3) compact_kernel(const Moves p)
         }
         __syncthreads();                                 // every row of the batch is read
 #pragma unroll
-        for (int d = 0; d < kMoveDepth; ++d)
+        for (int d = 0; d < kDepth; ++d)
             if (uint4 *to = chunk(d, false)) *to = v[d];
         if (stop < n) {                                  // the same for the CTA
             if (blockIdx.x == 0 && tid == 0) atomicOr(p.status, PKV_DEV_BAD_TREE);
             return;
         }
     }
+}
+
+// Short lists: as many pairs to a CTA as fill its batch.
+template <typename C>
+static int launch_moves(Moves p, int parts, int num_seqs, int64_t average, cudaStream_t st)
+{
+    p.part_chunks = std::min((p.chunks + parts - 1) / parts, C::kThreads);
+    p.parts = (p.chunks + p.part_chunks - 1) / p.part_chunks;
+    const int rows = C::kThreads / p.part_chunks * C::kDepth, all = 2 * p.num_kv_heads;
+    p.pairs = (int32_t)std::max<int64_t>(1, std::min<int64_t>(rows / std::max<int64_t>(1, average), all));
+    p.batch = std::min(rows / p.pairs, C::kBatch);
+    const dim3 grid((unsigned)((all + p.pairs - 1) / p.pairs * p.parts), (unsigned)num_seqs);
+    return launch(&compact_kernel<C>, grid, C::kThreads, st, p);
 }
 
 }  // namespace compact
@@ -285,7 +317,7 @@ extern "C" int kv_cache_compact(const pkv_pool *pool, const int32_t *block_table
     pkv::PoolGeometry g;
     if (!pkv::pool_geometry(pool, &g) || !pkv::is_16bit(g)) return PKV_ERR_INVALID_ARG;
     if (num_seqs < 0 || num_entries < 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
-    if (g.head_dim % 8) return PKV_ERR_UNSUPPORTED;
+    if (g.head_dim % 8 || num_seqs > 65535 || num_entries > INT32_MAX - 8192) return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0 || num_entries == 0) return PKV_OK;
     if (!block_tables || !kept || !kept_start || !num_kept || !first || !k_pool || !v_pool || !d_status)
         return PKV_ERR_INVALID_ARG;
@@ -305,19 +337,14 @@ extern "C" int kv_cache_compact(const pkv_pool *pool, const int32_t *block_table
     p.block_size = g.block_size;
     p.num_blocks = g.num_blocks;
     p.chunks = g.head_dim / 8;
-    const int64_t average = std::max<int64_t>(1, num_entries / num_seqs);
-    // long lists of few sequences share each row among CTAs, down to 64 bytes
-    const int64_t ctas = (int64_t)num_seqs * g.num_kv_heads * 2;
-    const int parts = average <= 128 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(p.chunks / 4, kMoveCtas / ctas));
-    p.part_chunks = std::min((p.chunks + parts - 1) / parts, kMoveThreads);
-    p.parts = (p.chunks + p.part_chunks - 1) / p.part_chunks;
-    const int rows = kMoveThreads / p.part_chunks * kMoveDepth;      // of a batch
-    p.pairs = (int32_t)std::max<int64_t>(1, std::min<int64_t>(rows / average, 2 * g.num_kv_heads));
-    p.batch = std::min(rows / p.pairs, kMoveBatch);
     p.k_pool = static_cast<uint4 *>(k_pool);
     p.v_pool = static_cast<uint4 *>(v_pool);
     p.status = d_status;
-    if (num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)((g.num_kv_heads * 2 + p.pairs - 1) / p.pairs * p.parts), (unsigned)num_seqs);
-    return launch(&compact_kernel, grid, kMoveThreads, (cudaStream_t)stream, p);
+    // a row is shared among CTAs where there are few, down to 64 bytes
+    const int64_t ctas = (int64_t)num_seqs * g.num_kv_heads * 2, average = num_entries / num_seqs;
+    const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(p.chunks / 4, kMoveCtas / ctas));
+    const cudaStream_t st = (cudaStream_t)stream;
+    if (ctas * parts <= kFewCtas) return launch_moves<Few>(p, parts, num_seqs, average, st);
+    if (average <= kBriefList) return launch_moves<Brief>(p, parts, num_seqs, average, st);
+    return launch_moves<Many>(p, parts, num_seqs, average, st);
 }
