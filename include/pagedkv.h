@@ -693,7 +693,9 @@ size_t paged_tree_workspace_bytes(int32_t num_tokens, int32_t num_q_heads, int32
  *              of no account before and after; calls that may run at the same
  *              time need one each
  * 16-bit pools, head_dim 64 or 128, block_size 16, num_q_heads / num_kv_heads
- * <= 16; results do not vary from run to run.
+ * <= 16; results do not vary from run to run.  Lengths whose key tiles (64 keys)
+ * of all sequences, kv heads and query tiles could pass 2^31 are
+ * PKV_ERR_UNSUPPORTED.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA. */
 int paged_tree_attention(const pkv_pool *pool, void *out, const void *q, const void *k_pool,
                          const void *v_pool, const int32_t *block_tables,
@@ -742,7 +744,8 @@ int kv_tree_accept(const void *tokens, const int32_t *parents, const void *targe
  * first position that does not rise, lies below its destination or outside the
  * table row on, the rest of the sequence's stay where they are
  * (PKV_DEV_BAD_TREE); a token whose own or destination block is not in the pool
- * is skipped (PKV_DEV_BAD_BLOCK).  16-bit pools, rows of a multiple of 16 bytes.
+ * is skipped (PKV_DEV_BAD_BLOCK).  16-bit pools, rows of a multiple of 16 bytes,
+ * at most 65,535 sequences.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA. */
 int kv_cache_compact(const pkv_pool *pool, const int32_t *block_tables,
                      int32_t max_blocks_per_seq, const int32_t *kept, const int32_t *kept_start,

@@ -15,7 +15,14 @@
 // Items go first query tiles first, by sequence and kv head, then the second ones, and so on:
 // where trees need two tiles, two CTAs read the same keys at about the same time, one of
 // them from L2.  Two CTAs fit an SM, with 256 columns of tensor memory each; while one waits for
-// its softmax or begins an item, the other keeps copies and products going.
+// its softmax or begins an item, the other keeps copies and products going (96 long sequences
+// 795 us with one CTA, 554 with two, then).
+//
+// What bounds it, 32 query heads over 8 of 128: at 96 sequences of up to 16,384 tokens with 16
+// drafted ones the copies of K and V (3.43 GB in 523 us, 6.6 TB/s; a plain copy's rate is
+// 6.8); at 24 sequences with 64 drafted, two full query tiles each, the softmax (143 us; the
+// bytes alone 70, the products 59); at 4 sequences, 22 us, the chain of lengths -> plan -> block
+// ids -> tiles -> pieces -> joining kernel (the bytes 6).
 //
 // Roles of a CTA's warps:
 //   0-3, softmax: thread r owns row r.  Weights are taken against a lazy reference (it moves
@@ -34,6 +41,8 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
+#include <cmath>
 #include <mutex>
 
 #include "pagedkv.h"
@@ -47,13 +56,14 @@ namespace tree {
 constexpr int kRows = 128;             // M: rows of a query tile
 constexpr int kKeys = 64;              // keys of a tile
 constexpr int kMaxWords = 32;
-constexpr int kTilesKnown = 16;
-constexpr int kTasks = 8;               // items under way, at most
-constexpr int kAhead = 2;               // lengths of so many 32 sequences are read at once
+constexpr int kTilesKnown = 16;        // tiles whose bad blocks are remembered
+constexpr int kTasks = 8;              // items under way, at most
+constexpr int kAhead = 2;              // lengths of so many 32 sequences are read at once
 constexpr float kLazy = 8.f;
-constexpr int kItemCost = 2;           // an item's beginning and end, in tiles
-constexpr int kMinRange = 2;           // a range has at least so many
-constexpr int kSnap = 2;               // no piece shorter than this is cut off an item
+// An item's beginning and end, in tiles (20 ragged sequences of 40 kv heads: 94 us, 125 when items
+// cost nothing, 95 when 4), and the shortest piece that is cut off an item (24 sequences of 64
+// drafted tokens: 143 us, 147 with 1; the 40 heads 97 with 4).
+constexpr int kItemCost = 2, kSnap = 2;
 constexpr int kMaxRanges = 304;        // CTAs of a call, at most
 
 struct Params {
@@ -201,7 +211,7 @@ struct Walk {
         }
         all = __reduce_add_sync(kFull, all);
         most = __reduce_max_sync(kFull, most);
-        const uint32_t ranges = max(1u, min(gridDim.x, all / kMinRange));
+        const uint32_t ranges = max(1u, min(gridDim.x, all));
         // range b begins at all b / ranges: the rest is spread evenly, so that CTAs at the same
         // place among first and among second query tiles keep in step
         const uint32_t size = all / ranges, more = all - size * ranges;
@@ -387,7 +397,8 @@ __device__ __forceinline__ void add_odd(uint32_t &sum, uint32_t w)
 template <int D>
 struct Layout {
     static constexpr int kRegions = D / 64;
-    // K and V tiles in flight, a ring each (V waits for the softmax, K does not)
+    // K and V tiles in flight, a ring each (V waits for the softmax, K does not: 24 sequences of
+    // 64 drafted tokens 143 us with 2 and 3, 147 with 3 and 2)
     static constexpr int kK = D == 128 ? 2 : 6, kV = D == 128 ? 3 : 6;
     static constexpr int kQBytes = kRegions * kRows * 128;     // a query tile: [region][row][128 B]
     static constexpr int kTileBytes = kRegions * kKeys * 128;  // a K or V tile
@@ -415,8 +426,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     using T = typename E::T;
     using LY = Layout<D>;
     constexpr int NK = LY::kK, NV = LY::kV;
-    // fp16 pools take their weights times 2^kTop: they stay within 2^15, and those down to 2^-21 of the largest are normal numbers in fp16 (a row
-    // far below a few dominant keys would lose its weights' bits).
+    // fp16 pools take their weights times 2^kTop: they stay within 2^15, and those down to 2^-21 of
+    // the largest are normal numbers in fp16 (a row far below a few dominant keys would lose
+    // its weights' bits).
     constexpr float kTop = BF16 ? 0.f : 7.f;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + LY::kMisc);
@@ -426,9 +438,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     // S out; P out; P V done, each for even and odd tiles
     uint64_t *s_full = clean + NV, *p_full = s_full + 2, *o_full = p_full + 2, *done = o_full + 2;
     uint64_t *task_full = done + 1, *task_empty = task_full + kTasks;
-    uint64_t *odd_keys = task_empty + kTasks;                            // [NV]: keys whose V held odd values
-    // tile's bad blocks: a K tile's slot is free once S is out, before the softmax reads this, so
-    // these have places of their own, more than there are tiles under way
+    uint64_t *odd_keys = task_empty + kTasks;            // [NV]: keys whose V held odd values
+    // a tile has a bad block: a K tile's slot is free once S is out, before the softmax reads this,
+    // so these have places of their own, more than there are tiles under way
     uint8_t *bad_blocks = reinterpret_cast<uint8_t *>(odd_keys + NV);   // [kTilesKnown]
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bad_blocks + kTilesKnown);
     volatile int *abort_flag = reinterpret_cast<int *>(tslot + 1);
@@ -493,256 +505,262 @@ __global__ void __launch_bounds__(kThreads, 2)
         return it.t0 < it.t1;
     };
     if (warp >= kProducer) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIo));
-    if (warp == kProducer) {
-        uint32_t kt = 0, vt = 0, items = 0;      // K tiles, V tiles and items under way or done
-        bool ok = true;
-        Walk walk;
-        walk.plan<D>(p);
-        // 32 block ids, 8 tiles, at a time, one batch ahead; behind the end any block will do
-        auto ids_from = [&](const Task &k, int t) {
-            const int b = 4 * t + lane;
-            return b < (k.L() + kBlock - 1) / kBlock ? p.block_tables[(int64_t)k.s * p.max_blocks_per_seq + b] : 0;
-        };
-        // the boxes of an item's query rows
-        auto each_box = [&](const Task &k, auto &&box) {
-            for (int i = 0; i < min(QT, k.n - k.first); i += p.box_tokens)
-                for (int rg = 0; rg < LY::kRegions; ++rg)
-                    box(rg * kRows * 128 + i * G * 128, rg * 64, k.g, k.r0 + k.first + i);
-        };
-        Task after = walk.next(p);
-        int ids_after = after.t0 < after.t1 ? ids_from(after, after.t0) : 0;
-        for (;;) {
-            it = after;
-            if (nt >= kTasks)
-                ok = mbar_wait(smem_addr(&task_empty[nt % kTasks]), (nt / kTasks - 1) & 1u, abort_flag, p.status);
-            ok = __all_sync(kFull, ok);
-            if (!ok) break;
-            if (elect_one()) {
-                tasks[nt % kTasks] = it;
-                mbar_arrive(smem_addr(&task_full[nt % kTasks]));
-            }
-            ++nt;
-            if (it.t0 >= it.t1) break;
-            int ids = ids_after, ids_next = ids_from(it, it.t0 + 8);
-            // the first row of the four blocks of tile t in the pools; all lanes call it
-            auto rows_of = [&](int t, int (&y)[4]) {
-                bool bad = false;
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    int id = __shfl_sync(kFull, ids, ((t - it.t0) & 7) * 4 + b);
-                    if (id < 0 || id >= p.num_blocks) {
-                        bad = true;
-                        id = 0;
-                    }
-                    y[b] = (id * Hkv + it.g) * kBlock;
-                }
-                return bad;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIo));
+        if (warp == kProducer) {
+            uint32_t kt = 0, vt = 0, items = 0;      // K tiles, V tiles and items under way or done
+            bool ok = true;
+            Walk walk;
+            walk.plan<D>(p);
+            // 32 block ids, 8 tiles, at a time, one batch ahead; behind the end any block will do
+            auto ids_from = [&](const Task &k, int t) {
+                const int b = 4 * t + lane;
+                return b < (k.L() + kBlock - 1) / kBlock ? p.block_tables[(int64_t)k.s * p.max_blocks_per_seq + b] : 0;
             };
-            auto copy = [&](const CUtensorMap *map, int at, uint64_t *bar, const int (&y)[4]) {
-                const uint32_t fb = smem_addr(bar), dst = smem_addr(smem + at);
-                mbar_arrive_expect_tx(fb, LY::kTileBytes);
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-#pragma unroll
+            // the boxes of an item's query rows
+            auto each_box = [&](const Task &k, auto &&box) {
+                for (int i = 0; i < min(QT, k.n - k.first); i += p.box_tokens)
                     for (int rg = 0; rg < LY::kRegions; ++rg)
-                        tma_load_2d(dst + rg * kKeys * 128 + b * kBlock * 128, map, rg * 64, y[b], fb);
+                        box(rg * kRows * 128 + i * G * 128, rg * 64, k.g, k.r0 + k.first + i);
             };
-            // K of a tile goes out before V of the tile before it
-            int y_v[4] = {};
-            for (int t = it.t0; t <= it.t1 && ok; ++t) {
-                int y[4] = {};
-                if (t < it.t1) {
-                    if (((t - it.t0) & 7) == 0 && t > it.t0) {
-                        ids = ids_next;
-                        ids_next = ids_from(it, t + 8);
-                    }
-                    const bool bad = rows_of(t, y);
-                    if (kt >= NK)
-                        ok = mbar_wait(smem_addr(&k_empty[kt % NK]), (kt / NK - 1) & 1u, abort_flag, p.status);
-                    ok = __all_sync(kFull, ok);
-                    if (!ok) break;
-                    if (elect_one()) {
-                        if (bad) atomicOr(p.status, PKV_DEV_BAD_BLOCK);
-                        bad_blocks[kt % kTilesKnown] = (uint8_t)bad;
-                        copy(&tmK, LY::kKRing + (kt % NK) * LY::kTileBytes, &k_full[kt % NK], y);
-                    }
-                    ++kt;
+            Task after = walk.next(p);
+            int ids_after = after.t0 < after.t1 ? ids_from(after, after.t0) : 0;
+            for (;;) {
+                it = after;
+                if (nt >= kTasks)
+                    ok = mbar_wait(smem_addr(&task_empty[nt % kTasks]), (nt / kTasks - 1) & 1u, abort_flag, p.status);
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+                if (elect_one()) {
+                    tasks[nt % kTasks] = it;
+                    mbar_arrive(smem_addr(&task_full[nt % kTasks]));
                 }
-                if (t == it.t0) {
-                    // the item's query rows, once its first K tile is under way
-                    if (items > 0) ok = mbar_wait(smem_addr(q_empty), (items - 1) & 1u, abort_flag, p.status);
-                    ok = __all_sync(kFull, ok);
-                    if (!ok) break;
-                    ++items;
-                    if (elect_one()) {
-                        int boxes = 0;
-                        each_box(it, [&](int, int, int, int) { ++boxes; });
-                        const uint32_t qb = smem_addr(q_full);
-                        mbar_arrive_expect_tx(qb, (uint32_t)(boxes * p.box_tokens * G * 128));
-                        each_box(it, [&](int at, int x, int g, int token) {
-                            tc::tma_load_4d(smem_addr(smem + at), &tmQ, x, 0, g, token, qb);
-                        });
-                    }
-                } else {
-                    if (vt >= NV)
-                        ok = mbar_wait(smem_addr(&v_empty[vt % NV]), (vt / NV - 1) & 1u, abort_flag, p.status);
-                    ok = __all_sync(kFull, ok);
-                    if (!ok) break;
-                    if (elect_one())
-                        copy(&tmV, LY::kVRing + (vt % NV) * LY::kTileBytes, &v_full[vt % NV], y_v);
-                    ++vt;
-                }
+                ++nt;
+                if (it.t0 >= it.t1) break;
+                int ids = ids_after, ids_next = ids_from(it, it.t0 + 8);
+                // the first row of the four blocks of tile t in the pools; all lanes call it
+                auto rows_of = [&](int t, int (&y)[4]) {
+                    bool bad = false;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) y_v[b] = y[b];
-                if (t == min(it.t0 + 1, it.t1)) {
-                    // the item after this one: its first block ids, its query rows into L2
-                    after = walk.next(p);
-                    if (after.t0 < after.t1) {
-                        ids_after = ids_from(after, after.t0);
-                        if (elect_one())
-                            each_box(after, [&](int, int x, int g, int token) {
-                                tc::tma_prefetch_4d(&tmQ, x, 0, g, token);
+                    for (int b = 0; b < 4; ++b) {
+                        int id = __shfl_sync(kFull, ids, ((t - it.t0) & 7) * 4 + b);
+                        if (id < 0 || id >= p.num_blocks) {
+                            bad = true;
+                            id = 0;
+                        }
+                        y[b] = (id * Hkv + it.g) * kBlock;
+                    }
+                    return bad;
+                };
+                auto copy = [&](const CUtensorMap *map, int at, uint64_t *bar, const int (&y)[4]) {
+                    const uint32_t fb = smem_addr(bar), dst = smem_addr(smem + at);
+                    mbar_arrive_expect_tx(fb, LY::kTileBytes);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+#pragma unroll
+                        for (int rg = 0; rg < LY::kRegions; ++rg)
+                            tma_load_2d(dst + rg * kKeys * 128 + b * kBlock * 128, map, rg * 64, y[b], fb);
+                };
+                // K of a tile goes out before V of the tile before it
+                int y_v[4] = {};
+                for (int t = it.t0; t <= it.t1 && ok; ++t) {
+                    int y[4] = {};
+                    if (t < it.t1) {
+                        if (((t - it.t0) & 7) == 0 && t > it.t0) {
+                            ids = ids_next;
+                            ids_next = ids_from(it, t + 8);
+                        }
+                        const bool bad = rows_of(t, y);
+                        if (kt >= NK)
+                            ok = mbar_wait(smem_addr(&k_empty[kt % NK]), (kt / NK - 1) & 1u, abort_flag, p.status);
+                        ok = __all_sync(kFull, ok);
+                        if (!ok) break;
+                        if (elect_one()) {
+                            if (bad) atomicOr(p.status, PKV_DEV_BAD_BLOCK);
+                            bad_blocks[kt % kTilesKnown] = (uint8_t)bad;
+                            copy(&tmK, LY::kKRing + (kt % NK) * LY::kTileBytes, &k_full[kt % NK], y);
+                        }
+                        ++kt;
+                    }
+                    if (t == it.t0) {
+                        // the item's query rows, once its first K tile is under way
+                        if (items > 0) ok = mbar_wait(smem_addr(q_empty), (items - 1) & 1u, abort_flag, p.status);
+                        ok = __all_sync(kFull, ok);
+                        if (!ok) break;
+                        ++items;
+                        if (elect_one()) {
+                            int boxes = 0;
+                            each_box(it, [&](int, int, int, int) { ++boxes; });
+                            const uint32_t qb = smem_addr(q_full);
+                            mbar_arrive_expect_tx(qb, (uint32_t)(boxes * p.box_tokens * G * 128));
+                            each_box(it, [&](int at, int x, int g, int token) {
+                                tc::tma_load_4d(smem_addr(smem + at), &tmQ, x, 0, g, token, qb);
                             });
+                        }
+                    } else {
+                        if (vt >= NV)
+                            ok = mbar_wait(smem_addr(&v_empty[vt % NV]), (vt / NV - 1) & 1u, abort_flag, p.status);
+                        ok = __all_sync(kFull, ok);
+                        if (!ok) break;
+                        if (elect_one())
+                            copy(&tmV, LY::kVRing + (vt % NV) * LY::kTileBytes, &v_full[vt % NV], y_v);
+                        ++vt;
+                    }
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) y_v[b] = y[b];
+                    if (t == min(it.t0 + 1, it.t1)) {
+                        // the item after this one: its first block ids, its query rows into L2
+                        after = walk.next(p);
+                        if (after.t0 < after.t1) {
+                            ids_after = ids_from(after, after.t0);
+                            if (elect_one())
+                                each_box(after, [&](int, int x, int g, int token) {
+                                    tc::tma_prefetch_4d(&tmQ, x, 0, g, token);
+                                });
+                        }
                     }
                 }
+                if (!ok) break;
             }
-            if (!ok) break;
-        }
-        // after a timed-out wait: let the copies still in flight land first
-        if (*abort_flag && lane == 0) {
-            auto drain = [&](uint64_t *bar, uint32_t parity) {
-                const unsigned long long t0 = globaltimer();
-                while (!mbar_try_wait(smem_addr(bar), parity))
-                    if (globaltimer() - t0 > kTimeoutNs) break;
+            // after a timed-out wait: let the copies still in flight land first
+            if (*abort_flag && lane == 0) {
+                auto drain = [&](uint64_t *bar, uint32_t parity) {
+                    const unsigned long long t0 = globaltimer();
+                    while (!mbar_try_wait(smem_addr(bar), parity))
+                        if (globaltimer() - t0 > kTimeoutNs) break;
+                };
+                for (uint32_t i = kt > NK ? kt - NK : 0; i < kt; ++i) drain(&k_full[i % NK], (i / NK) & 1u);
+                for (uint32_t i = vt > NV ? vt - NV : 0; i < vt; ++i) drain(&v_full[i % NV], (i / NV) & 1u);
+                if (items > 0) drain(q_full, (items - 1) & 1u);
+            }
+        } else if (warp == kIssuer) {
+            const uint32_t id_qk = tc::idesc_f16(BF16, kRows, kKeys, 0, 0);
+            const uint32_t id_pv = tc::idesc_f16(BF16, kRows, D, 0, 1);
+            const uint32_t t_s = __shfl_sync(kFull, tmem, 0), t_o = t_s + 128;
+            const uint64_t qa_d = tc::desc_sw128(smem_addr(smem), 16, 1024);
+            uint32_t kt = 0;                 // key tiles
+            bool ok = true;
+            auto reach = [&](uint64_t *bar, uint32_t parity) {
+                ok = __all_sync(kFull, mbar_wait(smem_addr(bar), parity, abort_flag, p.status));
+                return ok;
             };
-            for (uint32_t i = kt > NK ? kt - NK : 0; i < kt; ++i) drain(&k_full[i % NK], (i / NK) & 1u);
-            for (uint32_t i = vt > NV ? vt - NV : 0; i < vt; ++i) drain(&v_full[i % NV], (i / NV) & 1u);
-            if (items > 0) drain(q_full, (items - 1) & 1u);
-        }
-    } else if (warp == kIssuer) {
-        const uint32_t id_qk = tc::idesc_f16(BF16, kRows, kKeys, 0, 0);
-        const uint32_t id_pv = tc::idesc_f16(BF16, kRows, D, 0, 1);
-        const uint32_t t_s = __shfl_sync(kFull, tmem, 0), t_o = t_s + 128;
-        const uint64_t qa_d = tc::desc_sw128(smem_addr(smem), 16, 1024);
-        uint32_t kt = 0;                 // key tiles
-        bool ok = true;
-        auto reach = [&](uint64_t *bar, uint32_t parity) {
-            ok = __all_sync(kFull, mbar_wait(smem_addr(bar), parity, abort_flag, p.status));
-            return ok;
-        };
-        // P V of tile vt
-        auto issue_pv = [&](uint32_t vt) {
-            const uint32_t slot = vt % NV, par = (vt / NV) & 1u, b = vt & 1u;
-            if (!reach(&clean[slot], par) || !reach(&v_full[slot], par) || !reach(&p_full[b], (vt >> 1) & 1u)) return;
-            tc::fence_after_sync();
-            const uint64_t vb_d = tc::desc_sw128(smem_addr(smem + LY::kVRing + slot * LY::kTileBytes), kKeys * 128, 1024);
-            if (elect_one()) {
+            // P V of tile vt
+            auto issue_pv = [&](uint32_t vt) {
+                const uint32_t slot = vt % NV, par = (vt / NV) & 1u, b = vt & 1u;
+                if (!reach(&clean[slot], par) || !reach(&v_full[slot], par) ||
+                    !reach(&p_full[b], (vt >> 1) & 1u))
+                    return;
+                tc::fence_after_sync();
+                const uint64_t vb_d =
+                    tc::desc_sw128(smem_addr(smem + LY::kVRing + slot * LY::kTileBytes), kKeys * 128, 1024);
+                if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < 2 * kKeys / 16; ++i) {       // 16 keys, high or low parts
-                    const int kk = 2 * (i >> 2) + (i & 1);
-                    tc::mma_f16_ts(t_o, t_s + 64 * b + 8 * i, vb_d + (uint64_t)((kk * 16 * 128) >> 4), id_pv, true);
+                    for (int i = 0; i < 2 * kKeys / 16; ++i) {       // 16 keys, high or low parts
+                        const int kk = 2 * (i >> 2) + (i & 1);
+                        tc::mma_f16_ts(t_o, t_s + 64 * b + 8 * i, vb_d + (uint64_t)((kk * 16 * 128) >> 4),
+                                       id_pv, true);
+                    }
+                    tc::mma_commit(smem_addr(&o_full[b]));
+                    tc::mma_commit(smem_addr(&v_empty[slot]));
                 }
-                tc::mma_commit(smem_addr(&o_full[b]));
-                tc::mma_commit(smem_addr(&v_empty[slot]));
-            }
-            __syncwarp();
-        };
-        while (ok && __all_sync(kFull, next_task()) && reach(q_full, nt & 1u)) {
+                __syncwarp();
+            };
+            while (ok && __all_sync(kFull, next_task()) && reach(q_full, nt & 1u)) {
 #pragma unroll 1
-            for (int t = it.t0; t <= it.t1; ++t) {
-                if (t < it.t1) {
-                    const uint32_t slot = kt % NK;
-                    if (!reach(&k_full[slot], (kt / NK) & 1u)) break;
-                    tc::fence_after_sync();
-                    const uint64_t kb_d = tc::desc_sw128(smem_addr(smem + LY::kKRing + slot * LY::kTileBytes), 16, 1024);
-                    if (elect_one()) {
+                for (int t = it.t0; t <= it.t1; ++t) {
+                    if (t < it.t1) {
+                        const uint32_t slot = kt % NK;
+                        if (!reach(&k_full[slot], (kt / NK) & 1u)) break;
+                        tc::fence_after_sync();
+                        const uint64_t kb_d =
+                            tc::desc_sw128(smem_addr(smem + LY::kKRing + slot * LY::kTileBytes), 16, 1024);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = (kk & 3) * 32;              // 16 values inside the row
-                            tc::mma_f16(t_s + 64 * (kt & 1u), qa_d + (uint64_t)(((kk >> 2) * kRows * 128 + off) >> 4),
-                                        kb_d + (uint64_t)(((kk >> 2) * kKeys * 128 + off) >> 4), id_qk, kk > 0);
-                        }
-                        tc::mma_commit(smem_addr(&s_full[kt & 1u]));
-                        tc::mma_commit(smem_addr(&k_empty[slot]));
-                        if (t == it.t1 - 1) tc::mma_commit(smem_addr(q_empty));
-                    }
-                    __syncwarp();
-                }
-                if (t > it.t0) issue_pv(kt - 1);
-                if (!ok) break;
-                if (t < it.t1) ++kt;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&task_empty[nt % kTasks]));
-            ++nt;
-        }
-        // every MMA this warp issued has completed before the columns are freed
-        if (elect_one()) {
-            tc::mma_commit(smem_addr(done));
-            const unsigned long long t0 = globaltimer();
-            while (!mbar_try_wait(smem_addr(done), 0)) {
-                if (globaltimer() - t0 > kTimeoutNs) {
-                    atomicOr(p.status, PKV_DEV_TIMEOUT);
-                    break;
-                }
-            }
-        }
-        __syncwarp();
-    } else if (warp == kCleaner) {
-        uint32_t vt = 0;
-        bool ok = true;
-        for (; ok && next_task(); ++nt) {
-            for (int t = it.t0; t < it.t1; ++t, ++vt) {
-                const uint32_t slot = vt % NV;
-                ok = __all_sync(kFull, mbar_wait(smem_addr(&v_full[slot]), (vt / NV) & 1u, abort_flag, p.status));
-                if (!ok) break;
-                const int k0 = t * kKeys;
-                if (k0 + kKeys > it.base) {
-                    constexpr int kChunks = LY::kRegions * 8;
-                    // chunk e of the tile's rows
-                    auto chunk = [&](int e) -> uint4 & {
-                        const int r = e / kChunks, c = e % kChunks;
-                        return *reinterpret_cast<uint4 *>(smem + LY::kVRing + slot * LY::kTileBytes +
-                                                          (c >> 3) * kKeys * 128 + r * 128 + (c & 7) * 16);
-                    };
-                    const int e0 = max(it.base - k0, 0) * kChunks, e1 = min(it.L() - k0, kKeys) * kChunks;
-                    uint32_t sum[4] = {0u, 0u, 0u, 0u}, odd[2] = {0u, 0u};
-#pragma unroll 2
-                    for (int e = e0 + lane; e < e1; e += 32) {
-                        const uint4 w = chunk(e);
-                        add_odd<BF16>(sum[0], w.x);
-                        add_odd<BF16>(sum[1], w.y);
-                        add_odd<BF16>(sum[2], w.z);
-                        add_odd<BF16>(sum[3], w.w);
-                    }
-#pragma unroll 1
-                    for (int e = e1 + lane; e < kKeys * kChunks; e += 32) chunk(e) = make_uint4(0u, 0u, 0u, 0u);
-                    if (__any_sync(kFull, odd_halves<BF16>(sum[0]) | odd_halves<BF16>(sum[1]) |
-                                              odd_halves<BF16>(sum[2]) | odd_halves<BF16>(sum[3]))) {
-                        for (int e = e0 + lane; e < e1; e += 32) {
-                            uint4 &w = chunk(e);
-                            const uint4 o = make_uint4(odd_halves<BF16>(w.x), odd_halves<BF16>(w.y),
-                                                       odd_halves<BF16>(w.z), odd_halves<BF16>(w.w));
-                            if (o.x | o.y | o.z | o.w) {
-                                w = make_uint4(w.x & ~o.x, w.y & ~o.y, w.z & ~o.z, w.w & ~o.w);
-                                const int r = e / kChunks;
-                                odd[r >> 5] |= 1u << (r & 31);
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t off = (kk & 3) * 32;              // 16 values inside the row
+                                tc::mma_f16(t_s + 64 * (kt & 1u),
+                                            qa_d + (uint64_t)(((kk >> 2) * kRows * 128 + off) >> 4),
+                                            kb_d + (uint64_t)(((kk >> 2) * kKeys * 128 + off) >> 4), id_qk, kk > 0);
                             }
+                            tc::mma_commit(smem_addr(&s_full[kt & 1u]));
+                            tc::mma_commit(smem_addr(&k_empty[slot]));
+                            if (t == it.t1 - 1) tc::mma_commit(smem_addr(q_empty));
                         }
-                        odd[0] = __reduce_or_sync(kFull, odd[0]);
-                        odd[1] = __reduce_or_sync(kFull, odd[1]);
+                        __syncwarp();
                     }
-                    if (lane == 0) odd_keys[slot] = odd[0] | (uint64_t)odd[1] << 32;
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
+                    if (t > it.t0) issue_pv(kt - 1);
+                    if (!ok) break;
+                    if (t < it.t1) ++kt;
                 }
-                if (lane == 0) mbar_arrive(smem_addr(&clean[slot]));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&task_empty[nt % kTasks]));
+                ++nt;
+            }
+            // every MMA this warp issued has completed before the columns are freed
+            if (elect_one()) {
+                tc::mma_commit(smem_addr(done));
+                const unsigned long long t0 = globaltimer();
+                while (!mbar_try_wait(smem_addr(done), 0)) {
+                    if (globaltimer() - t0 > kTimeoutNs) {
+                        atomicOr(p.status, PKV_DEV_TIMEOUT);
+                        break;
+                    }
+                }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&task_empty[nt % kTasks]));
+        } else if (warp == kCleaner) {
+            uint32_t vt = 0;
+            bool ok = true;
+            for (; ok && next_task(); ++nt) {
+                for (int t = it.t0; t < it.t1; ++t, ++vt) {
+                    const uint32_t slot = vt % NV;
+                    ok = __all_sync(kFull, mbar_wait(smem_addr(&v_full[slot]), (vt / NV) & 1u, abort_flag, p.status));
+                    if (!ok) break;
+                    const int k0 = t * kKeys;
+                    if (k0 + kKeys > it.base) {
+                        constexpr int kChunks = LY::kRegions * 8;
+                        // chunk e of the tile's rows
+                        auto chunk = [&](int e) -> uint4 & {
+                            const int r = e / kChunks, c = e % kChunks;
+                            return *reinterpret_cast<uint4 *>(smem + LY::kVRing + slot * LY::kTileBytes +
+                                                              (c >> 3) * kKeys * 128 + r * 128 + (c & 7) * 16);
+                        };
+                        const int e0 = max(it.base - k0, 0) * kChunks, e1 = min(it.L() - k0, kKeys) * kChunks;
+                        uint32_t sum[4] = {0u, 0u, 0u, 0u}, odd[2] = {0u, 0u};
+#pragma unroll 2
+                        for (int e = e0 + lane; e < e1; e += 32) {
+                            const uint4 w = chunk(e);
+                            add_odd<BF16>(sum[0], w.x);
+                            add_odd<BF16>(sum[1], w.y);
+                            add_odd<BF16>(sum[2], w.z);
+                            add_odd<BF16>(sum[3], w.w);
+                        }
+#pragma unroll 1
+                        for (int e = e1 + lane; e < kKeys * kChunks; e += 32) chunk(e) = make_uint4(0u, 0u, 0u, 0u);
+                        if (__any_sync(kFull, odd_halves<BF16>(sum[0]) | odd_halves<BF16>(sum[1]) |
+                                                  odd_halves<BF16>(sum[2]) | odd_halves<BF16>(sum[3]))) {
+                            for (int e = e0 + lane; e < e1; e += 32) {
+                                uint4 &w = chunk(e);
+                                const uint4 o = make_uint4(odd_halves<BF16>(w.x), odd_halves<BF16>(w.y),
+                                                           odd_halves<BF16>(w.z), odd_halves<BF16>(w.w));
+                                if (o.x | o.y | o.z | o.w) {
+                                    w = make_uint4(w.x & ~o.x, w.y & ~o.y, w.z & ~o.z, w.w & ~o.w);
+                                    const int r = e / kChunks;
+                                    odd[r >> 5] |= 1u << (r & 31);
+                                }
+                            }
+                            odd[0] = __reduce_or_sync(kFull, odd[0]);
+                            odd[1] = __reduce_or_sync(kFull, odd[1]);
+                        }
+                        if (lane == 0) odd_keys[slot] = odd[0] | (uint64_t)odd[1] << 32;
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(smem_addr(&clean[slot]));
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&task_empty[nt % kTasks]));
+            }
         }
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---------------------------------------------------------- softmax
@@ -753,13 +771,17 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float hide = p.scale_log2 < 0.f ? INFINITY : -INFINITY;
         uint32_t kt = 0;                 // key tiles
         bool alive = true;
+        // a wait of the whole warp; false once it ran out
+        auto reach = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(kFull, mbar_wait(smem_addr(bar), parity, abort_flag, p.status));
+        };
         // the item is done with
         auto leave = [&]() {
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&task_empty[nt % kTasks]));
             ++nt;
         };
-        while (alive && __all_sync(kFull, mbar_wait(smem_addr(&task_full[nt % kTasks]), (nt / kTasks) & 1u, abort_flag, p.status))) {
+        while (alive && reach(&task_full[nt % kTasks], (nt / kTasks) & 1u)) {
             it = tasks[nt % kTasks];
             if (it.t0 >= it.t1) break;
             const int n = it.n, base = it.base, L = it.L();
@@ -779,8 +801,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             for (int t = it.t0; t < it.t1; ++t, ++kt) {
                 const uint32_t b = kt & 1u, vslot = kt % NV;
-                const bool got = mbar_wait(smem_addr(&s_full[b]), (kt >> 1) & 1u, abort_flag, p.status);
-                if (!__all_sync(kFull, got)) { alive = false; break; }
+                if (!(alive = reach(&s_full[b], (kt >> 1) & 1u))) break;
                 if (!busy) {
                     if (lane == 0) mbar_arrive(smem_addr(&p_full[b]));
                     continue;
@@ -861,16 +882,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                 l = l * f + (ls.x + ls.y);
                 uint64_t odd = 0ull;                     // keys whose V held odd values
                 if (edge) {
-                    const bool swept = mbar_wait(smem_addr(&clean[vslot]), (kt / NV) & 1u, abort_flag, p.status);
-                    if (!__all_sync(kFull, swept)) { alive = false; break; }
+                    if (!(alive = reach(&clean[vslot], (kt / NV) & 1u))) break;
                     odd = odd_keys[vslot];
                 }
                 // O changes before P V of this tile, once P V of the one before has ended; the
                 // wait for that consumes its o_full phase either here or after P is out
                 const bool touch = __any_sync(kFull, resc) || odd;
                 if (touch && t > it.t0) {
-                    const bool ended = mbar_wait(smem_addr(&o_full[b ^ 1u]), ((kt - 1) >> 1) & 1u, abort_flag, p.status);
-                    if (!__all_sync(kFull, ended)) { alive = false; break; }
+                    if (!(alive = reach(&o_full[b ^ 1u], ((kt - 1) >> 1) & 1u))) break;
                     tc::fence_after_sync();
                 }
                 if (touch) {
@@ -911,15 +930,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&p_full[b]));
                 if (!touch && t > it.t0) {
-                    const bool ended = mbar_wait(smem_addr(&o_full[b ^ 1u]), ((kt - 1) >> 1) & 1u, abort_flag, p.status);
-                    if (!__all_sync(kFull, ended)) { alive = false; break; }
+                    if (!(alive = reach(&o_full[b ^ 1u], ((kt - 1) >> 1) & 1u))) break;
                 }
             }
             if (!alive) break;
             // ---- the part's result, once its last P V is done (which writes the lanes of warps
             // without rows too: they wait before another item's zeros)
-            const bool ended = mbar_wait(smem_addr(&o_full[(kt - 1) & 1u]), ((kt - 1) >> 1) & 1u, abort_flag, p.status);
-            if (!__all_sync(kFull, ended)) break;
+            if (!reach(&o_full[(kt - 1) & 1u], ((kt - 1) >> 1) & 1u)) break;
             tc::fence_after_sync();
             if (!busy) {
                 leave();
@@ -956,7 +973,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                         for (int c = 0; c < 32; c += 8) {
                             auto two_of = [&](int k) {
-                                return none ? 0u : E::pack(__uint_as_float(v[c + k]) * inv, __uint_as_float(v[c + k + 1]) * inv);
+                                return none ? 0u : E::pack(__uint_as_float(v[c + k]) * inv,
+                                                           __uint_as_float(v[c + k + 1]) * inv);
                             };
                             *reinterpret_cast<uint4 *>(out + c0 + c) =
                                 make_uint4(two_of(0), two_of(2), two_of(4), two_of(6));
@@ -978,7 +996,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 // A task is 32 rows and 8 columns of a cut item; one, two, four or eight warps share its pieces
 // (in turn, so that the order of a sum does not vary), four pieces under way at a time, and
 // meet in shared memory.  Every CTA lists the cut items and their passes (as many tasks as a CTA
-// takes at once), and takes every gridDim-th pass.
+// takes at once), and takes every gridDim-th pass.  A CTA to an SM: 4 sequences 22.4 us (27 with
+// half as many, 23 with twice).
 constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32, kJoinCtas = 152;
 static_assert(kJoinThreads >= kMaxRanges, "a thread for each range");
 
@@ -1273,19 +1292,23 @@ extern "C" int paged_tree_attention(const pkv_pool *pool, void *out, const void 
     prm.num_kv_heads = g.num_kv_heads;
     prm.group = G;
     prm.max_blocks_per_seq = max_blocks_per_seq;
-    prm.max_tokens = (int32_t)std::min<int64_t>((int64_t)max_blocks_per_seq * pkv::kBlock, INT32_MAX);
+    prm.max_tokens = (int32_t)std::min<int64_t>((int64_t)max_blocks_per_seq * pkv::kBlock,
+                                                 INT32_MAX - 2 * kKeys);
     prm.num_blocks = g.num_blocks;
     prm.tile_tokens = tile_tokens(G);
     prm.box_tokens = box_tokens(G);
     prm.tile_inverse = ((1 << 20) + prm.tile_tokens - 1) / prm.tile_tokens;
     prm.piece_rows = (int32_t)piece_rows(num_tokens, G);
-    // the ranges are counted in 32 bits
-    const double most = ((double)num_tokens / prm.tile_tokens + num_seqs) * g.num_kv_heads *
-                        (prm.max_tokens / kKeys + 1 + kItemCost);
+    // the ranges are counted in 32 bits, whatever the row ranges hold
+    const int64_t tiles_of_seq = (std::min(num_tokens, 32 * mask_words) + prm.tile_tokens - 1) / prm.tile_tokens;
+    const double most = (double)num_seqs * tiles_of_seq * g.num_kv_heads * (prm.max_tokens / kKeys + 1 + kItemCost);
     if (most > INT32_MAX) return PKV_ERR_UNSUPPORTED;
-    // scores are hidden by an infinity that the scale must carry into the exponent; at scale 0
-    // the smallest normal number weighs all keys alike
-    prm.scale_log2 = scale == 0.f ? 0x1p-126f : scale * 1.4426950408889634f;
+    // Scores are hidden by an infinity that the scale must carry into the exponent, and a product
+    // that is the reference must weigh 1: the scale is a finite normal number.  At scale 0 the
+    // smallest one weighs all keys alike.
+    prm.scale_log2 = scale * 1.4426950408889634f;
+    if (fabsf(prm.scale_log2) < FLT_MIN) prm.scale_log2 = copysignf(FLT_MIN, scale);
+    if (fabsf(prm.scale_log2) > FLT_MAX) prm.scale_log2 = copysignf(FLT_MAX, scale);
     char *w = static_cast<char *>(workspace);
     prm.ranges = reinterpret_cast<int4 *>(w + ws.ranges);
     prm.part_ml = reinterpret_cast<float2 *>(w + ws.ml);
