@@ -135,6 +135,7 @@ struct Moves {
     int32_t part_chunks, parts;          // of them a CTA's, and CTAs that share a row
     int32_t pairs;                       // (kv head, K or V) of a CTA
     int32_t batch;                       // tokens of a batch
+    int32_t units;                       // shares of all sequences' rows, at most, see parts_of
     uint4 *k_pool, *v_pool;
     int32_t *status;
 };
@@ -143,34 +144,60 @@ struct Moves {
 // else reads or writes these bytes.  It goes through the kept tokens in order, a batch at a time:
 // all of the batch's rows are read, then written.  A destination is never above its source and
 // sources rise, so what a batch writes is no source of a later one.
-// The chain list -> table -> row -> store bounds it, and how many rows are under way at once:
-// places are looked up once for a CTA and a batch ahead of the rows, the list is read two ahead.
-// Nine caches of up to 16,384 tokens that keep 40,000 in all (305 MB moved): 71 us, 4.3 TB/s
-// (floor 45; the longest list's 8,000 tokens set the end); 93 us with whole rows to a CTA, four
-// times as long when each thread looked up its rows' places.
+// What bounds it is how many rows are under way at once and the instructions of a chunk: places are
+// looked up once for a CTA and a batch ahead of the rows, the list is read two ahead.  Nine caches
+// of up to 16,384 tokens that keep 40,000 in all (305 MB moved): 64 us, 4.8 TB/s (floor 45; the
+// longest list's 8,000 tokens set the end); before the last steps it was 71 us, 93 with whole rows to
+// a CTA, four times as long when each thread looked up its rows' places.
 //
-// Threads, chunks of a thread under way, tokens of a batch at most, CTAs to an SM.  What is under
-// way on an SM is the same for all; larger CTAs wait for their slowest row and end later, so they
-// are only for calls with no more CTAs than SMs (a cache of 16,000 tokens: 64 of them, 31 us
-// against 63 with Many; 100 caches of 300 to 900 tokens, 1,600 CTAs: 77 against 59).  Lists that
-// end within a batch want the fewer steps of Brief (96 lists of up to 60: 4.5 us against 6.2; the
-// nine caches: 81 against 71).
+// Threads, chunks of a thread under way, tokens of a batch at most, CTAs to an SM.
+//   Many: what is under way on an SM is the same as in Few, but a CTA waits for its slowest row, so
+//     many small ones end earlier (100 caches of 300 to 900 tokens 59 us, 77 with Few, then).
+//   Uneven: up to 32 long lists share their rows by length (10 lists of 1,000 to 14,000 tokens 113
+//     us, 140 with Many; below kLongList tokens on average the search costs more than it gives, 20
+//     lists of 130: 9.8 us against 6.6, then).
+//   Few: calls with no more CTAs than SMs (a cache of 16,000 tokens: 64; 29 us, 56 with Many).
+//   Brief: lists far shorter than a batch, several pairs to a CTA (96 lists of up to 6: 3.6 us, 8.0
+//     with Many; 64 lists of 20 to 100: 7.5, 6.2 with Many).
+struct Many {
+    static constexpr bool kByLength = false, kPairs = false;
+    static constexpr int kThreads = 256, kDepth = 8, kBatch = 512, kCtas = 3;
+};
+struct Uneven : Many {
+    static constexpr bool kByLength = true;
+};
 struct Few {
+    static constexpr bool kByLength = false, kPairs = false;
     static constexpr int kThreads = 1024, kDepth = 4, kBatch = 960, kCtas = 1;   // 46 KB of places
 };
 struct Brief {
+    static constexpr bool kByLength = false, kPairs = true;
     static constexpr int kThreads = 256, kDepth = 4, kBatch = 512, kCtas = 3;
 };
-struct Many {
-    static constexpr int kThreads = 256, kDepth = 8, kBatch = 512, kCtas = 3;
-};
-constexpr int kFewCtas = 152, kBriefList = 128;
-constexpr int kMoveCtas = 608;           // rows are shared until there are four CTAs for an SM (the nine caches
-                                         // 104 us with two, 71 with eight; 5 caches of 40 heads 65)
+constexpr int kFewCtas = 152, kBriefList = 32, kLongList = 512, kManyCtas = 152 * Many::kCtas;
+constexpr int kMoveCtas = 608;           // rows are shared until there are four CTAs for an SM
 
 struct Place {
-    int64_t from, to;                    // token rows of kv head 0 in the pool, -1: does not move
+    int64_t from, to;                    // chunks of the pool before kv head 0's row, -1: does not move
 };
+
+// CTAs that share each row of a sequence of n kept tokens, up to 32 sequences: 1, 2 or 4 (at most
+// p.parts), so that the longest list of a share is as short as it can be with all CTAs at work at once.
+__device__ __forceinline__ int parts_of(const Moves &p, int n)
+{
+    const int lane = threadIdx.x & 31, seqs = gridDim.y;
+    const int mine = lane < seqs ? min(max(p.num_kept[lane], 0), p.num_entries) : 0;
+    const int half = (mine + 1) / 2;
+    int low = 0, high = __reduce_max_sync(kFull, mine);
+    while (low < high) {
+        const int mid = low + (high - low) / 2;
+        const int units = seqs + __popc(__ballot_sync(kFull, mine > mid)) +
+                          (p.parts > 2 ? 2 * __popc(__ballot_sync(kFull, half > mid)) : 0);
+        if (units <= p.units) high = mid;
+        else low = mid + 1;
+    }
+    return n <= low ? 1 : (n + 1) / 2 <= low || p.parts == 2 ? 2 : 4;
+}
 
 template <typename C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas) compact_kernel(const Moves p)
@@ -188,9 +215,16 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) compact_kernel(const Mo
         if (blockIdx.x == 0 && tid == 0) atomicOr(p.status, PKV_DEV_BAD_LEN);
         return;
     }
+    int part_chunks = p.part_chunks, batch = p.batch;
     const int part = blockIdx.x % p.parts, pair0 = blockIdx.x / p.parts * p.pairs;
-    const int pairs = min(p.pairs, 2 * p.num_kv_heads - pair0);
-    const int c0 = part * p.part_chunks, nc = min(p.part_chunks, p.chunks - c0);
+    if constexpr (C::kByLength) {
+        const int parts = parts_of(p, n);
+        if (part >= parts) return;
+        part_chunks = (p.chunks + parts - 1) / parts;
+        batch = min(kThreads / part_chunks * kDepth, C::kBatch);
+    }
+    const int pairs = C::kPairs ? min(p.pairs, 2 * p.num_kv_heads - pair0) : 1;
+    const int c0 = part * part_chunks, nc = min(part_chunks, p.chunks - c0);
     const int per_pass = kThreads / nc;              // rows of one pass of the threads
     const int c = tid % nc, k = tid / nc;
     const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
@@ -198,8 +232,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) compact_kernel(const Mo
     const int64_t limit = (int64_t)p.max_blocks_per_seq * p.block_size;
     auto place = [&](int pos) -> int64_t {
         const int id = row[pos / p.block_size];
-        return id < 0 || id >= p.num_blocks ? -1 : (int64_t)id * p.num_kv_heads * p.block_size + pos % p.block_size;
+        return id < 0 || id >= p.num_blocks
+                   ? -1
+                   : ((int64_t)id * p.num_kv_heads * p.block_size + pos % p.block_size) * p.chunks;
     };
+    // the thread's chunk of the pool's first token
+    auto chunks_of = [&](int pair) -> uint4 * {
+        return (pair & 1 ? p.v_pool : p.k_pool) + c0 + c + (int64_t)(pair >> 1) * p.block_size * p.chunks;
+    };
+    uint4 *const base = chunks_of(pair0);
     // The list runs two batches ahead of the rows, the places one: `fetch` takes a thread's entries
     // of the batch from i0 on, `look_up` finds their places.
     constexpr int kEntries = (C::kBatch + kThreads - 1) / kThreads;
@@ -208,7 +249,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) compact_kernel(const Mo
 #pragma unroll
         for (int j = 0; j < kEntries; ++j) {
             const int e = j * kThreads + tid, i = i0 + e;
-            const bool mine = e < p.batch && i < n;
+            const bool mine = e < batch && i < n;
             pos[j] = mine ? kept[i] : 0;
             before[j] = mine && i > 0 ? kept[i - 1] : -1;
         }
@@ -217,7 +258,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) compact_kernel(const Mo
 #pragma unroll
         for (int j = 0; j < kEntries; ++j) {
             const int e = j * kThreads + tid, i = i0 + e;
-            if (e >= p.batch || i >= n) continue;
+            if (e >= batch || i >= n) continue;
             const int64_t dst = (int64_t)first + i;
             Place x = {-1, -1};
             if (pos[j] < dst || before[j] >= pos[j] || pos[j] >= limit) {
@@ -236,26 +277,37 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) compact_kernel(const Mo
     __syncthreads();
     fetch(0);
     look_up(0, 0);
-    fetch(p.batch);
+    fetch(batch);
     __syncthreads();
-    for (int i0 = 0, buffer = 0; i0 < n; i0 += p.batch, buffer = buffer == 2 ? 0 : buffer + 1) {
-        const int count = min(p.batch, n - i0), stop = stops[buffer];
+    for (int i0 = 0, buffer = 0; i0 < n; i0 += batch, buffer = buffer == 2 ? 0 : buffer + 1) {
+        const int count = min(batch, n - i0), stop = stops[buffer];
         uint4 v[kDepth];
-        // the thread's d-th chunk of the batch: where it comes from and goes to, null: nowhere
+        const int rows = k < per_pass ? min(count, stop - i0) : 0;
+        // the thread's d-th chunk of the batch: where it comes from or goes to, null: nowhere
         auto chunk = [&](int d, bool source) -> uint4 * {
-            const int r = d * per_pass + k, pair = pairs == 1 ? 0 : r / p.batch, e = r - pair * p.batch;
-            if (k >= per_pass || pair >= pairs || e >= count || i0 + e >= stop) return nullptr;
-            const int64_t at = source ? places[buffer][e].from : places[buffer][e].to;
-            if (at < 0) return nullptr;
-            return ((pair0 + pair) & 1 ? p.v_pool : p.k_pool) + c0 + c +
-                   (at + (int64_t)((pair0 + pair) >> 1) * p.block_size) * p.chunks;
+            int e = d * per_pass + k;
+            uint4 *at = base;
+            bool there = true;
+            if constexpr (C::kPairs) {
+                const int pair = e / batch;
+                e -= pair * batch;
+                at = chunks_of(pair0 + pair);
+                there = pair < pairs;
+            }
+            if constexpr (C::kPairs) {                   // (no branch: all loads are under way at once)
+                const int64_t off = source ? places[buffer][e].from : places[buffer][e].to;
+                return !there || e >= rows || off < 0 ? nullptr : at + off;
+            }
+            if (e >= rows) return nullptr;
+            const int64_t off = source ? places[buffer][e].from : places[buffer][e].to;
+            return off < 0 ? nullptr : at + off;
         };
 #pragma unroll
         for (int d = 0; d < kDepth; ++d)
             if (const uint4 *from = chunk(d, true)) v[d] = *from;
         if (stop >= n) {
-            look_up(i0 + p.batch, buffer == 2 ? 0 : buffer + 1);
-            fetch(i0 + 2 * p.batch);
+            look_up(i0 + batch, buffer == 2 ? 0 : buffer + 1);
+            fetch(i0 + 2 * batch);
         }
         __syncthreads();                                 // every row of the batch is read
 #pragma unroll
@@ -275,7 +327,8 @@ static int launch_moves(Moves p, int parts, int num_seqs, int64_t average, cudaS
     p.part_chunks = std::min((p.chunks + parts - 1) / parts, C::kThreads);
     p.parts = (p.chunks + p.part_chunks - 1) / p.part_chunks;
     const int rows = C::kThreads / p.part_chunks * C::kDepth, all = 2 * p.num_kv_heads;
-    p.pairs = (int32_t)std::max<int64_t>(1, std::min<int64_t>(rows / std::max<int64_t>(1, average), all));
+    const int64_t fit = C::kPairs ? rows / std::max<int64_t>(1, average) : 1;
+    p.pairs = (int32_t)std::max<int64_t>(1, std::min<int64_t>(fit, all));
     p.batch = std::min(rows / p.pairs, C::kBatch);
     const dim3 grid((unsigned)((all + p.pairs - 1) / p.pairs * p.parts), (unsigned)num_seqs);
     return launch(&compact_kernel<C>, grid, C::kThreads, st, p);
@@ -346,5 +399,14 @@ extern "C" int kv_cache_compact(const pkv_pool *pool, const int32_t *block_table
     const cudaStream_t st = (cudaStream_t)stream;
     if (ctas * parts <= kFewCtas) return launch_moves<Few>(p, parts, num_seqs, average, st);
     if (average <= kBriefList) return launch_moves<Brief>(p, parts, num_seqs, average, st);
+    // up to 32 long lists: as many shares of a row as their lengths ask for
+    if (num_seqs <= 32 && average >= kLongList && ctas <= kManyCtas && p.chunks >= 8 &&
+        p.chunks <= Many::kThreads) {
+        p.parts = p.chunks >= 16 ? 4 : 2;
+        p.pairs = 1;
+        p.units = kManyCtas / (2 * g.num_kv_heads);
+        const dim3 grid((unsigned)(2 * g.num_kv_heads * p.parts), (unsigned)num_seqs);
+        return launch(&compact_kernel<Uneven>, grid, Uneven::kThreads, st, p);
+    }
     return launch_moves<Many>(p, parts, num_seqs, average, st);
 }

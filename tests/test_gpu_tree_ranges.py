@@ -141,6 +141,27 @@ def test_lists_of_every_size(seqs, hkv, dim, lo, hi):
         assert torch.equal(got, ref)
 
 
+@pytest.mark.parametrize("hkv,dim", [(8, 128), (6, 96), (8, 64), (5, 256), (6, 136)])
+def test_long_lists_of_uneven_lengths(hkv, dim):
+    """Rows shared by length: an empty list, one that does not fit, one with a bad position."""
+    gen, nb, tables, k, v = compact_case([40, 6000, 900, 2500, 900, 30, 4100, 1000, 1200], hkv, dim, "f16", dim)
+    kept, first = [], [0, 3, 0, 7, 2, 0, 0, 1, 5]
+    for n, part, lo in zip((40, 6000, 900, 2500, 900, 30, 4100, 1000, 1200),
+                           (1.0, 0.98, 0.5, 0.4, 0.0, 0.5, 0.97, 0.3, 0.5), first):
+        some = torch.randperm(n - lo, generator=gen)[:int((n - lo) * part)] + lo
+        kept.append(some.sort().values.tolist())
+    num = [len(x) for x in kept]
+    num[5] = -1                                            # does not fit
+    kept[6][3000] = kept[6][2999]                          # does not rise
+    got_k, got_v, word = run_compact(tables, k, v, kept, first, "f16", num=num)
+    assert word == P.DEV_BAD_LEN | P.DEV_BAD_TREE
+    moved = [x if s not in (5, 6) else x[:3000] if s == 6 else [] for s, x in enumerate(kept)]
+    for got, ref in ((got_k, k), (got_v, v)):
+        for s, x in enumerate(moved):
+            compact(ref, tables[s].tolist(), x, first[s])
+        assert torch.equal(got, ref)
+
+
 def test_tokens_that_stay_and_tokens_of_no_one():
     """Nothing moves where positions equal their destinations; entries behind num_kept are not read."""
     gen, nb, tables, k, v = compact_case([300, 300], 2, 128, "bf16", 41)
