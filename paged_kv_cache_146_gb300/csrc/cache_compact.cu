@@ -378,7 +378,7 @@ extern "C" int kv_cache_compact(const pkv_pool *pool, const int32_t *block_table
         ((uintptr_t)kept & 3u) || ((uintptr_t)kept_start & 3u) || ((uintptr_t)num_kept & 3u) ||
         ((uintptr_t)first & 3u) || ((uintptr_t)d_status & 3u))
         return PKV_ERR_INVALID_ARG;
-    Moves p;
+    Moves p = {};
     p.block_tables = block_tables;
     p.kept = kept;
     p.kept_start = kept_start;
