@@ -686,9 +686,11 @@ size_t paged_tree_workspace_bytes(int32_t num_tokens, int32_t num_q_heads, int32
  * from n_s on count for nothing).  n_s <= 32 * mask_words, mask_words 1 .. 32.
  * context_lens[s] includes the drafted tokens.  A row that sees nothing is zero.
  * What a row does not see cannot reach it, whatever it holds, NaN and infinities
- * included.  A sequence whose lengths do not fit (PKV_DEV_BAD_LEN) or that has a
- * bad table entry among its ceil(context_lens[s] / 16) blocks (PKV_DEV_BAD_BLOCK)
- * gets zero rows.
+ * included.  (All rows see the cache before the drafted tokens: an infinity in its
+ * V gives that infinity, or NaN where the token's weight has no second 16-bit part.)
+ * A sequence whose lengths do not fit (PKV_DEV_BAD_LEN) or that has a bad table
+ * entry among its ceil(context_lens[s] / 16) blocks (PKV_DEV_BAD_BLOCK) gets zero
+ * rows.
  *   workspace  paged_tree_workspace_bytes(...) bytes, 256-byte aligned, contents
  *              of no account before and after; calls that may run at the same
  *              time need one each

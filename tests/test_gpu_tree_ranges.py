@@ -287,3 +287,46 @@ def test_parents_of_long_chains():
     starts = torch.tensor([0] + news).cumsum(0).to(I32)
     flat = torch.tensor([x for p in parents for x in p], dtype=I32)
     assert torch.equal(P.tree_mask(flat.cuda(), starts.cuda(), 32).cpu(), P.tree_mask(flat, starts, 32))
+
+
+FIRST_CALL = """
+import sys
+sys.path[:0] = [{tests!r}, {root!r}]
+import torch
+import paged_kv_cache_146_gb300 as P
+from test_gpu_tree_ranges import one_call, tree_data
+import test_gpu_tree_ranges as R
+d = tree_data()
+pool, status = R.pool_of(d["c"], "bf16"), R.new_status()
+out = torch.zeros_like(d["q"])
+kept, num, nxt = torch.zeros_like(d["kept"]), torch.zeros_like(d["num"]), torch.zeros_like(d["tokens"][:3])
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    P.paged_tree_attention(pool, d["q"], d["tables"], d["starts"], d["lens"], d["mask"], 0.125, d["ws"], status,
+                           out=out)
+    P.tree_accept(d["tokens"], d["parents"], d["targets"], d["starts"], d["first"], status, kept=kept,
+                  num_kept=num, next_tokens=nxt)
+    P.cache_compact(pool, d["tables"], d["kept"], d["starts"], d["num"], d["first"], status)
+assert not out.any() and not num.any()
+graph.replay()
+torch.cuda.synchronize()
+mine = [out, kept, num, nxt, pool.k_pool, pool.v_pool]
+want = one_call("tree", d)[:1] + one_call("accept", d)[:3] + one_call("compact", d)[:2]
+assert status.item() == 0
+for a, b in zip(mine, want):
+    assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+print("captured")
+"""
+
+
+def test_the_first_calls_of_a_process_are_captured(tmp_path):
+    """Nothing that a kernel's first launch needs stands in a capture's way."""
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    script = tmp_path / "first.py"
+    script.write_text(FIRST_CALL.format(tests=tests, root=os.path.dirname(tests)))
+    run = subprocess.run([sys.executable, str(script)], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and run.stdout.strip().endswith("captured"), run.stdout + run.stderr
