@@ -19,8 +19,8 @@
 // 795 us with one CTA, 554 with two, then).
 //
 // What bounds it, 32 query heads over 8 of 128: at 96 sequences of up to 16,384 tokens with 16
-// drafted ones the copies of K and V (3.43 GB in 515-523 us, 6.6 TB/s; a plain copy's rate is
-// 6.8).  At 24 sequences with 64 drafted, two full query tiles each, nothing alone (141-149 us; the
+// drafted ones the copies of K and V (3.43 GB in 511-556 us, 6.2-6.7 TB/s; a plain copy's
+// rate is 6.8).  At 24 sequences with 64 drafted, two full query tiles each, nothing alone (141-149 us; the
 // bytes 70, the products 59): the main kernel's 128 us bring every key tile twice (7.4 TB/s from
 // L2), keep the tensor pipe busy for 58 % (P V once for each part of the weights), and the softmax
 // warps wait for fixed latencies; 15 us go to joining 39 MB of pieces.  At 4 sequences, 22 us, the
