@@ -758,6 +758,24 @@ def _raw(stream):
     return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
+def _made_on(stream, device, make):
+    """A buffer that a call makes itself, made and filled by ``make()`` on the stream that the
+    call runs on: another stream's memory may still be in use by work that is queued there, and
+    its fills would not be ordered with the call.  The current stream, which need not wait for
+    ``stream`` before the buffer is let go, counts as a user of it too."""
+    torch = _torch or _load_torch()
+    raw = _raw(stream)
+    if raw is None or device.type != "cuda":
+        return make()
+    current = torch.cuda.current_stream(device)
+    if raw == current.cuda_stream:
+        return make()
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device)):
+        t = make()
+    t.record_stream(current)
+    return t
+
+
 def _refuse(name: str, t, shape: tuple, dtype, index: int, contiguous: bool):
     """Raise for a tensor that failed its check."""
     if t.shape != shape:
@@ -1199,11 +1217,13 @@ def tree_accept(tokens, parents, targets, query_start, first, status, kept=None,
     without one); buffers that are given are used."""
     torch = _torch or _load_torch()
     if kept is None:
-        kept = torch.full((tokens.shape[0],), -1, dtype=torch.int32, device=tokens.device)
+        kept = _made_on(stream, tokens.device, lambda: torch.full(
+            (tokens.shape[0],), -1, dtype=torch.int32, device=tokens.device))
     if num_kept is None:
-        num_kept = torch.empty_like(first)
+        num_kept = _made_on(stream, first.device, lambda: torch.empty_like(first))
     if next_tokens is None:
-        next_tokens = torch.empty((first.shape[0],), dtype=tokens.dtype, device=tokens.device)
+        next_tokens = _made_on(stream, tokens.device, lambda: torch.empty(
+            (first.shape[0],), dtype=tokens.dtype, device=tokens.device))
     if _fast is not None:
         rc = _fast.accept(tokens, parents, targets, query_start, first, kept, num_kept,
                           next_tokens, status, _raw(stream))
