@@ -494,7 +494,7 @@ def paged_decode_attention_planned(pool: KVPool, q, block_tables, context_lens, 
     from ``decode_plan`` for the same lengths and tables."""
     import torch
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     _check_decode_args(pool, q, out, block_tables, context_lens, status, workspace,
                        pool.k_pool, pool.v_pool)
     S, hq, d = q.shape
@@ -529,7 +529,7 @@ def paged_decode_attention(pool: KVPool, q, block_tables, context_lens, scale: f
     k_pool = pool.k_pool if k_pool is None else k_pool
     v_pool = pool.v_pool if v_pool is None else v_pool
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     _check_decode_args(pool, q, out, block_tables, context_lens, status, workspace,
                        k_pool, v_pool)
     S, hq, d = q.shape
@@ -654,7 +654,7 @@ def paged_prefill_attention(pool: KVPool, q, block_tables, query_start, context_
     k_pool = pool.k_pool if k_pool is None else k_pool
     v_pool = pool.v_pool if v_pool is None else v_pool
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     dt = _torch_dtype(pool.dtype_code)
     _check_rows("q", q, None, None, pool.head_dim, dt, None)
     T, hq, d = q.shape
@@ -702,7 +702,7 @@ def paged_decode_attention_q8(pool: KVPool, q, block_tables, context_lens, scale
     ``decode_workspace_bytes``."""
     import torch
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     _check_decode_args(pool, q, out, block_tables, context_lens, status, workspace,
                        pool.kv if pool.kv is not None else None)
     S, hq, d = q.shape
@@ -770,10 +770,18 @@ def _made_on(stream, device, make):
     current = torch.cuda.current_stream(device)
     if raw == current.cuda_stream:
         return make()
-    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device)):
+    # (a handle of 0 is the default stream; ExternalStream takes it for none)
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device) if raw else
+                           torch.cuda.default_stream(device)):
         t = make()
     t.record_stream(current)
     return t
+
+
+def _empty_like(t, stream):
+    import torch
+    return torch.empty_like(t) if stream is None else _made_on(stream, t.device,
+                                                               lambda: torch.empty_like(t))
 
 
 def _refuse(name: str, t, shape: tuple, dtype, index: int, contiguous: bool):
@@ -902,7 +910,8 @@ def cache_write_rope(pool: KVPool, k_new, v_new, positions, cos_sin, slot_mappin
     dt = pool._rows or _row_dtype(pool)
     torch = _torch
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _made_on(stream, q.device,
+                         lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
     if _fast is not None:
         a, b = ((pool.kv if kv is None else kv, None) if pool.record_bytes else
                 (pool.k_pool if k_pool is None else k_pool, pool.v_pool if v_pool is None else v_pool))
@@ -993,7 +1002,7 @@ def _decode_call(name: str, pool: KVPool, q, out, block_tables, context_lens, sc
     dt = pool._rows or _row_dtype(pool)
     torch = _torch
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     if _fast is not None:
         a, b = ((pool.kv if kv is None else kv, None) if pool.is_b8 else
                 (pool.k_pool if k_pool is None else k_pool, pool.v_pool if v_pool is None else v_pool))
@@ -1076,7 +1085,7 @@ def paged_prefill_attention_window(pool: KVPool, q, block_tables, query_start, c
         raise ValueError("paged_prefill_attention_window takes a 16-bit pool")
     window, sinks = _window(window, sinks)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     if _fast is not None:
         rc = _fast.prefill(pool._meta, q, out, block_tables, query_start, context_lens, float(scale),
                            window, sinks, workspace, status,
@@ -1167,7 +1176,7 @@ def paged_tree_attention(pool: KVPool, q, block_tables, query_start, context_len
     if pool.record_bytes:
         raise ValueError("paged_tree_attention takes a 16-bit pool")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     if _fast is not None:
         rc = _fast.tree(pool._meta, q, out, block_tables, query_start, context_lens, tree_mask,
                         float(scale), workspace, status, pool.k_pool if k_pool is None else k_pool,
@@ -1220,7 +1229,7 @@ def tree_accept(tokens, parents, targets, query_start, first, status, kept=None,
         kept = _made_on(stream, tokens.device, lambda: torch.full(
             (tokens.shape[0],), -1, dtype=torch.int32, device=tokens.device))
     if num_kept is None:
-        num_kept = _made_on(stream, first.device, lambda: torch.empty_like(first))
+        num_kept = _empty_like(first, stream)
     if next_tokens is None:
         next_tokens = _made_on(stream, tokens.device, lambda: torch.empty(
             (first.shape[0],), dtype=tokens.dtype, device=tokens.device))
