@@ -496,10 +496,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     // (the register split is taken inside each role's branch, so that all of a role's code
     // lies under one limit)
     uint32_t nt = 0;                     // items that this role has taken
+    // A wait of the whole warp, false for all lanes once it ran out for one: each lane looks at the
+    // barrier, the flag and the clock by itself, and lanes that went on without the others would
+    // leave these at the warp's next vote.
+    auto reach = [&](uint64_t *bar, uint32_t parity) {
+        return (bool)__all_sync(kFull, mbar_wait(smem_addr(bar), parity, abort_flag, p.status));
+    };
     // the next item's task, false once there is none or a wait ran out
     Task it;
     auto next_task = [&]() {
-        if (!mbar_wait(smem_addr(&task_full[nt % kTasks]), (nt / kTasks) & 1u, abort_flag, p.status)) return false;
+        if (!reach(&task_full[nt % kTasks], (nt / kTasks) & 1u)) return false;
         it = tasks[nt % kTasks];
         return it.t0 < it.t1;
     };
@@ -526,8 +532,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (;;) {
                 it = after;
                 if (nt >= kTasks)
-                    ok = mbar_wait(smem_addr(&task_empty[nt % kTasks]), (nt / kTasks - 1) & 1u, abort_flag, p.status);
-                ok = __all_sync(kFull, ok);
+                    ok = reach(&task_empty[nt % kTasks], (nt / kTasks - 1) & 1u);
                 if (!ok) break;
                 if (elect_one()) {
                     tasks[nt % kTasks] = it;
@@ -570,8 +575,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                         const bool bad = rows_of(t, y);
                         if (kt >= NK)
-                            ok = mbar_wait(smem_addr(&k_empty[kt % NK]), (kt / NK - 1) & 1u, abort_flag, p.status);
-                        ok = __all_sync(kFull, ok);
+                            ok = reach(&k_empty[kt % NK], (kt / NK - 1) & 1u);
                         if (!ok) break;
                         if (elect_one()) {
                             if (bad) atomicOr(p.status, PKV_DEV_BAD_BLOCK);
@@ -582,8 +586,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     if (t == it.t0) {
                         // the item's query rows, once its first K tile is under way
-                        if (items > 0) ok = mbar_wait(smem_addr(q_empty), (items - 1) & 1u, abort_flag, p.status);
-                        ok = __all_sync(kFull, ok);
+                        if (items > 0) ok = reach(q_empty, (items - 1) & 1u);
                         if (!ok) break;
                         ++items;
                         if (elect_one()) {
@@ -597,8 +600,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                     } else {
                         if (vt >= NV)
-                            ok = mbar_wait(smem_addr(&v_empty[vt % NV]), (vt / NV - 1) & 1u, abort_flag, p.status);
-                        ok = __all_sync(kFull, ok);
+                            ok = reach(&v_empty[vt % NV], (vt / NV - 1) & 1u);
                         if (!ok) break;
                         if (elect_one())
                             copy(&tmV, LY::kVRing + (vt % NV) * LY::kTileBytes, &v_full[vt % NV], y_v);
@@ -639,16 +641,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint64_t qa_d = tc::desc_sw128(smem_addr(smem), 16, 1024);
             uint32_t kt = 0;                 // key tiles
             bool ok = true;
-            auto reach = [&](uint64_t *bar, uint32_t parity) {
-                ok = __all_sync(kFull, mbar_wait(smem_addr(bar), parity, abort_flag, p.status));
-                return ok;
-            };
             // P V of tile vt
             auto issue_pv = [&](uint32_t vt) {
                 const uint32_t slot = vt % NV, par = (vt / NV) & 1u, b = vt & 1u;
-                if (!reach(&clean[slot], par) || !reach(&v_full[slot], par) ||
-                    !reach(&p_full[b], (vt >> 1) & 1u))
-                    return;
+                ok = reach(&clean[slot], par) && reach(&v_full[slot], par) && reach(&p_full[b], (vt >> 1) & 1u);
+                if (!ok) return;
                 tc::fence_after_sync();
                 const uint64_t vb_d =
                     tc::desc_sw128(smem_addr(smem + LY::kVRing + slot * LY::kTileBytes), kKeys * 128, 1024);
@@ -664,12 +661,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 __syncwarp();
             };
-            while (ok && __all_sync(kFull, next_task()) && reach(q_full, nt & 1u)) {
+            while (ok && next_task() && reach(q_full, nt & 1u)) {
 #pragma unroll 1
                 for (int t = it.t0; t <= it.t1; ++t) {
                     if (t < it.t1) {
                         const uint32_t slot = kt % NK;
-                        if (!reach(&k_full[slot], (kt / NK) & 1u)) break;
+                        if (!(ok = reach(&k_full[slot], (kt / NK) & 1u))) break;
                         tc::fence_after_sync();
                         const uint64_t kb_d =
                             tc::desc_sw128(smem_addr(smem + LY::kKRing + slot * LY::kTileBytes), 16, 1024);
@@ -713,8 +710,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (; ok && next_task(); ++nt) {
                 for (int t = it.t0; t < it.t1; ++t, ++vt) {
                     const uint32_t slot = vt % NV;
-                    ok = __all_sync(kFull, mbar_wait(smem_addr(&v_full[slot]), (vt / NV) & 1u, abort_flag, p.status));
-                    if (!ok) break;
+                    if (!(ok = reach(&v_full[slot], (vt / NV) & 1u))) break;
                     const int k0 = t * kKeys;
                     if (k0 + kKeys > it.base) {
                         constexpr int kChunks = LY::kRegions * 8;
@@ -769,10 +765,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int jj = r / G, h = r - jj * G;
         uint32_t kt = 0;                 // key tiles
         bool alive = true;
-        // a wait of the whole warp; false once it ran out
-        auto reach = [&](uint64_t *bar, uint32_t parity) {
-            return __all_sync(kFull, mbar_wait(smem_addr(bar), parity, abort_flag, p.status));
-        };
         // the item is done with
         auto leave = [&]() {
             __syncwarp();
