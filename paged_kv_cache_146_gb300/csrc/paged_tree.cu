@@ -449,7 +449,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                   "barriers and flags");
 
     if (smem_addr(smem) & 1023u) {       // the swizzle's atoms; no launch has been seen to do this
-        if (threadIdx.x == 0) atomicOr(p.status, PKV_DEV_TIMEOUT);
+        griddep_wait();
+        if (threadIdx.x == 0) {
+            atomicOr(p.status, PKV_DEV_TIMEOUT);
+            p.ranges[blockIdx.x] = make_int4(0, 0, 0, 0);        // nothing to join
+        }
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -32,3 +32,14 @@ def test_no_barrier_is_polled_without_a_limit():
     polls = [i for i, s in enumerate(code) if "mbar_try_wait(" in s]
     for i in polls:
         assert "while" in code[i] and any("kTimeoutNs" in s for s in code[i:i + 3]), code[i]
+
+
+def test_a_cta_that_gives_up_leaves_nothing_to_join():
+    """The joining kernel goes by what every CTA left in the workspace, so one that ends without a plan
+    leaves an empty range there, after the kernels before it have ended."""
+    with open(SOURCE) as f:
+        code = statements(f.read())
+    start = next(i for i, s in enumerate(code) if "& 1023u" in s)
+    end = next(i for i in range(start, len(code)) if code[i] == "return")
+    waited = code.index("griddep_wait()", start, end)
+    assert any(s.startswith("p.ranges[blockIdx.x] = make_int4(0, 0, 0, 0)") for s in code[waited:end])
