@@ -91,8 +91,9 @@ struct Params {
 
 // What CTA b leaves for the joining kernel: x = 1 it holds the continuation of an item that began
 // in an earlier range (piece 2 b), + 2 up to the item's end, + 4 it begins an item that ends in a
-// later range (piece 2 b + 1), of y tokens from row z on, kv head w.
-constexpr int kContinues = 1, kEnds = 2, kBegins = 4;
+// later range (piece 2 b + 1), of y tokens from row z on, kv head w; + 8 in every range where some
+// sequence's lengths do not fit: the joining kernel makes its rows zero.
+constexpr int kContinues = 1, kEnds = 2, kBegins = 4, kRefused = 8;
 
 // One sequence of a call.
 struct Seq {
@@ -177,8 +178,7 @@ struct Walk {
     }
 
     // The ranges: the units of all sequences are counted, and the two ends of this CTA's range
-    // looked up.  CTA s % gridDim also reports and clears sequences whose lengths do not fit.
-    template <int D>
+    // looked up.  CTA s % gridDim also reports sequences whose lengths do not fit.
     __device__ __forceinline__ void plan(const Params &p)
     {
         const int lane = threadIdx.x & 31;
@@ -186,6 +186,7 @@ struct Walk {
         auto units_of = [&](const Seq &x) { return (uint32_t)p.num_kv_heads * (uint32_t)(x.tiles + kItemCost); };
         uint32_t all = 0;
         most = 0;
+        bool refused = false;
 #pragma unroll 1
         for (int s0 = 0; s0 < p.num_seqs; s0 += 32 * kAhead) {
             int a[kAhead], b[kAhead], len[kAhead];       // the loads of several steps at once
@@ -205,13 +206,11 @@ struct Walk {
                 const Seq x = seq_of(p, a[k], b[k], len[k]);
                 all += x.parts * units_of(x);
                 most = max(most, x.parts);
-                if (x.bad && (s0 + 32 * k + lane) % gridDim.x == blockIdx.x) {
-                    atomicOr(p.status, PKV_DEV_BAD_LEN);
-                    uint4 *o = static_cast<uint4 *>(p.out) + (int64_t)x.r0 * p.num_q_heads * (D / 8);
-                    for (int64_t i = 0; i < (int64_t)x.n * p.num_q_heads * (D / 8); ++i) o[i] = make_uint4(0, 0, 0, 0);
-                }
+                refused |= x.bad;
+                if (x.bad && (s0 + 32 * k + lane) % gridDim.x == blockIdx.x) atomicOr(p.status, PKV_DEV_BAD_LEN);
             }
         }
+        refused = __any_sync(kFull, refused);
         all = __reduce_add_sync(kFull, all);
         most = __reduce_max_sync(kFull, most);
         const uint32_t ranges = max(1u, min(gridDim.x, all));
@@ -222,7 +221,7 @@ struct Walk {
         const uint32_t begin = size * blockIdx.x + more * blockIdx.x / ranges;
         const uint32_t end = size * (blockIdx.x + 1) + more * (blockIdx.x + 1) / ranges;
         at = to = Place{most, 0, 0, 0};
-        int4 left = make_int4(0, 0, 0, 0);               // for the joining kernel
+        int4 left = make_int4(refused ? kRefused : 0, 0, 0, 0);          // for the joining kernel
         uint32_t before = 0;
 #pragma unroll 1
         for (int k = 0; k < most && blockIdx.x < ranges && before <= end; ++k) {
@@ -251,7 +250,7 @@ struct Walk {
                     }
                     to = c;
                     const int first = k * p.tile_tokens;
-                    left = make_int4(0, min(p.tile_tokens, x.n - first), x.r0 + first, c.g);
+                    left = make_int4(left.x, min(p.tile_tokens, x.n - first), x.r0 + first, c.g);
                 }
                 before += __shfl_sync(kFull, upto, 31);
             }
@@ -519,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             uint32_t kt = 0, vt = 0, items = 0;      // K tiles, V tiles and items under way or done
             bool ok = true;
             Walk walk;
-            walk.plan<D>(p);
+            walk.plan(p);
             // 32 block ids, 8 tiles, at a time, one batch ahead; behind the end any block will do
             auto ids_from = [&](const Task &k, int t) {
                 const int b = 4 * t + lane;
@@ -992,6 +991,28 @@ __device__ __forceinline__ int tasks_of(const Params &p, int D, int tokens)
     return (tokens * p.group + 31) / 32 * (D / 8);
 }
 
+// Zero rows for the sequences whose lengths do not fit: their number of rows is whatever the
+// caller gave, so all CTAs share them (in the main kernel others would wait for the CTA that
+// does it).
+template <int D>
+__device__ __noinline__ void clear_refused(const Params &p)
+{
+    const int lane = threadIdx.x & 31;
+    for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+        const int i = min(s0 + lane, p.num_seqs - 1);
+        const Seq x = seq_of(p, p.query_start[i], p.query_start[i + 1], p.context_lens[i]);
+        for (unsigned bad = __ballot_sync(kFull, s0 + lane < p.num_seqs && x.bad); bad; bad &= bad - 1) {
+            const int src = __ffs(bad) - 1;
+            const int64_t row = (int64_t)p.num_q_heads * (D / 8);        // in 16-byte chunks
+            const int64_t all = row * __shfl_sync(kFull, x.n, src);
+            uint4 *out = static_cast<uint4 *>(p.out) + row * (all ? __shfl_sync(kFull, x.r0, src) : 0);
+            for (int64_t c = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; c < all;
+                 c += (int64_t)gridDim.x * kJoinThreads)
+                out[c] = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads, 1) tree_join_kernel(const Params p)
 {
@@ -1012,6 +1033,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1) tree_join_kernel(const Params
     };
     int4 range = make_int4(0, 0, 0, 0);
     if (tid < p.grid) ranges[tid] = range = p.ranges[tid];
+    if (p.ranges[0].x & kRefused) clear_refused<D>(p);
     const unsigned begun = __ballot_sync(kFull, range.x & kBegins);
     int items;
     const int rank = across(__popc(begun), items) + __popc(begun & ((1u << lane) - 1u));
