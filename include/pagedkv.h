@@ -687,7 +687,8 @@ size_t paged_tree_workspace_bytes(int32_t num_tokens, int32_t num_q_heads, int32
  * context_lens[s] includes the drafted tokens.  A row that sees nothing is zero.
  * What a row does not see cannot reach it, whatever it holds, NaN and infinities
  * included.  (All rows see the cache before the drafted tokens: an infinity in its
- * V gives that infinity, or NaN where the token's weight has no second 16-bit part.)
+ * V gives that infinity; for a token that weighs less than 2^-8 of the row's largest
+ * weight, fp16 pools, or 2^-78, bf16, it may give NaN.)
  * A sequence whose lengths do not fit (PKV_DEV_BAD_LEN) or that has a bad table
  * entry among its ceil(context_lens[s] / 16) blocks (PKV_DEV_BAD_BLOCK) gets zero
  * rows.

@@ -358,8 +358,11 @@ __device__ __forceinline__ uint64_t seen_keys(const Params &p, const uint32_t *w
 }
 
 // Weights (p0, p1), pp = the same pair packed, as two 16-bit parts, the even key in the low
-// half of each word.  bf16: truncated (its upper 16 bits, exact), then the remainder rounded:
-// to 2^-15.  fp16: rounded, then the remainder rounded: to 2^-22.
+// half of each word.  The first part is truncated, the rest rounded: bf16 2^-16, fp16 2^-22 (of
+// the weight).  The rest is taken 2^-24 of the first part too large, well within that, so that no
+// part is negative, or zero beside another one, as long as 16 bits can hold it: an infinity in V
+// times the parts is that infinity, where inf - inf or 0 inf would be NaN.
+constexpr float kRest = -(1.f - 0x1p-24f);
 template <bool BF16>
 __device__ __forceinline__ void two_parts(float p0, float p1, uint64_t pp, uint32_t &hi, uint32_t &lo)
 {
@@ -369,10 +372,10 @@ __device__ __forceinline__ void two_parts(float p0, float p1, uint64_t pp, uint3
         hi = __byte_perm(b0, b1, 0x7632);
         h = make_float2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u));
     } else {
-        hi = Elem<false>::pack(p0, p1);
+        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(p1), "f"(p0));
         h = Elem<false>::unpack(hi);
     }
-    const float2 d = unpack2f(sub2f(pp, pack2f(h.x, h.y)));
+    const float2 d = unpack2f(fma2f(pack2f(h.x, h.y), pack2f(kRest, kRest), pp));
     lo = Elem<BF16>::pack(d.x, d.y);
 }
 
