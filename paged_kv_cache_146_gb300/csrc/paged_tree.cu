@@ -800,6 +800,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (!(alive = reach(&s_full[b], (kt >> 1) & 1u))) break;
                 if (!busy) {
                     if (lane == 0) mbar_arrive(smem_addr(&p_full[b]));
+                    // (a barrier tells even phases from odd ones only: no phase is left out)
+                    if (t > it.t0 && !(alive = reach(&o_full[b ^ 1u], ((kt - 1) >> 1) & 1u))) break;
                     continue;
                 }
                 tc::fence_after_sync();

@@ -43,3 +43,14 @@ def test_a_cta_that_gives_up_leaves_nothing_to_join():
     end = next(i for i in range(start, len(code)) if code[i] == "return")
     waited = code.index("griddep_wait()", start, end)
     assert any(s.startswith("p.ranges[blockIdx.x] = make_int4(0, 0, 0, 0)") for s in code[waited:end])
+
+
+def test_warps_without_rows_take_every_phase():
+    """A barrier tells even phases from odd ones only.  A softmax warp that has no rows, and waits only
+    for the last product of an item, could take the end of the last but two for it; so it waits for each
+    tile's, as the others do."""
+    with open(SOURCE) as f:
+        code = statements(f.read())
+    start = next(i for i, s in enumerate(code) if s.startswith("if (!busy)") or s == "if (!busy)")
+    end = code.index("continue", start)
+    assert any("reach(&o_full[b ^ 1u], ((kt - 1) >> 1) & 1u)" in s for s in code[start:end])
