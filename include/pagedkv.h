@@ -746,8 +746,9 @@ int kv_tree_accept(const void *tokens, const int32_t *parents, const void *targe
  * A sequence whose ranges do not fit is left as it is (PKV_DEV_BAD_LEN); from the
  * first position that does not rise, lies below its destination or outside the
  * table row on, the rest of the sequence's stay where they are
- * (PKV_DEV_BAD_TREE); a token whose own or destination block is not in the pool
- * is skipped (PKV_DEV_BAD_BLOCK).  16-bit pools, rows of a multiple of 16 bytes,
+ * (PKV_DEV_BAD_TREE); a token that moves and whose own or destination block is not
+ * in the pool is skipped (PKV_DEV_BAD_BLOCK; tokens that are at their destination
+ * are not looked up).  16-bit pools, rows of a multiple of 16 bytes,
  * at most 65,535 sequences.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA. */
 int kv_cache_compact(const pkv_pool *pool, const int32_t *block_tables,
