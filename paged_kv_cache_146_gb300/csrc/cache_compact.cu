@@ -41,7 +41,8 @@ struct Trees {
 // A warp per sequence.  Trees of up to kHeld nodes are read at once, one latency for all, and
 // walked in registers: a step takes the target from the lane that holds the last kept node and
 // asks all nodes whether they are its child and hold that token.  256 trees of 21 to 64 nodes: 3.9
-// us back to back (6.4 when each step read its nodes from L1; one small tree 2.5, the launch).
+// us back to back (5.7 when each step read its nodes from L1; one small tree 2.6, the launch).
+// Larger trees read theirs at each step: 64 of 129 to 400 nodes 7.0, 8 of 1,024 10.7.
 constexpr int kAcceptWarps = 4, kSteps = 4, kHeld = 32 * kSteps;
 
 template <typename T>
@@ -150,15 +151,18 @@ struct Moves {
 // longest list's 8,000 tokens set the end); before the last steps it was 71 us, 93 with whole rows to
 // a CTA, four times as long when each thread looked up its rows' places.
 //
-// Threads, chunks of a thread under way, tokens of a batch at most, CTAs to an SM.
+// Threads, chunks of a thread under way, tokens of a batch at most, CTAs to an SM.  The host
+// chooses by the lists' room, num_entries / num_seqs, as what is kept of it is on the device: right
+// for lists that fill their room, while the few kept nodes of wide trees go to Many (96 trees of 64
+// nodes of which 1 to 6 are kept 7.9 us, 256 18.0; of 16 nodes, Brief, 3.5 and 7.2).
 //   Many: what is under way on an SM is the same as in Few, but a CTA waits for its slowest row, so
 //     many small ones end earlier (100 caches of 300 to 900 tokens 59 us, 77 with Few, then).
 //   Uneven: up to 32 long lists share their rows by length (10 lists of 1,000 to 14,000 tokens 113
-//     us, 140 with Many; below kLongList tokens on average the search costs more than it gives, 20
+//     us, 140 with Many; below kLongList entries on average the search costs more than it gives, 20
 //     lists of 130: 9.8 us against 6.6, then).
 //   Few: calls with no more CTAs than SMs (a cache of 16,000 tokens: 64; 29 us, 56 with Many).
-//   Brief: lists far shorter than a batch, several pairs to a CTA (96 lists of up to 6: 3.6 us, 8.0
-//     with Many; 64 lists of 20 to 100: 7.5, 6.2 with Many).
+//   Brief: room of up to kBriefList entries, far less than a batch, several pairs to a CTA (96 lists of
+//     up to 6 in 16: 3.6 us, 8.0 with Many; 64 lists of 20 to 100: 7.5, 6.2 with Many).
 struct Many {
     static constexpr bool kByLength = false, kPairs = false;
     static constexpr int kThreads = 256, kDepth = 8, kBatch = 512, kCtas = 3;

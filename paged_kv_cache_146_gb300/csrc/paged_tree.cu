@@ -20,11 +20,14 @@
 //
 // What bounds it, 32 query heads over 8 of 128: at 96 sequences of up to 16,384 tokens with 16
 // drafted ones the copies of K and V (3.43 GB in 511-556 us, 6.2-6.7 TB/s; a plain copy's
-// rate is 6.8).  At 24 sequences with 64 drafted, two full query tiles each, nothing alone (141-149 us; the
-// bytes 70, the products 59): the main kernel's 128 us bring every key tile twice (7.4 TB/s from
-// L2), keep the tensor pipe busy for 58 % (P V once for each part of the weights), and the softmax
-// warps wait for fixed latencies; 15 us go to joining 39 MB of pieces.  At 4 sequences, 22 us, the
-// chain of lengths -> plan -> block ids -> tiles -> pieces -> joining kernel (the bytes 6).
+// rate is 6.8).  At 24 sequences with 64 drafted, two full query tiles each, nothing alone (140-156 us
+// by machine; the bytes 70, the products 59): the main kernel's 128 us bring every key tile twice
+// (7.4 TB/s from L2), keep the tensor pipe busy for 58 % (P V once for each part of the weights), and
+// the softmax warps wait for fixed latencies; 15 us go to joining 39 MB of pieces.  A second tile
+// that is partly full costs as much as a full one: 64 sequences of 33 drafted tokens behind 500
+// 62 us, three times their bytes.  At 4 sequences, 22 us, the chain of lengths -> plan -> block ids ->
+// tiles -> pieces -> joining kernel (the bytes 6).  Heads of 64: a key tile is half the bytes, the chain
+// as long (29 sequences of 40 heads 90 us, the bytes 63).
 //
 // Roles of a CTA's warps:
 //   0-3, softmax: thread r owns row r.  Weights are taken against a lazy reference (it moves
@@ -648,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         } else if (warp == kIssuer) {
             // bit 13 negates A: with a negative scale the products, so that all else counts up
-        const uint32_t id_qk = tc::idesc_f16(BF16, kRows, kKeys, 0, 0) | (p.negate ? 1u << 13 : 0u);
+            const uint32_t id_qk = tc::idesc_f16(BF16, kRows, kKeys, 0, 0) | (p.negate ? 1u << 13 : 0u);
             const uint32_t id_pv = tc::idesc_f16(BF16, kRows, D, 0, 1);
             const uint32_t t_s = __shfl_sync(kFull, tmem, 0), t_o = t_s + 128;
             const uint64_t qa_d = tc::desc_sw128(smem_addr(smem), 16, 1024);
