@@ -32,7 +32,7 @@
 // Roles of a CTA's warps:
 //   0-3, softmax: thread r owns row r.  Weights are taken against a lazy reference (it moves
 //     when a score exceeds it by more than kLazy, in log2 units), as two 16-bit parts each,
-//     into tensor memory.
+//     into tensor memory.  Every kFlush tiles O goes to a sum in the workspace.
 //   4, producer: makes the plan and hands out the items; a ring of K tiles and one of V tiles,
 //     one TMA box to each block and 64 columns; the items' query rows.
 //   5, issuer: S = Q K^T into one of two buffers, then O += P V of the tile before.
@@ -70,6 +70,13 @@ constexpr float kLazy = 8.f;
 // drafted tokens: 143 us, 147 with 1; the 40 heads 97 with 4).
 constexpr int kItemCost = 2, kSnap = 2;
 constexpr int kMaxRanges = 304;        // CTAs of a call, at most
+// Tiles after which O is moved to a sum in the workspace.  The tensor cores' additions into O
+// truncate, so O falls behind by some 2^-23 of itself with every matrix instruction: 131,072 tokens of
+// positive values came out 1.1e-3 low, twice the half step of fp16, 16,384 2e-4.  Moved every 128
+// tiles it is 1e-4 whatever the length, and the sums of the moved ones round.  (96 sequences of up
+// to 16,384 tokens 528 -> 534 us; every 64 tiles 5e-5 and 539.  Without the hint that keeps the
+// sums in L2 545 and 557.)
+constexpr int kFlush = 128;
 
 struct Params {
     void *out;
@@ -367,11 +374,11 @@ __device__ __forceinline__ uint64_t seen_keys(const Params &p, const uint32_t *w
 // times the parts is that infinity, where inf - inf or 0 inf would be NaN.
 //
 // bf16 stays at two parts: 2^-16 is 2^-8 of what the output's own rounding takes off, and moves one
-// value in some hundred by that rounding's step (1.6 of 10,000 of a result's norm; its error
-// against 64 bits is the same, 1.66e-3).  A third part (2^-24, 0.4 of 10,000) is half as many
-// products again and has no place in tensor memory; with it in shared memory 96 long sequences
-// took 604-630 us in place of 512-528, 24 x 64 168-176 in place of 140-143, and as much where it
-// borrowed the next tile's columns.
+// value in some hundred by that rounding's step (1.4e-4 of a result's norm; its error against 64
+// bits is the same, 1.66e-3).  A third part (2^-24; 0.9e-4 on 4 sequences, no gain on long contexts,
+// where it is the sums' rounding) is half as many products again and has no place in tensor memory;
+// with it in shared memory 96 long sequences took 604-630 us in place of 512-528, 24 x 64 168-176 in
+// place of 140-143, and as much where it borrowed the next tile's columns.
 constexpr float kRest = -(1.f - 0x1p-24f);
 template <bool BF16>
 __device__ __forceinline__ void two_parts(float p0, float p1, uint64_t pp, uint32_t &hi, uint32_t &lo)
@@ -403,6 +410,57 @@ __device__ __forceinline__ void add_odd(uint32_t &sum, uint32_t w)
 {
     if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w), "r"(0u));
     else asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w), "r"(0u));
+}
+
+// The row's sum of the tiles before the last kFlush ones lies in the workspace, in the place of the
+// item's piece (an item that is not cut uses the later one: the cut item that fills it comes last).
+// O, of reference ref, is added to it and cleared, or (back) it is added to O; `any`: there is
+// something in it.  The whole warp calls it; as a function it leaves the loop's code alone (inlined,
+// calls that never come here took 8 % longer).
+template <int D>
+__device__ __noinline__ void move_sum(const Params &p, uint32_t t_o, bool begins, bool valid, bool any,
+                                      float sum_ref, float ref, bool back)
+{
+    const int64_t rows = p.piece_rows;
+    float4 *sum = p.part_o + (2 * blockIdx.x + begins) * (D / 4) * rows + threadIdx.x;
+    const float g = sum_ref == kHide ? 0.f : fast_exp2((sum_ref - ref) * p.scale_log2);
+    // most references do not move any more: then nothing is read
+    const bool plain = !back && any && __all_sync(kFull, !valid || g == 1.f);
+    const bool read = any && valid && !plain;
+    uint64_t keep;                       // in L2, as keys pass through it
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 32, sum += 8 * rows) {
+        float4 w[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            w[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (read)
+                asm volatile("ld.relaxed.gpu.global.L2::cache_hint.v4.f32 {%0, %1, %2, %3}, [%4], %5;"
+                             : "=f"(w[c].x), "=f"(w[c].y), "=f"(w[c].z), "=f"(w[c].w) : "l"(sum + c * rows), "l"(keep) : "memory");
+        }
+        uint32_t v[32];
+        tc::tmem_ld32(t_o + c0, v);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            uint32_t *x = &v[4 * c];
+            const float4 y = make_float4(__uint_as_float(x[0]) + g * w[c].x, __uint_as_float(x[1]) + g * w[c].y,
+                                         __uint_as_float(x[2]) + g * w[c].z, __uint_as_float(x[3]) + g * w[c].w);
+            if (plain && valid)
+                asm volatile("red.relaxed.gpu.global.add.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(sum + c * rows), "f"(y.x),
+                             "f"(y.y), "f"(y.z), "f"(y.w), "l"(keep) : "memory");
+            else if (!back && valid)
+                asm volatile("st.relaxed.gpu.global.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(sum + c * rows), "f"(y.x),
+                             "f"(y.y), "f"(y.z), "f"(y.w), "l"(keep) : "memory");
+            x[0] = back ? __float_as_uint(y.x) : 0u;
+            x[1] = back ? __float_as_uint(y.y) : 0u;
+            x[2] = back ? __float_as_uint(y.z) : 0u;
+            x[3] = back ? __float_as_uint(y.w) : 0u;
+        }
+        tc::tmem_st32(t_o + c0, v);
+    }
+    tc::tmem_wait_st();
 }
 
 template <int D>
@@ -797,6 +855,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint32_t *words = p.mask + (int64_t)(it.r0 + (valid ? token : it.first)) * p.words;
             const uint32_t w0 = words[0], w1 = p.words > 1 ? words[1] : 0u;
             float ref = kHide, l = 0.f;
+            float sum_ref = kHide;                       // the reference of the moved sum, see kFlush
             int bad = 0;
             if (busy) {
                 uint32_t z[32];
@@ -805,137 +864,146 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int c0 = 0; c0 < D; c0 += 32) tc::tmem_st32(t_o + c0, z);
             }
-            for (int t = it.t0; t < it.t1; ++t, ++kt) {
-                const uint32_t b = kt & 1u, vslot = kt % NV;
-                if (!(alive = reach(&s_full[b], (kt >> 1) & 1u))) break;
-                if (!busy) {
-                    if (lane == 0) mbar_arrive(smem_addr(&p_full[b]));
-                    // (a barrier tells even phases from odd ones only: no phase is left out)
-                    if (t > it.t0 && !(alive = reach(&o_full[b ^ 1u], ((kt - 1) >> 1) & 1u))) break;
-                    continue;
-                }
-                tc::fence_after_sync();
-                bad |= bad_blocks[kt % kTilesKnown];
-                const int k0 = t * kKeys;
-                const bool edge = k0 + kKeys > base;     // drafted tokens or the end: masks
-                uint64_t see = ~0ull;
-                if (edge && valid) see = seen_keys(p, words, w0, w1, k0, base, L);
-                // the tile's products (the scale is in the exponents), those that the row does not see
-                // hidden; read once (twice, 32 at a time: 22 sequences of 25,000 tokens in 3 heads
-                // of 64 take 93 us in place of 85)
-                float x[kKeys];
-                {
-                    uint32_t v[2][32];
-                    tc::tmem_ld32(t_s + 64 * b, v[0]);
-                    tc::tmem_ld32(t_s + 64 * b + 32, v[1]);
-                    tc::tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < kKeys; ++c) x[c] = __uint_as_float(v[c / 32][c % 32]);
-                }
-                if (edge) {
-#pragma unroll
-                    for (int c = 0; c < kKeys; ++c)
-                        if (!((uint32_t)(see >> (c & 32)) >> (c & 31) & 1u)) x[c] = kHide;
-                }
-                // the largest, in four chains (one of 32 steps would be waited for)
-                float m[4] = {kHide, kHide, kHide, kHide};
-#pragma unroll
-                for (int c = 0; c < kKeys; c += 2) m[c / 2 % 4] = max3f(m[c / 2 % 4], x[c], x[c + 1]);
-                const float mx = fmaxf(max3f(m[0], m[1], m[2]), m[3]);
-                // The reference is a product: a weight is 2^((x - ref) scale + kTop), so products
-                // that agree weigh alike whatever their size, and nothing is lost to the rounding
-                // of a scaled reference.
-                float f = 1.f;
-                bool resc = false;
-                const bool unset = ref == kHide;          // no key seen yet
-                if (valid && mx != kHide && (unset || (mx - ref) * p.scale_log2 > kLazy)) {
-                    if (!unset) {
-                        f = fast_exp2((ref - mx) * p.scale_log2);
-                        resc = true;
+            for (int s0 = it.t0; alive && s0 < it.t1; s0 += kFlush) {
+                const int s1 = min(s0 + kFlush, it.t1);
+                for (int t = s0; t < s1; ++t, ++kt) {
+                    const uint32_t b = kt & 1u, vslot = kt % NV;
+                    if (!(alive = reach(&s_full[b], (kt >> 1) & 1u))) break;
+                    if (!busy) {
+                        if (lane == 0) mbar_arrive(smem_addr(&p_full[b]));
+                        // (a barrier tells even phases from odd ones only: no phase is left out)
+                        if (t > s0 && !(alive = reach(&o_full[b ^ 1u], ((kt - 1) >> 1) & 1u))) break;
+                        continue;
                     }
-                    ref = mx;
-                }
-                // (any finite reference gives hidden products weight 2^-inf = 0)
-                const float sub = ref == kHide ? 0.f : ref;
-                const uint64_t sc2 = pack2f(p.scale_log2, p.scale_log2), sub2 = pack2f(-sub, -sub);
-                const uint64_t top2 = pack2f(kTop, kTop);
-                uint64_t lsum2 = pack2f(0.f, 0.f);
-                // weights over the products' columns: 16 of high parts, 16 of low parts
-#pragma unroll
-                for (int c0 = 0; c0 < kKeys; c0 += 32) {
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        const uint64_t d2 = add2f(pack2f(x[c0 + c], x[c0 + c + 1]), sub2);
-                        const float2 e = unpack2f(kTop == 0.f ? mul2f(d2, sc2) : fma2f(d2, sc2, top2));
-                        const float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
-                        const uint64_t pp = pack2f(p0, p1);
-                        lsum2 = add2f(lsum2, pp);
-                        two_parts<BF16>(p0, p1, pp, hi[c / 2], lo[c / 2]);
-                    }
-                    tc::tmem_st16(t_s + 64 * b + c0, hi);
-                    tc::tmem_st16(t_s + 64 * b + c0 + 16, lo);
-                }
-                const float2 ls = unpack2f(lsum2);
-                l = l * f + (ls.x + ls.y);
-                uint64_t odd = 0ull;                     // keys whose V held odd values
-                if (edge) {
-                    if (!(alive = reach(&clean[vslot], (kt / NV) & 1u))) break;
-                    odd = odd_keys[vslot];
-                }
-                // O changes before P V of this tile, once P V of the one before has ended; the
-                // wait for that consumes its o_full phase either here or after P is out
-                const bool touch = __any_sync(kFull, resc) || odd;
-                if (touch && t > it.t0) {
-                    if (!(alive = reach(&o_full[b ^ 1u], ((kt - 1) >> 1) & 1u))) break;
                     tc::fence_after_sync();
-                }
-                if (touch) {
-                    tc::tmem_wait_st();                  // (O's zeros, in an item's first tile; P)
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        uint32_t v[32];
-                        tc::tmem_ld32(t_o + c0, v);
+                    bad |= bad_blocks[kt % kTilesKnown];
+                    const int k0 = t * kKeys;
+                    const bool edge = k0 + kKeys > base;     // drafted tokens or the end: masks
+                    uint64_t see = ~0ull;
+                    if (edge && valid) see = seen_keys(p, words, w0, w1, k0, base, L);
+                    // the tile's products (the scale is in the exponents), those that the row does not see
+                    // hidden; read once (twice, 32 at a time: 22 sequences of 25,000 tokens in 3 heads
+                    // of 64 take 93 us in place of 85)
+                    float x[kKeys];
+                    {
+                        uint32_t v[2][32];
+                        tc::tmem_ld32(t_s + 64 * b, v[0]);
+                        tc::tmem_ld32(t_s + 64 * b + 32, v[1]);
                         tc::tmem_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * f);
-                        tc::tmem_st32(t_o + c0, v);
+    #pragma unroll
+                        for (int c = 0; c < kKeys; ++c) x[c] = __uint_as_float(v[c / 32][c % 32]);
                     }
-                    tc::tmem_wait_st();
-                    // the odd values of a key's V go to the rows that see it, times their weights
-                    // (an infinity, or NaN; 0 * infinity is NaN)
-#pragma unroll 1
-                    for (uint64_t left = odd; left; left &= left - 1) {
-                        const int c = __ffsll((long long)left) - 1, pos = k0 + c;
-                        const uint32_t word = t_s + 64 * b + (c & 32) + (c & 31) / 2;
-                        const uint32_t both = column(word) | column(word + 16);
-                        const bool some = (both >> (16 * (c & 1)) & 0x7fffu) != 0u;
-                        int id = p.block_tables[(int64_t)it.s * p.max_blocks_per_seq + pos / kBlock];
-                        if (id < 0 || id >= p.num_blocks) id = 0;            // (the result is zero anyway)
-                        const T *vp = static_cast<const T *>(p.v_pool) +
-                                      (((int64_t)id * Hkv + it.g) * kBlock + pos % kBlock) * D;
-#pragma unroll 1
-                        for (int d = 0; d < D; ++d) {
-                            const float y = (float)vp[d];
-                            if (fabsf(y) < INFINITY) continue;               // the same for the warp
-                            const float o = __uint_as_float(column(t_o + d));
-                            set_column(t_o + d, __float_as_uint(see >> c & 1u ? o + (some ? y : NAN) : o));
+                    if (edge) {
+    #pragma unroll
+                        for (int c = 0; c < kKeys; ++c)
+                            if (!((uint32_t)(see >> (c & 32)) >> (c & 31) & 1u)) x[c] = kHide;
+                    }
+                    // the largest, in four chains (one of 32 steps would be waited for)
+                    float m[4] = {kHide, kHide, kHide, kHide};
+    #pragma unroll
+                    for (int c = 0; c < kKeys; c += 2) m[c / 2 % 4] = max3f(m[c / 2 % 4], x[c], x[c + 1]);
+                    const float mx = fmaxf(max3f(m[0], m[1], m[2]), m[3]);
+                    // The reference is a product: a weight is 2^((x - ref) scale + kTop), so products
+                    // that agree weigh alike whatever their size, and nothing is lost to the rounding
+                    // of a scaled reference.
+                    float f = 1.f;
+                    bool resc = false;
+                    const bool unset = ref == kHide;          // no key seen yet
+                    if (valid && mx != kHide && (unset || (mx - ref) * p.scale_log2 > kLazy)) {
+                        if (!unset) {
+                            f = fast_exp2((ref - mx) * p.scale_log2);
+                            resc = true;
+                        }
+                        ref = mx;
+                    }
+                    // (any finite reference gives hidden products weight 2^-inf = 0)
+                    const float sub = ref == kHide ? 0.f : ref;
+                    const uint64_t sc2 = pack2f(p.scale_log2, p.scale_log2), sub2 = pack2f(-sub, -sub);
+                    const uint64_t top2 = pack2f(kTop, kTop);
+                    uint64_t lsum2 = pack2f(0.f, 0.f);
+                    // weights over the products' columns: 16 of high parts, 16 of low parts
+    #pragma unroll
+                    for (int c0 = 0; c0 < kKeys; c0 += 32) {
+                        uint32_t hi[16], lo[16];
+    #pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            const uint64_t d2 = add2f(pack2f(x[c0 + c], x[c0 + c + 1]), sub2);
+                            const float2 e = unpack2f(kTop == 0.f ? mul2f(d2, sc2) : fma2f(d2, sc2, top2));
+                            const float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
+                            const uint64_t pp = pack2f(p0, p1);
+                            lsum2 = add2f(lsum2, pp);
+                            two_parts<BF16>(p0, p1, pp, hi[c / 2], lo[c / 2]);
+                        }
+                        tc::tmem_st16(t_s + 64 * b + c0, hi);
+                        tc::tmem_st16(t_s + 64 * b + c0 + 16, lo);
+                    }
+                    const float2 ls = unpack2f(lsum2);
+                    l = l * f + (ls.x + ls.y);
+                    uint64_t odd = 0ull;                     // keys whose V held odd values
+                    if (edge) {
+                        if (!(alive = reach(&clean[vslot], (kt / NV) & 1u))) break;
+                        odd = odd_keys[vslot];
+                    }
+                    // O changes before P V of this tile, once P V of the one before has ended; the
+                    // wait for that consumes its o_full phase either here or after P is out
+                    const bool touch = __any_sync(kFull, resc) || odd;
+                    if (touch && t > s0) {
+                        if (!(alive = reach(&o_full[b ^ 1u], ((kt - 1) >> 1) & 1u))) break;
+                        tc::fence_after_sync();
+                    }
+                    if (touch) {
+                        tc::tmem_wait_st();                  // (O's zeros, in an item's first tile; P)
+    #pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t v[32];
+                            tc::tmem_ld32(t_o + c0, v);
+                            tc::tmem_wait_ld();
+    #pragma unroll
+                            for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * f);
+                            tc::tmem_st32(t_o + c0, v);
+                        }
+                        tc::tmem_wait_st();
+                        // the odd values of a key's V go to the rows that see it, times their weights
+                        // (an infinity, or NaN; 0 * infinity is NaN)
+    #pragma unroll 1
+                        for (uint64_t left = odd; left; left &= left - 1) {
+                            const int c = __ffsll((long long)left) - 1, pos = k0 + c;
+                            const uint32_t word = t_s + 64 * b + (c & 32) + (c & 31) / 2;
+                            const uint32_t both = column(word) | column(word + 16);
+                            const bool some = (both >> (16 * (c & 1)) & 0x7fffu) != 0u;
+                            int id = p.block_tables[(int64_t)it.s * p.max_blocks_per_seq + pos / kBlock];
+                            if (id < 0 || id >= p.num_blocks) id = 0;            // (the result is zero anyway)
+                            const T *vp = static_cast<const T *>(p.v_pool) +
+                                          (((int64_t)id * Hkv + it.g) * kBlock + pos % kBlock) * D;
+    #pragma unroll 1
+                            for (int d = 0; d < D; ++d) {
+                                const float y = (float)vp[d];
+                                if (fabsf(y) < INFINITY) continue;               // the same for the warp
+                                const float o = __uint_as_float(column(t_o + d));
+                                set_column(t_o + d, __float_as_uint(see >> c & 1u ? o + (some ? y : NAN) : o));
+                            }
                         }
                     }
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&p_full[b]));
+                    if (!touch && t > s0) {
+                        if (!(alive = reach(&o_full[b ^ 1u], ((kt - 1) >> 1) & 1u))) break;
+                    }
                 }
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&p_full[b]));
-                if (!touch && t > it.t0) {
-                    if (!(alive = reach(&o_full[b ^ 1u], ((kt - 1) >> 1) & 1u))) break;
+                if (!alive) break;
+                // the last P V is done (which writes the lanes of warps without rows too: they wait before
+                // another item's zeros)
+                if (!(alive = reach(&o_full[(kt - 1) & 1u], ((kt - 1) >> 1) & 1u))) break;
+                tc::fence_after_sync();
+                if (busy && it.t1 - it.t0 > kFlush) {
+                    move_sum<D>(p, t_o, it.t0 == 0, valid, s0 > it.t0, sum_ref, ref, s1 == it.t1);
+                    sum_ref = ref;
                 }
             }
             if (!alive) break;
-            // ---- the part's result, once its last P V is done (which writes the lanes of warps
-            // without rows too: they wait before another item's zeros)
-            if (!reach(&o_full[(kt - 1) & 1u], ((kt - 1) >> 1) & 1u)) break;
-            tc::fence_after_sync();
+            // ---- the part's result
             if (!busy) {
                 leave();
                 continue;
