@@ -143,3 +143,34 @@ def test_outputs_do_not_lie_where_queued_work_writes(name):
             torch.empty_like(q).fill_(9.0)
     torch.cuda.synchronize()
     assert torch.equal(copy, want)
+
+
+@pytest.mark.parametrize("name", ["tree", "accept"])
+def test_a_captured_call_on_a_stream_of_its_own(name):
+    """A capture that forks to the call's stream and joins it again; the results are the graph's."""
+    if name == "tree":
+        call, q, status = plain_call("tree")
+        want = call(None)
+    else:
+        args, kept, num, nxt = trees(5, [30, 9, 140])
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+        def call(st):
+            return torch.cat([t.long() for t in P.tree_accept(*args, status, stream=st)]) if st is None else \
+                P.tree_accept(*args, status, stream=st)
+        want = call(None)
+        assert want.tolist() == kept + num + nxt
+    side, held = torch.cuda.Stream(), torch.zeros_like(want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+        held.copy_(got if name == "tree" else torch.cat([t.long() for t in got]))
+        del got
+    for _ in range(3):
+        held.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert status.item() == 0 and torch.equal(held, want)
