@@ -427,8 +427,9 @@ __device__ __noinline__ void move_sum(const Params &p, uint32_t t_o, bool begins
     // most references do not move any more: then nothing is read
     const bool plain = !back && any && __all_sync(kFull, !valid || g == 1.f);
     const bool read = any && valid && !plain;
-    uint64_t keep;                       // in L2, as keys pass through it
-    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+    uint64_t hint;                       // stays in L2 while keys pass through it, until it is read back
+    if (back) asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(hint));
+    else asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(hint));
 #pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += 32, sum += 8 * rows) {
         float4 w[8];
@@ -437,7 +438,9 @@ __device__ __noinline__ void move_sum(const Params &p, uint32_t t_o, bool begins
             w[c] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (read)
                 asm volatile("ld.relaxed.gpu.global.L2::cache_hint.v4.f32 {%0, %1, %2, %3}, [%4], %5;"
-                             : "=f"(w[c].x), "=f"(w[c].y), "=f"(w[c].z), "=f"(w[c].w) : "l"(sum + c * rows), "l"(keep) : "memory");
+                             : "=f"(w[c].x), "=f"(w[c].y), "=f"(w[c].z), "=f"(w[c].w)
+                             : "l"(sum + c * rows), "l"(hint)
+                             : "memory");
         }
         uint32_t v[32];
         tc::tmem_ld32(t_o + c0, v);
@@ -445,14 +448,17 @@ __device__ __noinline__ void move_sum(const Params &p, uint32_t t_o, bool begins
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             uint32_t *x = &v[4 * c];
+            float4 *at = sum + c * rows;
             const float4 y = make_float4(__uint_as_float(x[0]) + g * w[c].x, __uint_as_float(x[1]) + g * w[c].y,
                                          __uint_as_float(x[2]) + g * w[c].z, __uint_as_float(x[3]) + g * w[c].w);
-            if (plain && valid)
-                asm volatile("red.relaxed.gpu.global.add.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(sum + c * rows), "f"(y.x),
-                             "f"(y.y), "f"(y.z), "f"(y.w), "l"(keep) : "memory");
+            if (plain && valid)          // (only this thread touches these words: always in the same order)
+                asm volatile("red.relaxed.gpu.global.add.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(at),
+                             "f"(y.x), "f"(y.y), "f"(y.z), "f"(y.w), "l"(hint)
+                             : "memory");
             else if (!back && valid)
-                asm volatile("st.relaxed.gpu.global.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(sum + c * rows), "f"(y.x),
-                             "f"(y.y), "f"(y.z), "f"(y.w), "l"(keep) : "memory");
+                asm volatile("st.relaxed.gpu.global.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(at),
+                             "f"(y.x), "f"(y.y), "f"(y.z), "f"(y.w), "l"(hint)
+                             : "memory");
             x[0] = back ? __float_as_uint(y.x) : 0u;
             x[1] = back ? __float_as_uint(y.y) : 0u;
             x[2] = back ? __float_as_uint(y.z) : 0u;

@@ -93,3 +93,13 @@ def test_few_very_long_contexts(name):
     """Every piece of a cut sequence holds a moved sum."""
     check(name, 128, [600000, 450001], [2, 1], 8)
     check(name, 64, [300000], [40], 8, rise=4.0)
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+def test_results_do_not_vary(name):
+    """Moved sums are added in one order, whatever the workspace held."""
+    priors = [(20000, 70, 12000, 9000)[s % 4] for s in range(90)]
+    args = (name, 128, priors, [1 + s % 3 for s in range(90)], 4, 4.0)
+    first = run(*args)[0]
+    for _ in range(4):
+        assert torch.equal(run(*args)[0], first)
